@@ -37,6 +37,10 @@
  *    both in one call). "Attention Optimizations", DSA / Computation Path
  *    (update_cache before attention) and Sliding-window (a rolling buffer of W
  *    entries); "All the attentions", section 4.
+ *  - kvd_rope_append, kvd_rope_append_q4: new tokens (one of each sequence, or a
+ *    ragged batch of many) rotated by their positions and written into a paged or
+ *    rolling cache, in the tensors' type or in 4 bits; attn_decode_gqa_q4:
+ *    single-token attention over the 4-bit cache.
  *  - quest_page_minmax, quest_select_pages, attn_decode_quest (and the split
  *    quest_page_bounds + attn_decode_quest_from_bounds): query-aware page
  *    selection. "Long context, KV eviction and sparse attention", Sparse attention
@@ -110,7 +114,8 @@ enum kvd_op {
     KVD_OP_SWA = 1,
     KVD_OP_MLA = 2,
     KVD_OP_DSA_TOPK = 3,
-    KVD_OP_MLA_SPARSE = 4
+    KVD_OP_MLA_SPARSE = 4,
+    KVD_OP_GQA_Q4 = 5
 };
 
 /*
@@ -239,6 +244,89 @@ int kvd_cache_append(const void *k_new, const void *v_new, void *k_pool, void *v
                      const int32_t *block_table, const int32_t *seq_lens, int B, int H, int D,
                      int page_size, int max_pages, int num_pages, int dtype, int window,
                      int n_sink, int *err, cudaStream_t stream);
+
+/*
+ * New tokens into the cache, the position rotation applied on the way. T rows of q, k and v are
+ * the new tokens of B sequences in order: rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (device,
+ * int32 [B + 1], ascending from 0) belong to sequence b, which may have none; cu_seqlens null
+ * means one token of each sequence (T == B). seq_lens[b] is the length WITH the new tokens: the
+ * i-th of n_b has position t = seq_lens[b] - n_b + i. Rows from cu_seqlens[B] on are padding: they
+ * are neither used nor written.
+ *  q       [T, Hq, D], nullable with q_out (only keys and values are appended then)
+ *  k_new, v_new [T, Hkv, D]. q, k_new and v_new have dense heads; their tokens lie q_stride,
+ *          k_stride, v_stride elements apart (multiples of 16 bytes, at least one token's heads),
+ *          so all three may be slices of one projection's output
+ *  cos_sin [max_pos, rot_dim] float32: row t holds the rot_dim / 2 cosines, then the sines, of
+ *          position t
+ *  q_out   [T, Hq, D] dense: the rotated queries (may be q itself, if that is dense)
+ *  k_pool, v_pool [num_pages, Hkv, page_size, D], updated in place
+ * The first rot_dim channels are rotated, channel i with i + rot_dim/2 (interleaved == 0) or 2i
+ * with 2i + 1 (interleaved != 0): y = x c - x' s, y' = x' c + x s, products and sums each rounded
+ * to float32, the result rounded once to dtype; the other channels pass unchanged. Values are
+ * copied. The cache slot of position t is as in kvd_cache_append (window == 0: paged; window > 0:
+ * rolling, n_sink pinned slots); of the call's tokens that share a rolling slot the last is kept.
+ *  err     int32 on the device, nullable: set to KVD_ERR_DEVICE_OOB, never cleared, for a length
+ *          below the number of new tokens or (paged) above the table's capacity, a position past
+ *          max_pos, offsets that do not ascend (nothing of such a token is written) or a page id
+ *          out of range (its cache rows are not written).
+ * Supported: D in {64, 128}, rot_dim a multiple of 16 in [16, D], page_size a power of two in
+ * [16, 256], dtype KVD_BF16 or KVD_F32; T == 0 does nothing. Outputs must not overlap inputs
+ * otherwise. No workspace; one launch.
+ */
+int kvd_rope_append(const void *q, const void *k_new, const void *v_new, const float *cos_sin,
+                    const int32_t *cu_seqlens, const int32_t *block_table,
+                    const int32_t *seq_lens, void *q_out, void *k_pool, void *v_pool, int B,
+                    int T, int Hq, int Hkv, int D, long long q_stride, long long k_stride,
+                    long long v_stride, int rot_dim, int interleaved, int max_pos, int page_size,
+                    int max_pages, int num_pages, int dtype, int window, int n_sink, int *err,
+                    cudaStream_t stream);
+
+/*
+ * kvd_rope_append into a cache held in 4 bits. k_pool and v_pool are bytes [num_pages, Hkv,
+ * kvd_q4_page_bytes(page_size, D)], 16-byte aligned; their layout is private to the library (it
+ * is described in csrc/kvd_q4.cuh). For each token, head and group of 64 channels x (the keys
+ * rotated in float32, not rounded to dtype first; clamped to +-65504):
+ *   b = f16(min x), s = f16((max x - min x) * f32(1/15)),
+ *   code = clamp(rint((x - b) * (1 / s)), 0, 15) (0 if s = 0), each step rounded to float32,
+ * and the cache stands for s * code + b. A group that holds a NaN or an infinity reads back as
+ * NaN.
+ *  k_out, v_out [T, Hkv, D] dense, each nullable: the values that the cache stands for, rounded
+ *          to dtype (for a prompt's own attention); also for tokens that a rolling cache does not
+ *          keep.
+ * Everything else as kvd_rope_append.
+ */
+int kvd_rope_append_q4(const void *q, const void *k_new, const void *v_new, const float *cos_sin,
+                       const int32_t *cu_seqlens, const int32_t *block_table,
+                       const int32_t *seq_lens, void *q_out, void *k_pool, void *v_pool,
+                       void *k_out, void *v_out, int B, int T, int Hq, int Hkv, int D,
+                       long long q_stride, long long k_stride, long long v_stride, int rot_dim,
+                       int interleaved, int max_pos, int page_size, int max_pages, int num_pages,
+                       int dtype, int window, int n_sink, int *err, cudaStream_t stream);
+
+/* Bytes of one KV head's page of a 4-bit pool (page_size * (D/2 + D/16)); 0 if not supported. */
+size_t kvd_q4_page_bytes(int page_size, int D);
+
+/*
+ * Single-token GQA / MHA / MQA decode over a 4-bit cache (as kvd_rope_append_q4 fills it).
+ *  q [B, Hq, D] dtype, out [B, Hq, D] dtype, lse_out [B, Hq] float32 nullable, block_table,
+ *  seq_lens and scale as attn_decode_gqa_paged; k_pool and v_pool as kvd_rope_append_q4. A length
+ *  of 0 is allowed here: out is 0 and lse -inf (the sink's logit with a learned sink).
+ *  window, n_sink_tokens: 0, 0 all tokens; window > 0 as attn_decode_swa_sink, or, with ring != 0,
+ *  as attn_decode_swa_ring (true lengths, unbounded). sink_logit as attn_decode_swa_sink.
+ *  ws: kvd_workspace_size(KVD_OP_GQA_Q4, B, Hq, Hkv, D, max_pages * page_size, ...) bytes, 16-byte
+ *  aligned, of any content: nothing is kept in it from call to call. Calls that share it must be
+ *  ordered on the device.
+ *  err: int32 on the device, nullable: receives KVD_ERR_DEVICE_OOB (a length or page id out of
+ *  range, clamped) or KVD_ERR_TIMEOUT; never cleared.
+ * The weights of a head are summed in float32 and multiply the values with at least 16 bits; the
+ * result does not depend on timing. Supported: as attn_decode_gqa_paged. Two launches.
+ */
+int attn_decode_gqa_q4(const void *q, const void *k_pool, const void *v_pool,
+                       const int32_t *block_table, const int32_t *seq_lens, void *out,
+                       float *lse_out, int B, int Hq, int Hkv, int D, int page_size,
+                       int max_pages, int num_pages, float scale, int dtype, int window,
+                       int n_sink_tokens, int ring, const float *sink_logit, void *ws,
+                       size_t ws_bytes, int *err, cudaStream_t stream);
 
 /*
  * Quest page summaries ("Long context, KV eviction and sparse attention", Sparse attention:

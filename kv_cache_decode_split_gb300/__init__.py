@@ -17,6 +17,9 @@ Operations:
   quantize_e4m3_rows      e4m3 row quantizer; dsa_indexer_cache_append_fp8 its cache append
   delta_decode_step       one gated delta-rule (Gated DeltaNet / KDA) decode step
   cache_append            the new token's K/V (or latent row) into a paged or rolling cache
+  rope_append, rope_append_q4   new tokens rotated by position into a paged or rolling cache,
+                          in the tensors' type or in 4 bits
+  attn_decode_gqa_q4      attention (dense, window + sinks, rolling) over the 4-bit cache
   attn_decode_swa_ring    sliding window + sinks over a rolling cache
   attn_decode_swa_ring_append   cache_append of the newest token, then attn_decode_swa_ring
   quest_page_minmax, quest_select_pages, attn_decode_quest   Quest page selection
@@ -37,6 +40,7 @@ __all__ = [
     "attn_decode_gqa_paged", "attn_decode_swa_sink", "attn_decode_mla", "dsa_indexer_topk",
     "dsa_indexer_topk_fp8", "quantize_e4m3_rows", "dsa_indexer_cache_append_fp8",
     "delta_decode_step", "attn_decode_swa_ring", "attn_decode_swa_ring_append", "cache_append",
+    "rope_append", "rope_append_q4", "attn_decode_gqa_q4", "q4_page_bytes", "q4_pool",
     "quest_page_minmax",
     "quest_select_pages", "attn_decode_quest", "quest_page_bounds",
     "attn_decode_quest_from_bounds",
@@ -277,6 +281,219 @@ def cache_append(k_new, v_new, k_pool, v_pool, block_table, seq_lens, window=0, 
                               _stream(stream))
     _check(st, "kvd_cache_append")
     return err
+
+
+def q4_page_bytes(page_size, D):
+    """Bytes of one KV head's page in a 4-bit pool."""
+    n = int(lib.kvd_q4_page_bytes(int(page_size), int(D)))
+    if n == 0:
+        raise KvdError(-2, "q4_page_bytes")
+    return n
+
+
+def q4_pool(num_pages, Hkv, page_size, D, device=None):
+    """A zero-filled 4-bit key or value pool: uint8 [num_pages, Hkv, q4_page_bytes]."""
+    return torch.zeros(num_pages, Hkv, q4_page_bytes(page_size, D), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def _on(dev, stream, call):
+    """call(stream handle) on the tensors' device: the given stream, which must be that
+    device's, or its current one."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("stream and tensors must be on one device")
+    if dev == torch.cuda.current_device():
+        return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    with torch.cuda.device(dev):
+        return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+
+
+def _empty(shape, dtype, like, stream):
+    """Uninitialised memory of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _same(t, name, dev, dtype, shape):
+    """A dense CUDA tensor of this device, type and shape; its address."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _tokens(t, name, dev, dtype, T, H, D):
+    """[T, H, D] with dense heads; its address and the elements between tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must be {[T, H, D]}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and H > 1):
+        raise ValueError(f"{name} must have dense heads (strides {D}, 1 in a token)")
+    return t.data_ptr(), (s[0] if T > 1 else H * D)
+
+
+def _rope_args(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens,
+               q_out, err, stream, q4):
+    """The arguments that both appends share, checked: (device, T, rotated queries, leading
+    C arguments, sizes)."""
+    if not isinstance(k_new, torch.Tensor) or not k_new.is_cuda:
+        raise TypeError("k_new must be a CUDA tensor")
+    if k_new.dim() != 3:
+        raise ValueError("k_new must be [T, Hkv, D]")
+    if k_new.dtype not in _DT:
+        raise TypeError("k_new must be float32 or bfloat16")
+    T, Hkv, D = k_new.shape
+    dev, dt = k_new.get_device(), k_new.dtype
+    _need(k_pool, "k_pool", torch.uint8 if q4 else dt, 3 if q4 else 4)
+    num_pages = k_pool.shape[0]
+    if q4:
+        P = k_pool.shape[2] // (D // 2 + D // 16) if D in (64, 128) else 0
+        if P < 1 or k_pool.shape[1] != Hkv or k_pool.shape[2] != P * (D // 2 + D // 16):
+            raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]")
+    else:
+        P = k_pool.shape[2]
+        if k_pool.shape[1] != Hkv or k_pool.shape[3] != D:
+            raise ValueError("k_pool must be [num_pages, Hkv, page_size, D]")
+    _need(cos_sin, "cos_sin", torch.float32, 2)
+    _need(block_table, "block_table", torch.int32, 2)
+    B, max_pages = block_table.shape
+    max_pos, rot = cos_sin.shape
+    for t, n in ((k_pool, "k_pool"), (cos_sin, "cos_sin"), (block_table, "block_table")):
+        if t.get_device() != dev:
+            raise ValueError(f"{n} must be on the device of the other tensors")
+    kp, ks = _tokens(k_new, "k_new", dev, dt, T, Hkv, D)
+    vp, vs = _tokens(v_new, "v_new", dev, dt, T, Hkv, D)
+    qp, qs, Hq, qo = None, 0, 0, None
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [T, Hq, D]")
+        Hq = q.shape[1]
+        qp, qs = _tokens(q, "q", dev, dt, T, Hq, D)
+        if q_out is None:
+            q_out = _empty((T, Hq, D), dt, k_new, stream)
+        qo = _same(q_out, "q_out", dev, dt, (T, Hq, D))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    cu = None
+    if cu_seqlens is not None:
+        cu = _same(cu_seqlens, "cu_seqlens", dev, torch.int32, (B + 1,))
+    elif T != B:
+        raise ValueError("without cu_seqlens there is one token of each sequence")
+    head = (qp, kp, vp, cos_sin.data_ptr(), cu, block_table.data_ptr(),
+            _same(seq_lens, "seq_lens", dev, torch.int32, (B,)), qo, k_pool.data_ptr(),
+            _same(v_pool, "v_pool", dev, k_pool.dtype, k_pool.shape))
+    err_p = None if err is None else _same(err, "err", dev, torch.int32, (1,))
+    sizes = (B, T, Hq, Hkv, D, qs, ks, vs, rot)
+    return dev, q_out, head, sizes, (max_pos, P, max_pages, num_pages, _DT[dt]), err_p
+
+
+def rope_append(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens=None,
+                window=0, n_sink=0, interleaved=False, q_out=None, err=None, stream=None):
+    """New tokens' keys and values, rotated by position, into a paged (or, window > 0, rolling)
+    cache [num_pages, Hkv, P, D], updated in place; the rotated queries are returned.
+
+    q [T, Hq, D] (None: keys and values only), k_new, v_new [T, Hkv, D]: the new tokens of B
+    sequences in order, sequence b's in rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (None: one
+    token of each; rows behind the last sequence are padding). They may be slices of one
+    projection's output (dense heads, any 16-byte stride between tokens). seq_lens [B]: lengths
+    with the new tokens. cos_sin [positions, rot_dim] float32: each position's rot_dim / 2
+    cosines, then sines; rotated are channels i and i + rot_dim / 2, or (interleaved) 2i and
+    2i + 1. q_out may be q itself if q is contiguous. A bad length, position or page id is
+    recorded in err (int32 [1]) and not written.
+    """
+    dev, q_out, head, sizes, pool, err_p = _rope_args(
+        q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens, q_out, err,
+        stream, False)
+    st = _on(dev, stream, lambda s: lib.kvd_rope_append(
+        *head, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink), err_p, s))
+    _check(st, "kvd_rope_append")
+    return q_out
+
+
+def rope_append_q4(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens,
+                   cu_seqlens=None, window=0, n_sink=0, interleaved=False, q_out=None, k_out=None,
+                   v_out=None, err=None, stream=None):
+    """rope_append into a cache held in 4 bits: k_pool and v_pool are uint8 pools of q4_pool().
+    k_out, v_out [T, Hkv, D] (optional) receive the values that the cache stands for."""
+    dev, q_out, head, sizes, pool, err_p = _rope_args(
+        q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens, q_out, err,
+        stream, True)
+    ko = None if k_out is None else _same(k_out, "k_out", dev, k_new.dtype, k_new.shape)
+    vo = None if v_out is None else _same(v_out, "v_out", dev, k_new.dtype, k_new.shape)
+    st = _on(dev, stream, lambda s: lib.kvd_rope_append_q4(
+        *head, ko, vo, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink), err_p,
+        s))
+    _check(st, "kvd_rope_append_q4")
+    return q_out
+
+
+def attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window=0, n_sink_tokens=0,
+                       ring=False, sink_logit=None, scale=None, out=None, lse_out=None,
+                       workspace=None, err=None, stream=None):
+    """Decode attention of q [B, Hq, D] over 4-bit pools (uint8 [num_pages, Hkv, page bytes], as
+    rope_append_q4 fills them): all tokens, or with window > 0 the last window tokens and the
+    first n_sink_tokens (ring: of a rolling cache). A sequence of length 0 gets zeros.
+
+    workspace: a uint8 tensor of kvd_workspace_size("gqa_q4", B, Hq, Hkv, D, max_pages * P) bytes
+    or a Workspace, of any content (calls that share one must be ordered); None takes fresh
+    memory from PyTorch's allocator, so calls on several streams and captured graphs never share
+    it. A bad length or page id is recorded in err (int32 [1]) and clamped.
+    """
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    if q.dtype not in _DT:
+        raise TypeError("q must be float32 or bfloat16")
+    B, Hq, D = q.shape
+    dev = q.get_device()
+    qp = _same(q, "q", dev, q.dtype, q.shape)
+    _need(k_pool, "k_pool", torch.uint8, 3)
+    num_pages, Hkv, page = k_pool.shape
+    P = page // (D // 2 + D // 16) if D in (64, 128) else 0
+    if P < 1 or page != P * (D // 2 + D // 16):
+        raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]")
+    kp = _same(k_pool, "k_pool", dev, torch.uint8, k_pool.shape)
+    vp = _same(v_pool, "v_pool", dev, torch.uint8, k_pool.shape)
+    _need(block_table, "block_table", torch.int32, 2)
+    max_pages = block_table.shape[1]
+    bt = _same(block_table, "block_table", dev, torch.int32, (B, max_pages))
+    sl = _same(seq_lens, "seq_lens", dev, torch.int32, (B,))
+    sink = None if sink_logit is None else _same(sink_logit, "sink_logit", dev, torch.float32, (Hq,))
+    lse = None if lse_out is None else _same(lse_out, "lse_out", dev, torch.float32, (B, Hq))
+    err_p = None if err is None else _same(err, "err", dev, torch.int32, (1,))
+    out = _empty((B, Hq, D), q.dtype, q, stream) if out is None else out
+    op = _same(out, "out", dev, q.dtype, q.shape)
+    if workspace is None or isinstance(workspace, Workspace):
+        nbytes = kvd_workspace_size("gqa_q4", B, Hq, Hkv, D, max_pages * P)
+        if workspace is None:
+            workspace = _empty((max(nbytes, 1),), torch.uint8, q, stream)
+        else:
+            workspace = workspace.get(nbytes, "gqa_q4")
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
+        raise TypeError("workspace must be a uint8 tensor or a Workspace")
+    ws = _same(workspace, "workspace", dev, torch.uint8, workspace.shape)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    st = _on(dev, stream, lambda s: lib.attn_decode_gqa_q4(
+        qp, kp, vp, bt, sl, op, lse, B, Hq, Hkv, D, P, max_pages, num_pages, scale, _DT[q.dtype],
+        int(window), int(n_sink_tokens), 1 if ring else 0, sink, ws, workspace.numel(), err_p, s))
+    _check(st, "attn_decode_gqa_q4")
+    return out
 
 
 def _err(err, device):

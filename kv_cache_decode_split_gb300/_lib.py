@@ -24,6 +24,10 @@ EXPORTS = (
     "attn_decode_swa_ring",
     "attn_decode_swa_ring_append",
     "kvd_cache_append",
+    "kvd_rope_append",
+    "kvd_rope_append_q4",
+    "kvd_q4_page_bytes",
+    "attn_decode_gqa_q4",
     "quest_page_minmax",
     "quest_select_pages",
     "attn_decode_quest",
@@ -41,7 +45,7 @@ STATUS = {
     0: "KVD_OK", -1: "KVD_ERR_INVALID_ARG", -2: "KVD_ERR_UNSUPPORTED", -3: "KVD_ERR_CUDA",
     -4: "KVD_ERR_TIMEOUT", -5: "KVD_ERR_WORKSPACE_TOO_SMALL", -6: "KVD_ERR_DEVICE_OOB", -7: "KVD_ERR_DEVICE_STATE",
 }
-OP = {"gqa": 0, "swa": 1, "mla": 2, "dsa_topk": 3, "mla_sparse": 4}
+OP = {"gqa": 0, "swa": 1, "mla": 2, "dsa_topk": 3, "mla_sparse": 4, "gqa_q4": 5}
 OPTION = {"pdl": 0, "gqa_chunk": 1, "mla_min_tiles": 2, "wait_timeout_test": 3,
           "gqa_cluster": 4}
 
@@ -73,6 +77,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.attn_decode_swa_ring_append.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I,
                                                 F, I, I, I, P, P, Z, P]
     lib.kvd_cache_append.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P]
+    LL = ctypes.c_longlong
+    lib.kvd_rope_append.argtypes = [P] * 10 + [I] * 5 + [LL] * 3 + [I] * 9 + [P, P]
+    lib.kvd_rope_append_q4.argtypes = [P] * 12 + [I] * 5 + [LL] * 3 + [I] * 9 + [P, P]
+    lib.kvd_q4_page_bytes.argtypes = [I, I]
+    lib.kvd_q4_page_bytes.restype = Z
+    lib.attn_decode_gqa_q4.argtypes = [P] * 7 + [I] * 7 + [F] + [I] * 4 + [P, P, Z, P, P]
     lib.quest_page_minmax.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P]
     lib.quest_select_pages.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P]
     lib.attn_decode_quest.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P,
@@ -87,6 +97,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "dsa_indexer_topk", "dsa_indexer_topk_fp8", "kvd_quantize_e4m3_rows",
                  "dsa_indexer_cache_append_fp8", "kvd_delta_decode_step",
                  "attn_decode_swa_ring", "attn_decode_swa_ring_append", "kvd_cache_append",
+                 "kvd_rope_append", "kvd_rope_append_q4", "attn_decode_gqa_q4",
                  "quest_page_minmax",
                  "quest_select_pages", "attn_decode_quest", "quest_page_bounds",
                  "attn_decode_quest_from_bounds", "dsa_topk",

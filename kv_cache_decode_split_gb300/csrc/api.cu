@@ -516,6 +516,177 @@ int kvd_cache_append(const void* k_new, const void* v_new, void* k_pool, void* v
     return append_launch(ap, stream);
 }
 
+// [a, a + na) and [b, b + nb) share a byte (either may be null).
+static bool overlap(const void* a, long long na, const void* b, long long nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+// Both rotated appends (q4: into 4-bit pages, with the stored values given back on request).
+static int rope_append(bool q4, const void* q, const void* k_new, const void* v_new,
+                       const float* cos_sin, const int32_t* cu_seqlens,
+                       const int32_t* block_table, const int32_t* seq_lens, void* q_out,
+                       void* k_pool, void* v_pool, void* k_out, void* v_out, int B, int T, int Hq,
+                       int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                       int rot_dim, int interleaved, int max_pos, int page_size, int max_pages,
+                       int num_pages, int dtype, int window, int n_sink, int* err,
+                       cudaStream_t stream) {
+    if (B < 1 || T < 0 || Hkv < 1 || max_pages < 1 || num_pages < 1 || max_pos < 1 ||
+        window < 0 || n_sink < 0 || (window == 0 && n_sink != 0))
+        return KVD_ERR_INVALID_ARG;
+    if (!q != !q_out || (q && Hq < 1) || (!cu_seqlens && T != B)) return KVD_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return KVD_ERR_UNSUPPORTED;
+    if (rot_dim < 16 || rot_dim > D || rot_dim % 16 != 0) return KVD_ERR_UNSUPPORTED;
+    if (!pow2(page_size) || page_size < 16 || page_size > 256) return KVD_ERR_UNSUPPORTED;
+    if (dtype != KVD_F32 && dtype != KVD_BF16) return KVD_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size >= (1LL << 30)) return KVD_ERR_UNSUPPORTED;
+    if (Hkv > (1 << 20) || (q && Hq > (1 << 20))) return KVD_ERR_UNSUPPORTED;
+    if (window > 0 && (long long)n_sink + window > (long long)max_pages * page_size)
+        return KVD_ERR_INVALID_ARG;
+    if (T == 0) return KVD_OK;
+    if (!k_new || !v_new || !cos_sin || !block_table || !seq_lens || !k_pool || !v_pool)
+        return KVD_ERR_INVALID_ARG;
+    const int e = dtype == KVD_F32 ? 4 : 2;
+    const long long q_row = (long long)Hq * D, kv_row = (long long)Hkv * D;
+    if (k_stride < kv_row || v_stride < kv_row || (q && q_stride < q_row) ||
+        k_stride * e % 16 != 0 || v_stride * e % 16 != 0 || (q && q_stride * e % 16 != 0))
+        return KVD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(cos_sin) ||
+        !aligned16(q_out) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) ||
+        !aligned16(v_out) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3) ||
+        (reinterpret_cast<uintptr_t>(block_table) & 3) ||
+        (reinterpret_cast<uintptr_t>(seq_lens) & 3) || (reinterpret_cast<uintptr_t>(err) & 3))
+        return KVD_ERR_INVALID_ARG;
+    // an output may only lie on an input where each thread has read what it writes: q_out == q
+    const long long q_in = ((T - 1) * q_stride + q_row) * e, k_in = ((T - 1) * k_stride + kv_row) * e,
+                    v_in = ((T - 1) * v_stride + kv_row) * e;
+    const bool in_place = q && q_out == q && q_stride == q_row;
+    const void* outs[3] = {q_out, k_out, v_out};
+    for (int i = 0; i < 3; ++i) {
+        const long long n = T * (i == 0 ? q_row : kv_row) * e;
+        if (!(i == 0 && in_place) && overlap(outs[i], n, q, q_in)) return KVD_ERR_INVALID_ARG;
+        if (overlap(outs[i], n, k_new, k_in) || overlap(outs[i], n, v_new, v_in))
+            return KVD_ERR_INVALID_ARG;
+    }
+    RopeAppendParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.k = k_new;
+    p.v = v_new;
+    p.cos_sin = cos_sin;
+    p.cu_seqlens = cu_seqlens;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.q_out = q_out;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.err = err;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.B = B;
+    p.T = T;
+    p.Hq = q ? Hq : 0;
+    p.Hkv = Hkv;
+    p.rows = p.Hq + 2 * Hkv;
+    p.rot = rot_dim;
+    p.interleaved = interleaved ? 1 : 0;
+    p.max_pos = max_pos;
+    p.page_shift = __builtin_ctz(page_size);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.window = window;
+    p.n_sink = n_sink;
+    return rope_append_launch(p, q4, D, dtype, stream);
+}
+
+int kvd_rope_append(const void* q, const void* k_new, const void* v_new, const float* cos_sin,
+                    const int32_t* cu_seqlens, const int32_t* block_table,
+                    const int32_t* seq_lens, void* q_out, void* k_pool, void* v_pool, int B,
+                    int T, int Hq, int Hkv, int D, long long q_stride, long long k_stride,
+                    long long v_stride, int rot_dim, int interleaved, int max_pos, int page_size,
+                    int max_pages, int num_pages, int dtype, int window, int n_sink, int* err,
+                    cudaStream_t stream) {
+    return rope_append(false, q, k_new, v_new, cos_sin, cu_seqlens, block_table, seq_lens, q_out,
+                       k_pool, v_pool, nullptr, nullptr, B, T, Hq, Hkv, D, q_stride, k_stride,
+                       v_stride, rot_dim, interleaved, max_pos, page_size, max_pages, num_pages,
+                       dtype, window, n_sink, err, stream);
+}
+
+int kvd_rope_append_q4(const void* q, const void* k_new, const void* v_new, const float* cos_sin,
+                       const int32_t* cu_seqlens, const int32_t* block_table,
+                       const int32_t* seq_lens, void* q_out, void* k_pool, void* v_pool,
+                       void* k_out, void* v_out, int B, int T, int Hq, int Hkv, int D,
+                       long long q_stride, long long k_stride, long long v_stride, int rot_dim,
+                       int interleaved, int max_pos, int page_size, int max_pages, int num_pages,
+                       int dtype, int window, int n_sink, int* err, cudaStream_t stream) {
+    return rope_append(true, q, k_new, v_new, cos_sin, cu_seqlens, block_table, seq_lens, q_out,
+                       k_pool, v_pool, k_out, v_out, B, T, Hq, Hkv, D, q_stride, k_stride,
+                       v_stride, rot_dim, interleaved, max_pos, page_size, max_pages, num_pages,
+                       dtype, window, n_sink, err, stream);
+}
+
+size_t kvd_q4_page_bytes(int page_size, int D) {
+    if (!pow2(page_size) || page_size < 16 || page_size > 256 || (D != 64 && D != 128)) return 0;
+    return (size_t)page_size * (D / 2 + D / 16);
+}
+
+int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
+                       const int32_t* block_table, const int32_t* seq_lens, void* out,
+                       float* lse_out, int B, int Hq, int Hkv, int D, int page_size,
+                       int max_pages, int num_pages, float scale, int dtype, int window,
+                       int n_sink_tokens, int ring, const float* sink_logit, void* ws,
+                       size_t ws_bytes, int* err, cudaStream_t stream) {
+    if (n_sink_tokens < 0 || (window == 0 && (n_sink_tokens != 0 || ring)))
+        return KVD_ERR_INVALID_ARG;
+    const long long cap = (long long)n_sink_tokens + window;
+    if (ring && (window < 0 || cap > (long long)max_pages * page_size)) return KVD_ERR_INVALID_ARG;
+    const int st = gqa_check(q, k_pool, v_pool, block_table, seq_lens, out, B, Hq, Hkv, D,
+                             page_size, max_pages, num_pages, scale, dtype, window, n_sink_tokens,
+                             0);
+    if (st != KVD_OK) return st;
+    if (!ws || !aligned16(ws) || (reinterpret_cast<uintptr_t>(block_table) & 3) ||
+        (reinterpret_cast<uintptr_t>(seq_lens) & 3) || (reinterpret_cast<uintptr_t>(lse_out) & 3) ||
+        (reinterpret_cast<uintptr_t>(sink_logit) & 3) || (reinterpret_cast<uintptr_t>(err) & 3))
+        return KVD_ERR_INVALID_ARG;
+    Q4Plan plan;
+    if (q4_plan(B, Hq, Hkv, D, (long long)max_pages * page_size, dtype, &plan) != KVD_OK)
+        return KVD_ERR_UNSUPPORTED;
+    if (ws_bytes < plan.total) return KVD_ERR_WORKSPACE_TOO_SMALL;
+    Q4Params p;
+    std::memset(&p, 0, sizeof p);
+    p.q = q;
+    p.k_pool = static_cast<const uint8_t*>(k_pool);
+    p.v_pool = static_cast<const uint8_t*>(v_pool);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.sink_logit = sink_logit;
+    p.out = out;
+    p.lse_out = lse_out;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    p.part_ml = reinterpret_cast<float*>(w + plan.off_ml);
+    p.part_o = reinterpret_cast<float*>(w + plan.off_o);
+    p.err = err;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.NHG = plan.NHG;
+    p.HU = Hkv * plan.NHG;
+    p.n_warps = plan.ctas * 8;
+    p.page_shift = __builtin_ctz(page_size);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.max_len = max_pages * page_size;
+    p.window = ring ? 0 : window;
+    p.n_sink = ring ? 0 : n_sink_tokens;
+    p.ring = ring ? static_cast<int>(cap) : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return q4_launch(plan, p, D, dtype, stream);
+}
+
 // Checks shared by the three Quest entry points.
 static int quest_common(QuestParams& qp, int B, int Hq, int Hkv, int D, int page_size,
                         int max_pages, int num_pages, int dtype, int* err) {
@@ -911,6 +1082,13 @@ size_t kvd_workspace_size(int op, int B, int H, int Hkv, int D, int max_len, int
     }
     if (op == KVD_OP_MLA) return mla_plan(B, max_len, false).total;
     if (op == KVD_OP_MLA_SPARSE) return k >= 1 ? mla_plan(B, k, true).total : 0;
+    if (op == KVD_OP_GQA_Q4) {
+        Q4Plan plan;
+        if (Hkv < 1 || H % Hkv != 0 || (D != 64 && D != 128) ||
+            q4_plan(B, H, Hkv, D, max_len, KVD_BF16, &plan) != KVD_OK)
+            return 0;
+        return plan.total;  // float32 queries need no more
+    }
     if (op == KVD_OP_GQA || op == KVD_OP_SWA) {
         if (Hkv < 1 || H % Hkv != 0 || (D != 64 && D != 128)) return 0;
         // the plan's chunk length is smallest (most partials) for 16-token pages

@@ -1,0 +1,787 @@
+// gqa_q4_decode.cu -- single-token attention over a paged or rolling cache held in 4 bits.
+//
+// What is computed, with k and v the values that the codes stand for (kvd_q4.cuh):
+//   o_h = sum_{t in V} e^{x_t} v_t / (sum_{t in V} e^{x_t} + [sink] e^{sigma_h}),
+//   x_t = scale q_h . k_t, query head h reading KV head h / (Hq / Hkv),
+// V the visible slots: all of the sequence, the window and the sink tokens, or what a rolling cache
+// holds. With k = s code + b per group of 64 channels the score is sum_g s_g (q_g . code) + b_g sum(q_g),
+// so the matrix product runs on the codes and scale and minimum enter once per token and group; with
+// v = s code + b the weight p s multiplies the codes, and sum_t p b is one number per head and group.
+//
+// GB300. 4 bits quarter the bytes but not the elements: at the measured copy bandwidth an SM has
+// about 2.7 lane operations for each element it reads, so what matters is instructions per
+// element. Codes go from shared memory to matrix-instruction fragments with one shift and one
+// three-input logic operation per two elements: code c in mantissa bits 3-6 under the exponent of
+// 16 is the bf16 number 16 + c, exactly. (Feeding tcgen05 would write every element back to
+// shared memory as 16 bits first, which alone costs more than the whole budget; with at most 16
+// query rows its rate is not needed.) The offset 16 is taken out of the scores through the
+// accumulator's start value, -16 sum(q_g). For the values, odd tokens are decoded with the sign
+// flipped and the code complemented, -(16 + 15 - c) = c - 31: offsets +16 and -31 average to the
+// middle of the code range, so the sums stay small over long sequences, and each token's minimum
+// is corrected by its own offset.
+//   scores^T [16 tokens x 8 heads] = K codes [16 x D] q^T           (mma.sync m16n8k16, fp32 sums)
+//   O^T [16 channels x 8 heads]   += V codes^T [16 x 16 tokens] (p s)^T
+// p s enters as the sum of two bf16 numbers (16 bits; three for float32 queries), so that rounding
+// the weights adds nothing to the output's own rounding.
+//
+// Work is divided over all warps of the grid: the visible 32-token tiles of all (sequence, KV
+// head, head block) units form one list, and warp i of N (at most one for each tile) takes tiles
+// [W i / N, W (i+1) / N) of it, whatever sequences they belong to. A warp streams its tiles through a ring of its own in shared
+// memory (bulk copies, one per page piece, codes and scales together) and needs no other warp: it
+// stores one partial (maximum, sum, O) for each unit it touches, or the result itself if it had
+// the whole unit. A second launch joins the partials of the units that were cut.
+
+#include <algorithm>
+
+#include "kvd_device.cuh"
+#include "kvd_host.h"
+#include "kvd_q4.cuh"
+
+namespace kvd {
+
+namespace {
+
+constexpr int kTileTok = 32;   // tokens of a tile: two 16-token blocks
+constexpr int kWarps = 8;      // warps of a CTA
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// maximum of nothing: finite, so that differences with it are defined
+constexpr float kNone = -3.0e38f;
+
+__device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
+
+// The visible slots of sequence b (at most two ranges), empty for a length of 0.
+__device__ __forceinline__ Ranges seq_ranges(const Q4Params& p, int b) {
+    int L = __ldg(p.seq_lens + b);
+    if (L < 0 || (p.ring <= 0 && L > p.max_len)) {
+        record_error(p.err, KVD_ERR_DEVICE_OOB);
+        L = L < 0 ? 0 : p.max_len;
+    }
+    if (p.ring > 0) return Ranges{0, min(L, p.ring), 0, 0};
+    return visible_ranges(L, p.window, p.n_sink);
+}
+__device__ __forceinline__ int range_tiles(int lo, int hi) {
+    return hi > lo ? ((hi - 1) >> 5) - (lo >> 5) + 1 : 0;
+}
+__device__ __forceinline__ int seq_tiles(const Q4Params& p, int b) {
+    const Ranges r = seq_ranges(p, b);
+    return range_tiles(r.lo0, r.hi0) + range_tiles(r.lo1, r.hi1);
+}
+
+// Tiles of all sequences in front of b_want (prefix) and of all of them (total), times HU;
+// one warp.
+struct Schedule {
+    long long prefix, total;
+    int tiles;  // of b_want's units
+};
+__device__ __forceinline__ Schedule schedule_of(const Q4Params& p, int b_want, int lane) {
+    Schedule s{0, 0, 0};
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int n = b < p.B ? seq_tiles(p, b) : 0;
+        long long sum = n, before = b < b_want ? n : 0;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            before += __shfl_xor_sync(0xffffffffu, before, off);
+        }
+        s.total += sum;
+        s.prefix += before;
+        if (b_want >= b0 && b_want < b0 + 32) s.tiles = __shfl_sync(0xffffffffu, n, b_want - b0);
+    }
+    s.total *= p.HU;
+    s.prefix *= p.HU;
+    return s;
+}
+
+// c[16x8] += a[16x16] * b[16x8], bf16 inputs, fp32 sums (not volatile: it may be reordered).
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr uint32_t kMask = 0x00780078u;
+constexpr uint32_t kKey = 0x41804180u;   // 16 + c in both halves
+constexpr uint32_t kVal = 0xC1F84180u;   // low half 16 + c, high half c - 31
+
+// 16 + c -> c - 8 (exact), for float32 queries: nothing is left to cancel
+__device__ __forceinline__ uint32_t centre(uint32_t x) {
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x),
+                                     __floats2bfloat162_rn(24.f, 24.f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// x as a sum of kSplit bf16 numbers: part k of two values, packed.
+template <int kSplit>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&part)[kSplit]) {
+#pragma unroll
+    for (int k = 0; k < kSplit; ++k) {
+        part[k] = pack_bf16(x, y);
+        if (k + 1 < kSplit) {
+            x -= __uint_as_float(part[k] << 16);
+            y -= __uint_as_float(part[k] & 0xffff0000u);
+        }
+    }
+}
+
+struct TileInfo {  // written with each tile's copies, read by the warp that uses the tile
+    int T, lo, hi;    // first token; the visible ones are lo <= t < hi
+    int b, u;         // sequence, unit of the sequence
+    int flags;        // 1 first tile of the warp's piece, 2 last; 4 first tile of the unit, 8 last
+    int pad[2];
+};
+
+template <int D, int NT, bool kF32>
+struct Q4Cfg {
+    static constexpr int kStages = 3;
+    static constexpr int kTileBytes = 4 * Q4<D>::kBlockBytes;  // K and V, two blocks each
+    static constexpr int kRing = kStages * kTileBytes;
+    static constexpr int kPerWarp = kRing + kStages * static_cast<int>(sizeof(TileInfo) + 8);
+    static constexpr int kSmem = kWarps * kPerWarp;
+    static constexpr int kCtas = (NT == 1 && !kF32) ? 2 : 1;   // per SM (registers)
+};
+
+template <int D, int NT, bool kF32>
+__global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
+    gqa_q4_kernel(const Q4Params p) {
+    using Cfg = Q4Cfg<D, NT, kF32>;
+    using L4 = Q4<D>;
+    constexpr int S = Cfg::kStages;
+    constexpr int NG = L4::kGroups;
+    constexpr int KW = D / 32;             // key words of a lane and row
+    constexpr int MT = D / 16;             // 16-channel tiles of the output
+    constexpr int kQ = kF32 ? 3 : 1;       // bf16 parts of a query
+    constexpr int kP = kF32 ? 3 : 2;       // bf16 parts of a weight
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t* ring = smem + warp * Cfg::kRing;
+    TileInfo* info = reinterpret_cast<TileInfo*>(smem + kWarps * Cfg::kRing) + warp * S;
+    uint64_t* full = reinterpret_cast<uint64_t*>(
+                         smem + kWarps * (Cfg::kRing + S * sizeof(TileInfo))) + warp * S;
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    griddep_wait();
+
+    // ---- this warp's share of the tile list, and where it begins
+    // (with fewer tiles than warps the first warps of all CTAs take one each)
+    const long long me = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
+    const Schedule sch = schedule_of(p, 0, lane);
+    const long long N = min(static_cast<long long>(p.n_warps), sch.total);
+    if (me >= N) return;
+    const long long begin = sch.total * me / N;
+    int left = static_cast<int>(sch.total * (me + 1) / N - begin);  // tiles to copy, at least 1
+    const int n_mine = left;
+    // cursor of the next tile to copy: sequence, unit, tile of the unit
+    int cb = 0, cu = 0, cj = 0, cn = 0;
+    Ranges cr{};
+    {
+        long long rem = begin;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            const int n = b < p.B ? seq_tiles(p, b) : 0;
+            long long inc = static_cast<long long>(n) * p.HU;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += o;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, inc > rem);
+            if (past) {
+                const int k = __ffs(past) - 1;
+                cb = b0 + k;
+                cn = __shfl_sync(0xffffffffu, n, k);
+                rem -= __shfl_sync(0xffffffffu, inc, k) - static_cast<long long>(cn) * p.HU;
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+        cu = static_cast<int>(rem / cn);
+        cj = static_cast<int>(rem % cn);
+        cr = seq_ranges(p, cb);
+    }
+    const uint64_t pol = l2_evict_first_policy();  // keys and values are read once
+    const int blk_shift = p.page_shift - 4;
+    auto cursor_tile = [&](int& lo, int& hi) -> int {
+        const int n0 = range_tiles(cr.lo0, cr.hi0);
+        if (cj < n0) {
+            lo = cr.lo0, hi = cr.hi0;
+            return ((lo >> 5) + cj) << 5;
+        }
+        lo = cr.lo1, hi = cr.hi1;
+        return ((lo >> 5) + cj - n0) << 5;
+    };
+    // pages of the cursor's tile (two when pages hold 16 tokens), requested a tile ahead
+    int pg0 = 0, pg1 = 0;
+    auto fetch_pages = [&]() {
+        int lo, hi;
+        const int T = cursor_tile(lo, hi);
+        const int32_t* row = p.block_table + static_cast<size_t>(cb) * p.max_pages;
+        pg0 = __ldg(row + (max(T, lo) >> p.page_shift));
+        pg1 = __ldg(row + (min(T + kTileTok, hi) - 1 >> p.page_shift));
+    };
+    fetch_pages();
+    // copy the cursor's tile into stage s and move on
+    auto issue = [&](int s) {
+        if (left == 0) return;
+        int lo, hi;
+        const int T = cursor_tile(lo, hi);
+        if (lane == 0) {
+            TileInfo ti;
+            ti.T = T, ti.lo = lo, ti.hi = hi, ti.b = cb, ti.u = cu;
+            ti.flags = ((left == n_mine || cj == 0) ? 1 : 0) |
+                       ((left == 1 || cj == cn - 1) ? 2 : 0) | (cj == 0 ? 4 : 0) |
+                       (cj == cn - 1 ? 8 : 0);
+            info[s] = ti;
+            if (pg0 < 0 || pg0 >= p.num_pages || pg1 < 0 || pg1 >= p.num_pages) {
+                record_error(p.err, KVD_ERR_DEVICE_OOB);
+                if (pg0 < 0 || pg0 >= p.num_pages) pg0 = 0;
+                if (pg1 < 0 || pg1 >= p.num_pages) pg1 = 0;
+            }
+            const int kvh = cu / p.NHG;
+            uint8_t* st = ring + s * Cfg::kTileBytes;
+            if (p.page_shift >= 5) {
+                const size_t off =
+                    (((static_cast<size_t>(pg0) * p.Hkv + kvh) << blk_shift) +
+                     ((T & ((1 << p.page_shift) - 1)) >> 4)) * L4::kBlockBytes;
+                mbar_arrive_expect_tx(&full[s], Cfg::kTileBytes);
+                bulk_load(st, p.k_pool + off, 2 * L4::kBlockBytes, &full[s], pol);
+                bulk_load(st + 2 * L4::kBlockBytes, p.v_pool + off, 2 * L4::kBlockBytes, &full[s],
+                          pol);
+            } else {  // a block without visible tokens is not copied (all of it is masked)
+                const bool h0 = T + 16 > lo, h1 = T + 16 < hi;
+                mbar_arrive_expect_tx(&full[s], (h0 + h1) * 2 * L4::kBlockBytes);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (!(k ? h1 : h0)) continue;
+                    const size_t off =
+                        (static_cast<size_t>(k ? pg1 : pg0) * p.Hkv + kvh) * L4::kBlockBytes;
+                    bulk_load(st + k * L4::kBlockBytes, p.k_pool + off, L4::kBlockBytes, &full[s],
+                              pol);
+                    bulk_load(st + (2 + k) * L4::kBlockBytes, p.v_pool + off, L4::kBlockBytes,
+                              &full[s], pol);
+                }
+            }
+        }
+        if (--left == 0) return;
+        if (++cj == cn) {
+            cj = 0;
+            if (++cu == p.HU) {
+                cu = 0;
+                do {
+                    ++cb;
+                    cr = seq_ranges(p, cb);
+                    cn = range_tiles(cr.lo0, cr.hi0) + range_tiles(cr.lo1, cr.hi1);
+                } while (cn == 0);
+            }
+        }
+        fetch_pages();
+    };
+    for (int s = 0; s < S; ++s) issue(s);
+
+    // ---- state of the current piece
+    uint32_t qf[kQ][NT][KW][4];
+    float q16[NT][NG][2], qsum[NT][NG][2];  // accumulator start and sum of q, heads 2t, 2t + 1
+    float o[NT][MT][4], ob[NT][NG][2], m[NT][2], l[NT][2];
+    bool from_start = false;
+    const float sl2 = p.scale_log2;
+
+    for (int i = 0; i < n_mine; ++i) {
+        const int s = i % S;
+        __syncwarp();
+        if (!mbar_wait(&full[s], (i / S) & 1, p.err)) {
+            // give up, once the copies in flight have landed (or their own limits have passed)
+            if (lane == 0)
+                for (int k = i + 1; k < min(n_mine, i + S); ++k)
+                    mbar_wait(&full[k % S], (k / S) & 1, p.err);
+            __syncwarp();
+            return;
+        }
+        const TileInfo ti = info[s];
+        const int kvh = ti.u / p.NHG, hg = ti.u % p.NHG;
+        const int G_cta = min(NT * 8, p.G - hg * NT * 8);
+        const int hq0 = kvh * p.G + hg * NT * 8;  // first query head of the unit
+        if (ti.flags & 1) {
+            from_start = (ti.flags & 4) != 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float part[NG] = {};
+                const int h = nt * 8 + g;
+                const bool ok = h < G_cta;
+                const size_t qrow =
+                    (static_cast<size_t>(ti.b) * p.Hq + hq0 + (ok ? h : 0)) * D;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    float x[8];
+                    if constexpr (kF32) {
+                        const float* q = static_cast<const float*>(p.q) + qrow + 32 * w + 8 * t;
+                        const float4 a = *reinterpret_cast<const float4*>(q);
+                        const float4 c = *reinterpret_cast<const float4*>(q + 4);
+                        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+                        x[4] = c.x, x[5] = c.y, x[6] = c.z, x[7] = c.w;
+                    } else {
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            static_cast<const __nv_bfloat16*>(p.q) + qrow + 32 * w + 8 * t);
+                        const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[2 * e] = __uint_as_float(r[e] << 16);
+                            x[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (!ok) x[e] = 0.f;
+                        part[w / 2] += x[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // fragments pair channels e and e + 4
+                        uint32_t sp[kQ];
+                        split2<kQ>(x[e], x[e + 4], sp);
+#pragma unroll
+                        for (int k = 0; k < kQ; ++k) qf[k][nt][w][e] = sp[k];
+                    }
+                }
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    part[gr] += __shfl_xor_sync(0xffffffffu, part[gr], 1);
+                    part[gr] += __shfl_xor_sync(0xffffffffu, part[gr], 2);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float v = __shfl_sync(0xffffffffu, part[gr], (2 * t + c) * 4);
+                        qsum[nt][gr][c] = v;
+                        // codes centred on 8 (float32) leave 8 sum(q) to add, below
+                        q16[nt][gr][c] = kF32 ? 8.f * v : -16.f * v;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    m[nt][c] = kNone;
+                    l[nt][c] = 0.f;
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) ob[nt][gr][c] = 0.f;
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[nt][mt][r] = 0.f;
+            }
+        }
+        const uint8_t* kt = ring + s * Cfg::kTileBytes;
+        const uint8_t* vt = kt + 2 * L4::kBlockBytes;
+        const bool ragged = ti.T < ti.lo || ti.T + kTileTok > ti.hi;
+
+        // ---- scores of the two blocks
+        float x[2][NT][4];
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk) {
+            const uint8_t* kb = kt + bk * L4::kBlockBytes;
+            uint32_t wa[KW], wb[KW];
+            if constexpr (D == 128) {
+                *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(kb + g * 64 + t * 16);
+                *reinterpret_cast<uint4*>(wb) =
+                    *reinterpret_cast<const uint4*>(kb + (g + 8) * 64 + t * 16);
+            } else {
+                *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(kb + g * 32 + t * 8);
+                *reinterpret_cast<uint2*>(wb) =
+                    *reinterpret_cast<const uint2*>(kb + (g + 8) * 32 + t * 8);
+            }
+            float acc[NT][NG][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[nt][gr][r] = kF32 ? 0.f : q16[nt][gr][r & 1];
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                uint32_t fa[4], fb[4];
+                fa[0] = (wa[w] & kMask) ^ kKey;
+                fb[0] = (wb[w] & kMask) ^ kKey;
+                fa[1] = ((wa[w] >> 4) & kMask) ^ kKey;
+                fb[1] = ((wb[w] >> 4) & kMask) ^ kKey;
+                fa[2] = ((wa[w] >> 8) & kMask) ^ kKey;
+                fb[2] = ((wb[w] >> 8) & kMask) ^ kKey;
+                fa[3] = (__funnelshift_r(wa[w], wa[w], 12) & kMask) ^ kKey;
+                fb[3] = (__funnelshift_r(wb[w], wb[w], 12) & kMask) ^ kKey;
+                if constexpr (kF32) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) fa[e] = centre(fa[e]), fb[e] = centre(fb[e]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < kQ; ++k) {
+                        mma(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
+                            qf[k][nt][w][1]);
+                        mma(acc[nt][w / 2], fa[2], fb[2], fa[3], fb[3], qf[k][nt][w][2],
+                            qf[k][nt][w][3]);
+                    }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const __half2* pr =
+                    reinterpret_cast<const __half2*>(kb + L4::param(g + 8 * half, 0));
+                const int tok = ti.T + bk * 16 + g + 8 * half;
+                const bool in = !ragged || (tok >= ti.lo && tok < ti.hi);
+                float sg[NG], bg[NG];
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    const float2 f = __half22float2(pr[gr]);
+                    sg[gr] = f.x, bg[gr] = f.y;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr) {
+                            float a = acc[nt][gr][2 * half + c];
+                            if (kF32) a += q16[nt][gr][c];
+                            v = fmaf(sg[gr], a, fmaf(bg[gr], qsum[nt][gr][c], v));
+                        }
+                        x[bk][nt][2 * half + c] = in ? v * sl2 : neg_inf();
+                    }
+            }
+        }
+        // ---- running maximum: raised only when a score passes it by more than 8 (p <= 2^8
+        // until then, harmless in fp32 sums and in p's bf16 parts)
+        bool up = false;
+        float mx[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mx[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][2 + c]),
+                                  fmaxf(x[1][nt][c], x[1][nt][2 + c]));
+                up = up || mx[nt][c] > m[nt][c] + 8.f;
+            }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = mx[nt][c];
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                    v = fmaxf(v, m[nt][c]);
+                    const float al = fast_exp2(m[nt][c] - v);
+                    m[nt][c] = v;
+                    l[nt][c] *= al;
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) ob[nt][gr][c] *= al;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        o[nt][mt][c] *= al;
+                        o[nt][mt][2 + c] *= al;
+                    }
+                }
+        }
+        // ---- weights and values of the two blocks
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk) {
+            const uint8_t* vb = vt + bk * L4::kBlockBytes;
+            float sg[2][NG], bg[2][NG];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const __half2* pr =
+                    reinterpret_cast<const __half2*>(vb + L4::param(g + 8 * half, 0));
+                const int tok = ti.T + bk * 16 + g + 8 * half;
+                const bool in = !ragged || (tok >= ti.lo && tok < ti.hi);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    const float2 f = __half22float2(pr[gr]);
+                    // what a masked slot holds may be anything, NaN included
+                    sg[half][gr] = in ? f.x : 0.f;
+                    // minimum corrected by the offset of the decoded codes (kF32: -8; else by
+                    // the token's parity, + 16 or - 31; g + 8 half has the parity of g)
+                    const float off = kF32 ? -8.f : ((g & 1) ? -31.f : 16.f);
+                    bg[half][gr] = in ? fmaf(-off, f.x, f.y) : 0.f;
+                }
+            }
+            uint32_t pf[NT][NG][kP][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float pr[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    pr[r] = fast_exp2(x[bk][nt][r] - m[nt][r & 1]);
+                    l[nt][r & 1] += pr[r];
+                }
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ob[nt][gr][0] = fmaf(pr[2 * half], bg[half][gr], ob[nt][gr][0]);
+                        ob[nt][gr][1] = fmaf(pr[2 * half + 1], bg[half][gr], ob[nt][gr][1]);
+                        uint32_t sp[kP];
+                        split2<kP>(pr[2 * half] * sg[half][gr], pr[2 * half + 1] * sg[half][gr],
+                                   sp);
+#pragma unroll
+                        for (int k = 0; k < kP; ++k) pf[nt][gr][k][half] = movmatrix_t(sp[k]);
+                    }
+                }
+            }
+            uint4 va, vc;  // words of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
+            if constexpr (D == 128) {
+                va = *reinterpret_cast<const uint4*>(vb + lane * 16);
+                vc = *reinterpret_cast<const uint4*>(vb + 512 + lane * 16);
+            } else {
+                va = *reinterpret_cast<const uint4*>(vb + lane * 16);
+            }
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                uint32_t w0, w1, w2, w3;  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+                if constexpr (D == 128) {
+                    w0 = gr ? va.y : va.x, w1 = gr ? va.w : va.z;
+                    w2 = gr ? vc.y : vc.x, w3 = gr ? vc.w : vc.z;
+                } else {
+                    w0 = va.x, w1 = va.y, w2 = va.z, w3 = va.w;
+                }
+#pragma unroll
+                for (int hw = 0; hw < 2; ++hw) {  // codes 0-3, then 4-7 of the words
+                    const uint32_t u = __byte_perm(w0, w1, hw ? 0x7632 : 0x5410);
+                    const uint32_t v = __byte_perm(w2, w3, hw ? 0x7632 : 0x5410);
+                    constexpr uint32_t kX = kF32 ? kKey : kVal;
+                    uint32_t fu[4], fv[4];
+                    fu[0] = ((u << 3) & kMask) ^ kX;
+                    fv[0] = ((v << 3) & kMask) ^ kX;
+                    fu[1] = ((u >> 1) & kMask) ^ kX;
+                    fv[1] = ((v >> 1) & kMask) ^ kX;
+                    fu[2] = ((u >> 5) & kMask) ^ kX;
+                    fv[2] = ((v >> 5) & kMask) ^ kX;
+                    fu[3] = ((u >> 9) & kMask) ^ kX;
+                    fv[3] = ((v >> 9) & kMask) ^ kX;
+                    if constexpr (kF32) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) fu[e] = centre(fu[e]), fv[e] = centre(fv[e]);
+                    }
+                    const int mt = gr * 4 + hw * 2;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < kP; ++k) {
+                            mma(o[nt][mt], fu[0], fu[1], fv[0], fv[1], pf[nt][gr][k][0],
+                                pf[nt][gr][k][1]);
+                            mma(o[nt][mt + 1], fu[2], fu[3], fv[2], fv[3], pf[nt][gr][k][0],
+                                pf[nt][gr][k][1]);
+                        }
+                }
+            }
+        }
+        // ---- end of the warp's piece of this unit
+        if (ti.flags & 2) {
+            const bool whole = from_start && (ti.flags & 8);
+            const long long unit = static_cast<long long>(ti.b) * p.HU + ti.u;
+            const size_t slot = static_cast<size_t>(me + unit);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float lv = l[nt][c], bv[NG];
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) bv[gr] = ob[nt][gr][c];
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) {
+                        lv += __shfl_xor_sync(0xffffffffu, lv, off);
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr)
+                            bv[gr] += __shfl_xor_sync(0xffffffffu, bv[gr], off);
+                    }
+                    const int h = nt * 8 + 2 * t + c;
+                    if (h >= G_cta) continue;
+                    float mul = 1.f;
+                    if (whole) {  // nothing to join: the output itself
+                        const int hq = hq0 + h;
+                        const float sig = p.sink_logit ? p.sink_logit[hq] * kLog2e : neg_inf();
+                        const float M = fmaxf(m[nt][c], sig);
+                        const float w = fast_exp2(m[nt][c] - M);
+                        const float den = lv * w + (p.sink_logit ? fast_exp2(sig - M) : 0.f);
+                        mul = w / den;
+                        if (p.lse_out && g == 0)
+                            p.lse_out[static_cast<size_t>(ti.b) * p.Hq + hq] =
+                                (M + log2f(den)) * kLn2;
+                    } else if (g == 0) {
+                        float* ml = p.part_ml + (slot * (NT * 8) + h) * 2;
+                        __stcg(reinterpret_cast<float2*>(ml), make_float2(m[nt][c], lv));
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int d = mt * 16 + g + 8 * e;
+                            const float v = (o[nt][mt][2 * e + c] + bv[mt / 4]) * mul;
+                            if (!whole) {
+                                __stcg(p.part_o + (slot * (NT * 8) + h) * D + d, v);
+                            } else {
+                                const size_t at = (static_cast<size_t>(ti.b) * p.Hq + hq0 + h) * D + d;
+                                if constexpr (kF32)
+                                    static_cast<float*>(p.out)[at] = v;
+                                else
+                                    static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(v);
+                            }
+                        }
+                }
+        }
+        __syncwarp();
+        issue(s);
+    }
+}
+
+// Joins the partials of one (unit, head): out = sum_i 2^{m_i - M} O_i / (sum_i 2^{m_i - M} l_i +
+// 2^{sigma - M}). Warps take every eighth partial and are then joined in shared memory. Units that
+// one warp had whole are written already; units without tiles get zeros.
+template <int D, int NT, bool kF32>
+__global__ void __launch_bounds__(256) gqa_q4_combine_kernel(const Q4Params p) {
+    constexpr int V = D / 32;  // channels of a lane
+    __shared__ float s_o[8][D], s_m[8], s_l[8];
+    griddep_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int hp = min(NT * 8, p.G);
+    const int h = blockIdx.x % hp;
+    const int unit = blockIdx.x / hp;
+    const int b = unit / p.HU, u = unit % p.HU;
+    const int kvh = u / p.NHG, hg = u % p.NHG;
+    if (hg * NT * 8 + h >= p.G) return;
+    const int hq = kvh * p.G + hg * NT * 8 + h;
+    const Schedule sch = schedule_of(p, b, lane);
+    const size_t at = (static_cast<size_t>(b) * p.Hq + hq) * D;
+    const float sig = p.sink_logit ? p.sink_logit[hq] * kLog2e : neg_inf();
+    int first = 0, n = 0;
+    if (sch.tiles > 0) {
+        const long long W = sch.total, N = min(static_cast<long long>(p.n_warps), W);
+        const long long t0 = sch.prefix + static_cast<long long>(u) * sch.tiles;
+        const long long t1 = t0 + sch.tiles - 1;
+        first = static_cast<int>(((t0 + 1) * N + W - 1) / W - 1);  // the warp that has tile t0
+        n = static_cast<int>(((t1 + 1) * N + W - 1) / W - 1) - first + 1;
+        if (n == 1) return;
+    }
+    float M = kNone, L = 0.f, acc[V] = {};
+    for (int i0 = warp; i0 < n; i0 += 256) {  // 32 partials of this warp at once
+        const int mine = i0 + 8 * lane;
+        float2 ml = make_float2(kNone, 0.f);
+        if (mine < n)
+            ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) +
+                        static_cast<size_t>(first + mine + unit) * (NT * 8) + h);
+        float top = ml.x;
+        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = fmaxf(top, M);
+        const float al = fast_exp2(M - top), w = fast_exp2(ml.x - top);
+        float sum = ml.y * w;
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        L = L * al + sum;
+        M = top;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] *= al;
+        const int cnt = min(32, (n - i0 + 7) / 8);
+#pragma unroll 4
+        for (int k = 0; k < cnt; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float* src = p.part_o +
+                               (static_cast<size_t>(first + i0 + 8 * k + unit) * (NT * 8) + h) * D +
+                               lane * V;
+            float v[V];
+            if constexpr (V == 4)
+                *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
+            else
+                *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(wk, v[e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+    if (lane == 0) s_m[warp] = M, s_l[warp] = L;
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d >= D) return;
+    float top = sig;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, s_m[k]);
+    float den = p.sink_logit ? fast_exp2(sig - top) : 0.f, v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float w = fast_exp2(s_m[k] - top);
+        den = fmaf(w, s_l[k], den);
+        v = fmaf(w, s_o[k][d], v);
+    }
+    // nothing visible: zeros, and the logarithm of the sink's share alone
+    v = n == 0 ? 0.f : v / den;
+    if constexpr (kF32)
+        static_cast<float*>(p.out)[at + d] = v;
+    else
+        static_cast<__nv_bfloat16*>(p.out)[at + d] = __float2bfloat16(v);
+    if (d == 0 && p.lse_out)
+        p.lse_out[static_cast<size_t>(b) * p.Hq + hq] =
+            n == 0 ? sig * kLn2 : (top + log2f(den)) * kLn2;
+}
+
+template <int D, int NT, bool kF32>
+int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
+    using Cfg = Q4Cfg<D, NT, kF32>;
+    auto kern = gqa_q4_kernel<D, NT, kF32>;
+    static int configured = 0;
+    if (!configured) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem) !=
+            cudaSuccess)
+            return KVD_ERR_CUDA;
+        configured = 1;
+    }
+    if (launch_kernel(kern, dim3(plan.ctas), dim3(kWarps * 32), Cfg::kSmem, stream, p) !=
+        cudaSuccess)
+        return KVD_ERR_CUDA;
+    const unsigned rows = static_cast<unsigned>(plan.units) * std::min(NT * 8, p.G);
+    if (launch_kernel(gqa_q4_combine_kernel<D, NT, kF32>, dim3(rows), dim3(256), 0, stream, p) !=
+        cudaSuccess)
+        return KVD_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
+}
+
+}  // namespace
+
+// A block of at most 8 (16) query heads of a KV head; as many CTAs as are resident at once, or as
+// the longest possible list of tiles keeps busy.
+int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan* plan) {
+    const int G = Hq / Hkv;
+    plan->nt = G > 8 ? 2 : 1;
+    plan->NHG = (G + plan->nt * 8 - 1) / (plan->nt * 8);
+    const long long units = static_cast<long long>(B) * Hkv * plan->NHG;
+    // one grid row per (unit, head) of the joining launch
+    if (units * std::min(G, plan->nt * 8) > 0x7fffffffLL) return KVD_ERR_UNSUPPORTED;
+    plan->units = static_cast<int>(units);
+    const int per_sm = (plan->nt == 1 && dtype == KVD_BF16) ? 2 : 1;
+    const long long tiles = units * ((max_len + kTileTok - 1) / kTileTok + 1);
+    plan->ctas = static_cast<int>(std::max(
+        1LL, std::min<long long>(1LL * num_sms() * per_sm, (tiles + kWarps - 1) / kWarps)));
+    const size_t slots = static_cast<size_t>(plan->ctas) * kWarps + units;
+    const size_t heads = static_cast<size_t>(plan->nt) * 8;
+    plan->off_ml = 0;
+    plan->off_o = (slots * heads * 8 + 255) & ~static_cast<size_t>(255);
+    plan->total = plan->off_o + slots * heads * D * 4;
+    return KVD_OK;
+}
+
+int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream) {
+    if (dtype == KVD_F32) {
+        if (D == 128)
+            return plan.nt == 1 ? launch_q4<128, 1, true>(plan, p, stream)
+                                : launch_q4<128, 2, true>(plan, p, stream);
+        return plan.nt == 1 ? launch_q4<64, 1, true>(plan, p, stream)
+                            : launch_q4<64, 2, true>(plan, p, stream);
+    }
+    if (D == 128)
+        return plan.nt == 1 ? launch_q4<128, 1, false>(plan, p, stream)
+                            : launch_q4<128, 2, false>(plan, p, stream);
+    return plan.nt == 1 ? launch_q4<64, 1, false>(plan, p, stream)
+                        : launch_q4<64, 2, false>(plan, p, stream);
+}
+
+}  // namespace kvd

@@ -164,6 +164,51 @@ struct AppendParams {
 };
 int append_launch(const AppendParams& p, cudaStream_t stream);
 
+// Arguments of the rotated append (rope_append.cu): T new tokens of B sequences.
+struct RopeAppendParams {
+    const void *q, *k, *v;     // [T, Hq or Hkv, D], tokens q_stride / k_stride / v_stride apart
+    const float* cos_sin;      // [max_pos, rot]: rot / 2 cosines, then rot / 2 sines
+    const int32_t* cu_seqlens; // [B + 1] first row of each sequence; null: one token each
+    const int32_t* block_table;
+    const int32_t* seq_lens;   // lengths with the new tokens
+    void* q_out;               // [T, Hq, D]
+    void *k_pool, *v_pool;     // [num_pages, Hkv, page_size, D], or 4-bit pages
+    void *k_out, *v_out;       // 4 bits: [T, Hkv, D] the stored values (optional)
+    int* err;                  // optional
+    long long q_stride, k_stride, v_stride;  // elements
+    int B, T, Hq, Hkv, rows;   // rows = Hq (0 without q) + 2 Hkv
+    int rot, interleaved, max_pos, page_shift, max_pages, num_pages, window, n_sink;
+};
+int rope_append_launch(const RopeAppendParams& p, bool q4, int D, int dtype,
+                       cudaStream_t stream);
+
+// Arguments of the attention over a 4-bit cache (gqa_q4_decode.cu).
+struct Q4Params {
+    const void* q;
+    const uint8_t *k_pool, *v_pool;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const float* sink_logit;
+    void* out;
+    float* lse_out;
+    float* part_o;             // [slots, heads of a block, D], one slot per (warp, unit) piece
+    float* part_ml;            // [slots, heads of a block, 2]: maximum (log2 domain) and sum
+    int* err;                  // optional
+    int B, Hq, Hkv, G, NHG;    // NHG: head blocks of a KV head
+    int HU;                    // units of a sequence: Hkv * NHG
+    int n_warps;               // warps that share the tile list
+    int page_shift, max_pages, num_pages, max_len;
+    int window, n_sink, ring;  // as GqaParams
+    float scale_log2;
+};
+struct Q4Plan {
+    int nt;                    // 8-head column tiles of a head block (1 or 2)
+    int NHG, units, ctas;
+    size_t off_ml, off_o, total;
+};
+int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan* plan);
+int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream);
+
 // Arguments of the Quest kernels (page summaries, page selection, attention over the pages).
 struct QuestParams {
     const void* q;             // [B, Hq, D]

@@ -1,0 +1,302 @@
+"""GPU: attention over the 4-bit cache against the float64 definition on the same stored values
+(tests/q4_reference.py, which derives each output's bound), and the whole decode chain: rotated
+append into 4 bits, then attention."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import q4_reference as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module")
+def kvd():
+    import kv_cache_decode_split_gb300 as m
+    return m
+
+
+class Case:
+    def __init__(self, lens, Hq, Hkv, D, P, dtype=BF, window=0, n_sink=0, ring=False, learned=False,
+                 seed=0, scale=None, vscale=1.0, qscale=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.D, self.P, self.dtype = list(lens), D, P, dtype
+        self.window, self.n_sink, self.ring = window, n_sink, ring
+        self.scale = 1 / math.sqrt(D) if scale is None else scale
+        cap = window + n_sink
+        self.bt, self.pages = R.make_table([cap] * len(lens) if ring else lens, P, g)
+        self.kp = R.make_pool(self.pages, Hkv, P, D, True, seed + 1)
+        self.vp = R.make_pool(self.pages, Hkv, P, D, False, seed + 2, vscale)
+        self.q = (torch.randn(len(lens), Hq, D, generator=g) * qscale).to(dtype)
+        self.sink = torch.randn(Hq, generator=g) * 2 if learned else None
+
+    def gpu(self):
+        return dict(q=self.q.to(DEV), k_pool=torch.from_numpy(self.kp).to(DEV),
+                    v_pool=torch.from_numpy(self.vp).to(DEV), block_table=self.bt.to(DEV),
+                    seq_lens=torch.tensor(self.lens, dtype=I32, device=DEV), window=self.window,
+                    n_sink_tokens=self.n_sink, ring=self.ring, scale=self.scale,
+                    sink_logit=None if self.sink is None else self.sink.to(DEV))
+
+    def check(self, out, lse, exclude=()):
+        ref, rl, tol, tol_l = R.attention(
+            self.q.float().numpy(), self.kp, self.vp, self.bt.numpy(), self.lens, self.D, self.P,
+            self.scale, self.window, self.n_sink, self.ring,
+            None if self.sink is None else self.sink.numpy())
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        # one rounding to the output's type
+        tol = tol + np.abs(ref) * float(torch.finfo(self.dtype).eps) / 2 + 1e-30
+        d = np.abs(out - ref)
+        assert (d <= tol).all(), f"out: {np.max(d / tol):.3g} of the bound at {np.unravel_index(np.argmax(d / tol), d.shape)}"
+        none = np.isneginf(rl)
+        assert np.array_equal(np.isneginf(lse), none)
+        dl = np.abs(np.where(none, 0, lse) - np.where(none, 0, rl))
+        assert (dl <= tol_l).all(), f"lse: {np.max(dl - tol_l):.3g} past its bound"
+
+
+def run(kvd, c, **kw):
+    a = c.gpu()
+    a.update(kw)
+    lse = torch.full(c.q.shape[:2], 55.0, device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    out = kvd.attn_decode_gqa_q4(**a, lse_out=lse, err=err)
+    torch.cuda.synchronize()
+    return out, lse, int(err.item())
+
+
+def check(kvd, c):
+    out, lse, err = run(kvd, c)
+    assert err == 0
+    c.check(out, lse)
+
+
+LENS = [0, 1, 15, 16, 17, 31, 32, 33, 64, 100, 255, 513]
+
+
+@pytest.mark.parametrize("D,P", [(64, 16), (64, 64), (128, 16), (128, 32), (128, 256)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lengths(kvd, dtype, D, P):
+    check(kvd, Case(LENS, 8, 2, D, P, dtype, seed=D + P))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (14, 2), (9, 1), (16, 1), (24, 1), (40, 2), (128, 1)])
+@pytest.mark.parametrize("D,dtype", [(64, F32), (128, BF), (64, BF), (128, F32)])
+def test_head_groups(kvd, Hq, Hkv, D, dtype):
+    check(kvd, Case([3, 77, 200], Hq, Hkv, D, 32, dtype, seed=Hq))
+
+
+@pytest.mark.parametrize("window,n_sink,learned", [(1, 0, False), (17, 3, True), (100, 4, False),
+                                                    (64, 40, True), (5000, 4, True), (32, 0, True)])
+@pytest.mark.parametrize("ring", [False, True])
+def test_windows_and_rings(kvd, window, n_sink, learned, ring):
+    cap = window + n_sink
+    lens = [0, 1, n_sink + 1, max(1, cap - 1), cap, cap + 1, 2 * cap + 35]
+    check(kvd, Case(lens, 8, 2, 64, 16, window=window, n_sink=n_sink, ring=ring, learned=learned,
+                    seed=window))
+    check(kvd, Case(lens[-3:], 4, 4, 128, 64, F32 if ring else BF, window=window, n_sink=n_sink,
+                    ring=ring, learned=learned, seed=window))
+
+
+def test_ring_lengths_are_unbounded(kvd):
+    check(kvd, Case([2 ** 31 - 1, 10 ** 6, 3], 4, 1, 64, 16, window=40, n_sink=4, ring=True))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_sequences_are_cut_and_joined(kvd, dtype):
+    check(kvd, Case([20011, 1, 9000], 4, 2, 128, 64, dtype, learned=True, seed=9))
+
+
+def test_large_scores_and_uneven_values(kvd):
+    # sharp weights, negative scale, values of very different sizes from token to token
+    check(kvd, Case([700, 33], 8, 2, 128, 16, qscale=20.0, seed=11))
+    check(kvd, Case([700, 33], 8, 2, 64, 16, scale=-0.5, seed=12))
+    c = Case([900], 4, 1, 128, 64, seed=13)
+    code, s, b = R.unpack(c.vp, 128, False)
+    f = (10.0 ** np.random.default_rng(0).uniform(-4, 3, s.shape[:3]))[..., None]
+    c.vp = R.pack(code, (s * f).astype(np.float16), (b * f).astype(np.float16), False)
+    check(kvd, c)
+
+
+def test_unused_slots_may_hold_anything(kvd):
+    # bytes 0xFF (NaN scales) behind each sequence's end and in unused pages
+    for P in (16, 64):
+        c = Case([1, 17, 40, 100], 8, 2, 128, P, seed=21)
+        for pool, is_k in ((c.kp, True), (c.vp, False)):
+            code, s, b = R.unpack(pool, 128, is_k)
+            used = np.zeros(s.shape[:1] + (P,), bool)
+            for i, L in enumerate(c.lens):
+                for t in range(L):
+                    used[c.bt[i, t // P], t % P] = True
+            free = ~used[:, None, :, None]
+            pool[:] = R.pack(np.where(free, 15, code).astype(np.uint8),
+                             np.where(free, np.float16(np.nan), s), np.where(free, np.float16(np.nan), b), is_k)
+        check(kvd, c)
+
+
+def test_nan_rows_reach_their_heads_only(kvd):
+    c = Case([50, 50], 4, 2, 64, 16, seed=22)
+    code, s, b = R.unpack(c.kp, 64, True)
+    b = b.copy()
+    b[int(c.bt[1, 1]), 1, 3] = np.nan     # sequence 1, token 19, KV head 1
+    c.kp = R.pack(code, s, b, True)
+    out, lse, err = run(kvd, c)
+    bad = torch.isnan(out).all(-1)
+    assert err == 0 and bad.tolist() == [[False] * 4, [False, False, True, True]]
+
+
+def test_repeated_calls_and_any_workspace_are_bit_equal(kvd):
+    big, small = Case([3000, 70, 1], 16, 2, 128, 16, seed=31), Case([5, 900], 8, 8, 64, 64, seed=32)
+    n = max(kvd.kvd_workspace_size("gqa_q4", 3, 16, 2, 128, big.bt.shape[1] * 16),
+            kvd.kvd_workspace_size("gqa_q4", 2, 8, 8, 64, small.bt.shape[1] * 64))
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    first = {}
+    for c in (big, small, big, small):
+        out, lse, err = run(kvd, c, workspace=ws)
+        assert err == 0
+        if id(c) in first:
+            assert torch.equal(out, first[id(c)][0]) and torch.equal(lse, first[id(c)][1])
+        else:
+            c.check(out, lse)
+            first[id(c)] = (out, lse)
+    out, _, _ = run(kvd, big, workspace=kvd.Workspace(DEV))
+    assert torch.equal(out, first[id(big)][0])
+
+
+def test_bad_lengths_and_pages_are_flagged(kvd):
+    c = Case([40, 60], 4, 2, 64, 16, seed=41)
+    bt = c.bt.clone()
+    bt[1, 2] = c.pages + 7
+    out, lse, err = run(kvd, c, block_table=bt.to(DEV))
+    assert err == -6 and torch.isfinite(out).all()
+    good, _, _ = run(kvd, c)
+    assert torch.equal(out[0], good[0])
+    for lens in ([40, -1], [40, c.bt.shape[1] * 16 + 1]):
+        bt = c.bt.clone()
+        bt[bt < 0] = 0
+        out, _, err = run(kvd, c, seq_lens=torch.tensor(lens, dtype=I32, device=DEV),
+                          block_table=bt.to(DEV))
+        assert err == -6 and torch.isfinite(out).all() and torch.equal(out[0], good[0])
+
+
+def test_refusals_of_the_binding(kvd):
+    a = Case([40, 60], 4, 2, 64, 16).gpu()
+    for name, bad, what in (("q", a["q"].transpose(0, 1), ValueError), ("q", a["q"].half(), TypeError),
+                            ("k_pool", a["k_pool"][..., :-4].contiguous(), ValueError),
+                            ("v_pool", a["v_pool"][:2], ValueError),
+                            ("block_table", a["block_table"].long(), TypeError),
+                            ("seq_lens", a["seq_lens"][:1], ValueError),
+                            ("sink_logit", torch.zeros(3, device=DEV), ValueError)):
+        with pytest.raises(what):
+            kvd.attn_decode_gqa_q4(**{**a, name: bad})
+    with pytest.raises(kvd.KvdError) as e:
+        kvd.attn_decode_gqa_q4(**a, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))
+    assert e.value.status == -5
+    with pytest.raises(kvd.KvdError):
+        kvd.attn_decode_gqa_q4(**{**a, "ring": True})
+
+
+def test_offsets_past_32_bits(kvd):
+    # pages in the last of more than 4 GiB of each pool
+    P, D, Hkv = 64, 128, 8
+    page = kvd.q4_page_bytes(P, D) * Hkv
+    pages = (5 << 30) // page
+    c = Case([100, 200], 16, Hkv, D, P, seed=51)
+    a = c.gpu()
+    for n in ("k_pool", "v_pool"):
+        big = torch.empty(pages, Hkv, page // Hkv, dtype=torch.uint8, device=DEV)
+        big[pages - c.pages:] = a[n]
+        a[n] = big
+    a["block_table"] = torch.where(a["block_table"] >= 0, a["block_table"] + pages - c.pages, -1).to(I32)
+    lse = torch.empty(2, 16, device=DEV)
+    out = kvd.attn_decode_gqa_q4(**a, lse_out=lse)
+    c.check(out, lse)
+
+
+def test_two_streams_and_two_graphs_at_once(kvd):
+    # without a workspace of the caller's, calls that run at the same time share nothing
+    cases = [Case([6000, 3000], 8, 2, 128, 64, seed=61), Case([5000, 100, 900], 8, 2, 128, 64, seed=62)]
+    args = [c.gpu() for c in cases]
+    want = [kvd.attn_decode_gqa_q4(**a) for a in args]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in cases], [], []
+    torch.cuda.synchronize()
+    for a, s in zip(args, streams):
+        outs.append([kvd.attn_decode_gqa_q4(**a, stream=s) for _ in range(20)])
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert all(torch.equal(x, w) for x in got)
+    outs = []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(kvd.attn_decode_gqa_q4(**a))
+        graphs.append(g)
+    for _ in range(10):
+        for x in outs:
+            x.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, w) for x, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("D,dtype,window,n_sink,ring", [(128, BF, 0, 0, False), (64, F32, 24, 2, True),
+                                                        (64, BF, 40, 4, False)])
+def test_decode_chain(kvd, D, dtype, window, n_sink, ring):
+    """A prompt, then single tokens: rotated append into 4 bits and attention, captured as one graph
+    whose inputs change; each step against the definition over the values handed back."""
+    B, Hq, Hkv, P, prompt, steps = 3, 8, 2, 16, [50, 7, 1], 40
+    g = torch.Generator().manual_seed(71)
+    lens = torch.tensor(prompt, dtype=I32)
+    cap = window + n_sink
+    bt, pages = R.make_table([cap if ring else n + steps for n in prompt], P, g)
+    kp, vp = kvd.q4_pool(pages, Hkv, P, D), kvd.q4_pool(pages, Hkv, P, D)
+    table = R.table(max(prompt) + steps, D).to(DEV)
+    bt_d, sl = bt.to(DEV), lens.to(DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    W = dict(window=window if ring else 0, n_sink=n_sink if ring else 0)
+    T = sum(prompt)
+    mk = lambda n, h: torch.randn(n, h, D, generator=g).to(dtype).to(DEV)
+    cu = torch.tensor(np.cumsum([0] + prompt), dtype=I32, device=DEV)
+    ko, vo = torch.empty(T, Hkv, D, dtype=dtype, device=DEV), torch.empty(T, Hkv, D, dtype=dtype, device=DEV)
+    kvd.rope_append_q4(mk(T, Hq), mk(T, Hkv), mk(T, Hkv), table, kp, vp, bt_d, sl, cu_seqlens=cu,
+                       k_out=ko, v_out=vo, err=err, **W)
+    q, k, v = mk(B, Hq), mk(B, Hkv), mk(B, Hkv)
+    k1, v1 = torch.empty_like(k), torch.empty_like(v)
+    lse = torch.empty(B, Hq, device=DEV)
+    q_rot, out = torch.empty_like(q), torch.empty_like(q)
+
+    def step():
+        sl.add_(1)
+        kvd.rope_append_q4(q, k, v, table, kp, vp, bt_d, sl, q_out=q_rot, k_out=k1, v_out=v1, err=err, **W)
+        kvd.attn_decode_gqa_q4(q_rot, kp, vp, bt_d, sl, window=window, n_sink_tokens=n_sink, ring=ring,
+                               out=out, lse_out=lse, err=err)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(steps):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=g).to(dtype))
+        graph.replay()
+        lens += 1
+        torch.cuda.synchronize()
+        if i not in (0, 1, 17, steps - 1):
+            continue
+        # what was handed back is what the cache holds
+        for b in range(B):
+            r = R.slot_of(int(lens[b]) - 1, W["window"], W["n_sink"])
+            pg, at = int(bt[b, r // P]), r % P
+            held = R.value(*(a[:, at] for a in R.unpack(kp[pg].cpu().numpy(), D, True)))
+            assert torch.equal(torch.from_numpy(held).to(dtype), k1[b].cpu())
+        c = Case.__new__(Case)
+        c.q, c.kp, c.vp, c.bt, c.lens = q_rot.cpu(), kp.cpu().numpy(), vp.cpu().numpy(), bt, lens.tolist()
+        c.D, c.P, c.dtype, c.scale, c.sink = D, P, dtype, 1 / math.sqrt(D), None
+        c.window, c.n_sink, c.ring = window, n_sink, ring
+        c.check(out, lse)
+    assert int(err.item()) == 0

@@ -1,0 +1,153 @@
+"""The rotated append, the 4-bit rows and the attention over them without a GPU: the reference's own
+layout, and every host-side refusal (none reaches a launch)."""
+import ctypes
+import os
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from tests import q4_reference as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def kvd():
+    sys.path.insert(0, ROOT)
+    import __graft_entry__ as g
+    g._builder().build()
+    import kv_cache_decode_split_gb300 as m
+    return m
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("is_k", [True, False])
+def test_layout_holds_every_code_once(D, is_k):
+    word, bit = R._address(D, is_k)
+    assert len({(w, b) for w, b in zip(word.ravel(), bit.ravel())}) == 16 * D
+    assert word.max() == 2 * D - 1
+    # every word belongs to one token
+    owner = {}
+    for r in range(16):
+        for w in word[r]:
+            assert owner.setdefault(w, r) == r
+    rng = np.random.default_rng(D)
+    code = rng.integers(0, 16, (3, 2, 32, D)).astype(np.uint8)
+    s, b = rng.random((2, 3, 2, 32, D // 64)).astype(np.float16)
+    got = R.unpack(R.pack(code, s, b, is_k), D, is_k)
+    assert all(np.array_equal(x, y) for x, y in zip(got, (code, s, b)))
+
+
+def test_reference_quantiser_is_within_half_a_step():
+    # |x - value| <= s / 2, what f16 rounding of b and s moves (2^-11 of b, 15 * 2^-11 of s) and
+    # the float32 steps
+    x = np.random.default_rng(0).standard_normal((100, 128)).astype(np.float32) * 3
+    code, s, b = R.quantise(x)
+    err = np.abs(R.value(code, s, b).astype(np.float64) - x).reshape(100, 2, 64).max(-1)
+    s, b = s.astype(np.float64), np.abs(b.astype(np.float64))
+    assert (err <= s * (0.5 + 16 * 2.0 ** -11) + b * 2.0 ** -11 + 1e-6).all()
+
+
+def test_page_bytes(kvd):
+    assert kvd.q4_page_bytes(16, 128) == 1152 and kvd.q4_page_bytes(64, 64) == 2304
+    assert kvd.lib.kvd_q4_page_bytes(48, 128) == 0 and kvd.lib.kvd_q4_page_bytes(64, 96) == 0
+    assert R.block_bytes(128) == 1152 and R.block_bytes(64) == 576
+    with pytest.raises(kvd.KvdError):
+        kvd.q4_page_bytes(8, 64)
+    assert kvd.q4_pool(3, 2, 16, 64, device="cpu").shape == (3, 2, 576)
+
+
+BASE = 1 << 24
+
+
+def _append(lib, q4=False, **kw):
+    a = dict(q=1, k=2, v=3, cs=4, cu=5, bt=6, sl=7, qo=8, kp=9, vp=10, ko=11, vo=12, B=2, T=6,
+             Hq=8, Hkv=2, D=64, qs=512, ks=128, vs=128, rot=64, inter=0, mp=100, P=16, max_pages=4,
+             num_pages=8, dt=1, W=0, ns=0, err=13)
+    at = {n: (BASE * a[n] if a[n] else None) for n in
+          ("q", "k", "v", "cs", "cu", "bt", "sl", "qo", "kp", "vp", "ko", "vo", "err")}
+    for n, v in kw.items():
+        (at if n in at else a)[n] = v
+    p = lambda n: None if at[n] is None else ctypes.c_void_p(at[n])
+    outs = ["qo", "kp", "vp"] + (["ko", "vo"] if q4 else [])
+    f = lib.kvd_rope_append_q4 if q4 else lib.kvd_rope_append
+    return f(*[p(n) for n in ["q", "k", "v", "cs", "cu", "bt", "sl"] + outs], a["B"], a["T"],
+             a["Hq"], a["Hkv"], a["D"], a["qs"], a["ks"], a["vs"], a["rot"], a["inter"], a["mp"],
+             a["P"], a["max_pages"], a["num_pages"], a["dt"], a["W"], a["ns"], p("err"), None)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_append_refusals(kvd, q4):
+    call = lambda **kw: _append(kvd.lib, q4, **kw)
+    for n in ("k", "v", "cs", "bt", "sl", "kp", "vp"):
+        assert call(**{n: None}) == -1, n
+        assert call(**{n: BASE + 2}) == -1, n              # misaligned
+    assert call(q=None) == -1 and call(qo=None) == -1      # q and q_out go together
+    assert call(cu=None) == -1                             # T != B without offsets
+    assert call(B=0) == -1 and call(T=-1) == -1 and call(Hkv=0) == -1 and call(Hq=0) == -1
+    assert call(mp=0) == -1 and call(num_pages=0) == -1 and call(max_pages=0) == -1
+    assert call(D=96) == -2 and call(P=48) == -2 and call(P=512) == -2 and call(P=8) == -2
+    assert call(dt=7) == -2
+    assert call(rot=0) == -2 and call(rot=72) == -2 and call(rot=80) == -2 and call(rot=24) == -2
+    assert call(W=-1) == -1 and call(ns=4) == -1           # sinks only of a rolling cache
+    assert call(W=62, ns=3) == -1                          # ring larger than its table
+    assert call(ks=64) == -1 and call(qs=500) == -1        # tokens overlap
+    assert call(ks=132) == -1 and call(vs=130) == -1       # not 16 bytes apart
+    assert call(err=BASE + 1) == -1 and call(cu=BASE + 2) == -1
+    # outputs on inputs: only q_out == q, dense
+    assert call(qo=BASE, qs=640) == -1
+    assert call(qo=BASE + 16) == -1
+    assert call(qo=2 * BASE) == -1
+    if q4:
+        assert call(ko=2 * BASE) == -1 and call(vo=BASE + 64) == -1
+    # nothing to do is no error, and nothing is launched
+    assert call(T=0, k=None, v=None, cs=None) == 0
+
+
+def _attn(lib, **kw):
+    a = dict(q=1, kp=2, vp=3, bt=4, sl=5, out=6, lse=7, sink=None, ws=8, err=9, B=2, Hq=8, Hkv=2,
+             D=64, P=16, max_pages=4, num_pages=8, scale=0.125, dt=1, W=0, ns=0, ring=0,
+             ws_bytes=1 << 34)
+    at = {n: (BASE * a[n] if a[n] else None) for n in
+          ("q", "kp", "vp", "bt", "sl", "out", "lse", "sink", "ws", "err")}
+    for n, v in kw.items():
+        (at if n in at else a)[n] = v
+    p = lambda n: None if at[n] is None else ctypes.c_void_p(at[n])
+    return lib.attn_decode_gqa_q4(p("q"), p("kp"), p("vp"), p("bt"), p("sl"), p("out"), p("lse"),
+                                  a["B"], a["Hq"], a["Hkv"], a["D"], a["P"], a["max_pages"],
+                                  a["num_pages"], a["scale"], a["dt"], a["W"], a["ns"], a["ring"],
+                                  p("sink"), p("ws"), a["ws_bytes"], p("err"), None)
+
+
+def test_attention_refusals(kvd):
+    call = lambda **kw: _attn(kvd.lib, **kw)
+    for n in ("q", "kp", "vp", "bt", "sl", "out", "ws"):
+        assert call(**{n: None}) == -1, n
+        assert call(**{n: BASE + 2}) == -1, n
+    for n in ("lse", "sink", "err"):
+        assert call(**{n: BASE + 2}) == -1, n
+    assert call(B=0) == -1 and call(Hq=7) == -1 and call(max_pages=0) == -1
+    assert call(scale=float("inf")) == -1
+    assert call(D=96) == -2 and call(P=24) == -2 and call(dt=2) == -2 and call(Hq=512) == -2
+    assert call(W=-1) == -1 and call(W=4, ns=-1) == -1
+    assert call(ns=4) == -1 and call(ring=1) == -1         # without a window
+    assert call(W=61, ns=4, ring=1) == -1                  # ring larger than its table
+    assert call(ws_bytes=64) == -5
+    assert kvd.kvd_workspace_size("gqa_q4", 2, 8, 2, 64, 64) > 0
+    assert kvd.kvd_workspace_size("gqa_q4", 2, 8, 3, 64, 64) == 0
+    assert kvd.kvd_workspace_size("gqa_q4", 2, 8, 2, 96, 64) == 0
+
+
+def test_host_tensors_are_refused(kvd):
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        kvd.rope_append(z(2, 8, 64), z(2, 2, 64), z(2, 2, 64), z(9, 64), z(4, 2, 16, 64),
+                        z(4, 2, 16, 64), i(2, 2), i(2))
+    pool = kvd.q4_pool(4, 2, 16, 64, device="cpu")
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        kvd.rope_append_q4(None, z(2, 2, 64), z(2, 2, 64), z(9, 64), pool, pool, i(2, 2), i(2))
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        kvd.attn_decode_gqa_q4(z(2, 8, 64), pool, pool, i(2, 2), i(2))
