@@ -10,19 +10,22 @@
 //
 // GB300. 4 bits quarter the bytes but not the elements: at the measured copy bandwidth an SM has
 // about 2.7 lane operations for each element it reads, so what matters is instructions per
-// element. Codes go from shared memory to matrix-instruction fragments with one shift and one
-// three-input logic operation per two elements: code c in mantissa bits 3-6 under the exponent of
-// 16 is the bf16 number 16 + c, exactly. (Feeding tcgen05 would write every element back to
+// element, logic and shift operations (half rate) first of all. Codes go from shared memory to
+// matrix-instruction fragments with one shift and one three-input logic operation per two
+// elements: code bits placed in the mantissa under a fixed exponent are the number 16 + c (keys,
+// bf16) or 64 + c (values, float16), exactly. (Feeding tcgen05 would write every element back to
 // shared memory as 16 bits first, which alone costs more than the whole budget; with at most 16
-// query rows its rate is not needed.) The offset 16 is taken out of the scores through the
-// accumulator's start value, -16 sum(q_g). For the values, odd tokens are decoded with the sign
-// flipped and the code complemented, -(16 + 15 - c) = c - 31: offsets +16 and -31 average to the
-// middle of the code range, so the sums stay small over long sequences, and each token's minimum
-// is corrected by its own offset.
+// query rows its rate is not needed.) The scores' offset is taken out with the group's minimum,
+// (b - 16 s) sum(q_g). Of the values, odd tokens are decoded with the sign
+// flipped and the code complemented, -(64 + 15 - c) = c - 79: the offsets 64 and -79 average to
+// the middle of the code range, so the sums stay small over long sequences; one more matrix
+// product, of a constant with the same rounded weights, takes them out again.
 //   scores^T [16 tokens x 8 heads] = K codes [16 x D] q^T           (mma.sync m16n8k16, fp32 sums)
 //   O^T [16 channels x 8 heads]   += V codes^T [16 x 16 tokens] (p s)^T
-// p s enters as the sum of two bf16 numbers (16 bits; three for float32 queries), so that rounding
-// the weights adds nothing to the output's own rounding.
+// p s is a float16 number (11 bits; two for float32 queries), so that rounding the weights adds
+// little to the output's own rounding. The softmax reference m is the largest score plus
+// logarithm of its scale, rather than the largest score: then p s fits float16 whatever the
+// values' sizes. It is raised only when a product leaves the range.
 //
 // Work is divided over all warps of the grid: the visible 32-token tiles of all (sequence, KV
 // head, head block) units form one list, and warp i of N (at most one for each tile) takes tiles
@@ -32,6 +35,7 @@
 // the whole unit. A second launch joins the partials of the units that were cut.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvd_device.cuh"
 #include "kvd_host.h"
@@ -94,29 +98,51 @@ __device__ __forceinline__ Schedule schedule_of(const Q4Params& p, int b_want, i
     return s;
 }
 
-// c[16x8] += a[16x16] * b[16x8], bf16 inputs, fp32 sums (not volatile: it may be reordered).
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+// c[16x8] += a[16x16] * b[16x8], fp32 sums (not volatile: they may be reordered).
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-constexpr uint32_t kMask = 0x00780078u;
-constexpr uint32_t kKey = 0x41804180u;   // 16 + c in both halves
-constexpr uint32_t kVal = 0xC1F84180u;   // low half 16 + c, high half c - 31
+// Keys: 16 + c as bf16, code bits under mantissa bits 3-6.
+constexpr uint32_t kKeyMask = 0x00780078u, kKey = 0x41804180u;
+// Values: float16, code bits at mantissa bits 4-7: 64 + c, for odd tokens (the high halves)
+// -(64 + 15 - c) = c - 79.
+constexpr uint32_t kValMask = 0x00F000F0u, kVal = 0xD4F05400u, kVal64 = 0x54005400u;
+constexpr uint32_t kValOff = 0x54F0D400u;  // minus the offsets: -64 and 79
 
-// 16 + c -> c - 8 (exact), for float32 queries: nothing is left to cancel
-__device__ __forceinline__ uint32_t centre(uint32_t x) {
+// A constant that stays in a register (a logic instruction takes one immediate, and the compiler
+// would rather split it in two): read back from shared memory.
+__device__ __forceinline__ uint32_t read_shared(const uint32_t* p) {
+    uint32_t r;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+
+// Codes with their offset -> c - 8 (exact), for float32 queries: nothing is left to cancel.
+__device__ __forceinline__ uint32_t centre_key(uint32_t x) {
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x),
                                      __floats2bfloat162_rn(24.f, 24.f));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t centre_val(uint32_t x) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&x), __floats2half2_rn(72.f, 72.f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-// x as a sum of kSplit bf16 numbers: part k of two values, packed.
+// Two values as sums of kSplit bf16 numbers, part k of both packed.
 template <int kSplit>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&part)[kSplit]) {
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t (&part)[kSplit]) {
 #pragma unroll
     for (int k = 0; k < kSplit; ++k) {
         part[k] = pack_bf16(x, y);
@@ -127,12 +153,10 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&part)[kSplit
     }
 }
 
-struct TileInfo {  // written with each tile's copies, read by the warp that uses the tile
-    int T, lo, hi;    // first token; the visible ones are lo <= t < hi
-    int b, u;         // sequence, unit of the sequence
-    int flags;        // 1 first tile of the warp's piece, 2 last; 4 first tile of the unit, 8 last
-    int pad[2];
-};
+// A tile as the warp that uses it sees it: the unit, and bits 0 first tile of the warp's piece of
+// the unit, 1 last, 2 first tile of the unit, 3 last, 4 not all of its tokens visible; from bit 8
+// the first visible token of the tile, from bit 16 the one behind the last.
+using TileInfo = int2;
 
 template <int D, int NT, bool kF32>
 struct Q4Cfg {
@@ -140,7 +164,7 @@ struct Q4Cfg {
     static constexpr int kTileBytes = 4 * Q4<D>::kBlockBytes;  // K and V, two blocks each
     static constexpr int kRing = kStages * kTileBytes;
     static constexpr int kPerWarp = kRing + kStages * static_cast<int>(sizeof(TileInfo) + 8);
-    static constexpr int kSmem = kWarps * kPerWarp;
+    static constexpr int kSmem = kWarps * kPerWarp + 16;
     static constexpr int kCtas = (NT == 1 && !kF32) ? 2 : 1;   // per SM (registers)
 };
 
@@ -154,7 +178,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
     constexpr int KW = D / 32;             // key words of a lane and row
     constexpr int MT = D / 16;             // 16-channel tiles of the output
     constexpr int kQ = kF32 ? 3 : 1;       // bf16 parts of a query
-    constexpr int kP = kF32 ? 3 : 2;       // bf16 parts of a weight
+    constexpr int kP = kF32 ? 2 : 1;       // float16 parts of a weight
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
@@ -162,11 +186,15 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
     TileInfo* info = reinterpret_cast<TileInfo*>(smem + kWarps * Cfg::kRing) + warp * S;
     uint64_t* full = reinterpret_cast<uint64_t*>(
                          smem + kWarps * (Cfg::kRing + S * sizeof(TileInfo))) + warp * S;
+    uint32_t* masks = reinterpret_cast<uint32_t*>(smem + kWarps * Cfg::kPerWarp);
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
+        masks[0] = kKeyMask;  // (every warp writes the same)
+        masks[1] = kValMask;
     }
     __syncwarp();
+    const uint32_t key_mask = read_shared(masks), val_mask = read_shared(masks + 1);
     griddep_wait();
 
     // ---- this warp's share of the tile list, and where it begins
@@ -176,17 +204,19 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
     const long long N = min(static_cast<long long>(p.n_warps), sch.total);
     if (me >= N) return;
     const long long begin = sch.total * me / N;
-    int left = static_cast<int>(sch.total * (me + 1) / N - begin);  // tiles to copy, at least 1
-    const int n_mine = left;
-    // cursor of the next tile to copy: sequence, unit, tile of the unit
-    int cb = 0, cu = 0, cj = 0, cn = 0;
-    Ranges cr{};
-    {
-        long long rem = begin;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            const int n = b < p.B ? seq_tiles(p, b) : 0;
-            long long inc = static_cast<long long>(n) * p.HU;
+    const int n_mine = static_cast<int>(sch.total * (me + 1) / N - begin);  // tiles, at least 1
+    // Tiles are looked up 32 at a time, lane k the k-th of the batch: its blocks in the pools
+    // (two when pages hold 16 tokens) and its TileInfo. That lane issues its copies.
+    int blk0 = 0, blk1 = 0;
+    TileInfo mine = make_int2(0, 0);
+    auto look_up = [&](int base) {  // tiles base .. base + 31 of this warp
+        long long rem = begin + base;
+        int b = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {  // the sequence that holds tile `base`
+            const int bl = b0 + lane;
+            const long long n =
+                bl < p.B ? static_cast<long long>(seq_tiles(p, bl)) * p.HU : 0;
+            long long inc = n;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const long long o = __shfl_up_sync(0xffffffffu, inc, off);
@@ -195,73 +225,64 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             const uint32_t past = __ballot_sync(0xffffffffu, inc > rem);
             if (past) {
                 const int k = __ffs(past) - 1;
-                cb = b0 + k;
-                cn = __shfl_sync(0xffffffffu, n, k);
-                rem -= __shfl_sync(0xffffffffu, inc, k) - static_cast<long long>(cn) * p.HU;
+                b = b0 + k;
+                rem -= __shfl_sync(0xffffffffu, inc - n, k);
                 break;
             }
             rem -= __shfl_sync(0xffffffffu, inc, 31);
         }
-        cu = static_cast<int>(rem / cn);
-        cj = static_cast<int>(rem % cn);
-        cr = seq_ranges(p, cb);
-    }
-    const uint64_t pol = l2_evict_first_policy();  // keys and values are read once
-    const int blk_shift = p.page_shift - 4;
-    auto cursor_tile = [&](int& lo, int& hi) -> int {
-        const int n0 = range_tiles(cr.lo0, cr.hi0);
-        if (cj < n0) {
-            lo = cr.lo0, hi = cr.hi0;
-            return ((lo >> 5) + cj) << 5;
+        if (base + lane >= n_mine) return;
+        rem += lane;
+        Ranges r = seq_ranges(p, b);
+        int n0 = range_tiles(r.lo0, r.hi0), n = n0 + range_tiles(r.lo1, r.hi1);
+        while (rem >= static_cast<long long>(n) * p.HU) {  // this lane's own tile is further on
+            rem -= static_cast<long long>(n) * p.HU;
+            r = seq_ranges(p, ++b);
+            n0 = range_tiles(r.lo0, r.hi0), n = n0 + range_tiles(r.lo1, r.hi1);
         }
-        lo = cr.lo1, hi = cr.hi1;
-        return ((lo >> 5) + cj - n0) << 5;
+        const int u = static_cast<int>(rem / n), j = static_cast<int>(rem - static_cast<long long>(u) * n);
+        const int kvh = u / p.NHG;
+        const int lo = j < n0 ? r.lo0 : r.lo1, hi = j < n0 ? r.hi0 : r.hi1;
+        const int T = ((lo >> 5) + (j < n0 ? j : j - n0)) * kTileTok;
+        const int v0 = max(lo - T, 0), v1 = min(hi - T, kTileTok);
+        mine.x = b * p.HU + u;
+        mine.y = ((base + lane == 0 || j == 0) ? 1 : 0) |
+                 ((base + lane == n_mine - 1 || j == n - 1) ? 2 : 0) | (j == 0 ? 4 : 0) |
+                 (j == n - 1 ? 8 : 0) | ((v0 > 0 || v1 < kTileTok) ? 16 : 0) | v0 << 8 | v1 << 16;
+        // pages of its first and last visible token
+        const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
+        int pg0 = __ldg(row + ((T + v0) >> p.page_shift));
+        int pg1 = p.page_shift == 4 ? __ldg(row + ((T + v1 - 1) >> 4)) : 0;
+        if (static_cast<unsigned>(pg0) >= static_cast<unsigned>(p.num_pages) ||
+            static_cast<unsigned>(pg1) >= static_cast<unsigned>(p.num_pages)) {
+            record_error(p.err, KVD_ERR_DEVICE_OOB);
+            if (static_cast<unsigned>(pg0) >= static_cast<unsigned>(p.num_pages)) pg0 = 0;
+            if (static_cast<unsigned>(pg1) >= static_cast<unsigned>(p.num_pages)) pg1 = 0;
+        }
+        blk0 = ((pg0 * p.Hkv + kvh) << (p.page_shift - 4)) +
+               ((T & ((1 << p.page_shift) - 1)) >> 4);
+        blk1 = pg1 * p.Hkv + kvh;
     };
-    // pages of the cursor's tile (two when pages hold 16 tokens), requested a tile ahead
-    int pg0 = 0, pg1 = 0;
-    auto fetch_pages = [&]() {
-        int lo, hi;
-        const int T = cursor_tile(lo, hi);
-        const int32_t* row = p.block_table + static_cast<size_t>(cb) * p.max_pages;
-        pg0 = __ldg(row + (max(T, lo) >> p.page_shift));
-        pg1 = __ldg(row + (min(T + kTileTok, hi) - 1 >> p.page_shift));
-    };
-    fetch_pages();
-    // copy the cursor's tile into stage s and move on
-    auto issue = [&](int s) {
-        if (left == 0) return;
-        int lo, hi;
-        const int T = cursor_tile(lo, hi);
-        if (lane == 0) {
-            TileInfo ti;
-            ti.T = T, ti.lo = lo, ti.hi = hi, ti.b = cb, ti.u = cu;
-            ti.flags = ((left == n_mine || cj == 0) ? 1 : 0) |
-                       ((left == 1 || cj == cn - 1) ? 2 : 0) | (cj == 0 ? 4 : 0) |
-                       (cj == cn - 1 ? 8 : 0);
-            info[s] = ti;
-            if (pg0 < 0 || pg0 >= p.num_pages || pg1 < 0 || pg1 >= p.num_pages) {
-                record_error(p.err, KVD_ERR_DEVICE_OOB);
-                if (pg0 < 0 || pg0 >= p.num_pages) pg0 = 0;
-                if (pg1 < 0 || pg1 >= p.num_pages) pg1 = 0;
-            }
-            const int kvh = cu / p.NHG;
+    const uint64_t pol = l2_evict_first_policy();  // keys and values are read once
+    // copy the warp's i-th tile into stage s
+    auto issue = [&](int s, int i) {
+        if ((i & 31) == 0) look_up(i);
+        if (lane == (i & 31)) {
+            info[s] = mine;
             uint8_t* st = ring + s * Cfg::kTileBytes;
             if (p.page_shift >= 5) {
-                const size_t off =
-                    (((static_cast<size_t>(pg0) * p.Hkv + kvh) << blk_shift) +
-                     ((T & ((1 << p.page_shift) - 1)) >> 4)) * L4::kBlockBytes;
+                const size_t off = static_cast<size_t>(blk0) * L4::kBlockBytes;
                 mbar_arrive_expect_tx(&full[s], Cfg::kTileBytes);
                 bulk_load(st, p.k_pool + off, 2 * L4::kBlockBytes, &full[s], pol);
                 bulk_load(st + 2 * L4::kBlockBytes, p.v_pool + off, 2 * L4::kBlockBytes, &full[s],
                           pol);
             } else {  // a block without visible tokens is not copied (all of it is masked)
-                const bool h0 = T + 16 > lo, h1 = T + 16 < hi;
+                const bool h0 = ((mine.y >> 8) & 63) < 16, h1 = ((mine.y >> 16) & 63) > 16;
                 mbar_arrive_expect_tx(&full[s], (h0 + h1) * 2 * L4::kBlockBytes);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (!(k ? h1 : h0)) continue;
-                    const size_t off =
-                        (static_cast<size_t>(k ? pg1 : pg0) * p.Hkv + kvh) * L4::kBlockBytes;
+                    const size_t off = static_cast<size_t>(k ? blk1 : blk0) * L4::kBlockBytes;
                     bulk_load(st + k * L4::kBlockBytes, p.k_pool + off, L4::kBlockBytes, &full[s],
                               pol);
                     bulk_load(st + (2 + k) * L4::kBlockBytes, p.v_pool + off, L4::kBlockBytes,
@@ -269,33 +290,27 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                 }
             }
         }
-        if (--left == 0) return;
-        if (++cj == cn) {
-            cj = 0;
-            if (++cu == p.HU) {
-                cu = 0;
-                do {
-                    ++cb;
-                    cr = seq_ranges(p, cb);
-                    cn = range_tiles(cr.lo0, cr.hi0) + range_tiles(cr.lo1, cr.hi1);
-                } while (cn == 0);
-            }
-        }
-        fetch_pages();
     };
-    for (int s = 0; s < S; ++s) issue(s);
+    for (int s = 0; s < min(S, n_mine); ++s) issue(s, s);
 
     // ---- state of the current piece
     uint32_t qf[kQ][NT][KW][4];
-    float q16[NT][NG][2], qsum[NT][NG][2];  // accumulator start and sum of q, heads 2t, 2t + 1
-    float o[NT][MT][4], ob[NT][NG][2], m[NT][2], l[NT][2];
+    float qsum[NT][NG][2];  // sums of q, heads 2t and 2t + 1
+    // o, and the values' offsets and minima in it: oo by the matrix product, ob in each lane
+    float o[NT][MT][4], oo[NT][NG][4], ob[NT][NG][2], m[NT][2], l[NT][2];
     bool from_start = false;
     const float sl2 = p.scale_log2;
 
+    // sequence, first query head, and number of heads of a unit
+    auto unit_of = [&](int unit) {
+        const int b = unit / p.HU, u = unit % p.HU;
+        const int kvh = u / p.NHG, hg = u % p.NHG;
+        return make_int4(b, kvh * p.G + hg * NT * 8, min(NT * 8, p.G - hg * NT * 8), 0);
+    };
+    int s = 0, phase = 0;
     for (int i = 0; i < n_mine; ++i) {
-        const int s = i % S;
         __syncwarp();
-        if (!mbar_wait(&full[s], (i / S) & 1, p.err)) {
+        if (!mbar_wait(&full[s], phase, p.err)) {
             // give up, once the copies in flight have landed (or their own limits have passed)
             if (lane == 0)
                 for (int k = i + 1; k < min(n_mine, i + S); ++k)
@@ -304,18 +319,15 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             return;
         }
         const TileInfo ti = info[s];
-        const int kvh = ti.u / p.NHG, hg = ti.u % p.NHG;
-        const int G_cta = min(NT * 8, p.G - hg * NT * 8);
-        const int hq0 = kvh * p.G + hg * NT * 8;  // first query head of the unit
-        if (ti.flags & 1) {
-            from_start = (ti.flags & 4) != 0;
+        if (ti.y & 1) {
+            const int4 un = unit_of(ti.x);
+            from_start = (ti.y & 4) != 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float part[NG] = {};
                 const int h = nt * 8 + g;
-                const bool ok = h < G_cta;
-                const size_t qrow =
-                    (static_cast<size_t>(ti.b) * p.Hq + hq0 + (ok ? h : 0)) * D;
+                const bool ok = h < un.z;
+                const size_t qrow = (static_cast<size_t>(un.x) * p.Hq + un.y + (ok ? h : 0)) * D;
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
                     float x[8];
@@ -343,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {  // fragments pair channels e and e + 4
                         uint32_t sp[kQ];
-                        split2<kQ>(x[e], x[e + 4], sp);
+                        split_bf16<kQ>(x[e], x[e + 4], sp);
 #pragma unroll
                         for (int k = 0; k < kQ; ++k) qf[k][nt][w][e] = sp[k];
                     }
@@ -354,18 +366,16 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                     part[gr] += __shfl_xor_sync(0xffffffffu, part[gr], 2);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float v = __shfl_sync(0xffffffffu, part[gr], (2 * t + c) * 4);
-                        qsum[nt][gr][c] = v;
-                        // codes centred on 8 (float32) leave 8 sum(q) to add, below
-                        q16[nt][gr][c] = kF32 ? 8.f * v : -16.f * v;
+                        qsum[nt][gr][c] = __shfl_sync(0xffffffffu, part[gr], (2 * t + c) * 4);
+                        ob[nt][gr][c] = 0.f;
                     }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) oo[nt][gr][r] = 0.f;
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     m[nt][c] = kNone;
                     l[nt][c] = 0.f;
-#pragma unroll
-                    for (int gr = 0; gr < NG; ++gr) ob[nt][gr][c] = 0.f;
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -375,9 +385,21 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
         }
         const uint8_t* kt = ring + s * Cfg::kTileBytes;
         const uint8_t* vt = kt + 2 * L4::kBlockBytes;
-        const bool ragged = ti.T < ti.lo || ti.T + kTileTok > ti.hi;
+        // tokens of this lane's score rows: 16 bk + 8 half + g, bit 2 bk + half of `seen`
+        // (two copies of the code: whole tiles do not look at them)
+        auto tile = [&](auto is_ragged) {
+        constexpr bool ragged = decltype(is_ragged)::value;
+        uint32_t seen = 15;
+        if constexpr (ragged) {
+            seen = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tok = 8 * k + g;
+                seen |= (tok >= ((ti.y >> 8) & 63) && tok < ((ti.y >> 16) & 63)) ? 1u << k : 0u;
+            }
+        }
 
-        // ---- scores of the two blocks
+        // ---- scores of the two blocks (before the softmax scale)
         float x[2][NT][4];
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk) {
@@ -398,77 +420,115 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[nt][gr][r] = kF32 ? 0.f : q16[nt][gr][r & 1];
+                    for (int r = 0; r < 4; ++r)
+                        acc[nt][gr][r] = 0.f;
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 uint32_t fa[4], fb[4];
-                fa[0] = (wa[w] & kMask) ^ kKey;
-                fb[0] = (wb[w] & kMask) ^ kKey;
-                fa[1] = ((wa[w] >> 4) & kMask) ^ kKey;
-                fb[1] = ((wb[w] >> 4) & kMask) ^ kKey;
-                fa[2] = ((wa[w] >> 8) & kMask) ^ kKey;
-                fb[2] = ((wb[w] >> 8) & kMask) ^ kKey;
-                fa[3] = (__funnelshift_r(wa[w], wa[w], 12) & kMask) ^ kKey;
-                fb[3] = (__funnelshift_r(wb[w], wb[w], 12) & kMask) ^ kKey;
+                fa[0] = (wa[w] & key_mask) ^ kKey;
+                fb[0] = (wb[w] & key_mask) ^ kKey;
+                fa[1] = ((wa[w] >> 4) & key_mask) ^ kKey;
+                fb[1] = ((wb[w] >> 4) & key_mask) ^ kKey;
+                fa[2] = ((wa[w] >> 8) & key_mask) ^ kKey;
+                fb[2] = ((wb[w] >> 8) & key_mask) ^ kKey;
+                fa[3] = (__funnelshift_r(wa[w], wa[w], 12) & key_mask) ^ kKey;
+                fb[3] = (__funnelshift_r(wb[w], wb[w], 12) & key_mask) ^ kKey;
                 if constexpr (kF32) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) fa[e] = centre(fa[e]), fb[e] = centre(fb[e]);
+                    for (int e = 0; e < 4; ++e)
+                        fa[e] = centre_key(fa[e]), fb[e] = centre_key(fb[e]);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < kQ; ++k) {
-                        mma(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
-                            qf[k][nt][w][1]);
-                        mma(acc[nt][w / 2], fa[2], fb[2], fa[3], fb[3], qf[k][nt][w][2],
-                            qf[k][nt][w][3]);
+                        mma_bf16(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
+                                 qf[k][nt][w][1]);
+                        mma_bf16(acc[nt][w / 2], fa[2], fb[2], fa[3], fb[3], qf[k][nt][w][2],
+                                 qf[k][nt][w][3]);
                     }
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const __half2* pr =
                     reinterpret_cast<const __half2*>(kb + L4::param(g + 8 * half, 0));
-                const int tok = ti.T + bk * 16 + g + 8 * half;
-                const bool in = !ragged || (tok >= ti.lo && tok < ti.hi);
-                float sg[NG], bg[NG];
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                    const float2 f = __half22float2(pr[gr]);
-                    sg[gr] = f.x, bg[gr] = f.y;
-                }
+                    const float2 f = __half22float2(pr[gr]);  // scale, minimum
+                    // codes were held as 16 + c, or centred as c - 8
+                    const float base = fmaf(kF32 ? 8.f : -16.f, f.x, f.y);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int gr = 0; gr < NG; ++gr) {
-                            float a = acc[nt][gr][2 * half + c];
-                            if (kF32) a += q16[nt][gr][c];
-                            v = fmaf(sg[gr], a, fmaf(bg[gr], qsum[nt][gr][c], v));
+                        for (int c = 0; c < 2; ++c) {
+                            float& v = x[bk][nt][2 * half + c];
+                            const float a = base * qsum[nt][gr][c];
+                            v = fmaf(f.x, acc[nt][gr][2 * half + c], gr ? v + a : a);
                         }
-                        x[bk][nt][2 * half + c] = in ? v * sl2 : neg_inf();
-                    }
+                }
             }
         }
-        // ---- running maximum: raised only when a score passes it by more than 8 (p <= 2^8
-        // until then, harmless in fp32 sums and in p's bf16 parts)
-        bool up = false;
-        float mx[NT][2];
+        // ---- weights: p = 2^{scaled score - m}, and p times the values' scales as float16
+        float vs[4][NG];  // scales of token 2 bk + half's groups
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int k = 0; k < 4; ++k) {
+            const __half2* pr = reinterpret_cast<const __half2*>(
+                vt + (k >> 1) * L4::kBlockBytes + L4::param(g + 8 * (k & 1), 0));
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                mx[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][2 + c]),
-                                  fmaxf(x[1][nt][c], x[1][nt][2 + c]));
-                up = up || mx[nt][c] > m[nt][c] + 8.f;
+            for (int gr = 0; gr < NG; ++gr) {
+                vs[k][gr] = __low2float(pr[gr]);
+                if (ragged && !((seen >> k) & 1))  // a masked slot may hold anything, NaN included
+                    vs[k][gr] = 0.f;
             }
-        if (__any_sync(0xffffffffu, up)) {
+        }
+        uint32_t y[NT][NG][kP][4];
+        float pw[2][NT][4];
+        bool over;
+        auto weights = [&]() {
+            __half2 top = __floats2half2_rn(0.f, 0.f);
+            float ptop = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float* pr = &pw[k >> 1][nt][2 * (k & 1)];
+                    const float* xr = &x[k >> 1][nt][2 * (k & 1)];
+                    pr[0] = fast_exp2(fmaf(xr[0], sl2, -m[nt][0]));
+                    pr[1] = fast_exp2(fmaf(xr[1], sl2, -m[nt][1]));
+                    if (ragged && !((seen >> k) & 1)) pr[0] = pr[1] = 0.f;
+                    ptop = fmaxf(ptop, fmaxf(pr[0], pr[1]));
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) {
+                        const float y0 = pr[0] * vs[k][gr], y1 = pr[1] * vs[k][gr];
+                        __half2 h = __floats2half2_rn(y0, y1);
+                        y[nt][gr][0][k] = *reinterpret_cast<uint32_t*>(&h);
+                        top = __hmax2(top, h);
+                        if constexpr (kP == 2) {
+                            const float2 back = __half22float2(h);
+                            __half2 lo2 = __floats2half2_rn(y0 - back.x, y1 - back.y);
+                            y[nt][gr][1][k] = *reinterpret_cast<uint32_t*>(&lo2);
+                        }
+                    }
+                }
+            over = ptop > 0x1p60f || __hmax(__low2half(top), __high2half(top)) >
+                                         __ushort_as_half(0x7800);  // 2^15
+        };
+        weights();
+        // Raise the reference m when a weight leaves float16's range: to where the largest
+        // product of weight and scale is 2^8 (7 binary orders of room, 22 below it before a weight
+        // loses bits), and the weights alone stay far from float32's limits.
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float v = mx[nt][c];
+                    float v = kNone;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float sc = NG == 2 ? fmaxf(vs[k][0], vs[k][NG - 1]) : vs[k][0];
+                        const float xs = x[k >> 1][nt][2 * (k & 1) + c] * sl2;
+                        if ((seen >> k) & 1) v = fmaxf(v, xs + fmaxf(log2f(sc) - 8.f, -60.f));
+                    }
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1)
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
@@ -477,59 +537,52 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                     m[nt][c] = v;
                     l[nt][c] *= al;
 #pragma unroll
-                    for (int gr = 0; gr < NG; ++gr) ob[nt][gr][c] *= al;
+                    for (int gr = 0; gr < NG; ++gr) {
+                        ob[nt][gr][c] *= al;
+                        oo[nt][gr][c] *= al;
+                        oo[nt][gr][2 + c] *= al;
+                    }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         o[nt][mt][c] *= al;
                         o[nt][mt][2 + c] *= al;
                     }
                 }
+            weights();
         }
-        // ---- weights and values of the two blocks
+        // ---- O += values * weights
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk) {
             const uint8_t* vb = vt + bk * L4::kBlockBytes;
-            float sg[2][NG], bg[2][NG];
+            float vm[2][NG];  // minima (and, codes centred on 8, 8 scales)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const __half2* pr =
                     reinterpret_cast<const __half2*>(vb + L4::param(g + 8 * half, 0));
-                const int tok = ti.T + bk * 16 + g + 8 * half;
-                const bool in = !ragged || (tok >= ti.lo && tok < ti.hi);
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                    const float2 f = __half22float2(pr[gr]);
-                    // what a masked slot holds may be anything, NaN included
-                    sg[half][gr] = in ? f.x : 0.f;
-                    // minimum corrected by the offset of the decoded codes (kF32: -8; else by
-                    // the token's parity, + 16 or - 31; g + 8 half has the parity of g)
-                    const float off = kF32 ? -8.f : ((g & 1) ? -31.f : 16.f);
-                    bg[half][gr] = in ? fmaf(-off, f.x, f.y) : 0.f;
+                    vm[half][gr] = __high2float(pr[gr]);
+                    if (kF32) vm[half][gr] = fmaf(8.f, __low2float(pr[gr]), vm[half][gr]);
+                    if (ragged && !((seen >> (2 * bk + half)) & 1)) vm[half][gr] = 0.f;
                 }
             }
             uint32_t pf[NT][NG][kP][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float pr[4];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    pr[r] = fast_exp2(x[bk][nt][r] - m[nt][r & 1]);
-                    l[nt][r & 1] += pr[r];
-                }
+                for (int half = 0; half < 2; ++half) {
+                    const float* pr = &pw[bk][nt][2 * half];
+                    l[nt][0] += pr[0];
+                    l[nt][1] += pr[1];
 #pragma unroll
-                for (int gr = 0; gr < NG; ++gr) {
+                    for (int gr = 0; gr < NG; ++gr) {
+                        ob[nt][gr][0] = fmaf(pr[0], vm[half][gr], ob[nt][gr][0]);
+                        ob[nt][gr][1] = fmaf(pr[1], vm[half][gr], ob[nt][gr][1]);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ob[nt][gr][0] = fmaf(pr[2 * half], bg[half][gr], ob[nt][gr][0]);
-                        ob[nt][gr][1] = fmaf(pr[2 * half + 1], bg[half][gr], ob[nt][gr][1]);
-                        uint32_t sp[kP];
-                        split2<kP>(pr[2 * half] * sg[half][gr], pr[2 * half + 1] * sg[half][gr],
-                                   sp);
-#pragma unroll
-                        for (int k = 0; k < kP; ++k) pf[nt][gr][k][half] = movmatrix_t(sp[k]);
+                        for (int k = 0; k < kP; ++k)
+                            pf[nt][gr][k][half] = movmatrix_t(y[nt][gr][k][2 * bk + half]);
                     }
                 }
-            }
             uint4 va, vc;  // words of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
             if constexpr (D == 128) {
                 va = *reinterpret_cast<const uint4*>(vb + lane * 16);
@@ -550,38 +603,50 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                 for (int hw = 0; hw < 2; ++hw) {  // codes 0-3, then 4-7 of the words
                     const uint32_t u = __byte_perm(w0, w1, hw ? 0x7632 : 0x5410);
                     const uint32_t v = __byte_perm(w2, w3, hw ? 0x7632 : 0x5410);
-                    constexpr uint32_t kX = kF32 ? kKey : kVal;
+                    constexpr uint32_t kX = kF32 ? kVal64 : kVal;
                     uint32_t fu[4], fv[4];
-                    fu[0] = ((u << 3) & kMask) ^ kX;
-                    fv[0] = ((v << 3) & kMask) ^ kX;
-                    fu[1] = ((u >> 1) & kMask) ^ kX;
-                    fv[1] = ((v >> 1) & kMask) ^ kX;
-                    fu[2] = ((u >> 5) & kMask) ^ kX;
-                    fv[2] = ((v >> 5) & kMask) ^ kX;
-                    fu[3] = ((u >> 9) & kMask) ^ kX;
-                    fv[3] = ((v >> 9) & kMask) ^ kX;
+                    fu[0] = ((u << 4) & val_mask) ^ kX;
+                    fv[0] = ((v << 4) & val_mask) ^ kX;
+                    fu[1] = (u & val_mask) ^ kX;
+                    fv[1] = (v & val_mask) ^ kX;
+                    fu[2] = ((u >> 4) & val_mask) ^ kX;
+                    fv[2] = ((v >> 4) & val_mask) ^ kX;
+                    fu[3] = ((u >> 8) & val_mask) ^ kX;
+                    fv[3] = ((v >> 8) & val_mask) ^ kX;
                     if constexpr (kF32) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) fu[e] = centre(fu[e]), fv[e] = centre(fv[e]);
+                        for (int e = 0; e < 4; ++e)
+                            fu[e] = centre_val(fu[e]), fv[e] = centre_val(fv[e]);
                     }
                     const int mt = gr * 4 + hw * 2;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k = 0; k < kP; ++k) {
-                            mma(o[nt][mt], fu[0], fu[1], fv[0], fv[1], pf[nt][gr][k][0],
-                                pf[nt][gr][k][1]);
-                            mma(o[nt][mt + 1], fu[2], fu[3], fv[2], fv[3], pf[nt][gr][k][0],
-                                pf[nt][gr][k][1]);
+                            mma_f16(o[nt][mt], fu[0], fu[1], fv[0], fv[1], pf[nt][gr][k][0],
+                                    pf[nt][gr][k][1]);
+                            mma_f16(o[nt][mt + 1], fu[2], fu[3], fv[2], fv[3], pf[nt][gr][k][0],
+                                    pf[nt][gr][k][1]);
                         }
+                }
+                if constexpr (!kF32) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(oo[nt][gr], kValOff, kValOff, kValOff, kValOff, pf[nt][gr][0][0],
+                                pf[nt][gr][0][1]);
                 }
             }
         }
+        };
+        if (ti.y & 16)
+            tile(std::true_type{});
+        else
+            tile(std::false_type{});
         // ---- end of the warp's piece of this unit
-        if (ti.flags & 2) {
-            const bool whole = from_start && (ti.flags & 8);
-            const long long unit = static_cast<long long>(ti.b) * p.HU + ti.u;
-            const size_t slot = static_cast<size_t>(me + unit);
+        if (ti.y & 2) {
+            const int4 un = unit_of(ti.x);
+            const bool whole = from_start && (ti.y & 8);
+            const size_t slot = static_cast<size_t>(me + ti.x);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -597,17 +662,17 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                             bv[gr] += __shfl_xor_sync(0xffffffffu, bv[gr], off);
                     }
                     const int h = nt * 8 + 2 * t + c;
-                    if (h >= G_cta) continue;
+                    if (h >= un.z) continue;
                     float mul = 1.f;
                     if (whole) {  // nothing to join: the output itself
-                        const int hq = hq0 + h;
+                        const int hq = un.y + h;
                         const float sig = p.sink_logit ? p.sink_logit[hq] * kLog2e : neg_inf();
                         const float M = fmaxf(m[nt][c], sig);
                         const float w = fast_exp2(m[nt][c] - M);
                         const float den = lv * w + (p.sink_logit ? fast_exp2(sig - M) : 0.f);
                         mul = w / den;
                         if (p.lse_out && g == 0)
-                            p.lse_out[static_cast<size_t>(ti.b) * p.Hq + hq] =
+                            p.lse_out[static_cast<size_t>(un.x) * p.Hq + hq] =
                                 (M + log2f(den)) * kLn2;
                     } else if (g == 0) {
                         float* ml = p.part_ml + (slot * (NT * 8) + h) * 2;
@@ -618,11 +683,11 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int d = mt * 16 + g + 8 * e;
-                            const float v = (o[nt][mt][2 * e + c] + bv[mt / 4]) * mul;
+                            const float v = ((o[nt][mt][2 * e + c] + oo[nt][mt / 4][c]) + bv[mt / 4]) * mul;
                             if (!whole) {
                                 __stcg(p.part_o + (slot * (NT * 8) + h) * D + d, v);
                             } else {
-                                const size_t at = (static_cast<size_t>(ti.b) * p.Hq + hq0 + h) * D + d;
+                                const size_t at = (static_cast<size_t>(un.x) * p.Hq + un.y + h) * D + d;
                                 if constexpr (kF32)
                                     static_cast<float*>(p.out)[at] = v;
                                 else
@@ -632,7 +697,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                 }
         }
         __syncwarp();
-        issue(s);
+        if (i + S < n_mine) issue(s, i + S);
+        if (++s == S) s = 0, phase ^= 1;
     }
 }
 

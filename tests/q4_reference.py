@@ -103,13 +103,18 @@ def visible(L, window, n_sink, ring):
     return t[(t >= L - window) | (t < n_sink)]
 
 
-def attention(q, k_pool, v_pool, bt, lens, D, P, scale, window=0, n_sink=0, ring=False, sink=None):
+def attention(q, k_pool, v_pool, bt, lens, D, P, scale, window=0, n_sink=0, ring=False, sink=None,
+              dtype=torch.bfloat16):
     """float64 (out, lse) and the error bound of each output, from packed pools (uint8 numpy).
 
     The bound counts, per weight: the score's float32 sums (each of the D products and of the
     scale and minimum terms, |q| (47 s + |b|) at most, rounded or cut by 2^-23 in each of about
-    32 steps), 2^-21 for the exponential, 2^-17 for the weight's two bf16 parts; and 2^-23 for
-    each of the steps in which 16 tokens are added to an output, plus its warps' joining."""
+    32 steps), 2^-21 for the exponential; the weight's rounding to float16 before it multiplies
+    the codes (half a step, 2^-11, of p s code, code <= 15; with float32 queries two float16
+    numbers, 2^-22, of codes held as c - 8 plus 8); and 2^-23 for each of the steps in which 16
+    tokens are added to an output, each at most p (94 s + |b|) since codes are held with an
+    offset of up to 79, plus the joining of partial sums."""
+    weight = 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22
     q = np.asarray(q, np.float64)
     B, Hq, _ = q.shape
     Hkv = k_pool.shape[1]
@@ -128,7 +133,7 @@ def attention(q, k_pool, v_pool, bt, lens, D, P, scale, window=0, n_sink=0, ring
         vc, vs, vb = (a[inv, :, at] for a in unpack(v_pool[used], D, False))
         k = value(kc, ks, kb).astype(np.float64)  # [n, Hkv, D]
         v = value(vc, vs, vb).astype(np.float64)
-        wide = 47 * vs.astype(np.float64) + np.abs(vb.astype(np.float64))
+        wide = 94 * vs.astype(np.float64) + np.abs(vb.astype(np.float64))
         kwide = 47 * ks.astype(np.float64) + np.abs(kb.astype(np.float64))
         for h in range(Hq):
             g = h // (Hq // Hkv)
@@ -140,8 +145,9 @@ def attention(q, k_pool, v_pool, bt, lens, D, P, scale, window=0, n_sink=0, ring
             den = p.sum() + (0 if sink is None else np.exp(sink[h] - top))
             out[b, h] = p @ v[:, g] / den
             lse[b, h] = top + np.log(den)
-            rel = ex + 2.0 ** -21 + 2.0 ** -17 + (len(t) / 16 + 64) * 2.0 ** -23
-            e = np.repeat((p * rel) @ wide[:, g], 64) / den
+            rel = ex + 2.0 ** -21 + (len(t) / 16 + 64) * 2.0 ** -23
+            e = (p * rel) @ wide[:, g] + (p * weight) @ (15 * vs[:, g].astype(np.float64))
+            e = np.repeat(e, 64) / den
             drift = (p * (ex + 2.0 ** -21 + (len(t) / 8 + 64) * 2.0 ** -24)).sum() / den
             tol[b, h] = e + np.abs(out[b, h]) * drift
             tol_lse[b, h] = drift + np.abs(lse[b, h]) * 2.0 ** -22 + 2.0 ** -20

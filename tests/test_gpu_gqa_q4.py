@@ -45,7 +45,7 @@ class Case:
         ref, rl, tol, tol_l = R.attention(
             self.q.float().numpy(), self.kp, self.vp, self.bt.numpy(), self.lens, self.D, self.P,
             self.scale, self.window, self.n_sink, self.ring,
-            None if self.sink is None else self.sink.numpy())
+            None if self.sink is None else self.sink.numpy(), self.dtype)
         out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
         # one rounding to the output's type
         tol = tol + np.abs(ref) * float(torch.finfo(self.dtype).eps) / 2 + 1e-30
