@@ -56,7 +56,7 @@ __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000);
 
 // The visible slots of sequence b (at most two ranges), empty for a length of 0.
 __device__ __forceinline__ Ranges seq_ranges(const Q4Params& p, int b) {
-    int L = __ldg(p.seq_lens + b);
+    int L = __ldcg(p.seq_lens + b);  // (from L2: the joining launch reads it early)
     if (L < 0 || (p.ring <= 0 && L > p.max_len)) {
         record_error(p.err, KVD_ERR_DEVICE_OOB);
         L = L < 0 ? 0 : p.max_len;
@@ -72,31 +72,42 @@ __device__ __forceinline__ int seq_tiles(const Q4Params& p, int b) {
     return range_tiles(r.lo0, r.hi0) + range_tiles(r.lo1, r.hi1);
 }
 
-// Tiles of all sequences in front of b_want (prefix) and of all of them (total), times HU;
-// one warp.
-struct Schedule {
-    long long prefix, total;
-    int tiles;  // of b_want's units
-};
-__device__ __forceinline__ Schedule schedule_of(const Q4Params& p, int b_want, int lane) {
-    Schedule s{0, 0, 0};
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        const int n = b < p.B ? seq_tiles(p, b) : 0;
-        long long sum = n, before = b < b_want ? n : 0;
+// Tiles of each unit of 32 sequences from b0 on, summed up to and with each lane's own (one warp);
+// n: the lane's own.
+__device__ __forceinline__ int scan_tiles(const Q4Params& p, int b0, int lane, int& n) {
+    n = b0 + lane < p.B ? seq_tiles(p, b0 + lane) : 0;
+    int inc = n;  // 32 sequences of fewer than 2^30 slots
 #pragma unroll
-        for (int off = 16; off; off >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            before += __shfl_xor_sync(0xffffffffu, before, off);
-        }
-        s.total += sum;
-        s.prefix += before;
-        if (b_want >= b0 && b_want < b0 + 32) s.tiles = __shfl_sync(0xffffffffu, n, b_want - b0);
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
     }
-    s.total *= p.HU;
-    s.prefix *= p.HU;
-    return s;
+    return inc;
 }
+
+__device__ __forceinline__ long long divide(long long a, int b) {  // a >= 0, b > 0
+    return (a >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+// The list of all units' tiles in order, shared evenly by n warps (at most one for each tile):
+// the first `extra` of them take one tile more.
+struct Shares {
+    long long total, base;
+    int n, extra;
+    __device__ Shares(const Q4Params& p, long long tiles_of_units) {
+        total = tiles_of_units * p.HU;
+        n = static_cast<int>(min(static_cast<long long>(p.n_warps), total));
+        base = n > 0 ? divide(total, n) : 0;
+        extra = static_cast<int>(total - base * n);
+    }
+    __device__ long long begin(int i) const { return i * base + min(i, extra); }
+    __device__ int count(int i) const { return static_cast<int>(base) + (i < extra ? 1 : 0); }
+    __device__ int owner(long long tile) const {
+        const long long longer = extra * (base + 1);
+        return static_cast<int>(tile < longer ? divide(tile, static_cast<int>(base + 1))
+                                              : extra + divide(tile - longer, static_cast<int>(base)));
+    }
+};
 
 // c[16x8] += a[16x16] * b[16x8], fp32 sums (not volatile: they may be reordered).
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -114,7 +125,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Keys: 16 + c as bf16, code bits under mantissa bits 3-6.
+// Keys: 16 + c as bf16, code bits at mantissa bits 3-6.
 constexpr uint32_t kKeyMask = 0x00780078u, kKey = 0x41804180u;
 // Values: float16, code bits at mantissa bits 4-7: 64 + c, for odd tokens (the high halves)
 // -(64 + 15 - c) = c - 79.
@@ -197,42 +208,33 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
     const uint32_t key_mask = read_shared(masks), val_mask = read_shared(masks + 1);
     griddep_wait();
 
-    // ---- this warp's share of the tile list, and where it begins
+    // The joining launch may come up as soon as this grid's CTAs leave (it waits for all of them
+    // before it reads a partial).
+    griddep_launch_dependents();
+
+    // ---- this warp's share of the tile list
     // (with fewer tiles than warps the first warps of all CTAs take one each)
-    const long long me = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
-    const Schedule sch = schedule_of(p, 0, lane);
-    const long long N = min(static_cast<long long>(p.n_warps), sch.total);
-    if (me >= N) return;
-    const long long begin = sch.total * me / N;
-    const int n_mine = static_cast<int>(sch.total * (me + 1) / N - begin);  // tiles, at least 1
+    const int me = warp * gridDim.x + blockIdx.x;
+    long long begin;
+    int n_mine;  // tiles, at least 1
+    {
+        long long tiles = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int n;
+            tiles += __shfl_sync(0xffffffffu, scan_tiles(p, b0, lane, n), 31);
+        }
+        const Shares sh(p, tiles);
+        if (me >= sh.n) return;
+        begin = sh.begin(me);
+        n_mine = sh.count(me);
+    }
     // Tiles are looked up 32 at a time, lane k the k-th of the batch: its blocks in the pools
     // (two when pages hold 16 tokens) and its TileInfo. That lane issues its copies.
     int blk0 = 0, blk1 = 0;
     TileInfo mine = make_int2(0, 0);
-    auto look_up = [&](int base) {  // tiles base .. base + 31 of this warp
-        long long rem = begin + base;
-        int b = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {  // the sequence that holds tile `base`
-            const int bl = b0 + lane;
-            const long long n =
-                bl < p.B ? static_cast<long long>(seq_tiles(p, bl)) * p.HU : 0;
-            long long inc = n;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += o;
-            }
-            const uint32_t past = __ballot_sync(0xffffffffu, inc > rem);
-            if (past) {
-                const int k = __ffs(past) - 1;
-                b = b0 + k;
-                rem -= __shfl_sync(0xffffffffu, inc - n, k);
-                break;
-            }
-            rem -= __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (base + lane >= n_mine) return;
-        rem += lane;
+    uint32_t special = 0;  // tiles of the batch that begin or end a piece or need masks
+    // the warp's i-th tile, the rem-th from the beginning of sequence b on
+    auto resolve = [&](int i, long long rem, int b) {
         Ranges r = seq_ranges(p, b);
         int n0 = range_tiles(r.lo0, r.hi0), n = n0 + range_tiles(r.lo1, r.hi1);
         while (rem >= static_cast<long long>(n) * p.HU) {  // this lane's own tile is further on
@@ -240,14 +242,14 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             r = seq_ranges(p, ++b);
             n0 = range_tiles(r.lo0, r.hi0), n = n0 + range_tiles(r.lo1, r.hi1);
         }
-        const int u = static_cast<int>(rem / n), j = static_cast<int>(rem - static_cast<long long>(u) * n);
+        const int u = static_cast<int>(divide(rem, n)), j = static_cast<int>(rem - static_cast<long long>(u) * n);
         const int kvh = u / p.NHG;
         const int lo = j < n0 ? r.lo0 : r.lo1, hi = j < n0 ? r.hi0 : r.hi1;
         const int T = ((lo >> 5) + (j < n0 ? j : j - n0)) * kTileTok;
         const int v0 = max(lo - T, 0), v1 = min(hi - T, kTileTok);
         mine.x = b * p.HU + u;
-        mine.y = ((base + lane == 0 || j == 0) ? 1 : 0) |
-                 ((base + lane == n_mine - 1 || j == n - 1) ? 2 : 0) | (j == 0 ? 4 : 0) |
+        mine.y = ((i == 0 || j == 0) ? 1 : 0) |
+                 ((i == n_mine - 1 || j == n - 1) ? 2 : 0) | (j == 0 ? 4 : 0) |
                  (j == n - 1 ? 8 : 0) | ((v0 > 0 || v1 < kTileTok) ? 16 : 0) | v0 << 8 | v1 << 16;
         // pages of its first and last visible token
         const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
@@ -263,10 +265,33 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                ((T & ((1 << p.page_shift) - 1)) >> 4);
         blk1 = pg1 * p.Hkv + kvh;
     };
+    auto look_up = [&](int base) {  // tiles base .. base + 31 of this warp
+        const long long at = begin + base, row = divide(at, p.HU);
+        long long before = 0;  // tiles of one unit of each sequence passed
+        int b = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {  // the sequence that holds tile `base`
+            int n;
+            const int inc = scan_tiles(p, b0, lane, n);
+            const uint32_t past = __ballot_sync(0xffffffffu, before + inc > row);
+            if (past) {
+                const int k = __ffs(past) - 1;
+                b = b0 + k;
+                before += __shfl_sync(0xffffffffu, inc - n, k);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        const long long rem = at - before * p.HU;
+        mine.y = 0;
+        if (base + lane < n_mine) resolve(base + lane, rem + lane, b);
+        special = __ballot_sync(0xffffffffu, (mine.y & 19) != 0);
+    };
     const uint64_t pol = l2_evict_first_policy();  // keys and values are read once
     // copy the warp's i-th tile into stage s
-    auto issue = [&](int s, int i) {
+    uint32_t queue = 0;  // bit k: the k-th tile from the current one is special
+    auto issue = [&](int s, int i, int ahead) {
         if ((i & 31) == 0) look_up(i);
+        queue |= ((special >> (i & 31)) & 1) << ahead;
         if (lane == (i & 31)) {
             info[s] = mine;
             uint8_t* st = ring + s * Cfg::kTileBytes;
@@ -291,15 +316,15 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             }
         }
     };
-    for (int s = 0; s < min(S, n_mine); ++s) issue(s, s);
+    for (int s = 0; s < min(S, n_mine); ++s) issue(s, s, s);
 
     // ---- state of the current piece
     uint32_t qf[kQ][NT][KW][4];
     float qsum[NT][NG][2];  // sums of q, heads 2t and 2t + 1
+    const float sl2 = p.scale_log2;
     // o, and the values' offsets and minima in it: oo by the matrix product, ob in each lane
     float o[NT][MT][4], oo[NT][NG][4], ob[NT][NG][2], m[NT][2], l[NT][2];
     bool from_start = false;
-    const float sl2 = p.scale_log2;
 
     // sequence, first query head, and number of heads of a unit
     auto unit_of = [&](int unit) {
@@ -310,16 +335,9 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
     int s = 0, phase = 0;
     for (int i = 0; i < n_mine; ++i) {
         __syncwarp();
-        if (!mbar_wait(&full[s], phase, p.err)) {
-            // give up, once the copies in flight have landed (or their own limits have passed)
-            if (lane == 0)
-                for (int k = i + 1; k < min(n_mine, i + S); ++k)
-                    mbar_wait(&full[k % S], (k / S) & 1, p.err);
-            __syncwarp();
-            return;
-        }
-        const TileInfo ti = info[s];
-        if (ti.y & 1) {
+        TileInfo ti = make_int2(0, 0);
+        if (queue & 1) ti = info[s];
+        if ((queue & 1) && (ti.y & 1)) {
             const int4 un = unit_of(ti.x);
             from_start = (ti.y & 4) != 0;
 #pragma unroll
@@ -367,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         qsum[nt][gr][c] = __shfl_sync(0xffffffffu, part[gr], (2 * t + c) * 4);
-                        ob[nt][gr][c] = 0.f;
+                    ob[nt][gr][c] = 0.f;
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) oo[nt][gr][r] = 0.f;
@@ -382,6 +400,14 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[nt][mt][r] = 0.f;
             }
+        }
+        if (!mbar_wait(&full[s], phase, p.err)) {
+            // give up, once the copies in flight have landed (or their own limits have passed)
+            if (lane == 0)
+                for (int k = i + 1; k < min(n_mine, i + S); ++k)
+                    mbar_wait(&full[k % S], (k / S) & 1, p.err);
+            __syncwarp();
+            return;
         }
         const uint8_t* kt = ring + s * Cfg::kTileBytes;
         const uint8_t* vt = kt + 2 * L4::kBlockBytes;
@@ -425,18 +451,11 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 uint32_t fa[4], fb[4];
-                fa[0] = (wa[w] & key_mask) ^ kKey;
-                fb[0] = (wb[w] & key_mask) ^ kKey;
-                fa[1] = ((wa[w] >> 4) & key_mask) ^ kKey;
-                fb[1] = ((wb[w] >> 4) & key_mask) ^ kKey;
-                fa[2] = ((wa[w] >> 8) & key_mask) ^ kKey;
-                fb[2] = ((wb[w] >> 8) & key_mask) ^ kKey;
-                fa[3] = (__funnelshift_r(wa[w], wa[w], 12) & key_mask) ^ kKey;
-                fb[3] = (__funnelshift_r(wb[w], wb[w], 12) & key_mask) ^ kKey;
-                if constexpr (kF32) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        fa[e] = centre_key(fa[e]), fb[e] = centre_key(fb[e]);
+                for (int e = 0; e < 4; ++e) {
+                    fa[e] = (__funnelshift_r(wa[w], wa[w], 4 * e) & key_mask) ^ kKey;
+                    fb[e] = (__funnelshift_r(wb[w], wb[w], 4 * e) & key_mask) ^ kKey;
+                    if (kF32) fa[e] = centre_key(fa[e]), fb[e] = centre_key(fb[e]);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -462,8 +481,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             float& v = x[bk][nt][2 * half + c];
-                            const float a = base * qsum[nt][gr][c];
-                            v = fmaf(f.x, acc[nt][gr][2 * half + c], gr ? v + a : a);
+                            v = gr ? fmaf(base, qsum[nt][gr][c], v) : base * qsum[nt][gr][c];
+                            v = fmaf(f.x, acc[nt][gr][2 * half + c], v);
                         }
                 }
             }
@@ -609,10 +628,11 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                     fv[0] = ((v << 4) & val_mask) ^ kX;
                     fu[1] = (u & val_mask) ^ kX;
                     fv[1] = (v & val_mask) ^ kX;
-                    fu[2] = ((u >> 4) & val_mask) ^ kX;
-                    fv[2] = ((v >> 4) & val_mask) ^ kX;
-                    fu[3] = ((u >> 8) & val_mask) ^ kX;
-                    fv[3] = ((v >> 8) & val_mask) ^ kX;
+                    const uint32_t u8 = u >> 8, v8 = v >> 8;
+                    fu[2] = ((u8 << 4) & val_mask) ^ kX;
+                    fv[2] = ((v8 << 4) & val_mask) ^ kX;
+                    fu[3] = (u8 & val_mask) ^ kX;
+                    fv[3] = (v8 & val_mask) ^ kX;
                     if constexpr (kF32) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -638,12 +658,12 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             }
         }
         };
-        if (ti.y & 16)
+        if ((queue & 1) && (ti.y & 16))
             tile(std::true_type{});
         else
             tile(std::false_type{});
         // ---- end of the warp's piece of this unit
-        if (ti.y & 2) {
+        if ((queue & 1) && (ti.y & 2)) {
             const int4 un = unit_of(ti.x);
             const bool whole = from_start && (ti.y & 8);
             const size_t slot = static_cast<size_t>(me + ti.x);
@@ -697,19 +717,21 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                 }
         }
         __syncwarp();
-        if (i + S < n_mine) issue(s, i + S);
+        if (i + S < n_mine) issue(s, i + S, S);
+        queue >>= 1;
         if (++s == S) s = 0, phase ^= 1;
     }
 }
 
 // Joins the partials of one (unit, head): out = sum_i 2^{m_i - M} O_i / (sum_i 2^{m_i - M} l_i +
-// 2^{sigma - M}). Warps take every eighth partial and are then joined in shared memory. Units that
-// one warp had whole are written already; units without tiles get zeros.
+// 2^{sigma - M}). Warps take every eighth partial, four at once, and are then joined in shared
+// memory. Units that one warp had whole are written already; units without tiles get zeros. What
+// there is to join follows from the lengths alone and is worked out before the wait for the main
+// launch.
 template <int D, int NT, bool kF32>
 __global__ void __launch_bounds__(256) gqa_q4_combine_kernel(const Q4Params p) {
     constexpr int V = D / 32;  // channels of a lane
     __shared__ float s_o[8][D], s_m[8], s_l[8];
-    griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int hp = min(NT * 8, p.G);
     const int h = blockIdx.x % hp;
@@ -718,49 +740,64 @@ __global__ void __launch_bounds__(256) gqa_q4_combine_kernel(const Q4Params p) {
     const int kvh = u / p.NHG, hg = u % p.NHG;
     if (hg * NT * 8 + h >= p.G) return;
     const int hq = kvh * p.G + hg * NT * 8 + h;
-    const Schedule sch = schedule_of(p, b, lane);
+    int first = 0, n = 0;  // the warps that share the unit
+    {
+        long long tiles = 0, before = 0;
+        int own = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int x;
+            const int inc = scan_tiles(p, b0, lane, x);
+            if (b >= b0 && b < b0 + 32) {
+                own = __shfl_sync(0xffffffffu, x, b - b0);
+                before = tiles + __shfl_sync(0xffffffffu, inc, b - b0) - own;
+            }
+            tiles += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (own > 0) {
+            const Shares sh(p, tiles);
+            const long long t0 = before * p.HU + static_cast<long long>(u) * own;
+            first = sh.owner(t0);
+            n = sh.owner(t0 + own - 1) - first + 1;
+            if (n == 1) return;
+        }
+    }
+    griddep_wait();
     const size_t at = (static_cast<size_t>(b) * p.Hq + hq) * D;
     const float sig = p.sink_logit ? p.sink_logit[hq] * kLog2e : neg_inf();
-    int first = 0, n = 0;
-    if (sch.tiles > 0) {
-        const long long W = sch.total, N = min(static_cast<long long>(p.n_warps), W);
-        const long long t0 = sch.prefix + static_cast<long long>(u) * sch.tiles;
-        const long long t1 = t0 + sch.tiles - 1;
-        first = static_cast<int>(((t0 + 1) * N + W - 1) / W - 1);  // the warp that has tile t0
-        n = static_cast<int>(((t1 + 1) * N + W - 1) / W - 1) - first + 1;
-        if (n == 1) return;
-    }
     float M = kNone, L = 0.f, acc[V] = {};
-    for (int i0 = warp; i0 < n; i0 += 256) {  // 32 partials of this warp at once
-        const int mine = i0 + 8 * lane;
-        float2 ml = make_float2(kNone, 0.f);
-        if (mine < n)
-            ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) +
-                        static_cast<size_t>(first + mine + unit) * (NT * 8) + h);
-        float top = ml.x;
-        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        top = fmaxf(top, M);
-        const float al = fast_exp2(M - top), w = fast_exp2(ml.x - top);
-        float sum = ml.y * w;
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        L = L * al + sum;
+    for (int i0 = warp; i0 < n; i0 += 32) {
+        float2 ml[4];
+        float v[4][V];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 8 * k;
+            ml[k] = make_float2(kNone, 0.f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[k][e] = 0.f;
+            if (i < n) {
+                const size_t row = static_cast<size_t>(first + i + unit) * (NT * 8) + h;
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + row);
+                const float* src = p.part_o + row * D + lane * V;
+                if constexpr (V == 4)
+                    *reinterpret_cast<float4*>(v[k]) = __ldcg(reinterpret_cast<const float4*>(src));
+                else
+                    *reinterpret_cast<float2*>(v[k]) = __ldcg(reinterpret_cast<const float2*>(src));
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+        const float al = fast_exp2(M - top);
         M = top;
+        L *= al;
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] *= al;
-        const int cnt = min(32, (n - i0 + 7) / 8);
-#pragma unroll 4
-        for (int k = 0; k < cnt; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float* src = p.part_o +
-                               (static_cast<size_t>(first + i0 + 8 * k + unit) * (NT * 8) + h) * D +
-                               lane * V;
-            float v[V];
-            if constexpr (V == 4)
-                *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
-            else
-                *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(wk, v[e], acc[e]);
+        for (int k = 0; k < 4; ++k) {
+            const float w = fast_exp2(ml[k].x - M);
+            L = fmaf(w, ml[k].y, L);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
         }
     }
 #pragma unroll
