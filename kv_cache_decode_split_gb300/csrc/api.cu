@@ -666,7 +666,8 @@ int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
     p.out = out;
     p.lse_out = lse_out;
     uint8_t* w = static_cast<uint8_t*>(ws);
-    p.part_ml = reinterpret_cast<float*>(w + plan.off_ml);
+    p.part_m = reinterpret_cast<float*>(w + plan.off_m);
+    p.part_l = reinterpret_cast<float*>(w + plan.off_l);
     p.part_o = reinterpret_cast<float*>(w + plan.off_o);
     p.err = err;
     p.B = B;
@@ -675,7 +676,7 @@ int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
     p.G = Hq / Hkv;
     p.NHG = plan.NHG;
     p.HU = Hkv * plan.NHG;
-    p.n_warps = plan.ctas * 8;
+    p.n_warps = plan.n_warps;
     p.page_shift = __builtin_ctz(page_size);
     p.max_pages = max_pages;
     p.num_pages = num_pages;

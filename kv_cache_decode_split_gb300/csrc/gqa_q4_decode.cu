@@ -45,8 +45,8 @@ namespace kvd {
 
 namespace {
 
-constexpr int kTileTok = 32;   // tokens of a tile: two 16-token blocks
-constexpr int kWarps = 8;      // warps of a CTA
+constexpr int kTileTok = 64;   // tokens of a tile: four 16-token blocks, used two at a time
+constexpr int kTileLog = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // maximum of nothing: finite, so that differences with it are defined
@@ -65,7 +65,7 @@ __device__ __forceinline__ Ranges seq_ranges(const Q4Params& p, int b) {
     return visible_ranges(L, p.window, p.n_sink);
 }
 __device__ __forceinline__ int range_tiles(int lo, int hi) {
-    return hi > lo ? ((hi - 1) >> 5) - (lo >> 5) + 1 : 0;
+    return hi > lo ? ((hi - 1) >> kTileLog) - (lo >> kTileLog) + 1 : 0;
 }
 __device__ __forceinline__ int seq_tiles(const Q4Params& p, int b) {
     const Ranges r = seq_ranges(p, b);
@@ -85,27 +85,22 @@ __device__ __forceinline__ int scan_tiles(const Q4Params& p, int b0, int lane, i
     return inc;
 }
 
-__device__ __forceinline__ long long divide(long long a, int b) {  // a >= 0, b > 0
-    return (a >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-
-// The list of all units' tiles in order, shared evenly by n warps (at most one for each tile):
-// the first `extra` of them take one tile more.
+// The list of all units' tiles in order (fewer than 2^31, which the host checks), shared evenly by
+// n warps (at most one for each tile): the first `extra` of them take one tile more.
 struct Shares {
-    long long total, base;
-    int n, extra;
-    __device__ Shares(const Q4Params& p, long long tiles_of_units) {
-        total = tiles_of_units * p.HU;
-        n = static_cast<int>(min(static_cast<long long>(p.n_warps), total));
-        base = n > 0 ? divide(total, n) : 0;
-        extra = static_cast<int>(total - base * n);
+    uint32_t n, base, extra;
+    __device__ Shares(const Q4Params& p, uint32_t tiles_of_units) {
+        const uint32_t total = tiles_of_units * p.HU;
+        n = min(static_cast<uint32_t>(p.n_warps), total);
+        base = n > 0 ? total / n : 0;
+        extra = total - base * n;
     }
-    __device__ long long begin(int i) const { return i * base + min(i, extra); }
-    __device__ int count(int i) const { return static_cast<int>(base) + (i < extra ? 1 : 0); }
-    __device__ int owner(long long tile) const {
-        const long long longer = extra * (base + 1);
-        return static_cast<int>(tile < longer ? divide(tile, static_cast<int>(base + 1))
-                                              : extra + divide(tile - longer, static_cast<int>(base)));
+    __device__ uint32_t begin(uint32_t i) const { return i * base + min(i, extra); }
+    __device__ int count(uint32_t i) const { return static_cast<int>(base + (i < extra ? 1 : 0)); }
+    __device__ int owner(uint32_t tile) const {
+        const uint32_t longer = extra * (base + 1);
+        return static_cast<int>(tile < longer ? tile / (base + 1)
+                                              : extra + (tile - longer) / base);
     }
 };
 
@@ -116,6 +111,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c = a * b (the accumulator starts at zero, without registers cleared for it).
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -169,22 +173,26 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t (&part)[kS
 // the first visible token of the tile, from bit 16 the one behind the last.
 using TileInfo = int2;
 
+// One CTA on each SM: its warps share the SM's registers (a warp's products, sums and operands
+// need about 150 of them; 120 with float32 queries' and 16-head blocks' 230).
+constexpr int warps_of(int nt, bool f32) { return nt == 1 && !f32 ? 12 : 8; }
+
 template <int D, int NT, bool kF32>
 struct Q4Cfg {
-    static constexpr int kStages = 3;
-    static constexpr int kTileBytes = 4 * Q4<D>::kBlockBytes;  // K and V, two blocks each
+    static constexpr int kWarps = warps_of(NT, kF32);
+    static constexpr int kStages = 2;
+    static constexpr int kTileBytes = 8 * Q4<D>::kBlockBytes;  // K and V, four blocks each
     static constexpr int kRing = kStages * kTileBytes;
     static constexpr int kPerWarp = kRing + kStages * static_cast<int>(sizeof(TileInfo) + 8);
     static constexpr int kSmem = kWarps * kPerWarp + 16;
-    static constexpr int kCtas = (NT == 1 && !kF32) ? 2 : 1;   // per SM (registers)
 };
 
 template <int D, int NT, bool kF32>
-__global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
+__global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     gqa_q4_kernel(const Q4Params p) {
     using Cfg = Q4Cfg<D, NT, kF32>;
     using L4 = Q4<D>;
-    constexpr int S = Cfg::kStages;
+    constexpr int S = Cfg::kStages, kWarps = Cfg::kWarps;
     constexpr int NG = L4::kGroups;
     constexpr int KW = D / 32;             // key words of a lane and row
     constexpr int MT = D / 16;             // 16-channel tiles of the output
@@ -214,12 +222,13 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
 
     // ---- this warp's share of the tile list
     // (with fewer tiles than warps the first warps of all CTAs take one each)
-    const int me = warp * gridDim.x + blockIdx.x;
-    long long begin;
+    const uint32_t me = warp * gridDim.x + blockIdx.x;
+    uint32_t begin;
     int n_mine;  // tiles, at least 1
+    int scan_n, scan_inc = scan_tiles(p, 0, lane, scan_n);  // of the first 32 sequences
     {
-        long long tiles = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
+        uint32_t tiles = __shfl_sync(0xffffffffu, scan_inc, 31);
+        for (int b0 = 32; b0 < p.B; b0 += 32) {
             int n;
             tiles += __shfl_sync(0xffffffffu, scan_tiles(p, b0, lane, n), 31);
         }
@@ -228,50 +237,62 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
         begin = sh.begin(me);
         n_mine = sh.count(me);
     }
-    // Tiles are looked up 32 at a time, lane k the k-th of the batch: its blocks in the pools
-    // (two when pages hold 16 tokens) and its TileInfo. That lane issues its copies.
-    int blk0 = 0, blk1 = 0;
+    // Tiles are looked up 32 at a time, lane k the k-th of the batch: its pieces' first blocks in
+    // the pools (one piece, or two or four when pages hold 32 or 16 tokens) and its TileInfo.
+    // That lane issues its copies.
+    int blk[4] = {};
     TileInfo mine = make_int2(0, 0);
     uint32_t special = 0;  // tiles of the batch that begin or end a piece or need masks
     // the warp's i-th tile, the rem-th from the beginning of sequence b on
-    auto resolve = [&](int i, long long rem, int b) {
+    auto resolve = [&](int i, uint32_t rem, int b) {
         Ranges r = seq_ranges(p, b);
         int n0 = range_tiles(r.lo0, r.hi0), n = n0 + range_tiles(r.lo1, r.hi1);
-        while (rem >= static_cast<long long>(n) * p.HU) {  // this lane's own tile is further on
-            rem -= static_cast<long long>(n) * p.HU;
+        while (rem >= static_cast<uint32_t>(n) * p.HU) {  // this lane's own tile is further on
+            rem -= static_cast<uint32_t>(n) * p.HU;
             r = seq_ranges(p, ++b);
             n0 = range_tiles(r.lo0, r.hi0), n = n0 + range_tiles(r.lo1, r.hi1);
         }
-        const int u = static_cast<int>(divide(rem, n)), j = static_cast<int>(rem - static_cast<long long>(u) * n);
+        const int u = static_cast<int>(rem / n), j = static_cast<int>(rem % n);
         const int kvh = u / p.NHG;
         const int lo = j < n0 ? r.lo0 : r.lo1, hi = j < n0 ? r.hi0 : r.hi1;
-        const int T = ((lo >> 5) + (j < n0 ? j : j - n0)) * kTileTok;
+        const int T = ((lo >> kTileLog) + (j < n0 ? j : j - n0)) * kTileTok;
         const int v0 = max(lo - T, 0), v1 = min(hi - T, kTileTok);
         mine.x = b * p.HU + u;
         mine.y = ((i == 0 || j == 0) ? 1 : 0) |
                  ((i == n_mine - 1 || j == n - 1) ? 2 : 0) | (j == 0 ? 4 : 0) |
                  (j == n - 1 ? 8 : 0) | ((v0 > 0 || v1 < kTileTok) ? 16 : 0) | v0 << 8 | v1 << 16;
-        // pages of its first and last visible token
+        // The pages of its (up to four) pieces: a piece is a page's part of the tile. Pieces
+        // without a visible token take the page of one that has.
         const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-        int pg0 = __ldg(row + ((T + v0) >> p.page_shift));
-        int pg1 = p.page_shift == 4 ? __ldg(row + ((T + v1 - 1) >> 4)) : 0;
-        if (static_cast<unsigned>(pg0) >= static_cast<unsigned>(p.num_pages) ||
-            static_cast<unsigned>(pg1) >= static_cast<unsigned>(p.num_pages)) {
-            record_error(p.err, KVD_ERR_DEVICE_OOB);
-            if (static_cast<unsigned>(pg0) >= static_cast<unsigned>(p.num_pages)) pg0 = 0;
-            if (static_cast<unsigned>(pg1) >= static_cast<unsigned>(p.num_pages)) pg1 = 0;
-        }
-        blk0 = ((pg0 * p.Hkv + kvh) << (p.page_shift - 4)) +
-               ((T & ((1 << p.page_shift) - 1)) >> 4);
-        blk1 = pg1 * p.Hkv + kvh;
+        const int piece = min(kTileTok, 1 << p.page_shift);
+        int pg[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k * piece < kTileTok) {
+                const int tok = T + min(max(k * piece, v0), v1 - 1);
+                pg[k] = __ldg(row + (tok >> p.page_shift));
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k * piece < kTileTok) {
+                if (static_cast<unsigned>(pg[k]) >= static_cast<unsigned>(p.num_pages)) {
+                    record_error(p.err, KVD_ERR_DEVICE_OOB);
+                    pg[k] = 0;
+                }
+                blk[k] = ((pg[k] * p.Hkv + kvh) << (p.page_shift - 4)) +
+                         ((T & ((1 << p.page_shift) - 1)) >> 4);
+            }
     };
     auto look_up = [&](int base) {  // tiles base .. base + 31 of this warp
-        const long long at = begin + base, row = divide(at, p.HU);
-        long long before = 0;  // tiles of one unit of each sequence passed
+        const uint32_t at = begin + base, row = at / static_cast<uint32_t>(p.HU);
+        uint32_t before = 0;  // tiles of one unit of each sequence passed
         int b = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {  // the sequence that holds tile `base`
-            int n;
-            const int inc = scan_tiles(p, b0, lane, n);
+            int n, inc;
+            if (b0 == 0 && base == 0)
+                n = scan_n, inc = scan_inc;
+            else
+                inc = scan_tiles(p, b0, lane, n);
             const uint32_t past = __ballot_sync(0xffffffffu, before + inc > row);
             if (past) {
                 const int k = __ffs(past) - 1;
@@ -281,7 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             }
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
-        const long long rem = at - before * p.HU;
+        const uint32_t rem = at - before * p.HU;
         mine.y = 0;
         if (base + lane < n_mine) resolve(base + lane, rem + lane, b);
         special = __ballot_sync(0xffffffffu, (mine.y & 19) != 0);
@@ -295,24 +316,29 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
         if (lane == (i & 31)) {
             info[s] = mine;
             uint8_t* st = ring + s * Cfg::kTileBytes;
-            if (p.page_shift >= 5) {
-                const size_t off = static_cast<size_t>(blk0) * L4::kBlockBytes;
+            if (p.page_shift >= kTileLog) {
+                const size_t off = static_cast<size_t>(blk[0]) * L4::kBlockBytes;
                 mbar_arrive_expect_tx(&full[s], Cfg::kTileBytes);
-                bulk_load(st, p.k_pool + off, 2 * L4::kBlockBytes, &full[s], pol);
-                bulk_load(st + 2 * L4::kBlockBytes, p.v_pool + off, 2 * L4::kBlockBytes, &full[s],
+                bulk_load(st, p.k_pool + off, Cfg::kTileBytes / 2, &full[s], pol);
+                bulk_load(st + Cfg::kTileBytes / 2, p.v_pool + off, Cfg::kTileBytes / 2, &full[s],
                           pol);
-            } else {  // a block without visible tokens is not copied (all of it is masked)
-                const bool h0 = ((mine.y >> 8) & 63) < 16, h1 = ((mine.y >> 16) & 63) > 16;
-                mbar_arrive_expect_tx(&full[s], (h0 + h1) * 2 * L4::kBlockBytes);
+            } else {  // a piece without visible tokens is not copied (all of it is masked)
+                const int v0 = (mine.y >> 8) & 127, v1 = (mine.y >> 16) & 127;
+                const int piece = 1 << p.page_shift;
+                const uint32_t bytes = (piece >> 4) * L4::kBlockBytes;
+                uint32_t total = 0;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (!(k ? h1 : h0)) continue;
-                    const size_t off = static_cast<size_t>(k ? blk1 : blk0) * L4::kBlockBytes;
-                    bulk_load(st + k * L4::kBlockBytes, p.k_pool + off, L4::kBlockBytes, &full[s],
-                              pol);
-                    bulk_load(st + (2 + k) * L4::kBlockBytes, p.v_pool + off, L4::kBlockBytes,
-                              &full[s], pol);
-                }
+                for (int k = 0; k < 4; ++k)
+                    if (k * piece < v1 && (k + 1) * piece > v0) total += 2 * bytes;
+                mbar_arrive_expect_tx(&full[s], total);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k * piece < v1 && (k + 1) * piece > v0) {
+                        const size_t off = static_cast<size_t>(blk[k]) * L4::kBlockBytes;
+                        bulk_load(st + k * bytes, p.k_pool + off, bytes, &full[s], pol);
+                        bulk_load(st + Cfg::kTileBytes / 2 + k * bytes, p.v_pool + off, bytes,
+                                  &full[s], pol);
+                    }
             }
         }
     };
@@ -409,19 +435,21 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             __syncwarp();
             return;
         }
-        const uint8_t* kt = ring + s * Cfg::kTileBytes;
-        const uint8_t* vt = kt + 2 * L4::kBlockBytes;
-        // tokens of this lane's score rows: 16 bk + 8 half + g, bit 2 bk + half of `seen`
-        // (two copies of the code: whole tiles do not look at them)
-        auto tile = [&](auto is_ragged) {
+        const int v0 = (ti.y >> 8) & 127, v1 = (ti.y >> 16) & 127;  // (special tiles only)
+        // half a tile: tokens 32 sub .. 32 sub + 31. This lane's score rows are tokens 16 bk +
+        // 8 half + g of them, bit 2 bk + half of `seen` (two copies of the code: whole tiles do
+        // not look at it)
+        auto half_tile = [&](auto is_ragged, int sub) {
+        const uint8_t* kt = ring + s * Cfg::kTileBytes + sub * (2 * L4::kBlockBytes);
+        const uint8_t* vt = kt + Cfg::kTileBytes / 2;
         constexpr bool ragged = decltype(is_ragged)::value;
         uint32_t seen = 15;
         if constexpr (ragged) {
             seen = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int tok = 8 * k + g;
-                seen |= (tok >= ((ti.y >> 8) & 63) && tok < ((ti.y >> 16) & 63)) ? 1u << k : 0u;
+                const int tok = 32 * sub + 8 * k + g;
+                seen |= (tok >= v0 && tok < v1) ? 1u << k : 0u;
             }
         }
 
@@ -442,13 +470,6 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             }
             float acc[NT][NG][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[nt][gr][r] = 0.f;
-#pragma unroll
             for (int w = 0; w < KW; ++w) {
                 uint32_t fa[4], fb[4];
 #pragma unroll
@@ -461,8 +482,12 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < kQ; ++k) {
-                        mma_bf16(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
-                                 qf[k][nt][w][1]);
+                        if (k == 0 && w % 2 == 0)
+                            mma_bf16_first(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1],
+                                           qf[k][nt][w][0], qf[k][nt][w][1]);
+                        else
+                            mma_bf16(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
+                                     qf[k][nt][w][1]);
                         mma_bf16(acc[nt][w / 2], fa[2], fb[2], fa[3], fb[3], qf[k][nt][w][2],
                                  qf[k][nt][w][3]);
                     }
@@ -658,63 +683,81 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
             }
         }
         };
-        if ((queue & 1) && (ti.y & 16))
-            tile(std::true_type{});
-        else
-            tile(std::false_type{});
+        if ((queue & 1) && (ti.y & 16)) {
+#pragma unroll 1
+            for (int sub = v0 >> 5; sub <= (v1 - 1) >> 5; ++sub) half_tile(std::true_type{}, sub);
+        } else {
+#pragma unroll 1
+            for (int sub = 0; sub < 2; ++sub) half_tile(std::false_type{}, sub);
+        }
         // ---- end of the warp's piece of this unit
         if ((queue & 1) && (ti.y & 2)) {
             const int4 un = unit_of(ti.x);
             const bool whole = from_start && (ti.y & 8);
-            const size_t slot = static_cast<size_t>(me + ti.x);
+            const size_t slot = static_cast<size_t>(me) + ti.x;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float mul[2], add[NG][2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float lv = l[nt][c], bv[NG];
+                    float lv = l[nt][c];
 #pragma unroll
-                    for (int gr = 0; gr < NG; ++gr) bv[gr] = ob[nt][gr][c];
+                    for (int gr = 0; gr < NG; ++gr) add[gr][c] = ob[nt][gr][c];
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) {
                         lv += __shfl_xor_sync(0xffffffffu, lv, off);
 #pragma unroll
                         for (int gr = 0; gr < NG; ++gr)
-                            bv[gr] += __shfl_xor_sync(0xffffffffu, bv[gr], off);
+                            add[gr][c] += __shfl_xor_sync(0xffffffffu, add[gr][c], off);
                     }
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) add[gr][c] += oo[nt][gr][c];
                     const int h = nt * 8 + 2 * t + c;
+                    mul[c] = 1.f;
                     if (h >= un.z) continue;
-                    float mul = 1.f;
                     if (whole) {  // nothing to join: the output itself
                         const int hq = un.y + h;
                         const float sig = p.sink_logit ? p.sink_logit[hq] * kLog2e : neg_inf();
                         const float M = fmaxf(m[nt][c], sig);
                         const float w = fast_exp2(m[nt][c] - M);
                         const float den = lv * w + (p.sink_logit ? fast_exp2(sig - M) : 0.f);
-                        mul = w / den;
+                        mul[c] = w / den;
                         if (p.lse_out && g == 0)
                             p.lse_out[static_cast<size_t>(un.x) * p.Hq + hq] =
                                 (M + log2f(den)) * kLn2;
                     } else if (g == 0) {
-                        float* ml = p.part_ml + (slot * (NT * 8) + h) * 2;
-                        __stcg(reinterpret_cast<float2*>(ml), make_float2(m[nt][c], lv));
+                        __stcg(p.part_m + slot * (NT * 8) + h, m[nt][c]);
+                        __stcg(p.part_l + slot * (NT * 8) + h, lv);
                     }
+                }
+                if (nt * 8 + 2 * t >= un.z) continue;
+                if (!whole) {  // as the lanes hold it: 16 bytes of 8 x 2 channels and heads each
+                    float* dst = p.part_o + (slot * NT + nt) * (D * 8) + lane * 4;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        __stcg(reinterpret_cast<float4*>(dst + mt * 128),
+                               make_float4(o[nt][mt][0] + add[mt / 4][0], o[nt][mt][1] + add[mt / 4][1],
+                                           o[nt][mt][2] + add[mt / 4][0], o[nt][mt][3] + add[mt / 4][1]));
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = nt * 8 + 2 * t + c;
+                    if (h >= un.z) continue;
+                    const size_t at = (static_cast<size_t>(un.x) * p.Hq + un.y + h) * D + g;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int d = mt * 16 + g + 8 * e;
-                            const float v = ((o[nt][mt][2 * e + c] + oo[nt][mt / 4][c]) + bv[mt / 4]) * mul;
-                            if (!whole) {
-                                __stcg(p.part_o + (slot * (NT * 8) + h) * D + d, v);
-                            } else {
-                                const size_t at = (static_cast<size_t>(un.x) * p.Hq + un.y + h) * D + d;
-                                if constexpr (kF32)
-                                    static_cast<float*>(p.out)[at] = v;
-                                else
-                                    static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(v);
-                            }
+                            const float v = (o[nt][mt][2 * e + c] + add[mt / 4][c]) * mul[c];
+                            if constexpr (kF32)
+                                static_cast<float*>(p.out)[at + mt * 16 + 8 * e] = v;
+                            else
+                                static_cast<__nv_bfloat16*>(p.out)[at + mt * 16 + 8 * e] =
+                                    __float2bfloat16(v);
                         }
                 }
+            }
         }
         __syncwarp();
         if (i + S < n_mine) issue(s, i + S, S);
@@ -723,26 +766,30 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Cfg<D, NT, kF32>::kCtas)
     }
 }
 
-// Joins the partials of one (unit, head): out = sum_i 2^{m_i - M} O_i / (sum_i 2^{m_i - M} l_i +
-// 2^{sigma - M}). Warps take every eighth partial, four at once, and are then joined in shared
-// memory. Units that one warp had whole are written already; units without tiles get zeros. What
-// there is to join follows from the lengths alone and is worked out before the wait for the main
-// launch.
-template <int D, int NT, bool kF32>
-__global__ void __launch_bounds__(256) gqa_q4_combine_kernel(const Q4Params p) {
-    constexpr int V = D / 32;  // channels of a lane
-    __shared__ float s_o[8][D], s_m[8], s_l[8];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int hp = min(NT * 8, p.G);
-    const int h = blockIdx.x % hp;
-    const int unit = blockIdx.x / hp;
+// Joins the partials of one unit's block of 8 heads: out = sum_i 2^{m_i - M} O_i / (sum_i 2^{m_i - M}
+// l_i + 2^{sigma - M}). A partial is 8 D floats as the main launch's lanes hold them; a thread takes
+// one quad of it (two channels of two heads) of every kSplit-th partial, kAtOnce of them in flight
+// with their references and sums, so that few partials cost one round trip and no barrier. A CTA
+// has all quads (kSplit = 1), or, where few units are cut into many partials each, 32 of them
+// (kSplit = 8), so that enough SMs read. Units that one warp had whole are written already; units
+// without tiles get zeros. What there is to join follows from the lengths alone and is worked out
+// while the main launch ends.
+template <int D, int NT, bool kF32, int kSplit>
+__global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
+    gqa_q4_combine_kernel(const Q4Params p) {
+    constexpr int kQuads = kSplit == 1 ? D * 2 : 32, kAtOnce = 4, H = NT * 8;
+    constexpr int kParts = D * 2 / kQuads;  // CTAs of a unit's 8 heads
+    const int unit = blockIdx.x, nt = blockIdx.y / kParts;
     const int b = unit / p.HU, u = unit % p.HU;
     const int kvh = u / p.NHG, hg = u % p.NHG;
-    if (hg * NT * 8 + h >= p.G) return;
-    const int hq = kvh * p.G + hg * NT * 8 + h;
+    const int hq0 = kvh * p.G + hg * H + nt * 8, heads = min(8, p.G - hg * H - nt * 8);
+    const int quad = threadIdx.x % kQuads + blockIdx.y % kParts * kQuads;
+    const int k0 = threadIdx.x / kQuads;
+    const int lane = threadIdx.x % 32, mt = quad / 32, g = lane >> 2, h = 2 * (lane & 3);
+    if (heads <= 0) return;
     int first = 0, n = 0;  // the warps that share the unit
     {
-        long long tiles = 0, before = 0;
+        uint32_t tiles = 0, before = 0;
         int own = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             int x;
@@ -755,76 +802,109 @@ __global__ void __launch_bounds__(256) gqa_q4_combine_kernel(const Q4Params p) {
         }
         if (own > 0) {
             const Shares sh(p, tiles);
-            const long long t0 = before * p.HU + static_cast<long long>(u) * own;
+            const uint32_t t0 = before * p.HU + static_cast<uint32_t>(u) * own;
             first = sh.owner(t0);
             n = sh.owner(t0 + own - 1) - first + 1;
             if (n == 1) return;
         }
     }
     griddep_wait();
-    const size_t at = (static_cast<size_t>(b) * p.Hq + hq) * D;
-    const float sig = p.sink_logit ? p.sink_logit[hq] * kLog2e : neg_inf();
-    float M = kNone, L = 0.f, acc[V] = {};
-    for (int i0 = warp; i0 < n; i0 += 32) {
-        float2 ml[4];
-        float v[4][V];
+    const bool mine = h < heads, both = h + 1 < heads;
+    float sig[2] = {neg_inf(), neg_inf()};
+    if (p.sink_logit) {
+        if (mine) sig[0] = p.sink_logit[hq0 + h] * kLog2e;
+        if (both) sig[1] = p.sink_logit[hq0 + h + 1] * kLog2e;
+    }
+    float M[2] = {kNone, kNone}, L[2] = {0.f, 0.f};
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const size_t slot0 = static_cast<size_t>(first) + unit;
+    const float* pm = p.part_m + slot0 * H + nt * 8 + h;
+    const float* pl = p.part_l + slot0 * H + nt * 8 + h;
+    const float* po = p.part_o + (slot0 * NT + nt) * (D * 8) + quad * 4;
+    if (mine) {
+        for (int i0 = k0; i0 < n; i0 += kSplit * kAtOnce) {
+            float2 mi[kAtOnce], li[kAtOnce];
+            float4 v[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = i0 + 8 * k;
-            ml[k] = make_float2(kNone, 0.f);
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = i0 + kSplit * k;
+                mi[k] = make_float2(kNone, kNone);
+                li[k] = make_float2(0.f, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    mi[k] = __ldcg(reinterpret_cast<const float2*>(pm + static_cast<size_t>(i) * H));
+                    li[k] = __ldcg(reinterpret_cast<const float2*>(pl + static_cast<size_t>(i) * H));
+                    v[k] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(i) * (D * H)));
+                }
+            }
+            float t0 = M[0], t1 = M[1];
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[k][e] = 0.f;
-            if (i < n) {
-                const size_t row = static_cast<size_t>(first + i + unit) * (NT * 8) + h;
-                ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + row);
-                const float* src = p.part_o + row * D + lane * V;
-                if constexpr (V == 4)
-                    *reinterpret_cast<float4*>(v[k]) = __ldcg(reinterpret_cast<const float4*>(src));
-                else
-                    *reinterpret_cast<float2*>(v[k]) = __ldcg(reinterpret_cast<const float2*>(src));
+            for (int k = 0; k < kAtOnce; ++k) {
+                t0 = fmaxf(t0, mi[k].x);
+                t1 = both ? fmaxf(t1, mi[k].y) : t1;  // (a head that is not there holds anything)
+            }
+            const float a0 = fast_exp2(M[0] - t0), a1 = fast_exp2(M[1] - t1);
+            M[0] = t0, M[1] = t1;
+            L[0] *= a0, L[1] *= a1;
+            acc.x *= a0, acc.z *= a0, acc.y *= a1, acc.w *= a1;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float w0 = fast_exp2(mi[k].x - t0), w1 = both ? fast_exp2(mi[k].y - t1) : 0.f;
+                L[0] = fmaf(w0, li[k].x, L[0]);
+                acc.x = fmaf(w0, v[k].x, acc.x);
+                acc.z = fmaf(w0, v[k].z, acc.z);
+                if (both) {
+                    L[1] = fmaf(w1, li[k].y, L[1]);
+                    acc.y = fmaf(w1, v[k].y, acc.y);
+                    acc.w = fmaf(w1, v[k].w, acc.w);
+                }
             }
         }
-        float top = M;
+    }
+    if constexpr (kSplit > 1) {
+        __shared__ float4 s_o[kSplit][kQuads], s_ml[kSplit][kQuads];
+        s_o[k0][lane] = acc;
+        s_ml[k0][lane] = make_float4(M[0], M[1], L[0], L[1]);
+        __syncthreads();
+        if (k0 != 0) return;
+        float t0 = kNone, t1 = kNone;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
-        const float al = fast_exp2(M - top);
-        M = top;
-        L *= al;
+        for (int k = 0; k < kSplit; ++k) {
+            t0 = fmaxf(t0, s_ml[k][lane].x);
+            t1 = fmaxf(t1, s_ml[k][lane].y);
+        }
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        M[0] = t0, M[1] = t1, L[0] = L[1] = 0.f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] *= al;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float w = fast_exp2(ml[k].x - M);
-            L = fmaf(w, ml[k].y, L);
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+        for (int k = 0; k < kSplit; ++k) {
+            const float4 a = s_ml[k][lane], v = s_o[k][lane];
+            const float w0 = fast_exp2(a.x - t0), w1 = fast_exp2(a.y - t1);
+            L[0] = fmaf(w0, a.z, L[0]), L[1] = fmaf(w1, a.w, L[1]);
+            acc.x = fmaf(w0, v.x, acc.x), acc.z = fmaf(w0, v.z, acc.z);
+            acc.y = fmaf(w1, v.y, acc.y), acc.w = fmaf(w1, v.w, acc.w);
         }
     }
+    const float r[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-    for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
-    if (lane == 0) s_m[warp] = M, s_l[warp] = L;
-    __syncthreads();
-    const int d = threadIdx.x;
-    if (d >= D) return;
-    float top = sig;
+    for (int c = 0; c < 2; ++c) {
+        if (h + c >= heads) continue;
+        const int hq = hq0 + h + c;
+        const float top = fmaxf(M[c], sig[c]), w = fast_exp2(M[c] - top);
+        const float den = fmaf(L[c], w, p.sink_logit ? fast_exp2(sig[c] - top) : 0.f);
+        const size_t at = (static_cast<size_t>(b) * p.Hq + hq) * D + mt * 16 + g;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, s_m[k]);
-    float den = p.sink_logit ? fast_exp2(sig - top) : 0.f, v = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float w = fast_exp2(s_m[k] - top);
-        den = fmaf(w, s_l[k], den);
-        v = fmaf(w, s_o[k][d], v);
+        for (int e = 0; e < 2; ++e) {
+            // nothing visible: zeros, and the logarithm of the sink's share alone
+            const float v = n == 0 ? 0.f : r[2 * e + c] * (w / den);
+            if constexpr (kF32)
+                static_cast<float*>(p.out)[at + 8 * e] = v;
+            else
+                static_cast<__nv_bfloat16*>(p.out)[at + 8 * e] = __float2bfloat16(v);
+        }
+        if (mt == 0 && g == 0 && p.lse_out)
+            p.lse_out[static_cast<size_t>(b) * p.Hq + hq] =
+                n == 0 ? sig[c] * kLn2 : (top + log2f(den)) * kLn2;
     }
-    // nothing visible: zeros, and the logarithm of the sink's share alone
-    v = n == 0 ? 0.f : v / den;
-    if constexpr (kF32)
-        static_cast<float*>(p.out)[at + d] = v;
-    else
-        static_cast<__nv_bfloat16*>(p.out)[at + d] = __float2bfloat16(v);
-    if (d == 0 && p.lse_out)
-        p.lse_out[static_cast<size_t>(b) * p.Hq + hq] =
-            n == 0 ? sig * kLn2 : (top + log2f(den)) * kLn2;
 }
 
 template <int D, int NT, bool kF32>
@@ -838,36 +918,41 @@ int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
             return KVD_ERR_CUDA;
         configured = 1;
     }
-    if (launch_kernel(kern, dim3(plan.ctas), dim3(kWarps * 32), Cfg::kSmem, stream, p) !=
+    if (launch_kernel(kern, dim3(plan.ctas), dim3(Cfg::kWarps * 32), Cfg::kSmem, stream, p) !=
         cudaSuccess)
         return KVD_ERR_CUDA;
-    const unsigned rows = static_cast<unsigned>(plan.units) * std::min(NT * 8, p.G);
-    if (launch_kernel(gqa_q4_combine_kernel<D, NT, kF32>, dim3(rows), dim3(256), 0, stream, p) !=
-        cudaSuccess)
-        return KVD_ERR_CUDA;
+    // (16 partials are two round trips of a thread)
+    const cudaError_t e =
+        plan.n_warps <= 16 * plan.units
+            ? launch_kernel(gqa_q4_combine_kernel<D, NT, kF32, 1>, dim3(plan.units, NT),
+                            dim3(D * 2), 0, stream, p)
+            : launch_kernel(gqa_q4_combine_kernel<D, NT, kF32, 8>,
+                            dim3(plan.units, NT * (D / 16)), dim3(256), 0, stream, p);
+    if (e != cudaSuccess) return KVD_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
 }
 
 }  // namespace
 
-// A block of at most 8 (16) query heads of a KV head; as many CTAs as are resident at once, or as
-// the longest possible list of tiles keeps busy.
+// Blocks of at most 8 (or 16) query heads of a KV head; one CTA on each SM, or as many as the
+// longest possible list of tiles keeps busy.
 int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan* plan) {
     const int G = Hq / Hkv;
     plan->nt = G > 8 ? 2 : 1;
     plan->NHG = (G + plan->nt * 8 - 1) / (plan->nt * 8);
     const long long units = static_cast<long long>(B) * Hkv * plan->NHG;
-    // one grid row per (unit, head) of the joining launch
-    if (units * std::min(G, plan->nt * 8) > 0x7fffffffLL) return KVD_ERR_UNSUPPORTED;
-    plan->units = static_cast<int>(units);
-    const int per_sm = (plan->nt == 1 && dtype == KVD_BF16) ? 2 : 1;
     const long long tiles = units * ((max_len + kTileTok - 1) / kTileTok + 1);
-    plan->ctas = static_cast<int>(std::max(
-        1LL, std::min<long long>(1LL * num_sms() * per_sm, (tiles + kWarps - 1) / kWarps)));
-    const size_t slots = static_cast<size_t>(plan->ctas) * kWarps + units;
+    if (tiles >= (1LL << 31)) return KVD_ERR_UNSUPPORTED;
+    plan->units = static_cast<int>(units);
+    const int warps = warps_of(plan->nt, dtype == KVD_F32);
+    plan->ctas = static_cast<int>(std::max(1LL, std::min<long long>(num_sms(), tiles)));
+    plan->n_warps = plan->ctas * warps;
+    const size_t slots = static_cast<size_t>(plan->n_warps) + units;
     const size_t heads = static_cast<size_t>(plan->nt) * 8;
-    plan->off_ml = 0;
-    plan->off_o = (slots * heads * 8 + 255) & ~static_cast<size_t>(255);
+    auto round = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    plan->off_m = 0;
+    plan->off_l = round(slots * heads * 4);
+    plan->off_o = plan->off_l + round(slots * heads * 4);
     plan->total = plan->off_o + slots * heads * D * 4;
     return KVD_OK;
 }

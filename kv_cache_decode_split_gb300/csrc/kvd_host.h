@@ -191,8 +191,9 @@ struct Q4Params {
     const float* sink_logit;
     void* out;
     float* lse_out;
-    float* part_o;             // [slots, heads of a block, D], one slot per (warp, unit) piece
-    float* part_ml;            // [slots, heads of a block, 2]: maximum (log2 domain) and sum
+    // one slot per (warp, unit) piece: unnormalised outputs, softmax references and sums
+    float* part_o;             // [slots, 8 heads, D], in the order of the lanes' registers
+    float *part_m, *part_l;    // [slots, heads of a block]
     int* err;                  // optional
     int B, Hq, Hkv, G, NHG;    // NHG: head blocks of a KV head
     int HU;                    // units of a sequence: Hkv * NHG
@@ -203,8 +204,8 @@ struct Q4Params {
 };
 struct Q4Plan {
     int nt;                    // 8-head column tiles of a head block (1 or 2)
-    int NHG, units, ctas;
-    size_t off_ml, off_o, total;
+    int NHG, units, ctas, n_warps;
+    size_t off_m, off_l, off_o, total;
 };
 int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan* plan);
 int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream);
