@@ -187,13 +187,20 @@ struct Q4Cfg {
     static constexpr int kSmem = kWarps * kPerWarp + 16;
 };
 
-template <int D, int NT, bool kF32>
+// kPair (128 channels, at most 4 heads): the matrix instructions' 8 columns are the heads once for
+// each group of 64 channels. Column h takes the queries of group 0 (and zeros), column 4 + h those
+// of group 1; a lane then scales its own group's products, adds the other half's (one exchange),
+// and its weights carry its own group's scale: half the scaling, packing and transposing of the
+// general form, where half the columns would be empty.
+template <int D, int NT, bool kF32, bool kPair>
 __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     gqa_q4_kernel(const Q4Params p) {
     using Cfg = Q4Cfg<D, NT, kF32>;
     using L4 = Q4<D>;
     constexpr int S = Cfg::kStages, kWarps = Cfg::kWarps;
-    constexpr int NG = L4::kGroups;
+    static_assert(!kPair || (D == 128 && NT == 1 && !kF32), "two groups, one column tile");
+    constexpr int NG = kPair ? 1 : L4::kGroups;  // groups that a lane scales
+    constexpr int NQ = kPair ? 2 : NG;           // accumulators of a score
     constexpr int KW = D / 32;             // key words of a lane and row
     constexpr int MT = D / 16;             // 16-channel tiles of the output
     constexpr int kQ = kF32 ? 3 : 1;       // bf16 parts of a query
@@ -201,6 +208,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
+    const int own = kPair ? t >> 1 : 0;  // (kPair) this lane's group
     uint8_t* ring = smem + warp * Cfg::kRing;
     TileInfo* info = reinterpret_cast<TileInfo*>(smem + kWarps * Cfg::kRing) + warp * S;
     uint64_t* full = reinterpret_cast<uint64_t*>(
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float part[NG] = {};
-                const int h = nt * 8 + g;
+                const int h = kPair ? g & 3 : nt * 8 + g;
                 const bool ok = h < un.z;
                 const size_t qrow = (static_cast<size_t>(un.x) * p.Hq + un.y + (ok ? h : 0)) * D;
 #pragma unroll
@@ -393,8 +401,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        if (!ok) x[e] = 0.f;
-                        part[w / 2] += x[e];
+                        if (!ok || (kPair && w / 2 != g >> 2)) x[e] = 0.f;
+                        part[kPair ? 0 : w / 2] += x[e];
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {  // fragments pair channels e and e + 4
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 *reinterpret_cast<uint2*>(wb) =
                     *reinterpret_cast<const uint2*>(kb + (g + 8) * 32 + t * 8);
             }
-            float acc[NT][NG][4];
+            float acc[NT][NQ][4];
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 uint32_t fa[4], fb[4];
@@ -482,20 +490,27 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < kQ; ++k) {
-                        if (k == 0 && w % 2 == 0)
-                            mma_bf16_first(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1],
-                                           qf[k][nt][w][0], qf[k][nt][w][1]);
+                        float(&c0)[4] = acc[nt][kPair ? 0 : w / 2];
+                        float(&c1)[4] = acc[nt][kPair ? 1 : w / 2];
+                        const bool fresh = k == 0 && (kPair ? w == 0 : w % 2 == 0);
+                        if (fresh)
+                            mma_bf16_first(c0, fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
+                                           qf[k][nt][w][1]);
                         else
-                            mma_bf16(acc[nt][w / 2], fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
+                            mma_bf16(c0, fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
                                      qf[k][nt][w][1]);
-                        mma_bf16(acc[nt][w / 2], fa[2], fb[2], fa[3], fb[3], qf[k][nt][w][2],
-                                 qf[k][nt][w][3]);
+                        if (fresh && kPair)
+                            mma_bf16_first(c1, fa[2], fb[2], fa[3], fb[3], qf[k][nt][w][2],
+                                           qf[k][nt][w][3]);
+                        else
+                            mma_bf16(c1, fa[2], fb[2], fa[3], fb[3], qf[k][nt][w][2],
+                                     qf[k][nt][w][3]);
                     }
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const __half2* pr =
-                    reinterpret_cast<const __half2*>(kb + L4::param(g + 8 * half, 0));
+                    reinterpret_cast<const __half2*>(kb + L4::param(g + 8 * half, own));
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
                     const float2 f = __half22float2(pr[gr]);  // scale, minimum
@@ -507,7 +522,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                         for (int c = 0; c < 2; ++c) {
                             float& v = x[bk][nt][2 * half + c];
                             v = gr ? fmaf(base, qsum[nt][gr][c], v) : base * qsum[nt][gr][c];
-                            v = fmaf(f.x, acc[nt][gr][2 * half + c], v);
+                            float a = acc[nt][gr][2 * half + c];
+                            if (kPair) a += acc[nt][NQ - 1][2 * half + c];
+                            v = fmaf(f.x, a, v);
+                            if (kPair) v += __shfl_xor_sync(0xffffffffu, v, 2);
                         }
                 }
             }
@@ -517,7 +535,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const __half2* pr = reinterpret_cast<const __half2*>(
-                vt + (k >> 1) * L4::kBlockBytes + L4::param(g + 8 * (k & 1), 0));
+                vt + (k >> 1) * L4::kBlockBytes + L4::param(g + 8 * (k & 1), own));
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
                 vs[k][gr] = __low2float(pr[gr]);
@@ -574,7 +592,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                         if ((seen >> k) & 1) v = fmaxf(v, xs + fmaxf(log2f(sc) - 8.f, -60.f));
                     }
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1)
+                    for (int off = kPair ? 2 : 4; off < 32; off <<= 1)
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
                     v = fmaxf(v, m[nt][c]);
                     const float al = fast_exp2(m[nt][c] - v);
@@ -602,7 +620,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const __half2* pr =
-                    reinterpret_cast<const __half2*>(vb + L4::param(g + 8 * half, 0));
+                    reinterpret_cast<const __half2*>(vb + L4::param(g + 8 * half, own));
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
                     vm[half][gr] = __high2float(pr[gr]);
@@ -635,7 +653,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 va = *reinterpret_cast<const uint4*>(vb + lane * 16);
             }
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
+            for (int gr = 0; gr < L4::kGroups; ++gr) {
+                const int gp = kPair ? 0 : gr;  // index of the group's weights
                 uint32_t w0, w1, w2, w3;  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
                 if constexpr (D == 128) {
                     w0 = gr ? va.y : va.x, w1 = gr ? va.w : va.z;
@@ -668,13 +687,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k = 0; k < kP; ++k) {
-                            mma_f16(o[nt][mt], fu[0], fu[1], fv[0], fv[1], pf[nt][gr][k][0],
-                                    pf[nt][gr][k][1]);
-                            mma_f16(o[nt][mt + 1], fu[2], fu[3], fv[2], fv[3], pf[nt][gr][k][0],
-                                    pf[nt][gr][k][1]);
+                            mma_f16(o[nt][mt], fu[0], fu[1], fv[0], fv[1], pf[nt][gp][k][0],
+                                    pf[nt][gp][k][1]);
+                            mma_f16(o[nt][mt + 1], fu[2], fu[3], fv[2], fv[3], pf[nt][gp][k][0],
+                                    pf[nt][gp][k][1]);
                         }
                 }
-                if constexpr (!kF32) {
+                if (!kF32 && gr < NG) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma_f16(oo[nt][gr], kValOff, kValOff, kValOff, kValOff, pf[nt][gr][0][0],
@@ -712,7 +731,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                     }
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) add[gr][c] += oo[nt][gr][c];
-                    const int h = nt * 8 + 2 * t + c;
+                    const int h = kPair ? 2 * (t & 1) + c : nt * 8 + 2 * t + c;
                     mul[c] = 1.f;
                     if (h >= un.z) continue;
                     if (whole) {  // nothing to join: the output itself
@@ -722,34 +741,45 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                         const float w = fast_exp2(m[nt][c] - M);
                         const float den = lv * w + (p.sink_logit ? fast_exp2(sig - M) : 0.f);
                         mul[c] = w / den;
-                        if (p.lse_out && g == 0)
+                        if (p.lse_out && g == 0 && own == 0)
                             p.lse_out[static_cast<size_t>(un.x) * p.Hq + hq] =
                                 (M + log2f(den)) * kLn2;
-                    } else if (g == 0) {
+                    } else if (g == 0 && own == 0) {
                         __stcg(p.part_m + slot * (NT * 8) + h, m[nt][c]);
                         __stcg(p.part_l + slot * (NT * 8) + h, lv);
                     }
                 }
-                if (nt * 8 + 2 * t >= un.z) continue;
-                if (!whole) {  // as the lanes hold it: 16 bytes of 8 x 2 channels and heads each
-                    float* dst = p.part_o + (slot * NT + nt) * (D * 8) + lane * 4;
+                // (kPair: this lane has its own group's half of the channels, of heads 0-3)
+                const int h0 = kPair ? 2 * (t & 1) : nt * 8 + 2 * t;
+                if (h0 >= un.z) continue;
+                constexpr int kHave = kPair ? MT / 2 : MT;
+                float r[kHave][4];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < kHave; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = kPair && own ? o[nt][mt + MT - kHave][e] : o[nt][mt][e];
+                        r[mt][e] = v + add[kPair ? 0 : mt / 4][e & 1];
+                    }
+                if (!whole) {  // 16 bytes of 8 x 2 channels and heads each
+                    float* dst = p.part_o + (slot * NT + nt) * (D * 8) +
+                                 (kPair ? own * (kHave * 128) + (4 * g + (t & 1)) * 4 : lane * 4);
+#pragma unroll
+                    for (int mt = 0; mt < kHave; ++mt)
                         __stcg(reinterpret_cast<float4*>(dst + mt * 128),
-                               make_float4(o[nt][mt][0] + add[mt / 4][0], o[nt][mt][1] + add[mt / 4][1],
-                                           o[nt][mt][2] + add[mt / 4][0], o[nt][mt][3] + add[mt / 4][1]));
+                               make_float4(r[mt][0], r[mt][1], r[mt][2], r[mt][3]));
                     continue;
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int h = nt * 8 + 2 * t + c;
-                    if (h >= un.z) continue;
-                    const size_t at = (static_cast<size_t>(un.x) * p.Hq + un.y + h) * D + g;
+                    if (h0 + c >= un.z) continue;
+                    const size_t at = (static_cast<size_t>(un.x) * p.Hq + un.y + h0 + c) * D + g +
+                                      own * (kHave * 16);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int mt = 0; mt < kHave; ++mt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float v = (o[nt][mt][2 * e + c] + add[mt / 4][c]) * mul[c];
+                            const float v = r[mt][2 * e + c] * mul[c];
                             if constexpr (kF32)
                                 static_cast<float*>(p.out)[at + mt * 16 + 8 * e] = v;
                             else
@@ -907,10 +937,10 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
     }
 }
 
-template <int D, int NT, bool kF32>
+template <int D, int NT, bool kF32, bool kPair>
 int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
     using Cfg = Q4Cfg<D, NT, kF32>;
-    auto kern = gqa_q4_kernel<D, NT, kF32>;
+    auto kern = gqa_q4_kernel<D, NT, kF32, kPair>;
     static int configured = 0;
     if (!configured) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem) !=
@@ -960,16 +990,18 @@ int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan*
 int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream) {
     if (dtype == KVD_F32) {
         if (D == 128)
-            return plan.nt == 1 ? launch_q4<128, 1, true>(plan, p, stream)
-                                : launch_q4<128, 2, true>(plan, p, stream);
-        return plan.nt == 1 ? launch_q4<64, 1, true>(plan, p, stream)
-                            : launch_q4<64, 2, true>(plan, p, stream);
+            return plan.nt == 1 ? launch_q4<128, 1, true, false>(plan, p, stream)
+                                : launch_q4<128, 2, true, false>(plan, p, stream);
+        return plan.nt == 1 ? launch_q4<64, 1, true, false>(plan, p, stream)
+                            : launch_q4<64, 2, true, false>(plan, p, stream);
     }
-    if (D == 128)
-        return plan.nt == 1 ? launch_q4<128, 1, false>(plan, p, stream)
-                            : launch_q4<128, 2, false>(plan, p, stream);
-    return plan.nt == 1 ? launch_q4<64, 1, false>(plan, p, stream)
-                        : launch_q4<64, 2, false>(plan, p, stream);
+    if (D == 128) {
+        if (p.G <= 4) return launch_q4<128, 1, false, true>(plan, p, stream);
+        return plan.nt == 1 ? launch_q4<128, 1, false, false>(plan, p, stream)
+                            : launch_q4<128, 2, false, false>(plan, p, stream);
+    }
+    return plan.nt == 1 ? launch_q4<64, 1, false, false>(plan, p, stream)
+                        : launch_q4<64, 2, false, false>(plan, p, stream);
 }
 
 }  // namespace kvd
