@@ -297,15 +297,27 @@ def q4_pool(num_pages, Hkv, page_size, D, device=None):
                        device="cuda" if device is None else device)
 
 
-def _on(dev, stream, call):
-    """call(stream handle) on the tensors' device: the given stream, which must be that
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the current stream's handle without building a Stream object (microseconds), where PyTorch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _on(dev, stream, fn, args):
+    """fn(*args, stream handle) on the tensors' device: the given stream, which must be that
     device's, or its current one."""
-    if stream is not None and stream.device.index != dev:
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
         raise ValueError("stream and tensors must be on one device")
     if dev == torch.cuda.current_device():
-        return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        return fn(*args, handle)
     with torch.cuda.device(dev):
-        return call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        return fn(*args, handle)
 
 
 def _empty(shape, dtype, like, stream):
@@ -318,6 +330,12 @@ def _empty(shape, dtype, like, stream):
 
 def _same(t, name, dev, dtype, shape):
     """A dense CUDA tensor of this device, type and shape; its address."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -326,80 +344,90 @@ def _same(t, name, dev, dtype, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the device of the other tensors")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _tokens(t, name, dev, dtype, T, H, D):
+def _tokens(t, name, dev, dtype, shape):
     """[T, H, D] with dense heads; its address and the elements between tokens."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            s0, s1, s2 = t.stride()
+            T, H, D = shape
+            if s2 == 1 and (s1 == D or H == 1):
+                return t.data_ptr(), (s0 if T > 1 else H * D)
+            raise ValueError(f"{name} must have dense heads (strides {D}, 1 in a token)")
+    except AttributeError:
+        pass
+    _same(t, name, dev, dtype, shape)  # says what is wrong
+
+
+def _cuda3(t, name, what):
+    """The leading tensor of a call: a float32 or bfloat16 CUDA tensor of three dims."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (T, H, D):
-        raise ValueError(f"{name} must be {[T, H, D]}, got {list(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the device of the other tensors")
-    s = t.stride()
-    if s[2] != 1 or (s[1] != D and H > 1):
-        raise ValueError(f"{name} must have dense heads (strides {D}, 1 in a token)")
-    return t.data_ptr(), (s[0] if T > 1 else H * D)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be {what}")
+    if t.dtype not in _DT:
+        raise TypeError(f"{name} must be float32 or bfloat16")
 
 
 def _rope_args(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens,
                q_out, err, stream, q4):
-    """The arguments that both appends share, checked: (device, T, rotated queries, leading
-    C arguments, sizes)."""
-    if not isinstance(k_new, torch.Tensor) or not k_new.is_cuda:
-        raise TypeError("k_new must be a CUDA tensor")
-    if k_new.dim() != 3:
-        raise ValueError("k_new must be [T, Hkv, D]")
-    if k_new.dtype not in _DT:
-        raise TypeError("k_new must be float32 or bfloat16")
-    T, Hkv, D = k_new.shape
+    """The arguments that both appends share, checked: (device, rotated queries, leading C
+    arguments, sizes up to rot_dim, pool sizes and dtype, err)."""
+    _cuda3(k_new, "k_new", "[T, Hkv, D]")
+    kv = k_new.shape
+    T, Hkv, D = kv
     dev, dt = k_new.get_device(), k_new.dtype
-    _need(k_pool, "k_pool", torch.uint8 if q4 else dt, 3 if q4 else 4)
-    num_pages = k_pool.shape[0]
-    if q4:
-        P = k_pool.shape[2] // (D // 2 + D // 16) if D in (64, 128) else 0
-        if P < 1 or k_pool.shape[1] != Hkv or k_pool.shape[2] != P * (D // 2 + D // 16):
-            raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]")
-    else:
-        P = k_pool.shape[2]
-        if k_pool.shape[1] != Hkv or k_pool.shape[3] != D:
-            raise ValueError("k_pool must be [num_pages, Hkv, page_size, D]")
-    _need(cos_sin, "cos_sin", torch.float32, 2)
-    _need(block_table, "block_table", torch.int32, 2)
-    B, max_pages = block_table.shape
-    max_pos, rot = cos_sin.shape
-    for t, n in ((k_pool, "k_pool"), (cos_sin, "cos_sin"), (block_table, "block_table")):
-        if t.get_device() != dev:
-            raise ValueError(f"{n} must be on the device of the other tensors")
-    kp, ks = _tokens(k_new, "k_new", dev, dt, T, Hkv, D)
-    vp, vs = _tokens(v_new, "v_new", dev, dt, T, Hkv, D)
-    qp, qs, Hq, qo = None, 0, 0, None
+    try:
+        pool = k_pool.shape
+        B, max_pages = block_table.shape
+        max_pos, rot = cos_sin.shape
+        if q4:
+            num_pages, h, P = pool
+            per = D // 2 + D // 16
+            ok = D in (64, 128) and P % per == 0
+            P //= per
+        else:
+            num_pages, h, P, d = pool
+            ok = d == D
+        if not ok or h != Hkv or P < 1:
+            raise ValueError
+    except (AttributeError, ValueError):
+        _need(k_pool, "k_pool", torch.uint8 if q4 else dt, 3 if q4 else 4)
+        _need(block_table, "block_table", torch.int32, 2)
+        _need(cos_sin, "cos_sin", torch.float32, 2)
+        raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]" if q4 else
+                         "k_pool must be [num_pages, Hkv, page_size, D]") from None
+    pool_dt = torch.uint8 if q4 else dt
+    kp, ks = _tokens(k_new, "k_new", dev, dt, kv)
+    vp, vs = _tokens(v_new, "v_new", dev, dt, kv)
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be [T, Hq, D]")
         Hq = q.shape[1]
-        qp, qs = _tokens(q, "q", dev, dt, T, Hq, D)
+        shape = (T, Hq, D)
+        qp, qs = _tokens(q, "q", dev, dt, shape)
         if q_out is None:
-            q_out = _empty((T, Hq, D), dt, k_new, stream)
-        qo = _same(q_out, "q_out", dev, dt, (T, Hq, D))
+            q_out = _empty(shape, dt, k_new, stream)
+        qo = _same(q_out, "q_out", dev, dt, shape)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    cu = None
+    else:
+        qp, qs, Hq, qo = None, 0, 0, None
     if cu_seqlens is not None:
         cu = _same(cu_seqlens, "cu_seqlens", dev, torch.int32, (B + 1,))
     elif T != B:
         raise ValueError("without cu_seqlens there is one token of each sequence")
-    head = (qp, kp, vp, cos_sin.data_ptr(), cu, block_table.data_ptr(),
-            _same(seq_lens, "seq_lens", dev, torch.int32, (B,)), qo, k_pool.data_ptr(),
-            _same(v_pool, "v_pool", dev, k_pool.dtype, k_pool.shape))
+    else:
+        cu = None
+    head = (qp, kp, vp, _same(cos_sin, "cos_sin", dev, torch.float32, (max_pos, rot)), cu,
+            _same(block_table, "block_table", dev, torch.int32, (B, max_pages)),
+            _same(seq_lens, "seq_lens", dev, torch.int32, (B,)), qo,
+            _same(k_pool, "k_pool", dev, pool_dt, pool), _same(v_pool, "v_pool", dev, pool_dt, pool))
     err_p = None if err is None else _same(err, "err", dev, torch.int32, (1,))
-    sizes = (B, T, Hq, Hkv, D, qs, ks, vs, rot)
-    return dev, q_out, head, sizes, (max_pos, P, max_pages, num_pages, _DT[dt]), err_p
+    return (dev, q_out, head, (B, T, Hq, Hkv, D, qs, ks, vs, rot),
+            (max_pos, P, max_pages, num_pages, _DT[dt]), err_p)
 
 
 def rope_append(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens=None,
@@ -419,8 +447,8 @@ def rope_append(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens,
     dev, q_out, head, sizes, pool, err_p = _rope_args(
         q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens, q_out, err,
         stream, False)
-    st = _on(dev, stream, lambda s: lib.kvd_rope_append(
-        *head, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink), err_p, s))
+    st = _on(dev, stream, lib.kvd_rope_append,
+             (*head, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink), err_p))
     _check(st, "kvd_rope_append")
     return q_out
 
@@ -435,9 +463,9 @@ def rope_append_q4(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_le
         stream, True)
     ko = None if k_out is None else _same(k_out, "k_out", dev, k_new.dtype, k_new.shape)
     vo = None if v_out is None else _same(v_out, "v_out", dev, k_new.dtype, k_new.shape)
-    st = _on(dev, stream, lambda s: lib.kvd_rope_append_q4(
-        *head, ko, vo, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink), err_p,
-        s))
+    st = _on(dev, stream, lib.kvd_rope_append_q4,
+             (*head, ko, vo, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink),
+              err_p))
     _check(st, "kvd_rope_append_q4")
     return q_out
 
@@ -454,44 +482,44 @@ def attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window=0, n_sin
     memory from PyTorch's allocator, so calls on several streams and captured graphs never share
     it. A bad length or page id is recorded in err (int32 [1]) and clamped.
     """
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
-    if q.dim() != 3:
-        raise ValueError("q must be [B, Hq, D]")
-    if q.dtype not in _DT:
-        raise TypeError("q must be float32 or bfloat16")
-    B, Hq, D = q.shape
-    dev = q.get_device()
-    qp = _same(q, "q", dev, q.dtype, q.shape)
-    _need(k_pool, "k_pool", torch.uint8, 3)
-    num_pages, Hkv, page = k_pool.shape
-    P = page // (D // 2 + D // 16) if D in (64, 128) else 0
-    if P < 1 or page != P * (D // 2 + D // 16):
-        raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]")
-    kp = _same(k_pool, "k_pool", dev, torch.uint8, k_pool.shape)
-    vp = _same(v_pool, "v_pool", dev, torch.uint8, k_pool.shape)
-    _need(block_table, "block_table", torch.int32, 2)
-    max_pages = block_table.shape[1]
+    _cuda3(q, "q", "[B, Hq, D]")
+    shape = q.shape
+    B, Hq, D = shape
+    dev, dt = q.get_device(), q.dtype
+    try:
+        pool = k_pool.shape
+        num_pages, Hkv, page = pool
+        max_pages = block_table.shape[1]
+        per = D // 2 + D // 16
+        if D not in (64, 128) or page < per or page % per:
+            raise ValueError
+    except (AttributeError, ValueError, IndexError):
+        _need(k_pool, "k_pool", torch.uint8, 3)
+        _need(block_table, "block_table", torch.int32, 2)
+        raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]") from None
+    P = page // per
+    kp = _same(k_pool, "k_pool", dev, torch.uint8, pool)
+    vp = _same(v_pool, "v_pool", dev, torch.uint8, pool)
     bt = _same(block_table, "block_table", dev, torch.int32, (B, max_pages))
     sl = _same(seq_lens, "seq_lens", dev, torch.int32, (B,))
     sink = None if sink_logit is None else _same(sink_logit, "sink_logit", dev, torch.float32, (Hq,))
     lse = None if lse_out is None else _same(lse_out, "lse_out", dev, torch.float32, (B, Hq))
     err_p = None if err is None else _same(err, "err", dev, torch.int32, (1,))
-    out = _empty((B, Hq, D), q.dtype, q, stream) if out is None else out
-    op = _same(out, "out", dev, q.dtype, q.shape)
+    out = _empty(shape, dt, q, stream) if out is None else out
     if workspace is None or isinstance(workspace, Workspace):
         nbytes = kvd_workspace_size("gqa_q4", B, Hq, Hkv, D, max_pages * P)
         if workspace is None:
             workspace = _empty((max(nbytes, 1),), torch.uint8, q, stream)
         else:
             workspace = workspace.get(nbytes, "gqa_q4")
-    elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
+    elif not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a uint8 tensor or a Workspace")
     ws = _same(workspace, "workspace", dev, torch.uint8, workspace.shape)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    st = _on(dev, stream, lambda s: lib.attn_decode_gqa_q4(
-        qp, kp, vp, bt, sl, op, lse, B, Hq, Hkv, D, P, max_pages, num_pages, scale, _DT[q.dtype],
-        int(window), int(n_sink_tokens), 1 if ring else 0, sink, ws, workspace.numel(), err_p, s))
+    st = _on(dev, stream, lib.attn_decode_gqa_q4, (
+        _same(q, "q", dev, dt, shape), kp, vp, bt, sl, _same(out, "out", dev, dt, shape), lse, B,
+        Hq, Hkv, D, P, max_pages, num_pages, scale, _DT[dt], int(window), int(n_sink_tokens),
+        1 if ring else 0, sink, ws, workspace.numel(), err_p))
     _check(st, "attn_decode_gqa_q4")
     return out
 
