@@ -590,7 +590,6 @@ static int rope_append(bool q4, const void* q, const void* k_new, const void* v_
     p.T = T;
     p.Hq = q ? Hq : 0;
     p.Hkv = Hkv;
-    p.rows = p.Hq + 2 * Hkv;
     p.rot = rot_dim;
     p.interleaved = interleaved ? 1 : 0;
     p.max_pos = max_pos;

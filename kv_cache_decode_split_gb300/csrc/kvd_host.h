@@ -176,7 +176,8 @@ struct RopeAppendParams {
     void *k_out, *v_out;       // 4 bits: [T, Hkv, D] the stored values (optional)
     int* err;                  // optional
     long long q_stride, k_stride, v_stride;  // elements
-    int B, T, Hq, Hkv, rows;   // rows = Hq (0 without q) + 2 Hkv
+    int B, T, Hq, Hkv;         // Hq 0 without q
+    int q_rows, kv_rows, q_items, kv_items;  // rows of a warp, warps of a token (each kind)
     int rot, interleaved, max_pos, page_shift, max_pages, num_pages, window, n_sink;
 };
 int rope_append_launch(const RopeAppendParams& p, bool q4, int D, int dtype,

@@ -123,259 +123,332 @@ __device__ __forceinline__ void rotate_pair(float& x, float& y, float c, float s
     x = a;
 }
 
+// One step of a transposition among neighbouring lanes: lane pairs kLane apart exchange the parts of
+// kBits bits that belong to the other.
+template <int kLane, int kBits>
+__device__ __forceinline__ uint32_t swap_parts(uint32_t w, int lane) {
+    constexpr uint32_t kLow = kBits == 16 ? 0x0000ffffu : kBits == 8 ? 0x00ff00ffu : 0x0f0f0f0fu;
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, w, kLane);
+    return (lane & kLane) ? (w & ~kLow) | ((o >> kBits) & kLow)
+                          : (w & kLow) | ((o & kLow) << kBits);
+}
 // Nibble m of lane j's word becomes nibble j of lane m's word, among 8 neighbouring lanes.
 __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane) {
-    uint32_t o = __shfl_xor_sync(0xffffffffu, w, 4);
-    w = (lane & 4) ? ((w & 0xffff0000u) | (o >> 16)) : ((w & 0x0000ffffu) | (o << 16));
-    o = __shfl_xor_sync(0xffffffffu, w, 2);
-    w = (lane & 2) ? ((w & 0xff00ff00u) | ((o >> 8) & 0x00ff00ffu))
-                   : ((w & 0x00ff00ffu) | ((o & 0x00ff00ffu) << 8));
-    o = __shfl_xor_sync(0xffffffffu, w, 1);
-    return (lane & 1) ? ((w & 0xf0f0f0f0u) | ((o >> 4) & 0x0f0f0f0fu))
-                      : ((w & 0x0f0f0f0fu) | ((o & 0x0f0f0f0fu) << 4));
+    return swap_parts<1, 4>(swap_parts<2, 8>(swap_parts<4, 16>(w, lane), lane), lane);
 }
 
-// One warp: one token, 32 / (D/16) rows at a time, R rows a lane.
-template <typename T, int D, bool kQ4, int R>
-__global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendParams p) {
-    griddep_wait();
+// Minimum and maximum that keep a NaN.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <int N>
+__device__ __forceinline__ float least(const float (&x)[N]) {
+    float d = min3(x[0], x[1], x[2]);
+#pragma unroll
+    for (int e = 3; e < N; e += 2) d = min3(d, x[e], x[e + 1 < N ? e + 1 : e]);
+    return d;
+}
+template <int N>
+__device__ __forceinline__ float most(const float (&x)[N]) {
+    float d = max3(x[0], x[1], x[2]);
+#pragma unroll
+    for (int e = 3; e < N; e += 2) d = max3(d, x[e], x[e + 1 < N ? e + 1 : e]);
+    return d;
+}
+
+// 4-bit codes of a row whose lane has pieces pa and pb (x, y): stored in the token's block, and,
+// where `vals` is given, as the values that they stand for. Every lane of the warp comes here;
+// `store` and `vals` say whether this lane's row is written.
+template <typename T, int D, bool kV>
+__device__ __forceinline__ void put_q4(float (&x)[8], float (&y)[8], int pa, int pb, int j,
+                                       uint8_t* blk, int r, bool store, T* vals) {
+    using L4 = Q4<D>;
+    constexpr int kTeam = D / 16, NG = L4::kGroups;
+    constexpr float kInf = __builtin_huge_valf();
+    // Scale and minimum of the row's groups (piece c belongs to group c / 8). Clamping to the
+    // float16 range commutes with minimum and maximum, and a value beyond it takes code 0 or 15
+    // either way; a NaN stays in the minimum and maximum, an infinity shows in one of them.
+    const float lo_a = least<8>(x), hi_a = most<8>(x), lo_b = least<8>(y), hi_b = most<8>(y);
+    // (one group: both pieces are of it; two: pieces a and b are of groups 0 and 1, or, with fewer
+    // channels rotated, of any)
+    float lo[NG], hi[NG];
+    if constexpr (NG == 1) {
+        lo[0] = min3(lo_a, lo_b, lo_b), hi[0] = max3(hi_a, hi_b, hi_b);
+    } else {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const bool ag = pa >> 3 == g, bg = pb >> 3 == g;
+            const float la = ag ? lo_a : kInf, lb = bg ? lo_b : kInf;
+            const float ha = ag ? hi_a : -kInf, hb = bg ? hi_b : -kInf;
+            lo[g] = min3(la, lb, lb), hi[g] = max3(ha, hb, hb);
+        }
+    }
+#pragma unroll
+    for (int off = 1; off < kTeam; off <<= 1)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float ol = __shfl_xor_sync(0xffffffffu, lo[g], off);
+            const float oh = __shfl_xor_sync(0xffffffffu, hi[g], off);
+            lo[g] = min3(lo[g], ol, ol), hi[g] = max3(hi[g], oh, oh);
+        }
+    float step[NG], base[NG], inv[NG];
+    uint32_t par[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const bool bad = !(lo[g] > -kInf && hi[g] < kInf);
+        const float l = fminf(fmaxf(lo[g], -65504.f), 65504.f);
+        const float h = fminf(fmaxf(hi[g], -65504.f), 65504.f);
+        const __half hb = bad ? __ushort_as_half(0x7fff) : __float2half_rn(l);
+        const __half hs = bad ? __ushort_as_half(0)
+                              : __float2half_rn(__fmul_rn(__fsub_rn(h, l), 1.0f / 15.0f));
+        step[g] = __half2float(hs);
+        base[g] = __half2float(hb);
+        inv[g] = step[g] > 0.f ? __frcp_rn(step[g]) : 0.f;
+        par[g] = __half_as_ushort(hs) | static_cast<uint32_t>(__half_as_ushort(hb)) << 16;
+    }
+    const bool a1 = NG == 2 && pa >= 8, b1 = NG == 2 && pb >= 8;
+    const float base_a = a1 ? base[NG - 1] : base[0], base_b = b1 ? base[NG - 1] : base[0];
+    const float inv_a = a1 ? inv[NG - 1] : inv[0], inv_b = b1 ? inv[NG - 1] : inv[0];
+    // rounding by adding 1.5 2^23: the code is then the sum's low bits (a NaN group has factor 0
+    // and a NaN minimum: the comparison makes it 0)
+    constexpr float kMagic = 12582912.f;
+    auto code = [&](float v, float from, float by) {
+        const float c = __fmul_rn(__fsub_rn(v, from), by);
+        return __fadd_rn(fminf(fmaxf(c, 0.f), 15.f), kMagic);
+    };
+    uint32_t wa = 0, wb = 0;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) {  // x and y become the codes (plus kMagic)
+        x[e] = code(x[e], base_a, inv_a);
+        y[e] = code(y[e], base_b, inv_b);
+        wa = wa * 16 + __float_as_uint(x[e]);
+        wb = wb * 16 + __float_as_uint(y[e]);
+    }
+    wa -= 0x4B400000u * 0x11111111u;
+    wb -= 0x4B400000u * 0x11111111u;
+    if (vals) {
+        const float step_a = a1 ? step[NG - 1] : step[0], step_b = b1 ? step[NG - 1] : step[0];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = fmaf(step_a, x[e] - kMagic, base_a);
+            y[e] = fmaf(step_b, y[e] - kMagic, base_b);
+        }
+        Piece<T>::put(vals + 8 * pa, x);
+        Piece<T>::put(vals + 8 * pb, y);
+    }
+    uint32_t* words = reinterpret_cast<uint32_t*>(blk);
+    if constexpr (!kV) {
+        if (store) {
+            words[L4::k_word(r, pa)] = __funnelshift_l(wa, wa, 3);
+            words[L4::k_word(r, pb)] = __funnelshift_l(wb, wb, 3);
+        }
+    } else if constexpr (D == 128) {
+        wa = transpose_nibbles(wa, j);
+        wb = transpose_nibbles(wb, j);
+        if (store)
+            *reinterpret_cast<uint2*>(words + L4::v_word(r, j, 0)) = make_uint2(wa, wb);
+    } else {  // pieces j and j + 4 of the 8: the first exchange stays in the thread
+        const uint32_t u = (wa & 0x0000ffffu) | (wb << 16), v = (wa >> 16) | (wb & 0xffff0000u);
+        wa = swap_parts<1, 4>(swap_parts<2, 8>(u, j), j);
+        wb = swap_parts<1, 4>(swap_parts<2, 8>(v, j), j);
+        if (store) {
+            words[L4::v_word(r, j, 0)] = wa;
+            words[L4::v_word(r, j + 4, 0)] = wb;
+        }
+    }
+    if (store && j < NG)
+        *reinterpret_cast<uint32_t*>(blk + L4::param(r, j)) = j ? par[NG - 1] : par[0];
+}
+
+// Rows begin .. end - 1 of one kind (0 queries, 1 keys, 2 values) of token i, by one warp, R rows of a
+// lane at a time.
+template <typename T, int D, bool kQ4, int R, int kKind>
+__device__ __forceinline__ void append_rows(const RopeAppendParams& p, int i, int begin, int end,
+                                            int lane) {
     using L4 = Q4<D>;
     constexpr int kTeam = D / 16;       // lanes of a row
-    constexpr int kTeams = 32 / kTeam;  // rows of a warp's step
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    constexpr int kTeams = 32 / kTeam;  // rows of a warp at once
     const int team = lane / kTeam, j = lane % kTeam;
-    const long long item = static_cast<long long>(blockIdx.x) * 8 + warp;
-    const int parts = (p.rows + kTeams * R - 1) / (kTeams * R);
-    if (item >= static_cast<long long>(p.T) * parts) return;
-    const int i = static_cast<int>(item / parts);
-    const int row0 = static_cast<int>(item % parts) * kTeams * R + team;
-
+    const T* src = kKind == 0   ? static_cast<const T*>(p.q) + i * p.q_stride
+                   : kKind == 1 ? static_cast<const T*>(p.k) + i * p.k_stride
+                                : static_cast<const T*>(p.v) + i * p.v_stride;
     // pieces of a rotated row: (c, c + rot/16) for the pairs, then neighbours; of a value row
     // (j, j + D/16)
     const int rp = p.rot / 16;
-    const int ca = j < rp ? j : 2 * j, cb = j < rp ? j + rp : 2 * j + 1;
+    const bool turns = kKind != 2 && j < rp;
+    const int pa = kKind == 2 || j < rp ? j : 2 * j;
+    const int pb = kKind == 2 ? j + kTeam : j < rp ? j + rp : 2 * j + 1;
     Piece<T> a[R], b[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const int row = row0 + k * kTeams;
-        if (row >= p.rows) continue;
-        const T* src;
-        int pa = ca, pb = cb;
-        if (row < p.Hq) {
-            src = static_cast<const T*>(p.q) + i * p.q_stride + row * D;
-        } else if (row < p.Hq + p.Hkv) {
-            src = static_cast<const T*>(p.k) + i * p.k_stride + (row - p.Hq) * D;
-        } else {
-            src = static_cast<const T*>(p.v) + i * p.v_stride + (row - p.Hq - p.Hkv) * D;
-            pa = j, pb = j + kTeam;
+    auto load = [&](int k, int row) {
+        if (row < end) {
+            a[k].load(src + row * D + 8 * pa);
+            b[k].load(src + row * D + 8 * pb);
         }
-        a[k].load(src + 8 * pa);
-        b[k].load(src + 8 * pb);
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < R; ++k) load(k, begin + team + k * kTeams);
     const TokenAt at = locate(p, i, lane);
     if (!at.ok) return;
-    // the token's row in the cache
-    int page = -1;
-    if (at.slot >= 0) {
-        page = __ldg(p.block_table + static_cast<size_t>(at.b) * p.max_pages +
-                     (at.slot >> p.page_shift));
-        if (page < 0 || page >= p.num_pages) {
-            record_error(p.err, KVD_ERR_DEVICE_OOB);
-            page = -1;
+    // where the rows go: queries, or the cache's rows of this token
+    T* dst = nullptr;    // (null: not written)
+    uint8_t* blk = nullptr;
+    T* vals = nullptr;
+    size_t dst_row = D;  // elements, or bytes of 4-bit pages, between heads
+    const int in_page = at.slot & ((1 << p.page_shift) - 1);
+    if constexpr (kKind == 0) {
+        dst = static_cast<T*>(p.q_out) + static_cast<size_t>(i) * p.Hq * D;
+    } else {
+        void* pool = kKind == 2 ? p.v_pool : p.k_pool;
+        int page = -1;
+        if (at.slot >= 0) {
+            page = __ldg(p.block_table + static_cast<size_t>(at.b) * p.max_pages +
+                         (at.slot >> p.page_shift));
+            if (page < 0 || page >= p.num_pages) {
+                record_error(p.err, KVD_ERR_DEVICE_OOB);
+                page = -1;
+            }
+        }
+        if constexpr (kQ4) {
+            dst_row = static_cast<size_t>(L4::kBlockBytes) << (p.page_shift - 4);
+            if (page >= 0)
+                blk = static_cast<uint8_t*>(pool) + page * (p.Hkv * dst_row) +
+                      (in_page >> 4) * L4::kBlockBytes;
+            vals = static_cast<T*>(kKind == 2 ? p.v_out : p.k_out);
+            if (vals) vals += static_cast<size_t>(i) * p.Hkv * D;
+        } else {
+            dst_row = static_cast<size_t>(D) << p.page_shift;
+            if (page >= 0)
+                dst = static_cast<T*>(pool) + page * (p.Hkv * dst_row) +
+                      static_cast<size_t>(in_page) * D;
         }
     }
-    const int in_page = at.slot & ((1 << p.page_shift) - 1);
     // cosines and sines of this lane's pairs: halves share them (8 + 8), interleaved pieces have
     // four pairs each
     float cs[8], sn[8];
-    {
+    if (turns) {
         const float* row = p.cos_sin + static_cast<size_t>(at.pos) * p.rot;
         const int h = p.rot / 2;
-        if (j < rp) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int o = p.interleaved ? (e ? cb : ca) * 4 : ca * 8 + 4 * e;
-                const float4 c = __ldg(reinterpret_cast<const float4*>(row + o));
-                const float4 s = __ldg(reinterpret_cast<const float4*>(row + h + o));
-                cs[4 * e] = c.x, cs[4 * e + 1] = c.y, cs[4 * e + 2] = c.z, cs[4 * e + 3] = c.w;
-                sn[4 * e] = s.x, sn[4 * e + 1] = s.y, sn[4 * e + 2] = s.z, sn[4 * e + 3] = s.w;
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int o = p.interleaved ? (e ? pb : pa) * 4 : pa * 8 + 4 * e;
+            const float4 c = __ldg(reinterpret_cast<const float4*>(row + o));
+            const float4 s = __ldg(reinterpret_cast<const float4*>(row + h + o));
+            cs[4 * e] = c.x, cs[4 * e + 1] = c.y, cs[4 * e + 2] = c.z, cs[4 * e + 3] = c.w;
+            sn[4 * e] = s.x, sn[4 * e + 1] = s.y, sn[4 * e + 2] = s.z, sn[4 * e + 3] = s.w;
         }
     }
+    for (int row0 = begin; row0 < end; row0 += kTeams * R) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const int row = row0 + k * kTeams;
-        const bool have = row < p.rows;
-        const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
-        float x[8], y[8];
-        if (have) {
+        for (int k = 0; k < R; ++k) {
+            if (k > 0 && row0 + k * kTeams >= end) break;
+            const int row = row0 + k * kTeams + team;
+            float x[8], y[8];
             a[k].get(x);
             b[k].get(y);
-        } else {
+            load(k, row + kTeams * R);  // the next step's
+            if (turns) {
+                if (p.interleaved) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-        }
-        if (have && !is_v && j < rp) {
-            if (p.interleaved) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    rotate_pair(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
-                    rotate_pair(y[2 * e], y[2 * e + 1], cs[4 + e], sn[4 + e]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], cs[e], sn[e]);
-            }
-        }
-        const int pa = is_v ? j : ca, pb = is_v ? j + kTeam : cb;
-        if (have && is_q) {
-            T* dst = static_cast<T*>(p.q_out) + (static_cast<size_t>(i) * p.Hq + row) * D;
-            Piece<T>::put(dst + 8 * pa, x);
-            Piece<T>::put(dst + 8 * pb, y);
-        }
-        const int h = row - p.Hq - (is_v ? p.Hkv : 0);
-        if constexpr (!kQ4) {
-            if (have && !is_q && page >= 0) {
-                T* dst = static_cast<T*>(is_v ? p.v_pool : p.k_pool) +
-                         (((static_cast<size_t>(page) * p.Hkv + h) << p.page_shift) + in_page) * D;
-                Piece<T>::put(dst + 8 * pa, x);
-                Piece<T>::put(dst + 8 * pb, y);
-            }
-        } else {
-            if (!__any_sync(0xffffffffu, have && !is_q)) continue;
-            // scale and minimum of the row's groups (piece c belongs to group c / 8)
-            const int ga = pa >> 3, gb = pb >> 3;
-            bool fa = true, fb = true;
-            float lo_a = 65504.f, hi_a = -65504.f, lo_b = 65504.f, hi_b = -65504.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                fa = fa && isfinite(x[e]);
-                fb = fb && isfinite(y[e]);
-                x[e] = fminf(fmaxf(x[e], -65504.f), 65504.f);
-                y[e] = fminf(fmaxf(y[e], -65504.f), 65504.f);
-                lo_a = fminf(lo_a, x[e]), hi_a = fmaxf(hi_a, x[e]);
-                lo_b = fminf(lo_b, y[e]), hi_b = fmaxf(hi_b, y[e]);
-            }
-            __half2 par[L4::kGroups];
-            float base[L4::kGroups], step[L4::kGroups], inv[L4::kGroups];
-#pragma unroll
-            for (int g = 0; g < L4::kGroups; ++g) {
-                float lo = fminf(ga == g ? lo_a : 65504.f, gb == g ? lo_b : 65504.f);
-                float hi = fmaxf(ga == g ? hi_a : -65504.f, gb == g ? hi_b : -65504.f);
-                int bad = (ga == g && !fa) || (gb == g && !fb);
-#pragma unroll
-                for (int off = 1; off < kTeam; off <<= 1) {
-                    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-                    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-                    bad |= __shfl_xor_sync(0xffffffffu, bad, off);
-                }
-                __half hb = __float2half_rn(lo);
-                const __half hs = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
-                step[g] = __half2float(hs);
-                base[g] = __half2float(hb);
-                inv[g] = step[g] > 0.f ? __frcp_rn(step[g]) : 0.f;
-                if (bad) {
-                    hb = __ushort_as_half(0x7fff);
-                    inv[g] = 0.f;
-                }
-                par[g] = __halves2half2(hs, hb);
-            }
-            auto code = [&](float v, int g) {
-                const float c = rintf(__fmul_rn(__fsub_rn(v, base[g]), inv[g]));
-                return static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
-            };
-            uint32_t wa = 0, wb = 0;
-            float va[8], vb[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int g0 = L4::kGroups == 1 ? 0 : ga, g1 = L4::kGroups == 1 ? 0 : gb;
-                const uint32_t c0 = g0 ? code(x[e], L4::kGroups - 1) : code(x[e], 0);
-                const uint32_t c1 = g1 ? code(y[e], L4::kGroups - 1) : code(y[e], 0);
-                wa |= c0 << (4 * e);
-                wb |= c1 << (4 * e);
-                const __half2 q0 = g0 ? par[L4::kGroups - 1] : par[0];
-                const __half2 q1 = g1 ? par[L4::kGroups - 1] : par[0];
-                va[e] = fmaf(__low2float(q0), static_cast<float>(c0), __high2float(q0));
-                vb[e] = fmaf(__low2float(q1), static_cast<float>(c1), __high2float(q1));
-            }
-            uint32_t ta = wa, tb = wb;
-            if (__any_sync(0xffffffffu, have && is_v)) {
-                if constexpr (D == 128) {
-                    ta = transpose_nibbles(wa, j);
-                    tb = transpose_nibbles(wb, j);
-                } else {  // pieces j and j + 4 of the 8: the first exchange stays in the thread
-                    const uint32_t u = (wa & 0x0000ffffu) | (wb << 16);
-                    const uint32_t v = (wa >> 16) | (wb & 0xffff0000u);
-                    uint32_t o = __shfl_xor_sync(0xffffffffu, u, 2);
-                    uint32_t u1 = (j & 2) ? ((u & 0xff00ff00u) | ((o >> 8) & 0x00ff00ffu))
-                                          : ((u & 0x00ff00ffu) | ((o & 0x00ff00ffu) << 8));
-                    o = __shfl_xor_sync(0xffffffffu, v, 2);
-                    uint32_t v1 = (j & 2) ? ((v & 0xff00ff00u) | ((o >> 8) & 0x00ff00ffu))
-                                          : ((v & 0x00ff00ffu) | ((o & 0x00ff00ffu) << 8));
-                    o = __shfl_xor_sync(0xffffffffu, u1, 1);
-                    ta = (j & 1) ? ((u1 & 0xf0f0f0f0u) | ((o >> 4) & 0x0f0f0f0fu))
-                                 : ((u1 & 0x0f0f0f0fu) | ((o & 0x0f0f0f0fu) << 4));
-                    o = __shfl_xor_sync(0xffffffffu, v1, 1);
-                    tb = (j & 1) ? ((v1 & 0xf0f0f0f0u) | ((o >> 4) & 0x0f0f0f0fu))
-                                 : ((v1 & 0x0f0f0f0fu) | ((o & 0x0f0f0f0fu) << 4));
-                }
-            }
-            if (!have || is_q) continue;
-            void* vals = is_v ? p.v_out : p.k_out;
-            if (vals) {
-                T* dst = static_cast<T*>(vals) + (static_cast<size_t>(i) * p.Hkv + h) * D;
-                Piece<T>::put(dst + 8 * pa, va);
-                Piece<T>::put(dst + 8 * pb, vb);
-            }
-            if (page < 0) continue;
-            uint8_t* blk = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool) +
-                           (((static_cast<size_t>(page) * p.Hkv + h) << (p.page_shift - 4)) +
-                            (in_page >> 4)) * L4::kBlockBytes;
-            const int r = in_page & 15;
-            uint32_t* words = reinterpret_cast<uint32_t*>(blk);
-            if (is_v) {
-                if constexpr (D == 128) {
-                    *reinterpret_cast<uint2*>(words + L4::v_word(r, j, 0)) = make_uint2(ta, tb);
+                    for (int e = 0; e < 4; ++e) {
+                        rotate_pair(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
+                        rotate_pair(y[2 * e], y[2 * e + 1], cs[4 + e], sn[4 + e]);
+                    }
                 } else {
-                    words[L4::v_word(r, j, 0)] = ta;
-                    words[L4::v_word(r, j + 4, 0)] = tb;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], cs[e], sn[e]);
                 }
-            } else {
-                words[L4::k_word(r, pa)] = __funnelshift_l(wa, wa, 3);
-                words[L4::k_word(r, pb)] = __funnelshift_l(wb, wb, 3);
             }
-            if (j < L4::kGroups)
-                *reinterpret_cast<__half2*>(blk + L4::param(r, j)) = j ? par[L4::kGroups - 1] : par[0];
+            if constexpr (kQ4 && kKind != 0) {
+                const bool have = row < end;
+                put_q4<T, D, kKind == 2>(x, y, pa, pb, j, blk + row * dst_row, in_page & 15,
+                                         have && blk, have && vals ? vals + row * D : nullptr);
+            } else if (row < end && dst) {
+                Piece<T>::put(dst + row * dst_row + 8 * pa, x);
+                Piece<T>::put(dst + row * dst_row + 8 * pb, y);
+            }
         }
     }
 }
 
-template <typename T, int D, bool kQ4, int R>
-int launch_rows(const RopeAppendParams& p, cudaStream_t stream) {
-    constexpr int per = 32 / (D / 16) * R;
-    const long long items = static_cast<long long>(p.T) * ((p.rows + per - 1) / per);
-    const long long blocks = (items + 7) / 8;
-    if (blocks > 0x7fffffffLL) return KVD_ERR_UNSUPPORTED;
-    if (launch_kernel(rope_append_kernel<T, D, kQ4, R>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(256), 0, stream, p) != cudaSuccess)
+// A warp's token, kind and rows. The kinds have code of their own (the queries' registers are not the
+// codes'), but one launch. kBlocks: CTAs that an SM is to hold at least.
+template <typename T, int D, bool kQ4, int R, int kBlocks>
+__global__ void __launch_bounds__(256, kBlocks) rope_append_kernel(const RopeAppendParams p) {
+    griddep_wait();
+    const uint32_t item = blockIdx.x * 8 + threadIdx.x / 32;
+    const uint32_t per = p.q_items + 2 * p.kv_items;
+    const int i = static_cast<int>(item / per);
+    if (i >= p.T) return;
+    int part = static_cast<int>(item % per);
+    const int lane = threadIdx.x % 32;
+    if (part < p.q_items) {
+        append_rows<T, D, kQ4, R, 0>(p, i, part * p.q_rows, min(p.Hq, (part + 1) * p.q_rows), lane);
+        return;
+    }
+    part -= p.q_items;
+    const bool values = part >= p.kv_items;
+    if (values) part -= p.kv_items;
+    const int begin = part * p.kv_rows, end = min(p.Hkv, begin + p.kv_rows);
+    constexpr int kR = kQ4 ? 1 : R;  // (the codes take the registers)
+    if (values)
+        append_rows<T, D, kQ4, kR, 2>(p, i, begin, end, lane);
+    else
+        append_rows<T, D, kQ4, kR, 1>(p, i, begin, end, lane);
+}
+
+// `steps`: steps of a warp (its rows are that many times a step's).
+template <typename T, int D, bool kQ4, int R, int kBlocks>
+int launch_rows(RopeAppendParams p, int steps, cudaStream_t stream) {
+    constexpr int step = 32 / (D / 16) * R;
+    p.q_rows = p.kv_rows = step * steps;
+    p.q_items = (p.Hq + p.q_rows - 1) / p.q_rows;
+    p.kv_items = (p.Hkv + p.kv_rows - 1) / p.kv_rows;
+    const long long items = static_cast<long long>(p.T) * (p.q_items + 2 * p.kv_items);
+    if (items >= (1LL << 31) - 8) return KVD_ERR_UNSUPPORTED;
+    const unsigned blocks = static_cast<unsigned>((items + 7) / 8);
+    if (launch_kernel(rope_append_kernel<T, D, kQ4, R, kBlocks>, dim3(blocks), dim3(256), 0,
+                      stream, p) != cudaSuccess)
         return KVD_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
 }
 
-template <typename T, int D>
-int launch_type(const RopeAppendParams& p, bool q4, cudaStream_t stream) {
-    return q4 ? launch_rows<T, D, true, 1>(p, stream) : launch_rows<T, D, false, 1>(p, stream);
+template <typename T, int D, bool kQ4>
+int launch_type(const RopeAppendParams& p, cudaStream_t stream) {
+    constexpr int teams = 32 / (D / 16);
+    const long long warps = static_cast<long long>(p.T) *
+                            ((p.Hq + teams - 1) / teams + 2 * ((p.Hkv + teams - 1) / teams));
+    // Few rows: one step a warp, as many warps as there are, for the shortest chain of reads.
+    // Many: two steps of a warp share the token's look-up, with more warps on an SM. Measured (us,
+    // 40 rows of 128 bf16 a token and 8 of values; one step against two): 192 tokens 2.59 / 2.78,
+    // 384 3.72 / 3.36, 3000 19.9 / 14.1; into 4 bits 192 3.07 / 3.87, 384 4.67 / 4.72, 3000 28.9 /
+    // 16.4; float32 192 3.18 / 3.15, 3000 33.2 / 25.6. 20 warps an SM are about 250 such tokens.
+    if (warps <= 20LL * num_sms()) return launch_rows<T, D, kQ4, 1, 1>(p, 1, stream);
+    if constexpr (sizeof(T) == 2) return launch_rows<T, D, kQ4, 2, 4>(p, 2, stream);
+    return launch_rows<T, D, kQ4, 1, 3>(p, 2, stream);  // (a float32 row is two bf16 ones)
 }
 
 }  // namespace
 
 int rope_append_launch(const RopeAppendParams& p, bool q4, int D, int dtype,
                        cudaStream_t stream) {
-    if (dtype == KVD_BF16)
-        return D == 128 ? launch_type<__nv_bfloat16, 128>(p, q4, stream)
-                        : launch_type<__nv_bfloat16, 64>(p, q4, stream);
-    return D == 128 ? launch_type<float, 128>(p, q4, stream)
-                    : launch_type<float, 64>(p, q4, stream);
+    if (dtype == KVD_BF16) {
+        if (D == 128)
+            return q4 ? launch_type<__nv_bfloat16, 128, true>(p, stream)
+                      : launch_type<__nv_bfloat16, 128, false>(p, stream);
+        return q4 ? launch_type<__nv_bfloat16, 64, true>(p, stream)
+                  : launch_type<__nv_bfloat16, 64, false>(p, stream);
+    }
+    if (D == 128)
+        return q4 ? launch_type<float, 128, true>(p, stream)
+                  : launch_type<float, 128, false>(p, stream);
+    return q4 ? launch_type<float, 64, true>(p, stream) : launch_type<float, 64, false>(p, stream);
 }
 
 }  // namespace kvd
