@@ -3,7 +3,8 @@ on one GB300 GPU.
 
 A thin Python binding over the C ABI of ``libkvdecode.so`` (``include/kvdecode.h``): each
 function has the name of its C entry point, takes torch CUDA tensors, and only marshals
-pointers, sizes and the current stream. Every step of the computation runs in the
+pointers, sizes and the current stream (with ctypes; the calls that take a few microseconds
+on the GPU through the compiled ``_binding`` module). Every step of the computation runs in the
 library's CUDA kernels; PyTorch provides device memory and streams.
 
 Operations:
@@ -35,6 +36,9 @@ from . import _lib
 from ._lib import KvdError, OP, OPTION
 
 lib = _lib.load()
+from . import _binding  # noqa: E402  (after the library that it calls)
+
+_binding.set_error(KvdError)
 
 __all__ = [
     "attn_decode_gqa_paged", "attn_decode_swa_sink", "attn_decode_mla", "dsa_indexer_topk",
@@ -297,137 +301,19 @@ def q4_pool(num_pages, Hkv, page_size, D, device=None):
                        device="cuda" if device is None else device)
 
 
-def _raw_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-# the current stream's handle without building a Stream object (microseconds), where PyTorch has it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-
-
-def _on(dev, stream, fn, args):
-    """fn(*args, stream handle) on the tensors' device: the given stream, which must be that
-    device's, or its current one."""
-    if stream is None:
-        handle = _raw_stream(dev)
-    elif stream.device.index == dev:
-        handle = stream.cuda_stream
-    else:
+def _own_stream(stream, t, name):
+    """Handle of the stream that a call is given, which must be of the tensors' device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if stream.device != t.device:
         raise ValueError("stream and tensors must be on one device")
-    if dev == torch.cuda.current_device():
-        return fn(*args, handle)
-    with torch.cuda.device(dev):
-        return fn(*args, handle)
+    return stream.cuda_stream
 
 
-def _empty(shape, dtype, like, stream):
+def _empty_on(stream, shape, like, dtype=None):
     """Uninitialised memory of the stream that the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _same(t, name, dev, dtype, shape):
-    """A dense CUDA tensor of this device, type and shape; its address."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the device of the other tensors")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _tokens(t, name, dev, dtype, shape):
-    """[T, H, D] with dense heads; its address and the elements between tokens."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
-            s0, s1, s2 = t.stride()
-            T, H, D = shape
-            if s2 == 1 and (s1 == D or H == 1):
-                return t.data_ptr(), (s0 if T > 1 else H * D)
-            raise ValueError(f"{name} must have dense heads (strides {D}, 1 in a token)")
-    except AttributeError:
-        pass
-    _same(t, name, dev, dtype, shape)  # says what is wrong
-
-
-def _cuda3(t, name, what):
-    """The leading tensor of a call: a float32 or bfloat16 CUDA tensor of three dims."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be {what}")
-    if t.dtype not in _DT:
-        raise TypeError(f"{name} must be float32 or bfloat16")
-
-
-def _rope_args(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens,
-               q_out, err, stream, q4):
-    """The arguments that both appends share, checked: (device, rotated queries, leading C
-    arguments, sizes up to rot_dim, pool sizes and dtype, err)."""
-    _cuda3(k_new, "k_new", "[T, Hkv, D]")
-    kv = k_new.shape
-    T, Hkv, D = kv
-    dev, dt = k_new.get_device(), k_new.dtype
-    try:
-        pool = k_pool.shape
-        B, max_pages = block_table.shape
-        max_pos, rot = cos_sin.shape
-        if q4:
-            num_pages, h, P = pool
-            per = D // 2 + D // 16
-            ok = D in (64, 128) and P % per == 0
-            P //= per
-        else:
-            num_pages, h, P, d = pool
-            ok = d == D
-        if not ok or h != Hkv or P < 1:
-            raise ValueError
-    except (AttributeError, ValueError):
-        _need(k_pool, "k_pool", torch.uint8 if q4 else dt, 3 if q4 else 4)
-        _need(block_table, "block_table", torch.int32, 2)
-        _need(cos_sin, "cos_sin", torch.float32, 2)
-        raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]" if q4 else
-                         "k_pool must be [num_pages, Hkv, page_size, D]") from None
-    pool_dt = torch.uint8 if q4 else dt
-    kp, ks = _tokens(k_new, "k_new", dev, dt, kv)
-    vp, vs = _tokens(v_new, "v_new", dev, dt, kv)
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must be [T, Hq, D]")
-        Hq = q.shape[1]
-        shape = (T, Hq, D)
-        qp, qs = _tokens(q, "q", dev, dt, shape)
-        if q_out is None:
-            q_out = _empty(shape, dt, k_new, stream)
-        qo = _same(q_out, "q_out", dev, dt, shape)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    else:
-        qp, qs, Hq, qo = None, 0, 0, None
-    if cu_seqlens is not None:
-        cu = _same(cu_seqlens, "cu_seqlens", dev, torch.int32, (B + 1,))
-    elif T != B:
-        raise ValueError("without cu_seqlens there is one token of each sequence")
-    else:
-        cu = None
-    head = (qp, kp, vp, _same(cos_sin, "cos_sin", dev, torch.float32, (max_pos, rot)), cu,
-            _same(block_table, "block_table", dev, torch.int32, (B, max_pages)),
-            _same(seq_lens, "seq_lens", dev, torch.int32, (B,)), qo,
-            _same(k_pool, "k_pool", dev, pool_dt, pool), _same(v_pool, "v_pool", dev, pool_dt, pool))
-    err_p = None if err is None else _same(err, "err", dev, torch.int32, (1,))
-    return (dev, q_out, head, (B, T, Hq, Hkv, D, qs, ks, vs, rot),
-            (max_pos, P, max_pages, num_pages, _DT[dt]), err_p)
+        return torch.empty(shape, dtype=like.dtype if dtype is None else dtype, device=like.device)
 
 
 def rope_append(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens=None,
@@ -444,13 +330,14 @@ def rope_append(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens,
     2i + 1. q_out may be q itself if q is contiguous. A bad length, position or page id is
     recorded in err (int32 [1]) and not written.
     """
-    dev, q_out, head, sizes, pool, err_p = _rope_args(
-        q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens, q_out, err,
-        stream, False)
-    st = _on(dev, stream, lib.kvd_rope_append,
-             (*head, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink), err_p))
-    _check(st, "kvd_rope_append")
-    return q_out
+    if stream is not None:
+        handle = _own_stream(stream, k_new, "k_new")
+        if q is not None and q_out is None:
+            q_out = _empty_on(stream, q.shape, q)
+        stream = handle
+    return _binding.rope_append(False, q, k_new, v_new, cos_sin, k_pool, v_pool, block_table,
+                                seq_lens, cu_seqlens, window, n_sink, interleaved, q_out, None,
+                                None, err, stream)
 
 
 def rope_append_q4(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens,
@@ -458,16 +345,14 @@ def rope_append_q4(q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_le
                    v_out=None, err=None, stream=None):
     """rope_append into a cache held in 4 bits: k_pool and v_pool are uint8 pools of q4_pool().
     k_out, v_out [T, Hkv, D] (optional) receive the values that the cache stands for."""
-    dev, q_out, head, sizes, pool, err_p = _rope_args(
-        q, k_new, v_new, cos_sin, k_pool, v_pool, block_table, seq_lens, cu_seqlens, q_out, err,
-        stream, True)
-    ko = None if k_out is None else _same(k_out, "k_out", dev, k_new.dtype, k_new.shape)
-    vo = None if v_out is None else _same(v_out, "v_out", dev, k_new.dtype, k_new.shape)
-    st = _on(dev, stream, lib.kvd_rope_append_q4,
-             (*head, ko, vo, *sizes, 1 if interleaved else 0, *pool, int(window), int(n_sink),
-              err_p))
-    _check(st, "kvd_rope_append_q4")
-    return q_out
+    if stream is not None:
+        handle = _own_stream(stream, k_new, "k_new")
+        if q is not None and q_out is None:
+            q_out = _empty_on(stream, q.shape, q)
+        stream = handle
+    return _binding.rope_append(True, q, k_new, v_new, cos_sin, k_pool, v_pool, block_table,
+                                seq_lens, cu_seqlens, window, n_sink, interleaved, q_out, k_out,
+                                v_out, err, stream)
 
 
 def attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window=0, n_sink_tokens=0,
@@ -482,46 +367,24 @@ def attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window=0, n_sin
     memory from PyTorch's allocator, so calls on several streams and captured graphs never share
     it. A bad length or page id is recorded in err (int32 [1]) and clamped.
     """
-    _cuda3(q, "q", "[B, Hq, D]")
-    shape = q.shape
-    B, Hq, D = shape
-    dev, dt = q.get_device(), q.dtype
-    try:
-        pool = k_pool.shape
-        num_pages, Hkv, page = pool
-        max_pages = block_table.shape[1]
-        per = D // 2 + D // 16
-        if D not in (64, 128) or page < per or page % per:
-            raise ValueError
-    except (AttributeError, ValueError, IndexError):
-        _need(k_pool, "k_pool", torch.uint8, 3)
-        _need(block_table, "block_table", torch.int32, 2)
-        raise ValueError("k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]") from None
-    P = page // per
-    kp = _same(k_pool, "k_pool", dev, torch.uint8, pool)
-    vp = _same(v_pool, "v_pool", dev, torch.uint8, pool)
-    bt = _same(block_table, "block_table", dev, torch.int32, (B, max_pages))
-    sl = _same(seq_lens, "seq_lens", dev, torch.int32, (B,))
-    sink = None if sink_logit is None else _same(sink_logit, "sink_logit", dev, torch.float32, (Hq,))
-    lse = None if lse_out is None else _same(lse_out, "lse_out", dev, torch.float32, (B, Hq))
-    err_p = None if err is None else _same(err, "err", dev, torch.int32, (1,))
-    out = _empty(shape, dt, q, stream) if out is None else out
-    if workspace is None or isinstance(workspace, Workspace):
-        nbytes = kvd_workspace_size("gqa_q4", B, Hq, Hkv, D, max_pages * P)
-        if workspace is None:
-            workspace = _empty((max(nbytes, 1),), torch.uint8, q, stream)
-        else:
-            workspace = workspace.get(nbytes, "gqa_q4")
-    elif not isinstance(workspace, torch.Tensor):
-        raise TypeError("workspace must be a uint8 tensor or a Workspace")
-    ws = _same(workspace, "workspace", dev, torch.uint8, workspace.shape)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    st = _on(dev, stream, lib.attn_decode_gqa_q4, (
-        _same(q, "q", dev, dt, shape), kp, vp, bt, sl, _same(out, "out", dev, dt, shape), lse, B,
-        Hq, Hkv, D, P, max_pages, num_pages, scale, _DT[dt], int(window), int(n_sink_tokens),
-        1 if ring else 0, sink, ws, workspace.numel(), err_p))
-    _check(st, "attn_decode_gqa_q4")
-    return out
+    if isinstance(workspace, Workspace) or (workspace is None and stream is not None):
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k_pool, torch.Tensor) \
+                or k_pool.dim() != 3 or block_table.dim() != 2:
+            raise ValueError("q, k_pool and block_table must have 3, 3 and 2 dims")
+        B, Hq, D = q.shape
+        P = k_pool.shape[2] // max(1, D // 2 + D // 16)
+        nbytes = max(1, kvd_workspace_size("gqa_q4", B, Hq, k_pool.shape[1], D,
+                                           block_table.shape[1] * P))
+        workspace = (_empty_on(stream, nbytes, q, torch.uint8) if workspace is None
+                     else workspace.get(nbytes, "gqa_q4"))
+    if stream is not None:
+        handle = _own_stream(stream, q, "q")
+        if out is None:
+            out = _empty_on(stream, q.shape, q)
+        stream = handle
+    return _binding.attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window,
+                                       n_sink_tokens, ring, sink_logit, scale, out, lse_out,
+                                       workspace, err, stream)
 
 
 def _err(err, device):

@@ -1,7 +1,8 @@
-"""Build libkvdecode.so (all CUDA sources, sm_103a) in-tree.
+"""Build libkvdecode.so (all CUDA sources, sm_103a) and the _binding module in-tree.
 
-Each translation unit is compiled in parallel with nvcc, then linked into one shared
-library next to this file. Intermediate objects go to ``_build/`` at the repo root.
+Each translation unit is compiled in parallel (nvcc; g++ for the CPython module, which is
+written against PyTorch's C++ headers), then linked into one shared library and one module
+next to this file. Intermediate objects go to ``_build/`` at the repo root.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvdecode.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,37 +38,58 @@ def flags(ptxas_verbose: bool = False):
                    "-v" if ptxas_verbose else "-O3"]
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)  # without importing it
+
+
 def _compile(src: str, obj: str, verbose: bool) -> tuple[str, str]:
-    cmd = [nvcc(), "-c", src, "-o", obj] + flags(verbose)
+    if src.endswith(".cpp"):
+        inc = os.path.join(_torch_dir(), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+        cmd = ["g++", "-c", src, "-o", obj, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+               "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
+               os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda]
+    else:
+        cmd = [nvcc(), "-c", src, "-o", obj] + flags(verbose)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
     return src, r.stderr
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA source and link libkvdecode.so (skipped when it is up to date);
     `verbose` prints ptxas register / shared-memory / spill figures per kernel."""
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    srcs = [BINDING_SRC] + sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(LIB):
-        lib_t = os.path.getmtime(LIB)
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
+        lib_t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
         if all(os.path.getmtime(d) <= lib_t for d in deps):
             return LIB
     os.makedirs(BUILD, exist_ok=True)
-    objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
+    objs = [os.path.join(BUILD, os.path.splitext(os.path.basename(s))[0] + ".o")
+            for s in srcs]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         for src, log in ex.map(lambda so: _compile(so[0], so[1], verbose), zip(srcs, objs)):
             if verbose and log:
                 print(f"== {os.path.basename(src)}\n{log}", file=sys.stderr)
     tmp = LIB + f".tmp{os.getpid()}"
     # -z defs: an unresolved symbol fails the build here, not the first import on the GPU box
-    cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xlinker", "-z", "-Xlinker", "defs"]
+    cmd = [nvcc(), "-shared", "-o", tmp] + objs[1:] + ARCH + ["-Xlinker", "-z", "-Xlinker", "defs"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, objs[0], "-L", PKG, "-l:libkvdecode.so",
+           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+           "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
