@@ -676,6 +676,7 @@ int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
     p.NHG = plan.NHG;
     p.HU = Hkv * plan.NHG;
     p.n_warps = plan.n_warps;
+    p.join = plan.join;
     p.page_shift = __builtin_ctz(page_size);
     p.max_pages = max_pages;
     p.num_pages = num_pages;

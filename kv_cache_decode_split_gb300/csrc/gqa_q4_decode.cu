@@ -85,22 +85,38 @@ __device__ __forceinline__ int scan_tiles(const Q4Params& p, int b0, int lane, i
     return inc;
 }
 
-// The list of all units' tiles in order (fewer than 2^31, which the host checks), shared evenly by
-// n warps (at most one for each tile): the first `extra` of them take one tile more.
+// The list of all units' tiles in order (fewer than 2^31, which the host checks), shared evenly by n
+// warps (at most one for each tile) in order. Some warps have one tile more than the others: the
+// first ones, or, where CTAs join their warps' partials (`join`; warps c kCta .. are CTA c's), as
+// many in each CTA, but for one more in the first ones.
+template <int kCta>
 struct Shares {
-    uint32_t n, base, extra;
+    uint32_t n, base, extra, each, more;
+    bool join;
     __device__ Shares(const Q4Params& p, uint32_t tiles_of_units) {
         const uint32_t total = tiles_of_units * p.HU;
         n = min(static_cast<uint32_t>(p.n_warps), total);
         base = n > 0 ? total / n : 0;
         extra = total - base * n;
+        join = p.join != 0 && n == static_cast<uint32_t>(p.n_warps);
+        each = extra / (n / kCta + !join);
+        more = extra - each * (n / kCta);
     }
-    __device__ uint32_t begin(uint32_t i) const { return i * base + min(i, extra); }
-    __device__ int count(uint32_t i) const { return static_cast<int>(base + (i < extra ? 1 : 0)); }
+    __device__ uint32_t begin(uint32_t i) const {
+        if (!join) return i * base + min(i, extra);
+        const uint32_t c = i / kCta;
+        return i * base + c * each + min(c, more) + min(i - c * kCta, each + (c < more));
+    }
     __device__ int owner(uint32_t tile) const {
-        const uint32_t longer = extra * (base + 1);
-        return static_cast<int>(tile < longer ? tile / (base + 1)
-                                              : extra + (tile - longer) / base);
+        if (!join) return find(tile, base, extra);
+        const uint32_t all = kCta * base + each;  // tiles of a CTA, but for the first ones' one more
+        const uint32_t c = find(tile, all, more);
+        return static_cast<int>(c * kCta + find(tile - c * all - min(c, more), base, each + (c < more)));
+    }
+    // tile -> share, the first `longer` shares having size + 1 tiles and the others size
+    __device__ static uint32_t find(uint32_t tile, uint32_t size, uint32_t longer) {
+        const uint32_t t = longer * (size + 1);
+        return tile < t ? tile / (size + 1) : longer + (tile - t) / size;
     }
 };
 
@@ -173,18 +189,23 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t (&part)[kS
 // the first visible token of the tile, from bit 16 the one behind the last.
 using TileInfo = int2;
 
-// One CTA on each SM: its warps share the SM's registers (a warp's products, sums and operands
-// need about 150 of them; 120 with float32 queries' and 16-head blocks' 230).
-constexpr int warps_of(int nt, bool f32) { return nt == 1 && !f32 ? 12 : 8; }
+// One CTA on each SM; as many warps as its registers hold (a thread's products, sums and operands
+// need 115 to 250) and, with 128 channels, its shared memory (two tiles of 18 KB a warp).
+constexpr int warps_of(int d, int nt, bool f32) {
+    return d == 128 ? (nt == 1 && !f32 ? 12 : 8) : f32 ? (nt == 1 ? 12 : 8) : (nt == 1 ? 16 : 11);
+}
 
 template <int D, int NT, bool kF32>
 struct Q4Cfg {
-    static constexpr int kWarps = warps_of(NT, kF32);
+    static constexpr int kWarps = warps_of(D, NT, kF32);
     static constexpr int kStages = 2;
     static constexpr int kTileBytes = 8 * Q4<D>::kBlockBytes;  // K and V, four blocks each
     static constexpr int kRing = kStages * kTileBytes;
     static constexpr int kPerWarp = kRing + kStages * static_cast<int>(sizeof(TileInfo) + 8);
-    static constexpr int kSmem = kWarps * kPerWarp + 16;
+    static constexpr int kSmem = kWarps * kPerWarp + 16 + kWarps * 8;
+    // a warp's last piece, for the CTA's own joining: O, references, sums, over its ring
+    static constexpr int kPieceFloats = NT * 8 * (D + 2);
+    static_assert(kPieceFloats * 4 <= kRing, "a piece fits the ring");
 };
 
 // kPair (128 channels, at most 4 heads): the matrix instructions' 8 columns are the heads once for
@@ -214,6 +235,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(
                          smem + kWarps * (Cfg::kRing + S * sizeof(TileInfo))) + warp * S;
     uint32_t* masks = reinterpret_cast<uint32_t*>(smem + kWarps * Cfg::kPerWarp);
+    // of each warp: its last piece's unit and that unit's heads
+    int2* last_piece = reinterpret_cast<int2*>(masks + 4);
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
@@ -229,10 +252,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     griddep_launch_dependents();
 
     // ---- this warp's share of the tile list
-    // (with fewer tiles than warps the first warps of all CTAs take one each)
-    const uint32_t me = warp * gridDim.x + blockIdx.x;
-    uint32_t begin;
+    // Where a CTA joins, its warps have neighbouring shares; elsewhere neighbouring shares are in
+    // different CTAs (with fewer tiles than warps, the first warps of all CTAs take one each).
+    uint32_t me, begin;
     int n_mine;  // tiles, at least 1
+    bool join;   // the CTA joins its warps' last pieces
     int scan_n, scan_inc = scan_tiles(p, 0, lane, scan_n);  // of the first 32 sequences
     {
         uint32_t tiles = __shfl_sync(0xffffffffu, scan_inc, 31);
@@ -240,10 +264,12 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
             int n;
             tiles += __shfl_sync(0xffffffffu, scan_tiles(p, b0, lane, n), 31);
         }
-        const Shares sh(p, tiles);
+        const Shares<kWarps> sh(p, tiles);
+        join = sh.join;
+        me = join ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
         if (me >= sh.n) return;
         begin = sh.begin(me);
-        n_mine = sh.count(me);
+        n_mine = static_cast<int>(sh.begin(me + 1) - begin);
     }
     // Tiles are looked up 32 at a time, lane k the k-th of the batch: its pieces' first blocks in
     // the pools (one piece, or two or four when pages hold 32 or 16 tokens) and its TileInfo.
@@ -366,6 +392,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         const int kvh = u / p.NHG, hg = u % p.NHG;
         return make_int4(b, kvh * p.G + hg * NT * 8, min(NT * 8, p.G - hg * NT * 8), 0);
     };
+    int2 left = make_int2(-1, 0);  // unit and heads of a last piece that this CTA is to join
     int s = 0, phase = 0;
     for (int i = 0; i < n_mine; ++i) {
         __syncwarp();
@@ -440,8 +467,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
             if (lane == 0)
                 for (int k = i + 1; k < min(n_mine, i + S); ++k)
                     mbar_wait(&full[k % S], (k / S) & 1, p.err);
-            __syncwarp();
-            return;
+            left.x = -1;
+            break;
         }
         const int v0 = (ti.y >> 8) & 127, v1 = (ti.y >> 16) & 127;  // (special tiles only)
         // half a tile: tokens 32 sub .. 32 sub + 31. This lane's score rows are tokens 16 bk +
@@ -714,6 +741,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
             const int4 un = unit_of(ti.x);
             const bool whole = from_start && (ti.y & 8);
             const size_t slot = static_cast<size_t>(me) + ti.x;
+            // A cut piece goes to the workspace, the warp's last one to shared memory, where no
+            // copy is in flight any more.
+            const bool at_end = join && i == n_mine - 1;
+            if (at_end && !whole) left = make_int2(ti.x, un.z);
+            float* held = reinterpret_cast<float*>(ring);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float mul[2], add[NG][2];
@@ -745,8 +777,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                             p.lse_out[static_cast<size_t>(un.x) * p.Hq + hq] =
                                 (M + log2f(den)) * kLn2;
                     } else if (g == 0 && own == 0) {
-                        __stcg(p.part_m + slot * (NT * 8) + h, m[nt][c]);
-                        __stcg(p.part_l + slot * (NT * 8) + h, lv);
+                        if (at_end) {
+                            held[NT * D * 8 + h] = m[nt][c];
+                            held[NT * 8 * (D + 1) + h] = lv;
+                        } else {
+                            __stcg(p.part_m + slot * (NT * 8) + h, m[nt][c]);
+                            __stcg(p.part_l + slot * (NT * 8) + h, lv);
+                        }
                     }
                 }
                 // (kPair: this lane has its own group's half of the channels, of heads 0-3)
@@ -762,12 +799,17 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                         r[mt][e] = v + add[kPair ? 0 : mt / 4][e & 1];
                     }
                 if (!whole) {  // 16 bytes of 8 x 2 channels and heads each
-                    float* dst = p.part_o + (slot * NT + nt) * (D * 8) +
-                                 (kPair ? own * (kHave * 128) + (4 * g + (t & 1)) * 4 : lane * 4);
+                    const int to = nt * (D * 8) +
+                                   (kPair ? own * (kHave * 128) + (4 * g + (t & 1)) * 4 : lane * 4);
+                    float* dst = p.part_o + slot * (NT * D * 8) + to;
 #pragma unroll
-                    for (int mt = 0; mt < kHave; ++mt)
-                        __stcg(reinterpret_cast<float4*>(dst + mt * 128),
-                               make_float4(r[mt][0], r[mt][1], r[mt][2], r[mt][3]));
+                    for (int mt = 0; mt < kHave; ++mt) {
+                        const float4 v = make_float4(r[mt][0], r[mt][1], r[mt][2], r[mt][3]);
+                        if (at_end)
+                            *reinterpret_cast<float4*>(held + to + mt * 128) = v;
+                        else
+                            __stcg(reinterpret_cast<float4*>(dst + mt * 128), v);
+                    }
                     continue;
                 }
 #pragma unroll
@@ -794,6 +836,54 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         queue >>= 1;
         if (++s == S) s = 0, phase ^= 1;
     }
+    // ---- join the CTA's last pieces, warps of one unit at a time, into one partial each: a twelfth
+    // of the workspace traffic, and one round trip of the joining launch, for long sequences
+    if (!join) return;
+    if (lane == 0) last_piece[warp] = left;
+    __syncthreads();
+    const int2 piece = lane < kWarps ? last_piece[lane] : make_int2(-1, 0);
+    const int before = __shfl_up_sync(0xffffffffu, piece.x, 1);
+    // bits of the warps that begin a run of one unit, bit kWarps behind the last
+    uint32_t starts = __ballot_sync(
+        0xffffffffu, lane == kWarps || (lane < kWarps && (lane == 0 || before != piece.x)));
+    for (int a = 0; a < kWarps;) {
+        starts &= starts - 1;
+        const int b = __ffs(starts) - 1;
+        const int unit = __shfl_sync(0xffffffffu, piece.x, a);
+        const int heads = __shfl_sync(0xffffffffu, piece.y, a);
+        const size_t slot = static_cast<size_t>(blockIdx.x * kWarps + a) + unit;
+        for (int quad = threadIdx.x; quad < NT * D * 2 && unit >= 0; quad += kWarps * 32) {
+            const int h = quad / (D * 2) * 8 + 2 * (quad & 3);  // heads h and h + 1
+            if (h >= heads) continue;
+            const float* held = reinterpret_cast<const float*>(smem);
+            float M0 = kNone, M1 = kNone;
+#pragma unroll 4
+            for (int w = a; w < b; ++w) {
+                const float2 x = *reinterpret_cast<const float2*>(
+                    held + w * (Cfg::kRing / 4) + NT * D * 8 + h);
+                M0 = fmaxf(M0, x.x), M1 = fmaxf(M1, x.y);
+            }
+            float L0 = 0.f, L1 = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = a; w < b; ++w) {
+                const float* of = held + w * (Cfg::kRing / 4);
+                const float2 x = *reinterpret_cast<const float2*>(of + NT * D * 8 + h);
+                const float2 y = *reinterpret_cast<const float2*>(of + NT * 8 * (D + 1) + h);
+                const float4 v = *reinterpret_cast<const float4*>(of + quad * 4);
+                const float w0 = fast_exp2(x.x - M0), w1 = fast_exp2(x.y - M1);
+                L0 = fmaf(w0, y.x, L0), L1 = fmaf(w1, y.y, L1);
+                acc.x = fmaf(w0, v.x, acc.x), acc.z = fmaf(w0, v.z, acc.z);
+                acc.y = fmaf(w1, v.y, acc.y), acc.w = fmaf(w1, v.w, acc.w);
+            }
+            __stcg(reinterpret_cast<float4*>(p.part_o + slot * (NT * D * 8)) + quad, acc);
+            if (quad % (D * 2) < 4) {
+                __stcg(reinterpret_cast<float2*>(p.part_m + slot * (NT * 8) + h), make_float2(M0, M1));
+                __stcg(reinterpret_cast<float2*>(p.part_l + slot * (NT * 8) + h), make_float2(L0, L1));
+            }
+        }
+        a = b;
+    }
 }
 
 // Joins the partials of one unit's block of 8 heads: out = sum_i 2^{m_i - M} O_i / (sum_i 2^{m_i - M}
@@ -804,7 +894,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
 // (kSplit = 8), so that enough SMs read. Units that one warp had whole are written already; units
 // without tiles get zeros. What there is to join follows from the lengths alone and is worked out
 // while the main launch ends.
-template <int D, int NT, bool kF32, int kSplit>
+template <int D, int NT, bool kF32, int kSplit, bool kJoin>
 __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
     gqa_q4_combine_kernel(const Q4Params p) {
     constexpr int kQuads = kSplit == 1 ? D * 2 : 32, kAtOnce = 4, H = NT * 8;
@@ -817,7 +907,10 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
     const int k0 = threadIdx.x / kQuads;
     const int lane = threadIdx.x % 32, mt = quad / 32, g = lane >> 2, h = 2 * (lane & 3);
     if (heads <= 0) return;
-    int first = 0, n = 0;  // the warps that share the unit
+    // The unit's partials: of warps first .. last, or, where CTAs have joined their warps' last
+    // pieces, of the first warp in each CTA, and the last warp's own if it went on to another unit.
+    constexpr int kCta = warps_of(D, NT, kF32);
+    int first = 0, last = 0, n = 0, joined = 0;
     {
         uint32_t tiles = 0, before = 0;
         int own = 0;
@@ -831,11 +924,18 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
             tiles += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (own > 0) {
-            const Shares sh(p, tiles);
+            const Shares<kCta> sh(p, tiles);
             const uint32_t t0 = before * p.HU + static_cast<uint32_t>(u) * own;
+            const uint32_t t1 = t0 + own - 1;
             first = sh.owner(t0);
-            n = sh.owner(t0 + own - 1) - first + 1;
-            if (n == 1) return;
+            last = sh.owner(t1);
+            if (first == last) return;
+            n = last - first + 1;
+            if (kJoin && sh.join) {
+                const bool goes_on = t1 + 1 != sh.begin(last + 1);
+                joined = (goes_on ? last - 1 : last) / kCta - first / kCta + 1;
+                n = joined + goes_on;
+            }
         }
     }
     griddep_wait();
@@ -847,10 +947,16 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
     }
     float M[2] = {kNone, kNone}, L[2] = {0.f, 0.f};
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const size_t slot0 = static_cast<size_t>(first) + unit;
-    const float* pm = p.part_m + slot0 * H + nt * 8 + h;
-    const float* pl = p.part_l + slot0 * H + nt * 8 + h;
-    const float* po = p.part_o + (slot0 * NT + nt) * (D * 8) + quad * 4;
+    auto slot_of = [&](int i) -> size_t {
+        const int w = !kJoin || joined == 0 ? first + i
+                      : i == 0    ? first
+                      : i < joined ? (first / kCta + i) * kCta
+                                   : last;
+        return static_cast<size_t>(w) + unit;
+    };
+    const float* pm = p.part_m + nt * 8 + h;
+    const float* pl = p.part_l + nt * 8 + h;
+    const float* po = p.part_o + nt * (D * 8) + quad * 4;
     if (mine) {
         for (int i0 = k0; i0 < n; i0 += kSplit * kAtOnce) {
             float2 mi[kAtOnce], li[kAtOnce];
@@ -862,9 +968,10 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
                 li[k] = make_float2(0.f, 0.f);
                 v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (i < n) {
-                    mi[k] = __ldcg(reinterpret_cast<const float2*>(pm + static_cast<size_t>(i) * H));
-                    li[k] = __ldcg(reinterpret_cast<const float2*>(pl + static_cast<size_t>(i) * H));
-                    v[k] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(i) * (D * H)));
+                    const size_t slot = slot_of(i);
+                    mi[k] = __ldcg(reinterpret_cast<const float2*>(pm + slot * H));
+                    li[k] = __ldcg(reinterpret_cast<const float2*>(pl + slot * H));
+                    v[k] = __ldcg(reinterpret_cast<const float4*>(po + slot * (D * H)));
                 }
             }
             float t0 = M[0], t1 = M[1];
@@ -951,13 +1058,15 @@ int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
     if (launch_kernel(kern, dim3(plan.ctas), dim3(Cfg::kWarps * 32), Cfg::kSmem, stream, p) !=
         cudaSuccess)
         return KVD_ERR_CUDA;
-    // (16 partials are two round trips of a thread)
+    // few units of many partials each: more CTAs and threads for each
+    const bool few = plan.n_warps > 16 * plan.units;
+    const dim3 all(plan.units, NT), parts(plan.units, NT * (D / 16));
     const cudaError_t e =
-        plan.n_warps <= 16 * plan.units
-            ? launch_kernel(gqa_q4_combine_kernel<D, NT, kF32, 1>, dim3(plan.units, NT),
-                            dim3(D * 2), 0, stream, p)
-            : launch_kernel(gqa_q4_combine_kernel<D, NT, kF32, 8>,
-                            dim3(plan.units, NT * (D / 16)), dim3(256), 0, stream, p);
+        !plan.join
+            ? launch_kernel(gqa_q4_combine_kernel<D, NT, kF32, 1, false>, all, dim3(D * 2), 0, stream, p)
+        : few
+            ? launch_kernel(gqa_q4_combine_kernel<D, NT, kF32, 8, true>, parts, dim3(256), 0, stream, p)
+            : launch_kernel(gqa_q4_combine_kernel<D, NT, kF32, 1, true>, all, dim3(D * 2), 0, stream, p);
     if (e != cudaSuccess) return KVD_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
 }
@@ -974,9 +1083,10 @@ int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan*
     const long long tiles = units * ((max_len + kTileTok - 1) / kTileTok + 1);
     if (tiles >= (1LL << 31)) return KVD_ERR_UNSUPPORTED;
     plan->units = static_cast<int>(units);
-    const int warps = warps_of(plan->nt, dtype == KVD_F32);
+    const int warps = warps_of(D, plan->nt, dtype == KVD_F32);
     plan->ctas = static_cast<int>(std::max(1LL, std::min<long long>(num_sms(), tiles)));
     plan->n_warps = plan->ctas * warps;
+    plan->join = plan->n_warps >= 4 * units;
     const size_t slots = static_cast<size_t>(plan->n_warps) + units;
     const size_t heads = static_cast<size_t>(plan->nt) * 8;
     auto round = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };

@@ -199,13 +199,14 @@ struct Q4Params {
     int B, Hq, Hkv, G, NHG;    // NHG: head blocks of a KV head
     int HU;                    // units of a sequence: Hkv * NHG
     int n_warps;               // warps that share the tile list
+    int join;                  // CTAs join their warps' partials of one unit
     int page_shift, max_pages, num_pages, max_len;
     int window, n_sink, ring;  // as GqaParams
     float scale_log2;
 };
 struct Q4Plan {
     int nt;                    // 8-head column tiles of a head block (1 or 2)
-    int NHG, units, ctas, n_warps;
+    int NHG, units, ctas, n_warps, join;
     size_t off_m, off_l, off_o, total;
 };
 int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan* plan);
