@@ -200,6 +200,7 @@ struct Q4Params {
     int HU;                    // units of a sequence: Hkv * NHG
     int n_warps;               // warps that share the tile list
     int join;                  // CTAs join their warps' partials of one unit
+    int cluster;               // CTAs of a unit, in the form for short calls
     int page_shift, max_pages, num_pages, max_len;
     int window, n_sink, ring;  // as GqaParams
     float scale_log2;
@@ -207,9 +208,14 @@ struct Q4Params {
 struct Q4Plan {
     int nt;                    // 8-head column tiles of a head block (1 or 2)
     int NHG, units, ctas, n_warps, join;
+    int cluster;               // > 0: a cluster of (at most) this many CTAs may take each unit
+    int most;                  // tiles that a unit may have
+    float even;                // tiles of an SM if all units have as many and all SMs share them
     size_t off_m, off_l, off_o, total;
 };
-int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int dtype, Q4Plan* plan);
+// visible: tokens that a query sees at most (max_len, or less with a window)
+int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible, int dtype,
+            Q4Plan* plan);
 int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream);
 
 // Arguments of the Quest kernels (page summaries, page selection, attention over the pages).

@@ -300,3 +300,44 @@ def test_decode_chain(kvd, D, dtype, window, n_sink, ring):
         c.window, c.n_sink, c.ring = window, n_sink, ring
         c.check(out, lse)
     assert int(err.item()) == 0
+
+
+def wide(c, pages=16384):
+    """The same call with a block table for far more tokens, as a server's is."""
+    c.bt = torch.cat([c.bt, torch.full((len(c.lens), pages - c.bt.shape[1]), -1, dtype=I32)], 1)
+    return c
+
+
+HEADS = [(8, 2, 128, BF), (10, 2, 128, BF), (32, 2, 128, BF), (32, 2, 128, F32), (8, 2, 64, BF),
+         (32, 2, 64, F32), (3, 3, 64, F32)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", HEADS)
+@pytest.mark.parametrize("lens", [[0, 1, 64, 65, 700, 2500], [2000], [130] * 17, [1500, 0] * 20,
+                                  [900, 33, 0, 64, 1] * 20])
+def test_tables_for_short_and_for_long_sequences(kvd, Hq, Hkv, D, dtype, lens):
+    # the table's width decides how the work is divided, never the answer
+    c = Case(lens, Hq, Hkv, D, 32, dtype, learned=True, seed=len(lens))
+    check(kvd, c)
+    check(kvd, wide(c))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", HEADS)
+def test_sequences_that_fill_every_warp(kvd, Hq, Hkv, D, dtype):
+    # long ones, cut into many pieces; then more sequences than warps
+    check(kvd, Case([45000, 21000, 0, 64 * 250, 1000], Hq, Hkv, D, 64, dtype, learned=True, seed=81))
+    lens = np.random.default_rng(82).integers(0, 500, 310).tolist()
+    check(kvd, Case(lens, Hq, Hkv, D, 16, dtype, seed=82))
+
+
+def test_windows_in_wide_tables(kvd):
+    for window, n_sink in ((200, 4), (64, 64), (3000, 0)):
+        check(kvd, wide(Case([5000, 70, 0, 3000, 201], 8, 2, 128, 16, window=window, n_sink=n_sink,
+                             seed=window)))
+
+
+def test_no_sequence_has_tokens(kvd):
+    for learned in (False, True):
+        c = Case([0, 0, 0], 8, 2, 128, 64, learned=learned, seed=91)
+        check(kvd, c)
+        check(kvd, wide(c))

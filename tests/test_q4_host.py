@@ -135,6 +135,9 @@ def test_attention_refusals(kvd):
     assert call(ns=4) == -1 and call(ring=1) == -1         # without a window
     assert call(W=61, ns=4, ring=1) == -1                  # ring larger than its table
     assert call(ws_bytes=64) == -5
+    # more tiles than a 32-bit count of them holds: refused, and no workspace is asked for
+    big = dict(B=65536, Hq=8, Hkv=8, P=256, max_pages=1 << 15)
+    assert call(**big) == -2 and kvd.kvd_workspace_size("gqa_q4", 65536, 8, 8, 64, 1 << 23) == 0
     assert kvd.kvd_workspace_size("gqa_q4", 2, 8, 2, 64, 64) > 0
     assert kvd.kvd_workspace_size("gqa_q4", 2, 8, 3, 64, 64) == 0
     assert kvd.kvd_workspace_size("gqa_q4", 2, 8, 2, 96, 64) == 0
