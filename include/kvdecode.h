@@ -318,8 +318,11 @@ size_t kvd_q4_page_bytes(int page_size, int D);
  *  ordered on the device.
  *  err: int32 on the device, nullable: receives KVD_ERR_DEVICE_OOB (a length or page id out of
  *  range, clamped) or KVD_ERR_TIMEOUT; never cleared.
- * The weights of a head are summed in float32 and multiply the values with at least 16 bits; the
- * result does not depend on timing. Supported: as attn_decode_gqa_paged. Two launches.
+ * Scores, softmax statistics and outputs are held in float32. A weight times its value's scale
+ * multiplies the codes as one float16 number (11 bits) with bfloat16 queries, as two with float32.
+ * The result does not depend on timing. Supported: as attn_decode_gqa_paged, and fewer than 2^31
+ * tiles of 64 tokens in all sequences of max_pages pages (KVD_ERR_UNSUPPORTED otherwise). One
+ * launch for short sequences, two for long ones.
  */
 int attn_decode_gqa_q4(const void *q, const void *k_pool, const void *v_pool,
                        const int32_t *block_table, const int32_t *seq_lens, void *out,

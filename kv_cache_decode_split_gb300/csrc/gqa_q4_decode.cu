@@ -1041,11 +1041,11 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
     const int quad = threadIdx.x % kQuads + blockIdx.y % kParts * kQuads;
     const int k0 = threadIdx.x / kQuads;
     const int lane = threadIdx.x % 32, mt = quad / 32, g = lane >> 2, h = 2 * (lane & 3);
-    if (heads <= 0) return;
     // The unit's partials: of warps first .. last, or, where CTAs have joined their warps' last
     // pieces, of the first warp in each CTA, and the last warp's own if it went on to another unit.
     constexpr int kCta = warps_of(D, NT, kF32);
     int first = 0, last = 0, n = 0, joined = 0;
+    bool whole = false;
     {
         uint32_t tiles = 0, before = 0;
         int own = 0;
@@ -1058,13 +1058,13 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
             }
             tiles += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (own > 0) {
+        if (own > 0 && heads > 0) {
             const Shares<kCta> sh(p, tiles);
             const uint32_t t0 = before * p.HU + static_cast<uint32_t>(u) * own;
             const uint32_t t1 = t0 + own - 1;
             first = sh.owner(t0);
             last = sh.owner(t1);
-            if (first == last) return;
+            whole = first == last;  // one warp had it: written already
             n = last - first + 1;
             if (kJoin && sh.join) {
                 const bool goes_on = t1 + 1 != sh.begin(last + 1);
@@ -1073,7 +1073,10 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
             }
         }
     }
+    // Every CTA waits, those with nothing to do as well: this grid must not end before the main one,
+    // or what follows it in the stream could start while the main launch is still writing.
     griddep_wait();
+    if (heads <= 0 || whole) return;
     const bool mine = h < heads, both = h + 1 < heads;
     float sig[2] = {neg_inf(), neg_inf()};
     if (p.sink_logit) {

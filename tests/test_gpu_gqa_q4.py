@@ -341,3 +341,20 @@ def test_no_sequence_has_tokens(kvd):
         c = Case([0, 0, 0], 8, 2, 128, 64, learned=learned, seed=91)
         check(kvd, c)
         check(kvd, wide(c))
+
+
+def test_outputs_are_complete_for_the_next_work_of_the_stream(kvd):
+    # sequences that one warp has whole, and cut ones; copied by the stream at once, no host wait
+    for lens in ([60] * 300, [60] * 299 + [30000]):
+        c = wide(Case(lens, 4, 4, 64, 16, seed=95), 4096)
+        a = c.gpu()
+        want = kvd.attn_decode_gqa_q4(**a)
+        out = torch.empty_like(want)
+        torch.cuda.synchronize()
+        copies = []
+        for _ in range(30):
+            out.zero_()
+            kvd.attn_decode_gqa_q4(**a, out=out)
+            copies.append(out.clone())
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) for x in copies)
