@@ -358,3 +358,9 @@ def test_outputs_are_complete_for_the_next_work_of_the_stream(kvd):
             copies.append(out.clone())
         torch.cuda.synchronize()
         assert all(torch.equal(x, want) for x in copies)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", HEADS)
+def test_fewer_tiles_than_warps(kvd, Hq, Hkv, D, dtype):
+    for lens in ([30000], [9000, 0, 20000], [65]):
+        check(kvd, wide(Case(lens, Hq, Hkv, D, 64, dtype, learned=True, seed=len(lens))))
