@@ -367,24 +367,25 @@ def attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window=0, n_sin
     memory from PyTorch's allocator, so calls on several streams and captured graphs never share
     it. A bad length or page id is recorded in err (int32 [1]) and clamped.
     """
+    handle = None if stream is None else _own_stream(stream, q, "q")
     if isinstance(workspace, Workspace) or (workspace is None and stream is not None):
-        if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k_pool, torch.Tensor) \
-                or k_pool.dim() != 3 or block_table.dim() != 2:
+        if not all(isinstance(t, torch.Tensor) and t.dim() == n
+                   for t, n in ((q, 3), (k_pool, 3), (block_table, 2))):
             raise ValueError("q, k_pool and block_table must have 3, 3 and 2 dims")
         B, Hq, D = q.shape
         P = k_pool.shape[2] // max(1, D // 2 + D // 16)
         nbytes = max(1, kvd_workspace_size("gqa_q4", B, Hq, k_pool.shape[1], D,
                                            block_table.shape[1] * P))
-        workspace = (_empty_on(stream, nbytes, q, torch.uint8) if workspace is None
-                     else workspace.get(nbytes, "gqa_q4"))
-    if stream is not None:
-        handle = _own_stream(stream, q, "q")
-        if out is None:
-            out = _empty_on(stream, q.shape, q)
-        stream = handle
+        if workspace is None:
+            workspace = _empty_on(stream, nbytes, q, torch.uint8)
+        else:  # (it may have to be filled with zeros: on the stream of the call)
+            with torch.cuda.stream(stream):
+                workspace = workspace.get(nbytes, "gqa_q4")
+    if stream is not None and out is None:
+        out = _empty_on(stream, q.shape, q)
     return _binding.attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window,
                                        n_sink_tokens, ring, sink_logit, scale, out, lse_out,
-                                       workspace, err, stream)
+                                       workspace, err, handle)
 
 
 def _err(err, device):

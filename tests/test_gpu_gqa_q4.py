@@ -364,3 +364,24 @@ def test_outputs_are_complete_for_the_next_work_of_the_stream(kvd):
 def test_fewer_tiles_than_warps(kvd, Hq, Hkv, D, dtype):
     for lens in ([30000], [9000, 0, 20000], [65]):
         check(kvd, wide(Case(lens, Hq, Hkv, D, 64, dtype, learned=True, seed=len(lens))))
+
+
+def test_workspace_shared_with_another_operation_on_its_own_stream(kvd):
+    # the shared buffer is filled with zeros for the other operation: on the call's stream
+    c = Case([30000, 700], 8, 2, 128, 64, seed=97)
+    a = c.gpu()
+    want = kvd.attn_decode_gqa_q4(**a)
+    q, pool = a["q"], torch.zeros(8, 2, 64, 128, dtype=BF, device=DEV)
+    bt, sl = torch.zeros(2, 4, dtype=I32, device=DEV), torch.full((2,), 200, dtype=I32, device=DEV)
+    other = kvd.attn_decode_gqa_paged(q, pool, pool, bt, sl)
+    ws, s = kvd.Workspace(DEV), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            got.append((kvd.attn_decode_gqa_q4(**a, workspace=ws, stream=s), want))
+            got.append((kvd.attn_decode_gqa_paged(q, pool, pool, bt, sl, workspace=ws), other))
+    for _ in range(20):
+        got.append((kvd.attn_decode_gqa_q4(**a, workspace=ws, stream=s), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for x, w in got)
