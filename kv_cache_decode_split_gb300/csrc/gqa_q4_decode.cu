@@ -40,10 +40,12 @@
 // Unit: in short calls a cluster of 1 to 8 CTAs takes one unit and joins it in distributed shared
 // memory, in one launch.
 //
-// Measured (times of calls in a graph, caches colder than one call's data). Full SMs read at the
+// Measured (calls in a graph, three sets of inputs in turn). Full SMs read at the
 // rate of a copy: 64K more tokens of 2 x 8 heads of 128 channels add 6.7 TB/s of codes. What a call
 // costs beside that is about 10 us: start and tile look-up 2.5, first data, joining. 2 x 131072
-// tokens, 32 query heads: 56 us (floor 44); 32 ragged sequences of up to 8192: 46 us (33).
+// tokens, 32 query heads: 56 us (floor 44); 32 ragged sequences of up to 8192: 46 us (33). With 9 to
+// 16 heads to a KV head registers leave two warps to a scheduler, which wait for their own
+// instructions: 96 ragged sequences 35 us (floor 10.6), 37% of issue slots used.
 // The unit form against the list's, 32 query and 8 KV heads: 1 x 520 tokens 6.8 us (list 7.0),
 // 8 x 2048 11.0 (14.8), 8 x 4096 16.0 (19.7), and one launch for the host to make, 2.8 us (4.3).
 

@@ -15,7 +15,10 @@
 // GB300: no reuse, so bytes are the bound. A row is handled by D/16 lanes, each with two pieces of
 // 8 channels (the two halves of the rotated pairs, so a pair never leaves its thread); the row's
 // data is requested before the token's sequence, length, page and table row are looked up, which
-// is a chain of dependent reads.
+// is a chain of dependent reads. Measured: one token of each of 32 sequences, 32 query and 8 KV
+// heads of 128 bf16 channels, 1.9 us (2.3 into 4 bits); 9 prompts, 400 MB in all, 61 us, 98% of the
+// rate of a copy (into 4 bits, with the stored values handed back, 70 us, 88%: the codes'
+// instructions).
 
 #include <algorithm>
 
