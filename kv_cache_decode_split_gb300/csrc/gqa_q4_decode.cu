@@ -41,13 +41,13 @@
 // memory, in one launch.
 //
 // Measured (calls in a graph, three sets of inputs in turn). Full SMs read at the
-// rate of a copy: 64K more tokens of 2 x 8 heads of 128 channels add 6.7 TB/s of codes. What a call
-// costs beside that is about 10 us: start and tile look-up 2.5, first data, joining. 2 x 131072
+// rate of a copy: 2 x 98304 more tokens of 8 heads of 128 channels at 6.7 TB/s. What a call costs
+// beside that is about 10 us: start and tile look-up 2.5, first data, joining. 2 x 131072
 // tokens, 32 query heads: 56 us (floor 44); 32 ragged sequences of up to 8192: 46 us (33). With 9 to
 // 16 heads to a KV head registers leave two warps to a scheduler, which wait for their own
 // instructions: 96 ragged sequences 35 us (floor 10.6), 37% of issue slots used.
-// The unit form against the list's, 32 query and 8 KV heads: 1 x 520 tokens 6.8 us (list 7.0),
-// 8 x 2048 11.0 (14.8), 8 x 4096 16.0 (19.7), and one launch for the host to make, 2.8 us (4.3).
+// The unit form against the list's, 32 query and 8 KV heads: 8 x 2048 tokens 10.9 us (12.8),
+// 8 x 4096 16.2 (18.3), and one launch for the host to make, 2.8 us (4.3).
 
 #include <algorithm>
 #include <type_traits>
@@ -1184,6 +1184,16 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
     }
 }
 
+// A cluster for each unit, with as many CTAs as give each of an SM's four schedulers a warp: where
+// all are resident at once (of 8 CTAs 15 clusters fit, of 4 36), no warp has more than four tiles
+// (the list evens out lengths that differ) and no SM ten tiles of 8 heads more than the list would
+// give it. 2 x 8192 tokens of 8 KV heads, clusters of 4, 18 more: 14.3 us, list 12.6;
+// 1 x 8192, clusters of 8, 9 more: 11.2, list 12.2; 4 x 16384, 10.2 more: 24.1, list 23.0.
+template <int NT>
+bool unit_form(const Q4Plan& plan, int cs, int warps) {
+    return cs > 0 && plan.most <= std::min(4.f * cs * warps, cs * (plan.even + 10.f / NT));
+}
+
 template <int D, int NT, bool kF32, bool kPair>
 int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
     using Cfg = Q4Cfg<D, NT, kF32>;
@@ -1200,14 +1210,7 @@ int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
         configured = 1;
     }
     Q4Params up = p;
-    // A cluster for each unit, with as many CTAs as give each of an SM's four schedulers a warp: where
-    // all are resident at once (of 8 CTAs 15 clusters fit, of 4 36), no warp has more than four tiles
-    // (the list evens out lengths that differ) and no SM ten tiles of 8 heads more than the list would
-    // give it. 2 x 8192 tokens of 8 KV heads, clusters of 4, 18 more: 14.3 us, list 12.6;
-    // 1 x 8192, clusters of 8, 9 more: 11.2, list 12.2; 4 x 16384, 10.2 more: 24.1, list 23.0.
-    for (int cs = plan.cluster;
-         cs > 0 && plan.most <= std::min(4.f * cs * Cfg::kWarps, cs * (plan.even + 10.f / NT));
-         cs /= 2) {
+    for (int cs = plan.cluster; unit_form<NT>(plan, cs, Cfg::kWarps); cs /= 2) {
         if (fits[cs] == 0) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(plan.units * cs);
@@ -1252,19 +1255,18 @@ int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Blocks of at most 8 (or 16) query heads of a KV head; one CTA on each SM, or as many as the
-// longest possible list of tiles keeps busy. CTAs join their warps' pieces where a unit has at least
-// four warps.
-int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible, int dtype,
-            Q4Plan* plan) {
-    const int G = Hq / Hkv;
-    plan->nt = G > 8 ? 2 : 1;
-    plan->NHG = (G + plan->nt * 8 - 1) / (plan->nt * 8);
+// The plan with blocks of at most 8 nt query heads of a KV head; one CTA on each SM, or as many as
+// the longest possible list of tiles keeps busy. CTAs join their warps' pieces where a unit has at
+// least four warps.
+static int plan_heads(int nt, int B, int Hkv, int G, int D, long long max_len, long long visible,
+                      int dtype, Q4Plan* plan) {
+    plan->nt = nt;
+    plan->NHG = (G + nt * 8 - 1) / (nt * 8);
     const long long units = static_cast<long long>(B) * Hkv * plan->NHG;
     const long long tiles = units * ((max_len + kTileTok - 1) / kTileTok + 1);
     if (tiles >= (1LL << 31)) return KVD_ERR_UNSUPPORTED;
     plan->units = static_cast<int>(units);
-    const int warps = warps_of(D, plan->nt, dtype == KVD_F32);
+    const int warps = warps_of(D, nt, dtype == KVD_F32);
     plan->ctas = static_cast<int>(std::max(1LL, std::min<long long>(num_sms(), tiles)));
     plan->n_warps = plan->ctas * warps;
     plan->join = plan->n_warps >= 4 * units;
@@ -1274,12 +1276,28 @@ int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible,
     while (cs < 8 && 2 * cs * units <= num_sms() && plan->most > 4 * cs) cs *= 2;
     plan->cluster = units <= num_sms() ? cs : 0;
     const size_t slots = static_cast<size_t>(plan->n_warps) + units;
-    const size_t heads = static_cast<size_t>(plan->nt) * 8;
+    const size_t heads = static_cast<size_t>(nt) * 8;
     auto round = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     plan->off_m = 0;
     plan->off_l = round(slots * heads * 4);
     plan->off_o = plan->off_l + round(slots * heads * 4);
     plan->total = plan->off_o + slots * heads * D * 4;
+    return KVD_OK;
+}
+
+// 9 to 16 heads of a KV head share the decoding of their codes, but where a call is short, two
+// blocks of 8 have more warps and shorter ones. The workspace is that of the larger plan.
+int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible, int dtype,
+            Q4Plan* plan) {
+    const int G = Hq / Hkv;
+    const int st = plan_heads(1, B, Hkv, G, D, max_len, visible, dtype, plan);
+    if (st != KVD_OK || G <= 8) return st;
+    const size_t total = plan->total;
+    if (!unit_form<1>(*plan, plan->cluster, warps_of(D, 1, dtype == KVD_F32)))
+        plan_heads(2, B, Hkv, G, D, max_len, visible, dtype, plan);
+    Q4Plan two;
+    plan_heads(2, B, Hkv, G, D, max_len, visible, dtype, &two);
+    plan->total = std::max(total, two.total);
     return KVD_OK;
 }
 
