@@ -320,9 +320,9 @@ size_t kvd_q4_page_bytes(int page_size, int D);
  *  range, clamped) or KVD_ERR_TIMEOUT; never cleared.
  * Scores, softmax statistics and outputs are held in float32. A weight times its value's scale
  * multiplies the codes as one float16 number (11 bits) with bfloat16 queries, as two with float32.
- * The result does not depend on timing. Supported: as attn_decode_gqa_paged, and fewer than 2^31
- * tiles of 64 tokens in all sequences of max_pages pages (KVD_ERR_UNSUPPORTED otherwise). One
- * launch for short sequences, two for long ones.
+ * The result does not depend on timing. Supported: as attn_decode_gqa_paged, and B * Hkv *
+ * ceil(Hq / Hkv / 8) * (max_pages * page_size / 64 + 2) < 2^31 (KVD_ERR_UNSUPPORTED otherwise).
+ * One launch for short sequences, two for long ones.
  */
 int attn_decode_gqa_q4(const void *q, const void *k_pool, const void *v_pool,
                        const int32_t *block_table, const int32_t *seq_lens, void *out,

@@ -903,41 +903,77 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 held[k] = k >= NT * D * 8 && k < NT * 8 * (D + 1) ? kNone : 0.f;
         }
         __syncwarp();
-        cluster_sync();
+        if (cs > 1)
+            cluster_sync();
+        else
+            __syncthreads();
         constexpr int kThreads = kWarps * 32;
         const int quads = NT * D * 2 / cs;  // this CTA's
         const int nq = min(quads, kThreads), groups = kThreads / nq;
         const int tid = static_cast<int>(threadIdx.x), grp = tid / nq;
         const int4 un = unit_of(my_unit);
-        const int pieces = min(unit_tiles, kWarps * cs);
+        const int pieces = min(unit_tiles, kWarps * cs), log_cs = __ffs(cs) - 1;
         // (behind a warp's own piece its ring is free)
         constexpr int kScratch = (Cfg::kPieceFloats * 4 + 15) / 16 * 16;
         static_assert(kScratch + 1024 <= Cfg::kRing, "the ring holds a piece and 32 bytes a lane");
         float4* mem = reinterpret_cast<float4*>(smem + kScratch);
         auto cell = [&](int i) { return mem + i / 32 * (Cfg::kRing / 16) + i % 32 * 2; };
+        static_assert(NT * D <= kThreads, "with several CTAs one pass takes all quads of one");
         for (int q0 = 0; q0 < quads; q0 += nq) {  // (16 heads of 128 channels and one CTA: twice)
             const int quad = rank * quads + q0 + tid % nq;
             const int h = quad / (D * 2) * 8 + 2 * (quad & 3);  // heads h and h + 1
             const bool mine_q = grp < groups && q0 + tid % nq < quads && h < un.z;
             float M0 = kNone, M1 = kNone, L0 = 0.f, L1 = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine_q) {
-#pragma unroll 4
-                for (int i = grp; i < pieces; i += groups) {
-                    const uint32_t at = map_peer(smem_u32(smem) + i / cs * Cfg::kRing,
-                                                 static_cast<uint32_t>(i % cs));
-                    const float x0 = ld_cluster_f32(at + (NT * D * 8 + h) * 4);
-                    const float x1 = ld_cluster_f32(at + (NT * D * 8 + h + 1) * 4);
-                    const float y0 = ld_cluster_f32(at + (NT * 8 * (D + 1) + h) * 4);
-                    const float y1 = ld_cluster_f32(at + (NT * 8 * (D + 1) + h + 1) * 4);
-                    const float4 v = ld_cluster_v4(at + quad * 16);
-                    add_piece(M0, M1, L0, L1, acc, x0, x1, y0, y1, v);
+            // kAtOnce of this thread's pieces in flight: one round trip (16 x 4000 tokens, 16 heads on a KV
+            // head, 12.1 us one after another, 11.4), but two where there are no more (60 tokens each:
+            // 6.4 us, with eight 6.9)
+            auto gather = [&](auto at_once) {
+                constexpr int kAtOnce = decltype(at_once)::value;
+                for (int i0 = grp; mine_q && i0 < pieces; i0 += groups * kAtOnce) {
+                    float2 x[kAtOnce], y[kAtOnce];
+                    float4 v[kAtOnce];
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        const int i = i0 + k * groups;
+                        x[k] = make_float2(kNone, kNone);
+                        y[k] = make_float2(0.f, 0.f);
+                        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (i < pieces) {
+                            const uint32_t at = map_peer(smem_u32(smem) + (i >> log_cs) * Cfg::kRing,
+                                                         static_cast<uint32_t>(i & (cs - 1)));
+                            x[k] = ld_cluster_v2(at + (NT * D * 8 + h) * 4);
+                            y[k] = ld_cluster_v2(at + (NT * 8 * (D + 1) + h) * 4);
+                            v[k] = ld_cluster_v4(at + quad * 16);
+                        }
+                    }
+                    float t0 = M0, t1 = M1;
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) t0 = fmaxf(t0, x[k].x), t1 = fmaxf(t1, x[k].y);
+                    const float a0 = fast_exp2(M0 - t0), a1 = fast_exp2(M1 - t1);
+                    M0 = t0, M1 = t1;
+                    L0 *= a0, L1 *= a1;
+                    acc.x *= a0, acc.z *= a0, acc.y *= a1, acc.w *= a1;
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        const float w0 = fast_exp2(x[k].x - t0), w1 = fast_exp2(x[k].y - t1);
+                        L0 = fmaf(w0, y[k].x, L0), L1 = fmaf(w1, y[k].y, L1);
+                        acc.x = fmaf(w0, v[k].x, acc.x), acc.z = fmaf(w0, v[k].z, acc.z);
+                        acc.y = fmaf(w1, v[k].y, acc.y), acc.w = fmaf(w1, v[k].w, acc.w);
+                    }
                 }
-            }
-            __syncthreads();  // (the cells of the pass before are read)
+            };
+            if (pieces <= groups * 2)
+                gather(std::integral_constant<int, 2>{});
+            else
+                gather(std::integral_constant<int, 8>{});
+            if (q0 > 0) __syncthreads();  // the cells of the pass before are read
             cell(tid)[0] = acc;
             cell(tid)[1] = make_float4(M0, M1, L0, L1);
             __syncthreads();
+            // Nothing is read from the other CTAs any more (with several there is one pass): they may
+            // leave once all have come here.
+            if (cs > 1) cluster_arrive_relaxed();
             if (grp != 0 || !mine_q) continue;
             for (int k = 1; k < groups; ++k) {
                 const float4 v = cell(tid + k * nq)[0], x = cell(tid + k * nq)[1];
@@ -969,8 +1005,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
             }
         }
         __syncwarp();
-        cluster_arrive_relaxed();
-        cluster_wait();  // no CTA leaves while another reads its shared memory
+        if (cs > 1) cluster_wait();  // no CTA leaves while another reads its shared memory
         return;
     }
     // ---- join the CTA's last pieces, warps of one unit at a time, into one partial each: a twelfth
@@ -1286,26 +1321,26 @@ static int plan_heads(int nt, int B, int Hkv, int G, int D, long long max_len, l
 }
 
 // 9 to 16 heads of a KV head share the decoding of their codes, but where a call is short, two
-// blocks of 8 have more warps and shorter ones. The workspace is that of the larger plan.
+// blocks of 8 have more warps and shorter ones (16 heads, 2000 tokens 7.4 us, together 9.2), and
+// with float32 queries of 128 channels 16 heads do not fit the registers (2 x 32768 tokens of 8 KV
+// heads 49 us, together 50; 32 x 4096 of 4 49 and 52). The workspace is that of the larger plan.
 int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible, int dtype,
             Q4Plan* plan) {
     const int G = Hq / Hkv;
+    const bool f32 = dtype == KVD_F32;
     const int st = plan_heads(1, B, Hkv, G, D, max_len, visible, dtype, plan);
-    if (st != KVD_OK || G <= 8) return st;
-    const size_t total = plan->total;
-    if (!unit_form<1>(*plan, plan->cluster, warps_of(D, 1, dtype == KVD_F32)))
-        plan_heads(2, B, Hkv, G, D, max_len, visible, dtype, plan);
-    Q4Plan two;
-    plan_heads(2, B, Hkv, G, D, max_len, visible, dtype, &two);
-    plan->total = std::max(total, two.total);
+    if (st != KVD_OK || G <= 8 || (D == 128 && f32)) return st;
+    Q4Plan both;  // (half the units: no more tiles than the plan above)
+    plan_heads(2, B, Hkv, G, D, max_len, visible, dtype, &both);
+    const size_t total = std::max(plan->total, both.total);
+    if (!unit_form<1>(*plan, plan->cluster, warps_of(D, 1, f32))) *plan = both;
+    plan->total = total;
     return KVD_OK;
 }
 
 int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream) {
     if (dtype == KVD_F32) {
-        if (D == 128)
-            return plan.nt == 1 ? launch_q4<128, 1, true, false>(plan, p, stream)
-                                : launch_q4<128, 2, true, false>(plan, p, stream);
+        if (D == 128) return launch_q4<128, 1, true, false>(plan, p, stream);
         return plan.nt == 1 ? launch_q4<64, 1, true, false>(plan, p, stream)
                             : launch_q4<64, 2, true, false>(plan, p, stream);
     }
