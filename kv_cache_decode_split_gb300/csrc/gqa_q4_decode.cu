@@ -46,8 +46,8 @@
 // tokens, 32 query heads: 56 us (floor 44); 32 ragged sequences of up to 8192: 46 us (33). With 9 to
 // 16 heads to a KV head registers leave two warps to a scheduler, which wait for their own
 // instructions: 96 ragged sequences 35 us (floor 10.6), 37% of issue slots used.
-// The unit form against the list's, 32 query and 8 KV heads: 8 x 2048 tokens 10.9 us (12.8),
-// 8 x 4096 16.2 (18.3), and one launch for the host to make, 2.8 us (4.3).
+// The unit form against the list's, 32 query and 8 KV heads: 8 x 2048 tokens 10.6 us (12.8),
+// 8 x 4096 15.6 (18.3), and one launch for the host to make, 2.8 us (4.3).
 
 #include <algorithm>
 #include <type_traits>
@@ -69,28 +69,30 @@ constexpr float kNone = -3.0e38f;
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
 
-// The visible slots of sequence b (at most two ranges), empty for a length of 0.
-__device__ __forceinline__ Ranges seq_ranges(const Q4Params& p, int b) {
-    int L = __ldcg(p.seq_lens + b);  // (from L2: the joining launch reads it early)
-    if (L < 0 || (p.ring <= 0 && L > p.max_len)) {
-        record_error(p.err, KVD_ERR_DEVICE_OOB);
-        L = L < 0 ? 0 : p.max_len;
-    }
+// Length of sequence b, within bounds.
+__device__ __forceinline__ int seq_len(const Q4Params& p, int b) {
+    const int L = __ldcg(p.seq_lens + b);  // (from L2: the joining launch reads it early)
+    if (L >= 0 && (p.ring > 0 || L <= p.max_len)) return L;
+    record_error(p.err, KVD_ERR_DEVICE_OOB);
+    return L < 0 ? 0 : p.max_len;
+}
+// The visible slots of a sequence (at most two ranges), empty for a length of 0.
+__device__ __forceinline__ Ranges slots_of(const Q4Params& p, int L) {
     if (p.ring > 0) return Ranges{0, min(L, p.ring), 0, 0};
     return visible_ranges(L, p.window, p.n_sink);
 }
 __device__ __forceinline__ int range_tiles(int lo, int hi) {
     return hi > lo ? ((hi - 1) >> kTileLog) - (lo >> kTileLog) + 1 : 0;
 }
-__device__ __forceinline__ int seq_tiles(const Q4Params& p, int b) {
-    const Ranges r = seq_ranges(p, b);
+__device__ __forceinline__ int tiles_of(const Ranges& r) {
     return range_tiles(r.lo0, r.hi0) + range_tiles(r.lo1, r.hi1);
 }
 
 // Tiles of each unit of 32 sequences from b0 on, summed up to and with each lane's own (one warp);
-// n: the lane's own.
-__device__ __forceinline__ int scan_tiles(const Q4Params& p, int b0, int lane, int& n) {
-    n = b0 + lane < p.B ? seq_tiles(p, b0 + lane) : 0;
+// n: the lane's own, L: its sequence's length.
+__device__ __forceinline__ int scan_tiles(const Q4Params& p, int b0, int lane, int& n, int& L) {
+    L = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
+    n = tiles_of(slots_of(p, L));
     int inc = n;  // 32 sequences of fewer than 2^30 slots
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -280,16 +282,15 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     uint32_t me = 0, begin = 0;
     int n_mine = 0;     // tiles
     bool join = false;  // the CTA joins its warps' last pieces
-    int scan_n = 0, scan_inc = 0;
+    int scan_n = 0, scan_inc = 0, scan_len = 0;
     // kUnit: this cluster's unit, its sequence's ranges, the tiles and the warps that have some
     const int cs = kUnit ? p.cluster : 1, rank = kUnit ? static_cast<int>(blockIdx.x) % cs : 0;
     const int my_unit = kUnit ? static_cast<int>(blockIdx.x) / cs : 0;
     Ranges unit_ranges{};
     int unit_tiles = 0;
     if constexpr (kUnit) {
-        unit_ranges = seq_ranges(p, my_unit / p.HU);
-        unit_tiles = range_tiles(unit_ranges.lo0, unit_ranges.hi0) +
-                     range_tiles(unit_ranges.lo1, unit_ranges.hi1);
+        unit_ranges = slots_of(p, seq_len(p, my_unit / p.HU));
+        unit_tiles = tiles_of(unit_ranges);
         const int i = warp * cs + rank, n = kWarps * cs;
         const int base = unit_tiles / n, extra = unit_tiles % n;
         begin = i * base + min(i, extra);
@@ -302,11 +303,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         // ---- this warp's share of the tile list
         // Where a CTA joins, its warps have neighbouring shares; elsewhere neighbouring shares are in
         // different CTAs (with fewer tiles than warps, the first warps of all CTAs take one each).
-        scan_inc = scan_tiles(p, 0, lane, scan_n);  // of the first 32 sequences
+        scan_inc = scan_tiles(p, 0, lane, scan_n, scan_len);  // of the first 32 sequences
         uint32_t tiles = __shfl_sync(0xffffffffu, scan_inc, 31);
         for (int b0 = 32; b0 < p.B; b0 += 32) {
-            int n;
-            tiles += __shfl_sync(0xffffffffu, scan_tiles(p, b0, lane, n), 31);
+            int n, L;
+            tiles += __shfl_sync(0xffffffffu, scan_tiles(p, b0, lane, n, L), 31);
         }
         const Shares<kWarps> sh(p, tiles);
         join = sh.join;
@@ -354,14 +355,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                          ((T & ((1 << p.page_shift) - 1)) >> 4);
             }
     };
-    // the warp's i-th tile, the rem-th from the beginning of sequence b on
-    auto resolve = [&](int i, uint32_t rem, int b) {
-        Ranges r = seq_ranges(p, b);
-        int n = range_tiles(r.lo0, r.hi0) + range_tiles(r.lo1, r.hi1);
+    // the warp's i-th tile, the rem-th from the beginning of sequence b (of length L) on
+    auto resolve = [&](int i, uint32_t rem, int b, int L) {
+        Ranges r = slots_of(p, L);
+        int n = tiles_of(r);
         while (rem >= static_cast<uint32_t>(n) * p.HU) {  // this lane's own tile is further on
             rem -= static_cast<uint32_t>(n) * p.HU;
-            r = seq_ranges(p, ++b);
-            n = range_tiles(r.lo0, r.hi0) + range_tiles(r.lo1, r.hi1);
+            r = slots_of(p, seq_len(p, ++b));
+            n = tiles_of(r);
         }
         const int u = static_cast<int>(rem / n), j = static_cast<int>(rem % n);
         describe(i, b, u, j, n, r);
@@ -377,17 +378,18 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         }
         const uint32_t at = begin + base, row = at / static_cast<uint32_t>(p.HU);
         uint32_t before = 0;  // tiles of one unit of each sequence passed
-        int b = 0;
+        int b = 0, len = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {  // the sequence that holds tile `base`
-            int n, inc;
-            if (b0 == 0 && base == 0)
-                n = scan_n, inc = scan_inc;
+            int n, inc, L;
+            if (b0 == 0)
+                n = scan_n, inc = scan_inc, L = scan_len;
             else
-                inc = scan_tiles(p, b0, lane, n);
+                inc = scan_tiles(p, b0, lane, n, L);
             const uint32_t past = __ballot_sync(0xffffffffu, before + inc > row);
             if (past) {
                 const int k = __ffs(past) - 1;
                 b = b0 + k;
+                len = __shfl_sync(0xffffffffu, L, k);
                 before += __shfl_sync(0xffffffffu, inc - n, k);
                 break;
             }
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         }
         const uint32_t rem = at - before * p.HU;
         mine.y = 0;
-        if (base + lane < n_mine) resolve(base + lane, rem + lane, b);
+        if (base + lane < n_mine) resolve(base + lane, rem + lane, b, len);
         special = __ballot_sync(0xffffffffu, (mine.y & 19) != 0);
     };
     const uint64_t pol = l2_evict_first_policy();  // keys and values are read once
@@ -1087,8 +1089,8 @@ __global__ void __launch_bounds__(kSplit == 1 ? D * 2 : 32 * kSplit)
         uint32_t tiles = 0, before = 0;
         int own = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int x;
-            const int inc = scan_tiles(p, b0, lane, x);
+            int x, L;
+            const int inc = scan_tiles(p, b0, lane, x, L);
             if (b >= b0 && b < b0 + 32) {
                 own = __shfl_sync(0xffffffffu, x, b - b0);
                 before = tiles + __shfl_sync(0xffffffffu, inc, b - b0) - own;
