@@ -178,6 +178,7 @@ struct RopeAppendParams {
     long long q_stride, k_stride, v_stride;  // elements
     int B, T, Hq, Hkv;         // Hq 0 without q
     int q_rows, kv_rows, q_items, kv_items;  // rows of a warp, warps of a token (each kind)
+    int q_log, kv_log;         // few heads: log2 of the rows that a warp has lanes for, a token
     int rot, interleaved, max_pos, page_shift, max_pages, num_pages, window, n_sink;
 };
 int rope_append_launch(const RopeAppendParams& p, bool q4, int D, int dtype,

@@ -31,8 +31,9 @@ namespace kvd {
 namespace {
 
 struct TokenAt {
-    int b, slot, pos;   // slot < 0: the cache is not written
+    int slot, pos;      // slot < 0: the cache is not written
     bool ok;            // false: the row belongs to no token, or the token's length is bad
+    int b, len, end;    // its sequence, that one's length, and the row behind its last new token's
 };
 
 // Sequence of token i: the last b with cu[b] <= i, by 32-way search (one warp).
@@ -49,27 +50,37 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int B, int i, int lan
     }
     return lo;
 }
+// The same by one lane.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int B, int i) {
+    int lo = -1, hi = B + 1;  // cu[lo] <= i < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        (__ldg(cu + mid) <= i ? lo : hi) = mid;
+    }
+    return lo;
+}
 
-// Where token i goes (the same answer in every lane of the warp).
-__device__ __forceinline__ TokenAt locate(const RopeAppendParams& p, int i, int lane) {
-    TokenAt a;
-    a.ok = false;
-    a.slot = -1;
-    a.pos = 0;
-    a.b = i;
+// Where token pos of a sequence with this length goes.
+__device__ __forceinline__ int slot_of(const RopeAppendParams& p, int pos, int len) {
+    if (p.window <= 0 || pos < p.n_sink) return pos;
+    return pos >= len - p.window ? p.n_sink + (pos - p.n_sink) % p.window : -1;
+}
+
+// Where token i of sequence b goes.
+__device__ __forceinline__ TokenAt place(const RopeAppendParams& p, int b, int i) {
+    TokenAt a = {-1, 0, false, b, 0, 0};
     int before = i, n = 1;  // the sequence's first row, its new tokens
     if (p.cu_seqlens) {
-        a.b = find_seq(p.cu_seqlens, p.B, i, lane);
-        if (a.b < 0 || a.b >= p.B) return a;  // in front of the first or behind the last sequence
-        before = __ldg(p.cu_seqlens + a.b);
-        const int next = __ldg(p.cu_seqlens + a.b + 1);
+        if (b < 0 || b >= p.B) return a;  // in front of the first or behind the last sequence
+        before = __ldg(p.cu_seqlens + b);
+        const int next = __ldg(p.cu_seqlens + b + 1);
         n = next - before;
         if (before > i || i >= next) {  // offsets that do not ascend
             record_error(p.err, KVD_ERR_DEVICE_OOB);
             return a;
         }
     }
-    const int L = __ldg(p.seq_lens + a.b);
+    const int L = __ldg(p.seq_lens + b);
     const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
     a.pos = L - n + (i - before);
     if (n > L || a.pos >= p.max_pos || (p.window <= 0 && L > cap)) {
@@ -77,10 +88,9 @@ __device__ __forceinline__ TokenAt locate(const RopeAppendParams& p, int i, int 
         return a;
     }
     a.ok = true;
-    if (p.window <= 0 || a.pos < p.n_sink)
-        a.slot = a.pos;
-    else if (a.pos >= L - p.window)
-        a.slot = p.n_sink + (a.pos - p.n_sink) % p.window;
+    a.len = L;
+    a.end = before + n;
+    a.slot = slot_of(p, a.pos, L);
     return a;
 }
 
@@ -270,35 +280,52 @@ __device__ __forceinline__ void put_q4(float (&x)[8], float (&y)[8], int pa, int
         *reinterpret_cast<uint32_t*>(blk + L4::param(r, j)) = j ? par[NG - 1] : par[0];
 }
 
-// Rows begin .. end - 1 of one kind (0 queries, 1 keys, 2 values) of token i, by one warp, R rows of a
-// lane at a time.
-template <typename T, int D, bool kQ4, int R, int kKind>
-__device__ __forceinline__ void append_rows(const RopeAppendParams& p, int i, int begin, int end,
-                                            int lane) {
+// Rows begin .. end - 1 of one kind (0 queries, 1 keys, 2 values) of token i0, by one warp, R rows of
+// a lane at a time. kFew: all rows (at most half of those that a warp has lanes for), 1 << log_rows
+// lanes' rows for each, of token i0 and the ones behind it; their sequence is i0's mostly.
+template <typename T, int D, bool kQ4, int R, int kKind, bool kFew>
+__device__ __forceinline__ void append_rows(const RopeAppendParams& p, int i0, int begin, int end,
+                                            int lane, int log_rows) {
     using L4 = Q4<D>;
     constexpr int kTeam = D / 16;       // lanes of a row
     constexpr int kTeams = 32 / kTeam;  // rows of a warp at once
-    const int team = lane / kTeam, j = lane % kTeam;
+    static_assert(!kFew || R == 1, "one step");
+    const int team = kFew ? lane / kTeam & ((1 << log_rows) - 1) : lane / kTeam, j = lane % kTeam;
+    const int i = kFew ? i0 + (lane / kTeam >> log_rows) : i0;
     const T* src = kKind == 0   ? static_cast<const T*>(p.q) + i * p.q_stride
                    : kKind == 1 ? static_cast<const T*>(p.k) + i * p.k_stride
                                 : static_cast<const T*>(p.v) + i * p.v_stride;
     // pieces of a rotated row: (c, c + rot/16) for the pairs, then neighbours; of a value row
     // (j, j + D/16)
     const int rp = p.rot / 16;
-    const bool turns = kKind != 2 && j < rp;
     const int pa = kKind == 2 || j < rp ? j : 2 * j;
     const int pb = kKind == 2 ? j + kTeam : j < rp ? j + rp : 2 * j + 1;
     Piece<T> a[R], b[R];
     auto load = [&](int k, int row) {
-        if (row < end) {
+        if (row < end && (!kFew || i < p.T)) {
             a[k].load(src + row * D + 8 * pa);
             b[k].load(src + row * D + 8 * pb);
         }
     };
 #pragma unroll
     for (int k = 0; k < R; ++k) load(k, begin + team + k * kTeams);
-    const TokenAt at = locate(p, i, lane);
-    if (!at.ok) return;
+    TokenAt at = place(p, p.cu_seqlens ? find_seq(p.cu_seqlens, p.B, i0, lane) : i0, i0);
+    if constexpr (kFew) {
+        if (i >= p.T) {
+            at.ok = false;
+        } else if (i > i0) {
+            if (at.ok && i < at.end && at.pos + (i - i0) < p.max_pos) {
+                at.pos += i - i0;
+                at.slot = slot_of(p, at.pos, at.len);
+            } else {
+                at = place(p, p.cu_seqlens ? find_seq(p.cu_seqlens, p.B, i) : i, i);
+            }
+        }
+        if (!at.ok) at.slot = -1;
+    } else {
+        if (!at.ok) return;
+    }
+    const bool turns = kKind != 2 && j < rp && (!kFew || at.ok);
     // where the rows go: queries, or the cache's rows of this token
     T* dst = nullptr;    // (null: not written)
     uint8_t* blk = nullptr;
@@ -306,7 +333,7 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams& p, int i, in
     size_t dst_row = D;  // elements, or bytes of 4-bit pages, between heads
     const int in_page = at.slot & ((1 << p.page_shift) - 1);
     if constexpr (kKind == 0) {
-        dst = static_cast<T*>(p.q_out) + static_cast<size_t>(i) * p.Hq * D;
+        if (!kFew || at.ok) dst = static_cast<T*>(p.q_out) + static_cast<size_t>(i) * p.Hq * D;
     } else {
         void* pool = kKind == 2 ? p.v_pool : p.k_pool;
         int page = -1;
@@ -323,7 +350,7 @@ __device__ __forceinline__ void append_rows(const RopeAppendParams& p, int i, in
             if (page >= 0)
                 blk = static_cast<uint8_t*>(pool) + page * (p.Hkv * dst_row) +
                       (in_page >> 4) * L4::kBlockBytes;
-            vals = static_cast<T*>(kKind == 2 ? p.v_out : p.k_out);
+            if (!kFew || at.ok) vals = static_cast<T*>(kKind == 2 ? p.v_out : p.k_out);
             if (vals) vals += static_cast<size_t>(i) * p.Hkv * D;
         } else {
             dst_row = static_cast<size_t>(D) << p.page_shift;
@@ -392,7 +419,8 @@ __global__ void __launch_bounds__(256, kBlocks) rope_append_kernel(const RopeApp
     int part = static_cast<int>(item % per);
     const int lane = threadIdx.x % 32;
     if (part < p.q_items) {
-        append_rows<T, D, kQ4, R, 0>(p, i, part * p.q_rows, min(p.Hq, (part + 1) * p.q_rows), lane);
+        append_rows<T, D, kQ4, R, 0, false>(p, i, part * p.q_rows, min(p.Hq, (part + 1) * p.q_rows),
+                                            lane, 0);
         return;
     }
     part -= p.q_items;
@@ -401,25 +429,77 @@ __global__ void __launch_bounds__(256, kBlocks) rope_append_kernel(const RopeApp
     const int begin = part * p.kv_rows, end = min(p.Hkv, begin + p.kv_rows);
     constexpr int kR = kQ4 ? 1 : R;  // (the codes take the registers)
     if (values)
-        append_rows<T, D, kQ4, kR, 2>(p, i, begin, end, lane);
+        append_rows<T, D, kQ4, kR, 2, false>(p, i, begin, end, lane, 0);
     else
-        append_rows<T, D, kQ4, kR, 1>(p, i, begin, end, lane);
+        append_rows<T, D, kQ4, kR, 1, false>(p, i, begin, end, lane, 0);
+}
+
+// Few heads: a warp has lanes for the keys (or values, or queries, if they are few as well) of several
+// tokens. Warps of queries come first, then those of keys, then of values; q_items, kv_items: all.
+template <typename T, int D, bool kQ4>
+__global__ void __launch_bounds__(256, 3) rope_append_few_kernel(const RopeAppendParams p) {
+    constexpr int kTeams = 32 / (D / 16);
+    griddep_wait();
+    uint32_t item = blockIdx.x * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (item < static_cast<uint32_t>(p.q_items)) {
+        if (p.q_log >= 0) {
+            append_rows<T, D, kQ4, 1, 0, true>(p, item * (kTeams >> p.q_log), 0, p.Hq, lane, p.q_log);
+        } else {
+            const int per = (p.Hq + p.q_rows - 1) / p.q_rows, begin = item % per * p.q_rows;
+            append_rows<T, D, kQ4, 1, 0, false>(p, item / per, begin, min(p.Hq, begin + p.q_rows),
+                                                lane, 0);
+        }
+        return;
+    }
+    item -= p.q_items;
+    const int step = kTeams >> p.kv_log;
+    if (item < static_cast<uint32_t>(p.kv_items))
+        append_rows<T, D, kQ4, 1, 1, true>(p, item * step, 0, p.Hkv, lane, p.kv_log);
+    else if (item < 2u * p.kv_items)
+        append_rows<T, D, kQ4, 1, 2, true>(p, (item - p.kv_items) * step, 0, p.Hkv, lane, p.kv_log);
+}
+
+template <typename... P>
+int launch_items(void (*kernel)(P...), const RopeAppendParams& p, long long items,
+                 cudaStream_t stream) {
+    if (items >= (1LL << 31) - 8) return KVD_ERR_UNSUPPORTED;
+    if (launch_kernel(kernel, dim3(static_cast<unsigned>((items + 7) / 8)), dim3(256), 0, stream,
+                      p) != cudaSuccess)
+        return KVD_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
 }
 
 // `steps`: steps of a warp (its rows are that many times a step's).
 template <typename T, int D, bool kQ4, int R, int kBlocks>
 int launch_rows(RopeAppendParams p, int steps, cudaStream_t stream) {
-    constexpr int step = 32 / (D / 16) * R;
-    p.q_rows = p.kv_rows = step * steps;
+    p.q_rows = p.kv_rows = 32 / (D / 16) * R * steps;
     p.q_items = (p.Hq + p.q_rows - 1) / p.q_rows;
     p.kv_items = (p.Hkv + p.kv_rows - 1) / p.kv_rows;
-    const long long items = static_cast<long long>(p.T) * (p.q_items + 2 * p.kv_items);
-    if (items >= (1LL << 31) - 8) return KVD_ERR_UNSUPPORTED;
-    const unsigned blocks = static_cast<unsigned>((items + 7) / 8);
-    if (launch_kernel(rope_append_kernel<T, D, kQ4, R, kBlocks>, dim3(blocks), dim3(256), 0,
-                      stream, p) != cudaSuccess)
-        return KVD_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
+    return launch_items(rope_append_kernel<T, D, kQ4, R, kBlocks>, p,
+                        static_cast<long long>(p.T) * (p.q_items + 2 * p.kv_items), stream);
+}
+
+template <typename T, int D, bool kQ4>
+int launch_few(RopeAppendParams p, cudaStream_t stream) {
+    constexpr int teams = 32 / (D / 16);
+    auto log_of = [](int heads) {
+        int n = 0;
+        while (1 << n < heads) ++n;
+        return n;
+    };
+    auto warps_of_log = [&](int n) { return (p.T + (teams >> n) - 1LL) / (teams >> n); };
+    p.q_rows = 2 * teams;
+    p.q_log = 2 * p.Hq <= teams ? log_of(p.Hq) : -1;  // (-1: the general form)
+    p.kv_log = log_of(p.Hkv);
+    const long long q = p.Hq == 0 ? 0
+                        : p.q_log >= 0 ? warps_of_log(p.q_log)
+                                       : static_cast<long long>(p.T) * ((p.Hq + p.q_rows - 1) / p.q_rows);
+    const long long kv = warps_of_log(p.kv_log);
+    if (q + 2 * kv >= (1LL << 31) - 8) return KVD_ERR_UNSUPPORTED;
+    p.q_items = static_cast<int>(q);
+    p.kv_items = static_cast<int>(kv);
+    return launch_items(rope_append_few_kernel<T, D, kQ4>, p, q + 2 * kv, stream);
 }
 
 template <typename T, int D, bool kQ4>
@@ -433,6 +513,10 @@ int launch_type(const RopeAppendParams& p, cudaStream_t stream) {
     // 384 3.72 / 3.36, 3000 19.9 / 14.1; into 4 bits 192 3.07 / 3.87, 384 4.67 / 4.72, 3000 28.9 /
     // 16.4; float32 192 3.18 / 3.15, 3000 33.2 / 25.6. 20 warps an SM are about 250 such tokens.
     if (warps <= 20LL * num_sms()) return launch_rows<T, D, kQ4, 1, 1>(p, 1, stream);
+    // Few heads: the lanes of several tokens in a warp, from two (bf16) or four (float32, whose rows are
+    // longer) on. 12000 tokens of 1 head of 128 5.0 us (14.4 otherwise), into 4 bits 7.6 (23.1); 3000 of
+    // 2 heads of 128 bf16 4.4 (5.2), float32 7.6 (7.1); 8000 of 1 head of 64 float32 8.3 (11.9).
+    if ((sizeof(T) == 2 ? 2 : 4) * p.Hkv <= teams) return launch_few<T, D, kQ4>(p, stream);
     if constexpr (sizeof(T) == 2) return launch_rows<T, D, kQ4, 2, 4>(p, 2, stream);
     return launch_rows<T, D, kQ4, 1, 3>(p, 2, stream);  // (a float32 row is two bf16 ones)
 }

@@ -281,3 +281,38 @@ def test_captured_and_on_another_stream(kvd, q4):
     graph.replay()
     torch.cuda.synchronize()
     assert same(got, q) and torch.equal(a["k_pool"].cpu(), kp) and torch.equal(a["v_pool"].cpu(), vp)
+
+
+FEW = [(1, 1, 128, BF), (15, 2, 128, BF), (2, 1, 64, BF), (3, 3, 64, BF), (4, 4, 64, BF), (6, 2, 64, F32), (4, 1, 128, F32)]
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", FEW)
+def test_many_tokens_of_few_heads(kvd, q4, Hq, Hkv, D, dtype):
+    # a warp has rows of several tokens: of one sequence, of neighbours, of none
+    new, old = [1, 0, 701, 1, 1, 1, 333, 2, 0, 450, 5], [0, 3, 7, 90, 0, 31, 0, 5, 1, 64, 0]
+    check(kvd, Case(new, old, Hq, Hkv, D, 32, dtype, 48, q4=q4, pad=7, inter=Hq == 2, seed=Hq))
+    check(kvd, Case(new, old, Hq, Hkv, D, 16, dtype, 64, q4=q4, window=60, n_sink=4, seed=Hq))
+    check(kvd, Case([1] * 1200, [i % 70 for i in range(1200)], Hq, Hkv, D, 16, dtype, 16, q4=q4, cu=False,
+                    seed=Hq))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_bad_sequences_among_few_heads(kvd, q4):
+    c = Case([3, 700, 2, 500, 1], [1, 5, 0, 9, 40], 2, 1, 128, 16, BF, 64, q4=q4, seed=8)
+    q, k, _, _, _ = c.want()
+    for b, lens in ((1, 699), (3, 508 + 1000), (2, -1)):
+        bad = list(c.lens)
+        bad[b] = lens
+        out, _, _, err = run(kvd, c, seq_lens=torch.tensor(bad, dtype=I32, device=DEV))
+        assert err == -6
+        rows = torch.ones(c.T, dtype=torch.bool)
+        rows[c.cu[b]:c.cu[b + 1]] = False
+        assert same(out["q_out"][rows], q[rows]) and (out["q_out"][~rows] == 77.0).all()
+        if q4:
+            assert same(out["k_out"][rows], k[rows]) and (out["k_out"][~rows] == 77.0).all()
+    # keys and values only
+    a = c.gpu()
+    a["q"] = None
+    (kvd.rope_append_q4 if q4 else kvd.rope_append)(**a)
+    assert torch.equal(a["k_pool"].cpu(), c.want()[3])
