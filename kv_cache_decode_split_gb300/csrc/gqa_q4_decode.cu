@@ -177,6 +177,16 @@ __device__ __forceinline__ uint32_t read_shared(const uint32_t* p) {
     return r;
 }
 
+// Load from another CTA's shared memory (cluster address from map_peer).
+__device__ __forceinline__ float2 ld_cluster_v2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Codes with their offset -> c - 8 (exact), for float32 queries: nothing is left to cancel.
 __device__ __forceinline__ uint32_t centre_key(uint32_t x) {
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x),
