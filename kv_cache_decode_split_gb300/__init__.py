@@ -36,7 +36,11 @@ from . import _lib
 from ._lib import KvdError, OP, OPTION
 
 lib = _lib.load()
-from . import _binding  # noqa: E402  (after the library that it calls)
+try:
+    from . import _binding  # (after the library that it calls)
+except ImportError as e:
+    raise ImportError("_binding.so is missing or not built for this PyTorch: build it first "
+                      "(python -c 'import __graft_entry__ as g; g.build()')") from e
 
 _binding.set_error(KvdError)
 

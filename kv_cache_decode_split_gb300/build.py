@@ -22,6 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvdecode.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BUILT_FOR = os.path.join(BUILD, "binding_torch")  # the PyTorch that _binding.so was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -43,6 +44,11 @@ def _torch_dir() -> str:
     return os.path.dirname(importlib.util.find_spec("torch").origin)  # without importing it
 
 
+def _torch_version() -> str:
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sys.version}\n{f.read()}"
+
+
 def _compile(src: str, obj: str, verbose: bool) -> tuple[str, str]:
     if src.endswith(".cpp"):
         inc = os.path.join(_torch_dir(), "include")
@@ -59,14 +65,16 @@ def _compile(src: str, obj: str, verbose: bool) -> tuple[str, str]:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source and link libkvdecode.so (skipped when it is up to date);
+    """Compile every CUDA source and link libkvdecode.so and _binding.so (skipped when up
+    to date and built for this PyTorch);
     `verbose` prints ptxas register / shared-memory / spill figures per kernel."""
     srcs = [BINDING_SRC] + sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
     if not force and os.path.exists(LIB) and os.path.exists(BINDING):
         lib_t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-        if all(os.path.getmtime(d) <= lib_t for d in deps):
+        built_for = open(BUILT_FOR).read() if os.path.exists(BUILT_FOR) else ""
+        if built_for == _torch_version() and all(os.path.getmtime(d) <= lib_t for d in deps):
             return LIB
     os.makedirs(BUILD, exist_ok=True)
     objs = [os.path.join(BUILD, os.path.splitext(os.path.basename(s))[0] + ".o")
@@ -90,6 +98,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BUILT_FOR, "w") as f:
+        f.write(_torch_version())
     return LIB
 
 
