@@ -186,8 +186,8 @@ __device__ __forceinline__ void put_q4(float (&x)[8], float (&y)[8], int pa, int
     constexpr int kTeam = D / 16, NG = L4::kGroups;
     constexpr float kInf = __builtin_huge_valf();
     // Scale and minimum of the row's groups (piece c belongs to group c / 8). Clamping to the
-    // float16 range commutes with minimum and maximum, and a value beyond it takes code 0 or 15
-    // either way; a NaN stays in the minimum and maximum, an infinity shows in one of them.
+    // float16 range commutes with minimum and maximum; a NaN stays in them, an infinity shows in
+    // one of them.
     const float lo_a = least<8>(x), hi_a = most<8>(x), lo_b = least<8>(y), hi_b = most<8>(y);
     // (one group: both pieces are of it; two: pieces a and b are of groups 0 and 1, or, with fewer
     // channels rotated, of any)
@@ -211,6 +211,13 @@ __device__ __forceinline__ void put_q4(float (&x)[8], float (&y)[8], int pa, int
             const float oh = __shfl_xor_sync(0xffffffffu, hi[g], off);
             lo[g] = min3(lo[g], ol, ol), hi[g] = max3(hi[g], oh, oh);
         }
+    // The values themselves: below -65504 (then b is that) a code is 0 either way, but past 65504 it
+    // would follow the value instead of its clamp where the minimum is next to 65504 as well. Rare,
+    // so one comparison a row decides.
+    if (hi[0] > 65504.f || hi[NG - 1] > 65504.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fminf(x[e], 65504.f), y[e] = fminf(y[e], 65504.f);
+    }
     float step[NG], base[NG], inv[NG];
     uint32_t par[NG];
 #pragma unroll

@@ -316,3 +316,20 @@ def test_bad_sequences_among_few_heads(kvd, q4):
     a["q"] = None
     (kvd.rope_append_q4 if q4 else kvd.rope_append)(**a)
     assert torch.equal(a["k_pool"].cpu(), c.want()[3])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_q4_values_past_float16_on_one_side(kvd, dtype, D):
+    # groups that lie next to the largest float16 (its steps are 32 there) and partly past it: the
+    # definition clamps every value before it takes the minimum off
+    c = Case([300, 41], [0, 3], 5, 3, D, 16, dtype, 16, q4=True, strided=False, seed=D)
+    g = torch.Generator().manual_seed(D + 1)
+    for x in (c.k, c.v):
+        low = 64900 + 700 * torch.rand(*x.shape[:2], 1, generator=g)
+        y = low + 400 * torch.rand(x.shape, generator=g)
+        y[1::3] *= -1
+        y[5, :, 1:], y[5, :, 0] = 65490.0, 70000.0
+        y[6, :, 1:], y[6, :, 0] = 65072.0, 3e38
+        x[2:] = y[2:].to(dtype)
+    check(kvd, c)
