@@ -317,7 +317,8 @@ size_t kvd_q4_page_bytes(int page_size, int D);
  *  aligned, of any content: nothing is kept in it from call to call. Calls that share it must be
  *  ordered on the device.
  *  err: int32 on the device, nullable: receives KVD_ERR_DEVICE_OOB (a length or page id out of
- *  range, clamped) or KVD_ERR_TIMEOUT; never cleared.
+ *  range, clamped) or KVD_ERR_TIMEOUT (a copy that did not arrive; the outputs and lse that needed
+ *  it are NaN); never cleared.
  * Scores, softmax statistics and outputs are held in float32. A weight times its value's scale
  * multiplies the codes as one float16 number (11 bits) with bfloat16 queries, as two with float32.
  * The result does not depend on timing. Supported: as attn_decode_gqa_paged, and B * Hkv *
@@ -564,13 +565,15 @@ int kvd_delta_decode_step(float *S, const float *q, const float *k, const float 
  *                         split, raised if the plan would exceed its chunk limit.
  *  KVD_OPT_MLA_MIN_TILES  0 (default): the MLA plan gives each two-CTA cluster at least one
  *                         64-token tile (dense) or two (sparse); >= 1: at least that many.
- *  KVD_OPT_WAIT_TIMEOUT_TEST  1: the next bf16 GQA / SWA call (and only that call) runs
+ *  KVD_OPT_WAIT_TIMEOUT_TEST  1 or 2: the next bf16 GQA / SWA call (and only that call) runs
  *                         with a limit of about 1000 SM cycles on each bounded wait of its
  *                         copy ring, and its consumer warps first wait on a barrier that
  *                         nothing completes: the wait runs out, the call records
  *                         KVD_ERR_TIMEOUT (read with kvd_check_device_error), waits for the
  *                         copies it issued and returns; its outputs are undefined and its
- *                         workspace stays ready for the next call.
+ *                         workspace stays ready for the next call. An attn_decode_gqa_q4 call
+ *                         takes the option in the same way: each warp's wait for its first (1)
+ *                         or second (2) tile runs out (KVD_ERR_TIMEOUT in err, NaN outputs).
  *  KVD_OPT_GQA_CLUSTER    1 (default): a bf16 GQA / SWA call with few (sequence, KV head)
  *                         groups, whose groups need few chunks, runs each group's chunks as
  *                         one thread-block cluster that combines them in distributed shared

@@ -687,6 +687,7 @@ int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
     p.n_sink = ring ? 0 : n_sink_tokens;
     p.ring = ring ? static_cast<int>(cap) : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.stall = g_opt_wait_test.exchange(0);  // KVD_OPT_WAIT_TIMEOUT_TEST, taken by this call only
     return q4_launch(plan, p, D, dtype, stream);
 }
 
@@ -1134,7 +1135,7 @@ int kvd_set_option(int option, long long value) {
             g_opt_mla_min_tiles.store(value);
             return KVD_OK;
         case KVD_OPT_WAIT_TIMEOUT_TEST:
-            if (value != 0 && value != 1) return KVD_ERR_INVALID_ARG;
+            if (value < 0 || value > 2) return KVD_ERR_INVALID_ARG;
             g_opt_wait_test.store(static_cast<int>(value));
             return KVD_OK;
         case KVD_OPT_GQA_CLUSTER:

@@ -257,7 +257,7 @@ __device__ __forceinline__ void add_piece(float& M0, float& M1, float& L0, float
 // joins it in distributed shared memory: no list of all tiles to work out, no second launch.
 template <int D, int NT, bool kF32, bool kPair, bool kUnit>
 __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
-    gqa_q4_kernel(const Q4Params p) {
+    gqa_q4_kernel(const __grid_constant__ Q4Params p) {
     using Cfg = Q4Cfg<D, NT, kF32>;
     using L4 = Q4<D>;
     constexpr int S = Cfg::kStages, kWarps = Cfg::kWarps;
@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     // of each warp: its last piece's unit and that unit's heads
     int2* last_piece = reinterpret_cast<int2*>(masks + 4);
     if (lane == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+        // (in a test of the give-up path, one that its tile does not complete)
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], s + 1 == p.stall ? 2 : 1);
         fence_mbar_init();
         masks[0] = kKeyMask;  // (every warp writes the same)
         masks[1] = kValMask;
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         return make_int4(b, kvh * p.G + hg * NT * 8, min(NT * 8, p.G - hg * NT * 8), 0);
     };
     int2 left = make_int2(-1, 0);  // unit and heads of a last piece that this CTA is to join
+    int lost = n_mine;  // the first tile that the warp did not get
     int s = 0, phase = 0;
     for (int i = 0; i < n_mine; ++i) {
         __syncwarp();
@@ -531,12 +533,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                     for (int r = 0; r < 4; ++r) o[nt][mt][r] = 0.f;
             }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, p.err))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, p.err, p.wait_cycles))) {
             // the warp gives up, once the copies in flight have landed (or their own limits have passed)
             if (lane == 0)
                 for (int k = i + 1; k < min(n_mine, i + S); ++k)
-                    mbar_wait(&full[k % S], (k / S) & 1, p.err);
-            left.x = -1;
+                    mbar_wait(&full[k % S], (k / S) & 1, p.err, p.wait_cycles);
+            __syncwarp();
+            lost = i;
             break;
         }
         const int v0 = (ti.y >> 8) & 127, v1 = (ti.y >> 16) & 127;  // (special tiles only)
@@ -905,15 +908,47 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         queue >>= 1;
         if (++s == S) s = 0, phase ^= 1;
     }
+    // Where a warp gave up, the result of every unit that it has tiles left of is NaN, never what the
+    // workspace or the output held before. (A reference that is NaN makes a joined piece so.)
+    if (lost < n_mine) {
+        const float nan = __int_as_float(0x7fffffff);
+        float* held_m = reinterpret_cast<float*>(ring) + NT * D * 8;
+        if constexpr (kUnit) {
+            if (lane < NT * 8) held_m[lane] = nan;
+        } else {
+            for (int base = lost & ~31; base < n_mine; base += 32) {
+                look_up(base);
+                uint32_t ends = __ballot_sync(0xffffffffu, base + lane >= lost && (mine.y & 2));
+                for (; ends; ends &= ends - 1) {
+                    const int k = __ffs(ends) - 1;
+                    const int unit = __shfl_sync(0xffffffffu, mine.x, k);
+                    const bool whole = from_start && (__shfl_sync(0xffffffffu, mine.y, k) & 8);
+                    from_start = true;  // (the next units begin in this warp's share)
+                    const int4 un = unit_of(unit);
+                    const size_t h0 = static_cast<size_t>(un.x) * p.Hq + un.y;
+                    if (whole) {
+                        for (int e = lane; e < un.z * D; e += 32) {
+                            if constexpr (kF32)
+                                static_cast<float*>(p.out)[h0 * D + e] = nan;
+                            else
+                                static_cast<__nv_bfloat16*>(p.out)[h0 * D + e] =
+                                    __float2bfloat16(nan);
+                        }
+                        if (p.lse_out && lane < un.z) p.lse_out[h0 + lane] = nan;
+                    } else if (join && base + k == n_mine - 1) {
+                        left = make_int2(unit, un.z);
+                        if (lane < NT * 8) held_m[lane] = nan;
+                    } else if (lane < NT * 8) {
+                        __stcg(p.part_m + (static_cast<size_t>(me) + unit) * (NT * 8) + lane, nan);
+                    }
+                }
+            }
+        }
+    }
     if constexpr (kUnit) {
         // ---- join the cluster's pieces (one of each warp that has tiles): CTA `rank` takes its share
         // of the quads of O, groups of threads every groups-th piece, from all the cluster's shared
         // memories
-        if (left.x == -1 && n_mine > 0) {  // (a wait gave up: nothing, rather than anything)
-            float* held = reinterpret_cast<float*>(ring);
-            for (int k = lane; k < Cfg::kPieceFloats; k += 32)
-                held[k] = k >= NT * D * 8 && k < NT * 8 * (D + 1) ? kNone : 0.f;
-        }
         __syncwarp();
         if (cs > 1)
             cluster_sync();
@@ -1350,7 +1385,11 @@ int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible,
     return KVD_OK;
 }
 
-int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream) {
+int q4_launch(const Q4Plan& plan, const Q4Params& args, int D, int dtype, cudaStream_t stream) {
+    Q4Params p = args;
+    // (in a test of the give-up path about a millisecond, longer than any copy takes: only the wait
+    // that the test holds up runs out)
+    p.wait_cycles = p.stall ? 2000000 : kWaitCycles;
     if (dtype == KVD_F32) {
         if (D == 128) return launch_q4<128, 1, true, false>(plan, p, stream);
         return plan.nt == 1 ? launch_q4<64, 1, true, false>(plan, p, stream)

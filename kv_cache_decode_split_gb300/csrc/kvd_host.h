@@ -205,6 +205,9 @@ struct Q4Params {
     int page_shift, max_pages, num_pages, max_len;
     int window, n_sink, ring;  // as GqaParams
     float scale_log2;
+    int stall;                 // test of the give-up path: each warp's wait for its first (1) or
+                               // second (2) tile runs out
+    long long wait_cycles;     // limit of each wait for a tile
 };
 struct Q4Plan {
     int nt;                    // 8-head column tiles of a head block (1 or 2)

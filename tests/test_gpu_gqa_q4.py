@@ -385,3 +385,42 @@ def test_workspace_shared_with_another_operation_on_its_own_stream(kvd):
         got.append((kvd.attn_decode_gqa_q4(**a, workspace=ws, stream=s), want))
     torch.cuda.synchronize()
     assert all(torch.equal(x, w) for x, w in got)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", HEADS + [(32, 2, 64, BF)])
+@pytest.mark.parametrize("lens,in_wide,tiles", [
+    ([1500, 0, 65, 900] * 10, False, [1, 2]), ([300, 0, 130, 64, 6000], False, [1]),
+    ([45000, 21000, 0, 1000, 30], True, [1, 2]), ([60] * 300 + [3000, 0], True, [1]),
+    (np.random.default_rng(83).integers(0, 900, 600).tolist(), True, [1, 2])])
+def test_a_wait_that_runs_out_leaves_nan(kvd, Hq, Hkv, D, dtype, lens, in_wide, tiles):
+    """Every warp's wait for its first or second tile runs out: each output is the right one or NaN, never what an
+    earlier call left in the workspace, and the call says so. The next call is right again."""
+    c = Case(lens, Hq, Hkv, D, 32, dtype, seed=len(lens))
+    if in_wide:
+        wide(c, 4096)
+    ref, rl, tol, tol_l = R.attention(c.q.float().numpy(), c.kp, c.vp, c.bt.numpy(), c.lens, D, 32, c.scale, dtype=dtype)
+    tol = tol + np.abs(ref) * float(torch.finfo(dtype).eps) / 2 + 1e-30
+    some = np.broadcast_to((np.array(lens) > 0)[:, None], rl.shape)
+    a = c.gpu()
+    ws = torch.zeros(kvd.kvd_workspace_size("gqa_q4", len(lens), Hq, Hkv, D, c.bt.shape[1] * 32), dtype=torch.uint8,
+                     device=DEV)
+    for n in tiles:
+        run(kvd, c, workspace=ws, q=(a["q"] * -2).contiguous())
+        kvd.kvd_set_option("wait_timeout_test", n)
+        try:
+            out, lse, err = run(kvd, c, workspace=ws, out=torch.full_like(a["q"], 55.0))
+        finally:
+            kvd.kvd_set_option("wait_timeout_test", 0)
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        bad = np.isnan(out).any(-1)
+        assert err == (-4 if bad.any() else 0) and not (bad & ~some).any()
+        # (600 sequences of 7 tiles and 2 or 3 KV heads are 3 tiles and more for each of at most 2432 warps;
+        # elsewhere no warp may have a second)
+        assert bad.any() or (n > 1 and len(lens) < 600)
+        assert n > 1 or (bad == some).all()
+        assert np.array_equal(np.isnan(out).all(-1), bad) and np.array_equal(np.isnan(lse), bad)
+        good = ~bad
+        assert (np.abs(out - ref)[good] <= tol[good]).all()
+        both = good & some
+        assert (np.abs(lse[both] - rl[both]) <= tol_l[both]).all() and np.isneginf(lse[~some]).all()
+        check(kvd, c)
