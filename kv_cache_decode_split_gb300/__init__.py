@@ -36,13 +36,25 @@ from . import _lib
 from ._lib import KvdError, OP, OPTION
 
 lib = _lib.load()
+
+
+class _NotBuilt:
+    """In the place of a _binding module that cannot be loaded: the calls that go through it raise,
+    the others need the library alone."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError("_binding.so is missing or not built for this PyTorch: build it first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')") from self._why
+
+
 try:
     from . import _binding  # (after the library that it calls)
+    _binding.set_error(KvdError)
 except ImportError as e:
-    raise ImportError("_binding.so is missing or not built for this PyTorch: build it first "
-                      "(python -c 'import __graft_entry__ as g; g.build()')") from e
-
-_binding.set_error(KvdError)
+    _binding = _NotBuilt(e)
 
 __all__ = [
     "attn_decode_gqa_paged", "attn_decode_swa_sink", "attn_decode_mla", "dsa_indexer_topk",

@@ -2,6 +2,8 @@
 layout, and every host-side refusal (none reaches a launch)."""
 import ctypes
 import os
+import shutil
+import subprocess
 import sys
 
 import numpy as np
@@ -154,3 +156,42 @@ def test_host_tensors_are_refused(kvd):
         kvd.rope_append_q4(None, z(2, 2, 64), z(2, 2, 64), z(9, 64), pool, pool, i(2, 2), i(2))
     with pytest.raises(TypeError, match="CUDA tensor"):
         kvd.attn_decode_gqa_q4(z(2, 8, 64), pool, pool, i(2, 2), i(2))
+
+
+def _elsewhere(tmp_path, code, *without):
+    """Run code where the package is a copy without some of its files: (exit code, output)."""
+    src = os.path.join(ROOT, "kv_cache_decode_split_gb300")
+    dst = tmp_path / "kv_cache_decode_split_gb300"
+    dst.mkdir()
+    for n in os.listdir(src):
+        if n.endswith((".py", ".so")) and n not in without:
+            shutil.copy(os.path.join(src, n), dst / n)
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    return r.returncode, r.stdout + r.stderr
+
+
+CALLS_ALL = """
+import torch
+{first}
+import kv_cache_decode_split_gb300 as kvd
+z, i = torch.zeros, lambda *s: torch.zeros(*s, dtype=torch.int32)
+def says(f, *a):
+    try:
+        f(*a)
+    except Exception as e:
+        print(f.__name__, type(e).__name__, e)
+says(kvd.attn_decode_gqa_paged, z(1, 8, 64), z(1, 2, 16, 64), z(1, 2, 16, 64), i(1, 1), i(1))
+says(kvd.rope_append, None, z(2, 2, 64), z(2, 2, 64), z(9, 64), z(4, 2, 16, 64), z(4, 2, 16, 64), i(2, 2), i(2))
+says(kvd.rope_append_q4, None, z(2, 2, 64), z(2, 2, 64), z(9, 64), z(4), z(4), i(2, 2), i(2))
+says(kvd.attn_decode_gqa_q4, z(2, 8, 64), z(4), z(4), i(2, 2), i(2))
+print(kvd.kvd_workspace_size("gqa_q4", 2, 8, 2, 64, 64) > 0)
+"""
+OWN = ("rope_append", "rope_append_q4", "attn_decode_gqa_q4")
+
+
+def test_without_the_compiled_module_the_other_calls_work(kvd, tmp_path):
+    rc, out = _elsewhere(tmp_path, CALLS_ALL.format(first=""), "_binding.so")
+    assert rc == 0, out
+    assert "attn_decode_gqa_paged TypeError q must be a CUDA tensor" in out and "True" in out
+    for n in OWN:
+        assert f"{n} ImportError _binding.so is missing" in out
