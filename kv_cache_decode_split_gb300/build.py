@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -49,11 +50,17 @@ def _torch_version() -> str:
         return f"{sys.version}\n{f.read()}"
 
 
+def _torch_name() -> str:
+    """torch.__version__, which the module carries and the package compares when it loads it."""
+    return re.search(r"^__version__ = '([^']*)'", _torch_version(), re.M)[1]
+
+
 def _compile(src: str, obj: str, verbose: bool) -> tuple[str, str]:
     if src.endswith(".cpp"):
         inc = os.path.join(_torch_dir(), "include")
         cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-        cmd = ["g++", "-c", src, "-o", obj, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+        cmd = ["g++", "-c", src, "-o", obj, "-O2", "-std=c++17", "-fPIC",
+               f'-DKVD_BUILT_FOR="{_torch_name()}"', "-I", INCLUDE,
                "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
                os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda]
     else:

@@ -320,4 +320,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject* m = PyModule_Create(&module);
+    // the PyTorch whose tensors this module can read (build.py gives it): the package compares
+    if (m && PyModule_AddStringConstant(m, "built_for", KVD_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -195,3 +195,13 @@ def test_without_the_compiled_module_the_other_calls_work(kvd, tmp_path):
     assert "attn_decode_gqa_paged TypeError q must be a CUDA tensor" in out and "True" in out
     for n in OWN:
         assert f"{n} ImportError _binding.so is missing" in out
+
+
+def test_a_module_built_for_another_pytorch_is_refused(kvd, tmp_path):
+    # its symbols may all be there, and tensors be laid out another way
+    assert kvd._binding.built_for == torch.__version__
+    rc, out = _elsewhere(tmp_path, CALLS_ALL.format(first="torch.__version__ = '2.0.0'"))
+    assert rc == 0, out
+    assert "attn_decode_gqa_paged TypeError q must be a CUDA tensor" in out and "True" in out
+    for n in OWN:
+        assert f"{n} ImportError _binding.so is missing or not built for this PyTorch" in out
