@@ -71,9 +71,21 @@ def _compile(src: str, obj: str, verbose: bool) -> tuple[str, str]:
     return src, r.stderr
 
 
+def _link_binding(obj: str) -> None:
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libkvdecode.so",
+           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+           "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA source and link libkvdecode.so and _binding.so (skipped when up
-    to date and built for this PyTorch);
+    to date and built for this PyTorch). Where the module cannot be built the library still is, and
+    the error is raised behind it.
     `verbose` prints ptxas register / shared-memory / spill figures per kernel."""
     srcs = [BINDING_SRC] + sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
@@ -87,7 +99,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     objs = [os.path.join(BUILD, os.path.splitext(os.path.basename(s))[0] + ".o")
             for s in srcs]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        for src, log in ex.map(lambda so: _compile(so[0], so[1], verbose), zip(srcs, objs)):
+        module = ex.submit(_compile, srcs[0], objs[0], verbose)
+        for src, log in ex.map(lambda so: _compile(so[0], so[1], verbose), zip(srcs[1:], objs[1:])):
             if verbose and log:
                 print(f"== {os.path.basename(src)}\n{log}", file=sys.stderr)
     tmp = LIB + f".tmp{os.getpid()}"
@@ -97,14 +110,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, objs[0], "-L", PKG, "-l:libkvdecode.so",
-           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
-           "-lc10", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    try:
+        module.result()
+        _link_binding(objs[0])
+    except Exception:
+        if os.path.exists(BINDING):  # one of an earlier library, with its calls
+            os.remove(BINDING)
+        raise
     with open(BUILT_FOR, "w") as f:
         f.write(_torch_version())
     return LIB

@@ -205,3 +205,28 @@ def test_a_module_built_for_another_pytorch_is_refused(kvd, tmp_path):
     assert "attn_decode_gqa_paged TypeError q must be a CUDA tensor" in out and "True" in out
     for n in OWN:
         assert f"{n} ImportError _binding.so is missing or not built for this PyTorch" in out
+
+
+def test_the_library_is_built_where_the_module_cannot_be(monkeypatch, tmp_path):
+    import __graft_entry__ as g
+    b = g._builder()
+    for n in ("LIB", "BINDING", "BUILT_FOR"):
+        monkeypatch.setattr(b, n, str(tmp_path / n))
+    monkeypatch.setattr(b, "BUILD", str(tmp_path))
+    (tmp_path / "BINDING").write_text("a module of an earlier library")
+
+    def compiles(src, obj, verbose):
+        if src.endswith(".cpp"):
+            raise RuntimeError("no headers here")
+        return src, ""
+
+    def links(cmd, **kw):
+        open(cmd[cmd.index("-o") + 1], "w").write("linked")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(b, "_compile", compiles)
+    monkeypatch.setattr(b.subprocess, "run", links)
+    with pytest.raises(RuntimeError, match="no headers here"):
+        b.build()
+    assert (tmp_path / "LIB").read_text() == "linked"
+    assert not (tmp_path / "BINDING").exists() and not (tmp_path / "BUILT_FOR").exists()
