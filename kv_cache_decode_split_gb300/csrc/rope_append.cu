@@ -524,8 +524,10 @@ int launch_type(const RopeAppendParams& p, cudaStream_t stream) {
     // longer) on. 12000 tokens of 1 head of 128 5.0 us (14.4 otherwise), into 4 bits 7.6 (23.1); 3000 of
     // 2 heads of 128 bf16 4.4 (5.2), float32 7.6 (7.1); 8000 of 1 head of 64 float32 8.3 (11.9).
     if ((sizeof(T) == 2 ? 2 : 4) * p.Hkv <= teams) return launch_few<T, D, kQ4>(p, stream);
-    if constexpr (sizeof(T) == 2) return launch_rows<T, D, kQ4, 2, 4>(p, 2, stream);
-    return launch_rows<T, D, kQ4, 1, 3>(p, 2, stream);  // (a float32 row is two bf16 ones)
+    if constexpr (sizeof(T) == 2)
+        return launch_rows<T, D, kQ4, 2, 4>(p, 2, stream);
+    else  // (a float32 row is two bf16 ones)
+        return launch_rows<T, D, kQ4, 1, 3>(p, 2, stream);
 }
 
 }  // namespace

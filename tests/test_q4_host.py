@@ -2,6 +2,7 @@
 layout, and every host-side refusal (none reaches a launch)."""
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -230,3 +231,14 @@ def test_the_library_is_built_where_the_module_cannot_be(monkeypatch, tmp_path):
         b.build()
     assert (tmp_path / "LIB").read_text() == "linked"
     assert not (tmp_path / "BINDING").exists() and not (tmp_path / "BUILT_FOR").exists()
+
+
+@pytest.mark.skipif(shutil.which("nm") is None, reason="reads the library's symbol names")
+def test_the_append_holds_only_kernels_that_a_call_launches(kvd):
+    names = subprocess.run(["nm", "-C", os.path.join(ROOT, "kv_cache_decode_split_gb300", "libkvdecode.so")],
+                           capture_output=True, text=True, check=True).stdout
+    got = set(re.findall(r"rope_append_kernel<(\w+), (\d+), (\w+), (\d+), (\d+)>", names))
+    # few rows; many of bfloat16, many of float32
+    forms = [(t, "1", "1") for t in ("float", "__nv_bfloat16")] + [("__nv_bfloat16", "2", "4"), ("float", "1", "3")]
+    want = {(t, d, q4, r, c) for t, r, c in forms for d in ("64", "128") for q4 in ("true", "false")}
+    assert got == want
