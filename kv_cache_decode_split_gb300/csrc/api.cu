@@ -652,8 +652,8 @@ int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
         return KVD_ERR_INVALID_ARG;
     Q4Plan plan;
     const long long max_len = (long long)max_pages * page_size;
-    if (q4_plan(B, Hq, Hkv, D, max_len, window > 0 ? std::min(max_len, cap) : max_len, dtype,
-                &plan) != KVD_OK)
+    const int most = q4_unit_tiles(max_len, window, n_sink_tokens, ring != 0);
+    if (q4_plan(B, Hq, Hkv, D, max_len, most, dtype, &plan) != KVD_OK)
         return KVD_ERR_UNSUPPORTED;
     if (ws_bytes < plan.total) return KVD_ERR_WORKSPACE_TOO_SMALL;
     Q4Params p;
@@ -1089,7 +1089,8 @@ size_t kvd_workspace_size(int op, int B, int H, int Hkv, int D, int max_len, int
     if (op == KVD_OP_GQA_Q4) {
         Q4Plan plan;
         if (Hkv < 1 || H % Hkv != 0 || (D != 64 && D != 128) ||
-            q4_plan(B, H, Hkv, D, max_len, max_len, KVD_BF16, &plan) != KVD_OK)
+            q4_plan(B, H, Hkv, D, max_len, q4_unit_tiles(max_len, 0, 0, false), KVD_BF16, &plan) !=
+                KVD_OK)
             return 0;
         return plan.total;  // float32 queries need no more
     }

@@ -1340,8 +1340,8 @@ int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
 // The plan with blocks of at most 8 nt query heads of a KV head; one CTA on each SM, or as many as
 // the longest possible list of tiles keeps busy. CTAs join their warps' pieces where a unit has at
 // least four warps.
-static int plan_heads(int nt, int B, int Hkv, int G, int D, long long max_len, long long visible,
-                      int dtype, Q4Plan* plan) {
+static int plan_heads(int nt, int B, int Hkv, int G, int D, long long max_len, int most, int dtype,
+                      Q4Plan* plan) {
     plan->nt = nt;
     plan->NHG = (G + nt * 8 - 1) / (nt * 8);
     const long long units = static_cast<long long>(B) * Hkv * plan->NHG;
@@ -1352,7 +1352,7 @@ static int plan_heads(int nt, int B, int Hkv, int G, int D, long long max_len, l
     plan->ctas = static_cast<int>(std::max(1LL, std::min<long long>(num_sms(), tiles)));
     plan->n_warps = plan->ctas * warps;
     plan->join = plan->n_warps >= 4 * units;
-    plan->most = static_cast<int>((visible + kTileTok - 1) / kTileTok) + 1;
+    plan->most = most;
     plan->even = static_cast<float>(units) * plan->most / num_sms();
     int cs = 1;
     while (cs < 8 && 2 * cs * units <= num_sms() && plan->most > 4 * cs) cs *= 2;
@@ -1371,14 +1371,13 @@ static int plan_heads(int nt, int B, int Hkv, int G, int D, long long max_len, l
 // blocks of 8 have more warps and shorter ones (16 heads, 2000 tokens 7.4 us, together 9.2), and
 // with float32 queries of 128 channels 16 heads do not fit the registers (2 x 32768 tokens of 8 KV
 // heads 49 us, together 50; 32 x 4096 of 4 49 and 52). The workspace is that of the larger plan.
-int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible, int dtype,
-            Q4Plan* plan) {
+int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int most, int dtype, Q4Plan* plan) {
     const int G = Hq / Hkv;
     const bool f32 = dtype == KVD_F32;
-    const int st = plan_heads(1, B, Hkv, G, D, max_len, visible, dtype, plan);
+    const int st = plan_heads(1, B, Hkv, G, D, max_len, most, dtype, plan);
     if (st != KVD_OK || G <= 8 || (D == 128 && f32)) return st;
     Q4Plan both;  // (half the units: no more tiles than the plan above)
-    plan_heads(2, B, Hkv, G, D, max_len, visible, dtype, &both);
+    plan_heads(2, B, Hkv, G, D, max_len, most, dtype, &both);
     const size_t total = std::max(plan->total, both.total);
     if (!unit_form<1>(*plan, plan->cluster, warps_of(D, 1, f32))) *plan = both;
     plan->total = total;

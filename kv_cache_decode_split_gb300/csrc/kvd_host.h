@@ -217,9 +217,18 @@ struct Q4Plan {
     float even;                // tiles of an SM if all units have as many and all SMs share them
     size_t off_m, off_l, off_o, total;
 };
-// visible: tokens that a query sees at most (max_len, or less with a window)
-int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, long long visible, int dtype,
-            Q4Plan* plan);
+// At most how many 64-slot tiles a unit has: of all slots (one too many, as the form choice was
+// measured), a rolling cache's, or, windowed, of two ranges. The sink tokens' tiles and the window's,
+// which may begin and end inside one, are counted apart; a tile that holds parts of both counts twice.
+inline int q4_unit_tiles(long long max_len, long long window, long long n_sink, bool ring) {
+    auto tiles = [](long long n) { return (n + 63) / 64; };
+    const long long all = tiles(max_len) + 1;
+    if (window <= 0) return static_cast<int>(all);
+    const long long seen = ring ? tiles(n_sink + window) : tiles(n_sink) + tiles(window);
+    return static_cast<int>(seen + 1 < all ? seen + 1 : all);
+}
+// most: tiles that a unit may have (q4_unit_tiles)
+int q4_plan(int B, int Hq, int Hkv, int D, long long max_len, int most, int dtype, Q4Plan* plan);
 int q4_launch(const Q4Plan& plan, const Q4Params& p, int D, int dtype, cudaStream_t stream);
 
 // Arguments of the Quest kernels (page summaries, page selection, attention over the pages).

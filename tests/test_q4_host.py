@@ -242,3 +242,33 @@ def test_the_append_holds_only_kernels_that_a_call_launches(kvd):
     forms = [(t, "1", "1") for t in ("float", "__nv_bfloat16")] + [("__nv_bfloat16", "2", "4"), ("float", "1", "3")]
     want = {(t, d, q4, r, c) for t, r, c in forms for d in ("64", "128") for q4 in ("true", "false")}
     assert got == want
+
+
+def test_no_unit_has_more_tiles_than_the_plan_counts(kvd, tmp_path):
+    # the count that the plan chooses a form by, compiled on its own, against every length's tiles
+    import __graft_entry__ as g
+    b = g._builder()
+    src = tmp_path / "tiles.cpp"
+    src.write_text("""#include <cstdio>
+        #include "kvd_host.h"
+        int main() {
+            long long n, w, s; int r;
+            while (std::scanf("%lld %lld %lld %d", &n, &w, &s, &r) == 4)
+                std::printf("%d\\n", kvd::q4_unit_tiles(n, w, s, r != 0));
+        }""")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(b.nvcc()))), "include")
+    subprocess.run(["g++", "-std=c++17", "-I", b.CSRC, "-I", b.INCLUDE, "-isystem", cuda, str(src), "-o",
+                    str(tmp_path / "tiles")], check=True)
+    cases = [(n, w, s, r) for n in (16, 64, 100, 192, 640) for w in (0, 1, 2, 63, 64, 65, 66, 130, 700)
+             for s in (0, 1, 4, 64, 65, 90) for r in (0, 1)
+             if not (w == 0 and (s or r)) and not (r and w + s > n)]
+    said = subprocess.run([str(tmp_path / "tiles")], input="\n".join(" ".join(map(str, c)) for c in cases), text=True,
+                          capture_output=True, check=True).stdout.split()
+    count = lambda lo, hi: 0 if hi <= lo else (hi - 1) // 64 - lo // 64 + 1
+    for (n, w, s, r), most in zip(cases, map(int, said)):
+        tiles = []
+        for L in range(n + 1):
+            lo = max(0, L - w) if w else 0
+            one = r or w == 0 or min(s, L) >= lo
+            tiles.append(count(0, min(L, w + s) if r else L) if one else count(0, min(s, L)) + count(lo, L))
+        assert max(tiles) <= most <= max(tiles) + 1, (n, w, s, r)
