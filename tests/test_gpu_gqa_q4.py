@@ -424,3 +424,28 @@ def test_a_wait_that_runs_out_leaves_nan(kvd, Hq, Hkv, D, dtype, lens, in_wide, 
         both = good & some
         assert (np.abs(lse[both] - rl[both]) <= tol_l[both]).all() and np.isneginf(lse[~some]).all()
         check(kvd, c)
+
+
+# bfloat16 heads of 64, more than 8 to a KV head: blocks of 16 heads, 11 warps a CTA
+WIDE_GROUPS = [(32, 2, 64, BF), (24, 2, 64, BF), (20, 1, 64, BF), (9, 1, 64, BF)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", WIDE_GROUPS)
+@pytest.mark.parametrize("lens", [[0, 1, 64, 65, 700, 2500], [2000], [130] * 17, [1500, 0] * 40,
+                                  [900, 33, 0, 64, 1] * 24, [1100, 5, 0, 64, 65, 640] * 16])
+def test_wide_groups_in_narrow_and_wide_tables(kvd, Hq, Hkv, D, dtype, lens):
+    c = Case(lens, Hq, Hkv, D, 32, dtype, learned=True, seed=len(lens))
+    check(kvd, c)
+    check(kvd, wide(c))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", WIDE_GROUPS)
+def test_wide_groups_that_fill_every_warp(kvd, Hq, Hkv, D, dtype):
+    check(kvd, Case([45000, 21000, 0, 64 * 250, 1000], Hq, Hkv, D, 64, dtype, learned=True, seed=81))
+    lens = np.random.default_rng(82).integers(0, 500, 310).tolist()
+    check(kvd, Case(lens, Hq, Hkv, D, 16, dtype, seed=82))
+    for lens in ([30000], [9000, 0, 20000], [65]):
+        check(kvd, wide(Case(lens, Hq, Hkv, D, 64, dtype, learned=True, seed=len(lens))))
+    for window, n_sink in ((200, 4), (3000, 0)):
+        check(kvd, wide(Case([5000, 70, 0, 3000, 201], Hq, Hkv, D, 16, dtype, window=window, n_sink=n_sink,
+                             seed=window)))

@@ -333,3 +333,42 @@ def test_q4_values_past_float16_on_one_side(kvd, dtype, D):
         y[6, :, 1:], y[6, :, 0] = 65072.0, 3e38
         x[2:] = y[2:].to(dtype)
     check(kvd, c)
+
+
+# many tokens of more heads than the several-token form takes; heads that leave partial steps
+LARGE = [(9, 3, 128, BF), (25, 5, 64, BF), (40, 8, 128, BF), (34, 17, 128, BF), (36, 35, 64, BF), (9, 3, 128, F32),
+         (25, 5, 64, F32), (34, 17, 64, F32), (20, 20, 128, F32)]
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", LARGE)
+def test_many_tokens_of_many_heads(kvd, q4, Hq, Hkv, D, dtype):
+    cut = 3 if Hkv > 8 else 1
+    new, old = [1, 0, 701 // cut, 1, 333 // cut, 2, 0, 450 // cut, 5], [0, 3, 7, 90, 31, 0, 5, 1, 64]
+    check(kvd, Case(new, old, Hq, Hkv, D, 32, dtype, 48, q4=q4, pad=7, inter=Hq % 2 == 1, seed=Hq))
+    check(kvd, Case(new, old, Hq, Hkv, D, 16, dtype, D, q4=q4, window=60, n_sink=4, seed=Hq))
+    n = 1200 // cut
+    check(kvd, Case([1] * n, [i % 70 for i in range(n)], Hq, Hkv, D, 16, dtype, 16, q4=q4, cu=False,
+                    strided=False, seed=Hq))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(9, 3, 128, BF), (25, 5, 64, F32)])
+def test_bad_sequences_among_many_heads(kvd, q4, Hq, Hkv, D, dtype):
+    c = Case([3, 700, 2, 500, 1], [1, 5, 0, 9, 40], Hq, Hkv, D, 16, dtype, 64, q4=q4, seed=8)
+    q, k, _, _, _ = c.want()
+    for b, lens in ((1, 699), (3, 508 + 1000), (2, -1)):
+        bad = list(c.lens)
+        bad[b] = lens
+        out, _, _, err = run(kvd, c, seq_lens=torch.tensor(bad, dtype=I32, device=DEV))
+        assert err == -6
+        rows = torch.ones(c.T, dtype=torch.bool)
+        rows[c.cu[b]:c.cu[b + 1]] = False
+        assert same(out["q_out"][rows], q[rows]) and (out["q_out"][~rows] == 77.0).all()
+        if q4:
+            assert same(out["k_out"][rows], k[rows]) and (out["k_out"][~rows] == 77.0).all()
+    # keys and values only
+    a = c.gpu()
+    a["q"] = None
+    (kvd.rope_append_q4 if q4 else kvd.rope_append)(**a)
+    assert torch.equal(a["k_pool"].cpu(), c.want()[3])
