@@ -177,6 +177,13 @@ __device__ __forceinline__ uint32_t read_shared(const uint32_t* p) {
     return r;
 }
 
+// One more copy's bytes for a barrier's phase to wait for.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
 // Load from another CTA's shared memory (cluster address from map_peer).
 __device__ __forceinline__ float2 ld_cluster_v2(uint32_t addr) {
     float2 v;
@@ -280,11 +287,12 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     // of each warp: its last piece's unit and that unit's heads
     int2* last_piece = reinterpret_cast<int2*>(masks + 4);
     if (lane == 0) {
-        // (in a test of the give-up path, one that its tile does not complete)
-        for (int s = 0; s < S; ++s) mbar_init(&full[s], s + 1 == p.stall ? 2 : 1);
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
         masks[0] = kKeyMask;  // (every warp writes the same)
         masks[1] = kValMask;
+        // (a test of the give-up path: one phase that the tile's copies do not complete)
+        if (p.stall > 0) mbar_expect_tx(&full[p.stall - 1], 16);
     }
     __syncwarp();
     const uint32_t key_mask = read_shared(masks), val_mask = read_shared(masks + 1);
@@ -463,7 +471,12 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         return make_int4(b, kvh * p.G + hg * NT * 8, min(NT * 8, p.G - hg * NT * 8), 0);
     };
     int2 left = make_int2(-1, 0);  // unit and heads of a last piece that this CTA is to join
-    int lost = n_mine;  // the first tile that the warp did not get
+    // The first tile that the warp did not get. Every unit that it has tiles left of then gets NaN for a
+    // result, never what the workspace or the output held before (a reference that is NaN makes a
+    // joined piece so).
+    int lost = n_mine;
+    const float kNan = __int_as_float(0x7fffffff);
+    float* held_m = reinterpret_cast<float*>(ring) + NT * D * 8;  // the last piece's references
     int s = 0, phase = 0;
     for (int i = 0; i < n_mine; ++i) {
         __syncwarp();
@@ -540,6 +553,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                     mbar_wait(&full[k % S], (k / S) & 1, p.err, p.wait_cycles);
             __syncwarp();
             lost = i;
+            if (kUnit && lane < NT * 8) held_m[lane] = kNan;
             break;
         }
         const int v0 = (ti.y >> 8) & 127, v1 = (ti.y >> 16) & 127;  // (special tiles only)
@@ -908,39 +922,30 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         queue >>= 1;
         if (++s == S) s = 0, phase ^= 1;
     }
-    // Where a warp gave up, the result of every unit that it has tiles left of is NaN, never what the
-    // workspace or the output held before. (A reference that is NaN makes a joined piece so.)
-    if (lost < n_mine) {
-        const float nan = __int_as_float(0x7fffffff);
-        float* held_m = reinterpret_cast<float*>(ring) + NT * D * 8;
-        if constexpr (kUnit) {
-            if (lane < NT * 8) held_m[lane] = nan;
-        } else {
-            for (int base = lost & ~31; base < n_mine; base += 32) {
-                look_up(base);
-                uint32_t ends = __ballot_sync(0xffffffffu, base + lane >= lost && (mine.y & 2));
-                for (; ends; ends &= ends - 1) {
-                    const int k = __ffs(ends) - 1;
-                    const int unit = __shfl_sync(0xffffffffu, mine.x, k);
-                    const bool whole = from_start && (__shfl_sync(0xffffffffu, mine.y, k) & 8);
-                    from_start = true;  // (the next units begin in this warp's share)
-                    const int4 un = unit_of(unit);
-                    const size_t h0 = static_cast<size_t>(un.x) * p.Hq + un.y;
-                    if (whole) {
-                        for (int e = lane; e < un.z * D; e += 32) {
-                            if constexpr (kF32)
-                                static_cast<float*>(p.out)[h0 * D + e] = nan;
-                            else
-                                static_cast<__nv_bfloat16*>(p.out)[h0 * D + e] =
-                                    __float2bfloat16(nan);
-                        }
-                        if (p.lse_out && lane < un.z) p.lse_out[h0 + lane] = nan;
-                    } else if (join && base + k == n_mine - 1) {
-                        left = make_int2(unit, un.z);
-                        if (lane < NT * 8) held_m[lane] = nan;
-                    } else if (lane < NT * 8) {
-                        __stcg(p.part_m + (static_cast<size_t>(me) + unit) * (NT * 8) + lane, nan);
+    if (!kUnit && lost < n_mine) {
+        for (int base = lost & ~31; base < n_mine; base += 32) {
+            look_up(base);
+            uint32_t ends = __ballot_sync(0xffffffffu, base + lane >= lost && (mine.y & 2));
+            for (; ends; ends &= ends - 1) {
+                const int k = __ffs(ends) - 1;
+                const int unit = __shfl_sync(0xffffffffu, mine.x, k);
+                const bool whole = from_start && (__shfl_sync(0xffffffffu, mine.y, k) & 8);
+                from_start = true;  // (the next units begin in this warp's share)
+                const int4 un = unit_of(unit);
+                const size_t h0 = static_cast<size_t>(un.x) * p.Hq + un.y;
+                if (whole) {
+                    for (int e = lane; e < un.z * D; e += 32) {
+                        if constexpr (kF32)
+                            static_cast<float*>(p.out)[h0 * D + e] = kNan;
+                        else
+                            static_cast<__nv_bfloat16*>(p.out)[h0 * D + e] = __float2bfloat16(kNan);
                     }
+                    if (p.lse_out && lane < un.z) p.lse_out[h0 + lane] = kNan;
+                } else if (join && base + k == n_mine - 1) {
+                    left = make_int2(unit, un.z);
+                    if (lane < NT * 8) held_m[lane] = kNan;
+                } else if (lane < NT * 8) {
+                    __stcg(p.part_m + (static_cast<size_t>(me) + unit) * (NT * 8) + lane, kNan);
                 }
             }
         }
