@@ -449,3 +449,22 @@ def test_wide_groups_that_fill_every_warp(kvd, Hq, Hkv, D, dtype):
     for window, n_sink in ((200, 4), (3000, 0)):
         check(kvd, wide(Case([5000, 70, 0, 3000, 201], Hq, Hkv, D, 16, dtype, window=window, n_sink=n_sink,
                              seed=window)))
+
+
+@pytest.mark.parametrize("Hq,D,dtype", [(3, 64, BF), (3, 128, F32), (12, 64, BF)])
+def test_thousands_of_sequences(kvd, Hq, D, dtype):
+    c = Case(np.random.default_rng(84).integers(0, 40, 5000).tolist(), Hq, 1, D, 16, dtype, learned=True, seed=85)
+    check(kvd, c)
+    check(kvd, wide(c, 512))
+
+
+@pytest.mark.parametrize("Hq", [4, 8])
+@pytest.mark.parametrize("dtype,ratio", [(BF, 2.0 ** 20), (F32, 2.0 ** 12)])
+def test_groups_of_very_different_sizes(kvd, Hq, dtype, ratio):
+    # the two groups of 64 channels share a softmax reference; one's scales are far above the other's
+    for qscale in (1.0, 4.0):
+        c = Case([3000, 41], Hq, 1, 128, 64, dtype, qscale=qscale, seed=86)
+        code, s, b = R.unpack(c.vp, 128, False)
+        f = np.array([ratio ** 0.5, ratio ** -0.5])
+        c.vp = R.pack(code, (s * f).astype(np.float16), (b * f).astype(np.float16), False)
+        check(kvd, c)

@@ -372,3 +372,23 @@ def test_bad_sequences_among_many_heads(kvd, q4, Hq, Hkv, D, dtype):
     a["q"] = None
     (kvd.rope_append_q4 if q4 else kvd.rope_append)(**a)
     assert torch.equal(a["k_pool"].cpu(), c.want()[3])
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_offsets_past_32_bits(kvd, q4):
+    # pages in the last of more than 4 GiB of each pool
+    c = Case([3, 40], [5, 60], 4, 8, 128, 64, BF, 128, q4=q4, seed=3)
+    _, _, _, kp, vp = c.want()
+    a = c.gpu()
+    pages = (5 << 30) // (a["k_pool"][0].numel() * a["k_pool"].element_size())
+    first = pages - c.pages
+    for n in ("k_pool", "v_pool"):
+        big = torch.empty((pages,) + a[n].shape[1:], dtype=a[n].dtype, device=DEV)
+        big[first:] = a[n]
+        a[n] = big
+    a["block_table"] = torch.where(a["block_table"] >= 0, a["block_table"] + first, -1).to(I32)
+    (kvd.rope_append_q4 if q4 else kvd.rope_append)(**a)
+    if q4:
+        assert same_pool(a["k_pool"][first:], kp, 128, True) and same_pool(a["v_pool"][first:], vp, 128, False)
+    else:
+        assert torch.equal(a["k_pool"][first:].cpu(), kp) and torch.equal(a["v_pool"][first:].cpu(), vp)
