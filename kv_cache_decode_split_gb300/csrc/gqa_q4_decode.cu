@@ -162,6 +162,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Keys: 16 + c as bf16, code bits at mantissa bits 3-6.
 constexpr uint32_t kKeyMask = 0x00780078u, kKey = 0x41804180u;
 // Values: float16, code bits at mantissa bits 4-7: 64 + c, for odd tokens (the high halves)
@@ -589,7 +597,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 *reinterpret_cast<uint2*>(wb) =
                     *reinterpret_cast<const uint2*>(kb + (g + 8) * 32 + t * 8);
             }
-            float acc[NT][NQ][4];
+            // (float32 queries: their leading parts, and what the other parts add)
+            float acc[NT][NQ][4], rest[NT][NQ][4];
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 uint32_t fa[4], fb[4];
@@ -603,9 +612,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < kQ; ++k) {
-                        float(&c0)[4] = acc[nt][kPair ? 0 : w / 2];
-                        float(&c1)[4] = acc[nt][kPair ? 1 : w / 2];
-                        const bool fresh = k == 0 && (kPair ? w == 0 : w % 2 == 0);
+                        auto& sums = k == 0 ? acc : rest;
+                        float(&c0)[4] = sums[nt][kPair ? 0 : w / 2];
+                        float(&c1)[4] = sums[nt][kPair ? 1 : w / 2];
+                        const bool fresh = k <= 1 && (kPair ? w == 0 : w % 2 == 0);
                         if (fresh)
                             mma_bf16_first(c0, fa[0], fb[0], fa[1], fb[1], qf[k][nt][w][0],
                                            qf[k][nt][w][1]);
@@ -636,6 +646,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                             float& v = x[bk][nt][2 * half + c];
                             v = gr ? fmaf(base, qsum[nt][gr][c], v) : base * qsum[nt][gr][c];
                             float a = acc[nt][gr][2 * half + c];
+                            if (kF32) a += rest[nt][gr][2 * half + c];
                             if (kPair) a += acc[nt][NQ - 1][2 * half + c];
                             v = fmaf(f.x, a, v);
                             if (kPair) v += __shfl_xor_sync(0xffffffffu, v, 2);
@@ -797,14 +808,28 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                     }
                     const int mt = gr * 4 + hw * 2;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t(&w)[2] = pf[nt][gp][0];
+                        // The matrix instructions cut their sums where float32 arithmetic rounds: with
+                        // float32 queries they add 16 tokens, the small parts first, and the rest is
+                        // rounded (2 x 16 million tokens: off by 4e-7, not 4e-4).
+                        if constexpr (kF32) {
+                            const uint32_t(&low)[2] = pf[nt][gp][1];
+                            float d0[4], d1[4];
+                            mma_f16_first(d0, fu[0], fu[1], fv[0], fv[1], low[0], low[1]);
+                            mma_f16_first(d1, fu[2], fu[3], fv[2], fv[3], low[0], low[1]);
+                            mma_f16(d0, fu[0], fu[1], fv[0], fv[1], w[0], w[1]);
+                            mma_f16(d1, fu[2], fu[3], fv[2], fv[3], w[0], w[1]);
 #pragma unroll
-                        for (int k = 0; k < kP; ++k) {
-                            mma_f16(o[nt][mt], fu[0], fu[1], fv[0], fv[1], pf[nt][gp][k][0],
-                                    pf[nt][gp][k][1]);
-                            mma_f16(o[nt][mt + 1], fu[2], fu[3], fv[2], fv[3], pf[nt][gp][k][0],
-                                    pf[nt][gp][k][1]);
+                            for (int e = 0; e < 4; ++e) {
+                                o[nt][mt][e] += d0[e];
+                                o[nt][mt + 1][e] += d1[e];
+                            }
+                        } else {
+                            mma_f16(o[nt][mt], fu[0], fu[1], fv[0], fv[1], w[0], w[1]);
+                            mma_f16(o[nt][mt + 1], fu[2], fu[3], fv[2], fv[3], w[0], w[1]);
                         }
+                    }
                 }
                 if (!kF32 && gr < NG) {
 #pragma unroll

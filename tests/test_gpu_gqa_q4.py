@@ -468,3 +468,28 @@ def test_groups_of_very_different_sizes(kvd, Hq, dtype, ratio):
         f = np.array([ratio ** 0.5, ratio ** -0.5])
         c.vp = R.pack(code, (s * f).astype(np.float16), (b * f).astype(np.float16), False)
         check(kvd, c)
+
+
+def repeated(kvd, c, log_tokens):
+    """The call of a one-sequence case whose table repeats the sequence's pages up to 2^log_tokens tokens (each
+    counts as often, so the output is the sequence's): relative error of the output in the 2-norm."""
+    a = c.gpu()
+    times = (1 << log_tokens) // c.lens[0]
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    lse = torch.empty(c.q.shape[:2], device=DEV)
+    a["block_table"] = c.bt.repeat(1, times).to(DEV)
+    a["seq_lens"] = torch.tensor([times * c.lens[0]], dtype=I32, device=DEV)
+    out = kvd.attn_decode_gqa_q4(**a, lse_out=lse, err=err)
+    ref, rl, _, tol_l = R.attention(c.q.float().numpy(), c.kp, c.vp, c.bt.numpy(), c.lens, c.D, c.P, c.scale, dtype=c.dtype)
+    assert int(err) == 0
+    # the logarithm's own rounding, and the sum's: n / 64 additions in a lane's share of a warp's part
+    assert (np.abs(lse.double().cpu().numpy() - rl - math.log(times)) <= tol_l + 2.0 ** -18).all()
+    return np.linalg.norm(out.double().cpu().numpy() - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (16, 2, 128), (16, 2, 64), (32, 2, 64)])
+def test_float32_sums_do_not_drift(kvd, Hq, Hkv, D):
+    # Scores below 8 are held to half a step of 2^-22, by at most 8 roundings, and each moves its token's
+    # weight alone; everything added up behind them is rounded, so its errors cancel: 2^-19 in all
+    for log_tokens in (18, 22):
+        assert repeated(kvd, Case([8192], Hq, Hkv, D, 256, F32, seed=7), log_tokens) <= 2.0 ** -19
