@@ -62,6 +62,7 @@ namespace {
 
 constexpr int kTileTok = 64;   // tokens of a tile: four 16-token blocks, used two at a time
 constexpr int kTileLog = 6;
+constexpr int kPutBy = 32;     // tiles of a warp between two times that it puts its sums by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // maximum of nothing: finite, so that differences with it are defined
@@ -227,8 +228,9 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t (&part)[kS
 }
 
 // A tile as the warp that uses it sees it: the unit, and bits 0 first tile of the warp's piece of
-// the unit, 1 last, 2 first tile of the unit, 3 last, 4 not all of its tokens visible; from bit 8
-// the first visible token of the tile, from bit 16 the one behind the last.
+// the unit, 1 last, 2 first tile of the unit, 3 last, 4 not all of its tokens visible, 5 the sums are
+// put by before it; from bit 8 the first visible token of the tile, from bit 16 the one behind the
+// last.
 using TileInfo = int2;
 
 // One CTA on each SM; as many warps as its registers hold (a thread's products, sums and operands
@@ -268,15 +270,23 @@ __device__ __forceinline__ void add_piece(float& M0, float& M1, float& L0, float
 // and its weights carry its own group's scale: half the scaling, packing and transposing of the
 // general form, where half the columns would be empty.
 //
+// kLong: the matrix instructions cut their float32 sums instead of rounding them, so that a sum over many
+// tokens drifts: with 18,400 tokens of a warp (16 million of 2 KV heads, bfloat16) the outputs were off by
+// 6.5e-3 of their size, where their own rounding is 1.7e-3. Every kPutBy tiles a warp therefore adds its
+// sums, by float32 arithmetic, to its slot of the workspace and starts from zero again: 1.8e-3. Calls that
+// have no more than kPutBy tiles for each warp, by their block table, do without the code, which costs the
+// others 1 to 3% (2 x 524288 tokens 195 us, 188 without; 32 x 4096 in a table for 131072 34.7 and 34.2).
+//
 // kUnit: short calls. A cluster of CTAs takes one unit, its warps the unit's tiles in equal shares, and
 // joins it in distributed shared memory: no list of all tiles to work out, no second launch.
-template <int D, int NT, bool kF32, bool kPair, bool kUnit>
+template <int D, int NT, bool kF32, bool kPair, bool kUnit, bool kLong>
 __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     gqa_q4_kernel(const __grid_constant__ Q4Params p) {
     using Cfg = Q4Cfg<D, NT, kF32>;
     using L4 = Q4<D>;
     constexpr int S = Cfg::kStages, kWarps = Cfg::kWarps;
     static_assert(!kPair || (D == 128 && NT == 1 && !kF32), "two groups, one column tile");
+    static_assert(!kLong || (!kF32 && !kUnit), "not needed there");
     constexpr int NG = kPair ? 1 : L4::kGroups;  // groups that a lane scales
     constexpr int NQ = kPair ? 2 : NG;           // accumulators of a score
     constexpr int KW = D / 32;             // key words of a lane and row
@@ -360,6 +370,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         mine.y = ((i == 0 || j == 0) ? 1 : 0) |
                  ((i == n_mine - 1 || j == n - 1) ? 2 : 0) | (j == 0 ? 4 : 0) |
                  (j == n - 1 ? 8 : 0) | ((v0 > 0 || v1 < kTileTok) ? 16 : 0) | v0 << 8 | v1 << 16;
+        if (kLong && i % kPutBy == 0 && !(mine.y & 1)) mine.y |= 32;
         // The pages of its (up to four) pieces: a piece is a page's part of the tile. Pieces
         // without a visible token take the page of one that has.
         const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
@@ -400,7 +411,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
             if (base + lane < n_mine)
                 describe(base + lane, my_unit / p.HU, my_unit % p.HU, begin + base + lane,
                          unit_tiles, unit_ranges);
-            special = __ballot_sync(0xffffffffu, (mine.y & 19) != 0);
+            special = __ballot_sync(0xffffffffu, (mine.y & 51) != 0);
             return;
         }
         const uint32_t at = begin + base, row = at / static_cast<uint32_t>(p.HU);
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
         const uint32_t rem = at - before * p.HU;
         mine.y = 0;
         if (base + lane < n_mine) resolve(base + lane, rem + lane, b, len);
-        special = __ballot_sync(0xffffffffu, (mine.y & 19) != 0);
+        special = __ballot_sync(0xffffffffu, (mine.y & 51) != 0);
     };
     const uint64_t pol = l2_evict_first_policy();  // keys and values are read once
     // copy the warp's i-th tile into stage s
@@ -471,6 +482,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
     // o, and the values' offsets and minima in it: oo by the matrix product, ob in each lane
     float o[NT][MT][4], oo[NT][NG][4], ob[NT][NG][2], m[NT][2], l[NT][2];
     bool from_start = false;
+    // (kLong) scale of the sums put by (0: none yet) against the present reference
+    float put[NT][2];
+    // this lane's quads of O in a partial, for heads 2t and 2t + 1 (kPair: 2 (t & 1) and the next, of its
+    // group's half of the channels)
+    constexpr int kHave = kPair ? MT / 2 : MT;
+    auto quads_of = [&](int nt) {
+        return nt * (D * 8) + (kPair ? own * (kHave * 128) + (4 * g + (t & 1)) * 4 : lane * 4);
+    };
 
     // sequence, first query head, and number of heads of a unit
     auto unit_of = [&](int unit) {
@@ -547,11 +566,48 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 for (int c = 0; c < 2; ++c) {
                     m[nt][c] = kNone;
                     l[nt][c] = 0.f;
+                    put[nt][c] = 0.f;
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[nt][mt][r] = 0.f;
+            }
+        }
+        // ---- the sums put by: in the warp's slot of the workspace, which is its own to the end of the
+        // piece (ob is rounded as it grows and stays; oo goes to it)
+        if (kLong && (queue & 1) && (ti.y & 32)) {
+            const int4 un = unit_of(ti.x);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int h0 = kPair ? 2 * (t & 1) : nt * 8 + 2 * t;
+                float* at = p.part_o + (static_cast<size_t>(me) + ti.x) * (NT * D * 8) + quads_of(nt);
+#pragma unroll
+                for (int mt = 0; mt < kHave; ++mt) {
+                    float4 was = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = kPair && own ? o[nt][mt + MT - kHave][e] : o[nt][mt][e];
+                        o[nt][mt][e] = 0.f;
+                        o[nt][mt + MT - kHave][e] = 0.f;
+                    }
+                    if (h0 < un.z) {
+                        float4* q = reinterpret_cast<float4*>(at + mt * 128);
+                        if (put[nt][0] > 0.f || put[nt][1] > 0.f) was = __ldcg(q);
+                        __stcg(q, make_float4(fmaf(was.x, put[nt][0], v[0]), fmaf(was.y, put[nt][1], v[1]),
+                                              fmaf(was.z, put[nt][0], v[2]), fmaf(was.w, put[nt][1], v[3])));
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    put[nt][c] = 1.f;
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) {
+                        if (g == 0) ob[nt][gr][c] += oo[nt][gr][c];
+                        oo[nt][gr][c] = oo[nt][gr][2 + c] = 0.f;
+                    }
+                }
             }
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, p.err, p.wait_cycles))) {
@@ -722,6 +778,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                     const float al = fast_exp2(m[nt][c] - v);
                     m[nt][c] = v;
                     l[nt][c] *= al;
+                    if (kLong) put[nt][c] *= al;
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) {
                         ob[nt][gr][c] *= al;
@@ -812,7 +869,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                         const uint32_t(&w)[2] = pf[nt][gp][0];
                         // The matrix instructions cut their sums where float32 arithmetic rounds: with
                         // float32 queries they add 16 tokens, the small parts first, and the rest is
-                        // rounded (2 x 16 million tokens: off by 4e-7, not 4e-4).
+                        // rounded (16 million tokens of 2 KV heads: off by 6e-7, not 4e-4).
                         if constexpr (kF32) {
                             const uint32_t(&low)[2] = pf[nt][gp][1];
                             float d0[4], d1[4];
@@ -900,7 +957,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                 // (kPair: this lane has its own group's half of the channels, of heads 0-3)
                 const int h0 = kPair ? 2 * (t & 1) : nt * 8 + 2 * t;
                 if (h0 >= un.z) continue;
-                constexpr int kHave = kPair ? MT / 2 : MT;
                 float r[kHave][4];
 #pragma unroll
                 for (int mt = 0; mt < kHave; ++mt)
@@ -909,15 +965,23 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT, kF32>::kWarps * 32, 1)
                         const float v = kPair && own ? o[nt][mt + MT - kHave][e] : o[nt][mt][e];
                         r[mt][e] = v + add[kPair ? 0 : mt / 4][e & 1];
                     }
+                float* dst = p.part_o + slot * (NT * D * 8) + quads_of(nt);
+                if (kLong && (put[nt][0] > 0.f || put[nt][1] > 0.f)) {
+#pragma unroll
+                    for (int mt = 0; mt < kHave; ++mt) {
+                        const float4 was = __ldcg(reinterpret_cast<const float4*>(dst + mt * 128));
+                        r[mt][0] = fmaf(was.x, put[nt][0], r[mt][0]);
+                        r[mt][1] = fmaf(was.y, put[nt][1], r[mt][1]);
+                        r[mt][2] = fmaf(was.z, put[nt][0], r[mt][2]);
+                        r[mt][3] = fmaf(was.w, put[nt][1], r[mt][3]);
+                    }
+                }
                 if (!whole) {  // 16 bytes of 8 x 2 channels and heads each
-                    const int to = nt * (D * 8) +
-                                   (kPair ? own * (kHave * 128) + (4 * g + (t & 1)) * 4 : lane * 4);
-                    float* dst = p.part_o + slot * (NT * D * 8) + to;
 #pragma unroll
                     for (int mt = 0; mt < kHave; ++mt) {
                         const float4 v = make_float4(r[mt][0], r[mt][1], r[mt][2], r[mt][3]);
                         if (at_end)
-                            *reinterpret_cast<float4*>(held + to + mt * 128) = v;
+                            *reinterpret_cast<float4*>(held + quads_of(nt) + mt * 128) = v;
                         else
                             __stcg(reinterpret_cast<float4*>(dst + mt * 128), v);
                     }
@@ -1309,13 +1373,17 @@ bool unit_form(const Q4Plan& plan, int cs, int warps) {
 template <int D, int NT, bool kF32, bool kPair>
 int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
     using Cfg = Q4Cfg<D, NT, kF32>;
-    auto kern = gqa_q4_kernel<D, NT, kF32, kPair, false>;
-    auto unit_kern = gqa_q4_kernel<D, NT, kF32, kPair, true>;
+    constexpr bool kDrifts = !kF32;
+    auto kern = gqa_q4_kernel<D, NT, kF32, kPair, false, false>;
+    auto long_kern = gqa_q4_kernel<D, NT, kF32, kPair, false, kDrifts>;
+    auto unit_kern = gqa_q4_kernel<D, NT, kF32, kPair, true, false>;
     static int configured = 0;
     static int fits[9] = {};  // clusters of this size that are resident at once, plus 1
     if (!configured) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem) !=
                 cudaSuccess ||
+            cudaFuncSetAttribute(long_kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg::kSmem) != cudaSuccess ||
             cudaFuncSetAttribute(unit_kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Cfg::kSmem) != cudaSuccess)
             return KVD_ERR_CUDA;
@@ -1348,6 +1416,8 @@ int launch_q4(const Q4Plan& plan, const Q4Params& p, cudaStream_t stream) {
             return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
         }
     }
+    if (static_cast<long long>(plan.units) * plan.most > kPutBy * static_cast<long long>(plan.n_warps))
+        kern = long_kern;
     if (launch_kernel(kern, dim3(plan.ctas), dim3(Cfg::kWarps * 32), Cfg::kSmem, stream, p) !=
         cudaSuccess)
         return KVD_ERR_CUDA;

@@ -493,3 +493,45 @@ def test_float32_sums_do_not_drift(kvd, Hq, Hkv, D):
     # weight alone; everything added up behind them is rounded, so its errors cancel: 2^-19 in all
     for log_tokens in (18, 22):
         assert repeated(kvd, Case([8192], Hq, Hkv, D, 256, F32, seed=7), log_tokens) <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (16, 2, 128), (32, 2, 128), (16, 2, 64), (32, 2, 64)])
+def test_bfloat16_sums_do_not_drift(kvd, Hq, Hkv, D):
+    # An output's rounding is spread over half a step, 2^-8 of a value between 1 and 2: 2^-8 / sqrt(3) at
+    # most in the 2-norm. The weights' (half a step of 2^-11, spread, of at most 15 + 15 steps of a code
+    # whose own spread is 4.6) add 2^-12 / sqrt(3) * 30 / 4.6 = 2^-10.1 of the same: 2^-8.6 together.
+    for log_tokens in (18, 24):
+        assert repeated(kvd, Case([8192], Hq, Hkv, D, 256, BF, seed=7), log_tokens) <= 2.0 ** -8.6
+
+
+@pytest.mark.parametrize("learned", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (14, 2, 128), (32, 2, 128), (10, 2, 64), (24, 2, 64)])
+def test_many_tokens_of_a_warp_in_many_sequences(kvd, Hq, Hkv, D, learned):
+    # sums put by across the ends of pieces, with references that rise and units that one warp has whole:
+    # a table repeats the pages, so every length's output is a weighted one of the same tokens
+    c = Case([4096], Hq, Hkv, D, 256, BF, qscale=3.0, learned=learned, seed=87)
+    a, times = c.gpu(), [900, 1, 0, 333, 40, 700, 2, 500]
+    width = max(times)
+    for n in ("q",):
+        a[n] = a[n].repeat(len(times), 1, 1)
+    a["block_table"] = c.bt.repeat(len(times), width).to(DEV)
+    a["seq_lens"] = torch.tensor([t * 4096 for t in times], dtype=I32, device=DEV)
+    lse = torch.empty(len(times), Hq, device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    out = kvd.attn_decode_gqa_q4(**a, lse_out=lse, err=err).double().cpu().numpy()
+    assert int(err) == 0
+    sink = None if c.sink is None else c.sink.numpy().astype(np.float64)
+    # without the sink; its share then follows from the number of repetitions
+    ref, rl, tol, tol_l = R.attention(c.q.float().numpy(), c.kp, c.vp, c.bt.numpy(), c.lens, D, 256, c.scale)
+    for i, t in enumerate(times):
+        if t == 0:
+            assert (out[i] == 0).all()
+            continue
+        total = rl[0] + math.log(t)
+        if sink is not None:
+            total = np.logaddexp(total, sink)
+        share = np.exp(rl[0] + math.log(t) - total)
+        want = ref[0] * share[:, None]
+        lim = tol[0] + np.abs(want) * (2.0 ** -8 + tol_l[0][:, None]) + 1e-30
+        assert (np.abs(out[i] - want) <= lim).all(), i
+        assert (np.abs(lse[i].double().cpu().numpy() - total) <= tol_l[0] + 2.0 ** -18).all()
