@@ -320,7 +320,10 @@ size_t kvd_q4_page_bytes(int page_size, int D);
  *  range, clamped) or KVD_ERR_TIMEOUT (a copy that did not arrive; the outputs and lse that needed
  *  it are NaN); never cleared.
  * Scores, softmax statistics and outputs are held in float32. A weight times its value's scale
- * multiplies the codes as one float16 number (11 bits) with bfloat16 queries, as two with float32.
+ * multiplies the codes as one float16 number (11 bits) with bfloat16 queries, as two with float32
+ * (22 bits). Such a product keeps its bits down to 2^-22 (the two: 2^-11) of the head's largest and is
+ * rounded to a step of 2^-32 of that below: one token's small weight is lost in the large ones' own
+ * rounding, but a group of 64 channels whose scales are that far below the other group's loses bits.
  * The result does not depend on timing. Supported: as attn_decode_gqa_paged, and B * Hkv *
  * ceil(Hq / Hkv / 8) * (max_pages * page_size / 64 + 2) < 2^31 (KVD_ERR_UNSUPPORTED otherwise).
  * One launch for short sequences, two for long ones.

@@ -383,7 +383,8 @@ def attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window=0, n_sin
     workspace: a uint8 tensor of kvd_workspace_size("gqa_q4", B, Hq, Hkv, D, max_pages * P) bytes
     or a Workspace, of any content (calls that share one must be ordered); None takes fresh
     memory from PyTorch's allocator, so calls on several streams and captured graphs never share
-    it. A bad length or page id is recorded in err (int32 [1]) and clamped.
+    it. A bad length or page id is recorded in err (int32 [1]) and clamped. A copy that
+    does not arrive in time is recorded too, and the outputs that needed it are NaN.
     """
     handle = None if stream is None else _own_stream(stream, q, "q")
     if isinstance(workspace, Workspace) or (workspace is None and stream is not None):

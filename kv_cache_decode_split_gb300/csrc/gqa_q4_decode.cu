@@ -40,14 +40,18 @@
 // Unit: in short calls a cluster of 1 to 8 CTAs takes one unit and joins it in distributed shared
 // memory, in one launch.
 //
-// Measured (calls in a graph, three sets of inputs in turn). Full SMs read at the
-// rate of a copy: 2 x 98304 more tokens of 8 heads of 128 channels at 6.7 TB/s. What a call costs
-// beside that is about 10 us: start and tile look-up 2.5, first data, joining. 2 x 131072
-// tokens, 32 query heads: 56 us (floor 44); 32 ragged sequences of up to 8192: 46 us (33). With 9 to
-// 16 heads to a KV head registers leave two warps to a scheduler, which wait for their own
-// instructions: 96 ragged sequences 35 us (floor 10.6), 37% of issue slots used.
-// The unit form against the list's, 32 query and 8 KV heads: 8 x 2048 tokens 10.6 us (12.8),
-// 8 x 4096 15.6 (18.3), and one launch for the host to make, 2.8 us (4.3).
+// Measured (calls in a graph, inputs in turn, more of them than L2 holds). Full SMs read at the rate of
+// a copy: 2 x 262144 more tokens of 8 heads of 128 channels at 6.6 TB/s. What a call costs beside that
+// is about 11 us: start and tile look-up 2.5, first data, joining. 2 x 131072 tokens, 32 query heads:
+// 56 us (floor 44); 32 ragged sequences of up to 8192: 46 us (33). With 9 to 16 heads to a KV head
+// registers leave two warps to a scheduler, which wait for their own instructions: 96 ragged sequences
+// 36 us (floor 10.6), 38% of issue slots used. Float32 queries have three and two products where
+// bfloat16 ones have one: 32 x 4096 tokens 51 us (34; floor 22).
+// The unit form against the list's, 32 query and 8 KV heads: 8 x 2048 tokens 11.8 us (14.1),
+// 8 x 4096 15.9 (18.4), and one launch for the host to make, 2.8 us (4.3). It is chosen by what the
+// block table has room for, so short sequences in a wide table take the list.
+// The list costs every warp, and every CTA that joins, a look at all lengths, 32 at a time: nothing at
+// a hundred sequences, most of the time at thousands of short ones (4096 x 64 tokens of one head 525 us).
 
 #include <algorithm>
 #include <type_traits>

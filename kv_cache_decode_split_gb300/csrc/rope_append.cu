@@ -17,8 +17,10 @@
 // data is requested before the token's sequence, length, page and table row are looked up, which
 // is a chain of dependent reads. Measured: one token of each of 32 sequences, 32 query and 8 KV
 // heads of 128 bf16 channels, 1.9 us (2.3 into 4 bits); 9 prompts, 400 MB in all, 61 us, 98% of the
-// rate of a copy (into 4 bits, with the stored values handed back, 70 us, 88%: the codes'
-// instructions).
+// rate of a copy (into 4 bits, with the stored values handed back, 71 us, 88%). What bounds the 4-bit
+// form is the codes' instructions for each key and value row: with as many KV heads as query heads
+// (8 and 8 of 128 bf16 channels, 365 MB) it takes 80 us, two thirds of the rate of a copy, the other
+// form 51 us, 97%; 5 and 5 of 64, where a step of a warp has 8 row slots, 90 and 62 us, 37% and 50%.
 
 #include <algorithm>
 
@@ -524,6 +526,8 @@ int launch_type(const RopeAppendParams& p, cudaStream_t stream) {
     // longer) on. 12000 tokens of 1 head of 128 5.0 us (14.4 otherwise), into 4 bits 7.6 (23.1); 3000 of
     // 2 heads of 128 bf16 4.4 (5.2), float32 7.6 (7.1); 8000 of 1 head of 64 float32 8.3 (11.9).
     if ((sizeof(T) == 2 ? 2 : 4) * p.Hkv <= teams) return launch_few<T, D, kQ4>(p, stream);
+    // (Registers are held to 64 and 80 a thread for the warps that the loads need; the 4-bit kernels then
+    // spill 56 to 72 bytes of a thread in bf16, 20 to 32 in float32.)
     if constexpr (sizeof(T) == 2)
         return launch_rows<T, D, kQ4, 2, 4>(p, 2, stream);
     else  // (a float32 row is two bf16 ones)
