@@ -52,8 +52,9 @@ class _NotBuilt:
 
 try:
     from . import _binding  # (after the library that it calls)
-    if _binding.built_for != torch.__version__:  # it may load all the same, and misread tensors
-        raise ImportError(f"built for PyTorch {_binding.built_for}, this is {torch.__version__}")
+    _for = getattr(_binding, "built_for", None)
+    if _for != torch.__version__:  # it may load all the same, and misread tensors
+        raise ImportError(f"built for PyTorch {_for}, this is {torch.__version__}")
     _binding.set_error(KvdError)
 except ImportError as e:
     _binding = _NotBuilt(e)

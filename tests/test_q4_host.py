@@ -163,7 +163,7 @@ def _elsewhere(tmp_path, code, *without):
     """Run code where the package is a copy without some of its files: (exit code, output)."""
     src = os.path.join(ROOT, "kv_cache_decode_split_gb300")
     dst = tmp_path / "kv_cache_decode_split_gb300"
-    dst.mkdir()
+    dst.mkdir(exist_ok=True)
     for n in os.listdir(src):
         if n.endswith((".py", ".so")) and n not in without:
             shutil.copy(os.path.join(src, n), dst / n)
@@ -272,3 +272,13 @@ def test_no_unit_has_more_tiles_than_the_plan_counts(kvd, tmp_path):
             one = r or w == 0 or min(s, L) >= lo
             tiles.append(count(0, min(L, w + s) if r else L) if one else count(0, min(s, L)) + count(lo, L))
         assert max(tiles) <= most <= max(tiles) + 1, (n, w, s, r)
+
+
+def test_a_module_without_a_version_is_refused(kvd, tmp_path):
+    # one that an earlier build left
+    (tmp_path / "kv_cache_decode_split_gb300").mkdir()
+    (tmp_path / "kv_cache_decode_split_gb300" / "_binding.py").write_text("set_error = print\n")
+    rc, out = _elsewhere(tmp_path, CALLS_ALL.format(first=""), "_binding.so")
+    assert rc == 0, out
+    for n in OWN:
+        assert f"{n} ImportError _binding.so is missing or not built for this PyTorch" in out
