@@ -41,6 +41,12 @@
  *    ragged batch of many) rotated by their positions and written into a paged or
  *    rolling cache, in the tensors' type or in 4 bits; attn_decode_gqa_q4:
  *    single-token attention over the 4-bit cache.
+ *  - attn_prefill_gqa, attn_prefill_gqa_paged: causal grouped-query attention of many new
+ *    tokens of each sequence (whole prompts packed one behind the other; chunks or draft
+ *    tokens over their paged cache). "Overview of Attention Mechanism", GQA / Code and the
+ *    causal mask; windows and sinks as attn_decode_swa_sink.
+ *  - kvd_cache_read, kvd_cache_read_q4: the tokens that a paged, rolling or 4-bit cache
+ *    holds, as packed rows (the inverse of the appends).
  *  - quest_page_minmax, quest_select_pages, attn_decode_quest (and the split
  *    quest_page_bounds + attn_decode_quest_from_bounds): query-aware page
  *    selection. "Long context, KV eviction and sparse attention", Sparse attention
@@ -115,7 +121,8 @@ enum kvd_op {
     KVD_OP_MLA = 2,
     KVD_OP_DSA_TOPK = 3,
     KVD_OP_MLA_SPARSE = 4,
-    KVD_OP_GQA_Q4 = 5
+    KVD_OP_GQA_Q4 = 5,
+    KVD_OP_PREFILL = 6
 };
 
 /*
@@ -334,6 +341,93 @@ int attn_decode_gqa_q4(const void *q, const void *k_pool, const void *v_pool,
                        int max_pages, int num_pages, float scale, int dtype, int window,
                        int n_sink_tokens, int ring, const float *sink_logit, void *ws,
                        size_t ws_bytes, int *err, cudaStream_t stream);
+
+/*
+ * Causal attention of many new tokens of each sequence. T rows of q are the new tokens of B
+ * sequences in order: rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 (device, int32 [B + 1],
+ * ascending from 0) belong to sequence b, which may have none. Its keys and values are rows
+ * cu_seqlens_k[b] .. cu_seqlens_k[b+1] - 1 of k and v, in the order of positions and with the new
+ * tokens' own at their end: of n_b new tokens and L_b keys the i-th new token has position
+ * t = L_b - n_b + i and sees the positions up to its own (window > 0: of them the last `window`, its
+ * own among them, and the first n_sink_tokens). A row that sees nothing (fewer keys than new tokens)
+ * gets out 0 and lse -inf (the sink's logit with a learned sink). Rows of q and out from
+ * cu_seqlens_q[B] on are padding: they are neither used nor written.
+ *  q       [T, Hq, D], k and v [Tk, Hkv, D]: dense heads; their tokens lie q_stride, k_stride,
+ *          v_stride elements apart (multiples of 16 bytes, at least one token's heads), so they may
+ *          be slices of one projection's output
+ *  out     [T, Hq, D] dense; lse_out [T, Hq] float32, nullable: natural-log normaliser. Neither may
+ *          overlap an input.
+ *  sink_logit [Hq] float32, nullable: as attn_decode_swa_sink
+ *  ws      kvd_workspace_size(KVD_OP_PREFILL, B, Hq, Hkv, D, ...) bytes (the other arguments do not
+ *          count), 16-byte aligned, of any content: nothing is kept in it from call to call. Calls
+ *          that share it must be ordered on the device.
+ *  err     int32 on the device, nullable, never cleared: receives KVD_ERR_DEVICE_OOB for offsets that
+ *          do not ascend or leave T or Tk (nothing of such a sequence is written)
+ * Scores, softmax statistics and sums are held in float32; with bfloat16 inputs the weights of the
+ * value product are bfloat16 numbers (8 bits, as its operands must be of one type), their sum is not
+ * rounded. A value that is NaN or infinite reaches the rows that see it alone. The result does not
+ * depend on timing.
+ * Supported: D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, dtype KVD_BF16 or KVD_F32; T == 0 does
+ * nothing.
+ */
+int attn_prefill_gqa(const void *q, const void *k, const void *v, const int32_t *cu_seqlens_q,
+                     const int32_t *cu_seqlens_k, void *out, float *lse_out, int B, int T, int Tk,
+                     int Hq, int Hkv, int D, long long q_stride, long long k_stride,
+                     long long v_stride, float scale, int dtype, int window, int n_sink_tokens,
+                     const float *sink_logit, void *ws, size_t ws_bytes, int *err,
+                     cudaStream_t stream);
+
+/*
+ * attn_prefill_gqa over a paged cache that holds the new tokens already (kvd_rope_append writes
+ * them): chunks of a prompt, draft tokens to be verified, or, with cu_seqlens null, one token of each
+ * sequence (T == B; as attn_decode_gqa_paged then). k_pool and v_pool [num_pages, Hkv, page_size, D],
+ * block_table and seq_lens (the lengths WITH the new tokens; 0 is allowed) as in
+ * attn_decode_gqa_paged. A rolling cache has lost keys that a chunk's first tokens see: read it
+ * before the append (kvd_cache_read) and use attn_prefill_gqa.
+ *  err also receives KVD_ERR_DEVICE_OOB for a length below the number of new tokens (the leading ones
+ *  see nothing) or above the table's capacity (clamped) and for a page id out of range (clamped).
+ * Everything else as attn_prefill_gqa; page_size a power of two in [16, 256].
+ */
+int attn_prefill_gqa_paged(const void *q, const void *k_pool, const void *v_pool,
+                           const int32_t *block_table, const int32_t *seq_lens,
+                           const int32_t *cu_seqlens, void *out, float *lse_out, int B, int T,
+                           int Hq, int Hkv, int D, long long q_stride, int page_size,
+                           int max_pages, int num_pages, float scale, int dtype, int window,
+                           int n_sink_tokens, const float *sink_logit, void *ws, size_t ws_bytes,
+                           int *err, cudaStream_t stream);
+
+/*
+ * What a cache holds, as packed rows. Sequence b of length seq_lens[b] (0 is allowed) holds, paged
+ * (window == 0), its positions 0 .. L_b - 1, or, rolling, its first n_sink and its last `window`
+ * (as kvd_cache_append and kvd_rope_append write them; lengths are unbounded). The j-th of these, in
+ * the order of positions, goes to row cu_seqlens[b] + j of k_out and v_out (cu_seqlens: device, int32
+ * [B + 1], ascending from 0); rows of a sequence past what it holds are left as they were.
+ *  k_pool, v_pool [num_pages, Hkv, page_size, D] dtype
+ *  k_out, v_out [T, Hkv, D] dtype: dense heads, tokens k_stride, v_stride elements apart (as q_stride
+ *          in attn_prefill_gqa); neither may overlap a pool or the other's rows
+ *  err     int32 on the device, nullable, never cleared: receives KVD_ERR_DEVICE_OOB for offsets that
+ *          do not ascend or leave T, a length below 0 or (paged) above the table's capacity, a
+ *          sequence that holds more than it has rows (nothing of such a sequence is written) or a
+ *          page id out of range (its rows are not written)
+ * Bytes are copied unchanged. Supported: D in {64, 128}, dtype KVD_BF16 or KVD_F32, page_size a power
+ * of two in [16, 256]; T == 0 does nothing. No workspace; one launch.
+ */
+int kvd_cache_read(const void *k_pool, const void *v_pool, const int32_t *block_table,
+                   const int32_t *seq_lens, const int32_t *cu_seqlens, void *k_out, void *v_out,
+                   int B, int T, int Hkv, int D, long long k_stride, long long v_stride,
+                   int page_size, int max_pages, int num_pages, int dtype, int window, int n_sink,
+                   int *err, cudaStream_t stream);
+
+/*
+ * kvd_cache_read of a 4-bit cache (pools as kvd_rope_append_q4 fills them): the values that it stands
+ * for, s * code + b, rounded once to dtype: for tokens that kvd_rope_append_q4 wrote, the rows that
+ * it gave back as k_out and v_out.
+ */
+int kvd_cache_read_q4(const void *k_pool, const void *v_pool, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens, void *k_out, void *v_out,
+                      int B, int T, int Hkv, int D, long long k_stride, long long v_stride,
+                      int page_size, int max_pages, int num_pages, int dtype, int window,
+                      int n_sink, int *err, cudaStream_t stream);
 
 /*
  * Quest page summaries ("Long context, KV eviction and sparse attention", Sparse attention:

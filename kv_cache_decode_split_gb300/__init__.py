@@ -21,6 +21,9 @@ Operations:
   rope_append, rope_append_q4   new tokens rotated by position into a paged or rolling cache,
                           in the tensors' type or in 4 bits
   attn_decode_gqa_q4      attention (dense, window + sinks, rolling) over the 4-bit cache
+  attn_prefill_gqa, attn_prefill_gqa_paged   causal attention of many new tokens of a sequence:
+                          packed prompts, or chunks and draft tokens over their paged cache
+  cache_read, cache_read_q4   the tokens that a paged, rolling or 4-bit cache holds, as rows
   attn_decode_swa_ring    sliding window + sinks over a rolling cache
   attn_decode_swa_ring_append   cache_append of the newest token, then attn_decode_swa_ring
   quest_page_minmax, quest_select_pages, attn_decode_quest   Quest page selection
@@ -64,6 +67,7 @@ __all__ = [
     "dsa_indexer_topk_fp8", "quantize_e4m3_rows", "dsa_indexer_cache_append_fp8",
     "delta_decode_step", "attn_decode_swa_ring", "attn_decode_swa_ring_append", "cache_append",
     "rope_append", "rope_append_q4", "attn_decode_gqa_q4", "q4_page_bytes", "q4_pool",
+    "attn_prefill_gqa", "attn_prefill_gqa_paged", "cache_read", "cache_read_q4",
     "quest_page_minmax",
     "quest_select_pages", "attn_decode_quest", "quest_page_bounds",
     "attn_decode_quest_from_bounds",
@@ -406,6 +410,88 @@ def attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window=0, n_sin
     return _binding.attn_decode_gqa_q4(q, k_pool, v_pool, block_table, seq_lens, window,
                                        n_sink_tokens, ring, sink_logit, scale, out, lse_out,
                                        workspace, err, handle)
+
+
+def _prefill(paged, q, k, v, block_table, lens, cu_seqlens_q, window, n_sink_tokens, sink_logit,
+             scale, out, lse_out, workspace, err, stream):
+    handle = None if stream is None else _own_stream(stream, q, "q")
+    if isinstance(workspace, Workspace) or (workspace is None and stream is not None):
+        if not all(isinstance(t, torch.Tensor) and t.dim() == n
+                   for t, n in ((q, 3), (k, 4 if paged else 3))):
+            raise ValueError(f"q and {'k_pool' if paged else 'k'} must have 3 and "
+                             f"{4 if paged else 3} dims")
+        nbytes = max(1, kvd_workspace_size("prefill", 1, q.shape[1], k.shape[1], q.shape[2]))
+        if workspace is None:
+            workspace = _empty_on(stream, nbytes, q, torch.uint8)
+        else:  # (it may have to be filled with zeros: on the stream of the call)
+            with torch.cuda.stream(stream):
+                workspace = workspace.get(nbytes, "prefill")
+    if stream is not None and out is None:
+        out = _empty_on(stream, q.shape, q)
+    return _binding.attn_prefill(paged, q, k, v, block_table, lens, cu_seqlens_q, window,
+                                 n_sink_tokens, sink_logit, scale, out, lse_out, workspace, err,
+                                 handle)
+
+
+def attn_prefill_gqa(q, k, v, cu_seqlens_q, cu_seqlens_k=None, window=0, n_sink_tokens=0,
+                     sink_logit=None, scale=None, out=None, lse_out=None, workspace=None, err=None,
+                     stream=None):
+    """Causal attention of the new tokens q [T, Hq, D] of B sequences over their packed keys and
+    values k, v [Tk, Hkv, D] (bfloat16 or float32; dense heads, any 16-byte stride between tokens, so
+    slices of one projection's output too).
+
+    Sequence b's new tokens are rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1, its keys rows
+    cu_seqlens_k[b] .. cu_seqlens_k[b+1] - 1 (int32 [B + 1], on the device; None: the same rows), with
+    the new tokens' own at their end: a prompt, or the end of one behind a prefix (read back with
+    cache_read). A token sees the keys up to its own; with window > 0 of them the last window and the
+    first n_sink_tokens. sink_logit [Hq] float32: a learned logit in each head's denominator.
+    lse_out [T, Hq] float32 receives the natural-log normaliser. Rows that see nothing are zeros; rows
+    behind the last sequence are padding and stay as they were.
+
+    workspace: a uint8 tensor of kvd_workspace_size("prefill", B, Hq, Hkv, D) bytes or a Workspace, of
+    any content (calls that share one must be ordered); None takes fresh memory from PyTorch's
+    allocator, so calls on several streams and captured graphs never share it. Bad offsets are recorded
+    in err (int32 [1]) and nothing of such a sequence is written.
+    """
+    return _prefill(False, q, k, v, None, cu_seqlens_q if cu_seqlens_k is None else cu_seqlens_k,
+                    cu_seqlens_q, window, n_sink_tokens, sink_logit, scale, out, lse_out, workspace,
+                    err, stream)
+
+
+def attn_prefill_gqa_paged(q, k_pool, v_pool, block_table, seq_lens, cu_seqlens=None, window=0,
+                           n_sink_tokens=0, sink_logit=None, scale=None, out=None, lse_out=None,
+                           workspace=None, err=None, stream=None):
+    """attn_prefill_gqa over a paged cache [num_pages, Hkv, P, D] that holds the new tokens already
+    (rope_append writes them): chunks of a prompt, draft tokens, or, with cu_seqlens None, one token of
+    each sequence. seq_lens [B]: lengths with the new tokens. A bad length or page id is recorded in
+    err and clamped. For a rolling cache read it (cache_read) before the append and use
+    attn_prefill_gqa."""
+    return _prefill(True, q, k_pool, v_pool, block_table, seq_lens, cu_seqlens, window,
+                    n_sink_tokens, sink_logit, scale, out, lse_out, workspace, err, stream)
+
+
+def cache_read(k_pool, v_pool, block_table, seq_lens, cu_seqlens, k_out, v_out, window=0, n_sink=0,
+               err=None, stream=None):
+    """The tokens that a paged (or, window > 0, rolling) cache [num_pages, Hkv, P, D] holds, as packed
+    rows: the j-th token that sequence b of length seq_lens[b] holds (rolling: its first n_sink, then its
+    last window) goes to row cu_seqlens[b] + j of k_out and v_out [T, Hkv, D] (dense heads, any 16-byte
+    stride between tokens), which are returned. Rows that a sequence does not fill stay as they were. A
+    bad length, offset or page id, or more tokens than rows, is recorded in err (int32 [1]) and not
+    written."""
+    handle = None if stream is None else _own_stream(stream, k_out, "k_out")
+    _binding.cache_read(False, k_pool, v_pool, block_table, seq_lens, cu_seqlens, k_out, v_out, window,
+                        n_sink, err, handle)
+    return k_out, v_out
+
+
+def cache_read_q4(k_pool, v_pool, block_table, seq_lens, cu_seqlens, k_out, v_out, window=0, n_sink=0,
+                  err=None, stream=None):
+    """cache_read of a 4-bit cache (uint8 pools of q4_pool(), as rope_append_q4 fills them): the values
+    that it stands for, rounded to the type of k_out and v_out."""
+    handle = None if stream is None else _own_stream(stream, k_out, "k_out")
+    _binding.cache_read(True, k_pool, v_pool, block_table, seq_lens, cu_seqlens, k_out, v_out, window,
+                        n_sink, err, handle)
+    return k_out, v_out
 
 
 def _err(err, device):

@@ -28,6 +28,10 @@ EXPORTS = (
     "kvd_rope_append_q4",
     "kvd_q4_page_bytes",
     "attn_decode_gqa_q4",
+    "attn_prefill_gqa",
+    "attn_prefill_gqa_paged",
+    "kvd_cache_read",
+    "kvd_cache_read_q4",
     "quest_page_minmax",
     "quest_select_pages",
     "attn_decode_quest",
@@ -45,7 +49,7 @@ STATUS = {
     0: "KVD_OK", -1: "KVD_ERR_INVALID_ARG", -2: "KVD_ERR_UNSUPPORTED", -3: "KVD_ERR_CUDA",
     -4: "KVD_ERR_TIMEOUT", -5: "KVD_ERR_WORKSPACE_TOO_SMALL", -6: "KVD_ERR_DEVICE_OOB", -7: "KVD_ERR_DEVICE_STATE",
 }
-OP = {"gqa": 0, "swa": 1, "mla": 2, "dsa_topk": 3, "mla_sparse": 4, "gqa_q4": 5}
+OP = {"gqa": 0, "swa": 1, "mla": 2, "dsa_topk": 3, "mla_sparse": 4, "gqa_q4": 5, "prefill": 6}
 OPTION = {"pdl": 0, "gqa_chunk": 1, "mla_min_tiles": 2, "wait_timeout_test": 3,
           "gqa_cluster": 4}
 
@@ -83,6 +87,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kvd_q4_page_bytes.argtypes = [I, I]
     lib.kvd_q4_page_bytes.restype = Z
     lib.attn_decode_gqa_q4.argtypes = [P] * 7 + [I] * 7 + [F] + [I] * 4 + [P, P, Z, P, P]
+    lib.attn_prefill_gqa.argtypes = [P] * 7 + [I] * 6 + [LL] * 3 + [F] + [I] * 3 + [P, P, Z, P, P]
+    lib.attn_prefill_gqa_paged.argtypes = ([P] * 8 + [I] * 5 + [LL] + [I] * 3 + [F] + [I] * 3 +
+                                           [P, P, Z, P, P])
+    lib.kvd_cache_read.argtypes = [P] * 7 + [I] * 4 + [LL] * 2 + [I] * 6 + [P, P]
+    lib.kvd_cache_read_q4.argtypes = lib.kvd_cache_read.argtypes
     lib.quest_page_minmax.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P]
     lib.quest_select_pages.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P]
     lib.attn_decode_quest.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P,
@@ -98,7 +107,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "dsa_indexer_cache_append_fp8", "kvd_delta_decode_step",
                  "attn_decode_swa_ring", "attn_decode_swa_ring_append", "kvd_cache_append",
                  "kvd_rope_append", "kvd_rope_append_q4", "attn_decode_gqa_q4",
-                 "quest_page_minmax",
+                 "attn_prefill_gqa", "attn_prefill_gqa_paged", "kvd_cache_read",
+                 "kvd_cache_read_q4", "quest_page_minmax",
                  "quest_select_pages", "attn_decode_quest", "quest_page_bounds",
                  "attn_decode_quest_from_bounds", "dsa_topk",
                  "attn_decode_mla_sparse",

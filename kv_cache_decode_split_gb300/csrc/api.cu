@@ -691,6 +691,211 @@ int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
     return q4_launch(plan, p, D, dtype, stream);
 }
 
+// What both prefill calls check and fill in; k and v rows or pools.
+static int prefill_common(PrefillParams& p, const void* q, const void* k, const void* v, void* out,
+                          float* lse_out, int B, int T, int Hq, int Hkv, int D,
+                          long long q_stride, float scale, int dtype, int window,
+                          int n_sink_tokens, const float* sink_logit, const void* ws,
+                          size_t ws_bytes, int* err) {
+    if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || window < 0 || n_sink_tokens < 0 ||
+        (window == 0 && n_sink_tokens != 0) || !std::isfinite(scale))
+        return KVD_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return KVD_ERR_UNSUPPORTED;
+    if (dtype != KVD_F32 && dtype != KVD_BF16) return KVD_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 128 || Hkv > 65535 || T >= (1 << 30)) return KVD_ERR_UNSUPPORTED;
+    const size_t need = kvd_workspace_size(KVD_OP_PREFILL, B, Hq, Hkv, D, 1, 0, 0, 0);
+    if (need == 0) return KVD_ERR_UNSUPPORTED;
+    if (T == 0) return KVD_OK;
+    const int e = dtype == KVD_F32 ? 4 : 2;
+    const long long row = (long long)Hq * D;
+    if (!q || !out || q_stride < row || q_stride * e % 16 != 0 || q_stride >= (1LL << 36))
+        return KVD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !ws ||
+        !aligned16(ws) || (reinterpret_cast<uintptr_t>(lse_out) & 3) ||
+        (reinterpret_cast<uintptr_t>(sink_logit) & 3) || (reinterpret_cast<uintptr_t>(err) & 3))
+        return KVD_ERR_INVALID_ARG;
+    if (ws_bytes < need) return KVD_ERR_WORKSPACE_TOO_SMALL;
+    const long long q_in = ((T - 1) * q_stride + row) * e;
+    if (overlap(out, T * row * e, q, q_in) || overlap(lse_out, (long long)T * Hq * 4, q, q_in) ||
+        overlap(lse_out, (long long)T * Hq * 4, out, T * row * e))
+        return KVD_ERR_INVALID_ARG;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.out = out;
+    p.lse_out = lse_out;
+    p.sink_logit = sink_logit;
+    p.err = err;
+    p.q_stride = q_stride;
+    p.B = B;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.window = window;
+    p.n_sink = n_sink_tokens;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return KVD_OK;
+}
+
+int attn_prefill_gqa(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                     const int32_t* cu_seqlens_k, void* out, float* lse_out, int B, int T, int Tk,
+                     int Hq, int Hkv, int D, long long q_stride, long long k_stride,
+                     long long v_stride, float scale, int dtype, int window, int n_sink_tokens,
+                     const float* sink_logit, void* ws, size_t ws_bytes, int* err,
+                     cudaStream_t stream) {
+    PrefillParams p;
+    std::memset(&p, 0, sizeof p);
+    const int st = prefill_common(p, q, k, v, out, lse_out, B, T, Hq, Hkv, D, q_stride, scale,
+                                  dtype, window, n_sink_tokens, sink_logit, ws, ws_bytes, err);
+    if (st != KVD_OK) return st;
+    if (Tk < 0) return KVD_ERR_INVALID_ARG;
+    if (Tk >= (1 << 30)) return KVD_ERR_UNSUPPORTED;
+    if (T == 0) return KVD_OK;
+    if (!cu_seqlens_q || !cu_seqlens_k || (Tk > 0 && (!k || !v)) ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3) ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens_k) & 3))
+        return KVD_ERR_INVALID_ARG;
+    const int e = dtype == KVD_F32 ? 4 : 2;
+    const long long row = (long long)Hkv * D;
+    if (k_stride < row || v_stride < row || k_stride * e % 16 != 0 || v_stride * e % 16 != 0 ||
+        k_stride >= (1LL << 36) || v_stride >= (1LL << 36))
+        return KVD_ERR_INVALID_ARG;
+    const long long n_out = (long long)T * Hq * D * e, n_lse = (long long)T * Hq * 4;
+    const void* in[2] = {k, v};
+    for (int i = 0; i < 2 && Tk > 0; ++i) {
+        const long long n = ((Tk - 1) * (i ? v_stride : k_stride) + row) * e;
+        if (overlap(out, n_out, in[i], n) || overlap(lse_out, n_lse, in[i], n))
+            return KVD_ERR_INVALID_ARG;
+    }
+    p.cu_q = cu_seqlens_q;
+    p.cu_k = cu_seqlens_k;
+    p.Tk = Tk;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    return prefill_launch(p, D, dtype, stream);
+}
+
+int attn_prefill_gqa_paged(const void* q, const void* k_pool, const void* v_pool,
+                           const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* cu_seqlens, void* out, float* lse_out, int B, int T,
+                           int Hq, int Hkv, int D, long long q_stride, int page_size,
+                           int max_pages, int num_pages, float scale, int dtype, int window,
+                           int n_sink_tokens, const float* sink_logit, void* ws, size_t ws_bytes,
+                           int* err, cudaStream_t stream) {
+    PrefillParams p;
+    std::memset(&p, 0, sizeof p);
+    const int st = prefill_common(p, q, k_pool, v_pool, out, lse_out, B, T, Hq, Hkv, D, q_stride,
+                                  scale, dtype, window, n_sink_tokens, sink_logit, ws, ws_bytes,
+                                  err);
+    if (st != KVD_OK) return st;
+    if (max_pages < 1 || num_pages < 1 || (!cu_seqlens && T != B)) return KVD_ERR_INVALID_ARG;
+    if (!pow2(page_size) || page_size < 16 || page_size > 256) return KVD_ERR_UNSUPPORTED;
+    if ((long long)num_pages * Hkv * page_size >= (1LL << 31)) return KVD_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size >= (1LL << 30)) return KVD_ERR_UNSUPPORTED;
+    if (T == 0) return KVD_OK;
+    if (!k_pool || !v_pool || !block_table || !seq_lens ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens) & 3) ||
+        (reinterpret_cast<uintptr_t>(block_table) & 3) ||
+        (reinterpret_cast<uintptr_t>(seq_lens) & 3))
+        return KVD_ERR_INVALID_ARG;
+    const long long e = dtype == KVD_F32 ? 4 : 2, n_out = (long long)T * Hq * D * e,
+                    n_lse = (long long)T * Hq * 4, n_pool = (long long)num_pages * Hkv * page_size * D * e;
+    if (overlap(out, n_out, k_pool, n_pool) || overlap(out, n_out, v_pool, n_pool) ||
+        overlap(lse_out, n_lse, k_pool, n_pool) || overlap(lse_out, n_lse, v_pool, n_pool))
+        return KVD_ERR_INVALID_ARG;
+    p.cu_q = cu_seqlens;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.page_shift = __builtin_ctz(page_size);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    return prefill_launch(p, D, dtype, stream);
+}
+
+static int cache_read(bool q4, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                      const int32_t* seq_lens, const int32_t* cu_seqlens, void* k_out, void* v_out,
+                      int B, int T, int Hkv, int D, long long k_stride, long long v_stride,
+                      int page_size, int max_pages, int num_pages, int dtype, int window,
+                      int n_sink, int* err, cudaStream_t stream) {
+    if (B < 1 || T < 0 || Hkv < 1 || max_pages < 1 || num_pages < 1 || window < 0 || n_sink < 0 ||
+        (window == 0 && n_sink != 0))
+        return KVD_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return KVD_ERR_UNSUPPORTED;
+    if (!pow2(page_size) || page_size < 16 || page_size > 256) return KVD_ERR_UNSUPPORTED;
+    if (dtype != KVD_F32 && dtype != KVD_BF16) return KVD_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size >= (1LL << 30)) return KVD_ERR_UNSUPPORTED;
+    if (Hkv > 65535 || T >= (1 << 30) || B >= (1 << 30)) return KVD_ERR_UNSUPPORTED;
+    if (window > 0 && (long long)n_sink + window > (long long)max_pages * page_size)
+        return KVD_ERR_INVALID_ARG;
+    if (T == 0) return KVD_OK;
+    const int e = dtype == KVD_F32 ? 4 : 2;
+    const long long row = (long long)Hkv * D;
+    if (!k_pool || !v_pool || !block_table || !seq_lens || !cu_seqlens || !k_out || !v_out ||
+        k_stride < row || v_stride < row || k_stride * e % 16 != 0 || v_stride * e % 16 != 0 ||
+        k_stride >= (1LL << 36) || v_stride >= (1LL << 36))
+        return KVD_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) || !aligned16(v_out) ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens) & 3) ||
+        (reinterpret_cast<uintptr_t>(block_table) & 3) ||
+        (reinterpret_cast<uintptr_t>(seq_lens) & 3) || (reinterpret_cast<uintptr_t>(err) & 3))
+        return KVD_ERR_INVALID_ARG;
+    const long long n_k = ((T - 1) * k_stride + row) * e, n_v = ((T - 1) * v_stride + row) * e;
+    const long long n_pool = (long long)num_pages * Hkv *
+                             (q4 ? (long long)kvd_q4_page_bytes(page_size, D)
+                                 : (long long)page_size * D * e);
+    if (overlap(k_out, n_k, k_pool, n_pool) || overlap(k_out, n_k, v_pool, n_pool) ||
+        overlap(v_out, n_v, k_pool, n_pool) || overlap(v_out, n_v, v_pool, n_pool))
+        return KVD_ERR_INVALID_ARG;
+    // the two outputs may be slices of one buffer: then a row of one lies between rows of the other
+    if (overlap(k_out, n_k, v_out, n_v)) {
+        const long long apart = (static_cast<const char*>(v_out) - static_cast<const char*>(k_out)) / e;
+        const long long off = ((apart % k_stride) + k_stride) % k_stride;
+        if (k_stride != v_stride || off < row || off + row > k_stride) return KVD_ERR_INVALID_ARG;
+    }
+    CacheReadParams p;
+    std::memset(&p, 0, sizeof p);
+    p.pool[0] = k_pool;
+    p.pool[1] = v_pool;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.cu_seqlens = cu_seqlens;
+    p.out[0] = k_out;
+    p.out[1] = v_out;
+    p.stride[0] = q4 ? k_stride : k_stride * e / 16;
+    p.stride[1] = q4 ? v_stride : v_stride * e / 16;
+    p.err = err;
+    p.B = B;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.page_shift = __builtin_ctz(page_size);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.window = window;
+    p.n_sink = n_sink;
+    return cache_read_launch(p, q4, D, dtype, stream);
+}
+
+int kvd_cache_read(const void* k_pool, const void* v_pool, const int32_t* block_table,
+                   const int32_t* seq_lens, const int32_t* cu_seqlens, void* k_out, void* v_out,
+                   int B, int T, int Hkv, int D, long long k_stride, long long v_stride,
+                   int page_size, int max_pages, int num_pages, int dtype, int window, int n_sink,
+                   int* err, cudaStream_t stream) {
+    return cache_read(false, k_pool, v_pool, block_table, seq_lens, cu_seqlens, k_out, v_out, B, T,
+                      Hkv, D, k_stride, v_stride, page_size, max_pages, num_pages, dtype, window,
+                      n_sink, err, stream);
+}
+
+int kvd_cache_read_q4(const void* k_pool, const void* v_pool, const int32_t* block_table,
+                      const int32_t* seq_lens, const int32_t* cu_seqlens, void* k_out, void* v_out,
+                      int B, int T, int Hkv, int D, long long k_stride, long long v_stride,
+                      int page_size, int max_pages, int num_pages, int dtype, int window,
+                      int n_sink, int* err, cudaStream_t stream) {
+    return cache_read(true, k_pool, v_pool, block_table, seq_lens, cu_seqlens, k_out, v_out, B, T,
+                      Hkv, D, k_stride, v_stride, page_size, max_pages, num_pages, dtype, window,
+                      n_sink, err, stream);
+}
+
 // Checks shared by the three Quest entry points.
 static int quest_common(QuestParams& qp, int B, int Hq, int Hkv, int D, int page_size,
                         int max_pages, int num_pages, int dtype, int* err) {
@@ -1086,6 +1291,10 @@ size_t kvd_workspace_size(int op, int B, int H, int Hkv, int D, int max_len, int
     }
     if (op == KVD_OP_MLA) return mla_plan(B, max_len, false).total;
     if (op == KVD_OP_MLA_SPARSE) return k >= 1 ? mla_plan(B, k, true).total : 0;
+    if (op == KVD_OP_PREFILL) {
+        if (Hkv < 1 || H % Hkv != 0 || H / Hkv > 128 || (D != 64 && D != 128)) return 0;
+        return 256;
+    }
     if (op == KVD_OP_GQA_Q4) {
         Q4Plan plan;
         if (Hkv < 1 || H % Hkv != 0 || (D != 64 && D != 128) ||

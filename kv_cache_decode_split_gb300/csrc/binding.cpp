@@ -1,4 +1,5 @@
-// binding.cpp -- the Python calls of the rotated appends and of the 4-bit attention, as a CPython module.
+// binding.cpp -- the Python calls of the rotated appends, of the 4-bit and prefill attention and of the
+// cache reads, as a CPython module.
 //
 // These calls take a few microseconds on the GPU (one decode step of an append: two), so their host
 // side counts: checking and marshalling a dozen tensors costs 8 us in Python and 4 us more through
@@ -119,6 +120,13 @@ cudaStream_t stream_of(PyObject* o, int dev) {
     const unsigned long long h = PyLong_AsUnsignedLongLong(o);
     if (PyErr_Occurred()) throw Refused{nullptr, ""};
     return reinterpret_cast<cudaStream_t>(h);
+}
+
+double scale_of(PyObject* o, int64_t D) {
+    if (o == Py_None) return 1.0 / std::sqrt(static_cast<double>(D));
+    const double scale = PyFloat_AsDouble(o);
+    if (scale == -1.0 && PyErr_Occurred()) throw Refused{nullptr, ""};
+    return scale;
 }
 
 template <typename F>
@@ -267,11 +275,7 @@ PyObject* attn_decode_gqa_q4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   mp = narrow(max_pages, "max_pages"), np = narrow(pool.size(0), "num_pages"),
                   window = integer(a[5], "window"), n_sink = integer(a[6], "n_sink_tokens");
         const int ring = truth(a[7]);
-        double scale = 1.0 / std::sqrt(static_cast<double>(D));
-        if (a[9] != Py_None) {
-            scale = PyFloat_AsDouble(a[9]);
-            if (scale == -1.0 && PyErr_Occurred()) throw Refused{nullptr, ""};
-        }
+        const double scale = scale_of(a[9], D);
         at::Tensor made, ws;
         void* out;
         if (a[10] == Py_None) {
@@ -301,6 +305,141 @@ PyObject* attn_decode_gqa_q4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// attn_prefill(paged, q, k, v, block_table, lens, cu_seqlens_q, window, n_sink_tokens, sink_logit, scale,
+//              out, lse_out, workspace, err, stream) -> out
+// paged: k, v are pools and lens is seq_lens; else block_table is None and lens is cu_seqlens_k.
+PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 16) type_error("attn_prefill takes 16 arguments");
+        const bool paged = truth(a[0]);
+        const at::Tensor& q = tensor(a[1], "q");
+        if (q.dim() != 3) value_error("q must be [T, Hq, D]");
+        const int dtype = dtype_of(q, "q");
+        const at::ScalarType dt = q.scalar_type();
+        const int dev = static_cast<int>(q.get_device());
+        const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
+        long long qs = 0, ks = 0, vs = 0;
+        const void* qp = tokens(a[1], "q", dev, dt, q.sizes(), &qs);
+        const at::Tensor& k = tensor(a[2], paged ? "k_pool" : "k");
+        if (k.dim() != (paged ? 4 : 3) || k.size(-1) != D)
+            value_error(paged ? "k_pool must be [num_pages, Hkv, page_size, D]" : "k must be [Tk, Hkv, D]");
+        const int64_t Hkv = k.size(1);
+        int64_t B;
+        const void *kp, *vp;
+        const int32_t *bt = nullptr, *lens, *cu;
+        int64_t max_pages = 0;
+        if (paged) {
+            const at::Tensor& t = tensor(a[4], "block_table");
+            if (t.dim() != 2) value_error("block_table must have 2 dims");
+            B = t.size(0);
+            max_pages = t.size(1);
+            kp = dense(a[2], "k_pool", dev, dt, k.sizes());
+            vp = dense(a[3], "v_pool", dev, dt, k.sizes());
+            bt = static_cast<const int32_t*>(dense(a[4], "block_table", dev, at::kInt, t.sizes()));
+            lens = static_cast<const int32_t*>(dense(a[5], "seq_lens", dev, at::kInt, {B}));
+            if (a[6] == Py_None && T != B)
+                value_error("without cu_seqlens there is one token of each sequence");
+            cu = static_cast<const int32_t*>(dense_or_null(a[6], "cu_seqlens", dev, at::kInt, {B + 1}));
+        } else {
+            const at::Tensor& t = tensor(a[6], "cu_seqlens_q");
+            if (t.dim() != 1 || t.size(0) < 1) value_error("cu_seqlens_q must be [B + 1]");
+            B = t.size(0) - 1;
+            kp = tokens(a[2], "k", dev, dt, k.sizes(), &ks);
+            vp = tokens(a[3], "v", dev, dt, k.sizes(), &vs);
+            cu = static_cast<const int32_t*>(dense(a[6], "cu_seqlens_q", dev, at::kInt, {B + 1}));
+            lens = static_cast<const int32_t*>(dense(a[5], "cu_seqlens_k", dev, at::kInt, {B + 1}));
+        }
+        const float* sink = static_cast<const float*>(
+            dense_or_null(a[9], "sink_logit", dev, at::kFloat, {Hq}));
+        float* lse =
+            static_cast<float*>(dense_or_null(a[12], "lse_out", dev, at::kFloat, {T, Hq}));
+        int* err = static_cast<int*>(dense_or_null(a[14], "err", dev, at::kInt, {1}));
+        const int b = narrow(B, "B"), t = narrow(T, "T"), hq = narrow(Hq, "Hq"),
+                  hkv = narrow(Hkv, "Hkv"), d = narrow(D, "D"), n0 = narrow(k.size(0), "k"),
+                  window = integer(a[7], "window"), n_sink = integer(a[8], "n_sink_tokens");
+        const float scale = static_cast<float>(scale_of(a[10], D));
+        at::Tensor made, ws;
+        void* out;
+        if (a[11] == Py_None) {
+            made = at::empty(q.sizes(), q.options());
+            out = made.data_ptr();
+        } else {
+            out = dense(a[11], "out", dev, dt, q.sizes());
+        }
+        if (a[13] == Py_None) {
+            const size_t bytes = kvd_workspace_size(KVD_OP_PREFILL, b, hq, hkv, d, 1, 0, 0, 0);
+            // (a shape that the call refuses needs none)
+            ws = at::empty({static_cast<int64_t>(bytes > 0 ? bytes : 1)}, q.options().dtype(at::kByte));
+        } else {
+            ws = tensor(a[13], "workspace");
+            dense(a[13], "workspace", dev, at::kByte, {ws.numel()});
+        }
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
+        const cudaStream_t stream = stream_of(a[15], dev);
+        int st;
+        if (paged)
+            st = attn_prefill_gqa_paged(qp, kp, vp, bt, lens, cu, out, lse, b, t, hq, hkv, d, qs,
+                                        narrow(k.size(2), "page_size"), narrow(max_pages, "max_pages"),
+                                        n0, scale, dtype, window, n_sink, sink, ws.data_ptr(),
+                                        static_cast<size_t>(ws.numel()), err, stream);
+        else
+            st = attn_prefill_gqa(qp, kp, vp, cu, lens, out, lse, b, t, n0, hq, hkv, d, qs, ks, vs,
+                                  scale, dtype, window, n_sink, sink, ws.data_ptr(),
+                                  static_cast<size_t>(ws.numel()), err, stream);
+        if (st != KVD_OK) return failed(st, paged ? "attn_prefill_gqa_paged" : "attn_prefill_gqa");
+        if (made.defined()) return THPVariable_Wrap(made);
+        return Py_NewRef(a[11]);
+    });
+}
+
+// cache_read(q4, k_pool, v_pool, block_table, seq_lens, cu_seqlens, k_out, v_out, window, n_sink, err,
+//            stream)
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 12) type_error("cache_read takes 12 arguments");
+        const bool q4 = truth(a[0]);
+        const at::Tensor& k = tensor(a[6], "k_out");
+        if (k.dim() != 3) value_error("k_out must be [T, Hkv, D]");
+        const int dtype = dtype_of(k, "k_out");
+        const at::ScalarType dt = k.scalar_type(), pool_dt = q4 ? at::kByte : dt;
+        const int dev = static_cast<int>(k.get_device());
+        const int64_t T = k.size(0), Hkv = k.size(1), D = k.size(2);
+        long long ks = 0, vs = 0;
+        void* ko = tokens(a[6], "k_out", dev, dt, k.sizes(), &ks);
+        void* vo = tokens(a[7], "v_out", dev, dt, k.sizes(), &vs);
+        const at::Tensor& pool = tensor(a[1], "k_pool");
+        if (pool.scalar_type() != pool_dt)
+            type_error(std::string("k_pool must be ") + c10::toString(pool_dt) + ", got " +
+                       c10::toString(pool.scalar_type()));
+        const int64_t P = q4 ? q4_page_size(pool, D) : pool.dim() == 4 ? pool.size(2) : 0;
+        if (P < 1 || pool.size(1) != Hkv || (!q4 && pool.size(3) != D))
+            value_error(q4 ? "k_pool must be [num_pages, Hkv, q4_page_bytes(page_size, D)]"
+                           : "k_pool must be [num_pages, Hkv, page_size, D]");
+        const at::Tensor& bt = tensor(a[3], "block_table");
+        if (bt.dim() != 2) value_error("block_table must have 2 dims");
+        const int64_t B = bt.size(0);
+        const void* kp = dense(a[1], "k_pool", dev, pool_dt, pool.sizes());
+        const void* vp = dense(a[2], "v_pool", dev, pool_dt, pool.sizes());
+        const int32_t* btp =
+            static_cast<const int32_t*>(dense(a[3], "block_table", dev, at::kInt, bt.sizes()));
+        const int32_t* sl =
+            static_cast<const int32_t*>(dense(a[4], "seq_lens", dev, at::kInt, {B}));
+        const int32_t* cu =
+            static_cast<const int32_t*>(dense(a[5], "cu_seqlens", dev, at::kInt, {B + 1}));
+        int* err = static_cast<int*>(dense_or_null(a[10], "err", dev, at::kInt, {1}));
+        const int b = narrow(B, "B"), t = narrow(T, "T"), hkv = narrow(Hkv, "Hkv"),
+                  d = narrow(D, "D"), ps = narrow(P, "page_size"),
+                  mp = narrow(bt.size(1), "max_pages"), np = narrow(pool.size(0), "num_pages"),
+                  window = integer(a[8], "window"), n_sink = integer(a[9], "n_sink");
+        const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
+        const auto call = q4 ? kvd_cache_read_q4 : kvd_cache_read;
+        const int st = call(kp, vp, btp, sl, cu, ko, vo, b, t, hkv, d, ks, vs, ps, mp, np, dtype,
+                            window, n_sink, err, stream_of(a[11], dev));
+        if (st != KVD_OK) return failed(st, q4 ? "kvd_cache_read_q4" : "kvd_cache_read");
+        Py_RETURN_NONE;
+    });
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
     Py_XSETREF(g_error, Py_NewRef(type));
     Py_RETURN_NONE;
@@ -311,6 +450,10 @@ PyMethodDef methods[] = {
      METH_FASTCALL, nullptr},
     {"attn_decode_gqa_q4",
      reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attn_decode_gqa_q4_py)),
+     METH_FASTCALL, nullptr},
+    {"attn_prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attn_prefill)),
+     METH_FASTCALL, nullptr},
+    {"cache_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(cache_read)),
      METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};

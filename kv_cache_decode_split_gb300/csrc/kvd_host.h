@@ -184,6 +184,39 @@ struct RopeAppendParams {
 int rope_append_launch(const RopeAppendParams& p, bool q4, int D, int dtype,
                        cudaStream_t stream);
 
+// Arguments of the cache read (cache_read.cu): B sequences' tokens as T packed rows.
+struct CacheReadParams {
+    const void* pool[2];       // keys, values: [num_pages, Hkv, page_size, D], or 4-bit pages
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* cu_seqlens; // [B + 1] first row of each sequence
+    void* out[2];              // [T, Hkv, D]
+    long long stride[2];       // between rows: 16-byte pieces, or (4 bits) elements
+    int* err;                  // optional
+    int B, T, Hkv, page_shift, max_pages, num_pages, window, n_sink;
+};
+int cache_read_launch(const CacheReadParams& p, bool q4, int D, int dtype, cudaStream_t stream);
+
+// Arguments of the attention of many new tokens of a sequence (prefill_simple.cu).
+struct PrefillParams {
+    const void* q;             // [T, Hq, D], tokens q_stride apart
+    const void *k, *v;         // packed [Tk, Hkv, D], or pools [num_pages, Hkv, page_size, D]
+    const int32_t* cu_q;       // [B + 1] first row of each sequence; null: one token each
+    const int32_t* cu_k;       // packed: [B + 1] first key of each sequence
+    const int32_t* block_table;  // paged (null: packed)
+    const int32_t* seq_lens;   // paged: lengths with the new tokens
+    const float* sink_logit;
+    void* out;                 // [T, Hq, D]
+    float* lse_out;            // [T, Hq], optional
+    int* err;                  // optional
+    long long q_stride, k_stride, v_stride;  // elements
+    int B, T, Tk, Hq, Hkv, G;
+    int page_shift, max_pages, num_pages;
+    int window, n_sink;        // window 0: all
+    float scale_log2;
+};
+int prefill_launch(const PrefillParams& p, int D, int dtype, cudaStream_t stream);
+
 // Arguments of the attention over a 4-bit cache (gqa_q4_decode.cu).
 struct Q4Params {
     const void* q;

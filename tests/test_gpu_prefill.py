@@ -1,0 +1,383 @@
+"""GPU: causal attention of many new tokens of each sequence, packed and over a paged cache, against the
+float64 definition (tests/prefill_reference.py, which derives each output's bound)."""
+import math
+
+import pytest
+import torch
+
+from tests import prefill_reference as R
+from tests import q4_reference as Q
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def kvd():
+    import kv_cache_decode_split_gb300 as m
+    return m
+
+
+def cu(n):
+    return torch.tensor([0] + list(torch.tensor(list(n)).cumsum(0)), dtype=I32, device=DEV)
+
+
+class Case:
+    """new[b] new tokens of sequence b, lens[b] keys with them."""
+
+    def __init__(self, new, lens, Hq, Hkv, D, dtype=BF, window=0, n_sink=0, learned=False, seed=0,
+                 scale=None, qscale=1.0, pad=0):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+        self.new, self.lens, self.Hkv, self.D, self.dtype, self.pad = list(new), list(lens), Hkv, D, dtype, pad
+        self.window, self.n_sink = window, n_sink
+        self.scale = 1 / math.sqrt(D) if scale is None else scale
+        self.q = (rnd(sum(new) + pad, Hq, D) * qscale).to(dtype)
+        self.k = [(rnd(n, Hkv, D) + 0.5 * rnd(Hkv, D)).to(dtype) for n in lens]
+        self.v = [rnd(n, Hkv, D).to(dtype) for n in lens]
+        self.sink = rnd(Hq) * 2 if learned else None
+        self.g = g
+
+    def more(self):
+        return dict(window=self.window, n_sink_tokens=self.n_sink, sink_logit=self.sink, scale=self.scale)
+
+    def packed(self, kvd, **kw):
+        k = torch.cat(self.k + [torch.full((3, self.Hkv, self.D), NAN, dtype=self.dtype, device=DEV)])
+        v = torch.cat(self.v + [torch.full((3, self.Hkv, self.D), NAN, dtype=self.dtype, device=DEV)])
+        return self.call(kvd.attn_prefill_gqa, (self.q, k, v, cu(self.new), cu(self.lens)), **kw)
+
+    def pools(self, P):
+        """Pages of the caches; whatever is not a token's row is NaN."""
+        bt, pages = Q.make_table([max(1, n) for n in self.lens], P, torch.Generator().manual_seed(P))
+        pools = []
+        for rows in (self.k, self.v):
+            pool = torch.full((pages, self.Hkv, P, self.D), NAN, dtype=self.dtype, device=DEV)
+            for b, x in enumerate(rows):
+                for i in range(0, x.shape[0], P):
+                    y = x[i:i + P]
+                    pool[int(bt[b, i // P]), :, :y.shape[0]] = y.transpose(0, 1)
+            pools.append(pool)
+        return pools + [bt.to(DEV), torch.tensor(self.lens, dtype=I32, device=DEV)]
+
+    def paged(self, kvd, P, **kw):
+        return self.call(kvd.attn_prefill_gqa_paged, (self.q, *self.pools(P), cu(self.new)), **kw)
+
+    def call(self, f, args, **kw):
+        out, lse = torch.full_like(self.q, 77.0), torch.full(self.q.shape[:2], 55.0, device=DEV)
+        err = torch.zeros(1, dtype=I32, device=DEV)
+        f(*args, **{**self.more(), **dict(out=out, lse_out=lse, err=err), **kw})
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return out, lse
+
+    def check(self, out, lse, what=""):
+        at = 0
+        for b, n in enumerate(self.new):
+            r = R.attention(self.q[at:at + n], self.k[b], self.v[b], self.scale, self.window, self.n_sink,
+                            self.sink, self.dtype)
+            R.compare(out[at:at + n], lse[at:at + n], *r, what=f"{what} sequence {b}")
+            at += n
+        assert (out[at:] == 77.0).all() and (lse[at:] == 55.0).all(), "padding rows were written"
+
+
+def check(kvd, c, P=64):
+    c.check(*c.packed(kvd), "packed")
+    c.check(*c.paged(kvd, P), "paged")
+
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64), (128, 256), (64, 128), (128, 32)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prompts_of_many_lengths(kvd, dtype, D, P):
+    n = [1, 2, 0, 31, 32, 33, 63, 64, 65, 127, 128, 129, 300]
+    check(kvd, Case(n, n, 8, 2, D, dtype, seed=D + P, pad=5), P)
+
+
+@pytest.mark.parametrize("D,P", [(64, 64), (128, 16), (128, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_chunks_behind_prefixes(kvd, dtype, D, P):
+    new = [1, 5, 17, 64, 130, 3, 1, 0, 200]
+    lens = [1, 700, 17, 65, 500, 128, 129, 40, 1000]
+    check(kvd, Case(new, lens, 8, 2, D, dtype, seed=D, pad=1), P)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (14, 2), (9, 1), (16, 1), (24, 1), (40, 2), (65, 1), (128, 1)])
+@pytest.mark.parametrize("D,dtype", [(64, F32), (128, BF), (64, BF), (128, F32)])
+def test_head_groups(kvd, Hq, Hkv, D, dtype):
+    check(kvd, Case([3, 50, 1], [3, 77, 200], Hq, Hkv, D, dtype, seed=Hq), 32)
+
+
+@pytest.mark.parametrize("window,n_sink,learned", [(1, 0, False), (17, 3, True), (100, 4, False),
+                                                    (128, 128, False), (64, 140, True), (5000, 4, True),
+                                                    (32, 0, True), (200, 300, False)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_windows_and_sinks(kvd, dtype, window, n_sink, learned):
+    new, lens = [1, 90, 400, 33], [600, 90, 700, 513]
+    check(kvd, Case(new, lens, 8, 2, 64, dtype, window, n_sink, learned, seed=window))
+    check(kvd, Case(new, lens, 4, 4, 128, dtype, window, n_sink, learned, seed=window), 16)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_that_see_nothing(kvd, dtype):
+    # more new tokens than keys: the leading ones see nothing
+    for learned in (False, True):
+        c = Case([5, 200, 3, 140], [3, 90, 0, 1], 8, 2, 64, dtype, learned=learned, seed=3)
+        out, lse = c.packed(kvd)
+        c.check(out, lse)
+        assert (out[:2] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_keys_fewer_than_new_tokens_are_recorded_in_a_cache(kvd, dtype):
+    c = Case([5, 20], [3, 40], 8, 2, 128, dtype, seed=4)
+    out, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:2], device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    kvd.attn_prefill_gqa_paged(c.q, *c.pools(16), cu(c.new), out=out, lse_out=lse, err=err, **c.more())
+    assert int(err.item()) == -6
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [0, 100])
+def test_values_that_are_not_finite_reach_their_rows_alone(kvd, dtype, window):
+    c = Case([150, 300, 60], [150, 420, 60], 4, 2, 128, dtype, window=window, n_sink=2 if window else 0, seed=5)
+    c.v[0][100, 0, 3] = math.inf
+    c.v[1][250, 1, :] = NAN
+    c.v[1][300, 0, 64] = -math.inf
+    c.v[1][1, 0, 5] = -math.inf
+    c.v[2][59, :, 0] = NAN  # the last token: seen by itself alone
+    check(kvd, c)
+    c = Case([300], [300], 2, 1, 64, dtype, window=window, n_sink=2 if window else 0, seed=6)
+    c.v[0][130, 0, 3] = math.inf
+    c.v[0][131, 0, 3] = -math.inf  # both: NaN
+    check(kvd, c, 16)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_keys_that_are_not_finite_reach_their_rows_alone(kvd, dtype):
+    c = Case([200, 40], [200, 300], 4, 2, 64, dtype, seed=7)
+    c.k[0][150, 0, 5] = NAN
+    c.k[1][290, 1, 0] = NAN
+    out, lse = c.packed(kvd)
+    for name, o, l in (("packed", out, lse), ("paged", *c.paged(kvd, 32))):
+        o, l = o.float(), l
+        assert torch.isnan(o[150:200, :2]).all() and torch.isnan(o[200 + 30:, 2:]).all(), name
+        c2 = Case([200, 40], [200, 300], 4, 2, 64, dtype, seed=7)
+        ref, _ = c2.packed(kvd)
+        assert torch.equal(o[:150], ref[:150].float()) and torch.equal(o[:, 2:][:200], ref[:, 2:][:200].float())
+        assert torch.equal(o[200:, :2], ref[200:, :2].float()) and torch.equal(o[200:230], ref[200:230].float())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_large_scores(kvd, dtype):
+    # sharp weights, maxima that grow along the keys, a negative scale
+    c = Case([300, 40], [300, 900], 8, 2, 128, dtype, qscale=20.0, seed=11)
+    for k in c.k:
+        k *= torch.linspace(0.01, 3.0, k.shape[0], device=DEV).to(dtype)[:, None, None]
+    check(kvd, c, 16)
+    check(kvd, Case([300], [400], 8, 2, 64, dtype, scale=-0.5, seed=12))
+    check(kvd, Case([300], [400], 8, 2, 64, dtype, scale=0.0, seed=12))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 32, 8), (64, 28, 4)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_sequences_are_cut_and_joined(kvd, dtype, D, Hq, Hkv):
+    # few rows over long caches, whole prompts, and both in one call
+    check(kvd, Case([4, 1, 7], [9001, 5000, 130], Hq, Hkv, D, dtype, seed=9))
+    check(kvd, Case([1700, 3, 900], [1700, 2500, 2111], Hq, Hkv, D, dtype, learned=True, seed=10), 256)
+    check(kvd, Case([700, 3], [6000, 2500], Hq, Hkv, D, dtype, window=1000, n_sink=5, seed=10), 32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_slices_of_a_projection(kvd, dtype):
+    Hq, Hkv, D, n = 8, 2, 64, [70, 3, 200]
+    T = sum(n)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g, device=DEV).to(dtype)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    out = kvd.attn_prefill_gqa(q, k, v, cu(n))
+    want = kvd.attn_prefill_gqa(q.contiguous(), k.contiguous(), v.contiguous(), cu(n), cu(n))
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_token_of_each_sequence_is_the_decode(kvd, dtype):
+    lens = [1, 64, 700, 129, 5000]
+    c = Case([1] * 5, lens, 32, 8, 128, dtype, seed=2)
+    kp, vp, bt, sl = c.pools(64)
+    lse = torch.empty(5, 32, device=DEV)
+    out = kvd.attn_prefill_gqa_paged(c.q, kp, vp, bt, sl, lse_out=lse, **c.more())
+    c.check(out, lse)
+    other = kvd.attn_decode_gqa_paged(c.q, kp.nan_to_num(), vp.nan_to_num(), bt.clamp_min(0), sl, scale=c.scale)
+    tol = 2.0 ** -6 if dtype == BF else 1e-5  # two kernels, each within its own bound
+    assert (out.float() - other.float()).abs().max() <= tol
+
+
+def test_streams_graphs_and_shared_workspaces(kvd):
+    cs = [Case([300, 5], [300, 3000], 8, 2, 128, BF, seed=20), Case([64, 64], [900, 70], 8, 2, 128, BF, seed=21)]
+    want = [c.paged(kvd, 64) for c in cs]
+    args = [(c.q, *c.pools(64), cu(c.new)) for c in cs]
+    outs = [torch.zeros_like(c.q) for c in cs]
+    # two streams at once, each call with memory of its own
+    ss = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for a, o, s in zip(args, outs, ss):
+            kvd.attn_prefill_gqa_paged(*a, out=o, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w[0])
+    # one workspace, two captured graphs replayed in turn; replayed on other inputs
+    ws = torch.full((kvd.kvd_workspace_size("prefill", 2, 8, 2, 128),), 255, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for a, o in zip(args, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kvd.attn_prefill_gqa_paged(*a, out=o, workspace=ws)
+        graphs.append(g)
+    for o in outs:
+        o.zero_()
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w[0])
+    q = args[0][0].clone()
+    args[0][0].copy_(q.flip(0))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], kvd.attn_prefill_gqa_paged(*args[0]))
+    # a Workspace object
+    assert torch.equal(kvd.attn_prefill_gqa_paged(*args[1], workspace=kvd.Workspace()), want[1][0])
+
+
+def test_results_do_not_depend_on_timing(kvd):
+    c = Case([900, 3, 40], [3000, 7000, 40], 8, 2, 128, BF, seed=22)
+    a = (c.q, *c.pools(64), cu(c.new))
+    first = kvd.attn_prefill_gqa_paged(*a)
+    for _ in range(20):
+        assert torch.equal(kvd.attn_prefill_gqa_paged(*a), first)
+
+
+def test_bad_offsets_lengths_and_pages_are_recorded(kvd):
+    c = Case([20, 30], [20, 30], 8, 2, 64, BF, seed=23)
+    k, v = torch.cat(c.k), torch.cat(c.v)
+
+    def run(cq, ck):
+        out = torch.full_like(c.q, 77.0)
+        err = torch.zeros(1, dtype=I32, device=DEV)
+        kvd.attn_prefill_gqa(c.q, k, v, torch.tensor(cq, dtype=I32, device=DEV),
+                             torch.tensor(ck, dtype=I32, device=DEV), out=out, err=err)
+        return out, int(err.item())
+
+    good, e = run([0, 20, 50], [0, 20, 50])
+    assert e == 0
+    out, e = run([0, 20, 51], [0, 20, 50])
+    assert e == -6 and torch.equal(out[:20], good[:20]) and (out[20:] == 77).all()
+    out, e = run([0, 20, 10], [0, 20, 50])
+    assert e == -6 and torch.equal(out[:20], good[:20]) and (out[20:] == 77).all()
+    out, e = run([0, 20, 50], [0, 20, 60])
+    assert e == -6 and torch.equal(out[:20], good[:20]) and (out[20:] == 77).all()
+    out, e = run([0, 20, 50], [0, -1, 50])
+    assert e == -6
+    kp, vp, bt, sl = c.pools(16)
+    kp, vp = kp.nan_to_num(), vp.nan_to_num()
+    for table, lens in ((bt.clone(), sl.clone()), (bt.clone(), sl.clone())):
+        err = torch.zeros(1, dtype=I32, device=DEV)
+        kvd.attn_prefill_gqa_paged(c.q, kp, vp, table, lens, cu(c.new), err=err)
+        assert int(err.item()) == 0
+    for page in (-1, kp.shape[0], 2 ** 30):
+        table = bt.clone()
+        table[1, 0] = page
+        err = torch.zeros(1, dtype=I32, device=DEV)
+        out = kvd.attn_prefill_gqa_paged(c.q, kp, vp, table, sl, cu(c.new), err=err)
+        assert int(err.item()) == -6 and torch.isfinite(out.float()).all()
+    for length in (-1, 16 * bt.shape[1] + 1, 2 ** 31 - 1):
+        lens = sl.clone()
+        lens[1] = length
+        err = torch.zeros(1, dtype=I32, device=DEV)
+        out = kvd.attn_prefill_gqa_paged(c.q, kp, vp, bt.clamp_min(0), lens, cu(c.new), err=err)
+        assert int(err.item()) == -6 and torch.isfinite(out.float()).all()
+
+
+def test_offsets_past_32_bits(kvd):
+    # pools of more than 2^31 elements each, a few long sequences at their end
+    Hkv, D, P = 8, 128, 256
+    pages = 8300
+    assert pages * Hkv * P * D > 2 ** 31
+    kp = torch.zeros(pages, Hkv, P, D, dtype=BF, device=DEV)
+    vp = torch.zeros(pages, Hkv, P, D, dtype=BF, device=DEV)
+    c = Case([9, 300], [1000, 513], 8, 8, D, BF, seed=24)
+    bt = torch.tensor([[pages - 1, pages - 3, pages - 2, 0], [pages - 5, 1, pages - 4, -1]], dtype=I32, device=DEV)
+    for pool, rows in ((kp, c.k), (vp, c.v)):
+        for b, x in enumerate(rows):
+            for i in range(0, x.shape[0], P):
+                y = x[i:i + P]
+                pool[int(bt[b, i // P]), :, :y.shape[0]] = y.transpose(0, 1)
+    sl = torch.tensor(c.lens, dtype=I32, device=DEV)
+    c.check(*c.call(kvd.attn_prefill_gqa_paged, (c.q, kp, vp, bt, sl, cu(c.new))))
+    del kp, vp
+    # packed rows whose tokens lie far apart
+    wide = 1 << 22
+    buf = torch.zeros(813, wide, dtype=BF, device=DEV)
+    k, v = (buf.as_strided((813, Hkv, D), (wide, D, 1), wide - (i + 1) * Hkv * D) for i in (0, 1))
+    c = Case([9, 300], [500, 313], 8, 8, D, BF, seed=25)
+    k.copy_(torch.cat(c.k))
+    v.copy_(torch.cat(c.v))
+    c.check(*c.call(kvd.attn_prefill_gqa, (c.q, k, v, cu(c.new), cu(c.lens))))
+
+
+def test_many_short_sequences(kvd):
+    g = torch.Generator().manual_seed(0)
+    new = torch.randint(0, 4, (700,), generator=g).tolist()
+    lens = [n + int(torch.randint(0, 90, (1,), generator=g)) for n in new]
+    c = Case(new, lens, 4, 2, 64, BF, seed=26)
+    c.check(*c.packed(kvd))
+    c.check(*c.paged(kvd, 16))
+
+
+def test_append_then_attend_and_read_back(kvd):
+    """The operators as they are used together: prompts appended to a 4-bit cache, later chunks appended,
+    everything read back, and the chunks' attention over it; the same over a plain cache; and chunks
+    behind a rolling cache."""
+    Hq, Hkv, D, P = 8, 2, 128, 16
+    g = torch.Generator(device=DEV).manual_seed(30)
+    old, new = [100, 33, 0], [40, 5, 70]
+    full = [a + b for a, b in zip(old, new)]
+    table = Q.table(256, D).to(DEV)
+    bt, pages = Q.make_table(full, P, torch.Generator().manual_seed(1))
+    bt = bt.to(DEV)
+    rnd = lambda n, h: torch.randn(n, h, D, generator=g, device=DEV).to(BF)  # noqa: E731
+    qs, ks, vs = ([rnd(sum(n), h) for n in (old, new)] for h in (Hq, Hkv, Hkv))
+    sl = [torch.tensor(x, dtype=I32, device=DEV) for x in (old, full)]
+    for q4 in (True, False):
+        append = kvd.rope_append_q4 if q4 else kvd.rope_append
+        kp, vp = ((kvd.q4_pool(pages, Hkv, P, D) for _ in range(2)) if q4 else
+                  (torch.full((pages, Hkv, P, D), NAN, dtype=BF, device=DEV) for _ in range(2)))
+        append(qs[0], ks[0], vs[0], table, kp, vp, bt, sl[0], cu(old))
+        q = append(qs[1], ks[1], vs[1], table, kp, vp, bt, sl[1], cu(new))
+        k, v = (torch.empty(sum(full), Hkv, D, dtype=BF, device=DEV) for _ in range(2))
+        (kvd.cache_read_q4 if q4 else kvd.cache_read)(kp, vp, bt, sl[1], cu(full), k, v)
+        c = Case(new, full, Hq, Hkv, D, BF)
+        c.q, c.k, c.v = q, list(k.split(full)), list(v.split(full))
+        c.check(*c.call(kvd.attn_prefill_gqa, (q, k, v, cu(new), cu(full))))
+        if not q4:
+            c.check(*c.call(kvd.attn_prefill_gqa_paged, (q, kp, vp, bt, sl[1], cu(new))))
+    # a rolling cache of 20 + 3: what it holds, then the chunk's own rows behind it
+    W, ns = 20, 3
+    bt, pages = Q.make_table([W + ns] * 3, P, torch.Generator().manual_seed(2))
+    bt = bt.to(DEV)
+    kp, vp = (torch.zeros(pages, Hkv, P, D, dtype=BF, device=DEV) for _ in range(2))
+    kvd.rope_append(None, ks[0], vs[0], table, kp, vp, bt, sl[0], cu(old), window=W, n_sink=ns)
+    held = [len(R.held_positions(n, W, ns)) for n in old]
+    rows = [h + n for h, n in zip(held, new)]
+    k, v = (torch.zeros(sum(rows), Hkv, D, dtype=BF, device=DEV) for _ in range(2))
+    kvd.cache_read(kp, vp, bt, sl[0], cu(rows), k, v, window=W, n_sink=ns)
+    at = cu(rows)[:-1].long()
+    where = torch.cat([at[b] + held[b] + torch.arange(n, device=DEV) for b, n in enumerate(new)])
+    k[where], v[where] = ks[1], vs[1]
+    c = Case(new, rows, Hq, Hkv, D, BF, window=W, n_sink=ns)
+    c.q, c.k, c.v = qs[1], list(k.split(rows)), list(v.split(rows))
+    c.check(*c.call(kvd.attn_prefill_gqa, (qs[1], k, v, cu(new), cu(rows))))
