@@ -116,6 +116,27 @@ int make_tmap_bf16_blocked(CUtensorMap* map, const void* base, uint64_t rows, ui
     return r == CUDA_SUCCESS ? KVD_OK : KVD_ERR_CUDA;
 }
 
+int make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                      const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+    std::call_once(g_encode_once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (!g_encode) return KVD_ERR_CUDA;
+    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+    const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st,
+                          bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KVD_OK : KVD_ERR_CUDA;
+}
+
 // Split plan. Every (sequence, group of KV heads, head block, chunk) is one CTA, two
 // CTAs per SM for bf16. A CTA pays a fixed start-up (barrier set-up, block-table read,
 // first TMA round trip) and a merge, and a second wave of CTAs pays them again, so:
@@ -773,7 +794,7 @@ int attn_prefill_gqa(const void* q, const void* k, const void* v, const int32_t*
     p.Tk = Tk;
     p.k_stride = k_stride;
     p.v_stride = v_stride;
-    return prefill_launch(p, D, dtype, stream);
+    return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, stream);
 }
 
 int attn_prefill_gqa_paged(const void* q, const void* k_pool, const void* v_pool,
@@ -810,7 +831,7 @@ int attn_prefill_gqa_paged(const void* q, const void* k_pool, const void* v_pool
     p.page_shift = __builtin_ctz(page_size);
     p.max_pages = max_pages;
     p.num_pages = num_pages;
-    return prefill_launch(p, D, dtype, stream);
+    return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, stream);
 }
 
 static int cache_read(bool q4, const void* k_pool, const void* v_pool, const int32_t* block_table,
@@ -1293,7 +1314,7 @@ size_t kvd_workspace_size(int op, int B, int H, int Hkv, int D, int max_len, int
     if (op == KVD_OP_MLA_SPARSE) return k >= 1 ? mla_plan(B, k, true).total : 0;
     if (op == KVD_OP_PREFILL) {
         if (Hkv < 1 || H % Hkv != 0 || H / Hkv > 128 || (D != 64 && D != 128)) return 0;
-        return 256;
+        return prefill_ws_bytes(D);
     }
     if (op == KVD_OP_GQA_Q4) {
         Q4Plan plan;

@@ -197,7 +197,14 @@ struct CacheReadParams {
 };
 int cache_read_launch(const CacheReadParams& p, bool q4, int D, int dtype, cudaStream_t stream);
 
-// Arguments of the attention of many new tokens of a sequence (prefill_simple.cu).
+// The first piece of a unit of the prefill attention that was cut (prefill_bf16.cu); nt == 0: none.
+struct PrefillHead {
+    int c0, n, h, tok0;        // first row, new tokens, KV head, the unit's first new token
+    int last, nt;              // CTA that has its last piece; tiles
+    long long u, w, V;         // the unit's position and length in the work list, the list's length
+};
+
+// Arguments of the attention of many new tokens of a sequence (prefill_bf16.cu, prefill_simple.cu).
 struct PrefillParams {
     const void* q;             // [T, Hq, D], tokens q_stride apart
     const void *k, *v;         // packed [Tk, Hkv, D], or pools [num_pages, Hkv, page_size, D]
@@ -214,8 +221,14 @@ struct PrefillParams {
     int page_shift, max_pages, num_pages;
     int window, n_sink;        // window 0: all
     float scale_log2;
+    // bfloat16: how work is cut, and the pieces of units that were cut
+    int unit_cost, flat_slack; // keys that a unit's start and end are worth; see load_role
+    PrefillHead* head;         // [CTAs]
+    float *part_ml, *part_o;   // [2 CTAs, 256 rows] (maximum, sum) and [.., D] unnormalised outputs
 };
-int prefill_launch(const PrefillParams& p, int D, int dtype, cudaStream_t stream);
+size_t prefill_ws_bytes(int D);
+int prefill_bf16_launch(const PrefillParams& p, int D, void* ws, cudaStream_t stream);
+int prefill_f32_launch(const PrefillParams& p, int D, cudaStream_t stream);
 
 // Arguments of the attention over a 4-bit cache (gqa_q4_decode.cu).
 struct Q4Params {
@@ -334,6 +347,9 @@ int make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
                     uint32_t box_rows);
 int make_tmap_bf16_blocked(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            uint32_t box_rows, uint32_t nblocks);
+// 4-D bf16 tensor map with 128-byte swizzle: element counts, strides of dims 1 to 3 in bytes, box.
+int make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                      const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 
 int num_sms();
 

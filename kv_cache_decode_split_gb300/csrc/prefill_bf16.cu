@@ -1,0 +1,1107 @@
+// prefill_bf16.cu -- causal attention of many new tokens of each sequence, bfloat16, over packed keys
+// and values or over a paged cache.
+//
+// What is computed: the i-th of a sequence's n new tokens, of L keys in all, has position
+// p = L - n + i and sees the keys t <= p (window > 0: of them t > p - window or t < n_sink):
+//   s_t = scale q.k_t,  out = sum_t exp(s_t - lse) v_t,  lse = log(sum_t exp(s_t) [+ exp(sink)]).
+//
+// Rows. A KV head's G query heads read the same keys, so the G heads of 128 / G tokens make the 128
+// rows of one tensor-core tile (row = token * G + head), and a unit of work is two such tiles of one
+// sequence and KV head: every key and value tile is read once for 256 rows.
+//
+// One persistent CTA an SM, roles by warp:
+//   * loads: query tiles and a ring of 128-token key and value tiles, all by TMA;
+//   * products: one thread issues S = Q K^T (tcgen05, 128 x 128, operands in shared memory) and
+//     O += P V (P in tensor memory, where it takes the place of its S);
+//   * softmax: two warpgroups, one row a thread, each with a score tile and an output accumulator of
+//     its own in tensor memory, so that one's exponentials run under the other's products. The row's
+//     reference maximum is only raised, and O rescaled, when a maximum grows by more than 2^8;
+//     weights are then at most 2^8 and are rounded to bfloat16 (the value product's operands have one
+//     type), their sums are float32 sums of the unrounded weights.
+//   * values: at the edges of the mask two warps clear the value rows behind the sequence's end and
+//     every value that is not finite, before a zero weight can meet them; the rows that see such a
+//     value get it back at the end.
+// A unit of at most 128 rows (draft tokens, a prompt's end) is one query tile: the two warpgroups then
+// take its key tiles in turn, and their accumulators are merged.
+//
+// Work is cut as a list: all units one behind the other, each as long as the keys that it walks and a
+// fixed part for its start and end, in equal ranges, one for each CTA. A unit that a cut divides is
+// left as partial results of its pieces, which a second launch merges by log-sum-exp (in the order of
+// the pieces: the result does not depend on timing).
+
+#include <algorithm>
+
+#include "kvd_device.cuh"
+#include "kvd_host.h"
+
+namespace kvd {
+
+namespace {
+
+constexpr int kM = 128;     // rows of a query tile
+constexpr int kN = 128;     // keys of a tile
+constexpr int kPieces = 4;  // ring of work descriptions
+constexpr int kSoftWarps = 8;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 10;
+constexpr int kFixWarps = 2;
+constexpr int kThreads = 384;
+// two softmax warpgroups and one of the others share what the CTA was launched with: 168 a thread
+constexpr int kRegsSoft = 216, kRegsOther = 72;
+static_assert(2 * kRegsSoft + kRegsOther <= 3 * 168, "registers");
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrowth = 8.0f;  // log2 units
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream
+
+// One piece of a unit: tiles [t0, t1) of its list.
+struct Piece {
+    int h;
+    int c0, n, L;     // the sequence's first row, new tokens and keys
+    int k0;           // its first key row (packed), or its sequence (paged)
+    int tok0;         // the unit's first new token
+    int nA, tB;       // the list: tiles 0 .. nA - 1, then from tB on
+    int t0, t1, nt;   // nt: tiles of the whole unit; t0 < 0: no more pieces
+    int slot;         // partial result, or -1: the piece is the whole unit
+    int pair;         // two query tiles
+};
+
+template <int D>
+struct Layout {
+    static constexpr int kTile = kN * D * 2;   // bytes of a key, value or query tile
+    static constexpr int kStages = D == 128 ? 5 : 8;
+};
+
+template <int D>
+struct Smem {
+    uint8_t q[2][Layout<D>::kTile];                   // offset 0, 1024-aligned
+    uint8_t kv[Layout<D>::kStages][Layout<D>::kTile];
+    float stat[2][kM][2];                             // one query tile: both streams' (max, sum)
+    uint64_t full[Layout<D>::kStages], empty[Layout<D>::kStages];
+    // values at a mask's edge: under way (a look at `full` alone could take an earlier round of the
+    // ring for this one), and looked through
+    uint64_t issued[Layout<D>::kStages], fixed[Layout<D>::kStages];
+    uint64_t qfull, qempty, sfull[2], pready[2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
+    uint64_t statw[2], statr[2];                      // a stream's stat written; read by the other
+    uint64_t end;
+    Piece piece[kPieces];
+    int bad[kPieces];                                 // a value at a mask's edge was not finite
+    uint32_t tmem_base;
+};
+
+struct Seq {
+    int c0, n, L, k0;
+};
+
+// Sequence b; n = 0 where its offsets are bad. (b < B)
+__device__ __forceinline__ Seq load_seq(const PrefillParams& p, int b, int* err) {
+    Seq s;
+    int c1;
+    if (p.cu_q) {
+        s.c0 = p.cu_q[b];
+        c1 = p.cu_q[b + 1];
+    } else {
+        s.c0 = b;
+        c1 = b + 1;
+    }
+    bool bad = s.c0 < 0 || c1 < s.c0 || c1 > p.T || (b == 0 && s.c0 != 0);
+    s.n = bad ? 0 : c1 - s.c0;
+    if (p.block_table) {
+        const int len = p.seq_lens[b];
+        s.L = min(max(len, 0), p.max_pages << p.page_shift);
+        s.k0 = b;
+        bad |= len != s.L || s.L < s.n;
+    } else {
+        s.k0 = p.cu_k[b];
+        const int k1 = p.cu_k[b + 1];
+        s.L = k1 - s.k0;
+        if (s.k0 < 0 || k1 < s.k0 || k1 > p.Tk || (b == 0 && s.k0 != 0)) {
+            bad = true;
+            s.n = 0;
+        }
+    }
+    if (bad) record_error(err, KVD_ERR_DEVICE_OOB);
+    return s;
+}
+
+// Length in the work list of a unit, and of a sequence's first m units (of one head): a fixed part and
+// the keys up to the unit's last token, at most what a window leaves. (Only the balance depends on
+// it. flat: every unit counts 1.)
+struct Weigh {
+    long long base, cap;
+    int U, fixed;
+    bool flat;
+    __device__ __forceinline__ Weigh(const PrefillParams& p, const Seq& s, int u, bool f)
+        : base(max(0, s.L - s.n)), U(u), fixed(p.unit_cost), flat(f) {
+        cap = p.window > 0 ? static_cast<long long>(p.window) + U + kN + min(p.n_sink, s.L) : 1LL << 40;
+    }
+    __device__ __forceinline__ long long upto(long long m) const {
+        if (flat) return m;
+        const long long free = cap > base ? (cap - base) / U : 0, m1 = min(m, free);
+        return m * fixed + m1 * base + U * (m1 * (m1 + 1) / 2) + (m - m1) * cap;
+    }
+};
+
+// The tiles that a unit walks: [0, nA) and nt - nA from tB on.
+__device__ __forceinline__ void unit_tiles(const PrefillParams& p, const Seq& s, int tok0, int U,
+                                           int& nA, int& tB, int& nt) {
+    const int first = s.L - s.n + tok0;                      // first and last position
+    const int last = s.L - s.n + min(s.n, tok0 + U) - 1;
+    nA = tB = nt = 0;
+    if (last < 0) return;
+    const int lo = p.window > 0 ? max(0, first - p.window + 1) / kN : 0;
+    const int sink = p.window > 0 ? (min(p.n_sink, last + 1) + kN - 1) / kN : 0;
+    nA = min(sink, lo);
+    tB = lo;
+    nt = nA + last / kN - lo + 1;
+}
+
+// Whether some row of the unit does not see all of the tile: the mask is applied, and its values are
+// looked through.
+__device__ __forceinline__ bool at_edge(const PrefillParams& p, const Piece& u, int tile, int U) {
+    const int first = u.L - u.n + u.tok0, last = u.L - u.n + min(u.n, u.tok0 + U) - 1;
+    const int ts = tile * kN;
+    if (ts + kN - 1 > first) return true;
+    return p.window > 0 && ts + kN > p.n_sink && ts <= last - p.window;
+}
+
+__device__ __forceinline__ int tile_of(const Piece& u, int t) {
+    return t < u.nA ? t : u.tB + (t - u.nA);
+}
+// Ring items of a piece of nt tiles: `la` key tiles, then value tile t and key tile t + la in turn.
+__device__ __forceinline__ int item_of_v(int t, int nt, int la) { return min(2 * t + la, 2 * nt - 1); }
+__device__ __forceinline__ int item_of_k(int t, int la) { return t < la ? t : 2 * t - (la - 1); }
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+                 : "memory");
+}
+
+// Registers of the executing warpgroup's threads, from the CTA's launch share (kThreads * 168).
+template <int N>
+__device__ __forceinline__ void regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_fewer() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair64(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair64(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// S (tensor memory) = Q (128 rows) K^T (128 keys), both K-major in shared memory.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
+    constexpr uint32_t idesc = idesc_bf16_f32(kM, kN, 0, 0);
+    const uint64_t a = sw128_kmajor_desc(q), b = sw128_kmajor_desc(k);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const uint64_t step = static_cast<uint64_t>(((ks >> 2) * kN * 128 + (ks & 3) * 32) >> 4);
+        tc_mma_bf16(s, a + step, b + step, idesc, ks > 0 ? 1u : 0u);
+    }
+}
+
+// O (tensor memory) (+)= P (tensor memory, 128 x 128) V (128 tokens, read MN-major).
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t pt, uint32_t v, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32(kM, D, 0, 1);
+    const uint64_t b = sw128_mnmajor_desc(v, kN * 128);
+#pragma unroll
+    for (int ks = 0; ks < kN / 16; ++ks)
+        tc_mma_bf16_ts(o, pt + ks * 8, b + static_cast<uint64_t>((ks * 16 * 128) >> 4), idesc,
+                       (accumulate || ks > 0) ? 1u : 0u);
+}
+
+// Range of CTA c: [V c / n, V (c + 1) / n); tile at which offset y of a unit of length w cuts it.
+__device__ __forceinline__ long long range_start(long long V, int c, int n) { return V * c / n; }
+__device__ __forceinline__ int cut_tile(long long y, long long w, int nt) {
+    return y <= 0 ? 0 : y >= w ? nt : static_cast<int>(y * nt / w);
+}
+
+// ------------------------------------------------------------------------------------- loads
+template <int D>
+__device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap* tq,
+                          const CUtensorMap* tk, const CUtensorMap* tv, int lane) {
+    using Ly = Layout<D>;
+    const int TM = kM / p.G, U = 2 * TM;
+    const int cta = blockIdx.x, n_cta = gridDim.x;
+    int* err = p.err;
+    // how long the list is
+    long long V = 0, units = 0, longest = 0;
+    for (int base = 0; base < p.B; base += 128) {
+        Seq s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = base + i * 32 + lane;
+            s[i].n = 0;
+            if (b < p.B) s[i] = load_seq(p, b, cta == 0 ? err : nullptr);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (s[i].n == 0) continue;
+            const int nm = (s[i].n + U - 1) / U;
+            const Weigh w(p, s[i], U, false);
+            const long long all = w.upto(nm);
+            V += all * p.Hkv;
+            units += static_cast<long long>(nm) * p.Hkv;
+            longest = max(longest, all - w.upto(nm - 1));
+        }
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        V += __shfl_xor_sync(0xffffffffu, V, off);
+        units += __shfl_xor_sync(0xffffffffu, units, off);
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, off));
+    }
+    // few short units: a CTA each, nothing is cut
+    const bool flat = units <= n_cta && longest <= V / n_cta + p.flat_slack;
+    if (flat) V = units;
+    const long long x0 = range_start(V, cta, n_cta), x1 = range_start(V, cta + 1, n_cta);
+
+    int ps = 0;               // pieces published
+    uint32_t g = 0, nq = 0;   // ring items and query loads issued
+    bool ok = true;
+    if (lane == 0) p.head[cta].nt = 0;
+    auto publish = [&](const Piece& u) {
+        const int i = ps % kPieces;
+        if (lane == 0) {
+            ok = mbar_wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
+            if (ok) {
+                sm.piece[i] = u;
+                sm.bad[i] = 0;
+                mbar_arrive(&sm.pfull[i]);
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++ps;
+    };
+
+    // the sequence that position x0 falls in
+    int b0 = 0;        // 32 sequences, one a lane
+    long long at = 0;  // position of the first of them
+    Seq mine;
+    long long my_len = 0;
+    auto load_batch = [&]() {
+        const int b = b0 + lane;
+        mine.n = mine.c0 = mine.L = mine.k0 = 0;
+        if (b < p.B) mine = load_seq(p, b, nullptr);
+        my_len = 0;
+        if (mine.n > 0) my_len = Weigh(p, mine, U, flat).upto((mine.n + U - 1) / U) * p.Hkv;
+    };
+    int j = 0;
+    if (x0 < x1) {
+        for (;; b0 += 32) {
+            if (b0 >= p.B) {  // (not while the lengths stay as they are)
+                at = x1;
+                break;
+            }
+            load_batch();
+            long long incl = my_len;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, at + incl > x0);
+            if (m) {
+                j = __ffs(m) - 1;
+                at += __shfl_sync(0xffffffffu, incl - my_len, j);
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    bool first_seq = true;
+    while (ok && at < x1 && x0 < x1) {
+        Seq s;
+        s.c0 = __shfl_sync(0xffffffffu, mine.c0, j);
+        s.n = __shfl_sync(0xffffffffu, mine.n, j);
+        s.L = __shfl_sync(0xffffffffu, mine.L, j);
+        s.k0 = __shfl_sync(0xffffffffu, mine.k0, j);
+        if (s.n > 0) {
+            const int nm = (s.n + U - 1) / U;
+            const Weigh wt(p, s, U, flat);
+            const long long per_head = wt.upto(nm);
+            int h = 0, m = 0;
+            long long u = at;  // position of the unit
+            if (first_seq) {
+                long long rem = x0 - at;
+                h = static_cast<int>(rem / per_head);
+                rem -= h * per_head;
+                int lo = 0, hi = nm - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (wt.upto(mid) <= rem) lo = mid; else hi = mid - 1;
+                }
+                m = lo;
+                u = at + h * per_head + wt.upto(m);
+            }
+            for (; h < p.Hkv && u < x1 && ok; ++h, m = 0) {
+                for (; m < nm && u < x1 && ok; ++m) {
+                    const long long w = wt.upto(m + 1) - wt.upto(m);
+                    Piece pc;
+                    pc.h = h;
+                    pc.c0 = s.c0;
+                    pc.n = s.n;
+                    pc.L = s.L;
+                    pc.k0 = s.k0;
+                    pc.tok0 = m * U;
+                    unit_tiles(p, s, pc.tok0, U, pc.nA, pc.tB, pc.nt);
+                    pc.t0 = cut_tile(x0 - u, w, pc.nt);
+                    pc.t1 = cut_tile(x1 - u, w, pc.nt);
+                    pc.pair = s.n - pc.tok0 > TM;
+                    const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
+                    pc.slot = whole ? -1 : 2 * cta + (pc.t0 == 0 ? 1 : 0);
+                    const long long start = u;
+                    u += w;
+                    if (pc.nt == 0 ? start < x0 : pc.t0 == pc.t1) continue;
+                    if (lane == 0 && !whole && pc.t0 == 0) {
+                        // the unit's first piece: what the merge needs to know
+                        PrefillHead& hd = p.head[cta];
+                        hd.c0 = pc.c0;
+                        hd.n = pc.n;
+                        hd.h = h;
+                        hd.tok0 = pc.tok0;
+                        hd.last = static_cast<int>(((start + w) * n_cta + V - 1) / V - 1);
+                        hd.u = start;
+                        hd.w = w;
+                        hd.V = V;
+                        hd.nt = pc.nt;
+                    }
+                    publish(pc);
+                    if (!ok) break;
+                    const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
+                    if (nt == 0) continue;
+                    // queries
+                    if (lane == 0) {
+                        ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err);
+                        if (ok) {
+                            const int rows = TM * p.G;
+                            mbar_arrive_expect_tx(&sm.qfull, (pc.pair ? 2 : 1) * rows * D * 2);
+                            for (int i = 0; i <= pc.pair; ++i)
+                                for (int k = 0; k < D / 64; ++k)
+                                    tma_load_4d(sm.q[i] + k * kM * 128, tq, &sm.qfull, 0, h * p.G,
+                                                pc.c0 + pc.tok0 + i * TM, k);
+                        }
+                    }
+                    ++nq;
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    // keys and values; paged: page ids 32 at a time, the next 32 on their way
+                    const int shift = min(p.page_shift, 7);          // rows of one copy
+                    const int per = kN >> shift;                     // copies of a tile (and block)
+                    auto row_of = [&](int e) -> int {                // entry e: row of the copy
+                        const int t = e / per;
+                        if (t >= nt) return 0;
+                        const int tok = tile_of(pc, pc.t0 + t) * kN + ((e % per) << shift);
+                        if (!p.block_table) return pc.k0 + tok;
+                        const int safe = min(tok, pc.L - 1);
+                        const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
+                                                 safe >> p.page_shift, err);
+                        return ((pg * p.Hkv + h) << p.page_shift) + (tok & ((1 << p.page_shift) - 1));
+                    };
+                    const bool paged = p.block_table != nullptr;
+                    const int hz = paged ? 0 : h;
+                    // keys run ahead of values by `la` tiles: each has its own place in the entries
+                    int kb = 0, vb = 0;
+                    int kcur = 0, knxt = 0, vcur = 0;
+                    if (paged) {
+                        kcur = row_of(lane);
+                        knxt = row_of(32 + lane);
+                        vcur = kcur;
+                    }
+                    auto fetch = [&](int t, bool is_v) {
+                        const int s_ = g % Ly::kStages;
+                        if (lane == 0) {
+                            ok = mbar_wait(&sm.empty[s_], ((g / Ly::kStages) & 1) ^ 1, err);
+                            if (ok) {
+                                mbar_arrive_expect_tx(&sm.full[s_], Ly::kTile);
+                                if (is_v && at_edge(p, pc, tile_of(pc, pc.t0 + t), U))
+                                    mbar_arrive(&sm.issued[s_]);
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) return;
+                        ++g;
+                        const CUtensorMap* map = is_v ? tv : tk;
+                        if (!paged) {
+                            if (lane == 0)
+                                tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0,
+                                            pc.k0 + tile_of(pc, pc.t0 + t) * kN, 0, hz);
+                            return;
+                        }
+                        const int e0 = t * per;
+                        if (is_v) {
+                            if (e0 >= vb + 32) {
+                                vb += 32;
+                                vcur = vb == kb ? kcur : row_of(vb + lane);
+                            }
+                        } else if (e0 >= kb + 32) {
+                            kb += 32;
+                            kcur = knxt;
+                            knxt = row_of(kb + 32 + lane);
+                        }
+                        // entry e0 + i is with lane e0 - base + i, which issues that copy
+                        const int i = lane - (e0 - (is_v ? vb : kb));
+                        if (i >= 0 && i < per) {
+                            const int row = is_v ? vcur : kcur;
+                            if (per == 1) {
+                                tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0, row, 0, 0);
+                            } else {
+                                for (int k = 0; k < D / 64; ++k)
+                                    tma_load_4d(sm.kv[s_] + k * kN * 128 + ((i << shift) * 128), map,
+                                                &sm.full[s_], 0, row, k, 0);
+                            }
+                        }
+                        __syncwarp();
+                    };
+                    for (int t = 0; t < la && t < nt && ok; ++t) fetch(t, false);
+                    for (int t = 0; t < nt && ok; ++t) {
+                        fetch(t, true);
+                        if (t + la < nt && ok) fetch(t + la, false);
+                    }
+                }
+            }
+        }
+        first_seq = false;
+        at += __shfl_sync(0xffffffffu, my_len, j);
+        if (++j == 32) {
+            j = 0;
+            b0 += 32;
+            load_batch();  // (past the last sequence only when the range ends there)
+        }
+        if (b0 + j >= p.B) break;
+    }
+    if (ok) {
+        Piece last;
+        last.t0 = -1;
+        publish(last);
+    }
+    // every copy lands before the CTA ends, also after a wait gave up
+    if (lane == 0) {
+        const uint32_t from = g > Ly::kStages ? g - Ly::kStages : 0;
+        for (uint32_t i = from; i < g; ++i)
+            mbar_wait(&sm.full[i % Ly::kStages], (i / Ly::kStages) & 1, err);
+        if (nq > 0) mbar_wait(&sm.qfull, (nq - 1) & 1, err);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------------------------- products
+template <int D>
+__device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
+    using Ly = Layout<D>;
+    const int U = 2 * (kM / p.G);
+    const uint32_t tmem = sm.tmem_base;
+    int* err = p.err;
+    uint32_t g = 0, nq = 0, fixed_phase = 0;
+    uint32_t np[2] = {0, 0};  // weight tiles taken, each stream
+    const uint32_t q[2] = {smem_u32(sm.q[0]), smem_u32(sm.q[1])};
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const int i = k % kPieces;
+        if (!(ok = mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err))) break;
+        const Piece pc = sm.piece[i];
+        mbar_arrive(&sm.pempty[i]);
+        if (pc.t0 < 0) break;
+        const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
+        auto slot = [&](int item) { return (g + item) % Ly::kStages; };
+        auto wait_full = [&](int item) {
+            return mbar_wait(&sm.full[slot(item)], ((g + item) / Ly::kStages) & 1, err);
+        };
+        auto wait_ofree = [&](int w) { return mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err); };
+        auto wait_v = [&](int t) {
+            const int item = item_of_v(t, nt, la), s = slot(item);
+            if (!at_edge(p, pc, tile_of(pc, pc.t0 + t), U)) return wait_full(item);
+            const bool r = mbar_wait(&sm.fixed[s], (fixed_phase >> s) & 1, err);
+            fixed_phase ^= 1u << s;
+            return r;
+        };
+        auto kv = [&](int item) { return smem_u32(sm.kv[slot(item)]); };
+        if (nt > 0) {
+            if (!(ok = mbar_wait(&sm.qfull, nq & 1, err))) break;
+            ++nq;
+        }
+        for (int t = 0; t < la && t < nt && ok; ++t) {
+            if (!(ok = wait_full(t))) break;
+            tc_fence_after();
+            for (int w = pc.pair ? 0 : t; w <= (pc.pair ? 1 : t); ++w) {
+                issue_qk<D>(tmem + kColS + 128 * w, q[pc.pair ? w : 0], kv(t));
+                tc_commit(&sm.sfull[w]);
+            }
+            tc_commit(&sm.empty[slot(t)]);
+        }
+        if (ok && nt > 0 && nt <= la) tc_commit(&sm.qempty);
+        for (int t = 0; t < nt && ok; ++t) {
+            const int iv = item_of_v(t, nt, la), ik = item_of_k(t + la, la);
+            const bool more = t + la < nt;
+            for (int w = pc.pair ? 0 : (t & 1); w <= (pc.pair ? 1 : (t & 1)); ++w) {
+                const bool first = pc.pair ? t == 0 : t < 2;
+                if (first && !(ok = wait_ofree(w))) break;
+                if ((w == 0 || !pc.pair) && !(ok = wait_v(t))) break;
+                if (!(ok = mbar_wait(&sm.pready[w], np[w] & 1, err))) break;
+                ++np[w];
+                tc_fence_after();
+                issue_pv<D>(tmem + kColO + 128 * w, tmem + kColS + 128 * w, kv(iv), !first);
+                if (w == 1 || !pc.pair) tc_commit(&sm.empty[slot(iv)]);
+                if (more) {
+                    if ((w == 0 || !pc.pair)) {
+                        if (!(ok = wait_full(ik))) break;
+                        tc_fence_after();
+                    }
+                    issue_qk<D>(tmem + kColS + 128 * w, q[pc.pair ? w : 0], kv(ik));
+                    tc_commit(&sm.sfull[w]);
+                    if (w == 1 || !pc.pair) {
+                        tc_commit(&sm.empty[slot(ik)]);
+                        if (t + la == nt - 1) tc_commit(&sm.qempty);
+                    }
+                } else {
+                    tc_commit(&sm.ofull[w]);
+                }
+            }
+        }
+        if (!ok) break;
+        // streams without a tile in this piece keep their barriers' phases
+        for (int w = 0; w < 2; ++w)
+            if (pc.pair ? nt == 0 : nt <= w) {
+                if (!(ok = wait_ofree(w))) break;
+                tc_commit(&sm.ofull[w]);
+            }
+        g += 2 * nt;
+    }
+    // all products complete before tensor memory is released
+    tc_commit(&sm.end);
+    mbar_wait(&sm.end, 0, err);
+}
+
+// ------------------------------------------------------------------------- values at the edges
+template <int D>
+__device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
+    using Ly = Layout<D>;
+    const int U = 2 * (kM / p.G);
+    int* err = p.err;
+    uint32_t g = 0, phase = 0;  // phase: a bit for each slot
+    for (int k = 0;; ++k) {
+        const int i = k % kPieces;
+        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        const Piece pc = sm.piece[i];
+        if (pc.t0 < 0) break;
+        const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
+        bool ok = true;
+        for (int t = 0; t < nt && ok; ++t) {
+            const int tile = tile_of(pc, pc.t0 + t);
+            if (!at_edge(p, pc, tile, U)) continue;
+            const uint32_t item = g + item_of_v(t, nt, la);
+            const int s = item % Ly::kStages;
+            ok = mbar_wait(&sm.issued[s], (phase >> s) & 1, err) &&
+                 mbar_wait(&sm.full[s], (item / Ly::kStages) & 1, err);
+            if (!ok) break;
+            phase ^= 1u << s;
+            const int valid = pc.L - tile * kN;  // rows of the sequence
+            bool bad = false;
+#pragma unroll 8
+            for (int c = warp * 32 + lane; c < Ly::kTile / 16; c += kFixWarps * 32) {
+                uint4* at = reinterpret_cast<uint4*>(sm.kv[s]) + c;
+                uint4 v = *at;
+                // bfloat16 pairs whose exponent bits are all ones
+                auto odd = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                const int row = (c / 8) % kN;
+                if (row >= valid) {
+                    *at = make_uint4(0, 0, 0, 0);
+                } else if (odd(v.x) | odd(v.y) | odd(v.z) | odd(v.w)) {
+                    bad = true;
+                    auto clear = [&](uint32_t x) {
+                        const uint32_t o = odd(x);
+                        return x & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
+                    };
+                    *at = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
+                }
+            }
+            if (bad) sm.bad[i] = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.fixed[s]);
+        }
+        if (lane == 0) mbar_arrive(&sm.pempty[i]);
+        if (!ok) break;
+        g += 2 * nt;
+    }
+}
+
+// ----------------------------------------------------------------------------------- softmax
+// What a row gets back of the values that were cleared: v itself, where the row sees it.
+template <int D>
+__device__ __noinline__ void add_cleared(const PrefillParams& p, const Piece& pc, int U, int pos,
+                                         int col, float (&o)[32]) {
+    for (int t = pc.t0; t < pc.t1; ++t) {
+        const int tile = tile_of(pc, t);
+        if (!at_edge(p, pc, tile, U)) continue;
+        for (int r = 0; r < kN; ++r) {
+            const int key = tile * kN + r;
+            if (key >= pc.L) break;
+            const bool seen = key <= pos && (p.window <= 0 || key > pos - p.window || key < p.n_sink);
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v);
+            if (p.block_table) {
+                const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
+                                         key >> p.page_shift, nullptr);
+                v += (((static_cast<size_t>(pg) * p.Hkv + pc.h) << p.page_shift) +
+                      (key & ((1 << p.page_shift) - 1))) * D;
+            } else {
+                v += static_cast<long long>(pc.k0 + key) * p.v_stride + pc.h * D;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const float x = __bfloat162float(v[col + c]);
+                if (seen && !isfinite(x)) o[c] += x;
+            }
+        }
+    }
+}
+
+template <int D>
+__device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
+    const int w = warp / 4;                       // stream
+    const int r = (warp % 4) * 32 + lane;         // row of the tile, lane of tensor memory
+    const int TM = kM / p.G, U = 2 * TM;
+    const uint32_t quad = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tS = sm.tmem_base + quad + kColS + 128 * w;
+    const uint32_t tO = sm.tmem_base + quad + kColO;
+    int* err = p.err;
+    const bool negative = p.scale_log2 < 0.f;
+    const float c = fmaxf(fabsf(p.scale_log2), 0x1p-100f);  // (0: -inf times it stays -inf)
+    const int tok_r = r / p.G, head_r = r - tok_r * p.G;
+    uint32_t ns = 0, n_two = 0;
+    for (int k = 0;; ++k) {
+        const int i = k % kPieces;
+        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        const Piece pc = sm.piece[i];
+        if (pc.t0 < 0) break;
+        const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
+        const bool valid = tok_r < TM && token < pc.n;
+        const bool busy = __any_sync(0xffffffffu, valid);
+        const int pos = valid ? pc.L - pc.n + token : 0x3fffffff;
+        float m = -INFINITY, l = 0.f;  // reference maximum (raw score units), sum
+        bool ok = true;
+        const int step = pc.pair ? 1 : 2;
+        const int t_first = pc.t0 + (pc.pair ? 0 : w);
+        for (int t = t_first; t < pc.t1; t += step) {
+            if (!(ok = mbar_wait(&sm.sfull[w], ns & 1, err))) break;
+            ++ns;
+            if (busy) {
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) tmem_ld_32x32b_x32(tS + 32 * a, s[a]);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) tmem_ld_wait(s[a]);
+                if (negative) {
+#pragma unroll
+                    for (int a = 0; a < 128; ++a) s[a / 32][a % 32] ^= 0x80000000u;
+                }
+                const int ts = tile_of(pc, t) * kN;
+                const int hi = pos - ts;  // last key seen
+                const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
+                if (__any_sync(0xffffffffu, hi < kN - 1 || (lo > 0 && sk < kN))) {
+#pragma unroll
+                    for (int a = 0; a < 128; ++a)
+                        if (a > hi || (a < lo && a >= sk)) s[a / 32][a % 32] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    mx[a] = __uint_as_float(s[a][0]);
+#pragma unroll
+                    for (int e = 1; e < 31; e += 2)
+                        mx[a] = max3(mx[a], __uint_as_float(s[a][e]), __uint_as_float(s[a][e + 1]));
+                    mx[a] = fmaxf(mx[a], __uint_as_float(s[a][31]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool raise = (top - m) * c > kGrowth;  // (m = -inf: always)
+                float fade = 1.f;
+                if (raise) {
+                    fade = fast_exp2((m - top) * c);
+                    m = top;
+                    l *= fade;
+                }
+                if (t != t_first && __any_sync(0xffffffffu, raise)) {
+                    // the products of all earlier tiles are complete: this tile's scores were
+                    // issued behind them
+#pragma unroll
+                    for (int a = 0; a < D / 32; ++a) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(tO + 128 * w + 32 * a, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                        tmem_st_32x32b_x32(tO + 128 * w + 32 * a, o);
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                const uint64_t c2 = pair64(c, c), n2 = pair64(-mc, -mc);
+                uint64_t sum[2] = {pair64(l, 0.f), pair64(0.f, 0.f)};
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    uint32_t pr[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int x = 64 * a + 2 * e;
+                        const uint64_t y = fma2(pair64(__uint_as_float(s[x / 32][x % 32]),
+                                                       __uint_as_float(s[x / 32][x % 32 + 1])), c2, n2);
+                        float u, v;
+                        unpair64(y, u, v);
+                        u = fast_exp2(u);
+                        v = fast_exp2(v);
+                        sum[e & 1] = add2(sum[e & 1], pair64(u, v));
+                        pr[e] = pack_bf16(u, v);
+                    }
+                    tmem_st_32x32b_x32(tS + 32 * a, pr);
+                }
+                float x0, x1;
+                unpair64(add2(sum[0], sum[1]), x0, x1);
+                l = x0 + x1;
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.pready[w]);
+        }
+        if (!ok) break;
+        // ---- the piece's end
+        float mc = m == -INFINITY ? -INFINITY : m * c;  // log2 units
+        const bool two = !pc.pair;                      // both streams hold a part
+        float oth_m = -INFINITY, oth_l = 0.f;
+        const bool has_own = t_first < pc.t1, has_oth = two && pc.t0 + (1 - w) < pc.t1;
+        if (two && pc.t1 > pc.t0) {
+            if (!(ok = mbar_wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
+            sm.stat[w][r][0] = mc;
+            sm.stat[w][r][1] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.statw[w]);
+            if (!(ok = mbar_wait(&sm.statw[1 - w], n_two & 1, err))) break;
+            oth_m = sm.stat[1 - w][r][0];
+            oth_l = sm.stat[1 - w][r][1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.statr[1 - w]);
+            ++n_two;
+        }
+        if (!(ok = mbar_wait(&sm.ofull[w], k & 1, err))) break;
+        if (two && !(ok = mbar_wait(&sm.ofull[1 - w], k & 1, err))) break;
+        tc_fence_after();
+        const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
+        float top = fmaxf(mc, oth_m), own_f = mc == -INFINITY ? 0.f : fast_exp2(mc - top),
+              oth_f = oth_m == -INFINITY ? 0.f : fast_exp2(oth_m - top);
+        // (a sum that is NaN has a maximum of -inf where all of its scores are NaN)
+        float sum = (mc == -INFINITY ? l : l * own_f) + (oth_m == -INFINITY ? oth_l : oth_l * oth_f);
+        if (mc == -INFINITY && oth_m == -INFINITY) own_f = oth_f = 1.f;
+        float scale = 1.f;
+        const int head = pc.h * p.G + head_r;
+        const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
+        if (pc.slot < 0) {
+            float ref = top;
+            if (p.sink_logit && valid) {
+                const float sink = p.sink_logit[head] * kLog2e;
+                ref = fmaxf(top, sink);
+                const float f = top == -INFINITY ? 1.f : fast_exp2(top - ref);
+                sum = sum * f + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
+                scale = f;
+            }
+            scale = sum == 0.f ? 0.f : scale / sum;
+            if (valid && p.lse_out && (!two || w == 0))
+                p.lse_out[row] = sum == 0.f ? -INFINITY
+                                            : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
+        } else if (valid && (!two || w == 0)) {
+            float2* ml = reinterpret_cast<float2*>(p.part_ml) +
+                         static_cast<size_t>(pc.slot) * 2 * kM + (two ? 0 : w * kM) + r;
+            *ml = make_float2(top, sum);
+        }
+        // one query tile: each warpgroup takes half of the columns, of both accumulators
+        const int col0 = two ? w * (D / 2) : 0, col1 = two ? col0 + D / 2 : D;
+        if (busy) {
+            for (int col = col0; col < col1; col += 32) {
+                float o[32];
+                {
+                    uint32_t a[32];
+                    if (has_own) {
+                        tmem_ld_32x32b_x32(tO + 128 * w + col, a);
+                        tmem_ld_wait(a);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = has_own ? __uint_as_float(a[e]) * own_f : 0.f;
+                    if (has_oth) {
+                        tmem_ld_32x32b_x32(tO + 128 * (1 - w) + col, a);
+                        tmem_ld_wait(a);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(a[e]), oth_f, o[e]);
+                    }
+                }
+                if (bad) add_cleared<D>(p, pc, U, valid ? pos : -1, col, o);
+                if (valid && pc.slot < 0) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D + col);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = make_uint4(pack_bf16(o[8 * e] * scale, o[8 * e + 1] * scale),
+                                            pack_bf16(o[8 * e + 2] * scale, o[8 * e + 3] * scale),
+                                            pack_bf16(o[8 * e + 4] * scale, o[8 * e + 5] * scale),
+                                            pack_bf16(o[8 * e + 6] * scale, o[8 * e + 7] * scale));
+                } else if (valid) {
+                    float4* dst = reinterpret_cast<float4*>(
+                        p.part_o + (static_cast<size_t>(pc.slot) * 2 * kM + (two ? 0 : w * kM) + r) * D + col);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if (two) {
+                mbar_arrive(&sm.ofree[0]);
+                mbar_arrive(&sm.ofree[1]);
+            } else {
+                mbar_arrive_n(&sm.ofree[w], 2);
+            }
+            mbar_arrive(&sm.pempty[i]);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_bf16_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const PrefillParams p) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (smem_u32(raw) & 1023u) {  // the layout needs a 1024-byte aligned window
+        griddep_wait();
+        if (threadIdx.x == 0) {
+            record_error(p.err, KVD_ERR_CUDA);
+            p.head[blockIdx.x].nt = 0;
+        }
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Layout<D>::kStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.issued[i], 1);
+            mbar_init(&sm.fixed[i], kFixWarps);
+        }
+        mbar_init(&sm.qfull, 1);
+        mbar_init(&sm.qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.sfull[i], 1);
+            mbar_init(&sm.pready[i], 4);
+            mbar_init(&sm.ofull[i], 1);
+            mbar_init(&sm.ofree[i], 8);
+            mbar_init(&sm.statw[i], 4);
+            mbar_init(&sm.statr[i], 4);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&sm.pfull[i], 1);
+            mbar_init(&sm.pempty[i], 1 + kFixWarps + kSoftWarps);
+        }
+        mbar_init(&sm.end, 1);
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    if (warp < kSoftWarps) {
+        regs_more<kRegsSoft>();
+        softmax_role<D>(p, sm, warp, lane);
+    } else {
+        regs_fewer<kRegsOther>();
+        if (warp == kWarpLoad) {
+            load_role<D>(p, sm, &tq, &tk, &tv, lane);
+        } else if (warp == kWarpMma) {
+            if (lane == 0) mma_role<D>(p, sm);
+            __syncwarp();
+        } else {
+            fix_role<D>(p, sm, warp - kWarpFix, lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) tmem_dealloc(sm.tmem_base, 512);
+}
+
+// Merges the pieces of the unit whose first piece CTA x of the main launch took: a warp a row, the
+// pieces in their order.
+template <int D>
+__global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams p, int n_cta) {
+    griddep_wait();
+    const PrefillHead hd = p.head[blockIdx.x];
+    if (hd.nt == 0) return;
+    const int TM = kM / p.G;
+    const int lane = threadIdx.x % 32;
+    const bool pair = hd.n - hd.tok0 > TM;
+    const int rows = pair ? 2 * kM : kM;
+    constexpr int E = D / 32;
+    for (int r = blockIdx.y * 4 + threadIdx.x / 32; r < rows; r += gridDim.y * 4) {
+        const int t = r % kM / p.G, token = hd.tok0 + (r / kM) * TM + t;
+        if (t >= TM || token >= hd.n) continue;
+        const int head = hd.h * p.G + (r % kM - t * p.G);
+        float top = -INFINITY, sum = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int c = blockIdx.x; c <= hd.last; ++c) {
+            // (a range that rounding left without a tile of the unit wrote nothing)
+            if (cut_tile(range_start(hd.V, c, n_cta) - hd.u, hd.w, hd.nt) ==
+                cut_tile(range_start(hd.V, c + 1, n_cta) - hd.u, hd.w, hd.nt))
+                continue;
+            const size_t at = static_cast<size_t>(2 * c + (c == static_cast<int>(blockIdx.x))) * 2 * kM + r;
+            const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[at];
+            const float nt = fmaxf(top, ml.x);
+            const float f0 = top == -INFINITY ? 1.f : fast_exp2(top - nt);
+            const float f1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - nt);
+            const float* src = p.part_o + at * D + lane * E;
+            float x[E];
+            if (E == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(src);
+                x[0] = v.x, x[1] = v.y, x[E - 2] = v.z, x[E - 1] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(src);
+                x[0] = v.x, x[1] = v.y;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + x[e] * f1;
+            sum = sum * f0 + ml.y * f1;
+            top = nt;
+        }
+        float scale = 1.f;
+        if (p.sink_logit) {
+            const float sink = p.sink_logit[head] * kLog2e, nt = fmaxf(top, sink);
+            const float f = top == -INFINITY ? 1.f : fast_exp2(top - nt);
+            sum = sum * f + (sink == -INFINITY ? 0.f : fast_exp2(sink - nt));
+            scale = f;
+            top = nt;
+        }
+        scale = sum == 0.f ? 0.f : scale / sum;
+        const long long row = static_cast<long long>(hd.c0 + token) * p.Hq + head;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * D + lane * E;
+        if (E == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16(o[0] * scale, o[1] * scale), pack_bf16(o[E - 2] * scale, o[E - 1] * scale));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[0] * scale, o[1] * scale);
+        if (p.lse_out && lane == 0)
+            p.lse_out[row] = sum == 0.f ? -INFINITY
+                                        : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
+    }
+}
+
+struct Plan {
+    size_t off_ml, off_o, total;
+};
+Plan make_plan(int D) {
+    const size_t n = static_cast<size_t>(num_sms());
+    Plan pl;
+    pl.off_ml = (n * sizeof(PrefillHead) + 255) & ~static_cast<size_t>(255);
+    pl.off_o = pl.off_ml + n * 2 * 2 * kM * 8;
+    pl.total = pl.off_o + n * 2 * 2 * kM * D * 4;
+    return pl;
+}
+
+template <int D>
+int launch(PrefillParams p, void* ws, cudaStream_t stream) {
+    const Plan pl = make_plan(D);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    p.head = reinterpret_cast<PrefillHead*>(base);
+    p.part_ml = reinterpret_cast<float*>(base + pl.off_ml);
+    p.part_o = reinterpret_cast<float*>(base + pl.off_o);
+    CUtensorMap tq, tk, tv;
+    const uint64_t blocks = D / 64;
+    {
+        const uint64_t dims[4] = {64, static_cast<uint64_t>(p.Hq), static_cast<uint64_t>(p.T), blocks};
+        const uint64_t strides[3] = {D * 2, static_cast<uint64_t>(p.q_stride) * 2, 128};
+        const uint32_t box[4] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(kM / p.G), 1};
+        if (make_tmap_bf16_4d(&tq, p.q, dims, strides, box) != KVD_OK) return KVD_ERR_CUDA;
+    }
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap* map = i ? &tv : &tk;
+        if (p.block_table) {
+            const uint32_t rows = 1u << std::min(p.page_shift, 7);
+            const uint64_t dims[4] = {64, (static_cast<uint64_t>(p.num_pages) * p.Hkv) << p.page_shift, blocks, 1};
+            const uint64_t strides[3] = {D * 2, 128, D * 2};
+            const uint32_t box[4] = {64, rows, rows == kN ? static_cast<uint32_t>(blocks) : 1, 1};
+            if (make_tmap_bf16_4d(map, i ? p.v : p.k, dims, strides, box) != KVD_OK) return KVD_ERR_CUDA;
+        } else {
+            // (without keys nothing is loaded; any address makes a map)
+            const void* at = p.Tk > 0 ? (i ? p.v : p.k) : p.q;
+            const uint64_t stride = static_cast<uint64_t>(i ? p.v_stride : p.k_stride) * 2;
+            const uint64_t dims[4] = {64, static_cast<uint64_t>(std::max(p.Tk, 1)), blocks,
+                                      static_cast<uint64_t>(p.Hkv)};
+            const uint64_t strides[3] = {stride, 128, D * 2};
+            const uint32_t box[4] = {64, kN, static_cast<uint32_t>(blocks), 1};
+            if (make_tmap_bf16_4d(map, at, dims, strides, box) != KVD_OK) return KVD_ERR_CUDA;
+        }
+    }
+    auto kernel = prefill_bf16_kernel<D>;
+    constexpr int smem = static_cast<int>(sizeof(Smem<D>));
+    static_assert(smem <= 227 * 1024, "prefill shared memory");
+    static const cudaError_t set =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (set != cudaSuccess) return KVD_ERR_CUDA;
+    const int TM = kM / p.G, U = 2 * TM, n_cta = num_sms();
+    p.unit_cost = 192;
+    p.flat_slack = 4 * kN;
+    // at most so many units, each at most so long: where both are few, no unit is cut
+    const long long units = static_cast<long long>(p.Hkv) * (p.T / U + std::min(p.B, p.T));
+    if (launch_kernel(kernel, dim3(static_cast<unsigned>(n_cta)), dim3(kThreads), smem, stream, tq, tk,
+                      tv, p) != cudaSuccess)
+        return KVD_ERR_CUDA;
+    const long long keys = p.block_table ? static_cast<long long>(p.max_pages) << p.page_shift : p.Tk;
+    const bool never_cut = units <= n_cta && std::min<long long>(keys, p.window > 0 ? p.window + p.n_sink + U + kN : keys) + U + p.unit_cost <= p.flat_slack;
+    if (!never_cut &&
+        launch_kernel(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(n_cta), 8), dim3(128), 0, stream,
+                      p, n_cta) != cudaSuccess)
+        return KVD_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t prefill_ws_bytes(int D) { return make_plan(D).total; }
+
+int prefill_bf16_launch(const PrefillParams& p, int D, void* ws, cudaStream_t stream) {
+    return D == 64 ? launch<64>(p, ws, stream) : launch<128>(p, ws, stream);
+}
+
+}  // namespace kvd

@@ -223,10 +223,8 @@ int launch(const PrefillParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int prefill_launch(const PrefillParams& p, int D, int dtype, cudaStream_t stream) {
-    if (dtype == KVD_F32)
-        return D == 64 ? launch<64, float>(p, stream) : launch<128, float>(p, stream);
-    return D == 64 ? launch<64, __nv_bfloat16>(p, stream) : launch<128, __nv_bfloat16>(p, stream);
+int prefill_f32_launch(const PrefillParams& p, int D, cudaStream_t stream) {
+    return D == 64 ? launch<64, float>(p, stream) : launch<128, float>(p, stream);
 }
 
 }  // namespace kvd
