@@ -46,7 +46,7 @@ constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 10;
 constexpr int kFixWarps = 2;
 constexpr int kThreads = 384;
 // two softmax warpgroups and one of the others share what the CTA was launched with: 168 a thread
-constexpr int kRegsSoft = 216, kRegsOther = 72;
+constexpr int kRegsSoft = 200, kRegsOther = 104;
 static_assert(2 * kRegsSoft + kRegsOther <= 3 * 168, "registers");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -80,7 +80,7 @@ struct Smem {
     // values at a mask's edge: under way (a look at `full` alone could take an earlier round of the
     // ring for this one), and looked through
     uint64_t issued[Layout<D>::kStages], fixed[Layout<D>::kStages];
-    uint64_t qfull, qempty, sfull[2], pready[2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
+    uint64_t qfull, qempty, sfull[2], pready[2][2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
     uint64_t statw[2], statr[2];                      // a stream's stat written; read by the other
     uint64_t end;
     Piece piece[kPieces];
@@ -220,6 +220,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// 16 columns of tensor memory, one lane a thread; the load's results are there behind the wait.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t t, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t t, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // S (tensor memory) = Q (128 rows) K^T (128 keys), both K-major in shared memory.
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
@@ -232,14 +253,17 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
     }
 }
 
-// O (tensor memory) (+)= P (tensor memory, 128 x 128) V (128 tokens, read MN-major).
+// O (tensor memory) (+)= half of P (tensor memory, 128 x 64 of its 128 keys) V (their 64 tokens, read
+// MN-major).
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t pt, uint32_t v, bool accumulate) {
+__device__ __forceinline__ void issue_pv_half(uint32_t o, uint32_t pt, uint32_t v, int half,
+                                              bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32(kM, D, 0, 1);
-    const uint64_t b = sw128_mnmajor_desc(v, kN * 128);
+    const uint64_t b = sw128_mnmajor_desc(v + half * (kN / 2) * 128, kN * 128);
 #pragma unroll
-    for (int ks = 0; ks < kN / 16; ++ks)
-        tc_mma_bf16_ts(o, pt + ks * 8, b + static_cast<uint64_t>((ks * 16 * 128) >> 4), idesc,
+    for (int ks = 0; ks < kN / 32; ++ks)
+        tc_mma_bf16_ts(o, pt + half * (kN / 4) + ks * 8,
+                       b + static_cast<uint64_t>((ks * 16 * 128) >> 4), idesc,
                        (accumulate || ks > 0) ? 1u : 0u);
 }
 
@@ -562,29 +586,55 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
             tc_commit(&sm.empty[slot(t)]);
         }
         if (ok && nt > 0 && nt <= la) tc_commit(&sm.qempty);
-        for (int t = 0; t < nt && ok; ++t) {
-            const int iv = item_of_v(t, nt, la), ik = item_of_k(t + la, la);
-            const bool more = t + la < nt;
-            for (int w = pc.pair ? 0 : (t & 1); w <= (pc.pair ? 1 : (t & 1)); ++w) {
-                const bool first = pc.pair ? t == 0 : t < 2;
-                if (first && !(ok = wait_ofree(w))) break;
-                if ((w == 0 || !pc.pair) && !(ok = wait_v(t))) break;
-                if (!(ok = mbar_wait(&sm.pready[w], np[w] & 1, err))) break;
-                ++np[w];
+        // stream w: the value product of its next tile, in halves as its weights come
+        auto pv = [&](int w, uint32_t v, bool first) {
+            const uint32_t o = tmem + kColO + 128 * w, pt = tmem + kColS + 128 * w;
+            for (int half = 0; half < 2; ++half) {
+                if (!mbar_wait(&sm.pready[w][half], np[w] & 1, err)) return false;
                 tc_fence_after();
-                issue_pv<D>(tmem + kColO + 128 * w, tmem + kColS + 128 * w, kv(iv), !first);
-                if (w == 1 || !pc.pair) tc_commit(&sm.empty[slot(iv)]);
+                issue_pv_half<D>(o, pt, v, half, !first || half > 0);
+            }
+            ++np[w];
+            return true;
+        };
+        if (pc.pair) {
+            for (int t = 0; t < nt; ++t) {
+                const int iv = 2 * t + 1, ik = iv + 1;
+                const uint32_t v = kv(iv), kt = kv(ik);
+                const bool more = t + 1 < nt;
+                if (t == 0 && !(ok = wait_ofree(0))) break;
+                if (!(ok = wait_v(t) && pv(0, v, t == 0))) break;
                 if (more) {
-                    if ((w == 0 || !pc.pair)) {
-                        if (!(ok = wait_full(ik))) break;
-                        tc_fence_after();
-                    }
-                    issue_qk<D>(tmem + kColS + 128 * w, q[pc.pair ? w : 0], kv(ik));
+                    if (!(ok = wait_full(ik))) break;
+                    issue_qk<D>(tmem + kColS, q[0], kt);
+                    tc_commit(&sm.sfull[0]);
+                } else {
+                    tc_commit(&sm.ofull[0]);
+                }
+                if (t == 0 && !(ok = wait_ofree(1))) break;
+                if (!(ok = pv(1, v, t == 0))) break;
+                tc_commit(&sm.empty[slot(iv)]);
+                if (more) {
+                    issue_qk<D>(tmem + kColS + 128, q[1], kt);
+                    tc_commit(&sm.sfull[1]);
+                    tc_commit(&sm.empty[slot(ik)]);
+                    if (t + 2 == nt) tc_commit(&sm.qempty);
+                } else {
+                    tc_commit(&sm.ofull[1]);
+                }
+            }
+        } else {
+            for (int t = 0; t < nt; ++t) {
+                const int w = t & 1, iv = item_of_v(t, nt, 2), ik = item_of_k(t + 2, 2);
+                if (t < 2 && !(ok = wait_ofree(w))) break;
+                if (!(ok = wait_v(t) && pv(w, kv(iv), t < 2))) break;
+                tc_commit(&sm.empty[slot(iv)]);
+                if (t + 2 < nt) {
+                    if (!(ok = wait_full(ik))) break;
+                    issue_qk<D>(tmem + kColS + 128 * w, q[0], kv(ik));
                     tc_commit(&sm.sfull[w]);
-                    if (w == 1 || !pc.pair) {
-                        tc_commit(&sm.empty[slot(ik)]);
-                        if (t + la == nt - 1) tc_commit(&sm.qempty);
-                    }
+                    tc_commit(&sm.empty[slot(ik)]);
+                    if (t + 3 == nt) tc_commit(&sm.qempty);
                 } else {
                     tc_commit(&sm.ofull[w]);
                 }
@@ -659,17 +709,15 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane
 }
 
 // ----------------------------------------------------------------------------------- softmax
-// What a row gets back of the values that were cleared: v itself, where the row sees it.
+// What a row gets back, in one column, of the values that were cleared: v itself, where the row sees it.
 template <int D>
-__device__ __noinline__ void add_cleared(const PrefillParams& p, const Piece& pc, int U, int pos,
-                                         int col, float (&o)[32]) {
+__device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, int U, int pos, int col) {
+    float sum = 0.f;
     for (int t = pc.t0; t < pc.t1; ++t) {
         const int tile = tile_of(pc, t);
         if (!at_edge(p, pc, tile, U)) continue;
-        for (int r = 0; r < kN; ++r) {
-            const int key = tile * kN + r;
-            if (key >= pc.L) break;
-            const bool seen = key <= pos && (p.window <= 0 || key > pos - p.window || key < p.n_sink);
+        for (int key = tile * kN; key < min(tile * kN + kN, min(pc.L, pos + 1)); ++key) {
+            if (p.window > 0 && key <= pos - p.window && key >= p.n_sink) continue;
             const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v);
             if (p.block_table) {
                 const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
@@ -679,13 +727,11 @@ __device__ __noinline__ void add_cleared(const PrefillParams& p, const Piece& pc
             } else {
                 v += static_cast<long long>(pc.k0 + key) * p.v_stride + pc.h * D;
             }
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const float x = __bfloat162float(v[col + c]);
-                if (seen && !isfinite(x)) o[c] += x;
-            }
+            const float x = __bfloat162float(v[col]);
+            if (!isfinite(x)) sum += x;
         }
     }
+    return sum;
 }
 
 template <int D>
@@ -720,32 +766,35 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
             if (busy) {
                 tc_fence_after();
                 uint32_t s[4][32];
-#pragma unroll
-                for (int a = 0; a < 4; ++a) tmem_ld_32x32b_x32(tS + 32 * a, s[a]);
-#pragma unroll
-                for (int a = 0; a < 4; ++a) tmem_ld_wait(s[a]);
-                if (negative) {
-#pragma unroll
-                    for (int a = 0; a < 128; ++a) s[a / 32][a % 32] ^= 0x80000000u;
-                }
                 const int ts = tile_of(pc, t) * kN;
                 const int hi = pos - ts;  // last key seen
                 const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
-                if (__any_sync(0xffffffffu, hi < kN - 1 || (lo > 0 && sk < kN))) {
-#pragma unroll
-                    for (int a = 0; a < 128; ++a)
-                        if (a > hi || (a < lo && a >= sk)) s[a / 32][a % 32] = 0xff800000u;
-                }
-                float mx[4];
+                const bool edge = __any_sync(0xffffffffu, hi < kN - 1 || (lo > 0 && sk < kN));
+                tmem_ld_32x32b_x32(tS, s[0]);
+                float top = -INFINITY;
 #pragma unroll
                 for (int a = 0; a < 4; ++a) {
-                    mx[a] = __uint_as_float(s[a][0]);
+                    tmem_ld_wait(s[a]);
+                    if (a < 3) tmem_ld_32x32b_x32(tS + 32 * (a + 1), s[a < 3 ? a + 1 : 3]);
+                    if (negative) {
 #pragma unroll
-                    for (int e = 1; e < 31; e += 2)
-                        mx[a] = max3(mx[a], __uint_as_float(s[a][e]), __uint_as_float(s[a][e + 1]));
-                    mx[a] = fmaxf(mx[a], __uint_as_float(s[a][31]));
+                        for (int e = 0; e < 32; ++e) s[a][e] ^= 0x80000000u;
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * a + e > hi || (32 * a + e < lo && 32 * a + e >= sk))
+                                s[a][e] = 0xff800000u;
+                    }
+                    float mx[2] = {__uint_as_float(s[a][0]), __uint_as_float(s[a][1])};
+#pragma unroll
+                    for (int e = 2; e < 30; e += 4) {
+                        mx[0] = max3(mx[0], __uint_as_float(s[a][e]), __uint_as_float(s[a][e + 1]));
+                        mx[1] = max3(mx[1], __uint_as_float(s[a][e + 2]), __uint_as_float(s[a][e + 3]));
+                    }
+                    mx[0] = max3(mx[0], __uint_as_float(s[a][30]), __uint_as_float(s[a][31]));
+                    top = max3(top, mx[0], mx[1]);
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool raise = (top - m) * c > kGrowth;  // (m = -inf: always)
                 float fade = 1.f;
                 if (raise) {
@@ -756,15 +805,14 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                 if (t != t_first && __any_sync(0xffffffffu, raise)) {
                     // the products of all earlier tiles are complete: this tile's scores were
                     // issued behind them
+#pragma unroll 1
+                    for (int a = 0; a < D / 16; ++a) {
+                        uint32_t o[16];
+                        tmem_ld_x16(tO + 128 * w + 16 * a, o);
 #pragma unroll
-                    for (int a = 0; a < D / 32; ++a) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(tO + 128 * w + 32 * a, o);
-                        tmem_ld_wait(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-                        tmem_st_32x32b_x32(tO + 128 * w + 32 * a, o);
+                        tmem_st_x16(tO + 128 * w + 16 * a, o);
                     }
                 }
                 const float mc = m == -INFINITY ? 0.f : m * c;
@@ -772,29 +820,34 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                 uint64_t sum[2] = {pair64(l, 0.f), pair64(0.f, 0.f)};
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    uint32_t pr[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int x = 64 * a + 2 * e;
-                        const uint64_t y = fma2(pair64(__uint_as_float(s[x / 32][x % 32]),
-                                                       __uint_as_float(s[x / 32][x % 32 + 1])), c2, n2);
-                        float u, v;
-                        unpair64(y, u, v);
-                        u = fast_exp2(u);
-                        v = fast_exp2(v);
-                        sum[e & 1] = add2(sum[e & 1], pair64(u, v));
-                        pr[e] = pack_bf16(u, v);
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t pr[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t y = fma2(pair64(__uint_as_float(s[2 * a + b][2 * e]),
+                                                           __uint_as_float(s[2 * a + b][2 * e + 1])), c2, n2);
+                            float u, v;
+                            unpair64(y, u, v);
+                            u = fast_exp2(u);
+                            v = fast_exp2(v);
+                            sum[e & 1] = add2(sum[e & 1], pair64(u, v));
+                            pr[e] = pack_bf16(u, v);
+                        }
+                        tmem_st_x16(tS + 32 * a + 16 * b, pr);
                     }
-                    tmem_st_32x32b_x32(tS + 32 * a, pr);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.pready[w][a]);
                 }
                 float x0, x1;
                 unpair64(add2(sum[0], sum[1]), x0, x1);
                 l = x0 + x1;
-                tmem_st_wait();
-                tc_fence_before();
+            } else if (lane == 0) {
+                mbar_arrive(&sm.pready[w][0]);
+                mbar_arrive(&sm.pready[w][1]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.pready[w]);
         }
         if (!ok) break;
         // ---- the piece's end
@@ -865,7 +918,11 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                         for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(a[e]), oth_f, o[e]);
                     }
                 }
-                if (bad) add_cleared<D>(p, pc, U, valid ? pos : -1, col, o);
+                if (bad) {
+                    const int seen = valid ? pos : -1;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] += cleared<D>(p, pc, U, seen, col + e);
+                }
                 if (valid && pc.slot < 0) {
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D + col);
 #pragma unroll
@@ -924,7 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.qempty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.sfull[i], 1);
-            mbar_init(&sm.pready[i], 4);
+            mbar_init(&sm.pready[i][0], 4);
+            mbar_init(&sm.pready[i][1], 4);
             mbar_init(&sm.ofull[i], 1);
             mbar_init(&sm.ofree[i], 8);
             mbar_init(&sm.statw[i], 4);
