@@ -200,7 +200,7 @@ int cache_read_launch(const CacheReadParams& p, bool q4, int D, int dtype, cudaS
 // The first piece of a unit of the prefill attention that was cut (prefill_bf16.cu); nt == 0: none.
 struct PrefillHead {
     int c0, n, h, tok0;        // first row, new tokens, KV head, the unit's first new token
-    int last, nt;              // CTA that has its last piece; tiles
+    int nt;                    // tiles
     long long u, w, V;         // the unit's position and length in the work list, the list's length
 };
 
@@ -223,6 +223,8 @@ struct PrefillParams {
     float scale_log2;
     // bfloat16: how work is cut, and the pieces of units that were cut
     int unit_cost, flat_slack; // keys that a unit's start and end are worth; see load_role
+    int n_cta;                 // CTAs, and 1 / n_cta
+    double inv_cta;
     PrefillHead* head;         // [CTAs]
     float *part_ml, *part_o;   // [2 CTAs, 256 rows] (maximum, sum) and [.., D] unnormalised outputs
 };

@@ -11,14 +11,14 @@
 //
 // One persistent CTA an SM, roles by warp:
 //   * loads: query tiles and a ring of 128-token key and value tiles, all by TMA;
-//   * products: one thread issues S = Q K^T (tcgen05, 128 x 128, operands in shared memory) and
-//     O += P V (P in tensor memory, where it takes the place of its S);
+//   * products: S = Q K^T (tcgen05, 128 x 128, operands in shared memory) and O += P V (P in tensor
+//     memory, where it takes the place of its S), issued by one thread for each stream;
 //   * softmax: two warpgroups, one row a thread, each with a score tile and an output accumulator of
 //     its own in tensor memory, so that one's exponentials run under the other's products. The row's
 //     reference maximum is only raised, and O rescaled, when a maximum grows by more than 2^8;
 //     weights are then at most 2^8 and are rounded to bfloat16 (the value product's operands have one
 //     type), their sums are float32 sums of the unrounded weights.
-//   * values: at the edges of the mask two warps clear the value rows behind the sequence's end and
+//   * values: at the edges of the mask a warp clears the value rows behind the sequence's end and
 //     every value that is not finite, before a zero weight can meet them; the rows that see such a
 //     value get it back at the end.
 // A unit of at most 128 rows (draft tokens, a prompt's end) is one query tile: the two warpgroups then
@@ -40,13 +40,13 @@ namespace {
 
 constexpr int kM = 128;     // rows of a query tile
 constexpr int kN = 128;     // keys of a tile
+constexpr int kMaxCtas = 256;  // of the main launch
 constexpr int kPieces = 4;  // ring of work descriptions
 constexpr int kSoftWarps = 8;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 10;
-constexpr int kFixWarps = 2;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 11;  // products: warp 9 + stream
 constexpr int kThreads = 384;
 // two softmax warpgroups and one of the others share what the CTA was launched with: 168 a thread
-constexpr int kRegsSoft = 200, kRegsOther = 104;
+constexpr int kRegsSoft = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoft + kRegsOther <= 3 * 168, "registers");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,7 +82,7 @@ struct Smem {
     uint64_t issued[Layout<D>::kStages], fixed[Layout<D>::kStages];
     uint64_t qfull, qempty, sfull[2], pready[2][2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
     uint64_t statw[2], statr[2];                      // a stream's stat written; read by the other
-    uint64_t end;
+    uint64_t end[2];
     Piece piece[kPieces];
     int bad[kPieces];                                 // a value at a mask's edge was not finite
     uint32_t tmem_base;
@@ -128,16 +128,20 @@ __device__ __forceinline__ Seq load_seq(const PrefillParams& p, int b, int* err)
 // it. flat: every unit counts 1.)
 struct Weigh {
     long long base, cap;
-    int U, fixed;
+    int U, fixed, free;  // free: units before the window cuts their keys
     bool flat;
     __device__ __forceinline__ Weigh(const PrefillParams& p, const Seq& s, int u, bool f)
-        : base(max(0, s.L - s.n)), U(u), fixed(p.unit_cost), flat(f) {
-        cap = p.window > 0 ? static_cast<long long>(p.window) + U + kN + min(p.n_sink, s.L) : 1LL << 40;
+        : base(max(0, s.L - s.n)), cap(0), U(u), fixed(p.unit_cost), free(0x7fffffff), flat(f) {
+        if (p.window > 0) {
+            const int c = min(p.window, 1 << 30) + U + kN + min(p.n_sink, s.L) - 1;  // < 2^31
+            cap = c;
+            free = c > base ? (c - static_cast<int>(base)) / U : 0;
+        }
     }
-    __device__ __forceinline__ long long upto(long long m) const {
+    __device__ __forceinline__ long long upto(int m) const {
         if (flat) return m;
-        const long long free = cap > base ? (cap - base) / U : 0, m1 = min(m, free);
-        return m * fixed + m1 * base + U * (m1 * (m1 + 1) / 2) + (m - m1) * cap;
+        const long long m1 = min(m, free);
+        return static_cast<long long>(m) * fixed + m1 * base + U * (m1 * (m1 + 1) / 2) + (m - m1) * cap;
     }
 };
 
@@ -169,7 +173,6 @@ __device__ __forceinline__ int tile_of(const Piece& u, int t) {
 }
 // Ring items of a piece of nt tiles: `la` key tiles, then value tile t and key tile t + la in turn.
 __device__ __forceinline__ int item_of_v(int t, int nt, int la) { return min(2 * t + la, 2 * nt - 1); }
-__device__ __forceinline__ int item_of_k(int t, int la) { return t < la ? t : 2 * t - (la - 1); }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
                                             int y, int z, int w) {
@@ -267,10 +270,31 @@ __device__ __forceinline__ void issue_pv_half(uint32_t o, uint32_t pt, uint32_t 
                        (accumulate || ks > 0) ? 1u : 0u);
 }
 
-// Range of CTA c: [V c / n, V (c + 1) / n); tile at which offset y of a unit of length w cuts it.
-__device__ __forceinline__ long long range_start(long long V, int c, int n) { return V * c / n; }
-__device__ __forceinline__ int cut_tile(long long y, long long w, int nt) {
-    return y <= 0 ? 0 : y >= w ? nt : static_cast<int>(y * nt / w);
+// Ranges: CTA c of n takes positions [range_start(c), range_start(c + 1)) of a list of length V. (No
+// quotient: any rule will do that is the same for all CTAs and ascends from 0 to V.)
+__device__ __forceinline__ long long range_start(const PrefillParams& p, long long V, int c) {
+    return c >= p.n_cta ? V : static_cast<long long>(static_cast<double>(V) * (c * p.inv_cta));
+}
+// Tile at which offset y of a unit of length w and nt tiles cuts it.
+__device__ __forceinline__ int cut_tile(const PrefillParams& p, long long y, long long w, int nt) {
+    if (y <= 0) return 0;
+    if (y >= w) return nt;
+    return static_cast<int>(min(static_cast<long long>(nt), max(0LL, (y - p.unit_cost) / kN)));
+}
+
+// Largest i in [0, n) with f(i) <= x, f ascending, f(0) <= x; by the warp, 32 at a time.
+template <typename F>
+__device__ __forceinline__ int last_below(int n, long long x, int lane, F&& f) {
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const bool le = lane * step < n && f(lo + lane * step) <= x;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int k = m ? 31 - __clz(m) : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo;
 }
 
 // ------------------------------------------------------------------------------------- loads
@@ -279,7 +303,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
                           const CUtensorMap* tk, const CUtensorMap* tv, int lane) {
     using Ly = Layout<D>;
     const int TM = kM / p.G, U = 2 * TM;
-    const int cta = blockIdx.x, n_cta = gridDim.x;
+    const int cta = blockIdx.x, n_cta = p.n_cta;
     int* err = p.err;
     // how long the list is
     long long V = 0, units = 0, longest = 0;
@@ -309,9 +333,10 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
         longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, off));
     }
     // few short units: a CTA each, nothing is cut
-    const bool flat = units <= n_cta && longest <= V / n_cta + p.flat_slack;
+    const bool flat = units <= n_cta && longest <= range_start(p, V, 1) + p.flat_slack;
     if (flat) V = units;
-    const long long x0 = range_start(V, cta, n_cta), x1 = range_start(V, cta + 1, n_cta);
+    const long long x0 = flat ? min(static_cast<long long>(cta), V) : range_start(p, V, cta);
+    const long long x1 = flat ? min(cta + 1LL, V) : range_start(p, V, cta + 1);
 
     int ps = 0;               // pieces published
     uint32_t g = 0, nq = 0;   // ring items and query loads issued
@@ -381,14 +406,9 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
             long long u = at;  // position of the unit
             if (first_seq) {
                 long long rem = x0 - at;
-                h = static_cast<int>(rem / per_head);
+                h = last_below(p.Hkv, rem, lane, [&](int i) { return i * per_head; });
                 rem -= h * per_head;
-                int lo = 0, hi = nm - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (wt.upto(mid) <= rem) lo = mid; else hi = mid - 1;
-                }
-                m = lo;
+                m = last_below(nm, rem, lane, [&](int i) { return wt.upto(i); });
                 u = at + h * per_head + wt.upto(m);
             }
             for (; h < p.Hkv && u < x1 && ok; ++h, m = 0) {
@@ -402,8 +422,8 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
                     pc.k0 = s.k0;
                     pc.tok0 = m * U;
                     unit_tiles(p, s, pc.tok0, U, pc.nA, pc.tB, pc.nt);
-                    pc.t0 = cut_tile(x0 - u, w, pc.nt);
-                    pc.t1 = cut_tile(x1 - u, w, pc.nt);
+                    pc.t0 = cut_tile(p, x0 - u, w, pc.nt);
+                    pc.t1 = cut_tile(p, x1 - u, w, pc.nt);
                     pc.pair = s.n - pc.tok0 > TM;
                     const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
                     pc.slot = whole ? -1 : 2 * cta + (pc.t0 == 0 ? 1 : 0);
@@ -417,7 +437,6 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
                         hd.n = pc.n;
                         hd.h = h;
                         hd.tok0 = pc.tok0;
-                        hd.last = static_cast<int>(((start + w) * n_cta + V - 1) / V - 1);
                         hd.u = start;
                         hd.w = w;
                         hd.V = V;
@@ -542,121 +561,112 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
 }
 
 // ---------------------------------------------------------------------------------- products
+// One thread for each stream. A stream's products run in the order of their issue, so a score product
+// may overwrite the weights that the value product before it reads; of the other stream's tensor memory
+// it touches nothing. Issuing both streams from one thread left the tensor cores idle while that thread
+// waited and signalled (16385 tokens: 2.18 ms). Both threads pass every ring item in order, also one
+// that is the other's: a barrier's phase is known by its parity alone.
 template <int D>
-__device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
+__device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
     using Ly = Layout<D>;
     const int U = 2 * (kM / p.G);
     const uint32_t tmem = sm.tmem_base;
+    const uint32_t tS = tmem + kColS + 128 * w, tO = tmem + kColO + 128 * w;
     int* err = p.err;
-    uint32_t g = 0, nq = 0, fixed_phase = 0;
-    uint32_t np[2] = {0, 0};  // weight tiles taken, each stream
-    const uint32_t q[2] = {smem_u32(sm.q[0]), smem_u32(sm.q[1])};
+    uint32_t slot = 0, round = 0;  // next ring item, parity of its round
+    uint32_t fixed_phase = 0, nq = 0, np = 0;
+    const uint32_t kv0 = smem_u32(sm.kv[0]);
     bool ok = true;
+    auto next = [&]() {
+        if (++slot == Ly::kStages) {
+            slot = 0;
+            round ^= 1;
+        }
+    };
+    auto wait_k = [&]() { return mbar_wait(&sm.full[slot], round, err); };
+    auto wait_v = [&](bool edge) {
+        if (!edge) return wait_k();
+        const bool r = mbar_wait(&sm.fixed[slot], (fixed_phase >> slot) & 1, err);
+        fixed_phase ^= 1u << slot;
+        return r;
+    };
+    // the value product of the next ring item, in halves as its weights come
+    auto pv = [&](bool first) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (!mbar_wait(&sm.pready[w][half], np & 1, err)) return false;
+            tc_fence_after();
+            issue_pv_half<D>(tO, tS, kv0 + slot * Ly::kTile, half, !first || half > 0);
+        }
+        ++np;
+        tc_commit(&sm.empty[slot]);
+        next();
+        return true;
+    };
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
         if (!(ok = mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err))) break;
         const Piece pc = sm.piece[i];
         mbar_arrive(&sm.pempty[i]);
         if (pc.t0 < 0) break;
-        const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
-        auto slot = [&](int item) { return (g + item) % Ly::kStages; };
-        auto wait_full = [&](int item) {
-            return mbar_wait(&sm.full[slot(item)], ((g + item) / Ly::kStages) & 1, err);
-        };
-        auto wait_ofree = [&](int w) { return mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err); };
-        auto wait_v = [&](int t) {
-            const int item = item_of_v(t, nt, la), s = slot(item);
-            if (!at_edge(p, pc, tile_of(pc, pc.t0 + t), U)) return wait_full(item);
-            const bool r = mbar_wait(&sm.fixed[s], (fixed_phase >> s) & 1, err);
-            fixed_phase ^= 1u << s;
-            return r;
-        };
-        auto kv = [&](int item) { return smem_u32(sm.kv[slot(item)]); };
-        if (nt > 0) {
-            if (!(ok = mbar_wait(&sm.qfull, nq & 1, err))) break;
-            ++nq;
-        }
-        for (int t = 0; t < la && t < nt && ok; ++t) {
-            if (!(ok = wait_full(t))) break;
+        const int nt = pc.t1 - pc.t0;
+        const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
+        // the score product of the next ring item
+        auto qk = [&](bool last) {
+            if (!wait_k()) return false;
             tc_fence_after();
-            for (int w = pc.pair ? 0 : t; w <= (pc.pair ? 1 : t); ++w) {
-                issue_qk<D>(tmem + kColS + 128 * w, q[pc.pair ? w : 0], kv(t));
-                tc_commit(&sm.sfull[w]);
-            }
-            tc_commit(&sm.empty[slot(t)]);
-        }
-        if (ok && nt > 0 && nt <= la) tc_commit(&sm.qempty);
-        // stream w: the value product of its next tile, in halves as its weights come
-        auto pv = [&](int w, uint32_t v, bool first) {
-            const uint32_t o = tmem + kColO + 128 * w, pt = tmem + kColS + 128 * w;
-            for (int half = 0; half < 2; ++half) {
-                if (!mbar_wait(&sm.pready[w][half], np[w] & 1, err)) return false;
-                tc_fence_after();
-                issue_pv_half<D>(o, pt, v, half, !first || half > 0);
-            }
-            ++np[w];
+            issue_qk<D>(tS, q, kv0 + slot * Ly::kTile);
+            tc_commit(&sm.sfull[w]);
+            tc_commit(&sm.empty[slot]);
+            if (last) tc_commit(&sm.qempty);
+            next();
             return true;
         };
+        auto pass = [&](bool edge_v) {  // an item of the other stream
+            if (!wait_v(edge_v)) return false;
+            mbar_arrive(&sm.empty[slot]);
+            next();
+            return true;
+        };
+        auto edge = [&](int t) { return at_edge(p, pc, tile_of(pc, pc.t0 + t), U); };
+        if (nt > 0 && !(ok = mbar_wait(&sm.qfull, nq++ & 1, err))) break;
+        const bool mine = pc.pair ? nt > 0 : nt > w;  // this stream has a tile
         if (pc.pair) {
+            if (nt > 0 && !(ok = qk(nt == 1))) break;
             for (int t = 0; t < nt; ++t) {
-                const int iv = 2 * t + 1, ik = iv + 1;
-                const uint32_t v = kv(iv), kt = kv(ik);
-                const bool more = t + 1 < nt;
-                if (t == 0 && !(ok = wait_ofree(0))) break;
-                if (!(ok = wait_v(t) && pv(0, v, t == 0))) break;
-                if (more) {
-                    if (!(ok = wait_full(ik))) break;
-                    issue_qk<D>(tmem + kColS, q[0], kt);
-                    tc_commit(&sm.sfull[0]);
-                } else {
-                    tc_commit(&sm.ofull[0]);
-                }
-                if (t == 0 && !(ok = wait_ofree(1))) break;
-                if (!(ok = pv(1, v, t == 0))) break;
-                tc_commit(&sm.empty[slot(iv)]);
-                if (more) {
-                    issue_qk<D>(tmem + kColS + 128, q[1], kt);
-                    tc_commit(&sm.sfull[1]);
-                    tc_commit(&sm.empty[slot(ik)]);
-                    if (t + 2 == nt) tc_commit(&sm.qempty);
-                } else {
-                    tc_commit(&sm.ofull[1]);
-                }
+                const bool e = edge(t);
+                if (t == 0 && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+                if (!(ok = wait_v(e) && pv(t == 0))) break;
+                if (t + 1 < nt && !(ok = qk(t + 2 == nt))) break;
             }
         } else {
-            for (int t = 0; t < nt; ++t) {
-                const int w = t & 1, iv = item_of_v(t, nt, 2), ik = item_of_k(t + 2, 2);
-                if (t < 2 && !(ok = wait_ofree(w))) break;
-                if (!(ok = wait_v(t) && pv(w, kv(iv), t < 2))) break;
-                tc_commit(&sm.empty[slot(iv)]);
-                if (t + 2 < nt) {
-                    if (!(ok = wait_full(ik))) break;
-                    issue_qk<D>(tmem + kColS + 128 * w, q[0], kv(ik));
-                    tc_commit(&sm.sfull[w]);
-                    tc_commit(&sm.empty[slot(ik)]);
-                    if (t + 3 == nt) tc_commit(&sm.qempty);
+            for (int t = 0; t < 2 && t < nt && ok; ++t) ok = t == w ? qk(t + 2 >= nt) : pass(false);
+            for (int t = 0; t < nt && ok; ++t) {
+                const bool own = (t & 1) == w;
+                if (own) {
+                    if (t < 2 && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+                    ok = wait_v(edge(t)) && pv(t < 2);
                 } else {
-                    tc_commit(&sm.ofull[w]);
+                    ok = pass(edge(t));
                 }
+                if (ok && t + 2 < nt) ok = own ? qk(t + 4 >= nt) : pass(false);
             }
         }
         if (!ok) break;
-        // streams without a tile in this piece keep their barriers' phases
-        for (int w = 0; w < 2; ++w)
-            if (pc.pair ? nt == 0 : nt <= w) {
-                if (!(ok = wait_ofree(w))) break;
-                tc_commit(&sm.ofull[w]);
-            }
-        g += 2 * nt;
+        if (!mine) {  // its barriers' phases go on
+            if (!(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+            if (nt > 0) mbar_arrive(&sm.qempty);
+        }
+        tc_commit(&sm.ofull[w]);
     }
     // all products complete before tensor memory is released
-    tc_commit(&sm.end);
-    mbar_wait(&sm.end, 0, err);
+    tc_commit(&sm.end[w]);
+    mbar_wait(&sm.end[w], 0, err);
 }
 
 // ------------------------------------------------------------------------- values at the edges
 template <int D>
-__device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
+__device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
     using Ly = Layout<D>;
     const int U = 2 * (kM / p.G);
     int* err = p.err;
@@ -680,7 +690,7 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane
             const int valid = pc.L - tile * kN;  // rows of the sequence
             bool bad = false;
 #pragma unroll 8
-            for (int c = warp * 32 + lane; c < Ly::kTile / 16; c += kFixWarps * 32) {
+            for (int c = lane; c < Ly::kTile / 16; c += 32) {
                 uint4* at = reinterpret_cast<uint4*>(sm.kv[s]) + c;
                 uint4 v = *at;
                 // bfloat16 pairs whose exponent bits are all ones
@@ -770,31 +780,31 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                 const int hi = pos - ts;  // last key seen
                 const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
                 const bool edge = __any_sync(0xffffffffu, hi < kN - 1 || (lo > 0 && sk < kN));
-                tmem_ld_32x32b_x32(tS, s[0]);
-                float top = -INFINITY;
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    tmem_ld_wait(s[a]);
-                    if (a < 3) tmem_ld_32x32b_x32(tS + 32 * (a + 1), s[a < 3 ? a + 1 : 3]);
-                    if (negative) {
+                for (int a = 0; a < 4; ++a) tmem_ld_32x32b_x32(tS + 32 * a, s[a]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[a][e] ^= 0x80000000u;
-                    }
-                    if (edge) {
+                for (int a = 0; a < 4; ++a) tmem_ld_wait(s[a]);
+                if (negative) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * a + e > hi || (32 * a + e < lo && 32 * a + e >= sk))
-                                s[a][e] = 0xff800000u;
-                    }
-                    float mx[2] = {__uint_as_float(s[a][0]), __uint_as_float(s[a][1])};
-#pragma unroll
-                    for (int e = 2; e < 30; e += 4) {
-                        mx[0] = max3(mx[0], __uint_as_float(s[a][e]), __uint_as_float(s[a][e + 1]));
-                        mx[1] = max3(mx[1], __uint_as_float(s[a][e + 2]), __uint_as_float(s[a][e + 3]));
-                    }
-                    mx[0] = max3(mx[0], __uint_as_float(s[a][30]), __uint_as_float(s[a][31]));
-                    top = max3(top, mx[0], mx[1]);
+                    for (int a = 0; a < 128; ++a) s[a / 32][a % 32] ^= 0x80000000u;
                 }
+                if (edge) {
+#pragma unroll
+                    for (int a = 0; a < 128; ++a)
+                        if (a > hi || (a < lo && a >= sk)) s[a / 32][a % 32] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) mx[a] = __uint_as_float(s[a][0]);
+#pragma unroll
+                for (int e = 1; e < 31; e += 2)
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+                        mx[a] = max3(mx[a], __uint_as_float(s[a][e]), __uint_as_float(s[a][e + 1]));
+                const float top = max3(
+                    max3(mx[0], mx[1], __uint_as_float(s[0][31])),
+                    max3(mx[2], mx[3], __uint_as_float(s[1][31])),
+                    fmaxf(__uint_as_float(s[2][31]), __uint_as_float(s[3][31])));
                 const bool raise = (top - m) * c > kGrowth;  // (m = -inf: always)
                 float fade = 1.f;
                 if (raise) {
@@ -973,12 +983,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < Layout<D>::kStages; ++i) {
             mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.empty[i], 2);
             mbar_init(&sm.issued[i], 1);
-            mbar_init(&sm.fixed[i], kFixWarps);
+            mbar_init(&sm.fixed[i], 1);
         }
         mbar_init(&sm.qfull, 1);
-        mbar_init(&sm.qempty, 1);
+        mbar_init(&sm.qempty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.sfull[i], 1);
             mbar_init(&sm.pready[i][0], 4);
@@ -987,12 +997,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.ofree[i], 8);
             mbar_init(&sm.statw[i], 4);
             mbar_init(&sm.statr[i], 4);
+            mbar_init(&sm.end[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.pfull[i], 1);
-            mbar_init(&sm.pempty[i], 1 + kFixWarps + kSoftWarps);
+            mbar_init(&sm.pempty[i], 2 + 1 + kSoftWarps);
         }
-        mbar_init(&sm.end, 1);
         fence_mbar_init();
     }
     if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, 512);
@@ -1007,11 +1017,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_fewer<kRegsOther>();
         if (warp == kWarpLoad) {
             load_role<D>(p, sm, &tq, &tk, &tv, lane);
-        } else if (warp == kWarpMma) {
-            if (lane == 0) mma_role<D>(p, sm);
+        } else if (warp < kWarpFix) {
+            if (lane == 0) mma_role<D>(p, sm, warp - kWarpMma);
             __syncwarp();
         } else {
-            fix_role<D>(p, sm, warp - kWarpFix, lane);
+            fix_role<D>(p, sm, lane);
         }
     }
     tc_fence_before();
@@ -1020,58 +1030,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpMma) tmem_dealloc(sm.tmem_base, 512);
 }
 
-// Merges the pieces of the unit whose first piece CTA x of the main launch took: a warp a row, the
-// pieces in their order.
+// Merges the pieces of the unit whose first piece CTA x of the main launch took, in their order: a warp
+// a row, its lanes over the pieces for the weights and over the columns for the sums.
 template <int D>
-__global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams p, int n_cta) {
+__global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams p) {
+    __shared__ int slots[kMaxCtas + 1];
+    __shared__ int n_slots;
     griddep_wait();
     const PrefillHead hd = p.head[blockIdx.x];
     if (hd.nt == 0) return;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (warp == 0) {
+        // CTAs from x on whose range holds a tile of the unit
+        int n = 0;
+        for (int c0 = blockIdx.x; c0 < p.n_cta; c0 += 32) {
+            const int c = c0 + lane;
+            bool has = false, past = true;
+            if (c < p.n_cta) {
+                const long long a = range_start(p, hd.V, c) - hd.u, b = range_start(p, hd.V, c + 1) - hd.u;
+                has = cut_tile(p, a, hd.w, hd.nt) < cut_tile(p, b, hd.w, hd.nt);
+                past = b >= hd.w;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, has);
+            if (has) slots[n + __popc(m & ((1u << lane) - 1))] = 2 * c + (c == static_cast<int>(blockIdx.x));
+            n += __popc(m);
+            if (__any_sync(0xffffffffu, past)) break;
+        }
+        if (lane == 0) n_slots = n;
+    }
+    __syncthreads();
+    const int n = n_slots;
     const int TM = kM / p.G;
-    const int lane = threadIdx.x % 32;
     const bool pair = hd.n - hd.tok0 > TM;
     const int rows = pair ? 2 * kM : kM;
     constexpr int E = D / 32;
-    for (int r = blockIdx.y * 4 + threadIdx.x / 32; r < rows; r += gridDim.y * 4) {
+    for (int r = blockIdx.y * 4 + warp; r < rows; r += gridDim.y * 4) {
         const int t = r % kM / p.G, token = hd.tok0 + (r / kM) * TM + t;
         if (t >= TM || token >= hd.n) continue;
         const int head = hd.h * p.G + (r % kM - t * p.G);
-        float top = -INFINITY, sum = 0.f, o[E];
+        // the row's maximum, sink included
+        const float sink = p.sink_logit ? p.sink_logit[head] * kLog2e : -INFINITY;
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+        float top = -INFINITY;
+        for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[static_cast<size_t>(slots[i]) * 2 * kM + r].x);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = fmaxf(top, sink);
+        float sum = 0.f, o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int c = blockIdx.x; c <= hd.last; ++c) {
-            // (a range that rounding left without a tile of the unit wrote nothing)
-            if (cut_tile(range_start(hd.V, c, n_cta) - hd.u, hd.w, hd.nt) ==
-                cut_tile(range_start(hd.V, c + 1, n_cta) - hd.u, hd.w, hd.nt))
-                continue;
-            const size_t at = static_cast<size_t>(2 * c + (c == static_cast<int>(blockIdx.x))) * 2 * kM + r;
-            const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[at];
-            const float nt = fmaxf(top, ml.x);
-            const float f0 = top == -INFINITY ? 1.f : fast_exp2(top - nt);
-            const float f1 = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - nt);
-            const float* src = p.part_o + at * D + lane * E;
-            float x[E];
-            if (E == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(src);
-                x[0] = v.x, x[1] = v.y, x[E - 2] = v.z, x[E - 1] = v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(src);
-                x[0] = v.x, x[1] = v.y;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            float f = 0.f;
+            if (i0 + lane < n) {
+                const float2 v = ml[static_cast<size_t>(slots[i0 + lane]) * 2 * kM + r];
+                // (a piece without a maximum: nothing seen, or all of it NaN)
+                f = v.x == -INFINITY ? 1.f : fast_exp2(v.x - top);
+                sum += v.y * f;
             }
+            const int m = min(32, n - i0);
+#pragma unroll 4
+            for (int i = 0; i < m; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, i);
+                const float* src = p.part_o + (static_cast<size_t>(slots[i0 + i]) * 2 * kM + r) * D + lane * E;
+                if (E == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    o[0] = fmaf(v.x, g, o[0]);
+                    o[1] = fmaf(v.y, g, o[1]);
+                    o[E - 2] = fmaf(v.z, g, o[E - 2]);
+                    o[E - 1] = fmaf(v.w, g, o[E - 1]);
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(src);
+                    o[0] = fmaf(v.x, g, o[0]);
+                    o[1] = fmaf(v.y, g, o[1]);
+                }
+            }
+        }
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + x[e] * f1;
-            sum = sum * f0 + ml.y * f1;
-            top = nt;
-        }
-        float scale = 1.f;
-        if (p.sink_logit) {
-            const float sink = p.sink_logit[head] * kLog2e, nt = fmaxf(top, sink);
-            const float f = top == -INFINITY ? 1.f : fast_exp2(top - nt);
-            sum = sum * f + (sink == -INFINITY ? 0.f : fast_exp2(sink - nt));
-            scale = f;
-            top = nt;
-        }
-        scale = sum == 0.f ? 0.f : scale / sum;
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (sink != -INFINITY) sum += fast_exp2(sink - top);
+        const float scale = sum == 0.f ? 0.f : 1.f / sum;
         const long long row = static_cast<long long>(hd.c0 + token) * p.Hq + head;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * D + lane * E;
         if (E == 4)
@@ -1085,11 +1122,15 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams 
     }
 }
 
+constexpr int kMergeRows = 8;  // blocks of a unit
+
+int ctas() { return std::min(num_sms(), kMaxCtas); }
+
 struct Plan {
     size_t off_ml, off_o, total;
 };
 Plan make_plan(int D) {
-    const size_t n = static_cast<size_t>(num_sms());
+    const size_t n = static_cast<size_t>(ctas());
     Plan pl;
     pl.off_ml = (n * sizeof(PrefillHead) + 255) & ~static_cast<size_t>(255);
     pl.off_o = pl.off_ml + n * 2 * 2 * kM * 8;
@@ -1137,9 +1178,11 @@ int launch(PrefillParams p, void* ws, cudaStream_t stream) {
     static const cudaError_t set =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (set != cudaSuccess) return KVD_ERR_CUDA;
-    const int TM = kM / p.G, U = 2 * TM, n_cta = num_sms();
+    const int TM = kM / p.G, U = 2 * TM, n_cta = ctas();
+    p.n_cta = n_cta;
+    p.inv_cta = 1.0 / n_cta;
     p.unit_cost = 192;
-    p.flat_slack = 4 * kN;
+    p.flat_slack = 6 * kN;
     // at most so many units, each at most so long: where both are few, no unit is cut
     const long long units = static_cast<long long>(p.Hkv) * (p.T / U + std::min(p.B, p.T));
     if (launch_kernel(kernel, dim3(static_cast<unsigned>(n_cta)), dim3(kThreads), smem, stream, tq, tk,
@@ -1148,8 +1191,8 @@ int launch(PrefillParams p, void* ws, cudaStream_t stream) {
     const long long keys = p.block_table ? static_cast<long long>(p.max_pages) << p.page_shift : p.Tk;
     const bool never_cut = units <= n_cta && std::min<long long>(keys, p.window > 0 ? p.window + p.n_sink + U + kN : keys) + U + p.unit_cost <= p.flat_slack;
     if (!never_cut &&
-        launch_kernel(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(n_cta), 8), dim3(128), 0, stream,
-                      p, n_cta) != cudaSuccess)
+        launch_kernel(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(n_cta), kMergeRows), dim3(128), 0,
+                      stream, p) != cudaSuccess)
         return KVD_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
 }
