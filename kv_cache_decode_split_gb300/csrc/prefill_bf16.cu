@@ -39,15 +39,13 @@ namespace kvd {
 namespace {
 
 constexpr int kM = 128;     // rows of a query tile
-constexpr int kN = 128;     // keys of a tile
+constexpr int kN = 128;     // keys of a tile, as it is loaded
+constexpr int kSub = 64;    // keys of a score buffer
 constexpr int kMaxCtas = 256;  // of the main launch
 constexpr int kPieces = 4;  // ring of work descriptions
 constexpr int kSoftWarps = 8;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 11;  // products: warp 9 + stream
 constexpr int kThreads = 384;
-// two softmax warpgroups and one of the others share what the CTA was launched with: 168 a thread
-constexpr int kRegsSoft = 208, kRegsOther = 88;
-static_assert(2 * kRegsSoft + kRegsOther <= 3 * 168, "registers");
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrowth = 8.0f;  // log2 units
@@ -80,7 +78,7 @@ struct Smem {
     // values at a mask's edge: under way (a look at `full` alone could take an earlier round of the
     // ring for this one), and looked through
     uint64_t issued[Layout<D>::kStages], fixed[Layout<D>::kStages];
-    uint64_t qfull, qempty, sfull[2], pready[2][2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
+    uint64_t qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
     uint64_t statw[2], statr[2];                      // a stream's stat written; read by the other
     uint64_t end[2];
     Piece piece[kPieces];
@@ -171,6 +169,26 @@ __device__ __forceinline__ bool at_edge(const PrefillParams& p, const Piece& u, 
 __device__ __forceinline__ int tile_of(const Piece& u, int t) {
     return t < u.nA ? t : u.tB + (t - u.nA);
 }
+// The halves (of 64 keys) of a tile that some row of a stream sees: bits 0 and 1.
+struct Need {
+    int first, last, window, n_sink;  // positions of the stream's first and last row
+    __device__ __forceinline__ Need(const PrefillParams& p, const Piece& u, int w, int TM)
+        : window(p.window), n_sink(p.n_sink) {
+        const int tok = u.tok0 + (u.pair ? w * TM : 0);
+        first = u.L - u.n + tok;
+        last = u.L - u.n + min(u.n, tok + TM) - 1;
+    }
+    __device__ __forceinline__ int operator()(int tile) const {
+        int bits = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int a = tile * kN + h * kSub;
+            const bool before = window > 0 && a + kSub - 1 <= first - window && a >= n_sink;
+            if (a <= last && !before) bits |= 1 << h;
+        }
+        return bits;
+    }
+};
 // Ring items of a piece of nt tiles: `la` key tiles, then value tile t and key tile t + la in turn.
 __device__ __forceinline__ int item_of_v(int t, int nt, int la) { return min(2 * t + la, 2 * nt - 1); }
 
@@ -186,16 +204,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
                  : "memory");
-}
-
-// Registers of the executing warpgroup's threads, from the CTA's launch share (kThreads * 168).
-template <int N>
-__device__ __forceinline__ void regs_more() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_fewer() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Two float32 operations in one instruction.
@@ -244,10 +252,10 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t t, const uint32_t (&r)[16])
         : "memory");
 }
 
-// S (tensor memory) = Q (128 rows) K^T (128 keys), both K-major in shared memory.
+// S (tensor memory) = Q (128 rows) K^T (64 keys), both K-major in shared memory.
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kM, kN, 0, 0);
+    constexpr uint32_t idesc = idesc_bf16_f32(kM, kSub, 0, 0);
     const uint64_t a = sw128_kmajor_desc(q), b = sw128_kmajor_desc(k);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
@@ -256,17 +264,14 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
     }
 }
 
-// O (tensor memory) (+)= half of P (tensor memory, 128 x 64 of its 128 keys) V (their 64 tokens, read
-// MN-major).
+// O (tensor memory) (+)= P (tensor memory, 128 x 64) V (64 tokens, read MN-major).
 template <int D>
-__device__ __forceinline__ void issue_pv_half(uint32_t o, uint32_t pt, uint32_t v, int half,
-                                              bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t pt, uint32_t v, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32(kM, D, 0, 1);
-    const uint64_t b = sw128_mnmajor_desc(v + half * (kN / 2) * 128, kN * 128);
+    const uint64_t b = sw128_mnmajor_desc(v, kN * 128);
 #pragma unroll
-    for (int ks = 0; ks < kN / 32; ++ks)
-        tc_mma_bf16_ts(o, pt + half * (kN / 4) + ks * 8,
-                       b + static_cast<uint64_t>((ks * 16 * 128) >> 4), idesc,
+    for (int ks = 0; ks < kSub / 16; ++ks)
+        tc_mma_bf16_ts(o, pt + ks * 8, b + static_cast<uint64_t>((ks * 16 * 128) >> 4), idesc,
                        (accumulate || ks > 0) ? 1u : 0u);
 }
 
@@ -563,18 +568,19 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
 // ---------------------------------------------------------------------------------- products
 // One thread for each stream. A stream's products run in the order of their issue, so a score product
 // may overwrite the weights that the value product before it reads; of the other stream's tensor memory
-// it touches nothing. Issuing both streams from one thread left the tensor cores idle while that thread
-// waited and signalled (16385 tokens: 2.18 ms). Both threads pass every ring item in order, also one
-// that is the other's: a barrier's phase is known by its parity alone.
+// it touches nothing. A stream has two score buffers, one for each half of a tile: the score product of
+// the next tile's half follows this half's value product, so that scores wait for the softmax and not
+// the softmax for scores. (One thread for both streams: 2.18 ms for 16385 tokens; one buffer of 128
+// keys a stream: 2.15.) Both threads pass every ring item in order, also one that is the other's.
 template <int D>
 __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
     using Ly = Layout<D>;
-    const int U = 2 * (kM / p.G);
+    const int TM = kM / p.G, U = 2 * TM;
     const uint32_t tmem = sm.tmem_base;
     const uint32_t tS = tmem + kColS + 128 * w, tO = tmem + kColO + 128 * w;
     int* err = p.err;
     uint32_t slot = 0, round = 0;  // next ring item, parity of its round
-    uint32_t fixed_phase = 0, nq = 0, np = 0;
+    uint32_t fixed_phase = 0, nq = 0, np = 0;  // np: a parity bit for each score buffer
     const uint32_t kv0 = smem_u32(sm.kv[0]);
     bool ok = true;
     auto next = [&]() {
@@ -590,73 +596,85 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
         fixed_phase ^= 1u << slot;
         return r;
     };
-    // the value product of the next ring item, in halves as its weights come
-    auto pv = [&](bool first) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (!mbar_wait(&sm.pready[w][half], np & 1, err)) return false;
-            tc_fence_after();
-            issue_pv_half<D>(tO, tS, kv0 + slot * Ly::kTile, half, !first || half > 0);
-        }
-        ++np;
-        tc_commit(&sm.empty[slot]);
-        next();
-        return true;
-    };
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
         if (!(ok = mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err))) break;
         const Piece pc = sm.piece[i];
         mbar_arrive(&sm.pempty[i]);
         if (pc.t0 < 0) break;
-        const int nt = pc.t1 - pc.t0;
+        const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
         const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
-        // the score product of the next ring item
-        auto qk = [&](bool last) {
-            if (!wait_k()) return false;
-            tc_fence_after();
-            issue_qk<D>(tS, q, kv0 + slot * Ly::kTile);
-            tc_commit(&sm.sfull[w]);
-            tc_commit(&sm.empty[slot]);
-            if (last) tc_commit(&sm.qempty);
-            next();
-            return true;
-        };
+        const Need need(p, pc, w, TM);
+        auto own = [&](int t) { return pc.pair || (t & 1) == w; };
+        auto wants = [&](int t) { return need(tile_of(pc, pc.t0 + t)); };
+        auto edge = [&](int t) { return at_edge(p, pc, tile_of(pc, pc.t0 + t), U); };
         auto pass = [&](bool edge_v) {  // an item of the other stream
             if (!wait_v(edge_v)) return false;
             mbar_arrive(&sm.empty[slot]);
             next();
             return true;
         };
-        auto edge = [&](int t) { return at_edge(p, pc, tile_of(pc, pc.t0 + t), U); };
+        auto qk = [&](int h, uint32_t kt) {
+            issue_qk<D>(tS + kSub * h, q, kt + h * kSub * 128);
+            tc_commit(&sm.sfull[w][h]);
+        };
+        bool first = true;  // the next value product is the piece's first
         if (nt > 0 && !(ok = mbar_wait(&sm.qfull, nq++ & 1, err))) break;
-        const bool mine = pc.pair ? nt > 0 : nt > w;  // this stream has a tile
-        if (pc.pair) {
-            if (nt > 0 && !(ok = qk(nt == 1))) break;
-            for (int t = 0; t < nt; ++t) {
-                const bool e = edge(t);
-                if (t == 0 && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
-                if (!(ok = wait_v(e) && pv(t == 0))) break;
-                if (t + 1 < nt && !(ok = qk(t + 2 == nt))) break;
+        for (int t = 0; t < la && t < nt && ok; ++t) {
+            if (!own(t)) {
+                ok = pass(false);
+                continue;
             }
-        } else {
-            for (int t = 0; t < 2 && t < nt && ok; ++t) ok = t == w ? qk(t + 2 >= nt) : pass(false);
-            for (int t = 0; t < nt && ok; ++t) {
-                const bool own = (t & 1) == w;
-                if (own) {
-                    if (t < 2 && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
-                    ok = wait_v(edge(t)) && pv(t < 2);
-                } else {
-                    ok = pass(edge(t));
+            if (!(ok = wait_k())) break;
+            tc_fence_after();
+            const int m = wants(t);
+            if (m & 1) qk(0, kv0 + slot * Ly::kTile);
+            if (m & 2) qk(1, kv0 + slot * Ly::kTile);
+            tc_commit(&sm.empty[slot]);
+            if (t + la >= nt) tc_commit(&sm.qempty);
+            next();
+        }
+        for (int t = 0; t < nt && ok; ++t) {
+            const bool more = t + la < nt;
+            if (!own(t)) {
+                ok = pass(edge(t));
+                if (ok && more) ok = pass(false);
+                continue;
+            }
+            const int mv = wants(t), mk = more ? wants(t + la) : 0;
+            const uint32_t v = kv0 + slot * Ly::kTile, v_slot = slot;
+            if (!(ok = wait_v(edge(t)))) break;
+            next();
+            const uint32_t kt = kv0 + slot * Ly::kTile;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (mv >> h & 1) {
+                    if (first && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+                    if (!(ok = mbar_wait(&sm.pready[w][h], np >> h & 1, err))) break;
+                    np ^= 1u << h;
+                    tc_fence_after();
+                    issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
+                    tc_commit(&sm.pvdone[w][h]);
+                    first = false;
                 }
-                if (ok && t + 2 < nt) ok = own ? qk(t + 4 >= nt) : pass(false);
+                if (h == 1) tc_commit(&sm.empty[v_slot]);
+                if (h == 0 && more) {
+                    if (!(ok = wait_k())) break;
+                    tc_fence_after();
+                }
+                if (mk >> h & 1) qk(h, kt);
+            }
+            if (!ok) break;
+            if (more) {
+                tc_commit(&sm.empty[slot]);
+                if (t + 2 * la >= nt) tc_commit(&sm.qempty);
+                next();
             }
         }
         if (!ok) break;
-        if (!mine) {  // its barriers' phases go on
-            if (!(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
-            if (nt > 0) mbar_arrive(&sm.qempty);
-        }
+        // without a product in this piece the barriers' phases still go on
+        if (first && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+        if (!pc.pair && nt > 0 && nt <= w) mbar_arrive(&sm.qempty);
         tc_commit(&sm.ofull[w]);
     }
     // all products complete before tensor memory is released
@@ -766,77 +784,81 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         const bool valid = tok_r < TM && token < pc.n;
         const bool busy = __any_sync(0xffffffffu, valid);
         const int pos = valid ? pc.L - pc.n + token : 0x3fffffff;
+        const Need need(p, pc, w, TM);
         float m = -INFINITY, l = 0.f;  // reference maximum (raw score units), sum
-        bool ok = true;
+        bool ok = true, any = false;   // any: a product of this piece has been or will be added to O
         const int step = pc.pair ? 1 : 2;
-        const int t_first = pc.t0 + (pc.pair ? 0 : w);
-        for (int t = t_first; t < pc.t1; t += step) {
-            if (!(ok = mbar_wait(&sm.sfull[w], ns & 1, err))) break;
-            ++ns;
-            if (busy) {
-                tc_fence_after();
-                uint32_t s[4][32];
-                const int ts = tile_of(pc, t) * kN;
-                const int hi = pos - ts;  // last key seen
-                const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
-                const bool edge = __any_sync(0xffffffffu, hi < kN - 1 || (lo > 0 && sk < kN));
-#pragma unroll
-                for (int a = 0; a < 4; ++a) tmem_ld_32x32b_x32(tS + 32 * a, s[a]);
-#pragma unroll
-                for (int a = 0; a < 4; ++a) tmem_ld_wait(s[a]);
-                if (negative) {
-#pragma unroll
-                    for (int a = 0; a < 128; ++a) s[a / 32][a % 32] ^= 0x80000000u;
-                }
-                if (edge) {
-#pragma unroll
-                    for (int a = 0; a < 128; ++a)
-                        if (a > hi || (a < lo && a >= sk)) s[a / 32][a % 32] = 0xff800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int a = 0; a < 4; ++a) mx[a] = __uint_as_float(s[a][0]);
-#pragma unroll
-                for (int e = 1; e < 31; e += 2)
-#pragma unroll
-                    for (int a = 0; a < 4; ++a)
-                        mx[a] = max3(mx[a], __uint_as_float(s[a][e]), __uint_as_float(s[a][e + 1]));
-                const float top = max3(
-                    max3(mx[0], mx[1], __uint_as_float(s[0][31])),
-                    max3(mx[2], mx[3], __uint_as_float(s[1][31])),
-                    fmaxf(__uint_as_float(s[2][31]), __uint_as_float(s[3][31])));
-                const bool raise = (top - m) * c > kGrowth;  // (m = -inf: always)
-                float fade = 1.f;
-                if (raise) {
-                    fade = fast_exp2((m - top) * c);
-                    m = top;
-                    l *= fade;
-                }
-                if (t != t_first && __any_sync(0xffffffffu, raise)) {
-                    // the products of all earlier tiles are complete: this tile's scores were
-                    // issued behind them
+        for (int t = pc.t0 + (pc.pair ? 0 : w); t < pc.t1 && ok; t += step) {
+            const int tile = tile_of(pc, t), halves = need(tile);
 #pragma unroll 1
-                    for (int a = 0; a < D / 16; ++a) {
-                        uint32_t o[16];
-                        tmem_ld_x16(tO + 128 * w + 16 * a, o);
+            for (int h = 0; h < 2; ++h) {
+                if (!(halves >> h & 1)) continue;
+                if (!(ok = mbar_wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
+                ns ^= 1u << h;
+                if (busy) {
+                    tc_fence_after();
+                    uint32_t s[2][32];
+                    tmem_ld_32x32b_x32(tS + kSub * h, s[0]);
+                    tmem_ld_32x32b_x32(tS + kSub * h + 32, s[1]);
+                    const int ts = tile * kN + kSub * h;
+                    const int hi = pos - ts;  // last key seen
+                    const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
+                    const bool edge = __any_sync(0xffffffffu, hi < kSub - 1 || (lo > 0 && sk < kSub));
+                    tmem_ld_wait(s[0]);
+                    tmem_ld_wait(s[1]);
+                    if (negative) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-                        tmem_st_x16(tO + 128 * w + 16 * a, o);
+                        for (int a = 0; a < kSub; ++a) s[a / 32][a % 32] ^= 0x80000000u;
                     }
-                }
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                const uint64_t c2 = pair64(c, c), n2 = pair64(-mc, -mc);
-                uint64_t sum[2] = {pair64(l, 0.f), pair64(0.f, 0.f)};
+                    if (edge) {
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
+                        for (int a = 0; a < kSub; ++a)
+                            if (a > hi || (a < lo && a >= sk)) s[a / 32][a % 32] = 0xff800000u;
+                    }
+                    float mx[4];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
+                    for (int a = 0; a < 4; ++a) mx[a] = __uint_as_float(s[a / 2][16 * (a % 2)]);
+#pragma unroll
+                    for (int e = 1; e < 15; e += 2)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            mx[a] = max3(mx[a], __uint_as_float(s[a / 2][16 * (a % 2) + e]),
+                                         __uint_as_float(s[a / 2][16 * (a % 2) + e + 1]));
+                    const float top = max3(max3(mx[0], mx[1], __uint_as_float(s[0][15])),
+                                           max3(mx[2], mx[3], __uint_as_float(s[0][31])),
+                                           fmaxf(__uint_as_float(s[1][15]), __uint_as_float(s[1][31])));
+                    const bool raise = (top - m) * c > kGrowth;  // (m = -inf: always)
+                    float fade = 1.f;
+                    if (raise) {
+                        fade = fast_exp2((m - top) * c);
+                        m = top;
+                        l *= fade;
+                    }
+                    if (any && __any_sync(0xffffffffu, raise)) {
+                        // the products up to the other buffer's last are complete (this buffer's are:
+                        // its scores were issued behind them)
+                        if (!(ok = mbar_wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int a = 0; a < D / 16; ++a) {
+                            uint32_t o[16];
+                            tmem_ld_x16(tO + 128 * w + 16 * a, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                            tmem_st_x16(tO + 128 * w + 16 * a, o);
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    const uint64_t c2 = pair64(c, c), n2 = pair64(-mc, -mc);
+                    uint64_t sum[2] = {pair64(l, 0.f), pair64(0.f, 0.f)};
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
                         uint32_t pr[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const uint64_t y = fma2(pair64(__uint_as_float(s[2 * a + b][2 * e]),
-                                                           __uint_as_float(s[2 * a + b][2 * e + 1])), c2, n2);
+                            const uint64_t y = fma2(pair64(__uint_as_float(s[a][2 * e]),
+                                                           __uint_as_float(s[a][2 * e + 1])), c2, n2);
                             float u, v;
                             unpair64(y, u, v);
                             u = fast_exp2(u);
@@ -844,19 +866,17 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                             sum[e & 1] = add2(sum[e & 1], pair64(u, v));
                             pr[e] = pack_bf16(u, v);
                         }
-                        tmem_st_x16(tS + 32 * a + 16 * b, pr);
+                        tmem_st_x16(tS + kSub * h + 16 * a, pr);
                     }
+                    float x0, x1;
+                    unpair64(add2(sum[0], sum[1]), x0, x1);
+                    l = x0 + x1;
                     tmem_st_wait();
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.pready[w][a]);
                 }
-                float x0, x1;
-                unpair64(add2(sum[0], sum[1]), x0, x1);
-                l = x0 + x1;
-            } else if (lane == 0) {
-                mbar_arrive(&sm.pready[w][0]);
-                mbar_arrive(&sm.pready[w][1]);
+                any = true;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.pready[w][h]);
             }
         }
         if (!ok) break;
@@ -864,7 +884,10 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         float mc = m == -INFINITY ? -INFINITY : m * c;  // log2 units
         const bool two = !pc.pair;                      // both streams hold a part
         float oth_m = -INFINITY, oth_l = 0.f;
-        const bool has_own = t_first < pc.t1, has_oth = two && pc.t0 + (1 - w) < pc.t1;
+        const bool has_own = any;
+        bool has_oth = false;  // (one query tile: the same keys are seen by both streams' rows)
+        if (two)
+            for (int t = pc.t0 + 1 - w; t < pc.t1; t += 2) has_oth |= need(tile_of(pc, t)) != 0;
         if (two && pc.t1 > pc.t0) {
             if (!(ok = mbar_wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
             sm.stat[w][r][0] = mc;
@@ -990,9 +1013,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.qfull, 1);
         mbar_init(&sm.qempty, 2);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.sfull[i], 1);
-            mbar_init(&sm.pready[i][0], 4);
-            mbar_init(&sm.pready[i][1], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sm.sfull[i][h], 1);
+                mbar_init(&sm.pready[i][h], 4);
+                mbar_init(&sm.pvdone[i][h], 1);
+            }
             mbar_init(&sm.ofull[i], 1);
             mbar_init(&sm.ofree[i], 8);
             mbar_init(&sm.statw[i], 4);
@@ -1011,10 +1036,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     griddep_wait();
     if (warp < kSoftWarps) {
-        regs_more<kRegsSoft>();
         softmax_role<D>(p, sm, warp, lane);
     } else {
-        regs_fewer<kRegsOther>();
         if (warp == kWarpLoad) {
             load_role<D>(p, sm, &tq, &tk, &tv, lane);
         } else if (warp < kWarpFix) {
