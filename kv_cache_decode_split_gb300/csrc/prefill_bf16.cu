@@ -606,8 +606,8 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
         const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
         const Need need(p, pc, w, TM);
         auto own = [&](int t) { return pc.pair || (t & 1) == w; };
-        auto wants = [&](int t) { return need(tile_of(pc, pc.t0 + t)); };
         auto edge = [&](int t) { return at_edge(p, pc, tile_of(pc, pc.t0 + t), U); };
+        auto wants = [&](int t, bool at) { return at ? need(tile_of(pc, pc.t0 + t)) : 3; };
         auto pass = [&](bool edge_v) {  // an item of the other stream
             if (!wait_v(edge_v)) return false;
             mbar_arrive(&sm.empty[slot]);
@@ -620,14 +620,17 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
         };
         bool first = true;  // the next value product is the piece's first
         if (nt > 0 && !(ok = mbar_wait(&sm.qfull, nq++ & 1, err))) break;
+        bool e = false;  // the stream's next tile is at an edge, and the halves of it that it sees
+        int m = 0;
         for (int t = 0; t < la && t < nt && ok; ++t) {
             if (!own(t)) {
                 ok = pass(false);
                 continue;
             }
+            e = edge(t);
+            m = wants(t, e);
             if (!(ok = wait_k())) break;
             tc_fence_after();
-            const int m = wants(t);
             if (m & 1) qk(0, kv0 + slot * Ly::kTile);
             if (m & 2) qk(1, kv0 + slot * Ly::kTile);
             tc_commit(&sm.empty[slot]);
@@ -641,28 +644,32 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
                 if (ok && more) ok = pass(false);
                 continue;
             }
-            const int mv = wants(t), mk = more ? wants(t + la) : 0;
             const uint32_t v = kv0 + slot * Ly::kTile, v_slot = slot;
-            if (!(ok = wait_v(edge(t)))) break;
+            if (!(ok = wait_v(e))) break;
             next();
             const uint32_t kt = kv0 + slot * Ly::kTile;
+            const bool e_next = more && edge(t + la);
+            const int m_next = more ? wants(t + la, e_next) : 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (mv >> h & 1) {
+                if (m >> h & 1) {
                     if (first && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
                     if (!(ok = mbar_wait(&sm.pready[w][h], np >> h & 1, err))) break;
                     np ^= 1u << h;
                     tc_fence_after();
                     issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
-                    tc_commit(&sm.pvdone[w][h]);
                     first = false;
                 }
-                if (h == 1) tc_commit(&sm.empty[v_slot]);
+                // (a commit holds its thread up for some 90 cycles: none that could be left out)
                 if (h == 0 && more) {
                     if (!(ok = wait_k())) break;
                     tc_fence_after();
                 }
-                if (mk >> h & 1) qk(h, kt);
+                if (m_next >> h & 1)
+                    qk(h, kt);
+                else if (m >> h & 1)
+                    tc_commit(&sm.pvdone[w][h]);
+                if (h == 1) tc_commit(&sm.empty[v_slot]);
             }
             if (!ok) break;
             if (more) {
@@ -670,6 +677,8 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
                 if (t + 2 * la >= nt) tc_commit(&sm.qempty);
                 next();
             }
+            e = e_next;
+            m = m_next;
         }
         if (!ok) break;
         // without a product in this piece the barriers' phases still go on
@@ -774,7 +783,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     const bool negative = p.scale_log2 < 0.f;
     const float c = fmaxf(fabsf(p.scale_log2), 0x1p-100f);  // (0: -inf times it stays -inf)
     const int tok_r = r / p.G, head_r = r - tok_r * p.G;
-    uint32_t ns = 0, n_two = 0;
+    uint32_t ns = 0, nd = 0, n_two = 0;  // ns, nd: a parity bit for each score buffer
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
         if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
@@ -788,8 +797,11 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         float m = -INFINITY, l = 0.f;  // reference maximum (raw score units), sum
         bool ok = true, any = false;   // any: a product of this piece has been or will be added to O
         const int step = pc.pair ? 1 : 2;
-        for (int t = pc.t0 + (pc.pair ? 0 : w); t < pc.t1 && ok; t += step) {
-            const int tile = tile_of(pc, t), halves = need(tile);
+        const int t_first = pc.t0 + (pc.pair ? 0 : w);
+        int m_next = t_first < pc.t1 ? need(tile_of(pc, t_first)) : 0;
+        for (int t = t_first; t < pc.t1 && ok; t += step) {
+            const int tile = tile_of(pc, t), halves = m_next;
+            m_next = t + step < pc.t1 ? need(tile_of(pc, t + step)) : 0;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (!(halves >> h & 1)) continue;
@@ -835,9 +847,14 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                         l *= fade;
                     }
                     if (any && __any_sync(0xffffffffu, raise)) {
-                        // the products up to the other buffer's last are complete (this buffer's are:
-                        // its scores were issued behind them)
-                        if (!(ok = mbar_wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err))) break;
+                        // the other buffer's last product is complete (this buffer's is: its scores
+                        // were issued behind it): when its next scores are there, or, without such,
+                        // when its barrier says so
+                        const int o = 1 - h;
+                        const bool more = (h == 0 ? halves : m_next) >> o & 1;
+                        ok = more ? mbar_wait(&sm.sfull[w][o], ns >> o & 1, err)
+                                  : mbar_wait(&sm.pvdone[w][o], (nd >> o & 1) ^ 1, err);
+                        if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int a = 0; a < D / 16; ++a) {
@@ -875,6 +892,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                     tc_fence_before();
                 }
                 any = true;
+                if (!(m_next >> h & 1)) nd ^= 1u << h;  // its product's completion is signalled
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.pready[w][h]);
             }
