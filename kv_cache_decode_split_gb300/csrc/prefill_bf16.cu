@@ -157,14 +157,22 @@ __device__ __forceinline__ void unit_tiles(const PrefillParams& p, const Seq& s,
     nt = nA + last / kN - lo + 1;
 }
 
-// Whether some row of the unit does not see all of the tile: the mask is applied, and its values are
-// looked through.
-__device__ __forceinline__ bool at_edge(const PrefillParams& p, const Piece& u, int tile, int U) {
-    const int first = u.L - u.n + u.tok0, last = u.L - u.n + min(u.n, u.tok0 + U) - 1;
-    const int ts = tile * kN;
-    if (ts + kN - 1 > first) return true;
-    return p.window > 0 && ts + kN > p.n_sink && ts <= last - p.window;
-}
+// The tiles at a mask's edge: some row of the unit does not see all of them. The mask is applied there,
+// and their values are looked through.
+struct Edge {
+    int from;          // tiles from here on reach past the first row's position
+    int low, sink;     // tiles below `low` lie (in part) behind the last row's window, but those below
+                       // `sink` hold sink tokens only
+    __device__ __forceinline__ Edge(const PrefillParams& p, const Piece& u, int U) {
+        const int first = u.L - u.n + u.tok0, last = u.L - u.n + min(u.n, u.tok0 + U) - 1;
+        from = first < 0 ? 0 : (first + 1) / kN;
+        low = p.window > 0 && last >= p.window ? (last - p.window) / kN + 1 : 0;
+        sink = p.n_sink / kN;
+    }
+    __device__ __forceinline__ bool operator()(int tile) const {
+        return tile >= from || (tile < low && tile >= sink);
+    }
+};
 
 __device__ __forceinline__ int tile_of(const Piece& u, int t) {
     return t < u.nA ? t : u.tB + (t - u.nA);
@@ -345,6 +353,8 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
 
     int ps = 0;               // pieces published
     uint32_t g = 0, nq = 0;   // ring items and query loads issued
+    uint32_t joints = 0;      // the last items, newest in bit 0: whether each is let go with the next
+    uint32_t let_go = 0;      // a parity bit for each slot's barrier
     bool ok = true;
     if (lane == 0) p.head[cta].nt = 0;
     auto publish = [&](const Piece& u) {
@@ -451,6 +461,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
                     if (!ok) break;
                     const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
                     if (nt == 0) continue;
+                    const Edge edge(p, pc, U);
                     // queries
                     if (lane == 0) {
                         ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err);
@@ -490,14 +501,21 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
                     }
                     auto fetch = [&](int t, bool is_v) {
                         const int s_ = g % Ly::kStages;
+                        const bool joint = is_v && t + la < nt;  // let go together with the next item
                         if (lane == 0) {
-                            ok = mbar_wait(&sm.empty[s_], ((g / Ly::kStages) & 1) ^ 1, err);
+                            // what this slot held, if anything, has been read: its barrier says so, or
+                            // that of the item behind it
+                            if (g >= Ly::kStages) {
+                                const int b = (joints >> (Ly::kStages - 1)) & 1 ? (s_ + 1) % Ly::kStages : s_;
+                                ok = mbar_wait(&sm.empty[b], let_go >> b & 1, err);
+                                if (b == s_) let_go ^= 1u << b;  // (of two items: with the second)
+                            }
                             if (ok) {
                                 mbar_arrive_expect_tx(&sm.full[s_], Ly::kTile);
-                                if (is_v && at_edge(p, pc, tile_of(pc, pc.t0 + t), U))
-                                    mbar_arrive(&sm.issued[s_]);
+                                if (is_v && edge(tile_of(pc, pc.t0 + t))) mbar_arrive(&sm.issued[s_]);
                             }
                         }
+                        joints = joints << 1 | (joint ? 1u : 0u);
                         ok = __shfl_sync(0xffffffffu, ok, 0);
                         if (!ok) return;
                         ++g;
@@ -573,7 +591,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
 // the softmax for scores. (One thread for both streams: 2.18 ms for 16385 tokens; one buffer of 128
 // keys a stream: 2.15.) Both threads pass every ring item in order, also one that is the other's.
 template <int D>
-__device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
+__device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const int lane) {
     using Ly = Layout<D>;
     const int TM = kM / p.G, U = 2 * TM;
     const uint32_t tmem = sm.tmem_base;
@@ -582,6 +600,7 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
     uint32_t slot = 0, round = 0;  // next ring item, parity of its round
     uint32_t fixed_phase = 0, nq = 0, np = 0;  // np: a parity bit for each score buffer
     const uint32_t kv0 = smem_u32(sm.kv[0]);
+    const bool one = lane == 0;
     bool ok = true;
     auto next = [&]() {
         if (++slot == Ly::kStages) {
@@ -596,27 +615,36 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
         fixed_phase ^= 1u << slot;
         return r;
     };
+    // (a commit holds its thread up for some 90 cycles: none that could be left out)
+    auto commit = [&](uint64_t* bar) {
+        if (one) tc_commit(bar);
+    };
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
         if (!(ok = mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err))) break;
         const Piece pc = sm.piece[i];
-        mbar_arrive(&sm.pempty[i]);
+        __syncwarp();
+        if (one) mbar_arrive(&sm.pempty[i]);
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
         const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
         const Need need(p, pc, w, TM);
+        const Edge at_edge(p, pc, U);
         auto own = [&](int t) { return pc.pair || (t & 1) == w; };
-        auto edge = [&](int t) { return at_edge(p, pc, tile_of(pc, pc.t0 + t), U); };
+        auto edge = [&](int t) { return at_edge(tile_of(pc, pc.t0 + t)); };
         auto wants = [&](int t, bool at) { return at ? need(tile_of(pc, pc.t0 + t)) : 3; };
-        auto pass = [&](bool edge_v) {  // an item of the other stream
+        auto pass = [&](bool edge_v, bool joint) {  // an item of the other stream
             if (!wait_v(edge_v)) return false;
-            mbar_arrive(&sm.empty[slot]);
+            __syncwarp();
+            if (one && !joint) mbar_arrive(&sm.empty[slot]);
             next();
             return true;
         };
         auto qk = [&](int h, uint32_t kt) {
-            issue_qk<D>(tS + kSub * h, q, kt + h * kSub * 128);
-            tc_commit(&sm.sfull[w][h]);
+            if (one) {
+                issue_qk<D>(tS + kSub * h, q, kt + h * kSub * 128);
+                tc_commit(&sm.sfull[w][h]);
+            }
         };
         bool first = true;  // the next value product is the piece's first
         if (nt > 0 && !(ok = mbar_wait(&sm.qfull, nq++ & 1, err))) break;
@@ -624,70 +652,68 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w) {
         int m = 0;
         for (int t = 0; t < la && t < nt && ok; ++t) {
             if (!own(t)) {
-                ok = pass(false);
+                ok = pass(false, false);
                 continue;
             }
             e = edge(t);
             m = wants(t, e);
             if (!(ok = wait_k())) break;
-            tc_fence_after();
             if (m & 1) qk(0, kv0 + slot * Ly::kTile);
             if (m & 2) qk(1, kv0 + slot * Ly::kTile);
-            tc_commit(&sm.empty[slot]);
-            if (t + la >= nt) tc_commit(&sm.qempty);
+            commit(&sm.empty[slot]);
+            if (t + la >= nt) commit(&sm.qempty);
             next();
         }
+        if (!(ok = ok && mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
         for (int t = 0; t < nt && ok; ++t) {
             const bool more = t + la < nt;
             if (!own(t)) {
-                ok = pass(edge(t));
-                if (ok && more) ok = pass(false);
+                ok = pass(edge(t), more);
+                if (ok && more) ok = pass(false, false);
                 continue;
             }
-            const uint32_t v = kv0 + slot * Ly::kTile, v_slot = slot;
+            const uint32_t v = kv0 + slot * Ly::kTile;
             if (!(ok = wait_v(e))) break;
+            const uint32_t v_slot = slot;
             next();
             const uint32_t kt = kv0 + slot * Ly::kTile;
-            const bool e_next = more && edge(t + la);
-            const int m_next = more ? wants(t + la, e_next) : 0;
+            bool e_next = false;
+            int m_next = 0;
+            if (more) {
+                e_next = edge(t + la);
+                m_next = wants(t + la, e_next);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (m >> h & 1) {
-                    if (first && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
                     if (!(ok = mbar_wait(&sm.pready[w][h], np >> h & 1, err))) break;
                     np ^= 1u << h;
                     tc_fence_after();
-                    issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
+                    if (one) issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
                     first = false;
                 }
-                // (a commit holds its thread up for some 90 cycles: none that could be left out)
-                if (h == 0 && more) {
-                    if (!(ok = wait_k())) break;
-                    tc_fence_after();
-                }
+                if (h == 0 && more && !(ok = wait_k())) break;
                 if (m_next >> h & 1)
                     qk(h, kt);
                 else if (m >> h & 1)
-                    tc_commit(&sm.pvdone[w][h]);
-                if (h == 1) tc_commit(&sm.empty[v_slot]);
+                    commit(&sm.pvdone[w][h]);
             }
             if (!ok) break;
+            // the value tile and the next key tile are let go together
+            commit(&sm.empty[more ? slot : v_slot]);
             if (more) {
-                tc_commit(&sm.empty[slot]);
-                if (t + 2 * la >= nt) tc_commit(&sm.qempty);
+                if (t + 2 * la >= nt) commit(&sm.qempty);
                 next();
             }
             e = e_next;
             m = m_next;
         }
         if (!ok) break;
-        // without a product in this piece the barriers' phases still go on
-        if (first && !(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
-        if (!pc.pair && nt > 0 && nt <= w) mbar_arrive(&sm.qempty);
-        tc_commit(&sm.ofull[w]);
+        if (!pc.pair && nt > 0 && nt <= w && one) mbar_arrive(&sm.qempty);
+        commit(&sm.ofull[w]);
     }
     // all products complete before tensor memory is released
-    tc_commit(&sm.end[w]);
+    commit(&sm.end[w]);
     mbar_wait(&sm.end[w], 0, err);
 }
 
@@ -704,10 +730,11 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
+        const Edge edge(p, pc, U);
         bool ok = true;
         for (int t = 0; t < nt && ok; ++t) {
             const int tile = tile_of(pc, pc.t0 + t);
-            if (!at_edge(p, pc, tile, U)) continue;
+            if (!edge(tile)) continue;
             const uint32_t item = g + item_of_v(t, nt, la);
             const int s = item % Ly::kStages;
             ok = mbar_wait(&sm.issued[s], (phase >> s) & 1, err) &&
@@ -749,10 +776,11 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
 // What a row gets back, in one column, of the values that were cleared: v itself, where the row sees it.
 template <int D>
 __device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, int U, int pos, int col) {
+    const Edge edge(p, pc, U);
     float sum = 0.f;
     for (int t = pc.t0; t < pc.t1; ++t) {
         const int tile = tile_of(pc, t);
-        if (!at_edge(p, pc, tile, U)) continue;
+        if (!edge(tile)) continue;
         for (int key = tile * kN; key < min(tile * kN + kN, min(pc.L, pos + 1)); ++key) {
             if (p.window > 0 && key <= pos - p.window && key >= p.n_sink) continue;
             const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v);
@@ -794,14 +822,19 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         const bool busy = __any_sync(0xffffffffu, valid);
         const int pos = valid ? pc.L - pc.n + token : 0x3fffffff;
         const Need need(p, pc, w, TM);
+        const Edge at_edge(p, pc, U);
         float m = -INFINITY, l = 0.f;  // reference maximum (raw score units), sum
         bool ok = true, any = false;   // any: a product of this piece has been or will be added to O
         const int step = pc.pair ? 1 : 2;
         const int t_first = pc.t0 + (pc.pair ? 0 : w);
-        int m_next = t_first < pc.t1 ? need(tile_of(pc, t_first)) : 0;
+        auto wants = [&](int t) {  // the halves of a tile of the list, and bit 2: it is at an edge
+            const int tile = tile_of(pc, t);
+            return at_edge(tile) ? need(tile) | 4 : 3;
+        };
+        int m_next = t_first < pc.t1 ? wants(t_first) : 0;
         for (int t = t_first; t < pc.t1 && ok; t += step) {
             const int tile = tile_of(pc, t), halves = m_next;
-            m_next = t + step < pc.t1 ? need(tile_of(pc, t + step)) : 0;
+            m_next = t + step < pc.t1 ? wants(t + step) : 0;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (!(halves >> h & 1)) continue;
@@ -812,17 +845,16 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                     uint32_t s[2][32];
                     tmem_ld_32x32b_x32(tS + kSub * h, s[0]);
                     tmem_ld_32x32b_x32(tS + kSub * h + 32, s[1]);
-                    const int ts = tile * kN + kSub * h;
-                    const int hi = pos - ts;  // last key seen
-                    const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
-                    const bool edge = __any_sync(0xffffffffu, hi < kSub - 1 || (lo > 0 && sk < kSub));
                     tmem_ld_wait(s[0]);
                     tmem_ld_wait(s[1]);
                     if (negative) {
 #pragma unroll
                         for (int a = 0; a < kSub; ++a) s[a / 32][a % 32] ^= 0x80000000u;
                     }
-                    if (edge) {
+                    if (halves & 4) {
+                        const int ts = tile * kN + kSub * h;
+                        const int hi = pos - ts;  // last key seen
+                        const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
 #pragma unroll
                         for (int a = 0; a < kSub; ++a)
                             if (a > hi || (a < lo && a >= sk)) s[a / 32][a % 32] = 0xff800000u;
@@ -1059,8 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kWarpLoad) {
             load_role<D>(p, sm, &tq, &tk, &tv, lane);
         } else if (warp < kWarpFix) {
-            if (lane == 0) mma_role<D>(p, sm, warp - kWarpMma);
-            __syncwarp();
+            mma_role<D>(p, sm, warp - kWarpMma, lane);
         } else {
             fix_role<D>(p, sm, lane);
         }
