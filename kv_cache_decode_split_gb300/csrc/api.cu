@@ -753,8 +753,8 @@ static int prefill_common(PrefillParams& p, const void* q, const void* k, const 
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.G = Hq / Hkv;
-    p.window = window;
-    p.n_sink = n_sink_tokens;
+    p.window = std::min(window, 1 << 30);  // (lengths are below that)
+    p.n_sink = std::min(n_sink_tokens, 1 << 30);
     p.scale_log2 = scale * 1.4426950408889634f;
     return KVD_OK;
 }
@@ -794,7 +794,7 @@ int attn_prefill_gqa(const void* q, const void* k, const void* v, const int32_t*
     p.Tk = Tk;
     p.k_stride = k_stride;
     p.v_stride = v_stride;
-    return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, stream);
+    return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, ws, stream);
 }
 
 int attn_prefill_gqa_paged(const void* q, const void* k_pool, const void* v_pool,
@@ -831,7 +831,7 @@ int attn_prefill_gqa_paged(const void* q, const void* k_pool, const void* v_pool
     p.page_shift = __builtin_ctz(page_size);
     p.max_pages = max_pages;
     p.num_pages = num_pages;
-    return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, stream);
+    return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, ws, stream);
 }
 
 static int cache_read(bool q4, const void* k_pool, const void* v_pool, const int32_t* block_table,

@@ -200,11 +200,11 @@ int cache_read_launch(const CacheReadParams& p, bool q4, int D, int dtype, cudaS
 // The first piece of a unit of the prefill attention that was cut (prefill_bf16.cu); nt == 0: none.
 struct PrefillHead {
     int c0, n, h, tok0;        // first row, new tokens, KV head, the unit's first new token
-    int nt;                    // tiles
+    int nt, tiles;             // key tiles; query tiles
     long long u, w, V;         // the unit's position and length in the work list, the list's length
 };
 
-// Arguments of the attention of many new tokens of a sequence (prefill_bf16.cu, prefill_simple.cu).
+// Arguments of the attention of many new tokens of a sequence (prefill_bf16.cu, prefill_f32.cu).
 struct PrefillParams {
     const void* q;             // [T, Hq, D], tokens q_stride apart
     const void *k, *v;         // packed [Tk, Hkv, D], or pools [num_pages, Hkv, page_size, D]
@@ -221,7 +221,7 @@ struct PrefillParams {
     int page_shift, max_pages, num_pages;
     int window, n_sink;        // window 0: all
     float scale_log2;
-    // bfloat16: how work is cut, and the pieces of units that were cut
+    // how work is cut, and the pieces of units that were cut
     int unit_cost, flat_slack; // keys that a unit's start and end are worth; see load_role
     int n_cta;                 // CTAs, and 1 / n_cta
     double inv_cta;
@@ -230,7 +230,7 @@ struct PrefillParams {
 };
 size_t prefill_ws_bytes(int D);
 int prefill_bf16_launch(const PrefillParams& p, int D, void* ws, cudaStream_t stream);
-int prefill_f32_launch(const PrefillParams& p, int D, cudaStream_t stream);
+int prefill_f32_launch(const PrefillParams& p, int D, void* ws, cudaStream_t stream);
 
 // Arguments of the attention over a 4-bit cache (gqa_q4_decode.cu).
 struct Q4Params {

@@ -31,37 +31,21 @@
 
 #include <algorithm>
 
-#include "kvd_device.cuh"
-#include "kvd_host.h"
+#include "prefill_common.cuh"
 
 namespace kvd {
 
 namespace {
 
-constexpr int kM = 128;     // rows of a query tile
+using namespace prefill;
+
 constexpr int kN = 128;     // keys of a tile, as it is loaded
 constexpr int kSub = 64;    // keys of a score buffer
-constexpr int kMaxCtas = 256;  // of the main launch
-constexpr int kPieces = 4;  // ring of work descriptions
 constexpr int kSoftWarps = 8;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 11;  // products: warp 9 + stream
 constexpr int kThreads = 384;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrowth = 8.0f;  // log2 units
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream
-
-// One piece of a unit: tiles [t0, t1) of its list.
-struct Piece {
-    int h;
-    int c0, n, L;     // the sequence's first row, new tokens and keys
-    int k0;           // its first key row (packed), or its sequence (paged)
-    int tok0;         // the unit's first new token
-    int nA, tB;       // the list: tiles 0 .. nA - 1, then from tB on
-    int t0, t1, nt;   // nt: tiles of the whole unit; t0 < 0: no more pieces
-    int slot;         // partial result, or -1: the piece is the whole unit
-    int pair;         // two query tiles
-};
 
 template <int D>
 struct Layout {
@@ -86,97 +70,6 @@ struct Smem {
     uint32_t tmem_base;
 };
 
-struct Seq {
-    int c0, n, L, k0;
-};
-
-// Sequence b; n = 0 where its offsets are bad. (b < B)
-__device__ __forceinline__ Seq load_seq(const PrefillParams& p, int b, int* err) {
-    Seq s;
-    int c1;
-    if (p.cu_q) {
-        s.c0 = p.cu_q[b];
-        c1 = p.cu_q[b + 1];
-    } else {
-        s.c0 = b;
-        c1 = b + 1;
-    }
-    bool bad = s.c0 < 0 || c1 < s.c0 || c1 > p.T || (b == 0 && s.c0 != 0);
-    s.n = bad ? 0 : c1 - s.c0;
-    if (p.block_table) {
-        const int len = p.seq_lens[b];
-        s.L = min(max(len, 0), p.max_pages << p.page_shift);
-        s.k0 = b;
-        bad |= len != s.L || s.L < s.n;
-    } else {
-        s.k0 = p.cu_k[b];
-        const int k1 = p.cu_k[b + 1];
-        s.L = k1 - s.k0;
-        if (s.k0 < 0 || k1 < s.k0 || k1 > p.Tk || (b == 0 && s.k0 != 0)) {
-            bad = true;
-            s.n = 0;
-        }
-    }
-    if (bad) record_error(err, KVD_ERR_DEVICE_OOB);
-    return s;
-}
-
-// Length in the work list of a unit, and of a sequence's first m units (of one head): a fixed part and
-// the keys up to the unit's last token, at most what a window leaves. (Only the balance depends on
-// it. flat: every unit counts 1.)
-struct Weigh {
-    long long base, cap;
-    int U, fixed, free;  // free: units before the window cuts their keys
-    bool flat;
-    __device__ __forceinline__ Weigh(const PrefillParams& p, const Seq& s, int u, bool f)
-        : base(max(0, s.L - s.n)), cap(0), U(u), fixed(p.unit_cost), free(0x7fffffff), flat(f) {
-        if (p.window > 0) {
-            const int c = min(p.window, 1 << 30) + U + kN + min(p.n_sink, s.L) - 1;  // < 2^31
-            cap = c;
-            free = c > base ? (c - static_cast<int>(base)) / U : 0;
-        }
-    }
-    __device__ __forceinline__ long long upto(int m) const {
-        if (flat) return m;
-        const long long m1 = min(m, free);
-        return static_cast<long long>(m) * fixed + m1 * base + U * (m1 * (m1 + 1) / 2) + (m - m1) * cap;
-    }
-};
-
-// The tiles that a unit walks: [0, nA) and nt - nA from tB on.
-__device__ __forceinline__ void unit_tiles(const PrefillParams& p, const Seq& s, int tok0, int U,
-                                           int& nA, int& tB, int& nt) {
-    const int first = s.L - s.n + tok0;                      // first and last position
-    const int last = s.L - s.n + min(s.n, tok0 + U) - 1;
-    nA = tB = nt = 0;
-    if (last < 0) return;
-    const int lo = p.window > 0 ? max(0, first - p.window + 1) / kN : 0;
-    const int sink = p.window > 0 ? (min(p.n_sink, last + 1) + kN - 1) / kN : 0;
-    nA = min(sink, lo);
-    tB = lo;
-    nt = nA + last / kN - lo + 1;
-}
-
-// The tiles at a mask's edge: some row of the unit does not see all of them. The mask is applied there,
-// and their values are looked through.
-struct Edge {
-    int from;          // tiles from here on reach past the first row's position
-    int low, sink;     // tiles below `low` lie (in part) behind the last row's window, but those below
-                       // `sink` hold sink tokens only
-    __device__ __forceinline__ Edge(const PrefillParams& p, const Piece& u, int U) {
-        const int first = u.L - u.n + u.tok0, last = u.L - u.n + min(u.n, u.tok0 + U) - 1;
-        from = first < 0 ? 0 : (first + 1) / kN;
-        low = p.window > 0 && last >= p.window ? (last - p.window) / kN + 1 : 0;
-        sink = p.n_sink / kN;
-    }
-    __device__ __forceinline__ bool operator()(int tile) const {
-        return tile >= from || (tile < low && tile >= sink);
-    }
-};
-
-__device__ __forceinline__ int tile_of(const Piece& u, int t) {
-    return t < u.nA ? t : u.tB + (t - u.nA);
-}
 // The halves (of 64 keys) of a tile that some row of a stream sees: bits 0 and 1.
 struct Need {
     int first, last, window, n_sink;  // positions of the stream's first and last row
@@ -209,57 +102,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
-                 : "memory");
-}
-
-// Two float32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair64(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair64(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// 16 columns of tensor memory, one lane a thread; the load's results are there behind the wait.
-__device__ __forceinline__ void tmem_ld_x16(uint32_t t, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(t)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_x16(uint32_t t, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
 // S (tensor memory) = Q (128 rows) K^T (64 keys), both K-major in shared memory.
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
@@ -283,80 +125,18 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t pt, uint32_t v, bo
                        (accumulate || ks > 0) ? 1u : 0u);
 }
 
-// Ranges: CTA c of n takes positions [range_start(c), range_start(c + 1)) of a list of length V. (No
-// quotient: any rule will do that is the same for all CTAs and ascends from 0 to V.)
-__device__ __forceinline__ long long range_start(const PrefillParams& p, long long V, int c) {
-    return c >= p.n_cta ? V : static_cast<long long>(static_cast<double>(V) * (c * p.inv_cta));
-}
-// Tile at which offset y of a unit of length w and nt tiles cuts it.
-__device__ __forceinline__ int cut_tile(const PrefillParams& p, long long y, long long w, int nt) {
-    if (y <= 0) return 0;
-    if (y >= w) return nt;
-    return static_cast<int>(min(static_cast<long long>(nt), max(0LL, (y - p.unit_cost) / kN)));
-}
-
-// Largest i in [0, n) with f(i) <= x, f ascending, f(0) <= x; by the warp, 32 at a time.
-template <typename F>
-__device__ __forceinline__ int last_below(int n, long long x, int lane, F&& f) {
-    int lo = 0;
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const bool le = lane * step < n && f(lo + lane * step) <= x;
-        const unsigned m = __ballot_sync(0xffffffffu, le);
-        const int k = m ? 31 - __clz(m) : 0;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    return lo;
-}
-
 // ------------------------------------------------------------------------------------- loads
 template <int D>
 __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap* tq,
                           const CUtensorMap* tk, const CUtensorMap* tv, int lane) {
     using Ly = Layout<D>;
     const int TM = kM / p.G, U = 2 * TM;
-    const int cta = blockIdx.x, n_cta = p.n_cta;
     int* err = p.err;
-    // how long the list is
-    long long V = 0, units = 0, longest = 0;
-    for (int base = 0; base < p.B; base += 128) {
-        Seq s[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = base + i * 32 + lane;
-            s[i].n = 0;
-            if (b < p.B) s[i] = load_seq(p, b, cta == 0 ? err : nullptr);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (s[i].n == 0) continue;
-            const int nm = (s[i].n + U - 1) / U;
-            const Weigh w(p, s[i], U, false);
-            const long long all = w.upto(nm);
-            V += all * p.Hkv;
-            units += static_cast<long long>(nm) * p.Hkv;
-            longest = max(longest, all - w.upto(nm - 1));
-        }
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        V += __shfl_xor_sync(0xffffffffu, V, off);
-        units += __shfl_xor_sync(0xffffffffu, units, off);
-        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, off));
-    }
-    // few short units: a CTA each, nothing is cut
-    const bool flat = units <= n_cta && longest <= range_start(p, V, 1) + p.flat_slack;
-    if (flat) V = units;
-    const long long x0 = flat ? min(static_cast<long long>(cta), V) : range_start(p, V, cta);
-    const long long x1 = flat ? min(cta + 1LL, V) : range_start(p, V, cta + 1);
-
     int ps = 0;               // pieces published
     uint32_t g = 0, nq = 0;   // ring items and query loads issued
     uint32_t joints = 0;      // the last items, newest in bit 0: whether each is let go with the next
     uint32_t let_go = 0;      // a parity bit for each slot's barrier
     bool ok = true;
-    if (lane == 0) p.head[cta].nt = 0;
     auto publish = [&](const Piece& u) {
         const int i = ps % kPieces;
         if (lane == 0) {
@@ -371,203 +151,108 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
         ++ps;
     };
 
-    // the sequence that position x0 falls in
-    int b0 = 0;        // 32 sequences, one a lane
-    long long at = 0;  // position of the first of them
-    Seq mine;
-    long long my_len = 0;
-    auto load_batch = [&]() {
-        const int b = b0 + lane;
-        mine.n = mine.c0 = mine.L = mine.k0 = 0;
-        if (b < p.B) mine = load_seq(p, b, nullptr);
-        my_len = 0;
-        if (mine.n > 0) my_len = Weigh(p, mine, U, flat).upto((mine.n + U - 1) / U) * p.Hkv;
-    };
-    int j = 0;
-    if (x0 < x1) {
-        for (;; b0 += 32) {
-            if (b0 >= p.B) {  // (not while the lengths stay as they are)
-                at = x1;
-                break;
+    walk<kN>(p, U, TM, lane, [&](const Piece& pc) {
+        publish(pc);
+        if (!ok) return false;
+        const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
+        if (nt == 0) return true;
+        const Edge<kN> edge(p, pc, U);
+        // queries
+        if (lane == 0) {
+            ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err);
+            if (ok) {
+                const int rows = TM * p.G;
+                mbar_arrive_expect_tx(&sm.qfull, (pc.pair ? 2 : 1) * rows * D * 2);
+                for (int i = 0; i <= pc.pair; ++i)
+                    for (int k = 0; k < D / 64; ++k)
+                        tma_load_4d(sm.q[i] + k * kM * 128, tq, &sm.qfull, 0, pc.h * p.G,
+                                    pc.c0 + pc.tok0 + i * TM, k);
             }
-            load_batch();
-            long long incl = my_len;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += y;
-            }
-            const unsigned m = __ballot_sync(0xffffffffu, at + incl > x0);
-            if (m) {
-                j = __ffs(m) - 1;
-                at += __shfl_sync(0xffffffffu, incl - my_len, j);
-                break;
-            }
-            at += __shfl_sync(0xffffffffu, incl, 31);
         }
-    }
-    bool first_seq = true;
-    while (ok && at < x1 && x0 < x1) {
-        Seq s;
-        s.c0 = __shfl_sync(0xffffffffu, mine.c0, j);
-        s.n = __shfl_sync(0xffffffffu, mine.n, j);
-        s.L = __shfl_sync(0xffffffffu, mine.L, j);
-        s.k0 = __shfl_sync(0xffffffffu, mine.k0, j);
-        if (s.n > 0) {
-            const int nm = (s.n + U - 1) / U;
-            const Weigh wt(p, s, U, flat);
-            const long long per_head = wt.upto(nm);
-            int h = 0, m = 0;
-            long long u = at;  // position of the unit
-            if (first_seq) {
-                long long rem = x0 - at;
-                h = last_below(p.Hkv, rem, lane, [&](int i) { return i * per_head; });
-                rem -= h * per_head;
-                m = last_below(nm, rem, lane, [&](int i) { return wt.upto(i); });
-                u = at + h * per_head + wt.upto(m);
-            }
-            for (; h < p.Hkv && u < x1 && ok; ++h, m = 0) {
-                for (; m < nm && u < x1 && ok; ++m) {
-                    const long long w = wt.upto(m + 1) - wt.upto(m);
-                    Piece pc;
-                    pc.h = h;
-                    pc.c0 = s.c0;
-                    pc.n = s.n;
-                    pc.L = s.L;
-                    pc.k0 = s.k0;
-                    pc.tok0 = m * U;
-                    unit_tiles(p, s, pc.tok0, U, pc.nA, pc.tB, pc.nt);
-                    pc.t0 = cut_tile(p, x0 - u, w, pc.nt);
-                    pc.t1 = cut_tile(p, x1 - u, w, pc.nt);
-                    pc.pair = s.n - pc.tok0 > TM;
-                    const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
-                    pc.slot = whole ? -1 : 2 * cta + (pc.t0 == 0 ? 1 : 0);
-                    const long long start = u;
-                    u += w;
-                    if (pc.nt == 0 ? start < x0 : pc.t0 == pc.t1) continue;
-                    if (lane == 0 && !whole && pc.t0 == 0) {
-                        // the unit's first piece: what the merge needs to know
-                        PrefillHead& hd = p.head[cta];
-                        hd.c0 = pc.c0;
-                        hd.n = pc.n;
-                        hd.h = h;
-                        hd.tok0 = pc.tok0;
-                        hd.u = start;
-                        hd.w = w;
-                        hd.V = V;
-                        hd.nt = pc.nt;
-                    }
-                    publish(pc);
-                    if (!ok) break;
-                    const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
-                    if (nt == 0) continue;
-                    const Edge edge(p, pc, U);
-                    // queries
-                    if (lane == 0) {
-                        ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err);
-                        if (ok) {
-                            const int rows = TM * p.G;
-                            mbar_arrive_expect_tx(&sm.qfull, (pc.pair ? 2 : 1) * rows * D * 2);
-                            for (int i = 0; i <= pc.pair; ++i)
-                                for (int k = 0; k < D / 64; ++k)
-                                    tma_load_4d(sm.q[i] + k * kM * 128, tq, &sm.qfull, 0, h * p.G,
-                                                pc.c0 + pc.tok0 + i * TM, k);
-                        }
-                    }
-                    ++nq;
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    // keys and values; paged: page ids 32 at a time, the next 32 on their way
-                    const int shift = min(p.page_shift, 7);          // rows of one copy
-                    const int per = kN >> shift;                     // copies of a tile (and block)
-                    auto row_of = [&](int e) -> int {                // entry e: row of the copy
-                        const int t = e / per;
-                        if (t >= nt) return 0;
-                        const int tok = tile_of(pc, pc.t0 + t) * kN + ((e % per) << shift);
-                        if (!p.block_table) return pc.k0 + tok;
-                        const int safe = min(tok, pc.L - 1);
-                        const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
-                                                 safe >> p.page_shift, err);
-                        return ((pg * p.Hkv + h) << p.page_shift) + (tok & ((1 << p.page_shift) - 1));
-                    };
-                    const bool paged = p.block_table != nullptr;
-                    const int hz = paged ? 0 : h;
-                    // keys run ahead of values by `la` tiles: each has its own place in the entries
-                    int kb = 0, vb = 0;
-                    int kcur = 0, knxt = 0, vcur = 0;
-                    if (paged) {
-                        kcur = row_of(lane);
-                        knxt = row_of(32 + lane);
-                        vcur = kcur;
-                    }
-                    auto fetch = [&](int t, bool is_v) {
-                        const int s_ = g % Ly::kStages;
-                        const bool joint = is_v && t + la < nt;  // let go together with the next item
-                        if (lane == 0) {
-                            // what this slot held, if anything, has been read: its barrier says so, or
-                            // that of the item behind it
-                            if (g >= Ly::kStages) {
-                                const int b = (joints >> (Ly::kStages - 1)) & 1 ? (s_ + 1) % Ly::kStages : s_;
-                                ok = mbar_wait(&sm.empty[b], let_go >> b & 1, err);
-                                if (b == s_) let_go ^= 1u << b;  // (of two items: with the second)
-                            }
-                            if (ok) {
-                                mbar_arrive_expect_tx(&sm.full[s_], Ly::kTile);
-                                if (is_v && edge(tile_of(pc, pc.t0 + t))) mbar_arrive(&sm.issued[s_]);
-                            }
-                        }
-                        joints = joints << 1 | (joint ? 1u : 0u);
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (!ok) return;
-                        ++g;
-                        const CUtensorMap* map = is_v ? tv : tk;
-                        if (!paged) {
-                            if (lane == 0)
-                                tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0,
-                                            pc.k0 + tile_of(pc, pc.t0 + t) * kN, 0, hz);
-                            return;
-                        }
-                        const int e0 = t * per;
-                        if (is_v) {
-                            if (e0 >= vb + 32) {
-                                vb += 32;
-                                vcur = vb == kb ? kcur : row_of(vb + lane);
-                            }
-                        } else if (e0 >= kb + 32) {
-                            kb += 32;
-                            kcur = knxt;
-                            knxt = row_of(kb + 32 + lane);
-                        }
-                        // entry e0 + i is with lane e0 - base + i, which issues that copy
-                        const int i = lane - (e0 - (is_v ? vb : kb));
-                        if (i >= 0 && i < per) {
-                            const int row = is_v ? vcur : kcur;
-                            if (per == 1) {
-                                tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0, row, 0, 0);
-                            } else {
-                                for (int k = 0; k < D / 64; ++k)
-                                    tma_load_4d(sm.kv[s_] + k * kN * 128 + ((i << shift) * 128), map,
-                                                &sm.full[s_], 0, row, k, 0);
-                            }
-                        }
-                        __syncwarp();
-                    };
-                    for (int t = 0; t < la && t < nt && ok; ++t) fetch(t, false);
-                    for (int t = 0; t < nt && ok; ++t) {
-                        fetch(t, true);
-                        if (t + la < nt && ok) fetch(t + la, false);
-                    }
+        ++nq;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        // keys and values; paged: page ids 32 at a time, the next 32 on their way
+        const int shift = min(p.page_shift, 7);          // rows of one copy
+        const int per = kN >> shift;                     // copies of a tile (and block)
+        auto row_of = [&](int e) -> int {                // entry e: row of the copy
+            const int t = e / per;
+            if (t >= nt) return 0;
+            const int tok = tile_of(pc, pc.t0 + t) * kN + ((e % per) << shift);
+            if (!p.block_table) return pc.k0 + tok;
+            const int safe = min(tok, pc.L - 1);
+            const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
+                                     safe >> p.page_shift, err);
+            return ((pg * p.Hkv + pc.h) << p.page_shift) + (tok & ((1 << p.page_shift) - 1));
+        };
+        const bool paged = p.block_table != nullptr;
+        const int hz = paged ? 0 : pc.h;
+        // keys run ahead of values by `la` tiles: each has its own place in the entries
+        int kb = 0, vb = 0;
+        int kcur = 0, knxt = 0, vcur = 0;
+        if (paged) {
+            kcur = row_of(lane);
+            knxt = row_of(32 + lane);
+            vcur = kcur;
+        }
+        auto fetch = [&](int t, bool is_v) {
+            const int s_ = g % Ly::kStages;
+            const bool joint = is_v && t + la < nt;  // let go together with the next item
+            if (lane == 0) {
+                // what this slot held, if anything, has been read: its barrier says so, or
+                // that of the item behind it
+                if (g >= Ly::kStages) {
+                    const int b = (joints >> (Ly::kStages - 1)) & 1 ? (s_ + 1) % Ly::kStages : s_;
+                    ok = mbar_wait(&sm.empty[b], let_go >> b & 1, err);
+                    if (b == s_) let_go ^= 1u << b;  // (of two items: with the second)
+                }
+                if (ok) {
+                    mbar_arrive_expect_tx(&sm.full[s_], Ly::kTile);
+                    if (is_v && edge(tile_of(pc, pc.t0 + t))) mbar_arrive(&sm.issued[s_]);
                 }
             }
+            joints = joints << 1 | (joint ? 1u : 0u);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) return;
+            ++g;
+            const CUtensorMap* map = is_v ? tv : tk;
+            if (!paged) {
+                if (lane == 0)
+                    tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0,
+                                pc.k0 + tile_of(pc, pc.t0 + t) * kN, 0, hz);
+                return;
+            }
+            const int e0 = t * per;
+            if (is_v) {
+                if (e0 >= vb + 32) {
+                    vb += 32;
+                    vcur = vb == kb ? kcur : row_of(vb + lane);
+                }
+            } else if (e0 >= kb + 32) {
+                kb += 32;
+                kcur = knxt;
+                knxt = row_of(kb + 32 + lane);
+            }
+            // entry e0 + i is with lane e0 - base + i, which issues that copy
+            const int i = lane - (e0 - (is_v ? vb : kb));
+            if (i >= 0 && i < per) {
+                const int row = is_v ? vcur : kcur;
+                if (per == 1) {
+                    tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0, row, 0, 0);
+                } else {
+                    for (int k = 0; k < D / 64; ++k)
+                        tma_load_4d(sm.kv[s_] + k * kN * 128 + ((i << shift) * 128), map,
+                                    &sm.full[s_], 0, row, k, 0);
+                }
+            }
+            __syncwarp();
+        };
+        for (int t = 0; t < la && t < nt && ok; ++t) fetch(t, false);
+        for (int t = 0; t < nt && ok; ++t) {
+            fetch(t, true);
+            if (t + la < nt && ok) fetch(t + la, false);
         }
-        first_seq = false;
-        at += __shfl_sync(0xffffffffu, my_len, j);
-        if (++j == 32) {
-            j = 0;
-            b0 += 32;
-            load_batch();  // (past the last sequence only when the range ends there)
-        }
-        if (b0 + j >= p.B) break;
-    }
+        return ok;
+    });
     if (ok) {
         Piece last;
         last.t0 = -1;
@@ -629,7 +314,7 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const
         const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
         const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
         const Need need(p, pc, w, TM);
-        const Edge at_edge(p, pc, U);
+        const Edge<kN> at_edge(p, pc, U);
         auto own = [&](int t) { return pc.pair || (t & 1) == w; };
         auto edge = [&](int t) { return at_edge(tile_of(pc, pc.t0 + t)); };
         auto wants = [&](int t, bool at) { return at ? need(tile_of(pc, pc.t0 + t)) : 3; };
@@ -730,7 +415,7 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
-        const Edge edge(p, pc, U);
+        const Edge<kN> edge(p, pc, U);
         bool ok = true;
         for (int t = 0; t < nt && ok; ++t) {
             const int tile = tile_of(pc, pc.t0 + t);
@@ -776,7 +461,7 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
 // What a row gets back, in one column, of the values that were cleared: v itself, where the row sees it.
 template <int D>
 __device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, int U, int pos, int col) {
-    const Edge edge(p, pc, U);
+    const Edge<kN> edge(p, pc, U);
     float sum = 0.f;
     for (int t = pc.t0; t < pc.t1; ++t) {
         const int tile = tile_of(pc, t);
@@ -822,7 +507,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         const bool busy = __any_sync(0xffffffffu, valid);
         const int pos = valid ? pc.L - pc.n + token : 0x3fffffff;
         const Need need(p, pc, w, TM);
-        const Edge at_edge(p, pc, U);
+        const Edge<kN> at_edge(p, pc, U);
         float m = -INFINITY, l = 0.f;  // reference maximum (raw score units), sum
         bool ok = true, any = false;   // any: a product of this piece has been or will be added to O
         const int step = pc.pair ? 1 : 2;
@@ -1102,121 +787,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpMma) tmem_dealloc(sm.tmem_base, 512);
 }
 
-// Merges the pieces of the unit whose first piece CTA x of the main launch took, in their order: a warp
-// a row, its lanes over the pieces for the weights and over the columns for the sums.
-template <int D>
-__global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams p) {
-    __shared__ int slots[kMaxCtas + 1];
-    __shared__ int n_slots;
-    griddep_wait();
-    const PrefillHead hd = p.head[blockIdx.x];
-    if (hd.nt == 0) return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (warp == 0) {
-        // CTAs from x on whose range holds a tile of the unit
-        int n = 0;
-        for (int c0 = blockIdx.x; c0 < p.n_cta; c0 += 32) {
-            const int c = c0 + lane;
-            bool has = false, past = true;
-            if (c < p.n_cta) {
-                const long long a = range_start(p, hd.V, c) - hd.u, b = range_start(p, hd.V, c + 1) - hd.u;
-                has = cut_tile(p, a, hd.w, hd.nt) < cut_tile(p, b, hd.w, hd.nt);
-                past = b >= hd.w;
-            }
-            const unsigned m = __ballot_sync(0xffffffffu, has);
-            if (has) slots[n + __popc(m & ((1u << lane) - 1))] = 2 * c + (c == static_cast<int>(blockIdx.x));
-            n += __popc(m);
-            if (__any_sync(0xffffffffu, past)) break;
-        }
-        if (lane == 0) n_slots = n;
-    }
-    __syncthreads();
-    const int n = n_slots;
-    const int TM = kM / p.G;
-    const bool pair = hd.n - hd.tok0 > TM;
-    const int rows = pair ? 2 * kM : kM;
-    constexpr int E = D / 32;
-    for (int r = blockIdx.y * 4 + warp; r < rows; r += gridDim.y * 4) {
-        const int t = r % kM / p.G, token = hd.tok0 + (r / kM) * TM + t;
-        if (t >= TM || token >= hd.n) continue;
-        const int head = hd.h * p.G + (r % kM - t * p.G);
-        // the row's maximum, sink included
-        const float sink = p.sink_logit ? p.sink_logit[head] * kLog2e : -INFINITY;
-        const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-        float top = -INFINITY;
-        for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[static_cast<size_t>(slots[i]) * 2 * kM + r].x);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        top = fmaxf(top, sink);
-        float sum = 0.f, o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            float f = 0.f;
-            if (i0 + lane < n) {
-                const float2 v = ml[static_cast<size_t>(slots[i0 + lane]) * 2 * kM + r];
-                // (a piece without a maximum: nothing seen, or all of it NaN)
-                f = v.x == -INFINITY ? 1.f : fast_exp2(v.x - top);
-                sum += v.y * f;
-            }
-            const int m = min(32, n - i0);
-#pragma unroll 4
-            for (int i = 0; i < m; ++i) {
-                const float g = __shfl_sync(0xffffffffu, f, i);
-                const float* src = p.part_o + (static_cast<size_t>(slots[i0 + i]) * 2 * kM + r) * D + lane * E;
-                if (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(src);
-                    o[0] = fmaf(v.x, g, o[0]);
-                    o[1] = fmaf(v.y, g, o[1]);
-                    o[E - 2] = fmaf(v.z, g, o[E - 2]);
-                    o[E - 1] = fmaf(v.w, g, o[E - 1]);
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(src);
-                    o[0] = fmaf(v.x, g, o[0]);
-                    o[1] = fmaf(v.y, g, o[1]);
-                }
-            }
-        }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (sink != -INFINITY) sum += fast_exp2(sink - top);
-        const float scale = sum == 0.f ? 0.f : 1.f / sum;
-        const long long row = static_cast<long long>(hd.c0 + token) * p.Hq + head;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * D + lane * E;
-        if (E == 4)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16(o[0] * scale, o[1] * scale), pack_bf16(o[E - 2] * scale, o[E - 1] * scale));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[0] * scale, o[1] * scale);
-        if (p.lse_out && lane == 0)
-            p.lse_out[row] = sum == 0.f ? -INFINITY
-                                        : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
-    }
-}
-
-constexpr int kMergeRows = 8;  // blocks of a unit
-
-int ctas() { return std::min(num_sms(), kMaxCtas); }
-
-struct Plan {
-    size_t off_ml, off_o, total;
-};
-Plan make_plan(int D) {
-    const size_t n = static_cast<size_t>(ctas());
-    Plan pl;
-    pl.off_ml = (n * sizeof(PrefillHead) + 255) & ~static_cast<size_t>(255);
-    pl.off_o = pl.off_ml + n * 2 * 2 * kM * 8;
-    pl.total = pl.off_o + n * 2 * 2 * kM * D * 4;
-    return pl;
-}
-
 template <int D>
 int launch(PrefillParams p, void* ws, cudaStream_t stream) {
-    const Plan pl = make_plan(D);
-    uint8_t* base = static_cast<uint8_t*>(ws);
-    p.head = reinterpret_cast<PrefillHead*>(base);
-    p.part_ml = reinterpret_cast<float*>(base + pl.off_ml);
-    p.part_o = reinterpret_cast<float*>(base + pl.off_o);
     CUtensorMap tq, tk, tv;
     const uint64_t blocks = D / 64;
     {
@@ -1250,21 +822,10 @@ int launch(PrefillParams p, void* ws, cudaStream_t stream) {
     static const cudaError_t set =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (set != cudaSuccess) return KVD_ERR_CUDA;
-    const int TM = kM / p.G, U = 2 * TM, n_cta = ctas();
-    p.n_cta = n_cta;
-    p.inv_cta = 1.0 / n_cta;
-    p.unit_cost = 192;
-    p.flat_slack = 6 * kN;
-    // at most so many units, each at most so long: where both are few, no unit is cut
-    const long long units = static_cast<long long>(p.Hkv) * (p.T / U + std::min(p.B, p.T));
-    if (launch_kernel(kernel, dim3(static_cast<unsigned>(n_cta)), dim3(kThreads), smem, stream, tq, tk,
-                      tv, p) != cudaSuccess)
-        return KVD_ERR_CUDA;
-    const long long keys = p.block_table ? static_cast<long long>(p.max_pages) << p.page_shift : p.Tk;
-    const bool never_cut = units <= n_cta && std::min<long long>(keys, p.window > 0 ? p.window + p.n_sink + U + kN : keys) + U + p.unit_cost <= p.flat_slack;
-    if (!never_cut &&
-        launch_kernel(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(n_cta), kMergeRows), dim3(128), 0,
-                      stream, p) != cudaSuccess)
+    set_plan(p, D, ws, 192, 6 * kN);
+    if (launch_kernel(kernel, dim3(static_cast<unsigned>(p.n_cta)), dim3(kThreads), smem, stream, tq, tk,
+                      tv, p) != cudaSuccess ||
+        launch_merge<D, __nv_bfloat16, kN>(p, 2 * (kM / p.G), stream) != cudaSuccess)
         return KVD_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
 }

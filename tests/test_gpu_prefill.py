@@ -126,6 +126,8 @@ def test_rows_that_see_nothing(kvd, dtype):
         out, lse = c.packed(kvd)
         c.check(out, lse)
         assert (out[:2] == 0).all()
+    c = Case([700], [10], 8, 2, 128, dtype, seed=5)  # a call whose work list new tokens fill
+    c.check(*c.packed(kvd))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
