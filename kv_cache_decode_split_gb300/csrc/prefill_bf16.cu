@@ -140,7 +140,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     auto publish = [&](const Piece& u) {
         const int i = ps % kPieces;
         if (lane == 0) {
-            ok = mbar_wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
+            ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
             if (ok) {
                 sm.piece[i] = u;
                 sm.bad[i] = 0;
@@ -159,7 +159,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
         const Edge<kN> edge(p, pc, U);
         // queries
         if (lane == 0) {
-            ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err);
+            ok = wait(&sm.qempty, (nq & 1) ^ 1, err);
             if (ok) {
                 const int rows = TM * p.G;
                 mbar_arrive_expect_tx(&sm.qfull, (pc.pair ? 2 : 1) * rows * D * 2);
@@ -171,85 +171,70 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
         }
         ++nq;
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        // keys and values; paged: page ids 32 at a time, the next 32 on their way
-        const int shift = min(p.page_shift, 7);          // rows of one copy
-        const int per = kN >> shift;                     // copies of a tile (and block)
-        auto row_of = [&](int e) -> int {                // entry e: row of the copy
+        // keys and values. Item i of the piece: key tiles 0 .. la - 1, then value tile t and key tile
+        // t + la in turn. Paged: a tile is `per` copies of a page's rows; lane e holds the row of copy e of
+        // the next 32, of the keys' in kcur and knxt, of the values' in vcur.
+        const bool paged = p.block_table != nullptr;
+        const int shift = min(p.page_shift, 7), per = paged ? kN >> shift : 1;
+        auto row_of = [&](int e) -> int {
             const int t = e / per;
             if (t >= nt) return 0;
             const int tok = tile_of(pc, pc.t0 + t) * kN + ((e % per) << shift);
-            if (!p.block_table) return pc.k0 + tok;
-            const int safe = min(tok, pc.L - 1);
             const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
-                                     safe >> p.page_shift, err);
+                                     min(tok, pc.L - 1) >> p.page_shift, err);
             return ((pg * p.Hkv + pc.h) << p.page_shift) + (tok & ((1 << p.page_shift) - 1));
         };
-        const bool paged = p.block_table != nullptr;
-        const int hz = paged ? 0 : pc.h;
-        // keys run ahead of values by `la` tiles: each has its own place in the entries
-        int kb = 0, vb = 0;
-        int kcur = 0, knxt = 0, vcur = 0;
-        if (paged) {
-            kcur = row_of(lane);
-            knxt = row_of(32 + lane);
-            vcur = kcur;
-        }
-        auto fetch = [&](int t, bool is_v) {
-            const int s_ = g % Ly::kStages;
-            const bool joint = is_v && t + la < nt;  // let go together with the next item
+        int kb = -32, vb = -32, kcur = 0, knxt = 0, vcur = 0;
+        if (paged) knxt = row_of(lane);
+#pragma unroll 1
+        for (int i = 0; i < 2 * nt && ok; ++i) {
+            // of the items behind the first ones the even are values; as many at the end are values too
+            const int lead = min(la, nt), at = i - lead;
+            const bool tail = i + lead >= 2 * nt, is_v = at >= 0 && (at % 2 == 0 || tail);
+            const int t = tail ? i - nt : is_v ? at / 2 : at < 0 ? i : (at - 1) / 2 + la;
+            const uint32_t s_ = g % Ly::kStages;
             if (lane == 0) {
-                // what this slot held, if anything, has been read: its barrier says so, or
-                // that of the item behind it
+                // what this slot held, if anything, has been read: its barrier says so, or that of the
+                // item behind it
                 if (g >= Ly::kStages) {
                     const int b = (joints >> (Ly::kStages - 1)) & 1 ? (s_ + 1) % Ly::kStages : s_;
-                    ok = mbar_wait(&sm.empty[b], let_go >> b & 1, err);
-                    if (b == s_) let_go ^= 1u << b;  // (of two items: with the second)
+                    ok = wait(&sm.empty[b], let_go >> b & 1, err);
+                    if (b == static_cast<int>(s_)) let_go ^= 1u << b;  // (of two items: with the second)
                 }
                 if (ok) {
                     mbar_arrive_expect_tx(&sm.full[s_], Ly::kTile);
                     if (is_v && edge(tile_of(pc, pc.t0 + t))) mbar_arrive(&sm.issued[s_]);
                 }
             }
-            joints = joints << 1 | (joint ? 1u : 0u);
+            joints = joints << 1 | (is_v && t + la < nt ? 1u : 0u);  // let go together with the next item
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) return;
+            if (!ok) break;
             ++g;
             const CUtensorMap* map = is_v ? tv : tk;
-            if (!paged) {
-                if (lane == 0)
-                    tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0,
-                                pc.k0 + tile_of(pc, pc.t0 + t) * kN, 0, hz);
-                return;
-            }
-            const int e0 = t * per;
-            if (is_v) {
-                if (e0 >= vb + 32) {
-                    vb += 32;
-                    vcur = vb == kb ? kcur : row_of(vb + lane);
+            int row = pc.k0 + tile_of(pc, pc.t0 + t) * kN, e = lane;
+            if (paged) {
+                const int e0 = t * per;
+                if (e0 >= (is_v ? vb : kb) + 32) {
+                    if (is_v) {
+                        vb += 32;
+                        vcur = vb == kb ? kcur : row_of(vb + lane);
+                    } else {
+                        kb += 32;
+                        kcur = knxt;
+                        knxt = row_of(kb + 32 + lane);
+                    }
                 }
-            } else if (e0 >= kb + 32) {
-                kb += 32;
-                kcur = knxt;
-                knxt = row_of(kb + 32 + lane);
+                // copy i of the tile is with lane e0 - base + i, which issues it
+                e = lane - (e0 - (is_v ? vb : kb));
+                row = is_v ? vcur : kcur;
             }
-            // entry e0 + i is with lane e0 - base + i, which issues that copy
-            const int i = lane - (e0 - (is_v ? vb : kb));
-            if (i >= 0 && i < per) {
-                const int row = is_v ? vcur : kcur;
-                if (per == 1) {
-                    tma_load_4d(sm.kv[s_], map, &sm.full[s_], 0, row, 0, 0);
-                } else {
-                    for (int k = 0; k < D / 64; ++k)
-                        tma_load_4d(sm.kv[s_] + k * kN * 128 + ((i << shift) * 128), map,
-                                    &sm.full[s_], 0, row, k, 0);
-                }
+            if (e >= 0 && e < per) {
+                uint8_t* dst = sm.kv[s_] + ((e << shift) * 128);
+                tma_load_4d(dst, map, &sm.full[s_], 0, row, 0, paged ? 0 : pc.h);
+                if (per > 1 && D == 128)
+                    tma_load_4d(dst + kN * 128, map, &sm.full[s_], 0, row, 1, 0);
             }
             __syncwarp();
-        };
-        for (int t = 0; t < la && t < nt && ok; ++t) fetch(t, false);
-        for (int t = 0; t < nt && ok; ++t) {
-            fetch(t, true);
-            if (t + la < nt && ok) fetch(t + la, false);
         }
         return ok;
     });
@@ -262,8 +247,8 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     if (lane == 0) {
         const uint32_t from = g > Ly::kStages ? g - Ly::kStages : 0;
         for (uint32_t i = from; i < g; ++i)
-            mbar_wait(&sm.full[i % Ly::kStages], (i / Ly::kStages) & 1, err);
-        if (nq > 0) mbar_wait(&sm.qfull, (nq - 1) & 1, err);
+            wait(&sm.full[i % Ly::kStages], (i / Ly::kStages) & 1, err);
+        if (nq > 0) wait(&sm.qfull, (nq - 1) & 1, err);
     }
     __syncwarp();
 }
@@ -293,10 +278,10 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const
             round ^= 1;
         }
     };
-    auto wait_k = [&]() { return mbar_wait(&sm.full[slot], round, err); };
+    auto wait_k = [&]() { return wait(&sm.full[slot], round, err); };
     auto wait_v = [&](bool edge) {
         if (!edge) return wait_k();
-        const bool r = mbar_wait(&sm.fixed[slot], (fixed_phase >> slot) & 1, err);
+        const bool r = wait(&sm.fixed[slot], (fixed_phase >> slot) & 1, err);
         fixed_phase ^= 1u << slot;
         return r;
     };
@@ -306,7 +291,7 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const
     };
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!(ok = mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err))) break;
+        if (!(ok = wait(&sm.pfull[i], (k / kPieces) & 1, err))) break;
         const Piece pc = sm.piece[i];
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
@@ -317,7 +302,6 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const
         const Edge<kN> at_edge(p, pc, U);
         auto own = [&](int t) { return pc.pair || (t & 1) == w; };
         auto edge = [&](int t) { return at_edge(tile_of(pc, pc.t0 + t)); };
-        auto wants = [&](int t, bool at) { return at ? need(tile_of(pc, pc.t0 + t)) : 3; };
         auto pass = [&](bool edge_v, bool joint) {  // an item of the other stream
             if (!wait_v(edge_v)) return false;
             __syncwarp();
@@ -325,63 +309,52 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const
             next();
             return true;
         };
-        auto qk = [&](int h, uint32_t kt) {
-            if (one) {
-                issue_qk<D>(tS + kSub * h, q, kt + h * kSub * 128);
-                tc_commit(&sm.sfull[w][h]);
-            }
-        };
+        if (nt > 0 && !(ok = wait(&sm.qfull, nq++ & 1, err))) break;
         bool first = true;  // the next value product is the piece's first
-        if (nt > 0 && !(ok = mbar_wait(&sm.qfull, nq++ & 1, err))) break;
-        bool e = false;  // the stream's next tile is at an edge, and the halves of it that it sees
+        bool e = false;     // the stream's next tile is at an edge, and the halves of it that it sees
         int m = 0;
-        for (int t = 0; t < la && t < nt && ok; ++t) {
-            if (!own(t)) {
-                ok = pass(false, false);
-                continue;
-            }
-            e = edge(t);
-            m = wants(t, e);
-            if (!(ok = wait_k())) break;
-            if (m & 1) qk(0, kv0 + slot * Ly::kTile);
-            if (m & 2) qk(1, kv0 + slot * Ly::kTile);
-            commit(&sm.empty[slot]);
-            if (t + la >= nt) commit(&sm.qempty);
-            next();
-        }
-        if (!(ok = ok && mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
-        for (int t = 0; t < nt && ok; ++t) {
+        // step t: value tile t (from 0 on) and key tile t + la; each half's value product, then, into the
+        // same buffer, the score product of that half of the stream's next tile
+#pragma unroll 1
+        for (int t = -la; t < nt && ok; ++t) {
             const bool more = t + la < nt;
-            if (!own(t)) {
-                ok = pass(edge(t), more);
+            if (t < 0 && !more) continue;
+            if (!own(t + la)) {  // (of the two query tiles' streams, or of every other tile's)
+                if (t >= 0) ok = pass(edge(t), more);
                 if (ok && more) ok = pass(false, false);
                 continue;
             }
-            const uint32_t v = kv0 + slot * Ly::kTile;
-            if (!(ok = wait_v(e))) break;
-            const uint32_t v_slot = slot;
-            next();
+            const uint32_t v = kv0 + slot * Ly::kTile, v_slot = slot;
+            if (t >= 0) {
+                if (!(ok = wait_v(e))) break;
+                next();
+            }
             const uint32_t kt = kv0 + slot * Ly::kTile;
             bool e_next = false;
             int m_next = 0;
             if (more) {
                 e_next = edge(t + la);
-                m_next = wants(t + la, e_next);
+                m_next = e_next ? need(tile_of(pc, pc.t0 + t + la)) : 3;
             }
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (m >> h & 1) {
-                    if (!(ok = mbar_wait(&sm.pready[w][h], np >> h & 1, err))) break;
+                    if (first && !(ok = wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+                    if (!(ok = wait(&sm.pready[w][h], np >> h & 1, err))) break;
                     np ^= 1u << h;
                     tc_fence_after();
                     if (one) issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
                     first = false;
                 }
                 if (h == 0 && more && !(ok = wait_k())) break;
-                if (m_next >> h & 1)
-                    qk(h, kt);
-                else if (m >> h & 1)
+                if (m_next >> h & 1) {
+                    if (one) {
+                        issue_qk<D>(tS + kSub * h, q, kt + h * kSub * 128);
+                        tc_commit(&sm.sfull[w][h]);
+                    }
+                } else if (m >> h & 1) {
                     commit(&sm.pvdone[w][h]);
+                }
             }
             if (!ok) break;
             // the value tile and the next key tile are let go together
@@ -393,13 +366,14 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const
             e = e_next;
             m = m_next;
         }
-        if (!ok) break;
+        // without a product in this piece the barriers' phases still go on
+        if (!ok || (first && !(ok = wait(&sm.ofree[w], (k & 1) ^ 1, err)))) break;
         if (!pc.pair && nt > 0 && nt <= w && one) mbar_arrive(&sm.qempty);
         commit(&sm.ofull[w]);
     }
     // all products complete before tensor memory is released
     commit(&sm.end[w]);
-    mbar_wait(&sm.end[w], 0, err);
+    wait(&sm.end[w], 0, err);
 }
 
 // ------------------------------------------------------------------------- values at the edges
@@ -411,7 +385,7 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
     uint32_t g = 0, phase = 0;  // phase: a bit for each slot
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
@@ -422,8 +396,8 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
             if (!edge(tile)) continue;
             const uint32_t item = g + item_of_v(t, nt, la);
             const int s = item % Ly::kStages;
-            ok = mbar_wait(&sm.issued[s], (phase >> s) & 1, err) &&
-                 mbar_wait(&sm.full[s], (item / Ly::kStages) & 1, err);
+            ok = wait(&sm.issued[s], (phase >> s) & 1, err) &&
+                 wait(&sm.full[s], (item / Ly::kStages) & 1, err);
             if (!ok) break;
             phase ^= 1u << s;
             const int valid = pc.L - tile * kN;  // rows of the sequence
@@ -499,7 +473,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     uint32_t ns = 0, nd = 0, n_two = 0;  // ns, nd: a parity bit for each score buffer
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
@@ -523,7 +497,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (!(halves >> h & 1)) continue;
-                if (!(ok = mbar_wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
+                if (!(ok = wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
                 ns ^= 1u << h;
                 if (busy) {
                     tc_fence_after();
@@ -533,16 +507,24 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                     tmem_ld_wait(s[0]);
                     tmem_ld_wait(s[1]);
                     if (negative) {
+                        uint32_t sign = 0x80000000u;
+                        asm volatile("" : "+r"(sign));  // (nor of this)
 #pragma unroll
-                        for (int a = 0; a < kSub; ++a) s[a / 32][a % 32] ^= 0x80000000u;
+                        for (int a = 0; a < kSub; ++a) s[a / 32][a % 32] ^= sign;
                     }
                     if (halves & 4) {
+                        // the keys seen, a bit each: up to the row's own, in its window or a sink
                         const int ts = tile * kN + kSub * h;
-                        const int hi = pos - ts;  // last key seen
-                        const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0, sk = p.n_sink - ts;
+                        const int hi = pos - ts, lo = p.window > 0 && valid ? hi - p.window + 1 : 0;
+                        auto below = [](int n) -> uint64_t {  // the first n of 64 bits
+                            return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+                        };
+                        const uint64_t seen = below(hi + 1) & (~below(lo) | below(p.n_sink - ts));
+                        uint32_t word[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
+                        asm volatile("" : "+r"(word[0]), "+r"(word[1]));  // (nothing of this ahead of the branch)
 #pragma unroll
                         for (int a = 0; a < kSub; ++a)
-                            if (a > hi || (a < lo && a >= sk)) s[a / 32][a % 32] = 0xff800000u;
+                            if (!(word[a / 32] >> (a % 32) & 1)) s[a / 32][a % 32] = 0xff800000u;
                     }
                     float mx[4];
 #pragma unroll
@@ -569,8 +551,8 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                         // when its barrier says so
                         const int o = 1 - h;
                         const bool more = (h == 0 ? halves : m_next) >> o & 1;
-                        ok = more ? mbar_wait(&sm.sfull[w][o], ns >> o & 1, err)
-                                  : mbar_wait(&sm.pvdone[w][o], (nd >> o & 1) ^ 1, err);
+                        ok = more ? wait(&sm.sfull[w][o], ns >> o & 1, err)
+                                  : wait(&sm.pvdone[w][o], (nd >> o & 1) ^ 1, err);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -624,20 +606,20 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         if (two)
             for (int t = pc.t0 + 1 - w; t < pc.t1; t += 2) has_oth |= need(tile_of(pc, t)) != 0;
         if (two && pc.t1 > pc.t0) {
-            if (!(ok = mbar_wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
+            if (!(ok = wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
             sm.stat[w][r][0] = mc;
             sm.stat[w][r][1] = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.statw[w]);
-            if (!(ok = mbar_wait(&sm.statw[1 - w], n_two & 1, err))) break;
+            if (!(ok = wait(&sm.statw[1 - w], n_two & 1, err))) break;
             oth_m = sm.stat[1 - w][r][0];
             oth_l = sm.stat[1 - w][r][1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.statr[1 - w]);
             ++n_two;
         }
-        if (!(ok = mbar_wait(&sm.ofull[w], k & 1, err))) break;
-        if (two && !(ok = mbar_wait(&sm.ofull[1 - w], k & 1, err))) break;
+        if (!(ok = wait(&sm.ofull[w], k & 1, err))) break;
+        if (two && !(ok = wait(&sm.ofull[1 - w], k & 1, err))) break;
         tc_fence_after();
         const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
         float top = fmaxf(mc, oth_m), own_f = mc == -INFINITY ? 0.f : fast_exp2(mc - top),

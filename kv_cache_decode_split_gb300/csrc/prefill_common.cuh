@@ -33,7 +33,7 @@ struct Seq {
 };
 
 // Sequence b; n = 0 where its offsets are bad. (b < B)
-__device__ __forceinline__ Seq load_seq(const PrefillParams& p, int b, int* err) {
+static __device__ __noinline__ Seq load_seq(const PrefillParams& p, int b, int* err) {
     Seq s;
     int c1;
     if (p.cu_q) {
@@ -78,7 +78,7 @@ struct Weigh {
             free = c > base ? (c - static_cast<int>(base)) / U : 0;
         }
     }
-    __device__ __forceinline__ long long upto(int m) const {
+    __device__ __noinline__ long long upto(int m) const {
         if (flat) return m;
         const long long m1 = min(m, free);
         return static_cast<long long>(m) * fixed + m1 * base + U * (m1 * (m1 + 1) / 2) + (m - m1) * cap;
@@ -124,6 +124,25 @@ __device__ __forceinline__ int tile_of(const Piece& u, int t) {
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
                  : "memory");
+}
+
+// mbar_wait with one copy of its loop: these kernels' code has to fit the instruction caches (see
+// prefill_bf16.cu).
+static __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err) {
+    return mbar_wait(bar, parity, err);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err) {
+    return mbar_try_wait(smem_u32(bar), parity) || wait_on(bar, parity, err);
+}
+
+// Registers of the executing warpgroup's threads, from the CTA's share at launch.
+template <int N>
+__device__ __forceinline__ void regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_fewer() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Two float32 operations in one instruction.
@@ -189,6 +208,7 @@ __device__ __forceinline__ int cut_tile(const PrefillParams& p, long long y, lon
 template <typename F>
 __device__ __forceinline__ int last_below(int n, long long x, int lane, F&& f) {
     int lo = 0;
+#pragma unroll 1
     while (n > 1) {
         const int step = (n + 31) / 32;
         const bool le = lane * step < n && f(lo + lane * step) <= x;
@@ -208,26 +228,18 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
     if (lane == 0) p.head[cta].nt = 0;
     // how long the list is
     long long V = 0, units = 0, longest = 0;
-    for (int base = 0; base < p.B; base += 128) {
-        Seq s[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = base + i * 32 + lane;
-            s[i].n = 0;
-            if (b < p.B) s[i] = load_seq(p, b, cta == 0 ? p.err : nullptr);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (s[i].n == 0) continue;
-            const int nm = (s[i].n + U - 1) / U;
-            const Weigh w(p, s[i], U, false);
-            const long long all = w.upto(nm);
-            V += all * p.Hkv;
-            units += static_cast<long long>(nm) * p.Hkv;
-            longest = max(longest, all - w.upto(nm - 1));
-        }
+#pragma unroll 1
+    for (int b = lane; b < p.B; b += 32) {
+        const Seq s = load_seq(p, b, cta == 0 ? p.err : nullptr);
+        if (s.n == 0) continue;
+        const int nm = (s.n + U - 1) / U;
+        const Weigh w(p, s, U, false);
+        const long long all = w.upto(nm);
+        V += all * p.Hkv;
+        units += static_cast<long long>(nm) * p.Hkv;
+        longest = max(longest, all - w.upto(nm - 1));
     }
-#pragma unroll
+#pragma unroll 1
     for (int off = 16; off; off >>= 1) {
         V += __shfl_xor_sync(0xffffffffu, V, off);
         units += __shfl_xor_sync(0xffffffffu, units, off);
@@ -252,31 +264,33 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
         my_len = 0;
         if (mine.n > 0) my_len = Weigh(p, mine, U, flat).upto((mine.n + U - 1) / U) * p.Hkv;
     };
-    int j = 0;
-    if (x0 < x1) {
-        for (;; b0 += 32) {
-            if (b0 >= p.B) {  // (not while the lengths stay as they are)
-                at = x1;
-                break;
-            }
+    int j = 32;
+    if (x0 >= x1) return;
+    bool first_seq = true;
+#pragma unroll 1
+    while (ok && at < x1) {
+        if (j == 32) {  // the next 32 sequences; at first, those that x0 falls in
+            if (b0 >= p.B) break;
             load_batch();
-            long long incl = my_len;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += y;
-            }
-            const unsigned m = __ballot_sync(0xffffffffu, at + incl > x0);
-            if (m) {
+            j = 0;
+            if (first_seq) {
+                long long incl = my_len;
+#pragma unroll 1
+                for (int off = 1; off < 32; off <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += y;
+                }
+                const unsigned m = __ballot_sync(0xffffffffu, at + incl > x0);
+                if (!m) {
+                    at += __shfl_sync(0xffffffffu, incl, 31);
+                    b0 += 32;
+                    j = 32;
+                    continue;
+                }
                 j = __ffs(m) - 1;
                 at += __shfl_sync(0xffffffffu, incl - my_len, j);
-                break;
             }
-            at += __shfl_sync(0xffffffffu, incl, 31);
         }
-    }
-    bool first_seq = true;
-    while (ok && at < x1 && x0 < x1) {
         Seq s;
         s.c0 = __shfl_sync(0xffffffffu, mine.c0, j);
         s.n = __shfl_sync(0xffffffffu, mine.n, j);
@@ -295,7 +309,9 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
                 m = last_below(nm, rem, lane, [&](int i) { return wt.upto(i); });
                 u = at + h * per_head + wt.upto(m);
             }
+#pragma unroll 1
             for (; h < p.Hkv && u < x1 && ok; ++h, m = 0) {
+#pragma unroll 1
                 for (; m < nm && u < x1 && ok; ++m) {
                     const long long w = wt.upto(m + 1) - wt.upto(m);
                     Piece pc;
@@ -333,12 +349,7 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
         }
         first_seq = false;
         at += __shfl_sync(0xffffffffu, my_len, j);
-        if (++j == 32) {
-            j = 0;
-            b0 += 32;
-            load_batch();  // (past the last sequence only when the range ends there)
-        }
-        if (b0 + j >= p.B) break;
+        if (++j == 32) b0 += 32;
     }
 }
 
