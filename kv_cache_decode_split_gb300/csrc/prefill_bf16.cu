@@ -42,29 +42,33 @@ using namespace prefill;
 constexpr int kN = 128;     // keys of a tile, as it is loaded
 constexpr int kSub = 64;    // keys of a score buffer
 constexpr int kSoftWarps = 8;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpFix = 11;  // products: warp 9 + stream
-constexpr int kThreads = 384;
+constexpr int kWarpLoad = 8, kWarpQk = 9, kWarpPv = 11, kWarpFix = 13;  // products: + stream
+constexpr int kThreads = 512;
+// registers of a thread of the softmax's two and the other two warpgroups, of 128 at launch
+constexpr int kRegsSoft = 176, kRegsOther = 80;
+static_assert(2 * (kRegsSoft + kRegsOther) <= 4 * 128, "registers");
 constexpr float kGrowth = 8.0f;  // log2 units
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream
 
 template <int D>
 struct Layout {
     static constexpr int kTile = kN * D * 2;   // bytes of a key, value or query tile
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 3 : 4;  // rings of key and value tiles
 };
 
 template <int D>
 struct Smem {
     uint8_t q[2][Layout<D>::kTile];                   // offset 0, 1024-aligned
-    uint8_t kv[Layout<D>::kStages][Layout<D>::kTile];
+    uint8_t k[Layout<D>::kK][Layout<D>::kTile];
+    uint8_t v[Layout<D>::kV][Layout<D>::kTile];
     float stat[2][kM][2];                             // one query tile: both streams' (max, sum)
-    uint64_t full[Layout<D>::kStages], empty[Layout<D>::kStages];
-    // values at a mask's edge: under way (a look at `full` alone could take an earlier round of the
-    // ring for this one), and looked through
-    uint64_t issued[Layout<D>::kStages], fixed[Layout<D>::kStages];
+    uint64_t kfull[Layout<D>::kK], kempty[Layout<D>::kK], vfull[Layout<D>::kV], vempty[Layout<D>::kV];
+    // values at a mask's edge: under way (a look at `vfull` alone could take an earlier round of the ring
+    // for this one), and looked through
+    uint64_t issued[Layout<D>::kV], fixed[Layout<D>::kV];
     uint64_t qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
     uint64_t statw[2], statr[2];                      // a stream's stat written; read by the other
-    uint64_t end[2];
+    uint64_t end[4];
     Piece piece[kPieces];
     int bad[kPieces];                                 // a value at a mask's edge was not finite
     uint32_t tmem_base;
@@ -90,9 +94,6 @@ struct Need {
         return bits;
     }
 };
-// Ring items of a piece of nt tiles: `la` key tiles, then value tile t and key tile t + la in turn.
-__device__ __forceinline__ int item_of_v(int t, int nt, int la) { return min(2 * t + la, 2 * nt - 1); }
-
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
                                             int y, int z, int w) {
     asm volatile(
@@ -133,14 +134,12 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     const int TM = kM / p.G, U = 2 * TM;
     int* err = p.err;
     int ps = 0;               // pieces published
-    uint32_t g = 0, nq = 0;   // ring items and query loads issued
-    uint32_t joints = 0;      // the last items, newest in bit 0: whether each is let go with the next
-    uint32_t let_go = 0;      // a parity bit for each slot's barrier
+    uint32_t gk = 0, gv = 0, nq = 0;  // key tiles, value tiles and query loads issued
     bool ok = true;
     auto publish = [&](const Piece& u) {
         const int i = ps % kPieces;
         if (lane == 0) {
-            ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
+            ok = mbar_wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
             if (ok) {
                 sm.piece[i] = u;
                 sm.bad[i] = 0;
@@ -159,7 +158,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
         const Edge<kN> edge(p, pc, U);
         // queries
         if (lane == 0) {
-            ok = wait(&sm.qempty, (nq & 1) ^ 1, err);
+            ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err);
             if (ok) {
                 const int rows = TM * p.G;
                 mbar_arrive_expect_tx(&sm.qfull, (pc.pair ? 2 : 1) * rows * D * 2);
@@ -192,24 +191,18 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
             const int lead = min(la, nt), at = i - lead;
             const bool tail = i + lead >= 2 * nt, is_v = at >= 0 && (at % 2 == 0 || tail);
             const int t = tail ? i - nt : is_v ? at / 2 : at < 0 ? i : (at - 1) / 2 + la;
-            const uint32_t s_ = g % Ly::kStages;
+            const uint32_t n = is_v ? gv : gk, size = is_v ? Ly::kV : Ly::kK, s_ = n % size;
+            uint64_t* full = is_v ? &sm.vfull[s_] : &sm.kfull[s_];
             if (lane == 0) {
-                // what this slot held, if anything, has been read: its barrier says so, or that of the
-                // item behind it
-                if (g >= Ly::kStages) {
-                    const int b = (joints >> (Ly::kStages - 1)) & 1 ? (s_ + 1) % Ly::kStages : s_;
-                    ok = wait(&sm.empty[b], let_go >> b & 1, err);
-                    if (b == static_cast<int>(s_)) let_go ^= 1u << b;  // (of two items: with the second)
-                }
+                ok = mbar_wait(is_v ? &sm.vempty[s_] : &sm.kempty[s_], ((n / size) & 1) ^ 1, err);
                 if (ok) {
-                    mbar_arrive_expect_tx(&sm.full[s_], Ly::kTile);
+                    mbar_arrive_expect_tx(full, Ly::kTile);
                     if (is_v && edge(tile_of(pc, pc.t0 + t))) mbar_arrive(&sm.issued[s_]);
                 }
             }
-            joints = joints << 1 | (is_v && t + la < nt ? 1u : 0u);  // let go together with the next item
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
-            ++g;
+            if (is_v) ++gv; else ++gk;
             const CUtensorMap* map = is_v ? tv : tk;
             int row = pc.k0 + tile_of(pc, pc.t0 + t) * kN, e = lane;
             if (paged) {
@@ -229,10 +222,9 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
                 row = is_v ? vcur : kcur;
             }
             if (e >= 0 && e < per) {
-                uint8_t* dst = sm.kv[s_] + ((e << shift) * 128);
-                tma_load_4d(dst, map, &sm.full[s_], 0, row, 0, paged ? 0 : pc.h);
-                if (per > 1 && D == 128)
-                    tma_load_4d(dst + kN * 128, map, &sm.full[s_], 0, row, 1, 0);
+                uint8_t* dst = (is_v ? sm.v[s_] : sm.k[s_]) + ((e << shift) * 128);
+                tma_load_4d(dst, map, full, 0, row, 0, paged ? 0 : pc.h);
+                if (per > 1 && D == 128) tma_load_4d(dst + kN * 128, map, full, 0, row, 1, 0);
             }
             __syncwarp();
         }
@@ -245,135 +237,152 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     }
     // every copy lands before the CTA ends, also after a wait gave up
     if (lane == 0) {
-        const uint32_t from = g > Ly::kStages ? g - Ly::kStages : 0;
-        for (uint32_t i = from; i < g; ++i)
-            wait(&sm.full[i % Ly::kStages], (i / Ly::kStages) & 1, err);
-        if (nq > 0) wait(&sm.qfull, (nq - 1) & 1, err);
+        for (uint32_t i = gk > Ly::kK ? gk - Ly::kK : 0; i < gk; ++i)
+            mbar_wait(&sm.kfull[i % Ly::kK], (i / Ly::kK) & 1, err);
+        for (uint32_t i = gv > Ly::kV ? gv - Ly::kV : 0; i < gv; ++i)
+            mbar_wait(&sm.vfull[i % Ly::kV], (i / Ly::kV) & 1, err);
+        if (nq > 0) mbar_wait(&sm.qfull, (nq - 1) & 1, err);
     }
     __syncwarp();
 }
 
 // ---------------------------------------------------------------------------------- products
-// One thread for each stream. A stream's products run in the order of their issue, so a score product
-// may overwrite the weights that the value product before it reads; of the other stream's tensor memory
-// it touches nothing. A stream has two score buffers, one for each half of a tile: the score product of
-// the next tile's half follows this half's value product, so that scores wait for the softmax and not
-// the softmax for scores. (One thread for both streams: 2.18 ms for 16385 tokens; one buffer of 128
-// keys a stream: 2.15.) Both threads pass every ring item in order, also one that is the other's.
-template <int D>
-__device__ void mma_role(const PrefillParams& p, Smem<D>& sm, const int w, const int lane) {
-    using Ly = Layout<D>;
-    const int TM = kM / p.G, U = 2 * TM;
-    const uint32_t tmem = sm.tmem_base;
-    const uint32_t tS = tmem + kColS + 128 * w, tO = tmem + kColO + 128 * w;
-    int* err = p.err;
-    uint32_t slot = 0, round = 0;  // next ring item, parity of its round
-    uint32_t fixed_phase = 0, nq = 0, np = 0;  // np: a parity bit for each score buffer
-    const uint32_t kv0 = smem_u32(sm.kv[0]);
-    const bool one = lane == 0;
-    bool ok = true;
-    auto next = [&]() {
-        if (++slot == Ly::kStages) {
+// Four threads: each stream's score products, and its value products. A wait or a commit holds its thread
+// up for some 100 cycles even where it has nothing to wait for, and a product's instructions until the one
+// before has begun: with one thread for a stream's products the tensor cores were idle half of the time
+// (16385 tokens: 1.80 ms; one thread for both streams: 2.18).
+// A stream has two score buffers, one for each half of a tile. The score product into a buffer waits for
+// the value product that reads its weights, the other buffer's softmax runs meanwhile. All threads of a
+// kind pass every tile of their ring in order, also one that is the other stream's.
+
+// A ring's next slot and the parity of its round.
+template <int N>
+struct Turn {
+    uint32_t slot = 0, round = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
             slot = 0;
             round ^= 1;
         }
-    };
-    auto wait_k = [&]() { return wait(&sm.full[slot], round, err); };
-    auto wait_v = [&](bool edge) {
-        if (!edge) return wait_k();
-        const bool r = wait(&sm.fixed[slot], (fixed_phase >> slot) & 1, err);
-        fixed_phase ^= 1u << slot;
-        return r;
-    };
-    // (a commit holds its thread up for some 90 cycles: none that could be left out)
-    auto commit = [&](uint64_t* bar) {
-        if (one) tc_commit(bar);
-    };
+    }
+};
+
+template <int D>
+__device__ void qk_role(const PrefillParams& p, Smem<D>& sm, const int w, const int lane) {
+    using Ly = Layout<D>;
+    const int TM = kM / p.G, U = 2 * TM;
+    const uint32_t tS = sm.tmem_base + kColS + 128 * w, k0 = smem_u32(sm.k[0]);
+    int* err = p.err;
+    const bool one = lane == 0;
+    Turn<Ly::kK> at;
+    uint32_t nq = 0, used = 0;  // used: a parity bit for each buffer's score tiles
+    bool ok = true;
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!(ok = wait(&sm.pfull[i], (k / kPieces) & 1, err))) break;
+        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
         if (pc.t0 < 0) break;
-        const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
+        if (pc.t1 == pc.t0) continue;
         const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
         const Need need(p, pc, w, TM);
-        const Edge<kN> at_edge(p, pc, U);
-        auto own = [&](int t) { return pc.pair || (t & 1) == w; };
-        auto edge = [&](int t) { return at_edge(tile_of(pc, pc.t0 + t)); };
-        auto pass = [&](bool edge_v, bool joint) {  // an item of the other stream
-            if (!wait_v(edge_v)) return false;
-            __syncwarp();
-            if (one && !joint) mbar_arrive(&sm.empty[slot]);
-            next();
-            return true;
-        };
-        if (nt > 0 && !(ok = wait(&sm.qfull, nq++ & 1, err))) break;
-        bool first = true;  // the next value product is the piece's first
-        bool e = false;     // the stream's next tile is at an edge, and the halves of it that it sees
-        int m = 0;
-        // step t: value tile t (from 0 on) and key tile t + la; each half's value product, then, into the
-        // same buffer, the score product of that half of the stream's next tile
+        const Edge<kN> edge(p, pc, U);
+        if (!(ok = mbar_wait(&sm.qfull, nq++ & 1, err))) break;
 #pragma unroll 1
-        for (int t = -la; t < nt && ok; ++t) {
-            const bool more = t + la < nt;
-            if (t < 0 && !more) continue;
-            if (!own(t + la)) {  // (of the two query tiles' streams, or of every other tile's)
-                if (t >= 0) ok = pass(edge(t), more);
-                if (ok && more) ok = pass(false, false);
-                continue;
-            }
-            const uint32_t v = kv0 + slot * Ly::kTile, v_slot = slot;
-            if (t >= 0) {
-                if (!(ok = wait_v(e))) break;
-                next();
-            }
-            const uint32_t kt = kv0 + slot * Ly::kTile;
-            bool e_next = false;
-            int m_next = 0;
-            if (more) {
-                e_next = edge(t + la);
-                m_next = e_next ? need(tile_of(pc, pc.t0 + t + la)) : 3;
-            }
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            const bool own = pc.pair || ((t - pc.t0) & 1) == w;
+            const int tile = tile_of(pc, t), m = !own ? 0 : edge(tile) ? need(tile) : 3;
+            if (!(ok = mbar_wait(&sm.kfull[at.slot], at.round, err))) break;
+            const uint32_t kt = k0 + at.slot * Ly::kTile;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
                 if (m >> h & 1) {
-                    if (first && !(ok = wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
-                    if (!(ok = wait(&sm.pready[w][h], np >> h & 1, err))) break;
-                    np ^= 1u << h;
+                    if (!(ok = mbar_wait(&sm.pvdone[w][h], (used >> h & 1) ^ 1, err))) break;
+                    used ^= 1u << h;
                     tc_fence_after();
-                    if (one) issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
-                    first = false;
-                }
-                if (h == 0 && more && !(ok = wait_k())) break;
-                if (m_next >> h & 1) {
                     if (one) {
                         issue_qk<D>(tS + kSub * h, q, kt + h * kSub * 128);
                         tc_commit(&sm.sfull[w][h]);
                     }
-                } else if (m >> h & 1) {
-                    commit(&sm.pvdone[w][h]);
                 }
-            }
             if (!ok) break;
-            // the value tile and the next key tile are let go together
-            commit(&sm.empty[more ? slot : v_slot]);
-            if (more) {
-                if (t + 2 * la >= nt) commit(&sm.qempty);
-                next();
+            if (one) {
+                if (own)
+                    tc_commit(&sm.kempty[at.slot]);
+                else
+                    mbar_arrive(&sm.kempty[at.slot]);
             }
-            e = e_next;
-            m = m_next;
+            at.next();
         }
-        // without a product in this piece the barriers' phases still go on
-        if (!ok || (first && !(ok = wait(&sm.ofree[w], (k & 1) ^ 1, err)))) break;
-        if (!pc.pair && nt > 0 && nt <= w && one) mbar_arrive(&sm.qempty);
-        commit(&sm.ofull[w]);
+        if (ok && one) tc_commit(&sm.qempty);
     }
     // all products complete before tensor memory is released
-    commit(&sm.end[w]);
-    wait(&sm.end[w], 0, err);
+    if (one) tc_commit(&sm.end[w]);
+    mbar_wait(&sm.end[w], 0, err);
+}
+
+template <int D>
+__device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const int lane) {
+    using Ly = Layout<D>;
+    const int TM = kM / p.G, U = 2 * TM;
+    const uint32_t tS = sm.tmem_base + kColS + 128 * w, tO = sm.tmem_base + kColO + 128 * w;
+    const uint32_t v0 = smem_u32(sm.v[0]);
+    int* err = p.err;
+    const bool one = lane == 0;
+    Turn<Ly::kV> at;
+    uint32_t fixed = 0, np = 0;  // a parity bit for each slot's `fixed`, each buffer's weights
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const int i = k % kPieces;
+        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        const Piece pc = sm.piece[i];
+        __syncwarp();
+        if (one) mbar_arrive(&sm.pempty[i]);
+        if (pc.t0 < 0) break;
+        const Need need(p, pc, w, TM);
+        const Edge<kN> edge(p, pc, U);
+        if (!(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+        bool first = true;  // the next product is the piece's first
+#pragma unroll 1
+        for (int t = pc.t0; t < pc.t1; ++t) {
+            const bool own = pc.pair || ((t - pc.t0) & 1) == w;
+            const int tile = tile_of(pc, t);
+            const bool e = edge(tile);
+            const int m = !own ? 0 : e ? need(tile) : 3;
+            if (e) {
+                ok = mbar_wait(&sm.fixed[at.slot], (fixed >> at.slot) & 1, err);
+                fixed ^= 1u << at.slot;
+            } else {
+                ok = mbar_wait(&sm.vfull[at.slot], at.round, err);
+            }
+            if (!ok) break;
+            const uint32_t v = v0 + at.slot * Ly::kTile;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (m >> h & 1) {
+                    if (!(ok = mbar_wait(&sm.pready[w][h], np >> h & 1, err))) break;
+                    np ^= 1u << h;
+                    tc_fence_after();
+                    if (one) {
+                        issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
+                        tc_commit(&sm.pvdone[w][h]);
+                    }
+                    first = false;
+                }
+            if (!ok) break;
+            if (one) {
+                if (own)
+                    tc_commit(&sm.vempty[at.slot]);
+                else
+                    mbar_arrive(&sm.vempty[at.slot]);
+            }
+            at.next();
+        }
+        if (ok && one) tc_commit(&sm.ofull[w]);
+    }
+    if (one) tc_commit(&sm.end[2 + w]);
+    mbar_wait(&sm.end[2 + w], 0, err);
 }
 
 // ------------------------------------------------------------------------- values at the edges
@@ -382,29 +391,28 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
     using Ly = Layout<D>;
     const int U = 2 * (kM / p.G);
     int* err = p.err;
-    uint32_t g = 0, phase = 0;  // phase: a bit for each slot
+    uint32_t g = 0, phase = 0;  // value tiles before the piece; a bit for each slot
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
-        const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
+        const int nt = pc.t1 - pc.t0;
         const Edge<kN> edge(p, pc, U);
         bool ok = true;
         for (int t = 0; t < nt && ok; ++t) {
             const int tile = tile_of(pc, pc.t0 + t);
             if (!edge(tile)) continue;
-            const uint32_t item = g + item_of_v(t, nt, la);
-            const int s = item % Ly::kStages;
-            ok = wait(&sm.issued[s], (phase >> s) & 1, err) &&
-                 wait(&sm.full[s], (item / Ly::kStages) & 1, err);
+            const uint32_t n = g + t;
+            const int s = n % Ly::kV;
+            ok = mbar_wait(&sm.issued[s], (phase >> s) & 1, err) && mbar_wait(&sm.vfull[s], (n / Ly::kV) & 1, err);
             if (!ok) break;
             phase ^= 1u << s;
             const int valid = pc.L - tile * kN;  // rows of the sequence
             bool bad = false;
 #pragma unroll 8
             for (int c = lane; c < Ly::kTile / 16; c += 32) {
-                uint4* at = reinterpret_cast<uint4*>(sm.kv[s]) + c;
+                uint4* at = reinterpret_cast<uint4*>(sm.v[s]) + c;
                 uint4 v = *at;
                 // bfloat16 pairs whose exponent bits are all ones
                 auto odd = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
@@ -427,7 +435,7 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
         }
         if (lane == 0) mbar_arrive(&sm.pempty[i]);
         if (!ok) break;
-        g += 2 * nt;
+        g += nt;
     }
 }
 
@@ -470,10 +478,10 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     const bool negative = p.scale_log2 < 0.f;
     const float c = fmaxf(fabsf(p.scale_log2), 0x1p-100f);  // (0: -inf times it stays -inf)
     const int tok_r = r / p.G, head_r = r - tok_r * p.G;
-    uint32_t ns = 0, nd = 0, n_two = 0;  // ns, nd: a parity bit for each score buffer
+    uint32_t ns = 0, n_two = 0;  // ns: a parity bit for each score buffer
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
@@ -486,18 +494,12 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         bool ok = true, any = false;   // any: a product of this piece has been or will be added to O
         const int step = pc.pair ? 1 : 2;
         const int t_first = pc.t0 + (pc.pair ? 0 : w);
-        auto wants = [&](int t) {  // the halves of a tile of the list, and bit 2: it is at an edge
-            const int tile = tile_of(pc, t);
-            return at_edge(tile) ? need(tile) | 4 : 3;
-        };
-        int m_next = t_first < pc.t1 ? wants(t_first) : 0;
         for (int t = t_first; t < pc.t1 && ok; t += step) {
-            const int tile = tile_of(pc, t), halves = m_next;
-            m_next = t + step < pc.t1 ? wants(t + step) : 0;
+            const int tile = tile_of(pc, t), halves = at_edge(tile) ? need(tile) | 4 : 3;  // 4: at an edge
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (!(halves >> h & 1)) continue;
-                if (!(ok = wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
+                if (!(ok = mbar_wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
                 ns ^= 1u << h;
                 if (busy) {
                     tc_fence_after();
@@ -546,13 +548,9 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                         l *= fade;
                     }
                     if (any && __any_sync(0xffffffffu, raise)) {
-                        // the other buffer's last product is complete (this buffer's is: its scores
-                        // were issued behind it): when its next scores are there, or, without such,
-                        // when its barrier says so
-                        const int o = 1 - h;
-                        const bool more = (h == 0 ? halves : m_next) >> o & 1;
-                        ok = more ? wait(&sm.sfull[w][o], ns >> o & 1, err)
-                                  : wait(&sm.pvdone[w][o], (nd >> o & 1) ^ 1, err);
+                        // this buffer's last product is complete (its scores waited for it); the
+                        // other's when its barrier says so
+                        ok = mbar_wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -591,7 +589,6 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                     tc_fence_before();
                 }
                 any = true;
-                if (!(m_next >> h & 1)) nd ^= 1u << h;  // its product's completion is signalled
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.pready[w][h]);
             }
@@ -606,20 +603,20 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         if (two)
             for (int t = pc.t0 + 1 - w; t < pc.t1; t += 2) has_oth |= need(tile_of(pc, t)) != 0;
         if (two && pc.t1 > pc.t0) {
-            if (!(ok = wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
+            if (!(ok = mbar_wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
             sm.stat[w][r][0] = mc;
             sm.stat[w][r][1] = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.statw[w]);
-            if (!(ok = wait(&sm.statw[1 - w], n_two & 1, err))) break;
+            if (!(ok = mbar_wait(&sm.statw[1 - w], n_two & 1, err))) break;
             oth_m = sm.stat[1 - w][r][0];
             oth_l = sm.stat[1 - w][r][1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.statr[1 - w]);
             ++n_two;
         }
-        if (!(ok = wait(&sm.ofull[w], k & 1, err))) break;
-        if (two && !(ok = wait(&sm.ofull[1 - w], k & 1, err))) break;
+        if (!(ok = mbar_wait(&sm.ofull[w], k & 1, err))) break;
+        if (two && !(ok = mbar_wait(&sm.ofull[1 - w], k & 1, err))) break;
         tc_fence_after();
         const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
         float top = fmaxf(mc, oth_m), own_f = mc == -INFINITY ? 0.f : fast_exp2(mc - top),
@@ -721,9 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < Layout<D>::kStages; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 2);
+        for (int i = 0; i < Layout<D>::kK; ++i) {
+            mbar_init(&sm.kfull[i], 1);
+            mbar_init(&sm.kempty[i], 2);
+        }
+        for (int i = 0; i < Layout<D>::kV; ++i) {
+            mbar_init(&sm.vfull[i], 1);
+            mbar_init(&sm.vempty[i], 2);
             mbar_init(&sm.issued[i], 1);
             mbar_init(&sm.fixed[i], 1);
         }
@@ -740,33 +741,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.statw[i], 4);
             mbar_init(&sm.statr[i], 4);
             mbar_init(&sm.end[i], 1);
+            mbar_init(&sm.end[2 + i], 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.pfull[i], 1);
-            mbar_init(&sm.pempty[i], 2 + 1 + kSoftWarps);
+            mbar_init(&sm.pempty[i], 4 + 1 + kSoftWarps);
         }
         fence_mbar_init();
     }
-    if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, 512);
+    if (warp == kWarpQk) tmem_alloc(&sm.tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     griddep_wait();
     if (warp < kSoftWarps) {
+        regs_more<kRegsSoft>();
         softmax_role<D>(p, sm, warp, lane);
     } else {
-        if (warp == kWarpLoad) {
+        regs_fewer<kRegsOther>();
+        if (warp == kWarpLoad)
             load_role<D>(p, sm, &tq, &tk, &tv, lane);
-        } else if (warp < kWarpFix) {
-            mma_role<D>(p, sm, warp - kWarpMma, lane);
-        } else {
+        else if (warp < kWarpPv)
+            qk_role<D>(p, sm, warp - kWarpQk, lane);
+        else if (warp < kWarpFix)
+            pv_role<D>(p, sm, warp - kWarpPv, lane);
+        else if (warp == kWarpFix)
             fix_role<D>(p, sm, lane);
-        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWarpMma) tmem_dealloc(sm.tmem_base, 512);
+    if (warp == kWarpQk) tmem_dealloc(sm.tmem_base, 512);
 }
 
 template <int D>

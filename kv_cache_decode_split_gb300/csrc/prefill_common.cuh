@@ -126,15 +126,6 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
                  : "memory");
 }
 
-// mbar_wait with one copy of its loop: these kernels' code has to fit the instruction caches (see
-// prefill_bf16.cu).
-static __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err) {
-    return mbar_wait(bar, parity, err);
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err) {
-    return mbar_try_wait(smem_u32(bar), parity) || wait_on(bar, parity, err);
-}
-
 // Registers of the executing warpgroup's threads, from the CTA's share at launch.
 template <int N>
 __device__ __forceinline__ void regs_more() {
