@@ -466,6 +466,30 @@ __device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, i
     return sum;
 }
 
+// 16-byte pieces of N-lane groups change places: lane i of a group holds piece j of row i in x[j] and then
+// piece i of row j.
+template <int N>
+__device__ __forceinline__ void transpose_pieces(uint4 (&x)[N], int lane) {
+#pragma unroll
+    for (int m = N / 2; m >= 1; m >>= 1) {
+        const bool upper = (lane & m) != 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (j & m) continue;
+            const int k = j | m;
+            uint4 y = upper ? x[j] : x[k];
+            y.x = __shfl_xor_sync(0xffffffffu, y.x, m);
+            y.y = __shfl_xor_sync(0xffffffffu, y.y, m);
+            y.z = __shfl_xor_sync(0xffffffffu, y.z, m);
+            y.w = __shfl_xor_sync(0xffffffffu, y.w, m);
+            if (upper)
+                x[j] = y;
+            else
+                x[k] = y;
+        }
+    }
+}
+
 template <int D>
 __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
     const int w = warp / 4;                       // stream
@@ -645,47 +669,76 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                          static_cast<size_t>(pc.slot) * 2 * kM + (two ? 0 : w * kM) + r;
             *ml = make_float2(top, sum);
         }
-        // one query tile: each warpgroup takes half of the columns, of both accumulators
+        own_f *= scale;
+        oth_f *= scale;
+        // One query tile: each warpgroup takes half of the columns, of both accumulators. Eight lanes
+        // exchange pieces so that they write runs of 128 bytes of a row. (A lane that writes its own row
+        // touches 32 rows an instruction: a unit's end took 8000 cycles.)
         const int col0 = two ? w * (D / 2) : 0, col1 = two ? col0 + D / 2 : D;
+        const bool last = pc.slot < 0;
+        const int size = last ? 2 : 4, step_cols = last ? (col1 - col0 < 64 ? 32 : 64) : 32;
+        char* base = last ? static_cast<char*>(p.out) + static_cast<long long>(pc.c0 + pc.tok0) * p.Hq * D * 2
+                          : reinterpret_cast<char*>(p.part_o) + static_cast<long long>(pc.slot) * 2 * kM * D * 4;
+        const int rel = !valid ? -1 : last ? (token - pc.tok0) * p.Hq + head : (two ? 0 : w * kM) + r;
         if (busy) {
-            for (int col = col0; col < col1; col += 32) {
-                float o[32];
-                {
-                    uint32_t a[32];
-                    if (has_own) {
-                        tmem_ld_32x32b_x32(tO + 128 * w + col, a);
-                        tmem_ld_wait(a);
-                    }
+#pragma unroll 1
+            for (int col = col0; col < col1; col += step_cols) {
+                uint4 x[8];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = has_own ? __uint_as_float(a[e]) * own_f : 0.f;
+                for (int a = 0; a < 4; ++a) {
+                    // 16 columns, or 8 (unfinished: float32) of the 32: two pieces
+                    if (last && 16 * a >= step_cols) {
+                        x[2 * a] = x[2 * a + 1] = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint32_t o[16];
+                    float f[16];
+                    const int c0 = col + (last ? 16 * a : 16 * (a / 2));
+                    if (has_own) tmem_ld_x16(tO + 128 * w + c0, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = has_own ? __uint_as_float(o[e]) * own_f : 0.f;
                     if (has_oth) {
-                        tmem_ld_32x32b_x32(tO + 128 * (1 - w) + col, a);
-                        tmem_ld_wait(a);
+                        tmem_ld_x16(tO + 128 * (1 - w) + c0, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(a[e]), oth_f, o[e]);
+                        for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), oth_f, f[e]);
+                    }
+                    if (last) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            x[2 * a + e] = make_uint4(
+                                pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                                pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int b = 8 * (a % 2) + 4 * e;
+                            x[2 * a + e] = make_uint4(__float_as_uint(f[b]), __float_as_uint(f[b + 1]),
+                                                      __float_as_uint(f[b + 2]), __float_as_uint(f[b + 3]));
+                        }
                     }
                 }
-                if (bad) {
-                    const int seen = valid ? pos : -1;
+                transpose_pieces<8>(x, lane);
+                const int at = col * size + (lane % 8) * 16;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] += cleared<D>(p, pc, U, seen, col + e);
+                for (int j = 0; j < 8; ++j) {
+                    const int to = __shfl_sync(0xffffffffu, rel, (lane & 24) + j);
+                    if (to >= 0 && (lane % 8) * 16 < step_cols * size)
+                        *reinterpret_cast<uint4*>(base + static_cast<long long>(to) * D * size + at) = x[j];
                 }
-                if (valid && pc.slot < 0) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * D + col);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = make_uint4(pack_bf16(o[8 * e] * scale, o[8 * e + 1] * scale),
-                                            pack_bf16(o[8 * e + 2] * scale, o[8 * e + 3] * scale),
-                                            pack_bf16(o[8 * e + 4] * scale, o[8 * e + 5] * scale),
-                                            pack_bf16(o[8 * e + 6] * scale, o[8 * e + 7] * scale));
-                } else if (valid) {
-                    float4* dst = reinterpret_cast<float4*>(
-                        p.part_o + (static_cast<size_t>(pc.slot) * 2 * kM + (two ? 0 : w * kM) + r) * D + col);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                }
+            }
+            if (bad) {
                 __syncwarp();
+#pragma unroll 1
+                for (int col = col0; col < col1 && valid; ++col) {
+                    const float v = cleared<D>(p, pc, U, pos, col);
+                    if (v == 0.f) continue;
+                    char* at = base + (static_cast<long long>(rel) * D + col) * size;
+                    if (last)
+                        *reinterpret_cast<__nv_bfloat16*>(at) =
+                            __float2bfloat16_rn(__bfloat162float(*reinterpret_cast<__nv_bfloat16*>(at)) + v);
+                    else
+                        *reinterpret_cast<float*>(at) += v;
+                }
             }
         }
         tc_fence_before();
