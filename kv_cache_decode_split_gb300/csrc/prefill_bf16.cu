@@ -43,6 +43,7 @@ constexpr int kN = 128;     // keys of a tile, as it is loaded
 constexpr int kSub = 64;    // keys of a score buffer
 constexpr int kSoftWarps = 8;
 constexpr int kWarpLoad = 8, kWarpQk = 9, kWarpPv = 11, kWarpFix = 13;  // products: + stream
+constexpr int kFixWarps = 3;
 constexpr int kThreads = 512;
 // registers of a thread of the softmax's two and the other two warpgroups, of 128 at launch
 constexpr int kRegsSoft = 176, kRegsOther = 80;
@@ -139,7 +140,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     auto publish = [&](const Piece& u) {
         const int i = ps % kPieces;
         if (lane == 0) {
-            ok = mbar_wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
+            ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
             if (ok) {
                 sm.piece[i] = u;
                 sm.bad[i] = 0;
@@ -158,7 +159,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
         const Edge<kN> edge(p, pc, U);
         // queries
         if (lane == 0) {
-            ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err);
+            ok = wait(&sm.qempty, (nq & 1) ^ 1, err);
             if (ok) {
                 const int rows = TM * p.G;
                 mbar_arrive_expect_tx(&sm.qfull, (pc.pair ? 2 : 1) * rows * D * 2);
@@ -194,7 +195,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
             const uint32_t n = is_v ? gv : gk, size = is_v ? Ly::kV : Ly::kK, s_ = n % size;
             uint64_t* full = is_v ? &sm.vfull[s_] : &sm.kfull[s_];
             if (lane == 0) {
-                ok = mbar_wait(is_v ? &sm.vempty[s_] : &sm.kempty[s_], ((n / size) & 1) ^ 1, err);
+                ok = wait(is_v ? &sm.vempty[s_] : &sm.kempty[s_], ((n / size) & 1) ^ 1, err);
                 if (ok) {
                     mbar_arrive_expect_tx(full, Ly::kTile);
                     if (is_v && edge(tile_of(pc, pc.t0 + t))) mbar_arrive(&sm.issued[s_]);
@@ -238,10 +239,10 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     // every copy lands before the CTA ends, also after a wait gave up
     if (lane == 0) {
         for (uint32_t i = gk > Ly::kK ? gk - Ly::kK : 0; i < gk; ++i)
-            mbar_wait(&sm.kfull[i % Ly::kK], (i / Ly::kK) & 1, err);
+            wait(&sm.kfull[i % Ly::kK], (i / Ly::kK) & 1, err);
         for (uint32_t i = gv > Ly::kV ? gv - Ly::kV : 0; i < gv; ++i)
-            mbar_wait(&sm.vfull[i % Ly::kV], (i / Ly::kV) & 1, err);
-        if (nq > 0) mbar_wait(&sm.qfull, (nq - 1) & 1, err);
+            wait(&sm.vfull[i % Ly::kV], (i / Ly::kV) & 1, err);
+        if (nq > 0) wait(&sm.qfull, (nq - 1) & 1, err);
     }
     __syncwarp();
 }
@@ -279,7 +280,7 @@ __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
@@ -288,17 +289,17 @@ __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
         const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
         const Need need(p, pc, w, TM);
         const Edge<kN> edge(p, pc, U);
-        if (!(ok = mbar_wait(&sm.qfull, nq++ & 1, err))) break;
+        if (!(ok = wait(&sm.qfull, nq++ & 1, err))) break;
 #pragma unroll 1
         for (int t = pc.t0; t < pc.t1; ++t) {
             const bool own = pc.pair || ((t - pc.t0) & 1) == w;
             const int tile = tile_of(pc, t), m = !own ? 0 : edge(tile) ? need(tile) : 3;
-            if (!(ok = mbar_wait(&sm.kfull[at.slot], at.round, err))) break;
+            if (!(ok = wait(&sm.kfull[at.slot], at.round, err))) break;
             const uint32_t kt = k0 + at.slot * Ly::kTile;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (m >> h & 1) {
-                    if (!(ok = mbar_wait(&sm.pvdone[w][h], (used >> h & 1) ^ 1, err))) break;
+                    if (!(ok = wait(&sm.pvdone[w][h], (used >> h & 1) ^ 1, err))) break;
                     used ^= 1u << h;
                     tc_fence_after();
                     if (one) {
@@ -319,7 +320,7 @@ __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
     }
     // all products complete before tensor memory is released
     if (one) tc_commit(&sm.end[w]);
-    mbar_wait(&sm.end[w], 0, err);
+    wait(&sm.end[w], 0, err);
 }
 
 template <int D>
@@ -335,14 +336,14 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
         if (pc.t0 < 0) break;
         const Need need(p, pc, w, TM);
         const Edge<kN> edge(p, pc, U);
-        if (!(ok = mbar_wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
+        if (!(ok = wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
         bool first = true;  // the next product is the piece's first
 #pragma unroll 1
         for (int t = pc.t0; t < pc.t1; ++t) {
@@ -351,17 +352,17 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
             const bool e = edge(tile);
             const int m = !own ? 0 : e ? need(tile) : 3;
             if (e) {
-                ok = mbar_wait(&sm.fixed[at.slot], (fixed >> at.slot) & 1, err);
+                ok = wait(&sm.fixed[at.slot], (fixed >> at.slot) & 1, err);
                 fixed ^= 1u << at.slot;
             } else {
-                ok = mbar_wait(&sm.vfull[at.slot], at.round, err);
+                ok = wait(&sm.vfull[at.slot], at.round, err);
             }
             if (!ok) break;
             const uint32_t v = v0 + at.slot * Ly::kTile;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (m >> h & 1) {
-                    if (!(ok = mbar_wait(&sm.pready[w][h], np >> h & 1, err))) break;
+                    if (!(ok = wait(&sm.pready[w][h], np >> h & 1, err))) break;
                     np ^= 1u << h;
                     tc_fence_after();
                     if (one) {
@@ -382,19 +383,19 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
         if (ok && one) tc_commit(&sm.ofull[w]);
     }
     if (one) tc_commit(&sm.end[2 + w]);
-    mbar_wait(&sm.end[2 + w], 0, err);
+    wait(&sm.end[2 + w], 0, err);
 }
 
 // ------------------------------------------------------------------------- values at the edges
 template <int D>
-__device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
+__device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
     using Ly = Layout<D>;
     const int U = 2 * (kM / p.G);
     int* err = p.err;
     uint32_t g = 0, phase = 0;  // value tiles before the piece; a bit for each slot
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0;
@@ -405,13 +406,13 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int lane) {
             if (!edge(tile)) continue;
             const uint32_t n = g + t;
             const int s = n % Ly::kV;
-            ok = mbar_wait(&sm.issued[s], (phase >> s) & 1, err) && mbar_wait(&sm.vfull[s], (n / Ly::kV) & 1, err);
+            ok = wait(&sm.issued[s], (phase >> s) & 1, err) && wait(&sm.vfull[s], (n / Ly::kV) & 1, err);
             if (!ok) break;
             phase ^= 1u << s;
             const int valid = pc.L - tile * kN;  // rows of the sequence
             bool bad = false;
-#pragma unroll 8
-            for (int c = lane; c < Ly::kTile / 16; c += 32) {
+#pragma unroll 2
+            for (int c = warp * 32 + lane; c < Ly::kTile / 16; c += kFixWarps * 32) {
                 uint4* at = reinterpret_cast<uint4*>(sm.v[s]) + c;
                 uint4 v = *at;
                 // bfloat16 pairs whose exponent bits are all ones
@@ -466,30 +467,6 @@ __device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, i
     return sum;
 }
 
-// 16-byte pieces of N-lane groups change places: lane i of a group holds piece j of row i in x[j] and then
-// piece i of row j.
-template <int N>
-__device__ __forceinline__ void transpose_pieces(uint4 (&x)[N], int lane) {
-#pragma unroll
-    for (int m = N / 2; m >= 1; m >>= 1) {
-        const bool upper = (lane & m) != 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (j & m) continue;
-            const int k = j | m;
-            uint4 y = upper ? x[j] : x[k];
-            y.x = __shfl_xor_sync(0xffffffffu, y.x, m);
-            y.y = __shfl_xor_sync(0xffffffffu, y.y, m);
-            y.z = __shfl_xor_sync(0xffffffffu, y.z, m);
-            y.w = __shfl_xor_sync(0xffffffffu, y.w, m);
-            if (upper)
-                x[j] = y;
-            else
-                x[k] = y;
-        }
-    }
-}
-
 template <int D>
 __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
     const int w = warp / 4;                       // stream
@@ -505,7 +482,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     uint32_t ns = 0, n_two = 0;  // ns: a parity bit for each score buffer
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
@@ -523,7 +500,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (!(halves >> h & 1)) continue;
-                if (!(ok = mbar_wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
+                if (!(ok = wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
                 ns ^= 1u << h;
                 if (busy) {
                     tc_fence_after();
@@ -574,7 +551,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                     if (any && __any_sync(0xffffffffu, raise)) {
                         // this buffer's last product is complete (its scores waited for it); the
                         // other's when its barrier says so
-                        ok = mbar_wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err);
+                        ok = wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -627,20 +604,20 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         if (two)
             for (int t = pc.t0 + 1 - w; t < pc.t1; t += 2) has_oth |= need(tile_of(pc, t)) != 0;
         if (two && pc.t1 > pc.t0) {
-            if (!(ok = mbar_wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
+            if (!(ok = wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
             sm.stat[w][r][0] = mc;
             sm.stat[w][r][1] = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.statw[w]);
-            if (!(ok = mbar_wait(&sm.statw[1 - w], n_two & 1, err))) break;
+            if (!(ok = wait(&sm.statw[1 - w], n_two & 1, err))) break;
             oth_m = sm.stat[1 - w][r][0];
             oth_l = sm.stat[1 - w][r][1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.statr[1 - w]);
             ++n_two;
         }
-        if (!(ok = mbar_wait(&sm.ofull[w], k & 1, err))) break;
-        if (two && !(ok = mbar_wait(&sm.ofull[1 - w], k & 1, err))) break;
+        if (!(ok = wait(&sm.ofull[w], k & 1, err))) break;
+        if (two && !(ok = wait(&sm.ofull[1 - w], k & 1, err))) break;
         tc_fence_after();
         const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
         float top = fmaxf(mc, oth_m), own_f = mc == -INFINITY ? 0.f : fast_exp2(mc - top),
@@ -671,75 +648,55 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         }
         own_f *= scale;
         oth_f *= scale;
-        // One query tile: each warpgroup takes half of the columns, of both accumulators. Eight lanes
-        // exchange pieces so that they write runs of 128 bytes of a row. (A lane that writes its own row
-        // touches 32 rows an instruction: a unit's end took 8000 cycles.)
+        // one query tile: each warpgroup takes half of the columns, of both accumulators
         const int col0 = two ? w * (D / 2) : 0, col1 = two ? col0 + D / 2 : D;
         const bool last = pc.slot < 0;
-        const int size = last ? 2 : 4, step_cols = last ? (col1 - col0 < 64 ? 32 : 64) : 32;
-        char* base = last ? static_cast<char*>(p.out) + static_cast<long long>(pc.c0 + pc.tok0) * p.Hq * D * 2
-                          : reinterpret_cast<char*>(p.part_o) + static_cast<long long>(pc.slot) * 2 * kM * D * 4;
-        const int rel = !valid ? -1 : last ? (token - pc.tok0) * p.Hq + head : (two ? 0 : w * kM) + r;
+        char* dst = last ? static_cast<char*>(p.out) + row * D * 2
+                         : reinterpret_cast<char*>(
+                               p.part_o + (static_cast<long long>(pc.slot) * 2 * kM + (two ? 0 : w * kM) + r) * D);
         if (busy) {
+            // (16 columns at a time, rolled: unrolled, or with lanes that exchange pieces to write whole
+            // lines, this took 8000 and 13600 cycles a unit for want of instructions)
 #pragma unroll 1
-            for (int col = col0; col < col1; col += step_cols) {
-                uint4 x[8];
+            for (int col = col0; col < col1; col += 16) {
+                float f[16];
+                uint32_t o[16];
+                if (has_own) tmem_ld_x16(tO + 128 * w + col, o);
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    // 16 columns, or 8 (unfinished: float32) of the 32: two pieces
-                    if (last && 16 * a >= step_cols) {
-                        x[2 * a] = x[2 * a + 1] = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    uint32_t o[16];
-                    float f[16];
-                    const int c0 = col + (last ? 16 * a : 16 * (a / 2));
-                    if (has_own) tmem_ld_x16(tO + 128 * w + c0, o);
+                for (int e = 0; e < 16; ++e) f[e] = has_own ? __uint_as_float(o[e]) * own_f : 0.f;
+                if (has_oth) {
+                    tmem_ld_x16(tO + 128 * (1 - w) + col, o);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = has_own ? __uint_as_float(o[e]) * own_f : 0.f;
-                    if (has_oth) {
-                        tmem_ld_x16(tO + 128 * (1 - w) + c0, o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), oth_f, f[e]);
-                    }
-                    if (last) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            x[2 * a + e] = make_uint4(
-                                pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                                pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int b = 8 * (a % 2) + 4 * e;
-                            x[2 * a + e] = make_uint4(__float_as_uint(f[b]), __float_as_uint(f[b + 1]),
-                                                      __float_as_uint(f[b + 2]), __float_as_uint(f[b + 3]));
-                        }
-                    }
+                    for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), oth_f, f[e]);
                 }
-                transpose_pieces<8>(x, lane);
-                const int at = col * size + (lane % 8) * 16;
+                if (valid && last) {
+                    uint4* at = reinterpret_cast<uint4*>(dst + col * 2);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int to = __shfl_sync(0xffffffffu, rel, (lane & 24) + j);
-                    if (to >= 0 && (lane % 8) * 16 < step_cols * size)
-                        *reinterpret_cast<uint4*>(base + static_cast<long long>(to) * D * size + at) = x[j];
+                    for (int e = 0; e < 2; ++e)
+                        at[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                                           pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+                } else if (valid) {
+                    float4* at = reinterpret_cast<float4*>(dst + col * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        at[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                 }
-            }
-            if (bad) {
                 __syncwarp();
+            }
+            if (bad && valid) {
 #pragma unroll 1
-                for (int col = col0; col < col1 && valid; ++col) {
+                for (int col = col0; col < col1; ++col) {
                     const float v = cleared<D>(p, pc, U, pos, col);
                     if (v == 0.f) continue;
-                    char* at = base + (static_cast<long long>(rel) * D + col) * size;
-                    if (last)
-                        *reinterpret_cast<__nv_bfloat16*>(at) =
-                            __float2bfloat16_rn(__bfloat162float(*reinterpret_cast<__nv_bfloat16*>(at)) + v);
-                    else
-                        *reinterpret_cast<float*>(at) += v;
+                    if (last) {
+                        __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(dst) + col;
+                        *at = __float2bfloat16_rn(__bfloat162float(*at) + v);
+                    } else {
+                        reinterpret_cast<float*>(dst)[col] += v;
+                    }
                 }
             }
+            __syncwarp();
         }
         tc_fence_before();
         __syncwarp();
@@ -779,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.vfull[i], 1);
             mbar_init(&sm.vempty[i], 2);
             mbar_init(&sm.issued[i], 1);
-            mbar_init(&sm.fixed[i], 1);
+            mbar_init(&sm.fixed[i], kFixWarps);
         }
         mbar_init(&sm.qfull, 1);
         mbar_init(&sm.qempty, 2);
@@ -798,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.pfull[i], 1);
-            mbar_init(&sm.pempty[i], 4 + 1 + kSoftWarps);
+            mbar_init(&sm.pempty[i], 4 + kFixWarps + kSoftWarps);
         }
         fence_mbar_init();
     }
@@ -818,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             qk_role<D>(p, sm, warp - kWarpQk, lane);
         else if (warp < kWarpFix)
             pv_role<D>(p, sm, warp - kWarpPv, lane);
-        else if (warp == kWarpFix)
-            fix_role<D>(p, sm, lane);
+        else
+            fix_role<D>(p, sm, warp - kWarpFix, lane);
     }
     tc_fence_before();
     __syncthreads();

@@ -126,6 +126,18 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
                  : "memory");
 }
 
+// mbar_wait in fewer instructions (a failing try_wait sleeps for about 1950 cycles, so this gives up after
+// some 2 s). Code that a unit runs once is not in the instruction caches: it costs some 10 cycles an
+// instruction, so that everything but the loops over tiles is kept short and rolled.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err) {
+    const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+    for (int n = 0; n < 2000000; ++n)
+        if (mbar_try_wait(a, parity)) return true;
+    record_error(err, KVD_ERR_TIMEOUT);
+    return false;
+}
+
 // Registers of the executing warpgroup's threads, from the CTA's share at launch.
 template <int N>
 __device__ __forceinline__ void regs_more() {

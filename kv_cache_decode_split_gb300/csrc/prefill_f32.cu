@@ -110,7 +110,7 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int slot = k % kPieces;
-        if (!mbar_wait(&sm.pfull[slot], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[slot], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[slot];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0;
@@ -143,7 +143,7 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
                 }
             }
             uint32_t& n = is_v ? nv : nk;
-            if (!(ok = mbar_wait(is_v ? &sm.vempty : &sm.kempty, (n & 1) ^ 1, err))) return;
+            if (!(ok = wait(is_v ? &sm.vempty : &sm.kempty, (n & 1) ^ 1, err))) return;
             ++n;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
@@ -157,7 +157,7 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
             done(is_v ? &sm.vfull : &sm.kfull);
         };
         if (nt > 0) {
-            if (!(ok = mbar_wait(&sm.qempty, (nq & 1) ^ 1, err))) break;
+            if (!(ok = wait(&sm.qempty, (nq & 1) ^ 1, err))) break;
             ++nq;
             for (int r = r0; r < kM; r += kStep) {
                 const int t = r / p.G, token = pc.tok0 + t;
@@ -194,7 +194,7 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
     uint32_t nq = 0, nk = 0, np = 0;  // query tiles, key tiles, value tiles taken
     bool ok = true;
     auto qk = [&](bool last) {
-        if (!mbar_wait(&sm.kfull, nk & 1, err)) return false;
+        if (!wait(&sm.kfull, nk & 1, err)) return false;
         tc_fence_after();
         const uint32_t s = tmem + kColS + kN * (nk & 1);
 #pragma unroll
@@ -212,15 +212,15 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
     };
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const int t0 = sm.piece[i].t0, nt = sm.piece[i].t1 - t0;
         mbar_arrive(&sm.pempty[i]);
         if (t0 < 0) break;
         if (nt == 0) continue;
-        if (!(ok = mbar_wait(&sm.qfull, nq++ & 1, err) && qk(nt == 1))) break;
+        if (!(ok = wait(&sm.qfull, nq++ & 1, err) && qk(nt == 1))) break;
         for (int t = 0; t < nt; ++t) {
             if (t + 1 < nt && !(ok = qk(t + 2 == nt))) break;
-            if (!(ok = mbar_wait(&sm.vfull, np & 1, err) && mbar_wait(&sm.pready, np & 1, err))) break;
+            if (!(ok = wait(&sm.vfull, np & 1, err) && wait(&sm.pready, np & 1, err))) break;
             ++np;
             tc_fence_after();
 #pragma unroll
@@ -235,7 +235,7 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
         }
     }
     tc_commit(&sm.end);  // all products complete before tensor memory is released
-    mbar_wait(&sm.end, 0, err);
+    wait(&sm.end, 0, err);
 }
 
 // ----------------------------------------------------------------------------------- softmax
@@ -275,7 +275,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     uint32_t ns = 0, no = 0;  // score tiles and output tiles taken
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!mbar_wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int token = pc.tok0 + tok_r;
@@ -290,7 +290,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         bool ok = true;
         // the tile's outputs are added to the row's
         auto add_tile = [&](float f) {
-            if (!mbar_wait(&sm.ofull, no & 1, err)) return false;
+            if (!wait(&sm.ofull, no & 1, err)) return false;
             ++no;
             if (!busy) return true;
             tc_fence_after();
@@ -309,7 +309,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
             return true;
         };
         for (int t = pc.t0; t < pc.t1; ++t) {
-            if (!(ok = mbar_wait(&sm.sfull[ns & 1], (ns >> 1) & 1, err))) break;
+            if (!(ok = wait(&sm.sfull[ns & 1], (ns >> 1) & 1, err))) break;
             float f = 1.f, s[kN];
             if (busy) {
                 tc_fence_after();
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const PrefillP
                 const int i = ps % kPieces;
                 bool ok = true;
                 if (lane == 0) {
-                    ok = mbar_wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, p.err);
+                    ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, p.err);
                     if (ok) {
                         sm.piece[i] = u;
                         sm.bad[i] = 0;
