@@ -42,12 +42,13 @@ using namespace prefill;
 constexpr int kN = 128;     // keys of a tile, as it is loaded
 constexpr int kSub = 64;    // keys of a score buffer
 constexpr int kSoftWarps = 8;
-constexpr int kWarpLoad = 8, kWarpQk = 9, kWarpPv = 11, kWarpFix = 13;  // products: + stream
+constexpr int kWarpLoad = 8, kWarpQk = 9, kWarpPv = 11, kWarpFix = 13,
+              kWarpEnd = 16;  // products: + stream
 constexpr int kFixWarps = 3;
-constexpr int kThreads = 512;
-// registers of a thread of the softmax's two and the other two warpgroups, of 128 at launch
-constexpr int kRegsSoft = 176, kRegsOther = 80;
-static_assert(2 * (kRegsSoft + kRegsOther) <= 4 * 128, "registers");
+constexpr int kThreads = 640;
+// registers of a thread of the softmax's two and the other three warpgroups, of 96 at launch
+constexpr int kRegsSoft = 120, kRegsOther = 80;
+static_assert(2 * kRegsSoft + 3 * kRegsOther <= 5 * 96, "registers");
 constexpr float kGrowth = 8.0f;  // log2 units
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * stream
 
@@ -62,13 +63,13 @@ struct Smem {
     uint8_t q[2][Layout<D>::kTile];                   // offset 0, 1024-aligned
     uint8_t k[Layout<D>::kK][Layout<D>::kTile];
     uint8_t v[Layout<D>::kV][Layout<D>::kTile];
-    float stat[2][kM][2];                             // one query tile: both streams' (max, sum)
+    float stat[2][kM][2];                             // each stream's rows' (maximum, sum)
     uint64_t kfull[Layout<D>::kK], kempty[Layout<D>::kK], vfull[Layout<D>::kV], vempty[Layout<D>::kV];
     // values at a mask's edge: under way (a look at `vfull` alone could take an earlier round of the ring
     // for this one), and looked through
     uint64_t issued[Layout<D>::kV], fixed[Layout<D>::kV];
     uint64_t qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
-    uint64_t statw[2], statr[2];                      // a stream's stat written; read by the other
+    uint64_t statw[2], statr[2];                      // a stream's stat written, read
     uint64_t end[4];
     Piece piece[kPieces];
     int bad[kPieces];                                 // a value at a mask's edge was not finite
@@ -478,8 +479,8 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     int* err = p.err;
     const bool negative = p.scale_log2 < 0.f;
     const float c = fmaxf(fabsf(p.scale_log2), 0x1p-100f);  // (0: -inf times it stays -inf)
-    const int tok_r = r / p.G, head_r = r - tok_r * p.G;
-    uint32_t ns = 0, n_two = 0;  // ns: a parity bit for each score buffer
+    const int tok_r = r / p.G;
+    uint32_t ns = 0;  // a parity bit for each score buffer
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
         if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
@@ -595,120 +596,152 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
             }
         }
         if (!ok) break;
-        // ---- the piece's end
-        float mc = m == -INFINITY ? -INFINITY : m * c;  // log2 units
-        const bool two = !pc.pair;                      // both streams hold a part
-        float oth_m = -INFINITY, oth_l = 0.f;
-        const bool has_own = any;
-        bool has_oth = false;  // (one query tile: the same keys are seen by both streams' rows)
-        if (two)
-            for (int t = pc.t0 + 1 - w; t < pc.t1; t += 2) has_oth |= need(tile_of(pc, t)) != 0;
-        if (two && pc.t1 > pc.t0) {
-            if (!(ok = wait(&sm.statr[w], (n_two & 1) ^ 1, err))) break;
-            sm.stat[w][r][0] = mc;
-            sm.stat[w][r][1] = l;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.statw[w]);
-            if (!(ok = wait(&sm.statw[1 - w], n_two & 1, err))) break;
-            oth_m = sm.stat[1 - w][r][0];
-            oth_l = sm.stat[1 - w][r][1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.statr[1 - w]);
-            ++n_two;
+        // what the unit's end needs; the softmax goes on with the next piece
+        if (!(ok = wait(&sm.statr[w], (k & 1) ^ 1, err))) break;
+        sm.stat[w][r][0] = m == -INFINITY ? -INFINITY : m * c;  // log2 units
+        sm.stat[w][r][1] = any ? l : -1.f;                      // (below 0: nothing has been added)
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sm.statw[w]);
+            mbar_arrive(&sm.pempty[i]);
         }
-        if (!(ok = wait(&sm.ofull[w], k & 1, err))) break;
-        if (two && !(ok = wait(&sm.ofull[1 - w], k & 1, err))) break;
-        tc_fence_after();
-        const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
-        float top = fmaxf(mc, oth_m), own_f = mc == -INFINITY ? 0.f : fast_exp2(mc - top),
-              oth_f = oth_m == -INFINITY ? 0.f : fast_exp2(oth_m - top);
-        // (a sum that is NaN has a maximum of -inf where all of its scores are NaN)
-        float sum = (mc == -INFINITY ? l : l * own_f) + (oth_m == -INFINITY ? oth_l : oth_l * oth_f);
-        if (mc == -INFINITY && oth_m == -INFINITY) own_f = oth_f = 1.f;
-        float scale = 1.f;
-        const int head = pc.h * p.G + head_r;
-        const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
-        if (pc.slot < 0) {
-            float ref = top;
-            if (p.sink_logit && valid) {
-                const float sink = p.sink_logit[head] * kLog2e;
-                ref = fmaxf(top, sink);
-                const float f = top == -INFINITY ? 1.f : fast_exp2(top - ref);
-                sum = sum * f + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
-                scale = f;
-            }
-            scale = sum == 0.f ? 0.f : scale / sum;
-            if (valid && p.lse_out && (!two || w == 0))
-                p.lse_out[row] = sum == 0.f ? -INFINITY
-                                            : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
-        } else if (valid && (!two || w == 0)) {
-            float2* ml = reinterpret_cast<float2*>(p.part_ml) +
-                         static_cast<size_t>(pc.slot) * 2 * kM + (two ? 0 : w * kM) + r;
-            *ml = make_float2(top, sum);
-        }
-        own_f *= scale;
-        oth_f *= scale;
-        // one query tile: each warpgroup takes half of the columns, of both accumulators
-        const int col0 = two ? w * (D / 2) : 0, col1 = two ? col0 + D / 2 : D;
+    }
+}
+
+// ------------------------------------------------------------------------------------ unit's end
+// 32 bytes (wide: from a multiple of 32).
+__device__ __forceinline__ void store32(char* dst, bool wide, const uint32_t* x) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]),
+                     "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// A piece's rows: from their sums and, as soon as their products are complete, their outputs. (Done by the
+// softmax's warps, this kept them from the next unit's scores for some 9000 cycles a unit.)
+template <int D>
+__device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int lane) {
+    const int r = quarter * 32 + lane;  // row of the tile, lane of tensor memory
+    const int TM = kM / p.G, U = 2 * TM;
+    const uint32_t tO = sm.tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + kColO;
+    int* err = p.err;
+    const int tok_r = r / p.G, head_r = r - tok_r * p.G;
+    for (int k = 0;; ++k) {
+        const int i = k % kPieces;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        const Piece pc = sm.piece[i];
+        if (pc.t0 < 0) break;
         const bool last = pc.slot < 0;
-        char* dst = last ? static_cast<char*>(p.out) + row * D * 2
-                         : reinterpret_cast<char*>(
-                               p.part_o + (static_cast<long long>(pc.slot) * 2 * kM + (two ? 0 : w * kM) + r) * D);
-        if (busy) {
-            // (16 columns at a time, rolled: unrolled, or with lanes that exchange pieces to write whole
-            // lines, this took 8000 and 13600 cycles a unit for want of instructions)
+        const int head = pc.h * p.G + head_r;
+        bool ok = true;
+        // two query tiles: stream w's rows in turn; one: its rows, from both streams
 #pragma unroll 1
-            for (int col = col0; col < col1; col += 16) {
-                float f[16];
-                uint32_t o[16];
-                if (has_own) tmem_ld_x16(tO + 128 * w + col, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) f[e] = has_own ? __uint_as_float(o[e]) * own_f : 0.f;
-                if (has_oth) {
-                    tmem_ld_x16(tO + 128 * (1 - w) + col, o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), oth_f, f[e]);
+        for (int w = 0; w <= pc.pair && ok; ++w) {
+            ok = wait(&sm.statw[w], k & 1, err) && (pc.pair || wait(&sm.statw[1], k & 1, err));
+            if (!ok) break;
+            const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
+            const bool valid = tok_r < TM && token < pc.n;
+            float m0 = sm.stat[w][r][0], l0 = sm.stat[w][r][1], m1 = -INFINITY, l1 = -1.f;
+            if (!pc.pair) {
+                m1 = sm.stat[1][r][0];
+                l1 = sm.stat[1][r][1];
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.statr[w]);
+                if (!pc.pair) mbar_arrive(&sm.statr[1]);
+            }
+            const bool has0 = !(l0 < 0.f), has1 = !(l1 < 0.f);  // (the same for all rows)
+            l0 = has0 ? l0 : 0.f;
+            l1 = has1 ? l1 : 0.f;
+            const float top = fmaxf(m0, m1);
+            float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - top), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - top);
+            // (a sum that is NaN has a maximum of -inf where all of its scores are NaN)
+            float sum = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
+            if (top == -INFINITY) f0 = f1 = 1.f;
+            const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
+            if (last) {
+                float ref = top, scale = 1.f;
+                if (p.sink_logit && valid) {
+                    const float sink = p.sink_logit[head] * kLog2e;
+                    ref = fmaxf(top, sink);
+                    scale = top == -INFINITY ? 1.f : fast_exp2(top - ref);
+                    sum = sum * scale + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
                 }
-                if (valid && last) {
-                    uint4* at = reinterpret_cast<uint4*>(dst + col * 2);
+                scale = sum == 0.f ? 0.f : scale / sum;
+                f0 *= scale;
+                f1 *= scale;
+                if (valid && p.lse_out)
+                    p.lse_out[row] =
+                        sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
+            } else if (valid) {
+                reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(pc.slot) * 2 * kM + w * kM + r] =
+                    make_float2(top, sum);
+            }
+            char* dst = last ? static_cast<char*>(p.out) + row * D * 2
+                             : reinterpret_cast<char*>(
+                                   p.part_o + (static_cast<long long>(pc.slot) * 2 * kM + w * kM + r) * D);
+            const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // (the same for all rows)
+            ok = wait(&sm.ofull[w], k & 1, err) && (pc.pair || wait(&sm.ofull[1], k & 1, err));
+            if (!ok) break;
+            tc_fence_after();
+            const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
+            if (__any_sync(0xffffffffu, valid)) {
+                // 32 bytes a store: the rows that a store's lanes touch, 2.7 cycles each, set its pace.
+                // (Exchanging pieces between lanes first, for runs of 64 bytes, takes more instructions
+                // than that saves.)
+#pragma unroll 1
+                for (int col = 0; col < D; col += 16) {
+                    float f[16];
+                    uint32_t o[16];
+                    if (has0) tmem_ld_x16(tO + 128 * w + col, o);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        at[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                                           pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-                } else if (valid) {
-                    float4* at = reinterpret_cast<float4*>(dst + col * 4);
+                    for (int e = 0; e < 16; ++e) f[e] = has0 ? __uint_as_float(o[e]) * f0 : 0.f;
+                    if (has1) {
+                        tmem_ld_x16(tO + 128 + col, o);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        at[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), f1, f[e]);
+                    }
+                    if (valid && last) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+                        store32(dst + col * 2, wide, o);
+                    } else if (valid) {
+                        store32(dst + col * 4, wide, reinterpret_cast<uint32_t*>(f));
+                        store32(dst + col * 4 + 32, wide, reinterpret_cast<uint32_t*>(f) + 8);
+                    }
+                    __syncwarp();
+                }
+                if (bad && valid) {
+                    const int pos = pc.L - pc.n + token;
+#pragma unroll 1
+                    for (int col = 0; col < D; ++col) {
+                        const float v = cleared<D>(p, pc, U, pos, col);
+                        if (v == 0.f) continue;
+                        if (last) {
+                            __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(dst) + col;
+                            *at = __float2bfloat16_rn(__bfloat162float(*at) + v);
+                        } else {
+                            reinterpret_cast<float*>(dst)[col] += v;
+                        }
+                    }
                 }
                 __syncwarp();
             }
-            if (bad && valid) {
-#pragma unroll 1
-                for (int col = col0; col < col1; ++col) {
-                    const float v = cleared<D>(p, pc, U, pos, col);
-                    if (v == 0.f) continue;
-                    if (last) {
-                        __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(dst) + col;
-                        *at = __float2bfloat16_rn(__bfloat162float(*at) + v);
-                    } else {
-                        reinterpret_cast<float*>(dst)[col] += v;
-                    }
-                }
-            }
+            tc_fence_before();
             __syncwarp();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            if (two) {
-                mbar_arrive(&sm.ofree[0]);
-                mbar_arrive(&sm.ofree[1]);
-            } else {
-                mbar_arrive_n(&sm.ofree[w], 2);
+            if (lane == 0) {
+                mbar_arrive(&sm.ofree[w]);
+                if (!pc.pair) mbar_arrive(&sm.ofree[1]);
             }
-            mbar_arrive(&sm.pempty[i]);
         }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pempty[i]);
     }
 }
 
@@ -747,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.pvdone[i][h], 1);
             }
             mbar_init(&sm.ofull[i], 1);
-            mbar_init(&sm.ofree[i], 8);
+            mbar_init(&sm.ofree[i], 4);
             mbar_init(&sm.statw[i], 4);
             mbar_init(&sm.statr[i], 4);
             mbar_init(&sm.end[i], 1);
@@ -755,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.pfull[i], 1);
-            mbar_init(&sm.pempty[i], 4 + kFixWarps + kSoftWarps);
+            mbar_init(&sm.pempty[i], 4 + kFixWarps + kSoftWarps + 4);
         }
         fence_mbar_init();
     }
@@ -775,6 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             qk_role<D>(p, sm, warp - kWarpQk, lane);
         else if (warp < kWarpFix)
             pv_role<D>(p, sm, warp - kWarpPv, lane);
+        else if (warp >= kWarpEnd)
+            end_role<D>(p, sm, warp - kWarpEnd, lane);
         else
             fix_role<D>(p, sm, warp - kWarpFix, lane);
     }
@@ -819,7 +854,7 @@ int launch(PrefillParams p, void* ws, cudaStream_t stream) {
     static const cudaError_t set =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (set != cudaSuccess) return KVD_ERR_CUDA;
-    set_plan(p, D, ws, 192, 6 * kN);
+    set_plan(p, D, ws, 512, 8 * kN);
     if (launch_kernel(kernel, dim3(static_cast<unsigned>(p.n_cta)), dim3(kThreads), smem, stream, tq, tk,
                       tv, p) != cudaSuccess ||
         launch_merge<D, __nv_bfloat16, kN>(p, 2 * (kM / p.G), stream) != cudaSuccess)
