@@ -222,7 +222,7 @@ struct PrefillParams {
     int window, n_sink;        // window 0: all
     float scale_log2;
     // how work is cut, and the pieces of units that were cut
-    int unit_cost, flat_slack; // keys that a unit's start and end are worth; see load_role
+    int unit_cost, flat_slack; // keys that a unit's start and end are worth; what an uncut call may lose
     int n_cta;                 // CTAs, and 1 / n_cta
     double inv_cta;
     PrefillHead* head;         // [CTAs]
