@@ -38,7 +38,7 @@ constexpr int kWarpConv = 4, kWarpWalk = 12, kWarpMma = 13;
 // registers of a thread of the softmax's, the two converting and the last warpgroup, of 128 at launch
 constexpr int kRegsSoft = 232, kRegsConv = 104, kRegsOther = 72;
 static_assert(kRegsSoft + 2 * kRegsConv + kRegsOther <= 4 * 128, "registers");
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;  // two score tiles; 3 x 32; D
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;  // two score tiles; 3 x 32; two of D
 
 template <int D>
 struct Smem {
@@ -52,13 +52,6 @@ struct Smem {
     uint32_t tmem_base;
 };
 
-__device__ __forceinline__ void tmem_st_x8(uint32_t t, const uint32_t (&r)[8]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-        : "memory");
-}
-
 // Two numbers as three pairs of bfloat16 numbers.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& a, uint32_t& b, uint32_t& c) {
     a = pack_bf16(x, y);
@@ -71,7 +64,8 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& a, uint32_t& 
 }
 
 // The products that are kept, smallest first: part of the left and of the right operand.
-__device__ constexpr int kLeft[6] = {2, 0, 1, 1, 0, 0}, kRight[6] = {0, 2, 1, 0, 1, 0};
+__device__ __forceinline__ int left_part(int i) { return (0x001102 >> (4 * i)) & 3; }   // 2 0 1 1 0 0
+__device__ __forceinline__ int right_part(int i) { return (0x010120 >> (4 * i)) & 3; }  // 0 2 1 0 1 0
 
 // ---------------------------------------------------------------------------------- converting
 // Eight channels (chunk c8) of a row into their three places; part: bytes of a part, rows: of a tile.
@@ -98,14 +92,20 @@ __device__ __forceinline__ void clear4(float4& v) {
     v.w = isfinite(v.w) ? v.w : 0.f;
 }
 
+// A unit's items of 64 rows: the queries (two), then keys and values, K(0), K(1), V(0), K(2), V(1), ...
+// An item's rows are on their way while the one before it is split. (One loop for all of them: code that
+// is not in the instruction caches costs more than its selects.)
 template <int D>
 __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int lane) {
     constexpr int kRow = D / 8;                    // chunks of a row
-    constexpr int kEach = kN * kRow / 256;         // chunks of a key or value tile that a thread takes
+    constexpr int kEach = kN * kRow / 256;         // chunks of an item that a thread takes
+    constexpr int kStep = 256 / kRow;              // in rows r0 + i * kStep
+    struct Rows {
+        float4 x[kEach][2];
+    };
     const int TM = kM / p.G;
     int* err = p.err;
-    const int c8 = tid % kRow, r0 = tid / kRow;    // row r0 + i * (256 / kRow)
-    constexpr int kStep = 256 / kRow;
+    const int c8 = tid % kRow, r0 = tid / kRow;
     uint32_t nq = 0, nk = 0, nv = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -113,70 +113,74 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
         if (!wait(&sm.pfull[slot], (k / kPieces) & 1, err)) break;
         const Piece pc = sm.piece[slot];
         if (pc.t0 < 0) break;
-        const int nt = pc.t1 - pc.t0;
-        auto done = [&](uint64_t* bar) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-        };
-        auto item = [&](int t, bool is_v) {
-            const float* src = static_cast<const float*>(is_v ? p.v : p.k);
+        const int nt = pc.t1 - pc.t0, items = nt > 0 ? 2 * nt : -2;
+        // item i: -2 and -1 are the queries
+        auto is_value = [&](int i) { return i == items - 1 || (i > 0 && i % 2 == 0); };
+        auto load = [&](Rows& rows, int i) {
+            const bool is_v = is_value(i);
+            const int t0 = i < 0 ? 0 : tile_of(pc, pc.t0 + (is_v ? (i == items - 1 ? nt : i / 2) - 1 : (i + 1) / 2)) * kN;
+            const float* base = static_cast<const float*>(i < 0 ? p.q : is_v ? p.v : p.k);
             const long long stride = is_v ? p.v_stride : p.k_stride;
-            const int t0 = tile_of(pc, pc.t0 + t) * kN;
-            float4 x[kEach][2];
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int key = t0 + r0 + i * kStep;
-                x[i][0] = x[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (key < pc.L) {
-                    const float* at;
+            for (int e = 0; e < kEach; ++e) {
+                const int r = r0 + e * kStep;
+                const float* at = nullptr;  // the row; null for one of zeros
+                if (i < 0) {
+                    const int row = (i + 2) * kN + r, t = row / p.G, token = pc.tok0 + t;
+                    if (t < TM && token < pc.n)
+                        at = base + (pc.c0 + token) * p.q_stride +
+                             (pc.h * p.G + (row - t * p.G)) * static_cast<long long>(D);
+                } else if (t0 + r < pc.L) {
                     if (p.block_table) {
+                        const int key = t0 + r;
                         const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
                                                  key >> p.page_shift, err);
-                        at = src + (((static_cast<size_t>(pg) * p.Hkv + pc.h) << p.page_shift) +
-                                    (key & ((1 << p.page_shift) - 1))) * D;
+                        at = base + (((static_cast<size_t>(pg) * p.Hkv + pc.h) << p.page_shift) +
+                                     (key & ((1 << p.page_shift) - 1))) * D;
                     } else {
-                        at = src + (pc.k0 + key) * stride + pc.h * D;
+                        at = base + (pc.k0 + t0 + r) * stride + pc.h * D;
                     }
-                    x[i][0] = reinterpret_cast<const float4*>(at)[2 * c8];
-                    x[i][1] = reinterpret_cast<const float4*>(at)[2 * c8 + 1];
+                }
+                rows.x[e][0] = rows.x[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (at) {
+                    rows.x[e][0] = reinterpret_cast<const float4*>(at)[2 * c8];
+                    rows.x[e][1] = reinterpret_cast<const float4*>(at)[2 * c8 + 1];
                 }
             }
-            uint32_t& n = is_v ? nv : nk;
-            if (!(ok = wait(is_v ? &sm.vempty : &sm.kempty, (n & 1) ^ 1, err))) return;
-            ++n;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                if (is_v && !(finite4(x[i][0]) && finite4(x[i][1]))) {
-                    clear4(x[i][0]);
-                    clear4(x[i][1]);
-                    sm.bad[slot] = 1;
-                }
-                put_split(is_v ? sm.v[0] : sm.k[0], kN * D * 2, kN, r0 + i * kStep, c8, x[i][0], x[i][1]);
-            }
-            done(is_v ? &sm.vfull : &sm.kfull);
         };
-        if (nt > 0) {
-            if (!(ok = wait(&sm.qempty, (nq & 1) ^ 1, err))) break;
-            ++nq;
-            for (int r = r0; r < kM; r += kStep) {
-                const int t = r / p.G, token = pc.tok0 + t;
-                float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-                if (t < TM && token < pc.n) {
-                    const float4* at = reinterpret_cast<const float4*>(
-                        static_cast<const float*>(p.q) + (pc.c0 + token) * p.q_stride +
-                        (pc.h * p.G + (r - t * p.G)) * static_cast<long long>(D));
-                    lo = at[2 * c8];
-                    hi = at[2 * c8 + 1];
-                }
-                put_split(sm.q[0], kM * D * 2, kM, r, c8, lo, hi);
+        Rows rows, next;
+        if (items > 0) load(next, -2);
+#pragma unroll 1
+        for (int i = -2; i < items; ++i) {
+            rows = next;
+            if (i + 1 < items) load(next, i + 1);
+            const bool is_v = is_value(i);
+            uint64_t* full = i < 0 ? &sm.qfull : is_v ? &sm.vfull : &sm.kfull;
+            if (i != -1) {  // (the queries' halves are one wait and one arrival)
+                uint32_t& n = i < 0 ? nq : is_v ? nv : nk;
+                if (!(ok = wait(i < 0 ? &sm.qempty : is_v ? &sm.vempty : &sm.kempty, (n & 1) ^ 1, err))) break;
+                ++n;
             }
-            done(&sm.qfull);
-            item(0, false);
-            for (int t = 0; t < nt && ok; ++t) {
-                if (t + 1 < nt) item(t + 1, false);
-                if (ok) item(t, true);
+            if (is_v) {
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                    if (!(finite4(rows.x[e][0]) && finite4(rows.x[e][1]))) {
+                        clear4(rows.x[e][0]);
+                        clear4(rows.x[e][1]);
+                        bad = true;
+                    }
+                if (bad) sm.bad[slot] = 1;
             }
+            uint8_t* dst = i < 0 ? sm.q[0] : is_v ? sm.v[0] : sm.k[0];
+            const int height = i < 0 ? kM : kN, first = i == -1 ? kN : 0;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                put_split(dst, height * D * 2, height, first + r0 + e * kStep, c8, rows.x[e][0], rows.x[e][1]);
+            if (i == -2) continue;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pempty[slot]);
@@ -197,13 +201,15 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
         if (!wait(&sm.kfull, nk & 1, err)) return false;
         tc_fence_after();
         const uint32_t s = tmem + kColS + kN * (nk & 1);
-#pragma unroll
-        for (int i = 0; i < 6; ++i)
+#pragma unroll 1
+        for (int i = 0; i < 6; ++i) {
+            const uint64_t a = q + ((left_part(i) * kM * D * 2) >> 4);
+            const uint64_t b = kk + ((right_part(i) * kN * D * 2) >> 4);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-                tc_mma_bf16(s, q + ((kLeft[i] * kM * D * 2 + (ks >> 2) * kM * 128 + (ks & 3) * 32) >> 4),
-                            kk + ((kRight[i] * kN * D * 2 + (ks >> 2) * kN * 128 + (ks & 3) * 32) >> 4),
-                            id_qk, i + ks > 0 ? 1u : 0u);
+                tc_mma_bf16(s, a + (((ks >> 2) * kM * 128 + (ks & 3) * 32) >> 4),
+                            b + (((ks >> 2) * kN * 128 + (ks & 3) * 32) >> 4), id_qk, i + ks > 0 ? 1u : 0u);
+        }
         tc_commit(&sm.sfull[nk & 1]);
         tc_commit(&sm.kempty);
         if (last) tc_commit(&sm.qempty);
@@ -221,15 +227,17 @@ __device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
         for (int t = 0; t < nt; ++t) {
             if (t + 1 < nt && !(ok = qk(t + 2 == nt))) break;
             if (!(ok = wait(&sm.vfull, np & 1, err) && wait(&sm.pready, np & 1, err))) break;
+            const uint32_t o = tmem + kColO + 128 * (np & 1);
             ++np;
             tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < 6; ++j)
+#pragma unroll 1
+            for (int j = 0; j < 6; ++j) {
+                const uint32_t a = tmem + kColP + left_part(j) * (kN / 2);
+                const uint64_t b = v + ((right_part(j) * kN * D * 2) >> 4);
 #pragma unroll
                 for (int ks = 0; ks < kN / 16; ++ks)
-                    tc_mma_bf16_ts(tmem + kColO, tmem + kColP + kLeft[j] * (kN / 2) + ks * 8,
-                                   v + ((kRight[j] * kN * D * 2 + ks * 16 * 128) >> 4), id_pv,
-                                   j + ks > 0 ? 1u : 0u);
+                    tc_mma_bf16_ts(o, a + ks * 8, b + ((ks * 16 * 128) >> 4), id_pv, j + ks > 0 ? 1u : 0u);
+            }
             tc_commit(&sm.ofull);
             tc_commit(&sm.vempty);
         }
@@ -283,131 +291,159 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         const bool busy = __any_sync(0xffffffffu, valid);
         const int pos = valid ? pc.L - pc.n + token : 0x3fffffff;
         const Edge<kN> at_edge(p, pc, U);
-        float m = -INFINITY, l = 0.f;  // maximum (raw score units), sum
-        float o[D];
+        float m = -INFINITY, l = 0.f, f = 1.f;  // maximum (raw score units), sum, the last rise's factor
+        uint64_t o[D / 2];
 #pragma unroll
-        for (int e = 0; e < D; ++e) o[e] = 0.f;
+        for (int e = 0; e < D / 2; ++e) o[e] = 0;
         bool ok = true;
-        // the tile's outputs are added to the row's
-        auto add_tile = [&](float f) {
-            if (!wait(&sm.ofull, no & 1, err)) return false;
-            ++no;
-            if (!busy) return true;
+        // the last tile's outputs are added to the row's
+        auto add_tile = [&]() {
+            const uint32_t at = tmem + kColO + 128 * ((no - 1) & 1);
+            const uint64_t f2 = pair64(f, f);
             tc_fence_after();
-            const bool same = __all_sync(0xffffffffu, f == 1.f);
 #pragma unroll
-            for (int a = 0; a < D / 16; ++a) {
-                uint32_t x[16];
-                tmem_ld_x16(tmem + kColO + 16 * a, x);
+            for (int a = 0; a < D / 32; ++a) {
+                uint32_t x[32];
+                tmem_ld_32x32b_x32(at + 32 * a, x);
+                tmem_ld_wait(x);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[16 * a + e] += __uint_as_float(x[e]);
+                for (int e = 0; e < 16; ++e)
+                    o[16 * a + e] = fma2(o[16 * a + e], f2,
+                                         pair64(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])));
             }
-            if (!same) {
-#pragma unroll
-                for (int e = 0; e < D; ++e) o[e] *= f;
-            }
-            return true;
+            tc_fence_before();
         };
+#pragma unroll 1
         for (int t = pc.t0; t < pc.t1; ++t) {
             if (!(ok = wait(&sm.sfull[ns & 1], (ns >> 1) & 1, err))) break;
-            float f = 1.f, s[kN];
+            const uint32_t s_at = tmem + kColS + kN * (ns & 1);
+            ++ns;
+            const int tile = tile_of(pc, t);
+            const bool edge = at_edge(tile);
+            // scores 32a .. 32a + 31 of the row, with the sign of the scale, -inf where they are masked
+            auto scores = [&](int a, uint32_t (&x)[32]) {
+                tmem_ld_32x32b_x32(s_at + 32 * a, x);
+                tmem_ld_wait(x);
+                if (negative) {
+                    uint32_t sign = 0x80000000u;
+                    asm volatile("" : "+r"(sign));  // (kept behind the branch)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] ^= sign;
+                }
+                if (edge) {
+                    int hi = pos - tile * kN - 32 * a;  // last key seen
+                    asm volatile("" : "+r"(hi));
+                    const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0;
+                    const int sk = p.n_sink - tile * kN - 32 * a;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e > hi || (e < lo && e >= sk)) x[e] = 0xff800000u;
+                }
+            };
+            float rise = 1.f;
             if (busy) {
                 tc_fence_after();
-                {
+                float top = m;
+#pragma unroll 1
+                for (int a = 0; a < kN / 32; ++a) {
                     uint32_t x[32];
+                    scores(a, x);
+                    float other = -INFINITY;
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        tmem_ld_32x32b_x32(tmem + kColS + kN * (ns & 1) + 32 * a, x);
-                        tmem_ld_wait(x);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[32 * a + e] = __uint_as_float(x[e]);
+                    for (int e = 0; e < 32; e += 4) {
+                        top = max3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        other = max3(other, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
                     }
+                    top = fmaxf(top, other);
                 }
-                if (negative) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) s[e] = -s[e];
-                }
-                const int tile = tile_of(pc, t);
-                if (at_edge(tile)) {
-                    const int hi = pos - tile * kN;  // last key seen
-                    const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0;
-                    const int sk = p.n_sink - tile * kN;
-#pragma unroll
-                    for (int e = 0; e < kN; ++e)
-                        if (e > hi || (e < lo && e >= sk)) s[e] = -INFINITY;
-                }
-                float top = fmaxf(m, s[0]);
-#pragma unroll
-                for (int e = 1; e < kN - 1; e += 2) top = max3(top, s[e], s[e + 1]);
-                top = fmaxf(top, s[kN - 1]);
                 if (top > m) {
-                    f = fast_exp2((m - top) * c);  // (m = -inf: 0)
+                    rise = fast_exp2((m - top) * c);  // (m = -inf: 0)
                     m = top;
-                    l *= f;
+                    l *= rise;
                 }
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    s[e] = fast_exp2(fmaf(s[e], c, -mc));
-                    sum[e % 4] += s[e];
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
-            ++ns;
-            if (t > pc.t0 && !(ok = add_tile(f))) break;  // (the weights before are read: P is free)
+            // (the weights before are read, and their outputs there: P is free)
+            if (t > pc.t0) {
+                if (!(ok = wait(&sm.ofull, no & 1, err))) break;
+                ++no;
+            }
             if (busy) {
+                const float mc = m == -INFINITY ? 0.f : -m * c;
+                const uint64_t c2 = pair64(c, c), mc2 = pair64(mc, mc);
+                uint64_t sum = 0;
+                tc_fence_after();
+#pragma unroll 1
+                for (int a = 0; a < kN / 32; ++a) {
+                    uint32_t x[32], y[3][16];
+                    scores(a, x);
 #pragma unroll
-                for (int a = 0; a < kN / 16; ++a) {
-                    uint32_t x[3][8];
+                    for (int e = 0; e < 16; ++e) {
+                        float w0, w1;
+                        unpair64(fma2(pair64(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, mc2),
+                                 w0, w1);
+                        w0 = fast_exp2(w0);
+                        w1 = fast_exp2(w1);
+                        sum = add2(sum, pair64(w0, w1));
+                        split2(w0, w1, y[0][e], y[1][e], y[2][e]);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        split2(s[16 * a + 2 * e], s[16 * a + 2 * e + 1], x[0][e], x[1][e], x[2][e]);
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) tmem_st_x8(tmem + kColP + b * (kN / 2) + 8 * a, x[b]);
+                    for (int b = 0; b < 3; ++b) tmem_st_x16(tmem + kColP + b * (kN / 2) + 16 * a, y[b]);
                 }
+                float s0, s1;
+                unpair64(sum, s0, s1);
+                l += s0 + s1;
                 tmem_st_wait();
                 tc_fence_before();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.pready);
+            // (the next tile's outputs go to the other place)
+            if (busy && t > pc.t0) add_tile();
+            f = rise;
         }
-        if (!ok || (pc.t1 > pc.t0 && !add_tile(1.f))) break;
-        tc_fence_before();
+        if (ok && pc.t1 > pc.t0) {
+            ok = wait(&sm.ofull, no & 1, err);
+            ++no;
+            if (ok && busy) add_tile();
+        }
+        if (!ok) break;
         // ---- the piece's end
-        const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
-        if (bad) {
-            const int seen = valid ? pos : -1;
-#pragma unroll
-            for (int e = 0; e < D; ++e) o[e] += cleared<D>(p, pc, seen, e);
-        }
         const int head = pc.h * p.G + head_r;
         const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
         const float top = m == -INFINITY ? -INFINITY : m * c;  // log2 units
-        if (valid && pc.slot < 0) {
-            float ref = top, sum = l, scale = 1.f;
-            if (p.sink_logit) {
-                const float sink = p.sink_logit[head] * kLog2e;
-                ref = fmaxf(top, sink);
-                scale = top == -INFINITY ? 1.f : fast_exp2(top - ref);
-                sum = sum * scale + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
+        if (valid) {
+            float scale = 1.f;
+            float* dst;
+            if (pc.slot < 0) {
+                float ref = top, sum = l;
+                if (p.sink_logit) {
+                    const float sink = p.sink_logit[head] * kLog2e;
+                    ref = fmaxf(top, sink);
+                    scale = top == -INFINITY ? 1.f : fast_exp2(top - ref);
+                    sum = sum * scale + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
+                }
+                scale = sum == 0.f ? 0.f : scale / sum;
+                if (p.lse_out)
+                    p.lse_out[row] = sum == 0.f ? -INFINITY
+                                                : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
+                dst = static_cast<float*>(p.out) + row * D;
+            } else {
+                const size_t at = static_cast<size_t>(pc.slot) * 2 * kM + r;
+                reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(top, l);
+                dst = p.part_o + at * D;
             }
-            scale = sum == 0.f ? 0.f : scale / sum;
-            if (p.lse_out)
-                p.lse_out[row] = sum == 0.f ? -INFINITY
-                                            : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D);
 #pragma unroll
-            for (int e = 0; e < D / 4; ++e)
-                dst[e] = make_float4(o[4 * e] * scale, o[4 * e + 1] * scale, o[4 * e + 2] * scale,
-                                     o[4 * e + 3] * scale);
-        } else if (valid) {
-            const size_t at = static_cast<size_t>(pc.slot) * 2 * kM + r;
-            reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(top, l);
-            float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
-#pragma unroll
-            for (int e = 0; e < D / 4; ++e)
-                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < D / 4; ++e) {
+                float4 y;
+                unpair64(o[2 * e], y.x, y.y);
+                unpair64(o[2 * e + 1], y.z, y.w);
+                reinterpret_cast<float4*>(dst)[e] = make_float4(y.x * scale, y.y * scale, y.z * scale, y.w * scale);
+            }
+            // values that were cleared are infinite or NaN, and so is what they make of a sum
+            if (*reinterpret_cast<volatile int*>(&sm.bad[i])) {
+#pragma unroll 1
+                for (int e = 0; e < D; ++e) dst[e] += cleared<D>(p, pc, pos, e);
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pempty[i]);
