@@ -16,7 +16,7 @@
 //   * eight warps read queries, keys and values, split them and write the parts to shared memory in the
 //     tensor core's layout; values that are not finite are cleared (their split is NaN), and the rows
 //     that see them get them back at the end;
-//   * one thread issues S = Q K^T (6 x D / 16 steps) and O = P V (6 x 4 steps): the scores of the next
+//   * a thread issues S = Q K^T (6 x D / 16 steps), another O = P V (6 x 4 steps): the scores of the next
 //     tile are under way while this tile's softmax runs;
 //   * four warps, a row a thread: running maximum and sum, weights split into three parts for tensor
 //     memory, outputs in registers.
@@ -34,7 +34,7 @@ using namespace prefill;
 constexpr int kN = 64;       // keys of a tile
 constexpr int kThreads = 512;
 constexpr int kSoftWarps = 4, kConvWarps = 8;
-constexpr int kWarpConv = 4, kWarpWalk = 12, kWarpMma = 13;
+constexpr int kWarpConv = 4, kWarpWalk = 12, kWarpQk = 13, kWarpPv = 14;
 // registers of a thread of the softmax's, the two converting and the last warpgroup, of 128 at launch
 constexpr int kRegsSoft = 232, kRegsConv = 104, kRegsOther = 72;
 static_assert(kRegsSoft + 2 * kRegsConv + kRegsOther <= 4 * 128, "registers");
@@ -45,8 +45,8 @@ struct Smem {
     uint8_t q[3][kM * D * 2];  // offset 0; every part is a multiple of 1024 bytes
     uint8_t k[3][kN * D * 2];
     uint8_t v[3][kN * D * 2];
-    uint64_t qfull, qempty, kfull, kempty, vfull, vempty, sfull[2], pready, ofull;
-    uint64_t pfull[kPieces], pempty[kPieces], end;
+    uint64_t qfull, qempty, kfull, kempty, vfull, vempty, sfull[2], pready[2], ofull;
+    uint64_t pfull[kPieces], pempty[kPieces], end[2];
     Piece piece[kPieces];
     int bad[kPieces];  // a value was not finite
     uint32_t tmem_base;
@@ -188,62 +188,91 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
 }
 
 // ---------------------------------------------------------------------------------- products
+// Scores and outputs are issued by a thread each, so that the tensor core has the one's products while
+// the other waits or commits (in one thread: 118 us for the ragged chunks, against XXX).
 template <int D>
-__device__ void mma_role(const PrefillParams& p, Smem<D>& sm) {
-    constexpr uint32_t id_qk = idesc_bf16_f32(kM, kN, 0, 0), id_pv = idesc_bf16_f32(kM, D, 0, 1);
-    const uint32_t tmem = sm.tmem_base;
+__device__ void qk_role(const PrefillParams& p, Smem<D>& sm, int lane) {
+    constexpr uint32_t id = idesc_bf16_f32(kM, kN, 0, 0);
     const uint64_t q = sw128_kmajor_desc(smem_u32(sm.q[0])), kk = sw128_kmajor_desc(smem_u32(sm.k[0]));
-    const uint64_t v = sw128_mnmajor_desc(smem_u32(sm.v[0]), kN * 128);
     int* err = p.err;
-    uint32_t nq = 0, nk = 0, np = 0;  // query tiles, key tiles, value tiles taken
+    const bool one = lane == 0;
+    uint32_t nq = 0, nk = 0;  // query tiles, key tiles taken
     bool ok = true;
-    auto qk = [&](bool last) {
-        if (!wait(&sm.kfull, nk & 1, err)) return false;
-        tc_fence_after();
-        const uint32_t s = tmem + kColS + kN * (nk & 1);
-#pragma unroll 1
-        for (int i = 0; i < 6; ++i) {
-            const uint64_t a = q + ((left_part(i) * kM * D * 2) >> 4);
-            const uint64_t b = kk + ((right_part(i) * kN * D * 2) >> 4);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                tc_mma_bf16(s, a + (((ks >> 2) * kM * 128 + (ks & 3) * 32) >> 4),
-                            b + (((ks >> 2) * kN * 128 + (ks & 3) * 32) >> 4), id_qk, i + ks > 0 ? 1u : 0u);
-        }
-        tc_commit(&sm.sfull[nk & 1]);
-        tc_commit(&sm.kempty);
-        if (last) tc_commit(&sm.qempty);
-        ++nk;
-        return true;
-    };
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
         if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
         const int t0 = sm.piece[i].t0, nt = sm.piece[i].t1 - t0;
-        mbar_arrive(&sm.pempty[i]);
+        __syncwarp();
+        if (one) mbar_arrive(&sm.pempty[i]);
         if (t0 < 0) break;
         if (nt == 0) continue;
-        if (!(ok = wait(&sm.qfull, nq++ & 1, err) && qk(nt == 1))) break;
-        for (int t = 0; t < nt; ++t) {
-            if (t + 1 < nt && !(ok = qk(t + 2 == nt))) break;
-            if (!(ok = wait(&sm.vfull, np & 1, err) && wait(&sm.pready, np & 1, err))) break;
-            const uint32_t o = tmem + kColO + 128 * (np & 1);
-            ++np;
+        if (!(ok = wait(&sm.qfull, nq++ & 1, err))) break;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t, ++nk) {
+            // (the scores two tiles ago have been read)
+            if (!(ok = wait(&sm.pready[nk & 1], ((nk >> 1) & 1) ^ 1, err) && wait(&sm.kfull, nk & 1, err))) break;
             tc_fence_after();
+            const uint32_t s = sm.tmem_base + kColS + kN * (nk & 1);
 #pragma unroll 1
             for (int j = 0; j < 6; ++j) {
-                const uint32_t a = tmem + kColP + left_part(j) * (kN / 2);
-                const uint64_t b = v + ((right_part(j) * kN * D * 2) >> 4);
+                const uint64_t a = q + ((left_part(j) * kM * D * 2) >> 4);
+                const uint64_t b = kk + ((right_part(j) * kN * D * 2) >> 4);
+                if (one) {
 #pragma unroll
-                for (int ks = 0; ks < kN / 16; ++ks)
-                    tc_mma_bf16_ts(o, a + ks * 8, b + ((ks * 16 * 128) >> 4), id_pv, j + ks > 0 ? 1u : 0u);
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma_bf16(s, a + (((ks >> 2) * kM * 128 + (ks & 3) * 32) >> 4),
+                                b + (((ks >> 2) * kN * 128 + (ks & 3) * 32) >> 4), id, j + ks > 0 ? 1u : 0u);
+                }
             }
-            tc_commit(&sm.ofull);
-            tc_commit(&sm.vempty);
+            if (one) {
+                tc_commit(&sm.sfull[nk & 1]);
+                tc_commit(&sm.kempty);
+            }
+        }
+        if (ok && one) tc_commit(&sm.qempty);
+    }
+    if (one) tc_commit(&sm.end[0]);  // all products complete before tensor memory is released
+    wait(&sm.end[0], 0, err);
+}
+
+template <int D>
+__device__ void pv_role(const PrefillParams& p, Smem<D>& sm, int lane) {
+    constexpr uint32_t id = idesc_bf16_f32(kM, D, 0, 1);
+    const uint64_t v = sw128_mnmajor_desc(smem_u32(sm.v[0]), kN * 128);
+    int* err = p.err;
+    const bool one = lane == 0;
+    uint32_t np = 0;  // value tiles taken
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const int i = k % kPieces;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        const int t0 = sm.piece[i].t0, nt = sm.piece[i].t1 - t0;
+        __syncwarp();
+        if (one) mbar_arrive(&sm.pempty[i]);
+        if (t0 < 0) break;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t, ++np) {
+            if (!(ok = wait(&sm.vfull, np & 1, err) && wait(&sm.pready[np & 1], (np >> 1) & 1, err))) break;
+            tc_fence_after();
+            const uint32_t o = sm.tmem_base + kColO + 128 * (np & 1);
+#pragma unroll 1
+            for (int j = 0; j < 6; ++j) {
+                const uint32_t a = sm.tmem_base + kColP + left_part(j) * (kN / 2);
+                const uint64_t b = v + ((right_part(j) * kN * D * 2) >> 4);
+                if (one) {
+#pragma unroll
+                    for (int ks = 0; ks < kN / 16; ++ks)
+                        tc_mma_bf16_ts(o, a + ks * 8, b + ((ks * 16 * 128) >> 4), id, j + ks > 0 ? 1u : 0u);
+                }
+            }
+            if (one) {
+                tc_commit(&sm.ofull);
+                tc_commit(&sm.vempty);
+            }
         }
     }
-    tc_commit(&sm.end);  // all products complete before tensor memory is released
-    wait(&sm.end, 0, err);
+    if (one) tc_commit(&sm.end[1]);
+    wait(&sm.end[1], 0, err);
 }
 
 // ----------------------------------------------------------------------------------- softmax
@@ -268,6 +297,10 @@ __device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, i
         }
     }
     return sum;
+}
+
+__device__ __forceinline__ uint64_t first_bits(int n) {
+    return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
 template <int D>
@@ -317,9 +350,16 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         for (int t = pc.t0; t < pc.t1; ++t) {
             if (!(ok = wait(&sm.sfull[ns & 1], (ns >> 1) & 1, err))) break;
             const uint32_t s_at = tmem + kColS + kN * (ns & 1);
-            ++ns;
             const int tile = tile_of(pc, t);
             const bool edge = at_edge(tile);
+            // the keys seen, a bit each: up to the row's own, in its window or a sink
+            uint32_t seen_lo = 0, seen_hi = 0;
+            if (edge) {
+                const int hi = pos - tile * kN, lo = p.window > 0 && valid ? hi - p.window + 1 : 0;
+                const uint64_t seen = first_bits(hi + 1) & (~first_bits(lo) | first_bits(p.n_sink - tile * kN));
+                seen_lo = static_cast<uint32_t>(seen);
+                seen_hi = static_cast<uint32_t>(seen >> 32);
+            }
             // scores 32a .. 32a + 31 of the row, with the sign of the scale, -inf where they are masked
             auto scores = [&](int a, uint32_t (&x)[32]) {
                 tmem_ld_32x32b_x32(s_at + 32 * a, x);
@@ -331,13 +371,11 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                     for (int e = 0; e < 32; ++e) x[e] ^= sign;
                 }
                 if (edge) {
-                    int hi = pos - tile * kN - 32 * a;  // last key seen
-                    asm volatile("" : "+r"(hi));
-                    const int lo = p.window > 0 && valid ? hi - p.window + 1 : 0;
-                    const int sk = p.n_sink - tile * kN - 32 * a;
+                    uint32_t word = a ? seen_hi : seen_lo;
+                    asm volatile("" : "+r"(word));
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (e > hi || (e < lo && e >= sk)) x[e] = 0xff800000u;
+                        if (!(word >> e & 1)) x[e] = 0xff800000u;
                 }
             };
             float rise = 1.f;
@@ -396,7 +434,8 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.pready);
+            if (lane == 0) mbar_arrive(&sm.pready[ns & 1]);
+            ++ns;
             // (the next tile's outputs go to the other place)
             if (busy && t > pc.t0) add_tile();
             f = rise;
@@ -472,16 +511,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const PrefillP
         mbar_init(&sm.vempty, 1);
         mbar_init(&sm.sfull[0], 1);
         mbar_init(&sm.sfull[1], 1);
-        mbar_init(&sm.pready, kSoftWarps);
+        mbar_init(&sm.pready[0], kSoftWarps);
+        mbar_init(&sm.pready[1], kSoftWarps);
         mbar_init(&sm.ofull, 1);
-        mbar_init(&sm.end, 1);
+        mbar_init(&sm.end[0], 1);
+        mbar_init(&sm.end[1], 1);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.pfull[i], 1);
-            mbar_init(&sm.pempty[i], 1 + kSoftWarps + kConvWarps);
+            mbar_init(&sm.pempty[i], 2 + kSoftWarps + kConvWarps);
         }
         fence_mbar_init();
     }
-    if (warp == kWarpMma) tmem_alloc(&sm.tmem_base, 512);
+    if (warp == kWarpQk) tmem_alloc(&sm.tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -519,15 +560,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const PrefillP
                 last.t1 = 0;
                 publish(last);
             }
-        } else if (warp == kWarpMma && lane == 0) {
-            mma_role<D>(p, sm);
+        } else if (warp == kWarpQk) {
+            qk_role<D>(p, sm, lane);
+        } else if (warp == kWarpPv) {
+            pv_role<D>(p, sm, lane);
         }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWarpMma) tmem_dealloc(sm.tmem_base, 512);
+    if (warp == kWarpQk) tmem_dealloc(sm.tmem_base, 512);
 }
 
 template <int D>
