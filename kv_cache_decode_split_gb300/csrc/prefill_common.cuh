@@ -32,29 +32,24 @@ struct Seq {
     int c0, n, L, k0;
 };
 
-// Sequence b; n = 0 where its offsets are bad. (b < B)
+// Sequence b; n = 0 where its offsets are bad. (b < B; every load is under way before the first is used)
 static __device__ __noinline__ Seq load_seq(const PrefillParams& p, int b, int* err) {
+    const bool paged = p.block_table != nullptr;
+    const int32_t* keys = paged ? p.seq_lens : p.cu_k;
     Seq s;
-    int c1;
-    if (p.cu_q) {
-        s.c0 = p.cu_q[b];
-        c1 = p.cu_q[b + 1];
-    } else {
-        s.c0 = b;
-        c1 = b + 1;
-    }
+    s.c0 = p.cu_q ? p.cu_q[b] : b;
+    const int c1 = p.cu_q ? p.cu_q[b + 1] : b + 1;
+    const int a = keys[b], k1 = keys[paged ? b : b + 1];
     bool bad = s.c0 < 0 || c1 < s.c0 || c1 > p.T || (b == 0 && s.c0 != 0);
     s.n = bad ? 0 : c1 - s.c0;
-    if (p.block_table) {
-        const int len = p.seq_lens[b];
-        s.L = min(max(len, 0), p.max_pages << p.page_shift);
+    if (paged) {
+        s.L = min(max(a, 0), p.max_pages << p.page_shift);
         s.k0 = b;
-        bad |= len != s.L || s.L < s.n;
+        bad |= a != s.L || s.L < s.n;
     } else {
-        s.k0 = p.cu_k[b];
-        const int k1 = p.cu_k[b + 1];
-        s.L = k1 - s.k0;
-        if (s.k0 < 0 || k1 < s.k0 || k1 > p.Tk || (b == 0 && s.k0 != 0)) {
+        s.k0 = a;
+        s.L = k1 - a;
+        if (a < 0 || k1 < a || k1 > p.Tk || (b == 0 && a != 0)) {
             bad = true;
             s.n = 0;
         }
@@ -230,17 +225,23 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
     const int cta = blockIdx.x, n_cta = p.n_cta;
     if (lane == 0) p.head[cta].nt = 0;
     // how long the list is
+    Seq mine{};             // of 32 sequences, one a lane
+    long long my_head = 0;  // its length in the list, per head
+    int my_units = 0;       // its units per head
+    auto load_mine = [&](int b, int* err) {
+        mine = b < p.B ? load_seq(p, b, err) : Seq{};
+        my_units = (mine.n + U - 1) / U;
+    };
     long long V = 0, units = 0, longest = 0;
 #pragma unroll 1
     for (int b = lane; b < p.B; b += 32) {
-        const Seq s = load_seq(p, b, cta == 0 ? p.err : nullptr);
-        if (s.n == 0) continue;
-        const int nm = (s.n + U - 1) / U;
-        const Weigh w(p, s, U, false);
-        const long long all = w.upto(nm);
-        V += all * p.Hkv;
-        units += static_cast<long long>(nm) * p.Hkv;
-        longest = max(longest, all - w.upto(nm - 1));
+        load_mine(b, cta == 0 ? p.err : nullptr);
+        if (mine.n == 0) continue;
+        const Weigh w(p, mine, U, false);
+        my_head = w.upto(my_units);
+        V += my_head * p.Hkv;
+        units += static_cast<long long>(my_units) * p.Hkv;
+        longest = max(longest, my_head - w.upto(my_units - 1));
     }
 #pragma unroll 1
     for (int off = 16; off; off >>= 1) {
@@ -258,14 +259,13 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
     // the sequence that position x0 falls in
     int b0 = 0;        // 32 sequences, one a lane
     long long at = 0;  // position of the first of them
-    Seq mine;
-    long long my_len = 0;
     auto load_batch = [&]() {
-        const int b = b0 + lane;
-        mine.n = mine.c0 = mine.L = mine.k0 = 0;
-        if (b < p.B) mine = load_seq(p, b, nullptr);
-        my_len = 0;
-        if (mine.n > 0) my_len = Weigh(p, mine, U, flat).upto((mine.n + U - 1) / U) * p.Hkv;
+        if (p.B > 32) {  // (up to 32 sequences are with their lanes)
+            load_mine(b0 + lane, nullptr);
+            my_head = Weigh(p, mine, U, flat).upto(my_units);
+        } else if (flat) {
+            my_head = my_units;
+        }
     };
     int j = 32;
     if (x0 >= x1) return;
@@ -277,6 +277,7 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
             load_batch();
             j = 0;
             if (first_seq) {
+                const long long my_len = my_head * p.Hkv;
                 long long incl = my_len;
 #pragma unroll 1
                 for (int off = 1; off < 32; off <<= 1) {
@@ -302,7 +303,7 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
         if (s.n > 0) {
             const int nm = (s.n + U - 1) / U;
             const Weigh wt(p, s, U, flat);
-            const long long per_head = wt.upto(nm);
+            const long long per_head = __shfl_sync(0xffffffffu, my_head, j);
             int h = 0, m = 0;
             long long u = at;  // position of the unit
             if (first_seq) {
@@ -351,7 +352,7 @@ __device__ __forceinline__ void walk(const PrefillParams& p, int U, int TM, int 
             }
         }
         first_seq = false;
-        at += __shfl_sync(0xffffffffu, my_len, j);
+        at += __shfl_sync(0xffffffffu, my_head, j) * p.Hkv;
         if (++j == 32) b0 += 32;
     }
 }
