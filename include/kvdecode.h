@@ -362,11 +362,15 @@ int attn_decode_gqa_q4(const void *q, const void *k_pool, const void *v_pool,
  *          count), 16-byte aligned, of any content: nothing is kept in it from call to call. Calls
  *          that share it must be ordered on the device.
  *  err     int32 on the device, nullable, never cleared: receives KVD_ERR_DEVICE_OOB for offsets that
- *          do not ascend or leave T or Tk (nothing of such a sequence is written)
+ *          do not ascend or leave T or Tk (nothing of such a sequence is written; rows of sequences
+ *          that overlap for that reason are undefined)
  * Scores, softmax statistics and sums are held in float32; with bfloat16 inputs the weights of the
  * value product are bfloat16 numbers (8 bits, as its operands must be of one type), their sum is not
- * rounded. A value that is NaN or infinite reaches the rows that see it alone. The result does not
- * depend on timing.
+ * rounded. A key or value that is NaN or infinite reaches the rows that see it alone. Float32 operands
+ * are taken apart into three bfloat16 numbers: a magnitude above 3.389e38 counts as infinite, and an
+ * infinite key or query makes the scores of its products NaN. The result does not depend on timing.
+ * One launch or, where a long sequence's work is divided, two. A kernel whose waits run out (which a
+ * fault of the device would have to cause) records KVD_ERR_TIMEOUT in err and leaves out undefined.
  * Supported: D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, dtype KVD_BF16 or KVD_F32; T == 0 does
  * nothing.
  */

@@ -10,24 +10,36 @@
 // sequence and KV head: every key and value tile is read once for 256 rows.
 //
 // One persistent CTA an SM, roles by warp:
-//   * loads: query tiles and a ring of 128-token key and value tiles, all by TMA;
-//   * products: S = Q K^T (tcgen05, 128 x 128, operands in shared memory) and O += P V (P in tensor
-//     memory, where it takes the place of its S), issued by one thread for each stream;
-//   * softmax: two warpgroups, one row a thread, each with a score tile and an output accumulator of
-//     its own in tensor memory, so that one's exponentials run under the other's products. The row's
-//     reference maximum is only raised, and O rescaled, when a maximum grows by more than 2^8;
+//   * loads: query tiles and rings of 128-token key and value tiles, all by TMA;
+//   * products: S = Q K^T (tcgen05, 128 x 64, operands in shared memory) and O += P V (P in tensor memory,
+//     where it takes the place of its S), each of the two streams' by a warp of its own;
+//   * softmax: two warpgroups, one row a thread, each with two score buffers of 64 keys and an output
+//     accumulator of its own in tensor memory, so that one's exponentials run under the other's products.
+//     The row's reference maximum is only raised, and O rescaled, when a maximum grows by more than 2^8;
 //     weights are then at most 2^8 and are rounded to bfloat16 (the value product's operands have one
 //     type), their sums are float32 sums of the unrounded weights.
-//   * values: at the edges of the mask a warp clears the value rows behind the sequence's end and
+//   * values: at the edges of the mask three warps clear the value rows behind the sequence's end and
 //     every value that is not finite, before a zero weight can meet them; the rows that see such a
 //     value get it back at the end.
-// A unit of at most 128 rows (draft tokens, a prompt's end) is one query tile: the two warpgroups then
+//   * a unit's end: a warpgroup divides and writes the outputs while the softmax goes on with the next unit.
+// A unit of at most 128 rows (draft tokens, a prompt's end) is one query tile: the two streams then
 // take its key tiles in turn, and their accumulators are merged.
 //
 // Work is cut as a list: all units one behind the other, each as long as the keys that it walks and a
 // fixed part for its start and end, in equal ranges, one for each CTA. A unit that a cut divides is
 // left as partial results of its pieces, which a second launch merges by log-sum-exp (in the order of
 // the pieces: the result does not depend on timing).
+//
+// Bound, in long units, by the softmax's instructions next to the products: a 128 x 128 tile is 512 cycles of
+// QK (768 in the halves of 64 keys that let the exponentials start early; it is shared memory's rate then),
+// 512 of PV and 512 of exponentials, two tiles at a time. 16385 tokens of 32/8 heads of 128 take 1.60 ms,
+// 1.38 PFLOP/s (72 % of what a library matrix product reaches); 2048-token chunks behind 28 thousand 1.34 to
+// 1.48. Short units are bound by their ends: the next unit's queries take the last one's place, so that 1500
+// to 3000 cycles pass without products, and code that a unit runs once is not in the instruction caches
+// (nine prompts of 61 to 3581 tokens: 404 us, 0.84 PFLOP/s). Loading the next unit's first keys ahead of its
+// queries did not help (420 us). A call of one short unit an SM (513 tokens: 18.3 us) is a chain: 5 us to
+// the first load (lengths, then the CTA's range), 3 to the first scores, 2 a tile, 3 for the end.
+// Draft tokens (32 sequences, 1 to 8 tokens behind 4096 to 8184) read the cache at 5.5 TB/s: 146 us.
 
 #include <algorithm>
 
@@ -857,7 +869,7 @@ int launch(PrefillParams p, void* ws, cudaStream_t stream) {
     // A unit's start and end count as 320 keys (nine prompts of 61 to 3581 tokens, 32/8 heads of 128: 490 us
     // with 0, 411 with 192, 402 with 320, 396 with 512, 399 with 768; one of 16385: 1.63 ms, 1.53, 1.53, 1.55,
     // 1.57). A call of fewer units than SMs is left uncut if that makes its longest range at most 8 tiles
-    // longer (5 draft tokens behind 4091: 19.8 us; with 24 tiles 22.4).
+    // longer (5 draft tokens behind 1024: 19.8 us; with 24 tiles 22.4).
     set_plan(p, D, ws, 320, 8 * kN);
     if (launch_kernel(kernel, dim3(static_cast<unsigned>(p.n_cta)), dim3(kThreads), smem, stream, tq, tk,
                       tv, p) != cudaSuccess ||

@@ -5,21 +5,28 @@
 // exponents), x = x1 + x2 + x3, each the rounding of what the ones before it leave. Of the nine products
 // of two such sums the six of at least 2^-16 are kept, x1 y1 + x1 y2 + x2 y1 + x2 y2 + x1 y3 + x3 y1; the
 // three left out are below 2^-24 of |x||y| each. (Three products of two tf32 numbers cost as much time
-// at half the rate, and a third more shared memory. CUDA cores took 78 ms for 16385 tokens of 32 heads of
-// 128 in bfloat16, and 3.9 ms for the ragged float32 chunks that take less than 0.2 here.)
+// at half the rate, and a third more shared memory. On CUDA cores the chunks below took 3.9 ms.)
 // The smallest products are added first. A tensor core cuts what it adds, so the weighted sums of one
 // 64-key tile at most are left to it: every tile's outputs start from zero and are added to float32
 // registers, rounded.
+//
+// Bound by shared memory: the score product reads 6 KB for 128 x 64 x 16, and the parts of keys and values
+// are written once and read by three products each, 4400 of the 6600 cycles of a tile of D = 128; the rest
+// is waiting for the converting warps, which have one buffer (192 KB hold no second). Six chunks of 1 to 301
+// tokens behind 400 to 5003, 14/2 heads of 128, take 115 us, 98 TFLOP/s of the formula's operations, which
+// are a sixth of those issued; the windowed prompts below 117 us.
 //
 // One persistent CTA an SM takes units of one query tile (128 rows: the G query heads of a KV head of
 // 128 / G tokens) from the list of prefill_common.cuh. Roles:
 //   * eight warps read queries, keys and values, split them and write the parts to shared memory in the
 //     tensor core's layout; values that are not finite are cleared (their split is NaN), and the rows
 //     that see them get them back at the end;
-//   * a thread issues S = Q K^T (6 x D / 16 steps), another O = P V (6 x 4 steps): the scores of the next
+//   * a warp issues S = Q K^T (6 x D / 16 steps), another O = P V (6 x 4 steps): the scores of the next
 //     tile are under way while this tile's softmax runs;
 //   * four warps, a row a thread: running maximum and sum, weights split into three parts for tensor
-//     memory, outputs in registers.
+//     memory, outputs in registers. They read the scores twice, 32 at a time, in rolled loops (with a row's
+//     64 in registers and all loops unrolled the kernel was 145 KB of code, now 90, and the chunks took
+//     169 us), and add a tile's outputs behind the next tile's weights.
 
 #include <algorithm>
 
@@ -82,14 +89,18 @@ __device__ __forceinline__ void put_split(uint8_t* base, int part, int rows, int
     *reinterpret_cast<uint4*>(at + 2 * part) = c;
 }
 
-__device__ __forceinline__ bool finite4(const float4& v) {
-    return isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
+// Numbers whose first part is finite. (What rounds to a bfloat16 infinity counts as infinite.)
+__device__ __forceinline__ bool splits(float x) {
+    return (__float_as_uint(x) & 0x7fffffffu) < 0x7f7f8000u;
+}
+__device__ __forceinline__ bool splits4(const float4& v) {
+    return splits(v.x) && splits(v.y) && splits(v.z) && splits(v.w);
 }
 __device__ __forceinline__ void clear4(float4& v) {
-    v.x = isfinite(v.x) ? v.x : 0.f;
-    v.y = isfinite(v.y) ? v.y : 0.f;
-    v.z = isfinite(v.z) ? v.z : 0.f;
-    v.w = isfinite(v.w) ? v.w : 0.f;
+    v.x = splits(v.x) ? v.x : 0.f;
+    v.y = splits(v.y) ? v.y : 0.f;
+    v.z = splits(v.z) ? v.z : 0.f;
+    v.w = splits(v.w) ? v.w : 0.f;
 }
 
 // A unit's items of 64 rows: the queries (two), then keys and values, K(0), K(1), V(0), K(2), V(1), ...
@@ -165,7 +176,7 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
                 bool bad = false;
 #pragma unroll
                 for (int e = 0; e < kEach; ++e)
-                    if (!(finite4(rows.x[e][0]) && finite4(rows.x[e][1]))) {
+                    if (!(splits4(rows.x[e][0]) && splits4(rows.x[e][1]))) {
                         clear4(rows.x[e][0]);
                         clear4(rows.x[e][1]);
                         bad = true;
@@ -188,8 +199,10 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
 }
 
 // ---------------------------------------------------------------------------------- products
-// Scores and outputs are issued by a thread each, so that the tensor core has the one's products while
-// the other waits or commits (in one thread: 118 us for the ragged chunks, against XXX).
+// Scores and outputs are issued by a warp each, so that the tensor core has the one's products while the
+// other waits or commits; all lanes take the loops, so that descriptors are in uniform registers, which a
+// product's instruction reads. (Five windowed prompts of 33 to 1500 tokens, 16/4 heads of 64: 117 us; one
+// thread for both, in code of its own: 142; two: 134.)
 template <int D>
 __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, int lane) {
     constexpr uint32_t id = idesc_bf16_f32(kM, kN, 0, 0);
@@ -276,7 +289,8 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, int lane) {
 }
 
 // ----------------------------------------------------------------------------------- softmax
-// What a row gets back, in one column, of the values that were cleared: v itself, where the row sees it.
+// What a row gets back, in one column, of the values that were cleared: NaN, or infinities, where the row
+// sees them.
 template <int D>
 __device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, int pos, int col) {
     float sum = 0.f;
@@ -293,7 +307,7 @@ __device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, i
             } else {
                 v += (pc.k0 + key) * p.v_stride + pc.h * D;
             }
-            if (!isfinite(v[col])) sum += v[col];
+            if (!splits(v[col])) sum += v[col] * INFINITY;
         }
     }
     return sum;

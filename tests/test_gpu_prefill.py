@@ -383,3 +383,32 @@ def test_append_then_attend_and_read_back(kvd):
     c = Case(new, rows, Hq, Hkv, D, BF, window=W, n_sink=ns)
     c.q, c.k, c.v = qs[1], list(k.split(rows)), list(v.split(rows))
     c.check(*c.call(kvd.attn_prefill_gqa, (qs[1], k, v, cu(new), cu(rows))))
+
+
+def test_float32_values_beyond_bfloat16_count_as_infinite(kvd):
+    """3.4e38 is a float32 number that rounds to a bfloat16 infinity: infinite for the rows that see it,
+    nothing for the others, also those of the same tile."""
+    c = Case([150, 40], [150, 300], 4, 2, 64, F32, seed=30)
+    ref, _ = c.packed(kvd)
+    c.v[0][100, 0, 3], c.v[0][90, 1, 5], c.v[1][270, 0, 60] = 3.4e38, 3.38e38, -3.4e38
+    for out in (c.packed(kvd)[0], c.paged(kvd, 16)[0]):
+        assert (out[100:150, :2, 3] == math.inf).all() and (out[150 + 10:, :2, 60] == -math.inf).all()
+        same = torch.ones_like(ref, dtype=torch.bool)
+        same[100:150, :2, 3] = same[160:, :2, 60] = same[90:150, 2:, 5] = False
+        assert torch.equal(out[same], ref[same])
+        assert torch.isfinite(out[90:150, 2:, 5]).all()  # 3.38e38 is a number like others
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 4), (128, 32, 8)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_outputs_that_begin_at_16_bytes(kvd, dtype, D, Hq, Hkv):
+    c = Case([1, 130, 5], [900, 130, 260], Hq, Hkv, D, dtype, seed=31)
+    step = 16 // c.q.element_size()
+    room = torch.full((c.q.numel() + 2 * step,), 77.0, dtype=dtype, device=DEV)
+    out = room[step:-step].view(c.q.shape)
+    assert out.data_ptr() % 32 == 16
+    for f in (lambda **kw: c.packed(kvd, **kw), lambda **kw: c.paged(kvd, 64, **kw)):
+        want, _ = f()
+        f(out=out)
+        assert torch.equal(out, want)
+        assert (room[:step] == 77).all() and (room[-step:] == 77).all()
