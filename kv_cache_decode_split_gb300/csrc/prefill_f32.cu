@@ -10,11 +10,12 @@
 // 64-key tile at most are left to it: every tile's outputs start from zero and are added to float32
 // registers, rounded.
 //
-// Bound by shared memory: the score product reads 6 KB for 128 x 64 x 16, and the parts of keys and values
-// are written once and read by three products each, 4400 of the 6600 cycles of a tile of D = 128; the rest
-// is waiting for the converting warps, which have one buffer (192 KB hold no second). Six chunks of 1 to 301
-// tokens behind 400 to 5003, 14/2 heads of 128, take 115 us, 98 TFLOP/s of the formula's operations, which
-// are a sixth of those issued; the windowed prompts below 117 us.
+// Bound by the converting warps: 500 instructions for 64 rows, two such items a tile, and one buffer for
+// each (192 KB hold no second), so that a tile of D = 128 takes 6600 cycles where the products take 3800
+// and shared memory, which the score product's operands fill (6 KB for 128 x 64 x 16), 4400. Six chunks of
+// 1 to 301 tokens behind 400 to 5003, 14/2 heads of 128: 115 us, 98 TFLOP/s of the formula's operations,
+// a sixth of those issued; the windowed prompts below 116 us. (Pages looked up two items ahead, or 32-byte
+// loads, change nothing: 117 us each.)
 //
 // One persistent CTA an SM takes units of one query tile (128 rows: the G query heads of a KV head of
 // 128 / G tokens) from the list of prefill_common.cuh. Roles:
@@ -202,7 +203,7 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
 // Scores and outputs are issued by a warp each, so that the tensor core has the one's products while the
 // other waits or commits; all lanes take the loops, so that descriptors are in uniform registers, which a
 // product's instruction reads. (Five windowed prompts of 33 to 1500 tokens, 16/4 heads of 64: 117 us; one
-// thread for both, in code of its own: 142; two: 134.)
+// thread for both: 142; two threads: 134.)
 template <int D>
 __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, int lane) {
     constexpr uint32_t id = idesc_bf16_f32(kM, kN, 0, 0);
