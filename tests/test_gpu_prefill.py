@@ -412,3 +412,54 @@ def test_outputs_that_begin_at_16_bytes(kvd, dtype, D, Hq, Hkv):
         f(out=out)
         assert torch.equal(out, want)
         assert (room[:step] == 77).all() and (room[-step:] == 77).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_replayed_graph_follows_its_lengths(kvd, dtype):
+    """Captured with short caches (no unit would be cut), replayed with long ones, other offsets and
+    empty sequences, and back."""
+    c = Case([5, 0, 40], [4000, 300, 2500], 8, 2, 128, dtype, seed=40)
+    kp, vp, bt, _ = c.pools(64)
+    sl, at = torch.zeros(3, dtype=I32, device=DEV), torch.zeros(4, dtype=I32, device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    ws = torch.empty(kvd.kvd_workspace_size("prefill", 3, 8, 2, 128), dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(c.q), torch.empty(45, 8, device=DEV)
+
+    def call(**kw):
+        kvd.attn_prefill_gqa_paged(c.q, kp, vp, bt, sl, at, out=out, lse_out=lse, workspace=ws, err=err, **kw)
+
+    def lengths(new, lens):
+        sl.copy_(torch.tensor(lens, dtype=I32))
+        at.copy_(cu(new))
+
+    short, long_, other = ([5, 0, 40], [9, 0, 41]), ([5, 0, 40], [4000, 300, 2500]), ([1, 44, 0], [1, 290, 7])
+    lengths(*short)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for new, lens in (short, long_, other, short, long_):
+        lengths(new, lens)
+        out.fill_(77)
+        graph.replay()
+        got, got_lse = out.clone(), lse.clone()
+        out.fill_(77)
+        call()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        assert torch.equal(got, out) and torch.equal(got_lse, lse)
+        cut = Case.__new__(Case)
+        cut.__dict__.update(c.__dict__)
+        cut.new, cut.lens = new, lens
+        cut.k, cut.v = [k[:n] for k, n in zip(c.k, lens)], [v[:n] for v, n in zip(c.v, lens)]
+        cut.check(got, got_lse, f"{lens}")
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scales(kvd, dtype, scale):
+    check(kvd, Case([1, 70, 200], [300, 70, 333], 6, 2, 64, dtype, scale=scale, window=90, n_sink=3, seed=41), 32)
