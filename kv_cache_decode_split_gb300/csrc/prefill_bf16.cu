@@ -30,7 +30,8 @@
 // left as partial results of its pieces, which a second launch merges by log-sum-exp (in the order of
 // the pieces: the result does not depend on timing).
 //
-// Bound, in long units, by the softmax's instructions next to the products: a 128 x 128 tile is 512 cycles of
+// Bound, in long units, by the softmax's chain (some 1400 cycles for 64 keys, two such warps a scheduler, issue
+// slots busy 44 %) next to the products, whose pipe is busy 72 %: a 128 x 128 tile is 512 cycles of
 // QK (768 in the halves of 64 keys that let the exponentials start early; it is shared memory's rate then),
 // 512 of PV and 512 of exponentials, two tiles at a time. 16385 tokens of 32/8 heads of 128 take 1.60 ms,
 // 1.38 PFLOP/s (72 % of what a library matrix product reaches); 2048-token chunks behind 28 thousand 1.34 to
