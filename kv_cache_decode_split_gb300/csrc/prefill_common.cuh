@@ -116,6 +116,118 @@ struct Edge {
 __device__ __forceinline__ int tile_of(const Piece& u, int t) {
     return t < u.nA ? t : u.tB + (t - u.nA);
 }
+
+// Values that are not finite are cleared in shared memory (a masked key's weight of zero would make NaN of
+// them) and put back into the outputs of the rows that see them. Each piece has a word that says where: a
+// bit for 1 << odd_shift() of its tiles.
+__device__ __forceinline__ int odd_shift(const Piece& u) {
+    return max(0, 27 - __clz(u.t1 - u.t0 - 1));
+}
+
+// Numbers of which the products' operands are made. (A float32 number goes in three bfloat16 parts, so what
+// rounds to a bfloat16 infinity counts as infinite.)
+__device__ __forceinline__ bool splits(float x) {
+    return (__float_as_uint(x) & 0x7fffffffu) < 0x7f7f8000u;
+}
+
+// A lane's D / 32 columns of a value row.
+template <int E>
+__device__ __forceinline__ void get_row(const float* v, float (&x)[E]) {
+    if (E == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(v);
+        x[0] = y.x;
+        x[1] = y.y;
+        x[E - 2] = y.z;
+        x[E - 1] = y.w;
+    } else {
+        const float2 y = *reinterpret_cast<const float2*>(v);
+        x[0] = y.x;
+        x[1] = y.y;
+    }
+}
+template <int E>
+__device__ __forceinline__ void get_row(const __nv_bfloat16* v, float (&x)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        const uint32_t y = reinterpret_cast<const uint32_t*>(v)[e / 2];
+        x[e] = __uint_as_float(y << 16);
+        x[e + 1] = __uint_as_float(y & 0xffff0000u);
+    }
+}
+
+// Puts back what was cleared into a warp's rows of outputs, one row a lane: dst, D numbers (half: bfloat16)
+// of the row at position pos, valid or not. The marked tiles' values are read once more for all 32 rows, a
+// lane taking columns of each key, and their signs collected, a bit a column, by the rows that see them:
+// one infinity costs a row that sees it some hundred instructions and a read of a 32nd of its tiles.
+template <int D, int kN, typename T, bool kEdgesOnly>
+__device__ __noinline__ void put_back(const PrefillParams& p, const Piece& pc, uint32_t marks, int U, bool valid,
+                                      int pos, void* dst, bool half, int lane) {
+    constexpr int E = D / 32, kBatch = 8;
+    uint32_t up[E] = {}, down[E] = {};  // column i * E + e is bit i of word e; a NaN is in both
+    const Edge<kN> edge(p, pc, U);
+    const int shift = odd_shift(pc);
+    bool full = false;
+#pragma unroll 1
+    for (int t = pc.t0; t < pc.t1 && !full; ++t) {
+        const int tile = tile_of(pc, t);
+        if (!(marks >> ((t - pc.t0) >> shift) & 1) || (kEdgesOnly && !edge(tile))) continue;
+        const int end = min(pc.L, tile * kN + kN);
+        auto row = [&](int key) -> const T* {
+            const T* v = static_cast<const T*>(p.v) + lane * E;
+            if (!p.block_table) return v + static_cast<long long>(pc.k0 + key) * p.v_stride + pc.h * D;
+            const int pg =
+                load_page(p.block_table, p.max_pages, p.num_pages, pc.k0, key >> p.page_shift, nullptr);
+            return v + (((static_cast<size_t>(pg) * p.Hkv + pc.h) << p.page_shift) +
+                        (key & ((1 << p.page_shift) - 1))) * D;
+        };
+#pragma unroll 1
+        for (int k0 = tile * kN; k0 < end; k0 += kBatch) {
+            float x[kBatch][E];
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) get_row(row(min(k0 + i, end - 1)), x[i]);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) all &= splits(x[i][e]);
+            if (__all_sync(0xffffffffu, all)) continue;
+#pragma unroll 1
+            for (int key = k0; key < min(k0 + kBatch, end); ++key) {
+                const bool sees =
+                    valid && key <= pos && (p.window <= 0 || key > pos - p.window || key < p.n_sink);
+                float y[E];
+                get_row(row(key), y);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const uint32_t u = __ballot_sync(0xffffffffu, !splits(y[e]) && !(y[e] < 0.f));
+                    const uint32_t d = __ballot_sync(0xffffffffu, !splits(y[e]) && !(y[e] > 0.f));
+                    up[e] |= sees ? u : 0;
+                    down[e] |= sees ? d : 0;
+                }
+            }
+        }
+        // (all NaN: no more can come)
+        uint32_t both = 0xffffffffu;
+#pragma unroll
+        for (int e = 0; e < E; ++e) both &= up[e] & down[e];
+        full = __all_sync(0xffffffffu, !valid || both == 0xffffffffu);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+#pragma unroll 1
+        for (uint32_t left = up[e] | down[e]; left; left &= left - 1) {
+            const int i = __ffs(left) - 1, col = i * E + e;
+            const float x = (up[e] >> i & 1 ? INFINITY : 0.f) + (down[e] >> i & 1 ? -INFINITY : 0.f);
+            if (half) {
+                __nv_bfloat16* at = static_cast<__nv_bfloat16*>(dst) + col;
+                *at = __float2bfloat16_rn(__bfloat162float(*at) + x);
+            } else {
+                static_cast<float*>(dst)[col] += x;
+            }
+        }
+    }
+    __syncwarp();
+}
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
                  : "memory");

@@ -56,7 +56,7 @@ struct Smem {
     uint64_t qfull, qempty, kfull, kempty, vfull, vempty, sfull[2], pready[2], ofull;
     uint64_t pfull[kPieces], pempty[kPieces], end[2];
     Piece piece[kPieces];
-    int bad[kPieces];  // a value was not finite
+    uint32_t bad[kPieces];  // tiles with values that are not finite
     uint32_t tmem_base;
 };
 
@@ -90,10 +90,6 @@ __device__ __forceinline__ void put_split(uint8_t* base, int part, int rows, int
     *reinterpret_cast<uint4*>(at + 2 * part) = c;
 }
 
-// Numbers whose first part is finite. (What rounds to a bfloat16 infinity counts as infinite.)
-__device__ __forceinline__ bool splits(float x) {
-    return (__float_as_uint(x) & 0x7fffffffu) < 0x7f7f8000u;
-}
 __device__ __forceinline__ bool splits4(const float4& v) {
     return splits(v.x) && splits(v.y) && splits(v.z) && splits(v.w);
 }
@@ -182,7 +178,8 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
                         clear4(rows.x[e][1]);
                         bad = true;
                     }
-                if (bad) sm.bad[slot] = 1;
+                if (bad)
+                    atomicOr(&sm.bad[slot], 1u << (((i == items - 1 ? nt : i / 2) - 1) >> odd_shift(pc)));
             }
             uint8_t* dst = i < 0 ? sm.q[0] : is_v ? sm.v[0] : sm.k[0];
             const int height = i < 0 ? kM : kN, first = i == -1 ? kN : 0;
@@ -290,30 +287,6 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, int lane) {
 }
 
 // ----------------------------------------------------------------------------------- softmax
-// What a row gets back, in one column, of the values that were cleared: NaN, or infinities, where the row
-// sees them.
-template <int D>
-__device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, int pos, int col) {
-    float sum = 0.f;
-    for (int t = pc.t0; t < pc.t1; ++t) {
-        const int t0 = tile_of(pc, t) * kN;
-        for (int key = t0; key < min(t0 + kN, min(pc.L, pos + 1)); ++key) {
-            if (p.window > 0 && key <= pos - p.window && key >= p.n_sink) continue;
-            const float* v = static_cast<const float*>(p.v);
-            if (p.block_table) {
-                const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
-                                         key >> p.page_shift, nullptr);
-                v += (((static_cast<size_t>(pg) * p.Hkv + pc.h) << p.page_shift) +
-                      (key & ((1 << p.page_shift) - 1))) * D;
-            } else {
-                v += (pc.k0 + key) * p.v_stride + pc.h * D;
-            }
-            if (!splits(v[col])) sum += v[col] * INFINITY;
-        }
-    }
-    return sum;
-}
-
 __device__ __forceinline__ uint64_t first_bits(int n) {
     return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
@@ -465,9 +438,9 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         const int head = pc.h * p.G + head_r;
         const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
         const float top = m == -INFINITY ? -INFINITY : m * c;  // log2 units
+        float* dst = nullptr;
         if (valid) {
             float scale = 1.f;
-            float* dst;
             if (pc.slot < 0) {
                 float ref = top, sum = l;
                 if (p.sink_logit) {
@@ -493,12 +466,9 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                 unpair64(o[2 * e + 1], y.z, y.w);
                 reinterpret_cast<float4*>(dst)[e] = make_float4(y.x * scale, y.y * scale, y.z * scale, y.w * scale);
             }
-            // values that were cleared are infinite or NaN, and so is what they make of a sum
-            if (*reinterpret_cast<volatile int*>(&sm.bad[i])) {
-#pragma unroll 1
-                for (int e = 0; e < D; ++e) dst[e] += cleared<D>(p, pc, pos, e);
-            }
         }
+        const uint32_t marks = *reinterpret_cast<volatile uint32_t*>(&sm.bad[i]);
+        if (marks && busy) put_back<D, kN, float, false>(p, sm.piece[i], marks, U, valid, pos, dst, false, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pempty[i]);
     }

@@ -463,3 +463,81 @@ def test_a_replayed_graph_follows_its_lengths(kvd, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_scales(kvd, dtype, scale):
     check(kvd, Case([1, 70, 200], [300, 70, 333], 6, 2, 64, dtype, scale=scale, window=90, n_sink=3, seed=41), 32)
+
+
+def fastest(f, n=6):
+    """Milliseconds of the quickest of n calls behind a first one."""
+    best = math.inf
+    for i in range(n + 1):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        if i:
+            best = min(best, a.elapsed_time(b))
+    return best
+
+
+def strew(c, share, seed):
+    """Infinities and NaN in a share of the values."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    for v in c.v:
+        r = torch.rand(v.shape, generator=g, device=DEV)
+        kind = torch.randint(0, 3, v.shape, generator=g, device=DEV)
+        bad = torch.tensor([math.inf, -math.inf, NAN], device=DEV)[kind].to(v.dtype)
+        v.copy_(torch.where(r < share, bad, v))
+
+
+# dtypes of the tests of values that are not finite
+NOT_FINITE = [F32]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 128), (2, 2, 64), (14, 2, 64), (65, 1, 128)])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (1, 0), (70, 3), (200, 100), (64, 140)])
+@pytest.mark.parametrize("dtype", NOT_FINITE)
+def test_many_values_that_are_not_finite(kvd, dtype, window, n_sink, Hq, Hkv, D):
+    for share in (0.001, 0.5) if Hq < 10 else (0.002,):
+        c = Case([150, 200, 5, 1], [150, 420, 300, 200], Hq, Hkv, D, dtype, window=window, n_sink=n_sink, seed=50)
+        strew(c, share, 51)
+        check(kvd, c, 32)
+
+
+@pytest.mark.parametrize("dtype", NOT_FINITE)
+def test_values_that_are_not_finite_in_cut_units(kvd, dtype):
+    c = Case([4, 1, 300], [3001, 1500, 2111], 8, 2, 128, dtype, seed=52)
+    strew(c, 0.0005, 53)
+    check(kvd, c, 64)
+
+
+@pytest.mark.parametrize("new,n", [(8192, 8192), (1, 65536), (200, 65536)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", NOT_FINITE)
+def test_a_value_that_is_not_finite_costs_little(kvd, dtype, D, new, n):
+    """Near the start of a long sequence: no wait may run out for it, its rows alone change, in its column
+    alone, and the call takes about the time that it takes without."""
+    Hq, Hkv = 4, 2
+    c = Case([new, 40], [n, 300], Hq, Hkv, D, dtype, seed=54)
+    cq, ck = cu(c.new), cu(c.lens)
+    k, v = torch.cat(c.k), torch.cat(c.v)
+    out, err = torch.empty_like(c.q), torch.zeros(1, dtype=I32, device=DEV)
+
+    def call():
+        kvd.attn_prefill_gqa(c.q, k, v, cq, ck, out=out, err=err)
+
+    clean = fastest(call)
+    ref = out.clone()
+    v[1, 0, 5], v[n // 2, 1, D - 1] = -math.inf, NAN
+    first = n - new  # position of the first row
+    want = ref.clone()
+    want[max(0, 1 - first):new, :Hq // Hkv, 5] = -math.inf
+    want[max(0, n // 2 - first):new, Hq // Hkv:, D - 1] = NAN
+    time = fastest(call)
+    assert int(err.item()) == 0
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0))
+    assert time <= 1.5 * clean + 0.005, f"{time:.3f} ms, {clean:.3f} without"
+    # all of them
+    v[:n] = NAN
+    call()
+    assert torch.isnan(out[:new]).all() and torch.equal(out[new:], ref[new:]) and int(err.item()) == 0
