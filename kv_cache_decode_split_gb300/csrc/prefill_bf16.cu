@@ -85,7 +85,7 @@ struct Smem {
     uint64_t statw[2], statr[2];                      // a stream's stat written, read
     uint64_t end[4];
     Piece piece[kPieces];
-    int bad[kPieces];                                 // a value at a mask's edge was not finite
+    uint32_t bad[kPieces];                            // tiles at a mask's edge with values that are not finite
     uint32_t tmem_base;
 };
 
@@ -443,7 +443,7 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane
                     *at = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
                 }
             }
-            if (bad) sm.bad[i] = 1;
+            if (bad) atomicOr(&sm.bad[i], 1u << (t >> odd_shift(pc)));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.fixed[s]);
@@ -455,32 +455,6 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane
 }
 
 // ----------------------------------------------------------------------------------- softmax
-// What a row gets back, in one column, of the values that were cleared: v itself, where the row sees it.
-template <int D>
-__device__ __noinline__ float cleared(const PrefillParams& p, const Piece& pc, int U, int pos, int col) {
-    const Edge<kN> edge(p, pc, U);
-    float sum = 0.f;
-    for (int t = pc.t0; t < pc.t1; ++t) {
-        const int tile = tile_of(pc, t);
-        if (!edge(tile)) continue;
-        for (int key = tile * kN; key < min(tile * kN + kN, min(pc.L, pos + 1)); ++key) {
-            if (p.window > 0 && key <= pos - p.window && key >= p.n_sink) continue;
-            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v);
-            if (p.block_table) {
-                const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
-                                         key >> p.page_shift, nullptr);
-                v += (((static_cast<size_t>(pg) * p.Hkv + pc.h) << p.page_shift) +
-                      (key & ((1 << p.page_shift) - 1))) * D;
-            } else {
-                v += static_cast<long long>(pc.k0 + key) * p.v_stride + pc.h * D;
-            }
-            const float x = __bfloat162float(v[col]);
-            if (!isfinite(x)) sum += x;
-        }
-    }
-    return sum;
-}
-
 template <int D>
 __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
     const int w = warp / 4;                       // stream
@@ -634,12 +608,31 @@ __device__ __forceinline__ void store32(char* dst, bool wide, const uint32_t* x)
     }
 }
 
+// Values that are not finite, put back into the rows (r of each query tile) that a lane has written. (Called
+// where little else is in registers: by the end of each tile, 513 tokens took 19.4 us, so 18.9.)
+template <int D>
+__device__ __noinline__ void put_back_rows(const PrefillParams& p, const Piece& pc, uint32_t marks, int r) {
+    const int TM = kM / p.G, t = r / p.G;
+    const bool last = pc.slot < 0;
+#pragma unroll 1
+    for (int w = 0; w <= pc.pair; ++w) {
+        const int token = pc.tok0 + w * TM + t;
+        const long long at =
+            last ? static_cast<long long>(pc.c0 + token) * p.Hq + pc.h * p.G + (r - t * p.G)
+                 : static_cast<long long>(pc.slot) * 2 * kM + w * kM + r;
+        put_back<D, kN, __nv_bfloat16, true>(
+            p, pc, marks, 2 * TM, t < TM && token < pc.n, pc.L - pc.n + token,
+            last ? static_cast<void*>(static_cast<__nv_bfloat16*>(p.out) + at * D) : p.part_o + at * D, last,
+            threadIdx.x % 32);
+    }
+}
+
 // A piece's rows: from their sums and, as soon as their products are complete, their outputs. (Done by the
 // softmax's warps, this kept them from the next unit's scores for some 9000 cycles a unit.)
 template <int D>
 __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int lane) {
     const int r = quarter * 32 + lane;  // row of the tile, lane of tensor memory
-    const int TM = kM / p.G, U = 2 * TM;
+    const int TM = kM / p.G;
     const uint32_t tO = sm.tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + kColO;
     int* err = p.err;
     const int tok_r = r / p.G, head_r = r - tok_r * p.G;
@@ -702,7 +695,6 @@ __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int l
             ok = wait(&sm.ofull[w], k & 1, err) && (pc.pair || wait(&sm.ofull[1], k & 1, err));
             if (!ok) break;
             tc_fence_after();
-            const int bad = *reinterpret_cast<volatile int*>(&sm.bad[i]);
             if (__any_sync(0xffffffffu, valid)) {
                 // 32 bytes a store: the rows that a store's lanes touch, 2.7 cycles each, set its pace.
                 // (Exchanging pieces between lanes first, for runs of 64 bytes, takes more instructions
@@ -729,20 +721,6 @@ __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int l
                     }
                     __syncwarp();
                 }
-                if (bad && valid) {
-                    const int pos = pc.L - pc.n + token;
-#pragma unroll 1
-                    for (int col = 0; col < D; ++col) {
-                        const float v = cleared<D>(p, pc, U, pos, col);
-                        if (v == 0.f) continue;
-                        if (last) {
-                            __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(dst) + col;
-                            *at = __float2bfloat16_rn(__bfloat162float(*at) + v);
-                        } else {
-                            reinterpret_cast<float*>(dst)[col] += v;
-                        }
-                    }
-                }
                 __syncwarp();
             }
             tc_fence_before();
@@ -754,6 +732,8 @@ __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int l
         }
         if (!ok) break;
         __syncwarp();
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&sm.bad[i]);
+        if (bad) put_back_rows<D>(p, sm.piece[i], bad, r);
         if (lane == 0) mbar_arrive(&sm.pempty[i]);
     }
 }

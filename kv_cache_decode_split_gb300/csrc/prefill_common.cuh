@@ -160,9 +160,9 @@ __device__ __forceinline__ void get_row(const __nv_bfloat16* v, float (&x)[E]) {
 // lane taking columns of each key, and their signs collected, a bit a column, by the rows that see them:
 // one infinity costs a row that sees it some hundred instructions and a read of a 32nd of its tiles.
 template <int D, int kN, typename T, bool kEdgesOnly>
-__device__ __noinline__ void put_back(const PrefillParams& p, const Piece& pc, uint32_t marks, int U, bool valid,
+__device__ __forceinline__ void put_back(const PrefillParams& p, const Piece& pc, uint32_t marks, int U, bool valid,
                                       int pos, void* dst, bool half, int lane) {
-    constexpr int E = D / 32, kBatch = 8;
+    constexpr int E = D / 32, kBatch = 4;
     uint32_t up[E] = {}, down[E] = {};  // column i * E + e is bit i of word e; a NaN is in both
     const Edge<kN> edge(p, pc, U);
     const int shift = odd_shift(pc);

@@ -287,6 +287,17 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, int lane) {
 }
 
 // ----------------------------------------------------------------------------------- softmax
+// Values that are not finite, put back into the row (of the piece's 128) that a lane has written.
+template <int D>
+__device__ __noinline__ void put_back_rows(const PrefillParams& p, const Piece& pc, uint32_t marks, int r) {
+    const int TM = kM / p.G, t = r / p.G, token = pc.tok0 + t;
+    const long long at = pc.slot < 0 ? static_cast<long long>(pc.c0 + token) * p.Hq + pc.h * p.G + (r - t * p.G)
+                                     : static_cast<long long>(pc.slot) * 2 * kM + r;
+    put_back<D, kN, float, false>(p, pc, marks, TM, t < TM && token < pc.n, pc.L - pc.n + token,
+                                  (pc.slot < 0 ? static_cast<float*>(p.out) : p.part_o) + at * D, false,
+                                  threadIdx.x % 32);
+}
+
 __device__ __forceinline__ uint64_t first_bits(int n) {
     return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
@@ -438,9 +449,9 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         const int head = pc.h * p.G + head_r;
         const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
         const float top = m == -INFINITY ? -INFINITY : m * c;  // log2 units
-        float* dst = nullptr;
         if (valid) {
             float scale = 1.f;
+            float* dst;
             if (pc.slot < 0) {
                 float ref = top, sum = l;
                 if (p.sink_logit) {
@@ -468,7 +479,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
             }
         }
         const uint32_t marks = *reinterpret_cast<volatile uint32_t*>(&sm.bad[i]);
-        if (marks && busy) put_back<D, kN, float, false>(p, sm.piece[i], marks, U, valid, pos, dst, false, lane);
+        if (marks && busy) put_back_rows<D>(p, sm.piece[i], marks, r);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pempty[i]);
     }

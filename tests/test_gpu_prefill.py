@@ -490,7 +490,7 @@ def strew(c, share, seed):
 
 
 # dtypes of the tests of values that are not finite
-NOT_FINITE = [F32]
+NOT_FINITE = [F32, BF]
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 128), (2, 2, 64), (14, 2, 64), (65, 1, 128)])
