@@ -16,8 +16,9 @@
 //   * softmax: two warpgroups, one row a thread, each with two score buffers of 64 keys and an output
 //     accumulator of its own in tensor memory, so that one's exponentials run under the other's products.
 //     The row's reference maximum is only raised, and O rescaled, when a maximum grows by more than 2^8;
-//     weights are then at most 2^8 and are rounded to bfloat16 (the value product's operands have one
-//     type), their sums are float32 sums of the unrounded weights.
+//     weights are taken against 2^8 times it, so that they are at most 1 and a large value's product stays a
+//     number (against the maximum itself a weight of 2^7.5 made 2.5e36 infinite). They are rounded to bfloat16
+//     (the value product's operands have one type), their sums are float32 sums of the unrounded weights.
 //   * values: at the edges of the mask three warps clear the value rows behind the sequence's end and
 //     every value that is not finite, before a zero weight can meet them; the rows that see such a
 //     value get it back at the end.
@@ -552,7 +553,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                             tmem_st_x16(tO + 128 * w + 16 * a, o);
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    const float mc = m == -INFINITY ? 0.f : fmaf(m, c, kGrowth);
                     const uint64_t c2 = pair64(c, c), n2 = pair64(-mc, -mc);
                     uint64_t sum[2] = {pair64(l, 0.f), pair64(0.f, 0.f)};
 #pragma unroll
@@ -585,7 +586,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         if (!ok) break;
         // what the unit's end needs; the softmax goes on with the next piece
         if (!(ok = wait(&sm.statr[w], (k & 1) ^ 1, err))) break;
-        sm.stat[w][r][0] = m == -INFINITY ? -INFINITY : m * c;  // log2 units
+        sm.stat[w][r][0] = m == -INFINITY ? -INFINITY : fmaf(m, c, kGrowth);  // log2 units
         sm.stat[w][r][1] = any ? l : -1.f;                      // (below 0: nothing has been added)
         __syncwarp();
         if (lane == 0) {

@@ -541,3 +541,19 @@ def test_a_value_that_is_not_finite_costs_little(kvd, dtype, D, new, n):
     v[:n] = NAN
     call()
     assert torch.isnan(out[:new]).all() and torch.equal(out[new:], ref[new:]) and int(err.item()) == 0
+
+
+@pytest.mark.parametrize("rise", [7.5, 8.5, 60.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_large_values_stay_numbers(kvd, dtype, rise):
+    """A score that lies 2^rise above all before it, and large values there: with a row's weights at most 1
+    the sums are the values themselves. Masked by a window, at the end of a unit, and in cut units."""
+    for new, L in ((300, 300), (3, 4000)):
+        for D in (64, 128):
+            c = Case([new], [L], 4, 2, D, dtype, scale=1.0, seed=60)
+            c.q.zero_()
+            c.q[:, :, 0] = 1
+            c.k[0][:, :, 0] = 0
+            c.k[0][L - 2, :, 0] = rise * math.log(2)
+            c.v[0][L - 2] = (c.v[0][L - 2] / c.v[0][L - 2].abs().amax() * 2.0 ** 127).to(dtype)
+            check(kvd, c)
