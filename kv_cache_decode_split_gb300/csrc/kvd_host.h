@@ -226,7 +226,7 @@ struct PrefillParams {
     int n_cta;                 // CTAs, and 1 / n_cta
     double inv_cta;
     PrefillHead* head;         // [CTAs]
-    float *part_ml, *part_o;   // [2 CTAs, 256 rows] (maximum, sum) and [.., D] unnormalised outputs
+    float *part_ml, *part_o;   // [3 CTAs, 256 rows] (maximum, sum) and [.., D] unnormalised outputs
 };
 size_t prefill_ws_bytes(int D);
 int prefill_bf16_launch(const PrefillParams& p, int D, void* ws, cudaStream_t stream);

@@ -55,6 +55,11 @@ using namespace prefill;
 
 constexpr int kN = 128;     // keys of a tile, as it is loaded
 constexpr int kSub = 64;    // keys of a score buffer
+// Tiles that tensor memory adds up. A tensor core cuts what it adds, so that a sum over many keys shrinks: by
+// 1e-4 over 2048 tiles, 0.2 to 1.2 % over 32768 (4 million keys), where an output's own rounding is 0.2 %. Longer
+// pieces go in parts, which are added up in float32 arithmetic in the workspace: for loads and scores they are
+// one piece, but its statistics and outputs are handed over kMost tiles at a time.
+constexpr int kMost = 512;
 constexpr int kSoftWarps = 8;
 constexpr int kWarpLoad = 8, kWarpQk = 9, kWarpPv = 11, kWarpFix = 13,
               kWarpEnd = 16;  // products: + stream
@@ -348,6 +353,7 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
     const bool one = lane == 0;
     Turn<Ly::kV> at;
     uint32_t fixed = 0, np = 0;  // a parity bit for each slot's `fixed`, each buffer's weights
+    uint32_t parts = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
@@ -358,44 +364,48 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
         if (pc.t0 < 0) break;
         const Need need(p, pc, w, TM);
         const Edge<kN> edge(p, pc, U);
-        if (!(ok = wait(&sm.ofree[w], (k & 1) ^ 1, err))) break;
-        bool first = true;  // the next product is the piece's first
+        int t = pc.t0;
+        do {
+            if (!(ok = wait(&sm.ofree[w], (parts++ & 1) ^ 1, err))) break;
+            bool first = true;  // the next product is the part's first
+            const int end = min(pc.t1, t + kMost);
 #pragma unroll 1
-        for (int t = pc.t0; t < pc.t1; ++t) {
-            const bool own = pc.pair || ((t - pc.t0) & 1) == w;
-            const int tile = tile_of(pc, t);
-            const bool e = edge(tile);
-            const int m = !own ? 0 : e ? need(tile) : 3;
-            if (e) {
-                ok = wait(&sm.fixed[at.slot], (fixed >> at.slot) & 1, err);
-                fixed ^= 1u << at.slot;
-            } else {
-                ok = wait(&sm.vfull[at.slot], at.round, err);
-            }
-            if (!ok) break;
-            const uint32_t v = v0 + at.slot * Ly::kTile;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (m >> h & 1) {
-                    if (!(ok = wait(&sm.pready[w][h], np >> h & 1, err))) break;
-                    np ^= 1u << h;
-                    tc_fence_after();
-                    if (one) {
-                        issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
-                        tc_commit(&sm.pvdone[w][h]);
-                    }
-                    first = false;
+            for (; t < end; ++t) {
+                const bool own = pc.pair || ((t - pc.t0) & 1) == w;
+                const int tile = tile_of(pc, t);
+                const bool e = edge(tile);
+                const int m = !own ? 0 : e ? need(tile) : 3;
+                if (e) {
+                    ok = wait(&sm.fixed[at.slot], (fixed >> at.slot) & 1, err);
+                    fixed ^= 1u << at.slot;
+                } else {
+                    ok = wait(&sm.vfull[at.slot], at.round, err);
                 }
-            if (!ok) break;
-            if (one) {
-                if (own)
-                    tc_commit(&sm.vempty[at.slot]);
-                else
-                    mbar_arrive(&sm.vempty[at.slot]);
+                if (!ok) break;
+                const uint32_t v = v0 + at.slot * Ly::kTile;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (m >> h & 1) {
+                        if (!(ok = wait(&sm.pready[w][h], np >> h & 1, err))) break;
+                        np ^= 1u << h;
+                        tc_fence_after();
+                        if (one) {
+                            issue_pv<D>(tO, tS + kSub * h, v + h * kSub * 128, !first);
+                            tc_commit(&sm.pvdone[w][h]);
+                        }
+                        first = false;
+                    }
+                if (!ok) break;
+                if (one) {
+                    if (own)
+                        tc_commit(&sm.vempty[at.slot]);
+                    else
+                        mbar_arrive(&sm.vempty[at.slot]);
+                }
+                at.next();
             }
-            at.next();
-        }
-        if (ok && one) tc_commit(&sm.ofull[w]);
+            if (ok && one) tc_commit(&sm.ofull[w]);
+        } while (ok && t < pc.t1);
     }
     if (one) tc_commit(&sm.end[2 + w]);
     wait(&sm.end[2 + w], 0, err);
@@ -468,7 +478,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     const bool negative = p.scale_log2 < 0.f;
     const float c = fmaxf(fabsf(p.scale_log2), 0x1p-100f);  // (0: -inf times it stays -inf)
     const int tok_r = r / p.G;
-    uint32_t ns = 0;  // a parity bit for each score buffer
+    uint32_t ns = 0, parts = 0;  // a parity bit for each score buffer; parts handed over
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
         if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
@@ -481,118 +491,120 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         const Need need(p, pc, w, TM);
         const Edge<kN> at_edge(p, pc, U);
         float m = -INFINITY, l = 0.f;  // reference maximum (raw score units), sum
-        bool ok = true, any = false;   // any: a product of this piece has been or will be added to O
-        const int step = pc.pair ? 1 : 2;
-        const int t_first = pc.t0 + (pc.pair ? 0 : w);
-        for (int t = t_first; t < pc.t1 && ok; t += step) {
-            const int tile = tile_of(pc, t), halves = at_edge(tile) ? need(tile) | 4 : 3;  // 4: at an edge
+        bool ok = true, any = false;   // any: a product of this part has been or will be added to O
+        int t = pc.t0 + (pc.pair ? 0 : w), end = pc.t0;
+        do {
+            end = min(pc.t1, end + kMost);
+            for (; t < end && ok; t += pc.pair ? 1 : 2) {
+                const int tile = tile_of(pc, t), halves = at_edge(tile) ? need(tile) | 4 : 3;  // 4: at an edge
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                if (!(halves >> h & 1)) continue;
-                if (!(ok = wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
-                ns ^= 1u << h;
-                if (busy) {
-                    tc_fence_after();
-                    uint32_t s[2][32];
-                    tmem_ld_32x32b_x32(tS + kSub * h, s[0]);
-                    tmem_ld_32x32b_x32(tS + kSub * h + 32, s[1]);
-                    tmem_ld_wait(s[0]);
-                    tmem_ld_wait(s[1]);
-                    if (negative) {
-                        uint32_t sign = 0x80000000u;
-                        asm volatile("" : "+r"(sign));  // (nor of this)
-#pragma unroll
-                        for (int a = 0; a < kSub; ++a) s[a / 32][a % 32] ^= sign;
-                    }
-                    if (halves & 4) {
-                        // the keys seen, a bit each: up to the row's own, in its window or a sink
-                        const int ts = tile * kN + kSub * h;
-                        const int hi = pos - ts, lo = p.window > 0 && valid ? hi - p.window + 1 : 0;
-                        auto below = [](int n) -> uint64_t {  // the first n of 64 bits
-                            return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
-                        };
-                        const uint64_t seen = below(hi + 1) & (~below(lo) | below(p.n_sink - ts));
-                        uint32_t word[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
-                        asm volatile("" : "+r"(word[0]), "+r"(word[1]));  // (nothing of this ahead of the branch)
-#pragma unroll
-                        for (int a = 0; a < kSub; ++a)
-                            if (!(word[a / 32] >> (a % 32) & 1)) s[a / 32][a % 32] = 0xff800000u;
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) mx[a] = __uint_as_float(s[a / 2][16 * (a % 2)]);
-#pragma unroll
-                    for (int e = 1; e < 15; e += 2)
-#pragma unroll
-                        for (int a = 0; a < 4; ++a)
-                            mx[a] = max3(mx[a], __uint_as_float(s[a / 2][16 * (a % 2) + e]),
-                                         __uint_as_float(s[a / 2][16 * (a % 2) + e + 1]));
-                    const float top = max3(max3(mx[0], mx[1], __uint_as_float(s[0][15])),
-                                           max3(mx[2], mx[3], __uint_as_float(s[0][31])),
-                                           fmaxf(__uint_as_float(s[1][15]), __uint_as_float(s[1][31])));
-                    const bool raise = (top - m) * c > kGrowth;  // (m = -inf: always)
-                    float fade = 1.f;
-                    if (raise) {
-                        fade = fast_exp2((m - top) * c);
-                        m = top;
-                        l *= fade;
-                    }
-                    if (any && __any_sync(0xffffffffu, raise)) {
-                        // this buffer's last product is complete (its scores waited for it); the
-                        // other's when its barrier says so
-                        ok = wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err);
-                        if (!ok) break;
+                for (int h = 0; h < 2; ++h) {
+                    if (!(halves >> h & 1)) continue;
+                    if (!(ok = wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
+                    ns ^= 1u << h;
+                    if (busy) {
                         tc_fence_after();
+                        uint32_t s[2][32];
+                        tmem_ld_32x32b_x32(tS + kSub * h, s[0]);
+                        tmem_ld_32x32b_x32(tS + kSub * h + 32, s[1]);
+                        tmem_ld_wait(s[0]);
+                        tmem_ld_wait(s[1]);
+                        if (negative) {
+                            uint32_t sign = 0x80000000u;
+                            asm volatile("" : "+r"(sign));  // (nor of this)
+#pragma unroll
+                            for (int a = 0; a < kSub; ++a) s[a / 32][a % 32] ^= sign;
+                        }
+                        if (halves & 4) {
+                            // the keys seen, a bit each: up to the row's own, in its window or a sink
+                            const int ts = tile * kN + kSub * h;
+                            const int hi = pos - ts, lo = p.window > 0 && valid ? hi - p.window + 1 : 0;
+                            auto below = [](int n) -> uint64_t {  // the first n of 64 bits
+                                return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+                            };
+                            const uint64_t seen = below(hi + 1) & (~below(lo) | below(p.n_sink - ts));
+                            uint32_t word[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
+                            asm volatile("" : "+r"(word[0]), "+r"(word[1]));  // (nothing of this ahead of the branch)
+#pragma unroll
+                            for (int a = 0; a < kSub; ++a)
+                                if (!(word[a / 32] >> (a % 32) & 1)) s[a / 32][a % 32] = 0xff800000u;
+                        }
+                        float mx[4];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) mx[a] = __uint_as_float(s[a / 2][16 * (a % 2)]);
+#pragma unroll
+                        for (int e = 1; e < 15; e += 2)
+#pragma unroll
+                            for (int a = 0; a < 4; ++a)
+                                mx[a] = max3(mx[a], __uint_as_float(s[a / 2][16 * (a % 2) + e]),
+                                             __uint_as_float(s[a / 2][16 * (a % 2) + e + 1]));
+                        const float top = max3(max3(mx[0], mx[1], __uint_as_float(s[0][15])),
+                                               max3(mx[2], mx[3], __uint_as_float(s[0][31])),
+                                               fmaxf(__uint_as_float(s[1][15]), __uint_as_float(s[1][31])));
+                        const bool raise = (top - m) * c > kGrowth;  // (m = -inf: always)
+                        float fade = 1.f;
+                        if (raise) {
+                            fade = fast_exp2((m - top) * c);
+                            m = top;
+                            l *= fade;
+                        }
+                        if (any && __any_sync(0xffffffffu, raise)) {
+                            // this buffer's last product is complete (its scores waited for it); the
+                            // other's when its barrier says so
+                            ok = wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int a = 0; a < D / 16; ++a) {
-                            uint32_t o[16];
-                            tmem_ld_x16(tO + 128 * w + 16 * a, o);
+                            for (int a = 0; a < D / 16; ++a) {
+                                uint32_t o[16];
+                                tmem_ld_x16(tO + 128 * w + 16 * a, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-                            tmem_st_x16(tO + 128 * w + 16 * a, o);
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                                tmem_st_x16(tO + 128 * w + 16 * a, o);
+                            }
                         }
-                    }
-                    const float mc = m == -INFINITY ? 0.f : fmaf(m, c, kGrowth);
-                    const uint64_t c2 = pair64(c, c), n2 = pair64(-mc, -mc);
-                    uint64_t sum[2] = {pair64(l, 0.f), pair64(0.f, 0.f)};
+                        const float mc = m == -INFINITY ? 0.f : fmaf(m, c, kGrowth);
+                        const uint64_t c2 = pair64(c, c), n2 = pair64(-mc, -mc);
+                        uint64_t sum[2] = {pair64(0.f, 0.f), pair64(0.f, 0.f)};
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        uint32_t pr[16];
+                        for (int a = 0; a < 2; ++a) {
+                            uint32_t pr[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint64_t y = fma2(pair64(__uint_as_float(s[a][2 * e]),
-                                                           __uint_as_float(s[a][2 * e + 1])), c2, n2);
-                            float u, v;
-                            unpair64(y, u, v);
-                            u = fast_exp2(u);
-                            v = fast_exp2(v);
-                            sum[e & 1] = add2(sum[e & 1], pair64(u, v));
-                            pr[e] = pack_bf16(u, v);
+                            for (int e = 0; e < 16; ++e) {
+                                const uint64_t y = fma2(pair64(__uint_as_float(s[a][2 * e]),
+                                                               __uint_as_float(s[a][2 * e + 1])), c2, n2);
+                                float u, v;
+                                unpair64(y, u, v);
+                                u = fast_exp2(u);
+                                v = fast_exp2(v);
+                                sum[e & 1] = add2(sum[e & 1], pair64(u, v));
+                                pr[e] = pack_bf16(u, v);
+                            }
+                            tmem_st_x16(tS + kSub * h + 16 * a, pr);
                         }
-                        tmem_st_x16(tS + kSub * h + 16 * a, pr);
+                        float x0, x1;
+                        unpair64(add2(sum[0], sum[1]), x0, x1);
+                        l += x0 + x1;  // (once for 64 keys: one by one, small weights are rounded away)
+                        tmem_st_wait();
+                        tc_fence_before();
                     }
-                    float x0, x1;
-                    unpair64(add2(sum[0], sum[1]), x0, x1);
-                    l = x0 + x1;
-                    tmem_st_wait();
-                    tc_fence_before();
+                    any = true;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.pready[w][h]);
                 }
-                any = true;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.pready[w][h]);
             }
-        }
+            // what the unit's end needs; the softmax goes on with the next part or piece
+            if (!ok || !(ok = wait(&sm.statr[w], (parts++ & 1) ^ 1, err))) break;
+            sm.stat[w][r][0] = m == -INFINITY ? -INFINITY : fmaf(m, c, kGrowth);  // log2 units
+            sm.stat[w][r][1] = any ? l : -1.f;  // (below 0: nothing has been added)
+            l = 0.f;
+            any = false;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.statw[w]);
+        } while (end < pc.t1);
         if (!ok) break;
-        // what the unit's end needs; the softmax goes on with the next piece
-        if (!(ok = wait(&sm.statr[w], (k & 1) ^ 1, err))) break;
-        sm.stat[w][r][0] = m == -INFINITY ? -INFINITY : fmaf(m, c, kGrowth);  // log2 units
-        sm.stat[w][r][1] = any ? l : -1.f;                      // (below 0: nothing has been added)
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&sm.statw[w]);
-            mbar_arrive(&sm.pempty[i]);
-        }
+        if (lane == 0) mbar_arrive(&sm.pempty[i]);
     }
 }
 
@@ -609,23 +621,29 @@ __device__ __forceinline__ void store32(char* dst, bool wide, const uint32_t* x)
     }
 }
 
-// Values that are not finite, put back into the rows (r of each query tile) that a lane has written. (Called
-// where little else is in registers: by the end of each tile, 513 tokens took 19.4 us, so 18.9.)
+// What a piece with values that are not finite (marks), or a part of one, needs behind its stores, to the output or
+// to a slot: the thread's rows are row r of each query tile. (Behind both tiles, and not a function of its own: the
+// call, made where much is in registers, spilled what a unit's end needs, and 513 tokens took 19.6 us for 18.3.)
 template <int D>
-__device__ __noinline__ void put_back_rows(const PrefillParams& p, const Piece& pc, uint32_t marks, int r) {
+__device__ __forceinline__ void end_more(const PrefillParams& p, const Piece& pc, uint32_t marks, int slot, int end,
+                                      int r) {
     const int TM = kM / p.G, t = r / p.G;
-    const bool last = pc.slot < 0;
+    const bool first = end - kMost <= pc.t0, last = end >= pc.t1;
+    if (marks && last) {
 #pragma unroll 1
-    for (int w = 0; w <= pc.pair; ++w) {
-        const int token = pc.tok0 + w * TM + t;
-        const long long at =
-            last ? static_cast<long long>(pc.c0 + token) * p.Hq + pc.h * p.G + (r - t * p.G)
-                 : static_cast<long long>(pc.slot) * 2 * kM + w * kM + r;
-        put_back<D, kN, __nv_bfloat16, true>(
-            p, pc, marks, 2 * TM, t < TM && token < pc.n, pc.L - pc.n + token,
-            last ? static_cast<void*>(static_cast<__nv_bfloat16*>(p.out) + at * D) : p.part_o + at * D, last,
-            threadIdx.x % 32);
+        for (int w = 0; w <= pc.pair; ++w) {
+            const int token = pc.tok0 + w * TM + t;
+            const long long at =
+                slot < 0 ? static_cast<long long>(pc.c0 + token) * p.Hq + pc.h * p.G + (r - t * p.G)
+                         : static_cast<long long>(slot) * 2 * kM + w * kM + r;
+            put_back<D, kN, __nv_bfloat16, true>(
+                p, pc, marks, 2 * TM, t < TM && token < pc.n, pc.L - pc.n + token,
+                slot < 0 ? static_cast<void*>(static_cast<__nv_bfloat16*>(p.out) + at * D) : p.part_o + at * D,
+                slot < 0, threadIdx.x % 32);
+        }
     }
+    if (!(first && last)) add_part<D, __nv_bfloat16>(p, pc, slot, first, last, r);
+    __syncwarp();
 }
 
 // A piece's rows: from their sums and, as soon as their products are complete, their outputs. (Done by the
@@ -637,104 +655,112 @@ __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int l
     const uint32_t tO = sm.tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + kColO;
     int* err = p.err;
     const int tok_r = r / p.G, head_r = r - tok_r * p.G;
+    uint32_t parts = 0;  // taken over
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
         if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
-        const Piece pc = sm.piece[i];
+        const Piece& pc = sm.piece[i];
         if (pc.t0 < 0) break;
-        const bool last = pc.slot < 0;
         const int head = pc.h * p.G + head_r;
         bool ok = true;
-        // two query tiles: stream w's rows in turn; one: its rows, from both streams
+        int end = pc.t0;
+        do {
+            end += kMost;
+            const int slot = pc.t1 - pc.t0 > kMost ? 2 * p.n_cta + static_cast<int>(blockIdx.x) : pc.slot;
+            const bool last = slot < 0;
+            // two query tiles: stream w's rows in turn; one: its rows, from both streams
 #pragma unroll 1
-        for (int w = 0; w <= pc.pair && ok; ++w) {
-            ok = wait(&sm.statw[w], k & 1, err) && (pc.pair || wait(&sm.statw[1], k & 1, err));
-            if (!ok) break;
-            const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
-            const bool valid = tok_r < TM && token < pc.n;
-            float m0 = sm.stat[w][r][0], l0 = sm.stat[w][r][1], m1 = -INFINITY, l1 = -1.f;
-            if (!pc.pair) {
-                m1 = sm.stat[1][r][0];
-                l1 = sm.stat[1][r][1];
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sm.statr[w]);
-                if (!pc.pair) mbar_arrive(&sm.statr[1]);
-            }
-            const bool has0 = !(l0 < 0.f), has1 = !(l1 < 0.f);  // (the same for all rows)
-            l0 = has0 ? l0 : 0.f;
-            l1 = has1 ? l1 : 0.f;
-            const float top = fmaxf(m0, m1);
-            float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - top), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - top);
-            // (a sum that is NaN has a maximum of -inf where all of its scores are NaN)
-            float sum = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
-            if (top == -INFINITY) f0 = f1 = 1.f;
-            const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
-            if (last) {
-                float ref = top, scale = 1.f;
-                if (p.sink_logit && valid) {
-                    const float sink = p.sink_logit[head] * kLog2e;
-                    ref = fmaxf(top, sink);
-                    scale = top == -INFINITY ? 1.f : fast_exp2(top - ref);
-                    sum = sum * scale + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
+            for (int w = 0; w <= pc.pair && ok; ++w) {
+                ok = wait(&sm.statw[w], parts & 1, err) && (pc.pair || wait(&sm.statw[1], parts & 1, err));
+                if (!ok) break;
+                const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
+                const bool valid = tok_r < TM && token < pc.n;
+                float m0 = sm.stat[w][r][0], l0 = sm.stat[w][r][1], m1 = -INFINITY, l1 = -1.f;
+                if (!pc.pair) {
+                    m1 = sm.stat[1][r][0];
+                    l1 = sm.stat[1][r][1];
                 }
-                scale = sum == 0.f ? 0.f : scale / sum;
-                f0 *= scale;
-                f1 *= scale;
-                if (valid && p.lse_out)
-                    p.lse_out[row] =
-                        sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
-            } else if (valid) {
-                reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(pc.slot) * 2 * kM + w * kM + r] =
-                    make_float2(top, sum);
-            }
-            char* dst = last ? static_cast<char*>(p.out) + row * D * 2
-                             : reinterpret_cast<char*>(
-                                   p.part_o + (static_cast<long long>(pc.slot) * 2 * kM + w * kM + r) * D);
-            const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // (the same for all rows)
-            ok = wait(&sm.ofull[w], k & 1, err) && (pc.pair || wait(&sm.ofull[1], k & 1, err));
-            if (!ok) break;
-            tc_fence_after();
-            if (__any_sync(0xffffffffu, valid)) {
-                // 32 bytes a store: the rows that a store's lanes touch, 2.7 cycles each, set its pace.
-                // (Exchanging pieces between lanes first, for runs of 64 bytes, takes more instructions
-                // than that saves.)
-#pragma unroll 1
-                for (int col = 0; col < D; col += 16) {
-                    float f[16];
-                    uint32_t o[16];
-                    if (has0) tmem_ld_x16(tO + 128 * w + col, o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = has0 ? __uint_as_float(o[e]) * f0 : 0.f;
-                    if (has1) {
-                        tmem_ld_x16(tO + 128 + col, o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), f1, f[e]);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.statr[w]);
+                    if (!pc.pair) mbar_arrive(&sm.statr[1]);
+                }
+                const bool has0 = !(l0 < 0.f), has1 = !(l1 < 0.f);  // (the same for all rows)
+                l0 = has0 ? l0 : 0.f;
+                l1 = has1 ? l1 : 0.f;
+                const float top = fmaxf(m0, m1);
+                float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - top), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - top);
+                // (a sum that is NaN has a maximum of -inf where all of its scores are NaN)
+                float sum = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
+                if (top == -INFINITY) f0 = f1 = 1.f;
+                const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
+                if (last) {
+                    float ref = top, scale = 1.f;
+                    if (p.sink_logit && valid) {
+                        const float sink = p.sink_logit[head] * kLog2e;
+                        ref = fmaxf(top, sink);
+                        scale = top == -INFINITY ? 1.f : fast_exp2(top - ref);
+                        sum = sum * scale + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
                     }
-                    if (valid && last) {
+                    scale = sum == 0.f ? 0.f : scale / sum;
+                    f0 *= scale;
+                    f1 *= scale;
+                    if (valid && p.lse_out)
+                        p.lse_out[row] =
+                            sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
+                } else if (valid) {
+                    reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(slot) * 2 * kM + w * kM + r] =
+                        make_float2(top, sum);
+                }
+                char* dst = last ? static_cast<char*>(p.out) + row * D * 2
+                                 : reinterpret_cast<char*>(
+                                       p.part_o + (static_cast<long long>(slot) * 2 * kM + w * kM + r) * D);
+                const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // (the same for all rows)
+                ok = wait(&sm.ofull[w], parts & 1, err) && (pc.pair || wait(&sm.ofull[1], parts & 1, err));
+                if (!ok) break;
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, valid)) {
+                    // 32 bytes a store: the rows that a store's lanes touch, 2.7 cycles each, set its pace.
+                    // (Exchanging pieces between lanes first, for runs of 64 bytes, takes more instructions
+                    // than that saves.)
+#pragma unroll 1
+                    for (int col = 0; col < D; col += 16) {
+                        float f[16];
+                        uint32_t o[16];
+                        if (has0) tmem_ld_x16(tO + 128 * w + col, o);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
-                        store32(dst + col * 2, wide, o);
-                    } else if (valid) {
-                        store32(dst + col * 4, wide, reinterpret_cast<uint32_t*>(f));
-                        store32(dst + col * 4 + 32, wide, reinterpret_cast<uint32_t*>(f) + 8);
+                        for (int e = 0; e < 16; ++e) f[e] = has0 ? __uint_as_float(o[e]) * f0 : 0.f;
+                        if (has1) {
+                            tmem_ld_x16(tO + 128 + col, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), f1, f[e]);
+                        }
+                        if (valid && last) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+                            store32(dst + col * 2, wide, o);
+                        } else if (valid) {
+                            store32(dst + col * 4, wide, reinterpret_cast<uint32_t*>(f));
+                            store32(dst + col * 4 + 32, wide, reinterpret_cast<uint32_t*>(f) + 8);
+                        }
+                        __syncwarp();
                     }
                     __syncwarp();
                 }
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.ofree[w]);
+                    if (!pc.pair) mbar_arrive(&sm.ofree[1]);
+                }
             }
-            tc_fence_before();
+            if (!ok) break;
+            ++parts;
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sm.ofree[w]);
-                if (!pc.pair) mbar_arrive(&sm.ofree[1]);
-            }
-        }
+            const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&sm.bad[i]);
+            if (__builtin_expect(bad || pc.t1 - pc.t0 > kMost, 0)) end_more<D>(p, sm.piece[i], bad, slot, end, r);
+        } while (end < pc.t1);
         if (!ok) break;
-        __syncwarp();
-        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&sm.bad[i]);
-        if (bad) put_back_rows<D>(p, sm.piece[i], bad, r);
         if (lane == 0) mbar_arrive(&sm.pempty[i]);
     }
 }

@@ -13,6 +13,7 @@ namespace prefill {
 constexpr int kM = 128;        // rows of a query tile
 constexpr int kMaxCtas = 256;  // of the main launch
 constexpr int kPieces = 4;     // ring of work descriptions
+constexpr int kSlots = 3;      // partial results of a CTA: of its first and its last piece, and of a part
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -574,6 +575,69 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams 
     }
 }
 
+// Adds a part of a piece, which lies in slot `from`, to the parts before it (first: there are none), or ends the
+// piece (last): one row a thread, r of each query tile, which it has written. A whole unit's parts are added up
+// in the slot of the CTA's last piece, which comes behind it.
+template <int D, typename T>
+__device__ __forceinline__ void add_part(const PrefillParams& p, const Piece& pc, int from, bool first, bool last,
+                                         int r) {
+    const int TM = kM / p.G, t = r / p.G, head = pc.h * p.G + (r - t * p.G);
+    float2* ml = reinterpret_cast<float2*>(p.part_ml);
+#pragma unroll 1
+    for (int w = 0; w <= pc.pair; ++w) {
+        const int token = pc.tok0 + w * TM + t;
+        if (t >= TM || token >= pc.n) continue;
+        const long long own = (static_cast<long long>(from) * 2 + w) * kM + r;
+        const long long sum_at =
+            (static_cast<long long>(pc.slot < 0 ? 2 * blockIdx.x + 1 : pc.slot) * 2 + w) * kM + r;
+        float top = ml[own].x, sum = ml[own].y, f = 1.f, fp = 0.f;
+        if (!first) {
+            const float2 was = ml[sum_at];
+            const float both = fmaxf(top, was.x);
+            // (a part without a maximum: nothing seen, or all of it NaN)
+            f = top == -INFINITY ? 1.f : fast_exp2(top - both);
+            fp = was.x == -INFINITY ? 1.f : fast_exp2(was.x - both);
+            sum = sum * f + was.y * fp;
+            top = both;
+        }
+        const long long row = static_cast<long long>(pc.c0 + token) * p.Hq + head;
+        const bool done = last && pc.slot < 0;
+        if (done) {
+            float scale = 1.f;
+            if (p.sink_logit) {
+                const float sink = p.sink_logit[head] * kLog2e, ref = fmaxf(top, sink);
+                scale = top == -INFINITY ? 1.f : fast_exp2(top - ref);
+                sum = sum * scale + (sink == -INFINITY ? 0.f : fast_exp2(sink - ref));
+                top = ref;
+            }
+            scale = sum == 0.f ? 0.f : scale / sum;
+            f *= scale;
+            fp *= scale;
+            if (p.lse_out)
+                p.lse_out[row] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
+        } else {
+            ml[sum_at] = make_float2(top, sum);
+        }
+#pragma unroll 1
+        for (int col = 0; col < D; col += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p.part_o + own * D + col);
+            float o[4] = {x.x * f, x.y * f, x.z * f, x.w * f};
+            float* at = p.part_o + sum_at * D + col;
+            if (fp != 0.f) {
+                const float4 y = *reinterpret_cast<const float4*>(at);
+                o[0] = fmaf(y.x, fp, o[0]);
+                o[1] = fmaf(y.y, fp, o[1]);
+                o[2] = fmaf(y.z, fp, o[2]);
+                o[3] = fmaf(y.w, fp, o[3]);
+            }
+            if (done)
+                put_row<4>(static_cast<T*>(p.out) + row * D + col, o);
+            else
+                put_row<4>(at, o);
+        }
+    }
+}
+
 constexpr int kMergeRows = 8;  // blocks of a unit
 
 inline int ctas() { return std::min(num_sms(), kMaxCtas); }
@@ -585,8 +649,8 @@ inline Plan make_plan(int D) {
     const size_t n = static_cast<size_t>(ctas());
     Plan pl;
     pl.off_ml = (n * sizeof(PrefillHead) + 255) & ~static_cast<size_t>(255);
-    pl.off_o = pl.off_ml + n * 2 * 2 * kM * 8;
-    pl.total = pl.off_o + n * 2 * 2 * kM * D * 4;
+    pl.off_o = pl.off_ml + n * kSlots * 2 * kM * 8;
+    pl.total = pl.off_o + n * kSlots * 2 * kM * D * 4;
     return pl;
 }
 

@@ -557,3 +557,101 @@ def test_large_values_stay_numbers(kvd, dtype, rise):
             c.k[0][L - 2, :, 0] = rise * math.log(2)
             c.v[0][L - 2] = (c.v[0][L - 2] / c.v[0][L - 2].abs().amax() * 2.0 ** 127).to(dtype)
             check(kvd, c)
+
+
+def repeated(q, k, v, L, scale, window=0, n_sink=0, sink=None, tiles=512):
+    """prefill_reference.attention of one sequence whose L keys are those of k and v [U, Hkv, D] over and over:
+    position t has key t % U. float64 outputs, lse and their bounds, for sums of which a tensor core cuts those of
+    `tiles` tiles of 128 keys, 16 keys at a time (2^-23 of what has been added up), and the rest is rounded."""
+    n, Hq, D = q.shape
+    U, Hkv = k.shape[:2]
+    pos = L - n + torch.arange(n, device=DEV)[:, None]
+    at = torch.arange(U, device=DEV)[None, :]
+    count = lambda x: (x - at + U - 1).clamp_min(0) // U  # noqa: E731 (of at's positions below x)
+    low = (pos - window + 1).clamp_min(0) if window else torch.zeros_like(pos)
+    times = (count(pos + 1) - count(low) + count(low.clamp_max(n_sink))).to(torch.float64)
+    out = torch.empty(n, Hq, D, dtype=torch.float64, device=DEV)
+    lse, tol, tol_l = torch.empty(n, Hq, dtype=torch.float64, device=DEV), torch.empty_like(out), None
+    tol_l = torch.empty_like(lse)
+    adds = tiles * 8 + L / (128 * tiles) * 8 + 64
+    for h in range(Hq):
+        x, y, z = q[:, h].double(), k[:, h // (Hq // Hkv)].double(), v[:, h // (Hq // Hkv)].double()
+        s = scale * (x @ y.T) + times.log()
+        A = abs(scale) * (x.abs() @ y.abs().T).amax(1)
+        lse[:, h] = s.logsumexp(1) if sink is None else torch.logaddexp(s.logsumexp(1), sink[h].double())
+        w = (s - lse[:, h, None]).exp()
+        out[:, h] = w @ z
+        ds = (D + 8) * 2.0 ** -23 * A
+        wr = 2.0 ** -8 if scale else 0.0  # (equal weights are powers of two)
+        tol[:, h] = (w @ z.abs()) * (2 * (ds + 2.0 ** -21) + wr + adds * 2.0 ** -23)[:, None]
+        tol_l[:, h] = ds + 2.0 ** -21 + (adds / 4) * 2.0 ** -24 + 2.0 ** -22 * lse[:, h].abs()
+    return out, lse, tol + 2.0 ** -8 * out.abs(), tol_l
+
+
+def long_call(kvd, new, lens, Hq, Hkv, D, U=1024, P=256, seed=70, zero=False, **kw):
+    """Sequences of lens[b] keys out of the same U / P pages."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)  # noqa: E731
+    q, kp, vp = rnd(sum(new), Hq, D), rnd(U // P, Hkv, P, D), rnd(U // P, Hkv, P, D) * 0.5 + 1
+    scale = 0.0 if zero else 1 / math.sqrt(D)
+    bt = (torch.arange(-(-max(lens) // P), device=DEV) % (U // P)).to(I32).repeat(len(lens), 1)
+    out, lse = torch.full_like(q, 77.0), torch.full((sum(new), Hq), 55.0, device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    kvd.attn_prefill_gqa_paged(q, kp, vp, bt, torch.tensor(lens, dtype=I32, device=DEV), cu(new), scale=scale,
+                               out=out, lse_out=lse, err=err, **kw)
+    assert int(err.item()) == 0
+    k, v = (x.transpose(1, 2).reshape(U, Hkv, D) for x in (kp, vp))
+    at = 0
+    for b, n in enumerate(new):
+        if n == 0 or (b > 3 and b < len(new) - 3 and b % 16):  # (a sample of many alike)
+            at += n
+            continue
+        r = repeated(q[at:at + n], k, v, lens[b], scale, kw.get("window", 0), kw.get("n_sink_tokens", 0),
+                     kw.get("sink_logit"))
+        R.compare(out[at:at + n], lse[at:at + n], *r, what=f"sequence {b}")
+        at += n
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("zero", [False, True])
+def test_bfloat16_sums_do_not_drift(kvd, D, zero):
+    # one token of 152 heads: as many units as CTAs, of 4 million keys each (before: lse 7e-4 off, equal
+    # weights' means 1.2e-2)
+    long_call(kvd, [1], [2 ** 22], 152, 152, D, zero=zero)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (4, 1, 128), (7, 1, 64)])
+@pytest.mark.parametrize("learned", [False, True])
+def test_long_pieces_go_in_parts(kvd, Hq, Hkv, D, learned):
+    # units of one and of two query tiles, whole and cut, of one part and of several
+    sink = torch.randn(Hq, device=DEV) * 2 + 9 if learned else None
+    long_call(kvd, [3, 0, 300, 1, 70], [65536, 65537, 200001, 131072, 66000], Hq, Hkv, D, sink_logit=sink)
+    long_call(kvd, [1, 5] * 100, [65536 + 77 * i for i in range(200)], Hq, Hkv, D, sink_logit=sink)
+    long_call(kvd, [300] * 40 + [40] * 50, [140000 - 50 * i for i in range(90)], Hq, Hkv, D, sink_logit=sink)
+    long_call(kvd, [200, 1] * 60, [150000] * 120, Hq, Hkv, D, window=100000, n_sink_tokens=300, sink_logit=sink)
+
+
+@pytest.mark.parametrize("Hq,new", [(4, 1), (4, 40), (1, 200)])
+def test_values_that_are_not_finite_in_parts(kvd, Hq, new):
+    # 160 units of several parts; the odd values lie in the last page of each sequence, which is seen by some rows
+    g = torch.Generator(device=DEV).manual_seed(75)
+    D, P, n, B = 64, 64, 1100, 160
+    kp, vp = (torch.randn(6, 1, P, D, generator=g, device=DEV).to(BF) for _ in range(2))
+    q = torch.randn(B * new, Hq, D, generator=g, device=DEV).to(BF)
+    bt = (torch.arange(n, device=DEV) % 5).to(I32).repeat(B, 1)
+    bt[:, -1] = 5
+    lens = torch.tensor([n * P - b % P for b in range(B)], dtype=I32, device=DEV)
+    err = torch.zeros(1, dtype=I32, device=DEV)
+
+    def call():
+        return kvd.attn_prefill_gqa_paged(q, kp, vp, bt, lens, cu([new] * B), err=err)
+
+    want = call()
+    for slot, col, x in ((0, 5, math.inf), (30, 63, -math.inf), (40, 0, NAN)):
+        vp[5, 0, slot, col] = x
+        pos = (lens[:, None] - new + torch.arange(new, device=DEV)[None]).flatten()
+        want[pos >= (n - 1) * P + slot, :, col] = x
+    got = call()
+    assert int(err.item()) == 0
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(7.0, 8.0, 9.0), want.nan_to_num(7.0, 8.0, 9.0))
