@@ -371,7 +371,8 @@ int attn_decode_gqa_q4(const void *q, const void *k_pool, const void *v_pool,
  * are taken apart into three bfloat16 numbers: a magnitude above 3.389e38 counts as infinite, and an
  * infinite key or query makes the scores of its products NaN. The result does not depend on timing.
  * One launch or, where a long sequence's work is divided, two. A kernel whose waits run out (which a
- * fault of the device would have to cause) records KVD_ERR_TIMEOUT in err and leaves out undefined.
+ * fault of the device would have to cause: they allow for the longest sequence's work) records
+ * KVD_ERR_TIMEOUT in err and leaves out undefined.
  * Supported: D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, dtype KVD_BF16 or KVD_F32; T == 0 does
  * nothing.
  */
@@ -667,7 +668,7 @@ int kvd_delta_decode_step(float *S, const float *q, const float *k, const float 
  *                         split, raised if the plan would exceed its chunk limit.
  *  KVD_OPT_MLA_MIN_TILES  0 (default): the MLA plan gives each two-CTA cluster at least one
  *                         64-token tile (dense) or two (sparse); >= 1: at least that many.
- *  KVD_OPT_WAIT_TIMEOUT_TEST  1 or 2: the next bf16 GQA / SWA call (and only that call) runs
+ *  KVD_OPT_WAIT_TIMEOUT_TEST  1 to 6: the next bf16 GQA / SWA call (and only that call) runs
  *                         with a limit of about 1000 SM cycles on each bounded wait of its
  *                         copy ring, and its consumer warps first wait on a barrier that
  *                         nothing completes: the wait runs out, the call records
@@ -676,6 +677,11 @@ int kvd_delta_decode_step(float *S, const float *q, const float *k, const float 
  *                         workspace stays ready for the next call. An attn_decode_gqa_q4 call
  *                         takes the option in the same way: each warp's wait for its first (1)
  *                         or second (2) tile runs out (KVD_ERR_TIMEOUT in err, NaN outputs).
+ *                         So does an attn_prefill_gqa(_paged) call: the warps that take the
+ *                         n-th of its roles (loads and work list, scores, outputs, values,
+ *                         softmax, ends of units; float32 has no sixth) wait some milliseconds
+ *                         for what does not come, and all others run out behind them
+ *                         (KVD_ERR_TIMEOUT in err, outputs undefined).
  *  KVD_OPT_GQA_CLUSTER    1 (default): a bf16 GQA / SWA call with few (sequence, KV head)
  *                         groups, whose groups need few chunks, runs each group's chunks as
  *                         one thread-block cluster that combines them in distributed shared

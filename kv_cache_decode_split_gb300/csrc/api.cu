@@ -708,7 +708,9 @@ int attn_decode_gqa_q4(const void* q, const void* k_pool, const void* v_pool,
     p.n_sink = ring ? 0 : n_sink_tokens;
     p.ring = ring ? static_cast<int>(cap) : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.stall = g_opt_wait_test.exchange(0);  // KVD_OPT_WAIT_TIMEOUT_TEST, taken by this call only
+    // KVD_OPT_WAIT_TIMEOUT_TEST, taken by this call only
+    p.stall = g_opt_wait_test.exchange(0);
+    if (p.stall > 2) p.stall = 0;
     return q4_launch(plan, p, D, dtype, stream);
 }
 
@@ -794,6 +796,7 @@ int attn_prefill_gqa(const void* q, const void* k, const void* v, const int32_t*
     p.Tk = Tk;
     p.k_stride = k_stride;
     p.v_stride = v_stride;
+    p.stall = g_opt_wait_test.exchange(0);  // KVD_OPT_WAIT_TIMEOUT_TEST, taken by this call only
     return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, ws, stream);
 }
 
@@ -831,6 +834,7 @@ int attn_prefill_gqa_paged(const void* q, const void* k_pool, const void* v_pool
     p.page_shift = __builtin_ctz(page_size);
     p.max_pages = max_pages;
     p.num_pages = num_pages;
+    p.stall = g_opt_wait_test.exchange(0);  // KVD_OPT_WAIT_TIMEOUT_TEST, taken by this call only
     return dtype == KVD_BF16 ? prefill_bf16_launch(p, D, ws, stream) : prefill_f32_launch(p, D, ws, stream);
 }
 
@@ -1366,7 +1370,7 @@ int kvd_set_option(int option, long long value) {
             g_opt_mla_min_tiles.store(value);
             return KVD_OK;
         case KVD_OPT_WAIT_TIMEOUT_TEST:
-            if (value < 0 || value > 2) return KVD_ERR_INVALID_ARG;
+            if (value < 0 || value > 6) return KVD_ERR_INVALID_ARG;
             g_opt_wait_test.store(static_cast<int>(value));
             return KVD_OK;
         case KVD_OPT_GQA_CLUSTER:

@@ -225,6 +225,8 @@ struct PrefillParams {
     int unit_cost, flat_slack; // keys that a unit's start and end are worth; what an uncut call may lose
     int n_cta;                 // CTAs, and 1 / n_cta
     double inv_cta;
+    long long wait_cycles;     // limit of a wait
+    int stall;                 // test of the give-up path: the role that waits for what does not come
     PrefillHead* head;         // [CTAs]
     float *part_ml, *part_o;   // [3 CTAs, 256 rows] (maximum, sum) and [.., D] unnormalised outputs
 };

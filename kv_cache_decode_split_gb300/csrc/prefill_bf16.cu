@@ -89,7 +89,7 @@ struct Smem {
     uint64_t issued[Layout<D>::kV], fixed[Layout<D>::kV];
     uint64_t qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], ofull[2], ofree[2], pfull[kPieces], pempty[kPieces];
     uint64_t statw[2], statr[2];                      // a stream's stat written, read
-    uint64_t end[4];
+    uint64_t end[4], never;
     Piece piece[kPieces];
     uint32_t bad[kPieces];                            // tiles at a mask's edge with values that are not finite
     uint32_t tmem_base;
@@ -156,11 +156,11 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     int* err = p.err;
     int ps = 0;               // pieces published
     uint32_t gk = 0, gv = 0, nq = 0;  // key tiles, value tiles and query loads issued
-    bool ok = true;
+    bool ok = !stalls(p, &sm.never, 1);
     auto publish = [&](const Piece& u) {
         const int i = ps % kPieces;
         if (lane == 0) {
-            ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, err);
+            ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, p);
             if (ok) {
                 sm.piece[i] = u;
                 sm.bad[i] = 0;
@@ -172,14 +172,14 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     };
 
     walk<kN>(p, U, TM, lane, [&](const Piece& pc) {
-        publish(pc);
+        if (ok) publish(pc);
         if (!ok) return false;
         const int nt = pc.t1 - pc.t0, la = pc.pair ? 1 : 2;
         if (nt == 0) return true;
         const Edge<kN> edge(p, pc, U);
         // queries
         if (lane == 0) {
-            ok = wait(&sm.qempty, (nq & 1) ^ 1, err);
+            ok = wait(&sm.qempty, (nq & 1) ^ 1, p);
             if (ok) {
                 const int rows = TM * p.G;
                 mbar_arrive_expect_tx(&sm.qfull, (pc.pair ? 2 : 1) * rows * D * 2);
@@ -215,7 +215,7 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
             const uint32_t n = is_v ? gv : gk, size = is_v ? Ly::kV : Ly::kK, s_ = n % size;
             uint64_t* full = is_v ? &sm.vfull[s_] : &sm.kfull[s_];
             if (lane == 0) {
-                ok = wait(is_v ? &sm.vempty[s_] : &sm.kempty[s_], ((n / size) & 1) ^ 1, err);
+                ok = wait(is_v ? &sm.vempty[s_] : &sm.kempty[s_], ((n / size) & 1) ^ 1, p);
                 if (ok) {
                     mbar_arrive_expect_tx(full, Ly::kTile);
                     if (is_v && edge(tile_of(pc, pc.t0 + t))) mbar_arrive(&sm.issued[s_]);
@@ -259,10 +259,10 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
     // every copy lands before the CTA ends, also after a wait gave up
     if (lane == 0) {
         for (uint32_t i = gk > Ly::kK ? gk - Ly::kK : 0; i < gk; ++i)
-            wait(&sm.kfull[i % Ly::kK], (i / Ly::kK) & 1, err);
+            drain(&sm.kfull[i % Ly::kK], (i / Ly::kK) & 1, p);
         for (uint32_t i = gv > Ly::kV ? gv - Ly::kV : 0; i < gv; ++i)
-            wait(&sm.vfull[i % Ly::kV], (i / Ly::kV) & 1, err);
-        if (nq > 0) wait(&sm.qfull, (nq - 1) & 1, err);
+            drain(&sm.vfull[i % Ly::kV], (i / Ly::kV) & 1, p);
+        if (nq > 0) drain(&sm.qfull, (nq - 1) & 1, p);
     }
     __syncwarp();
 }
@@ -293,14 +293,13 @@ __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
     using Ly = Layout<D>;
     const int TM = kM / p.G, U = 2 * TM;
     const uint32_t tS = sm.tmem_base + kColS + 128 * w, k0 = smem_u32(sm.k[0]);
-    int* err = p.err;
     const bool one = lane == 0;
     Turn<Ly::kK> at;
     uint32_t nq = 0, used = 0;  // used: a parity bit for each buffer's score tiles
-    bool ok = true;
+    bool ok = !stalls(p, &sm.never, 2);
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const Piece pc = sm.piece[i];
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
@@ -309,17 +308,17 @@ __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
         const uint32_t q = smem_u32(sm.q[pc.pair ? w : 0]);
         const Need need(p, pc, w, TM);
         const Edge<kN> edge(p, pc, U);
-        if (!(ok = wait(&sm.qfull, nq++ & 1, err))) break;
+        if (!(ok = wait(&sm.qfull, nq++ & 1, p))) break;
 #pragma unroll 1
         for (int t = pc.t0; t < pc.t1; ++t) {
             const bool own = pc.pair || ((t - pc.t0) & 1) == w;
             const int tile = tile_of(pc, t), m = !own ? 0 : edge(tile) ? need(tile) : 3;
-            if (!(ok = wait(&sm.kfull[at.slot], at.round, err))) break;
+            if (!(ok = wait(&sm.kfull[at.slot], at.round, p))) break;
             const uint32_t kt = k0 + at.slot * Ly::kTile;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (m >> h & 1) {
-                    if (!(ok = wait(&sm.pvdone[w][h], (used >> h & 1) ^ 1, err))) break;
+                    if (!(ok = wait(&sm.pvdone[w][h], (used >> h & 1) ^ 1, p))) break;
                     used ^= 1u << h;
                     tc_fence_after();
                     if (one) {
@@ -340,7 +339,7 @@ __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
     }
     // all products complete before tensor memory is released
     if (one) tc_commit(&sm.end[w]);
-    wait(&sm.end[w], 0, err);
+    drain(&sm.end[w], 0, p);
 }
 
 template <int D>
@@ -349,15 +348,14 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
     const int TM = kM / p.G, U = 2 * TM;
     const uint32_t tS = sm.tmem_base + kColS + 128 * w, tO = sm.tmem_base + kColO + 128 * w;
     const uint32_t v0 = smem_u32(sm.v[0]);
-    int* err = p.err;
     const bool one = lane == 0;
     Turn<Ly::kV> at;
     uint32_t fixed = 0, np = 0;  // a parity bit for each slot's `fixed`, each buffer's weights
     uint32_t parts = 0;
-    bool ok = true;
+    bool ok = !stalls(p, &sm.never, 3);
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const Piece pc = sm.piece[i];
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
@@ -366,7 +364,7 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
         const Edge<kN> edge(p, pc, U);
         int t = pc.t0;
         do {
-            if (!(ok = wait(&sm.ofree[w], (parts++ & 1) ^ 1, err))) break;
+            if (!(ok = wait(&sm.ofree[w], (parts++ & 1) ^ 1, p))) break;
             bool first = true;  // the next product is the part's first
             const int end = min(pc.t1, t + kMost);
 #pragma unroll 1
@@ -376,17 +374,17 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
                 const bool e = edge(tile);
                 const int m = !own ? 0 : e ? need(tile) : 3;
                 if (e) {
-                    ok = wait(&sm.fixed[at.slot], (fixed >> at.slot) & 1, err);
+                    ok = wait(&sm.fixed[at.slot], (fixed >> at.slot) & 1, p);
                     fixed ^= 1u << at.slot;
                 } else {
-                    ok = wait(&sm.vfull[at.slot], at.round, err);
+                    ok = wait(&sm.vfull[at.slot], at.round, p);
                 }
                 if (!ok) break;
                 const uint32_t v = v0 + at.slot * Ly::kTile;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (m >> h & 1) {
-                        if (!(ok = wait(&sm.pready[w][h], np >> h & 1, err))) break;
+                        if (!(ok = wait(&sm.pready[w][h], np >> h & 1, p))) break;
                         np ^= 1u << h;
                         tc_fence_after();
                         if (one) {
@@ -408,7 +406,7 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, const int w, const 
         } while (ok && t < pc.t1);
     }
     if (one) tc_commit(&sm.end[2 + w]);
-    wait(&sm.end[2 + w], 0, err);
+    drain(&sm.end[2 + w], 0, p);
 }
 
 // ------------------------------------------------------------------------- values at the edges
@@ -416,11 +414,11 @@ template <int D>
 __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane) {
     using Ly = Layout<D>;
     const int U = 2 * (kM / p.G);
-    int* err = p.err;
     uint32_t g = 0, phase = 0;  // value tiles before the piece; a bit for each slot
+    if (stalls(p, &sm.never, 4)) return;
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0;
@@ -431,7 +429,7 @@ __device__ void fix_role(const PrefillParams& p, Smem<D>& sm, int warp, int lane
             if (!edge(tile)) continue;
             const uint32_t n = g + t;
             const int s = n % Ly::kV;
-            ok = wait(&sm.issued[s], (phase >> s) & 1, err) && wait(&sm.vfull[s], (n / Ly::kV) & 1, err);
+            ok = wait(&sm.issued[s], (phase >> s) & 1, p) && wait(&sm.vfull[s], (n / Ly::kV) & 1, p);
             if (!ok) break;
             phase ^= 1u << s;
             const int valid = pc.L - tile * kN;  // rows of the sequence
@@ -474,14 +472,14 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     const uint32_t quad = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tS = sm.tmem_base + quad + kColS + 128 * w;
     const uint32_t tO = sm.tmem_base + quad + kColO;
-    int* err = p.err;
     const bool negative = p.scale_log2 < 0.f;
     const float c = fmaxf(fabsf(p.scale_log2), 0x1p-100f);  // (0: -inf times it stays -inf)
     const int tok_r = r / p.G;
     uint32_t ns = 0, parts = 0;  // a parity bit for each score buffer; parts handed over
+    if (stalls(p, &sm.never, 5)) return;
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
@@ -500,7 +498,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     if (!(halves >> h & 1)) continue;
-                    if (!(ok = wait(&sm.sfull[w][h], ns >> h & 1, err))) break;
+                    if (!(ok = wait(&sm.sfull[w][h], ns >> h & 1, p))) break;
                     ns ^= 1u << h;
                     if (busy) {
                         tc_fence_after();
@@ -551,7 +549,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                         if (any && __any_sync(0xffffffffu, raise)) {
                             // this buffer's last product is complete (its scores waited for it); the
                             // other's when its barrier says so
-                            ok = wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, err);
+                            ok = wait(&sm.pvdone[w][1 - h], (ns >> (1 - h) & 1) ^ 1, p);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
@@ -595,7 +593,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
                 }
             }
             // what the unit's end needs; the softmax goes on with the next part or piece
-            if (!ok || !(ok = wait(&sm.statr[w], (parts++ & 1) ^ 1, err))) break;
+            if (!ok || !(ok = wait(&sm.statr[w], (parts++ & 1) ^ 1, p))) break;
             sm.stat[w][r][0] = m == -INFINITY ? -INFINITY : fmaf(m, c, kGrowth);  // log2 units
             sm.stat[w][r][1] = any ? l : -1.f;  // (below 0: nothing has been added)
             l = 0.f;
@@ -653,12 +651,12 @@ __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int l
     const int r = quarter * 32 + lane;  // row of the tile, lane of tensor memory
     const int TM = kM / p.G;
     const uint32_t tO = sm.tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + kColO;
-    int* err = p.err;
     const int tok_r = r / p.G, head_r = r - tok_r * p.G;
     uint32_t parts = 0;  // taken over
+    if (stalls(p, &sm.never, 6)) return;
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const Piece& pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int head = pc.h * p.G + head_r;
@@ -671,7 +669,7 @@ __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int l
             // two query tiles: stream w's rows in turn; one: its rows, from both streams
 #pragma unroll 1
             for (int w = 0; w <= pc.pair && ok; ++w) {
-                ok = wait(&sm.statw[w], parts & 1, err) && (pc.pair || wait(&sm.statw[1], parts & 1, err));
+                ok = wait(&sm.statw[w], parts & 1, p) && (pc.pair || wait(&sm.statw[1], parts & 1, p));
                 if (!ok) break;
                 const int token = pc.tok0 + (pc.pair ? w * TM : 0) + tok_r;
                 const bool valid = tok_r < TM && token < pc.n;
@@ -716,7 +714,7 @@ __device__ void end_role(const PrefillParams& p, Smem<D>& sm, int quarter, int l
                                  : reinterpret_cast<char*>(
                                        p.part_o + (static_cast<long long>(slot) * 2 * kM + w * kM + r) * D);
                 const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // (the same for all rows)
-                ok = wait(&sm.ofull[w], parts & 1, err) && (pc.pair || wait(&sm.ofull[1], parts & 1, err));
+                ok = wait(&sm.ofull[w], parts & 1, p) && (pc.pair || wait(&sm.ofull[1], parts & 1, p));
                 if (!ok) break;
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, valid)) {
@@ -806,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.end[i], 1);
             mbar_init(&sm.end[2 + i], 1);
         }
+        mbar_init(&sm.never, 1);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.pfull[i], 1);
             mbar_init(&sm.pempty[i], 4 + kFixWarps + kSoftWarps + 4);

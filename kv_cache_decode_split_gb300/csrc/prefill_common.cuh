@@ -234,16 +234,19 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
                  : "memory");
 }
 
-// mbar_wait in fewer instructions (a failing try_wait sleeps for about 1950 cycles, so this gives up after
-// some 2 s). Code that a unit runs once is not in the instruction caches: it costs some 10 cycles an
-// instruction, so that everything but the loops over tiles is kept short and rolled.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err) {
-    const uint32_t a = smem_u32(bar);
-#pragma unroll 1
-    for (int n = 0; n < 2000000; ++n)
-        if (mbar_try_wait(a, parity)) return true;
-    record_error(err, KVD_ERR_TIMEOUT);
-    return false;
+// A bounded wait. (Code that a unit runs once is not in the instruction caches: it costs some 10 cycles an
+// instruction, so that everything but the loops over tiles is kept short and rolled.)
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const PrefillParams& p) {
+    return mbar_wait(bar, parity, p.err, p.wait_cycles);
+}
+// For what is under way already: copies and products that must be complete before the CTA ends, also after a
+// wait gave up.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, const PrefillParams& p) {
+    mbar_wait(bar, parity, p.err);
+}
+// The test of a wait that runs out: the role first waits for what nothing completes.
+__device__ __forceinline__ bool stalls(const PrefillParams& p, uint64_t* never, int role) {
+    return p.stall == role && !wait(never, 0, p);
 }
 
 // Registers of the executing warpgroup's threads, from the CTA's share at launch.
@@ -670,6 +673,10 @@ inline cudaError_t launch_merge(const PrefillParams& p, int U, cudaStream_t stre
 
 // The call's part of the parameters: workspace and how work is cut.
 inline void set_plan(PrefillParams& p, int D, void* ws, int unit_cost, int flat_slack) {
+    // A wait may be as long as the four pieces that are under way, of at most 103 cycles a key, or as the look
+    // through all sequences' lengths.
+    const long long keys = p.block_table ? static_cast<long long>(p.max_pages) << p.page_shift : p.Tk;
+    p.wait_cycles = p.stall ? 4000000 : kWaitCycles + 1024 * keys + 256LL * p.B;
     const Plan pl = make_plan(D);
     uint8_t* base = static_cast<uint8_t*>(ws);
     p.head = reinterpret_cast<PrefillHead*>(base);

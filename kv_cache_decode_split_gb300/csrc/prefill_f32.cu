@@ -54,7 +54,7 @@ struct Smem {
     uint8_t k[3][kN * D * 2];
     uint8_t v[3][kN * D * 2];
     uint64_t qfull, qempty, kfull, kempty, vfull, vempty, sfull[2], pready[2], ofull;
-    uint64_t pfull[kPieces], pempty[kPieces], end[2];
+    uint64_t pfull[kPieces], pempty[kPieces], end[2], never;
     Piece piece[kPieces];
     uint32_t bad[kPieces];  // tiles with values that are not finite
     uint32_t tmem_base;
@@ -115,10 +115,10 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
     int* err = p.err;
     const int c8 = tid % kRow, r0 = tid / kRow;
     uint32_t nq = 0, nk = 0, nv = 0;
-    bool ok = true;
+    bool ok = !stalls(p, &sm.never, 4);
     for (int k = 0; ok; ++k) {
         const int slot = k % kPieces;
-        if (!wait(&sm.pfull[slot], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[slot], (k / kPieces) & 1, p)) break;
         const Piece pc = sm.piece[slot];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0, items = nt > 0 ? 2 * nt : -2;
@@ -166,7 +166,7 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
             uint64_t* full = i < 0 ? &sm.qfull : is_v ? &sm.vfull : &sm.kfull;
             if (i != -1) {  // (the queries' halves are one wait and one arrival)
                 uint32_t& n = i < 0 ? nq : is_v ? nv : nk;
-                if (!(ok = wait(i < 0 ? &sm.qempty : is_v ? &sm.vempty : &sm.kempty, (n & 1) ^ 1, err))) break;
+                if (!(ok = wait(i < 0 ? &sm.qempty : is_v ? &sm.vempty : &sm.kempty, (n & 1) ^ 1, p))) break;
                 ++n;
             }
             if (is_v) {
@@ -205,23 +205,22 @@ template <int D>
 __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, int lane) {
     constexpr uint32_t id = idesc_bf16_f32(kM, kN, 0, 0);
     const uint64_t q = sw128_kmajor_desc(smem_u32(sm.q[0])), kk = sw128_kmajor_desc(smem_u32(sm.k[0]));
-    int* err = p.err;
     const bool one = lane == 0;
     uint32_t nq = 0, nk = 0;  // query tiles, key tiles taken
-    bool ok = true;
+    bool ok = !stalls(p, &sm.never, 2);
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const int t0 = sm.piece[i].t0, nt = sm.piece[i].t1 - t0;
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
         if (t0 < 0) break;
         if (nt == 0) continue;
-        if (!(ok = wait(&sm.qfull, nq++ & 1, err))) break;
+        if (!(ok = wait(&sm.qfull, nq++ & 1, p))) break;
 #pragma unroll 1
         for (int t = 0; t < nt; ++t, ++nk) {
             // (the scores two tiles ago have been read)
-            if (!(ok = wait(&sm.pready[nk & 1], ((nk >> 1) & 1) ^ 1, err) && wait(&sm.kfull, nk & 1, err))) break;
+            if (!(ok = wait(&sm.pready[nk & 1], ((nk >> 1) & 1) ^ 1, p) && wait(&sm.kfull, nk & 1, p))) break;
             tc_fence_after();
             const uint32_t s = sm.tmem_base + kColS + kN * (nk & 1);
 #pragma unroll 1
@@ -243,27 +242,26 @@ __device__ void qk_role(const PrefillParams& p, Smem<D>& sm, int lane) {
         if (ok && one) tc_commit(&sm.qempty);
     }
     if (one) tc_commit(&sm.end[0]);  // all products complete before tensor memory is released
-    wait(&sm.end[0], 0, err);
+    drain(&sm.end[0], 0, p);
 }
 
 template <int D>
 __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, int lane) {
     constexpr uint32_t id = idesc_bf16_f32(kM, D, 0, 1);
     const uint64_t v = sw128_mnmajor_desc(smem_u32(sm.v[0]), kN * 128);
-    int* err = p.err;
     const bool one = lane == 0;
     uint32_t np = 0;  // value tiles taken
-    bool ok = true;
+    bool ok = !stalls(p, &sm.never, 3);
     for (int k = 0; ok; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const int t0 = sm.piece[i].t0, nt = sm.piece[i].t1 - t0;
         __syncwarp();
         if (one) mbar_arrive(&sm.pempty[i]);
         if (t0 < 0) break;
 #pragma unroll 1
         for (int t = 0; t < nt; ++t, ++np) {
-            if (!(ok = wait(&sm.vfull, np & 1, err) && wait(&sm.pready[np & 1], (np >> 1) & 1, err))) break;
+            if (!(ok = wait(&sm.vfull, np & 1, p) && wait(&sm.pready[np & 1], (np >> 1) & 1, p))) break;
             tc_fence_after();
             const uint32_t o = sm.tmem_base + kColO + 128 * (np & 1);
 #pragma unroll 1
@@ -283,7 +281,7 @@ __device__ void pv_role(const PrefillParams& p, Smem<D>& sm, int lane) {
         }
     }
     if (one) tc_commit(&sm.end[1]);
-    wait(&sm.end[1], 0, err);
+    drain(&sm.end[1], 0, p);
 }
 
 // ----------------------------------------------------------------------------------- softmax
@@ -308,14 +306,14 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
     const int TM = kM / p.G, U = TM;
     const uint32_t quad = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tmem = sm.tmem_base + quad;
-    int* err = p.err;
     const bool negative = p.scale_log2 < 0.f;
     const float c = fmaxf(fabsf(p.scale_log2), 0x1p-100f);  // (0: -inf times it stays -inf)
     const int tok_r = r / p.G, head_r = r - tok_r * p.G;
     uint32_t ns = 0, no = 0;  // score tiles and output tiles taken
+    if (stalls(p, &sm.never, 5)) return;
     for (int k = 0;; ++k) {
         const int i = k % kPieces;
-        if (!wait(&sm.pfull[i], (k / kPieces) & 1, err)) break;
+        if (!wait(&sm.pfull[i], (k / kPieces) & 1, p)) break;
         const Piece pc = sm.piece[i];
         if (pc.t0 < 0) break;
         const int token = pc.tok0 + tok_r;
@@ -347,7 +345,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
         };
 #pragma unroll 1
         for (int t = pc.t0; t < pc.t1; ++t) {
-            if (!(ok = wait(&sm.sfull[ns & 1], (ns >> 1) & 1, err))) break;
+            if (!(ok = wait(&sm.sfull[ns & 1], (ns >> 1) & 1, p))) break;
             const uint32_t s_at = tmem + kColS + kN * (ns & 1);
             const int tile = tile_of(pc, t);
             const bool edge = at_edge(tile);
@@ -401,7 +399,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
             }
             // (the weights before are read, and their outputs there: P is free)
             if (t > pc.t0) {
-                if (!(ok = wait(&sm.ofull, no & 1, err))) break;
+                if (!(ok = wait(&sm.ofull, no & 1, p))) break;
                 ++no;
             }
             if (busy) {
@@ -440,7 +438,7 @@ __device__ void softmax_role(const PrefillParams& p, Smem<D>& sm, int warp, int 
             f = rise;
         }
         if (ok && pc.t1 > pc.t0) {
-            ok = wait(&sm.ofull, no & 1, err);
+            ok = wait(&sm.ofull, no & 1, p);
             ++no;
             if (ok && busy) add_tile();
         }
@@ -512,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const PrefillP
         mbar_init(&sm.ofull, 1);
         mbar_init(&sm.end[0], 1);
         mbar_init(&sm.end[1], 1);
+        mbar_init(&sm.never, 1);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.pfull[i], 1);
             mbar_init(&sm.pempty[i], 2 + kSoftWarps + kConvWarps);
@@ -537,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const PrefillP
                 const int i = ps % kPieces;
                 bool ok = true;
                 if (lane == 0) {
-                    ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, p.err);
+                    ok = wait(&sm.pempty[i], ((ps / kPieces) & 1) ^ 1, p);
                     if (ok) {
                         sm.piece[i] = u;
                         sm.bad[i] = 0;
@@ -547,9 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_f32_kernel(const PrefillP
                 ++ps;
                 return __shfl_sync(0xffffffffu, ok, 0) != 0;
             };
-            bool ok = true;
+            bool ok = !stalls(p, &sm.never, 1);
             const int TM = kM / p.G;
-            walk<kN>(p, TM, TM, lane, [&](const Piece& u) { return ok = publish(u); });
+            walk<kN>(p, TM, TM, lane, [&](const Piece& u) { return ok = ok && publish(u); });
             if (ok) {
                 Piece last;
                 last.t0 = -1;

@@ -655,3 +655,43 @@ def test_values_that_are_not_finite_in_parts(kvd, Hq, new):
     assert int(err.item()) == 0
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(got.nan_to_num(7.0, 8.0, 9.0), want.nan_to_num(7.0, 8.0, 9.0))
+
+
+@pytest.mark.parametrize("new,lens", [([40, 1, 3], [40, 900, 70]), ([700, 5], [700, 5000]), ([3], [9000])])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("role", [1, 2, 3, 4, 5, 6])
+def test_a_wait_that_runs_out_is_recorded(kvd, role, dtype, new, lens):
+    """One role's warps first wait for what does not come: all roles give up, within their limits, copies and
+    products that are under way are waited for, the call says so, and the next one is right again, with the
+    same workspace. (float32 has no sixth role.)"""
+    c = Case(new, lens, 8, 2, 128, dtype, seed=80)
+    args = (c.q, *c.pools(64), cu(c.new))
+    ws = torch.full((kvd.kvd_workspace_size("prefill", len(new), 8, 2, 128),), 255, dtype=torch.uint8, device=DEV)
+    out, err = torch.empty_like(c.q), torch.zeros(1, dtype=I32, device=DEV)
+
+    def call():
+        kvd.attn_prefill_gqa_paged(*args, out=out, workspace=ws, err=err, **c.more())
+
+    kvd.kvd_set_option("wait_timeout_test", role)
+    try:
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        time = a.elapsed_time(b)
+    finally:
+        kvd.kvd_set_option("wait_timeout_test", 0)
+    assert int(err.item()) == (0 if dtype == F32 and role == 6 else -4)
+    assert time < 100  # ms; the limit of a wait is about 2
+    for _ in range(2):
+        c.check(*c.call(kvd.attn_prefill_gqa_paged, args, workspace=ws))
+    # a packed call takes the option too
+    kvd.kvd_set_option("wait_timeout_test", role)
+    try:
+        err.zero_()
+        kvd.attn_prefill_gqa(c.q, torch.cat(c.k), torch.cat(c.v), cu(c.new), cu(c.lens), workspace=ws, err=err)
+        assert int(err.item()) == (0 if dtype == F32 and role == 6 else -4)
+    finally:
+        kvd.kvd_set_option("wait_timeout_test", 0)
+    c.check(*c.packed(kvd, workspace=ws))

@@ -143,3 +143,14 @@ def test_host_tensors_are_refused(kvd):
                                            z(2, dtype=i), z(3, 2, 64), z(3, 2, 64))):
         with pytest.raises(TypeError, match="CUDA tensor"):
             call()
+
+
+def test_the_option_that_lets_a_wait_run_out_has_a_range(kvd):
+    try:
+        for n in range(7):
+            kvd.kvd_set_option("wait_timeout_test", n)
+        for n in (-1, 7):
+            with pytest.raises(kvd.KvdError):
+                kvd.kvd_set_option("wait_timeout_test", n)
+    finally:
+        kvd.kvd_set_option("wait_timeout_test", 0)
