@@ -69,9 +69,10 @@ struct Weigh {
     __device__ __forceinline__ Weigh(const PrefillParams& p, const Seq& s, int u, bool f)
         : base(max(0, s.L - s.n)), cap(0), U(u), fixed(p.unit_cost), free(0x7fffffff), flat(f) {
         if (p.window > 0) {
-            const int c = min(p.window, 1 << 30) + U + 128 + min(p.n_sink, s.L) - 1;  // < 2^31
+            // (below 2^31 + 2^9: both of the first two may be 2^30)
+            const unsigned c = static_cast<unsigned>(min(p.window, 1 << 30)) + U + 128 + min(p.n_sink, s.L) - 1;
             cap = c;
-            free = c > base ? (c - static_cast<int>(base)) / U : 0;
+            free = c > base ? static_cast<int>(min((c - static_cast<unsigned>(base)) / U, 0x7fffffffu)) : 0;
         }
     }
     __device__ __noinline__ long long upto(int m) const {

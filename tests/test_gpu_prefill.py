@@ -695,3 +695,10 @@ def test_a_wait_that_runs_out_is_recorded(kvd, role, dtype, new, lens):
     finally:
         kvd.kvd_set_option("wait_timeout_test", 0)
     c.check(*c.packed(kvd, workspace=ws))
+
+
+@pytest.mark.parametrize("new", [1, 3, 300])
+def test_the_longest_window_sinks_and_table(kvd, new):
+    # a unit's length in the work list is above 2^31 (held in an int, the call would have written nothing)
+    long_call(kvd, [new], [2 ** 30 - 256], 1, 1, 64, window=2 ** 30, n_sink_tokens=2 ** 30)
+    long_call(kvd, [new], [2 ** 30 - 256], 1, 1, 64, window=2 ** 31 - 1, n_sink_tokens=2 ** 31 - 1)
