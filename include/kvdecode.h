@@ -392,6 +392,8 @@ int attn_prefill_gqa(const void *q, const void *k, const void *v, const int32_t 
  * before the append (kvd_cache_read) and use attn_prefill_gqa.
  *  err also receives KVD_ERR_DEVICE_OOB for a length below the number of new tokens (the leading ones
  *  see nothing) or above the table's capacity (clamped) and for a page id out of range (clamped).
+ * Entries of pages that no new token sees, behind the window and past the sinks, are not used: those
+ * pages may be gone.
  * Everything else as attn_prefill_gqa; page_size a power of two in [16, 256].
  */
 int attn_prefill_gqa_paged(const void *q, const void *k_pool, const void *v_pool,

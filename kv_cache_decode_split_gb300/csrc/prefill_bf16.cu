@@ -200,8 +200,12 @@ __device__ void load_role(const PrefillParams& p, Smem<D>& sm, const CUtensorMap
             const int t = e / per;
             if (t >= nt) return 0;
             const int tok = tile_of(pc, pc.t0 + t) * kN + ((e % per) << shift);
-            const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,
-                                     min(tok, pc.L - 1) >> p.page_shift, err);
+            int key = min(tok, pc.L - 1);
+            // (a page that no row of the unit sees may be gone: any other, all of it is masked)
+            if (p.window > 0 && tok >= p.n_sink && tok + (1 << shift) <= pc.L - pc.n + pc.tok0 - p.window + 1)
+                key = pc.L - 1;
+            const int pg =
+                load_page(p.block_table, p.max_pages, p.num_pages, pc.k0, key >> p.page_shift, err);
             return ((pg * p.Hkv + pc.h) << p.page_shift) + (tok & ((1 << p.page_shift) - 1));
         };
         int kb = -32, vb = -32, kcur = 0, knxt = 0, vcur = 0;

@@ -122,6 +122,9 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
         const Piece pc = sm.piece[slot];
         if (pc.t0 < 0) break;
         const int nt = pc.t1 - pc.t0, items = nt > 0 ? 2 * nt : -2;
+        // the first key in the first row's window: those before it, that are no sinks, no row of the unit sees
+        // (and their pages may be gone)
+        const int low = p.window > 0 ? pc.L - pc.n + pc.tok0 - p.window + 1 : 0;
         // item i: -2 and -1 are the queries
         auto is_value = [&](int i) { return i == items - 1 || (i > 0 && i % 2 == 0); };
         auto load = [&](Rows& rows, int i) {
@@ -138,7 +141,7 @@ __device__ void convert_role(const PrefillParams& p, Smem<D>& sm, int tid, int l
                     if (t < TM && token < pc.n)
                         at = base + (pc.c0 + token) * p.q_stride +
                              (pc.h * p.G + (row - t * p.G)) * static_cast<long long>(D);
-                } else if (t0 + r < pc.L) {
+                } else if (t0 + r < pc.L && (t0 + r >= low || t0 + r < p.n_sink)) {
                     if (p.block_table) {
                         const int key = t0 + r;
                         const int pg = load_page(p.block_table, p.max_pages, p.num_pages, pc.k0,

@@ -702,3 +702,19 @@ def test_the_longest_window_sinks_and_table(kvd, new):
     # a unit's length in the work list is above 2^31 (held in an int, the call would have written nothing)
     long_call(kvd, [new], [2 ** 30 - 256], 1, 1, 64, window=2 ** 30, n_sink_tokens=2 ** 30)
     long_call(kvd, [new], [2 ** 30 - 256], 1, 1, 64, window=2 ** 31 - 1, n_sink_tokens=2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("P", [16, 64, 128, 256])
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (100, 4), (300, 0), (700, 33), (130, 260)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_pages_behind_the_window_may_be_gone(kvd, dtype, window, n_sink, P):
+    for Hq, Hkv, D in ((8, 2, 64), (2, 2, 128)):
+        new, lens = [1, 300, 40, 9], [1500, 1700, 900, 2311]
+        c = Case(new, lens, Hq, Hkv, D, dtype, window=window, n_sink=n_sink, seed=90)
+        kp, vp, bt, sl = c.pools(P)
+        for b, (n, L) in enumerate(zip(new, lens)):
+            seen = set(range(max(0, L - n - window + 1) // P, (L - 1) // P + 1)) | set(range(-(-min(n_sink, L) // P)))
+            gone = [i for i in range(bt.shape[1]) if i not in seen]
+            bt[b, torch.tensor(gone, device=DEV)] = -1
+        assert (bt[1] < 0).any()
+        c.check(*c.call(kvd.attn_prefill_gqa_paged, (c.q, kp, vp, bt, sl, cu(new))))
