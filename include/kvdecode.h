@@ -417,6 +417,8 @@ int attn_prefill_gqa_paged(const void *q, const void *k_pool, const void *v_pool
  *          do not ascend or leave T, a length below 0 or (paged) above the table's capacity, a
  *          sequence that holds more than it has rows (nothing of such a sequence is written) or a
  *          page id out of range (its rows are not written)
+ *          Sequences behind an offset that does not ascend, and of more than 32 sequences up to
+ *          B / 16 in front of it, may be left unwritten.
  * Bytes are copied unchanged. Supported: D in {64, 128}, dtype KVD_BF16 or KVD_F32, page_size a power
  * of two in [16, 256]; T == 0 does nothing. No workspace; one launch.
  */

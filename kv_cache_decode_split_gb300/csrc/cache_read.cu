@@ -50,14 +50,17 @@ __device__ __forceinline__ long long row_of(const CacheReadParams& p, const Read
 }
 
 __device__ __forceinline__ ReadBlock find_block(const CacheReadParams& p, int item, int lane) {
-    // largest b with cu[b] / 16 + b <= item
+    // largest b with cu[b] / 16 + b <= item, of those up to which offsets ascend: a sequence behind a bad offset
+    // is given no block, so that it takes none of a sequence in front of it. (Of more than 32 sequences the
+    // first round looks at every so many.)
     int lo = 0, n = p.B;  // the answer is in [lo, lo + n)
     while (n > 1) {
         const int step = (n + 31) / 32;
         const int b = lo + lane * step;
-        const bool le = lane * step < n && (p.cu_seqlens[b] >> 4) + b <= item;
+        const int c = lane * step < n ? p.cu_seqlens[b] : 0, before = __shfl_up_sync(0xffffffffu, c, 1);
+        const bool le = lane * step < n && (lane == 0 || c >= before) && (c >> 4) + b <= item;
         const unsigned m = __ballot_sync(0xffffffffu, le);
-        const int k = m ? 31 - __clz(m) : 0;
+        const int k = max(__ffs(~m) - 2, m == 0xffffffffu ? 31 : 0);
         lo += k * step;
         n = min(step, n - k * step);
     }
@@ -65,7 +68,7 @@ __device__ __forceinline__ ReadBlock find_block(const CacheReadParams& p, int it
     r.page = -1;
     const int c0 = p.cu_seqlens[lo], c1 = p.cu_seqlens[lo + 1];
     const int L = p.seq_lens[lo];
-    if (c0 < 0 || c1 < c0 || c1 > p.T) return r;  // (recorded by the grid's first block)
+    if (c0 < 0 || c1 < c0 || c1 > p.T || (lo == 0 && c0 != 0)) return r;  // (recorded by the grid's first block)
     const long long cap = p.window > 0 ? static_cast<long long>(p.n_sink) + p.window
                                        : static_cast<long long>(p.max_pages) << p.page_shift;
     if (L < 0 || (p.window <= 0 && L > cap)) return r;

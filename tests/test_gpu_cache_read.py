@@ -165,3 +165,32 @@ def test_the_values_that_an_append_handed_back(kvd):
     for x, y in ((ko, kr), (vo, vr)):
         assert torch.equal(torch.isnan(x), torch.isnan(y))
         assert torch.equal(x.nan_to_num(5.0), y.nan_to_num(5.0))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_sequences_in_front_of_a_bad_offset_are_written(kvd, q4):
+    lens = [40, 70, 9, 100, 33, 1, 16, 200]
+    c = Case(lens, 2, 64, 16, BF, q4, seed=7)
+    good = cu(c.rows)
+    for at in range(2, len(lens) + 1):  # offset `at` ends sequence at - 1
+        for bad in (-5, -2 ** 31, 0, 17, int(good[at - 1]) - 1, sum(lens) + 4, 2 ** 31 - 1):
+            offsets = good.clone()
+            offsets[at] = bad
+            outs = c.outs()
+            assert c.run(kvd, outs, cu_seqlens=offsets) == -6
+            for values, out in zip(c.values, outs):
+                want = R.read(values, c.bt, lens, 16)
+                for b in range(at - 1):
+                    assert torch.equal(out[int(good[b]):int(good[b + 1])].cpu(), want[b]), (at, bad, b)
+                assert (out[sum(lens):] == 9.0).all()
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_a_first_offset_other_than_0_is_bad(kvd, q4):
+    c = Case([9, 30], 2, 64, 16, BF, q4, seed=8, spare=20)
+    for first in (1, 5, 16):
+        outs = c.outs()
+        offsets = cu(c.rows)
+        offsets[0] = first
+        assert c.run(kvd, outs, cu_seqlens=offsets) == -6
+        assert all((o[:29] == 9.0).all() for o in outs)
