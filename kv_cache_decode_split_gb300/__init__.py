@@ -464,7 +464,7 @@ def attn_prefill_gqa_paged(q, k_pool, v_pool, block_table, seq_lens, cu_seqlens=
     """attn_prefill_gqa over a paged cache [num_pages, Hkv, P, D] that holds the new tokens already
     (rope_append writes them): chunks of a prompt, draft tokens, or, with cu_seqlens None, one token of
     each sequence. seq_lens [B]: lengths with the new tokens. A bad length or page id is recorded in
-    err and clamped. For a rolling cache read it (cache_read) before the append and use
+    err and clamped; pages behind the window that no new token sees may be gone. For a rolling cache read it (cache_read) before the append and use
     attn_prefill_gqa."""
     return _prefill(True, q, k_pool, v_pool, block_table, seq_lens, cu_seqlens, window,
                     n_sink_tokens, sink_logit, scale, out, lse_out, workspace, err, stream)

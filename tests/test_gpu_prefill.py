@@ -718,3 +718,33 @@ def test_pages_behind_the_window_may_be_gone(kvd, dtype, window, n_sink, P):
             bt[b, torch.tensor(gone, device=DEV)] = -1
         assert (bt[1] < 0).any()
         c.check(*c.call(kvd.attn_prefill_gqa_paged, (c.q, kp, vp, bt, sl, cu(new))))
+
+
+def test_where_float32_values_begin_to_count_as_infinite(kvd):
+    # the neighbours of the first number that rounds to a bfloat16 infinity, as the only value of their column
+    # that is not small
+    below, first = (torch.tensor(x, dtype=I32).view(F32).item() for x in (0x7f7f7fff, 0x7f7f8000))
+    for sign in (1, -1):
+        c = Case([70, 5], [70, 300], 4, 2, 64, F32, seed=91)
+        c.v[0][40, 0, 3], c.v[0][40, 1, 4] = sign * below, sign * first
+        c.v[1][296, 0, 7], c.v[1][296, 1, 8] = sign * below, sign * first
+        ref = Case([70, 5], [70, 300], 4, 2, 64, F32, seed=91)
+        for r, x in zip(ref.v, c.v):
+            r.copy_(x)
+        ref.v[0][40, 1, 4] = ref.v[1][296, 1, 8] = sign * math.inf
+        for out, lse in (c.packed(kvd), c.paged(kvd, 16)):
+            ref.check(out, lse)
+
+
+@pytest.mark.parametrize("exponent", [-100, -110, -118, -123])
+def test_small_float32_values(kvd, exponent):
+    # operands keep the bits down to 2^-133: half of the last, and as much for what is added up
+    c = Case([70, 5], [70, 300], 4, 2, 64, F32, seed=92)
+    for v in c.v:
+        v *= 2.0 ** exponent
+    out, lse = c.packed(kvd)
+    at = 0
+    for b, n in enumerate(c.new):
+        ref, rl, tol, tol_l = R.attention(c.q[at:at + n], c.k[b], c.v[b], c.scale, dtype=F32)
+        assert ((out[at:at + n].double() - ref).abs() <= tol + 2.0 ** -133).all()
+        at += n
