@@ -392,7 +392,8 @@ int attn_prefill_gqa(const void *q, const void *k, const void *v, const int32_t 
  * attn_decode_gqa_paged. A rolling cache has lost keys that a chunk's first tokens see: read it
  * before the append (kvd_cache_read) and use attn_prefill_gqa.
  *  err also receives KVD_ERR_DEVICE_OOB for a length below the number of new tokens (the leading ones
- *  see nothing) or above the table's capacity (clamped) and for a page id out of range (clamped).
+ *  see nothing; not with cu_seqlens null, where a length of 0 is an empty sequence, whose row sees
+ *  nothing) or above the table's capacity (clamped) and for a page id out of range (clamped).
  * Entries of pages that no new token sees, behind the window and past the sinks, are not used: those
  * pages may be gone.
  * Everything else as attn_prefill_gqa; page_size a power of two in [16, 256].

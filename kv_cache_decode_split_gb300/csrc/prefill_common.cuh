@@ -46,7 +46,7 @@ static __device__ __noinline__ Seq load_seq(const PrefillParams& p, int b, int* 
     if (paged) {
         s.L = min(max(a, 0), p.max_pages << p.page_shift);
         s.k0 = b;
-        bad |= a != s.L || s.L < s.n;
+        bad |= a != s.L || (s.L < s.n && p.cu_q);  // (without offsets: an empty sequence)
     } else {
         s.k0 = a;
         s.L = k1 - a;

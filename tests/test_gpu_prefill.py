@@ -748,3 +748,17 @@ def test_small_float32_values(kvd, exponent):
         ref, rl, tol, tol_l = R.attention(c.q[at:at + n], c.k[b], c.v[b], c.scale, dtype=F32)
         assert ((out[at:at + n].double() - ref).abs() <= tol + 2.0 ** -133).all()
         at += n
+
+
+@pytest.mark.parametrize("learned", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_empty_sequences_of_one_token_each(kvd, dtype, learned):
+    # without offsets a length of 0 is no error, as for the 4-bit decode
+    lens = [0, 5, 0, 300, 64, 0]
+    c = Case([1] * 6, lens, 8, 2, 64, dtype, learned=learned, seed=93)
+    kp, vp, bt, sl = c.pools(16)
+    c.check(*c.call(kvd.attn_prefill_gqa_paged, (c.q, kp, vp, bt, sl)))
+    err = torch.zeros(1, dtype=I32, device=DEV)
+    sl[2] = -1
+    kvd.attn_prefill_gqa_paged(c.q, kp, vp, bt, sl, err=err)
+    assert int(err.item()) == -6
