@@ -167,13 +167,13 @@ __device__ __forceinline__ void put_back(const PrefillParams& p, const Piece& pc
     constexpr int E = D / 32, kBatch = 4;
     uint32_t up[E] = {}, down[E] = {};  // column i * E + e is bit i of word e; a NaN is in both
     const Edge<kN> edge(p, pc, U);
-    const int shift = odd_shift(pc);
-    bool full = false;
+    const int shift = odd_shift(pc), top = __reduce_max_sync(0xffffffffu, valid ? pos : -1);
+    bool full = false;  // all NaN: no more can come
 #pragma unroll 1
     for (int t = pc.t0; t < pc.t1 && !full; ++t) {
         const int tile = tile_of(pc, t);
         if (!(marks >> ((t - pc.t0) >> shift) & 1) || (kEdgesOnly && !edge(tile))) continue;
-        const int end = min(pc.L, tile * kN + kN);
+        const int end = min(min(pc.L, top + 1), tile * kN + kN);
         auto row = [&](int key) -> const T* {
             const T* v = static_cast<const T*>(p.v) + lane * E;
             if (!p.block_table) return v + static_cast<long long>(pc.k0 + key) * p.v_stride + pc.h * D;
@@ -183,7 +183,7 @@ __device__ __forceinline__ void put_back(const PrefillParams& p, const Piece& pc
                         (key & ((1 << p.page_shift) - 1))) * D;
         };
 #pragma unroll 1
-        for (int k0 = tile * kN; k0 < end; k0 += kBatch) {
+        for (int k0 = tile * kN; k0 < end && !full; k0 += kBatch) {
             float x[kBatch][E];
             bool all = true;
 #pragma unroll
@@ -207,12 +207,11 @@ __device__ __forceinline__ void put_back(const PrefillParams& p, const Piece& pc
                     down[e] |= sees ? d : 0;
                 }
             }
-        }
-        // (all NaN: no more can come)
-        uint32_t both = 0xffffffffu;
+            uint32_t both = 0xffffffffu;
 #pragma unroll
-        for (int e = 0; e < E; ++e) both &= up[e] & down[e];
-        full = __all_sync(0xffffffffu, !valid || both == 0xffffffffu);
+            for (int e = 0; e < E; ++e) both &= up[e] & down[e];
+            full = __all_sync(0xffffffffu, !valid || both == 0xffffffffu);
+        }
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -674,10 +673,10 @@ inline cudaError_t launch_merge(const PrefillParams& p, int U, cudaStream_t stre
 
 // The call's part of the parameters: workspace and how work is cut.
 inline void set_plan(PrefillParams& p, int D, void* ws, int unit_cost, int flat_slack) {
-    // A wait may be as long as the four pieces that are under way, of at most 103 cycles a key, or as the look
-    // through all sequences' lengths.
+    // A wait may be as long as the four pieces that are under way, of some 100 cycles a key and four times that
+    // with values that are not finite in each tile, or as the look through all sequences' lengths.
     const long long keys = p.block_table ? static_cast<long long>(p.max_pages) << p.page_shift : p.Tk;
-    p.wait_cycles = p.stall ? 4000000 : kWaitCycles + 1024 * keys + 256LL * p.B;
+    p.wait_cycles = p.stall ? 4000000 : kWaitCycles + 4096 * keys + 256LL * p.B;
     const Plan pl = make_plan(D);
     uint8_t* base = static_cast<uint8_t*>(ws);
     p.head = reinterpret_cast<PrefillHead*>(base);
