@@ -12,10 +12,13 @@
 // without a scan: block k of sequence b is item cu[b] / 16 + b + k, which is unique and ascending, so
 // a 32-way search over b (one round of loads up to 32 sequences, two up to 1024) inverts it.
 //
-// Bound by the rows written, of which every SM can hand on 32 bytes a cycle: 4 bits to bf16, 41,000
-// tokens of 8 heads of 128 (48 MB read, 171 MB written) take 45.0 us, 4.8 TB/s, with that path busy 70 %
-// of the time. (Whole rows at a time for the keys as well, or codes turned to numbers without a
-// conversion, leave it there: 45.5 us. A short call, four contexts of 33 to 700 tokens, takes 3.4 us.)
+// Bound by the bytes written, of which every SM can hand on 32 a cycle: 4 bits to bf16, 41,000 tokens of 8
+// heads of 128 (48 MB read, 171 MB written) take 45.6 us, 4.8 TB/s, with that path busy 68 % of the time. But
+// nearly half of what is on it is a copy of the arguments, which each thread writes to its stack, as they are
+// indexed at run time: without it the same call takes 36.1 us, which is left for a change of its own. (Whole
+// rows at a time for the keys as well, or codes turned to numbers without a conversion, did not change the
+// time.) Plain rows of as many tokens 53.9 us, 6.3 TB/s. A short call, four contexts of 33 to 700 tokens,
+// takes 3.5 us: four dependent reads (the search, offsets and length, the page, the rows).
 
 #include <algorithm>
 
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kReadWarps * 32) cache_read_q4_kernel(const Ca
         // values: the 64 channels of a token's group lie in eight words, 8 channels 8j .. 8j + 7 in their
         // codes j. So the words go through shared memory: eight lanes take the group and write its 128
         // (float32: 256) bytes together. (A lane that takes a group alone writes 16 bytes of 32 lines at
-        // a time: nine contexts of 1001 to 8191 tokens, 8 KV heads of 128, take 50.4 us, against 45.0.)
+        // a time: nine contexts of 1001 to 8191 tokens, 8 KV heads of 128, take 5 us more.)
         constexpr int kRows = 16 * L::kGroups, kPer = 8 * kRows / 32;  // groups; words that a lane fetches
         struct __align__(16) Group {
             uint32_t w[8];

@@ -32,16 +32,16 @@
 // the pieces: the result does not depend on timing).
 //
 // Bound, in long units, by the softmax's chain (some 1400 cycles for 64 keys, two such warps a scheduler, issue
-// slots busy 44 %) next to the products, whose pipe is busy 72 %: a 128 x 128 tile is 512 cycles of
+// slots busy 48 %) next to the products, whose pipe is busy 75 %: a 128 x 128 tile is 512 cycles of
 // QK (768 in the halves of 64 keys that let the exponentials start early; it is shared memory's rate then),
 // 512 of PV and 512 of exponentials, two tiles at a time. 16385 tokens of 32/8 heads of 128 take 1.60 ms,
 // 1.38 PFLOP/s (72 % of what a library matrix product reaches); 2048-token chunks behind 28 thousand 1.34 to
-// 1.48. Short units are bound by their ends: the next unit's queries take the last one's place, so that 1500
+// 1.50. Short units are bound by their ends: the next unit's queries take the last one's place, so that 1500
 // to 3000 cycles pass without products, and code that a unit runs once is not in the instruction caches
-// (nine prompts of 61 to 3581 tokens: 404 us, 0.84 PFLOP/s). Loading the next unit's first keys ahead of its
-// queries did not help (420 us). A call of one short unit an SM (513 tokens: 18.3 us) is a chain: 5 us to
+// (nine prompts of 61 to 3581 tokens: 390 us, 0.87 PFLOP/s). Loading the next unit's first keys ahead of its
+// queries did not help (5 % slower). A call of one short unit an SM (513 tokens: 18.8 us) is a chain: 5 us to
 // the first load (lengths, then the CTA's range), 3 to the first scores, 2 a tile, 3 for the end.
-// Draft tokens (32 sequences, 1 to 8 tokens behind 4096 to 8184) read the cache at 5.5 TB/s: 146 us.
+// Draft tokens (32 sequences, 1 to 8 tokens behind 4096 to 8184) read the cache at 5.6 TB/s: 143 us.
 
 #include <algorithm>
 
@@ -877,10 +877,10 @@ int launch(PrefillParams p, void* ws, cudaStream_t stream) {
     static const cudaError_t set =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (set != cudaSuccess) return KVD_ERR_CUDA;
-    // A unit's start and end count as 320 keys (nine prompts of 61 to 3581 tokens, 32/8 heads of 128: 490 us
-    // with 0, 411 with 192, 402 with 320, 396 with 512, 399 with 768; one of 16385: 1.63 ms, 1.53, 1.53, 1.55,
-    // 1.57). A call of fewer units than SMs is left uncut if that makes its longest range at most 8 tiles
-    // longer (5 draft tokens behind 1024: 19.8 us; with 24 tiles 22.4).
+    // A unit's start and end count as 320 keys (nine prompts of 61 to 3581 tokens, 32/8 heads of 128: 500 us
+    // with 0, 395 with 192, 390 with 320, 385 with 512, 391 with 768; one of 16385: 1.67 ms, 1.59, 1.60, 1.61,
+    // 1.63). A call of fewer units than SMs is left uncut if that makes its longest range at most 8 tiles
+    // longer (5 draft tokens behind 1024: 19.1 us; with 24 tiles 20.9).
     set_plan(p, D, ws, 320, 8 * kN);
     if (launch_kernel(kernel, dim3(static_cast<unsigned>(p.n_cta)), dim3(kThreads), smem, stream, tq, tk,
                       tv, p) != cudaSuccess ||

@@ -11,11 +11,12 @@
 // registers, rounded.
 //
 // Bound by the converting warps: 500 instructions for 64 rows, two such items a tile, and one buffer for
-// each (192 KB hold no second), so that a tile of D = 128 takes 6600 cycles where the products take 3800
+// each (at D = 128, where a set of operands takes 192 KB, there is no room for a second; at D = 64 there
+// would be), so that a tile of D = 128 takes 6600 cycles where the products take 3800
 // and shared memory, which the score product's operands fill (6 KB for 128 x 64 x 16), 4400. Six chunks of
-// 1 to 301 tokens behind 400 to 5003, 14/2 heads of 128: 115 us, 98 TFLOP/s of the formula's operations,
-// a sixth of those issued; the windowed prompts below 116 us. (Pages looked up two items ahead, or 32-byte
-// loads, change nothing: 117 us each.)
+// 1 to 301 tokens behind 400 to 5003, 14/2 heads of 128: 118 us, 96 TFLOP/s of the formula's operations,
+// a sixth of those issued; the windowed prompts below 118 us. (Pages looked up two items ahead, or 32-byte
+// loads, change nothing.)
 //
 // One persistent CTA an SM takes units of one query tile (128 rows: the G query heads of a KV head of
 // 128 / G tokens) from the list of prefill_common.cuh. Roles:
