@@ -368,12 +368,13 @@ int attn_decode_gqa_q4(const void *q, const void *k_pool, const void *v_pool,
  * value product are bfloat16 numbers (8 bits, as its operands must be of one type), their sum is not
  * rounded. Values are added up with weights of at most 1 and divided by the weights' sum at the end
  * (the sums have float32's range). A key or value that is NaN or infinite reaches the rows that see
- * it alone. Float32 operands are taken apart into three bfloat16 numbers: a magnitude that rounds to
- * a bfloat16 infinity (from 0x7f7f8000, 3.396e38, on) counts as infinite, an infinite key or query
- * makes the scores of its products NaN, and of a magnitude below 2^-102 the bits down to 2^-133 are
- * kept. The result does not depend on timing. One launch or, where a long sequence's work is
- * divided, two. A kernel whose waits run out (which a fault of the device would have to cause: they
- * allow for the longest sequence's work) records KVD_ERR_TIMEOUT in err and leaves out undefined.
+ * it alone. (An infinite value whose weight is 0 in float32 may give NaN.) Float32 operands are
+ * taken apart into three bfloat16 numbers: a magnitude that rounds to a bfloat16 infinity (from
+ * 0x7f7f8000, 3.396e38, on) counts as infinite, an infinite key or query makes the scores of its
+ * products NaN, and of a magnitude below 2^-102 the bits down to 2^-133 are kept. The result does
+ * not depend on timing. One launch or, where a long sequence's work is divided, two. A kernel whose
+ * waits run out (which a fault of the device would have to cause: they allow for the longest
+ * sequence's work) records KVD_ERR_TIMEOUT in err and leaves out undefined.
  * Supported: D in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 128, dtype KVD_BF16 or KVD_F32; T == 0 does
  * nothing.
  */
